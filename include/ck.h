@@ -317,6 +317,121 @@ ck_status ck_adam_update(float *param, const float *grad, float *m, float *v, in
 ck_status ck_step_advance(int64_t *step, void *stream);
 
 /*
+ * Readout operators: what a program does with the states of a recurrent token
+ * model (connectome-kernels page, intro: a connectome trained on text).  They
+ * need no graph handle.  Element types are given as a ck_dtype; everything is
+ * computed in 32-bit floats and rounded once to the output's type.
+ */
+typedef enum { CK_F32 = 0, CK_BF16 = 1, CK_F16 = 2 } ck_dtype;
+
+/*
+ * The generator: Philox-4x32-10 (Salmon, Moraes, Dror, Shaw, SC 2011) with key
+ * = seed (64 bits, low word first) and counter = {block (64 bits), step (64
+ * bits)}.  Element i takes word i % 4 of block i / 4.  Every (seed, step) is a
+ * stream of its own.  Where a call has step_dev, a non-NULL (device) int64[1]
+ * replaces `step` when the kernel runs, so that a captured graph that advances
+ * it (ck_step_advance) draws anew on every replay.
+ *
+ * ck_dropout -- y[i] = keep_i ? x[i] / (1 - p) : 0 over a tensor [n0][n1][n2]
+ * of `dtype` with the element strides given for x and y (x strides may be 0);
+ * keep_i = word_i >= round(p 2^32), i the row-major index in [n0][n1][n2], or in
+ * [n1][n2] when `locked` (one mask for all n0 entries: the input steps of a
+ * recurrence).  The factor is 1 / (1 - p) rounded to 32 bits; p = 1 drops all.
+ * A dropped element is 0 whatever x holds there.  The mask is not stored: the
+ * gradient is the same call on the output's gradient with the same p, seed,
+ * step and shape.  y may be x where their strides agree.
+ * Asynchronous.  Errors: CK_ERR_INVALID_ARG (dtype, p outside [0, 1], negative
+ * size, NULL pointer), CK_ERR_UNSUPPORTED (2^59 elements), CK_ERR_CUDA.
+ */
+ck_status ck_dropout(const void *x, void *y, int64_t dtype, int64_t n0, int64_t n1, int64_t n2,
+                     int64_t x0, int64_t x1, int64_t x2, int64_t y0, int64_t y1, int64_t y2,
+                     int64_t locked, double p, uint64_t seed, uint64_t step,
+                     const int64_t *step_dev, void *stream);
+
+/*
+ * ck_int4_matvec -- y[m][v] = bias[v] + sum_k s[v][k/group] (q[v][k] - z[v][k/group]) x[m][k]
+ *   x        (device) `dtype` [M][K], rows x_stride elements apart
+ *   qweight  (device) V rows, q_pitch bytes apart, of (K + 1) / 2 bytes: k even
+ *            in the low nibble of byte k / 2, k odd in the high one; the base
+ *            and q_pitch multiples of 16 bytes (nothing past a row's bytes is read)
+ *   scales   (device) `scale_dtype` [V][ceil(K / group)], rows s_stride elements apart
+ *   zeros    (device) uint8, the same shape, rows z_stride apart, its low four
+ *            bits read; NULL: 8 everywhere
+ *   bias     (device) float[V] or NULL
+ *   group    32, 64 or 128
+ *   y        (device) `dtype` [M][V], rows y_stride elements apart, overwritten
+ * An x row that holds an infinity or NaN gives outputs that are not finite.
+ * Asynchronous.  Errors: CK_ERR_INVALID_ARG (types, group, sizes, alignment,
+ * short strides, NULL pointers), CK_ERR_UNSUPPORTED (a size of 2^30 or more),
+ * CK_ERR_CUDA.
+ */
+ck_status ck_int4_matvec(const void *x, int64_t dtype, int64_t M, int64_t K, int64_t x_stride,
+                         const uint8_t *qweight, int64_t V, int64_t q_pitch, const void *scales,
+                         int64_t scale_dtype, int64_t s_stride, const uint8_t *zeros,
+                         int64_t z_stride, const float *bias, int64_t group, void *y,
+                         int64_t y_stride, void *stream);
+
+/*
+ * ck_int4_quantize -- weights for ck_int4_matvec from (device) `dtype` w[V][K],
+ * rows w_stride elements apart.  Per group, with lo = min(0, w), hi = max(0, w):
+ *   symmetric   s = max(-lo / 8, hi / 7), z = 8 (zeros is not written, may be NULL)
+ *   otherwise   s = (hi - lo) / 15, z = round(-lo / s) in 0..15
+ * s is rounded to scale_dtype first, then q = clamp(round(w / s) + z, 0, 15).  A
+ * group of zeros has s = 0.  A group that holds an infinity or NaN has scale NaN.
+ * Layouts as ck_int4_matvec (any q_pitch of at least (K + 1) / 2 bytes).
+ * Asynchronous.  Errors: as ck_int4_matvec.
+ */
+ck_status ck_int4_quantize(const void *w, int64_t dtype, int64_t V, int64_t K, int64_t w_stride,
+                           int64_t group, int64_t symmetric, uint8_t *qweight, int64_t q_pitch,
+                           void *scales, int64_t scale_dtype, int64_t s_stride, uint8_t *zeros,
+                           int64_t z_stride, void *stream);
+
+/*
+ * ck_control_logits -- the controls of an answering loop on logits[B][V] and,
+ * when `tokens` is given, the next token of each row.  For row b and token v,
+ * in this order, in 32-bit floats:
+ *   1. v anywhere in history[b][0 : len_b]: z > 0 ? z / repetition : z * repetition
+ *   2. z - (n frequency + (n > 0) presence), n = times v occurs in
+ *      history[b][prompt_b : len_b]
+ *   3. z + bias[v]
+ *   4. -inf where bit v % 32 of mask word v / 32 is 0
+ *   5. z / temperature where temperature > 0
+ * Ids outside [0, V) in the history are ignored (padding).  len_b and prompt_b
+ * are clamped to [0, L].  out[b][v] = z, rounded to the logits' type.
+ * tokens[b] = the v of the largest z (of equal ones the lowest v), before
+ * rounding; with `sample`, in rows whose temperature is above 0, of the largest
+ * z + g, g = -log(-log1p(-u)), u = min(word 2^-32 + 2^-33, 1 - 2^-24), the word
+ * that of element b V + v of the generator above: a draw from softmax(z).  NaN is
+ * never picked; a row with nothing above -inf has token -1.
+ * All pointers are device pointers; a pointer that is NULL takes the *_all value
+ * for every row (repetition, frequency, presence, temperature), L (history_len),
+ * 0 (prompt_len), or leaves its control out (history, bias, mask, out, tokens).
+ * out may be logits.  Strides are in elements (mask: words); a bias_stride or
+ * mask_stride of 0 shares one row.  Asynchronous.
+ * Errors: CK_ERR_INVALID_ARG (types, sizes, NULL logits, neither out nor
+ * tokens), CK_ERR_UNSUPPORTED (V >= 2^31, B > 65535), CK_ERR_CUDA.
+ */
+typedef struct {
+    const void *logits;
+    int64_t dtype, B, V, logits_stride;
+    const void *history, *history_len, *prompt_len; /* all int32 or all int64 (history_bits) */
+    int64_t history_bits, L, history_stride;
+    const float *repetition, *frequency, *presence, *temperature; /* [B] */
+    float repetition_all, frequency_all, presence_all, temperature_all;
+    const float *bias;
+    int64_t bias_stride;
+    const int32_t *mask;
+    int64_t mask_stride;
+    void *out;
+    int64_t out_stride;
+    int64_t *tokens;
+    int64_t sample;
+    uint64_t seed, step;
+    const int64_t *step_dev;
+} ck_logit_call;
+ck_status ck_control_logits(const ck_logit_call *call, void *stream);
+
+/*
  * ck_forward_static_scratch -- ck_forward without a scratch buffer: the
  * temporary workspace comes from a 32 MiB array of device memory compiled into
  * the library.  The pages have no counterpart for this call; it exists for

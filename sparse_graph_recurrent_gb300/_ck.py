@@ -26,8 +26,24 @@ GRAPH_EDGES_IN_HOST_MEMORY, GRAPH_TILING = 1, 2  # ck_graph_flag
  BARRIER_FLAGS8, BARRIER_CLUSTER_SYNC, BARRIER_CLUSTER_MBARRIER) = range(7)
 PROBE_BARRIER_WORDS = 16384
 PHASE_PROFILE_CTAS, PHASE_PROFILE_WORDS = 1024, 8  # ck_phase_profile_read
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # ck_dtype
+INT4_GROUPS = (32, 64, 128)
 
 _lib = None
+
+
+class LogitCall(ctypes.Structure):
+    """ck_logit_call: the arguments of ck_control_logits."""
+    _p, _i, _f, _u = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_uint64
+    _fields_ = [("logits", _p), ("dtype", _i), ("B", _i), ("V", _i), ("logits_stride", _i),
+                ("history", _p), ("history_len", _p), ("prompt_len", _p),
+                ("history_bits", _i), ("L", _i), ("history_stride", _i),
+                ("repetition", _p), ("frequency", _p), ("presence", _p), ("temperature", _p),
+                ("repetition_all", _f), ("frequency_all", _f), ("presence_all", _f),
+                ("temperature_all", _f),
+                ("bias", _p), ("bias_stride", _i), ("mask", _p), ("mask_stride", _i),
+                ("out", _p), ("out_stride", _i), ("tokens", _p), ("sample", _i),
+                ("seed", _u), ("step", _u), ("step_dev", _p)]
 
 
 class CKError(RuntimeError):
@@ -57,7 +73,7 @@ def load() -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"libck.so not found at {path}")
     lib = ctypes.CDLL(path)
-    p, i64, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
+    p, i64, sz, u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint64
     psz = ctypes.POINTER(ctypes.c_size_t)
     pi64 = ctypes.POINTER(ctypes.c_int64)
     sig = {
@@ -82,6 +98,11 @@ def load() -> ctypes.CDLL:
         "ck_query_status": [p, p],
         "ck_query_status_static": [p],
         "ck_set_option": [ctypes.c_int, i64],
+        "ck_dropout": [p, p, i64, *[i64] * 9, i64, ctypes.c_double, u64, u64, p, p],
+        "ck_int4_matvec": [p, i64, i64, i64, i64, p, i64, i64, p, i64, i64, p, i64, p, i64, p, i64,
+                           p],
+        "ck_int4_quantize": [p, i64, i64, i64, i64, i64, i64, p, i64, p, i64, i64, p, i64, p],
+        "ck_control_logits": [ctypes.POINTER(LogitCall), p],
         "ck_forward_static_scratch": [p, p, p, p, p, p, i64, i64, i64, p, p, sz, p],
         "ck_probe_read": [p, sz, i64, p, p],
         "ck_probe_gather": [p, i64, i64, p, i64, p, p],
@@ -118,6 +139,13 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+_U64 = (1 << 64) - 1
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _need(t, dtype, name):
@@ -287,6 +315,95 @@ def ck_backward_recompute(handle, edge_values, leak, bias, drives, B, T, microst
         _ptr(d_edge_values), _ptr(d_leak), _ptr(d_bias),
         _ptr(d_drives) if d_drives is not None and d_drives.numel() else None, _ptr(d_state0),
         _ptr(scratch), scratch.numel() * scratch.element_size(), _stream(stream)))
+
+
+def _step_args(step, device):
+    """(host step, device pointer) of a step given as an int or a device int64[1]."""
+    if isinstance(step, torch.Tensor):
+        if step.dtype != torch.int64 or step.numel() != 1 or step.device != device:
+            raise ValueError(f"a step tensor is one int64 on {device}")
+        return 0, step.data_ptr()
+    return int(step) & _U64, None
+
+
+def ck_dropout(x, y, shape, x_strides, y_strides, p: float, seed: int, step=0, locked=False,
+               stream=None):
+    """x and y as [n0][n1][n2] with the given sizes and strides in elements."""
+    if x.dtype not in DTYPES or y.dtype != x.dtype or not x.is_cuda or y.device != x.device:
+        raise ValueError("dropout takes CUDA tensors of float32, bfloat16 or float16, out like x")
+    at, dev = _step_args(step, x.device)
+    _check(load().ck_dropout(x.data_ptr(), y.data_ptr(), DTYPES[x.dtype], *shape, *x_strides,
+                             *y_strides, 1 if locked else 0, p, int(seed) & _U64, at, dev,
+                             _raw_stream(stream)))
+
+
+def _like(t, device, dtype, shape, name):
+    if t.device != device or (dtype is not None and t.dtype != dtype) or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype or 'a tensor'} of shape {tuple(shape)} on {device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _rows(t, name):
+    """Elements between the rows of a 2-D tensor with dense rows."""
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be dense")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
+    """x [M, K], qweight uint8 [V, (K + 1) / 2], scales and zeros [V, ceil(K / group)], y [M, V]."""
+    if x.dtype not in DTYPES or scales.dtype not in DTYPES or not x.is_cuda:
+        raise ValueError("x and scales are CUDA tensors of float32, bfloat16 or float16")
+    if group not in INT4_GROUPS:
+        raise ValueError(f"group_size must be one of {INT4_GROUPS}, not {group}")
+    if x.dim() != 2 or qweight.dim() != 2 or scales.dim() != 2:
+        raise ValueError("x, qweight and scales are 2-D")
+    M, K = x.shape
+    V, dev = qweight.shape[0], x.device
+    if K < 1:
+        raise ValueError("x needs at least one column")
+    G = -(-K // group)
+    _like(qweight, dev, torch.uint8, (V, (K + 1) // 2), "qweight")
+    _like(scales, dev, None, (V, G), "scales")
+    _like(y, dev, x.dtype, (M, V), "out")
+    if zeros is not None:
+        _like(zeros, dev, torch.uint8, (V, G), "zeros")
+    if bias is not None:
+        _like(bias, dev, torch.float32, (V,), "bias")
+        if not bias.is_contiguous():
+            raise ValueError("bias must be contiguous")
+    pitch = qweight.stride(0) if V > 1 else -(-qweight.shape[1] // 16) * 16
+    if qweight.shape[1] > 1 and qweight.stride(1) != 1:
+        raise ValueError("the rows of qweight must be dense")
+    _check(load().ck_int4_matvec(
+        x.data_ptr(), DTYPES[x.dtype], M, K, _rows(x, "x"), qweight.data_ptr(), V, pitch,
+        scales.data_ptr(), DTYPES[scales.dtype], _rows(scales, "scales"),
+        None if zeros is None else zeros.data_ptr(), 0 if zeros is None else _rows(zeros, "zeros"),
+        None if bias is None else bias.data_ptr(), group, y.data_ptr(), _rows(y, "out"),
+        _raw_stream(stream)))
+
+
+def ck_int4_quantize(w, group: int, qweight, scales, zeros, stream=None):
+    """Fills qweight, scales and, unless None (symmetric), zeros from w [V, K]."""
+    if w.dtype not in DTYPES or scales.dtype not in DTYPES or not w.is_cuda or w.dim() != 2:
+        raise ValueError("w (2-D) and scales are CUDA tensors of float32, bfloat16 or float16")
+    if group not in INT4_GROUPS:
+        raise ValueError(f"group_size must be one of {INT4_GROUPS}, not {group}")
+    V, K = w.shape
+    G = -(-K // group)
+    _like(qweight, w.device, torch.uint8, (V, (K + 1) // 2), "qweight")
+    _like(scales, w.device, None, (V, G), "scales")
+    if zeros is not None:
+        _like(zeros, w.device, torch.uint8, (V, G), "zeros")
+    _check(load().ck_int4_quantize(
+        w.data_ptr(), DTYPES[w.dtype], V, K, _rows(w, "w"), group, 1 if zeros is None else 0,
+        qweight.data_ptr(), _rows(qweight, "qweight"), scales.data_ptr(), DTYPES[scales.dtype],
+        _rows(scales, "scales"), None if zeros is None else zeros.data_ptr(),
+        0 if zeros is None else _rows(zeros, "zeros"), _raw_stream(stream)))
+
+
+def ck_control_logits(call: LogitCall, stream=None):
+    _check(load().ck_control_logits(ctypes.byref(call), _raw_stream(stream)))
 
 
 def ck_forward_static_scratch(handle, edge_values, leak, bias, drives, state0, microsteps,

@@ -1,0 +1,45 @@
+// Element types of the readout operators (ck_dtype): conversions to and from
+// the 32-bit floats that all of them compute in.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ck_internal.h"
+
+namespace ck {
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+
+// Rounded once, to nearest even.
+template <typename T> __device__ __forceinline__ T from_float(float v);
+template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+
+inline bool known_dtype(int64_t d) { return d == CK_F32 || d == CK_BF16 || d == CK_F16; }
+inline size_t dtype_size(int64_t d) { return d == CK_F32 ? 4 : 2; }
+
+// f((T *)nullptr) with T the element type of a (checked) ck_dtype.
+template <typename F> auto with_dtype(int64_t d, F &&f) {
+    switch (d) {
+        case CK_BF16: return f((__nv_bfloat16 *)nullptr);
+        case CK_F16: return f((__half *)nullptr);
+        default: return f((float *)nullptr);
+    }
+}
+
+// SMs of the current device (1 when it cannot be asked: the launch then reports why).
+inline int device_sms() {
+    int dev = 0, sms = 1;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 1;
+    return sms;
+}
+
+}  // namespace ck

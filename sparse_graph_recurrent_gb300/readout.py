@@ -1,0 +1,269 @@
+"""From the states of a recurrent token model to its next token: dropout on the
+states while it trains, a 4-bit readout and the controls on its logits while it
+answers (connectome-kernels page, intro: a connectome trained on text).
+
+    h = dropout(out, 0.2, seed, step, locked=True)          # training, differentiable
+    q, scales, zeros = int4_quantize(w_readout)              # once
+    logits = int4_matvec(state, q, scales, zeros)            # [B, N] -> [B, V]
+    tokens = pick_tokens(logits, history, history_len=n, repetition=1.1,
+                         mask=allowed, temperature=0.8, seed=seed, step=step)
+
+Every call runs one kernel on the current stream and returns without waiting.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import _ck
+
+__all__ = ["dropout", "dropout_backward", "int4_quantize", "int4_matvec", "control_logits",
+           "pick_tokens"]
+
+
+def _on(device):
+    """The device's context when it is not the current one already."""
+    return torch.cuda.device(device)
+
+
+def _here(t):
+    return t.device.index == torch.cuda.current_device()
+
+
+# -- dropout ---------------------------------------------------------------------------------
+
+
+def _as3(x, locked):
+    """x as [n0][n1][n2] (with its first axis alone when locked): (x, sizes,
+    strides); a copy where its axes do not join into that many."""
+    if x.dim() == 0:
+        x = x.view(1)
+    if x.is_contiguous():
+        n = x.numel()
+        if not locked:
+            return x, (1, 1, n), (0, 0, 1)
+        n0 = x.shape[0]
+        m = n // n0 if n0 else 0
+        return x, (n0, 1, m), (m, 0, 1)
+    dims = [(n, s) for n, s in zip(x.shape, x.stride())]
+    head, dims = (dims[:1], dims[1:]) if locked else ([], dims)
+    joined = []
+    for n, s in dims:
+        if n == 1:
+            continue
+        if joined and joined[-1][1] == s * n:
+            joined[-1] = (joined[-1][0] * n, s)
+        else:
+            joined.append((n, s))
+    if len(head) + len(joined) > 3:
+        return _as3(x.contiguous(), locked)
+    joined = [(1, 0)] * (3 - len(head) - len(joined)) + joined
+    dims = head + joined
+    return x, tuple(n for n, _ in dims), tuple(s for _, s in dims)
+
+
+def _dropout(x, p, seed, step, locked):
+    if not x.is_cuda:
+        raise ValueError("dropout takes CUDA tensors")
+    if locked and x.dim() < 2:
+        raise ValueError("a locked mask is shared along the first of at least two dimensions")
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    x, (n0, n1, n2), strides = _as3(x, locked)
+    args = (x, y, (n0, n1, n2), strides, (n1 * n2, n2, 1), p, seed, step, locked)
+    if _here(x):
+        _ck.ck_dropout(*args)
+    else:
+        with _on(x.device):
+            _ck.ck_dropout(*args)
+    return y
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, seed, step, locked):
+        if isinstance(step, torch.Tensor):
+            step = step.clone()  # the backward's mask is this forward's, wherever the counter is by then
+        ctx.args = (p, seed, step, locked)
+        return _dropout(x.detach(), p, seed, step, locked)
+
+    @staticmethod
+    def backward(ctx, d_out):
+        return _dropout(d_out, *ctx.args), None, None, None, None
+
+
+def dropout(x, p: float, seed: int, step=0, locked: bool = False):
+    """x with each element kept and scaled by 1 / (1 - p), or set to 0 with
+    probability p, differentiable in x.  The mask follows from (seed, step) and
+    an element's index and is stored nowhere; give every call of a program a
+    seed of its own and every training step another `step`, an int or a device
+    int64[1] that ck_step_advance counts up (also inside a captured step).
+    With locked=True one mask serves every entry of the first dimension, as for
+    the T input steps of out[T, B, N].  float32, bfloat16 or float16, any strides."""
+    if torch.is_grad_enabled() and x.requires_grad:
+        return _Dropout.apply(x, p, seed, step, locked)
+    return _dropout(x, p, seed, step, locked)
+
+
+def dropout_backward(d_out, p: float, seed: int, step=0, locked: bool = False):
+    """The gradient of dropout's x from its output's: the same mask again."""
+    return _dropout(d_out, p, seed, step, locked)
+
+
+# -- the 4-bit readout -----------------------------------------------------------------------
+
+
+def int4_quantize(w, group_size: int = 128, symmetric: bool = True, scale_dtype=None):
+    """4-bit weights of w [V, K] in groups of 32, 64 or 128 along K: (qweight,
+    scales, zeros) for int4_matvec, zeros None when symmetric.  qweight is uint8
+    [V, (K + 1) // 2], low nibble first, its rows at a multiple of 16 bytes;
+    scales [V, ceil(K / group_size)] in scale_dtype (w's by default)."""
+    if w.dim() != 2 or w.shape[1] < 1 or not w.is_cuda:
+        raise ValueError("w must be a CUDA tensor [V, K] with K >= 1")
+    if group_size not in _ck.INT4_GROUPS:
+        raise ValueError(f"group_size must be one of {_ck.INT4_GROUPS}, not {group_size}")
+    w = w.detach()
+    if w.shape[1] > 1 and w.stride(1) != 1:
+        w = w.contiguous()
+    V, K = w.shape
+    G, n = -(-K // group_size), (K + 1) // 2
+    q = torch.zeros((V, -(-n // 16) * 16), dtype=torch.uint8, device=w.device)[:, :n]
+    scales = torch.empty((V, G), dtype=scale_dtype or w.dtype, device=w.device)
+    zeros = None if symmetric else torch.empty((V, G), dtype=torch.uint8, device=w.device)
+    with _on(w.device):
+        _ck.ck_int4_quantize(w, group_size, q, scales, zeros)
+    return q, scales, zeros
+
+
+def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128, out=None):
+    """x [..., K] times the transpose of the 4-bit weights (int4_quantize), plus
+    bias (float32 [V]): [..., V] in x's type.  For a few rows of x at a time, as
+    when answering; it has no gradient.  `out`, if given, is written instead of a
+    new tensor."""
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("int4_matvec has no gradient: call it under no_grad or on a detached x")
+    if x.dim() < 1 or qweight.dim() != 2:
+        raise ValueError("x is [..., K] and qweight [V, (K + 1) // 2]")
+    V = qweight.shape[0]
+    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    if x2.shape[1] > 1 and x2.stride(1) != 1:
+        x2 = x2.contiguous()
+    if out is None:
+        y = torch.empty((x2.shape[0], V), dtype=x.dtype, device=x.device)
+    else:
+        if tuple(out.shape) != (*x.shape[:-1], V):
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(*x.shape[:-1], V)}")
+        y = out if out.dim() == 2 else out.view(-1, V)
+    if not x.is_cuda:
+        raise ValueError("int4_matvec takes CUDA tensors")
+    if _here(x):
+        _ck.ck_int4_matvec(x2, qweight, scales, zeros, bias, group_size, y)
+    else:
+        with _on(x.device):
+            _ck.ck_int4_matvec(x2, qweight, scales, zeros, bias, group_size, y)
+    if out is not None:
+        return out
+    return y if x.dim() == 2 else y.view(*x.shape[:-1], V)
+
+
+# -- controls on logits, and the token -------------------------------------------------------
+
+
+def _per_row(call, name, v, B, device, low):
+    """A control given as one number or as float32 [B]."""
+    if isinstance(v, torch.Tensor):
+        if v.dtype != torch.float32 or v.shape != (B,) or v.device != device or not v.is_contiguous():
+            raise ValueError(f"{name} must be a number or a contiguous float32 [{B}] on {device}")
+        setattr(call, name, v.data_ptr())
+        return
+    v = float(v)
+    if not (v >= low and v < math.inf):
+        raise ValueError(f"{name} = {v} is out of range")
+    setattr(call, name + "_all", v)
+
+
+def _control(logits, history, history_len, prompt_len, repetition, frequency, presence, bias, mask,
+             temperature, out, tokens, seed, step):
+    if not logits.is_cuda or logits.dtype not in _ck.DTYPES or logits.dim() != 2:
+        raise ValueError("logits must be a CUDA tensor [B, V] of float32, bfloat16 or float16")
+    if logits.requires_grad and torch.is_grad_enabled():
+        raise ValueError("the logit controls have no gradient: call them under no_grad")
+    B, V = logits.shape
+    dev = logits.device
+    c = _ck.LogitCall(logits=logits.data_ptr(), dtype=_ck.DTYPES[logits.dtype], B=B, V=V,
+                      logits_stride=_ck._rows(logits, "logits"))
+    if history is not None:
+        it = history.dtype
+        if it not in (torch.int64, torch.int32) or history.dim() != 2 or history.shape[0] != B or history.device != dev:
+            raise ValueError(f"history must be int64 or int32 [{B}, L] on {dev}")
+        c.history, c.history_bits = history.data_ptr(), 64 if it == torch.int64 else 32
+        c.L, c.history_stride = history.shape[1], _ck._rows(history, "history")
+        for name, t in (("history_len", history_len), ("prompt_len", prompt_len)):
+            if t is None:
+                continue
+            if t.dtype != it or t.shape != (B,) or t.device != dev or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {it} [{B}] on {dev}")
+            setattr(c, name, t.data_ptr())
+    elif history_len is not None or prompt_len is not None:
+        raise ValueError("history_len and prompt_len need a history")
+    _per_row(c, "repetition", 1.0 if repetition is None else repetition, B, dev, 1e-30)
+    _per_row(c, "frequency", 0.0 if frequency is None else frequency, B, dev, -1e30)
+    _per_row(c, "presence", 0.0 if presence is None else presence, B, dev, -1e30)
+    _per_row(c, "temperature", 1.0 if temperature is None else temperature, B, dev, 0.0)
+    for name, t, n, dt in (("bias", bias, V, torch.float32), ("mask", mask, -(-V // 32), torch.int32)):
+        if t is None:
+            continue
+        if t.dtype != dt or t.device != dev or t.shape not in ((n,), (B, n)):
+            raise ValueError(f"{name} must be {dt} [{n}] or [{B}, {n}] on {dev}")
+        if n > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the rows of {name} must be dense")
+        setattr(c, name, t.data_ptr())
+        setattr(c, name + "_stride", t.stride(0) if t.dim() == 2 else 0)
+    if out is not None:
+        if out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev:
+            raise ValueError("out must be like logits")
+        c.out, c.out_stride = out.data_ptr(), _ck._rows(out, "out")
+    if tokens is not None:
+        c.tokens = tokens.data_ptr()
+        if seed is not None:
+            c.sample, c.seed = 1, int(seed) & _ck._U64
+            c.step, c.step_dev = _ck._step_args(step, dev)
+    if _here(logits):
+        _ck.ck_control_logits(c)
+    else:
+        with _on(dev):
+            _ck.ck_control_logits(c)
+
+
+def control_logits(logits, history=None, history_len=None, prompt_len=None, repetition=None,
+                   frequency=None, presence=None, bias=None, mask=None, temperature=None, out=None):
+    """logits [B, V] with the controls of an answering loop, in this order: the
+    repetition penalty on every token of history[b, :history_len[b]] (z / r where
+    z > 0, else z * r), frequency and presence penalties by its count in
+    history[b, prompt_len[b]:history_len[b]], bias (float32 [V] or [B, V]), mask
+    (int32 words [ceil(V / 32)] or [B, ceil(V / 32)], bit v % 32 of word v // 32
+    allows token v, else -inf), then division by temperature (not where it is 0).
+    Penalties and temperature are numbers or float32 [B]; history int64 or int32
+    [B, L], ids outside [0, V) ignored; lengths [B] in its type."""
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    _control(logits, history, history_len, prompt_len, repetition, frequency, presence, bias, mask,
+             temperature, out, None, None, 0)
+    return out
+
+
+def pick_tokens(logits, history=None, history_len=None, prompt_len=None, repetition=None,
+                frequency=None, presence=None, bias=None, mask=None, temperature=None, seed=None,
+                step=0, return_logits: bool = False, out=None):
+    """The next token of each row (int64 [B]) after control_logits's controls, in
+    one pass: the largest logit (the lowest token among equal ones) or, given a
+    seed, a draw from their softmax in the rows whose temperature is above 0.  A
+    row with no token left gives -1.  `step` as in dropout: another one for
+    every token drawn.  With return_logits=True, or an `out` to write them to,
+    (tokens, controlled logits)."""
+    if out is None and return_logits:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    tokens = torch.empty(logits.shape[:1], dtype=torch.int64, device=logits.device)
+    _control(logits, history, history_len, prompt_len, repetition, frequency, presence, bias, mask,
+             temperature, out, tokens, seed, step)
+    return tokens if out is None else (tokens, out)

@@ -1,0 +1,160 @@
+"""Readout operators without a GPU: the oracle's generator against the published
+known answers, the view logic of dropout, and refusals made on the host."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import readout_oracle as ro
+
+
+@pytest.mark.parametrize("ctr,key,want", [
+    ((0, 0, 0, 0), (0, 0), (0x6627e8d5, 0xe169c58d, 0xbc57ac4c, 0x9b00dbd8)),
+    ((0xffffffff,) * 4, (0xffffffff,) * 2, (0x408f276d, 0x41c83b0e, 0xa20bc7c6, 0x6d5451fd)),
+    ((0x243f6a88, 0x85a308d3, 0x13198a2e, 0x03707344), (0xa4093822, 0x299f31d0),
+     (0xd16cfe09, 0x94fdcceb, 0x5001e420, 0x24126ea1)),
+])
+def test_oracle_generator_gives_the_published_answers(ctr, key, want):
+    # the block's index is counter words 0 and 1; an element index is four times it, so
+    # blocks above 2^62 are reached through the words directly
+    block, step = ctr[0] | ctr[1] << 32, ctr[2] | ctr[3] << 32
+    if block < 1 << 62:
+        got = ro.philox_words(np.arange(4, dtype=np.uint64) + np.uint64(4 * block),
+                              key[0] | key[1] << 32, step)
+    else:
+        c = list(ctr)
+        k = list(key)
+        for _ in range(10):
+            a, b = c[0] * 0xD2511F53, c[2] * 0xCD9E8D57
+            c = [(b >> 32) ^ c[1] ^ k[0], b & ro.M32, (a >> 32) ^ c[3] ^ k[1], a & ro.M32]
+            k = [(k[0] + 0x9E3779B9) & ro.M32, (k[1] + 0xBB67AE85) & ro.M32]
+        got = c
+    assert [int(v) for v in got] == list(want)
+
+
+@pytest.mark.parametrize("locked", [False, True])
+@pytest.mark.parametrize("make", [
+    lambda b: b[:6 * 4 * 5].view(6, 4, 5),
+    lambda b: b[:6 * 4 * 9].view(6, 4, 9)[..., :5],
+    lambda b: b[:6 * 4 * 5].view(4, 6, 5).transpose(0, 1),
+    lambda b: b[:6 * 4 * 5].view(5, 4, 6).permute(2, 1, 0),
+    lambda b: b[:5].view(1, 1, 5).expand(6, 4, 5),
+    lambda b: b[:2 * 3 * 4 * 10].view(2, 3, 4, 10)[:, :, 1:3, ::2],
+    lambda b: b[:240].view(3, 2, 2, 20)[:, :, ::2].permute(0, 3, 1, 2),
+    lambda b: b[:1].view(1, 1),
+    lambda b: b[:40].view(4, 10)[:, ::3],
+])
+def test_views_join_into_three_axes(make, locked):
+    """The sizes and strides name the same elements, in the same order, as the tensor."""
+    from sparse_graph_recurrent_gb300.readout import _as3
+    x = make(torch.arange(1000))
+    y, n, s = _as3(x, locked)
+    got = torch.as_strided(y, n, s, y.storage_offset())
+    assert torch.equal(got.reshape(-1), x.reshape(-1))
+    if locked:
+        assert n[0] == x.shape[0]
+
+
+def _lib():
+    from sparse_graph_recurrent_gb300 import _ck
+    return _ck, _ck.load()
+
+
+def test_dropout_refuses_on_the_host():
+    _, lib = _lib()
+    buf = (ctypes.c_float * 8)()
+
+    def call(dtype=0, n=(1, 1, 8), p=0.5, x=buf, y=buf):
+        return lib.ck_dropout(x, y, dtype, *n, 0, 0, 1, 0, 0, 1, 0, p, 1, 1, None, None)
+
+    assert call(dtype=3) == 1 and call(dtype=-1) == 1
+    for p in (-0.1, 1.0001, float("nan"), float("inf")):
+        assert call(p=p) == 1
+        assert b"p must" in lib.ck_last_error_message()
+    assert call(n=(1, -1, 8)) == 1
+    assert call(x=None) == 1 and call(y=None) == 1
+    assert call(n=(1 << 40, 1 << 40, 1)) == 7
+    assert call(n=(0, 4, 8)) == 0 and call(n=(4, 0, 8), x=None, y=None) == 0  # nothing to do
+
+
+def test_int4_refuses_on_the_host():
+    _, lib = _lib()
+    raw = ctypes.create_string_buffer(4096)
+    base = -(-ctypes.addressof(raw) // 16) * 16
+
+    def call(x=base, dtype=0, M=1, K=64, xs=64, q=base, V=2, pitch=32, s=base, sdt=0, ss=2, z=None,
+             zs=0, group=32, y=base, ys=2):
+        return lib.ck_int4_matvec(x, dtype, M, K, xs, q, V, pitch, s, sdt, ss, z, zs, None, group, y,
+                                  ys, None)
+
+    assert call(dtype=5) == 1 and call(sdt=9) == 1
+    for g in (0, 16, 33, 256, -32):
+        assert call(group=g) == 1
+    assert call(K=0) == 1 and call(M=-1) == 1 and call(V=-1) == 1
+    assert call(x=None) == 1 and call(q=None) == 1 and call(s=None) == 1 and call(y=None) == 1
+    assert call(pitch=40) == 1 and call(q=base + 8) == 1 and call(pitch=16) == 1
+    assert b"16 bytes" in lib.ck_last_error_message()
+    assert call(ss=1) == 1 and call(ys=1) == 1 and call(z=base, zs=1) == 1
+    assert call(K=1 << 30) == 7
+    assert call(M=0) == 0 and call(V=0) == 0
+    assert lib.ck_int4_quantize(base, 0, 2, 64, 64, 48, 1, base, 32, base, 0, 2, None, 0, None) == 1
+    assert lib.ck_int4_quantize(base, 0, 2, 64, 64, 32, 0, base, 32, base, 0, 2, None, 0, None) == 1
+    assert lib.ck_int4_quantize(base, 0, 2, 64, 64, 32, 1, base, 31, base, 0, 2, None, 0, None) == 1
+    assert lib.ck_int4_quantize(base, 0, 0, 64, 64, 32, 1, base, 32, base, 0, 2, None, 0, None) == 0
+
+
+def test_control_logits_refuses_on_the_host():
+    _ck, lib = _lib()
+    buf = (ctypes.c_float * 8)()
+    at = ctypes.addressof(buf)
+
+    def call(**kw):
+        args = dict(logits=at, dtype=0, B=1, V=8, logits_stride=8, out=at, out_stride=8,
+                    repetition_all=1.0, temperature_all=1.0)
+        args.update(kw)
+        return lib.ck_control_logits(ctypes.byref(_ck.LogitCall(**args)), None)
+
+    assert lib.ck_control_logits(None, None) == 1
+    assert call(dtype=4) == 1 and call(V=0) == 1 and call(B=-1) == 1
+    assert call(logits=None) == 1 and call(out=None) == 1
+    assert call(history=at, history_bits=16, L=4) == 1 and call(history=at, history_bits=32, L=-1) == 1
+    assert call(V=1 << 31) == 7 and call(B=1 << 17) == 7
+    assert call(B=0) == 0
+
+
+def test_struct_matches_the_header():
+    """ck_logit_call's fields, in order, are the binding's."""
+    import os
+    import re
+
+    from sparse_graph_recurrent_gb300 import _ck
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(root, "include", "ck.h")).read(), flags=re.S)
+    body = re.search(r"typedef struct \{([^}]*)\} ck_logit_call;", text).group(1)
+    kinds = {"int64_t": ctypes.c_int64, "uint64_t": ctypes.c_uint64, "float": ctypes.c_float}
+    want = []
+    for line in body.split(";"):
+        m = re.match(r"\s*((?:const )?\w+)\s+(.*)", line.strip(), flags=re.S)
+        if not m:
+            continue
+        for name in m.group(2).split(","):
+            name = name.strip()
+            kind = ctypes.c_void_p if name.startswith("*") else kinds[m.group(1)]
+            want.append((name.lstrip("*"), kind))
+    assert want == [(n, k) for n, k in _ck.LogitCall._fields_]
+
+
+def test_cpu_tensors_are_refused():
+    import sparse_graph_recurrent_gb300 as ck
+    x = torch.zeros(2, 64)
+    with pytest.raises(ValueError):
+        ck.dropout(x, 0.5, 1)
+    with pytest.raises(ValueError):
+        ck.int4_quantize(x)
+    with pytest.raises(ValueError):
+        ck.int4_matvec(x, torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 1))
+    with pytest.raises(ValueError):
+        ck.control_logits(x)
+    with pytest.raises(ValueError):
+        ck.pick_tokens(x)
