@@ -144,8 +144,19 @@ def _stream(stream):
 _U64 = (1 << 64) - 1
 
 
+# The current device's current stream as a plain integer.  The call torch's own
+# code generators use costs 0.1 us, building a Stream object 3 us, on a path of
+# about 8; the public way stays for a torch that lacks it.
+_get_device = torch.cuda.current_device
+_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _get_raw_stream is not None:
+        return _get_raw_stream(_get_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _need(t, dtype, name):
@@ -317,11 +328,11 @@ def ck_backward_recompute(handle, edge_values, leak, bias, drives, B, T, microst
         _ptr(scratch), scratch.numel() * scratch.element_size(), _stream(stream)))
 
 
-def _step_args(step, device):
+def _step_args(step, device: int):
     """(host step, device pointer) of a step given as an int or a device int64[1]."""
     if isinstance(step, torch.Tensor):
-        if step.dtype != torch.int64 or step.numel() != 1 or step.device != device:
-            raise ValueError(f"a step tensor is one int64 on {device}")
+        if step.dtype != torch.int64 or step.numel() != 1 or step.get_device() != device:
+            raise ValueError(f"a step tensor is one int64 on cuda:{device}")
         return 0, step.data_ptr()
     return int(step) & _U64, None
 
@@ -329,25 +340,27 @@ def _step_args(step, device):
 def ck_dropout(x, y, shape, x_strides, y_strides, p: float, seed: int, step=0, locked=False,
                stream=None):
     """x and y as [n0][n1][n2] with the given sizes and strides in elements."""
-    if x.dtype not in DTYPES or y.dtype != x.dtype or not x.is_cuda or y.device != x.device:
+    dtype, device = DTYPES.get(x.dtype), x.get_device()
+    if dtype is None or device < 0 or y.dtype != x.dtype or y.get_device() != device:
         raise ValueError("dropout takes CUDA tensors of float32, bfloat16 or float16, out like x")
-    at, dev = _step_args(step, x.device)
-    _check(load().ck_dropout(x.data_ptr(), y.data_ptr(), DTYPES[x.dtype], *shape, *x_strides,
-                             *y_strides, 1 if locked else 0, p, int(seed) & _U64, at, dev,
-                             _raw_stream(stream)))
+    at, dev = _step_args(step, device)
+    _check((_lib or load()).ck_dropout(
+        x.data_ptr(), y.data_ptr(), dtype, *shape, *x_strides, *y_strides, 1 if locked else 0, p,
+        int(seed) & _U64, at, dev, _raw_stream(stream)))
 
 
-def _like(t, device, dtype, shape, name):
-    if t.device != device or (dtype is not None and t.dtype != dtype) or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype or 'a tensor'} of shape {tuple(shape)} on {device}, "
-                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+def _like(t, device: int, dtype, shape, name):
+    if t.get_device() != device or (dtype is not None and t.dtype != dtype) or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype or 'a tensor'} of shape {tuple(shape)} on "
+                         f"cuda:{device}, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _rows(t, name):
     """Elements between the rows of a 2-D tensor with dense rows."""
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    (n, m), (pitch, one) = t.shape, t.stride()
+    if one != 1 and m > 1:
         raise ValueError(f"the rows of {name} must be dense")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return pitch if n > 1 else m
 
 
 def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
@@ -359,7 +372,7 @@ def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
     if x.dim() != 2 or qweight.dim() != 2 or scales.dim() != 2:
         raise ValueError("x, qweight and scales are 2-D")
     M, K = x.shape
-    V, dev = qweight.shape[0], x.device
+    V, dev = qweight.shape[0], x.get_device()
     if K < 1:
         raise ValueError("x needs at least one column")
     G = -(-K // group)
@@ -372,10 +385,11 @@ def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
         _like(bias, dev, torch.float32, (V,), "bias")
         if not bias.is_contiguous():
             raise ValueError("bias must be contiguous")
-    pitch = qweight.stride(0) if V > 1 else -(-qweight.shape[1] // 16) * 16
+    # a single row may be of any pitch
+    pitch = _rows(qweight, "qweight") if V > 1 else -(-qweight.shape[1] // 16) * 16
     if qweight.shape[1] > 1 and qweight.stride(1) != 1:
         raise ValueError("the rows of qweight must be dense")
-    _check(load().ck_int4_matvec(
+    _check((_lib or load()).ck_int4_matvec(
         x.data_ptr(), DTYPES[x.dtype], M, K, _rows(x, "x"), qweight.data_ptr(), V, pitch,
         scales.data_ptr(), DTYPES[scales.dtype], _rows(scales, "scales"),
         None if zeros is None else zeros.data_ptr(), 0 if zeros is None else _rows(zeros, "zeros"),
@@ -390,11 +404,11 @@ def ck_int4_quantize(w, group: int, qweight, scales, zeros, stream=None):
     if group not in INT4_GROUPS:
         raise ValueError(f"group_size must be one of {INT4_GROUPS}, not {group}")
     V, K = w.shape
-    G = -(-K // group)
-    _like(qweight, w.device, torch.uint8, (V, (K + 1) // 2), "qweight")
-    _like(scales, w.device, None, (V, G), "scales")
+    G, dev = -(-K // group), w.get_device()
+    _like(qweight, dev, torch.uint8, (V, (K + 1) // 2), "qweight")
+    _like(scales, dev, None, (V, G), "scales")
     if zeros is not None:
-        _like(zeros, w.device, torch.uint8, (V, G), "zeros")
+        _like(zeros, dev, torch.uint8, (V, G), "zeros")
     _check(load().ck_int4_quantize(
         w.data_ptr(), DTYPES[w.dtype], V, K, _rows(w, "w"), group, 1 if zeros is None else 0,
         qweight.data_ptr(), _rows(qweight, "qweight"), scales.data_ptr(), DTYPES[scales.dtype],
@@ -403,7 +417,7 @@ def ck_int4_quantize(w, group: int, qweight, scales, zeros, stream=None):
 
 
 def ck_control_logits(call: LogitCall, stream=None):
-    _check(load().ck_control_logits(ctypes.byref(call), _raw_stream(stream)))
+    _check((_lib or load()).ck_control_logits(ctypes.byref(call), _raw_stream(stream)))
 
 
 def ck_forward_static_scratch(handle, edge_values, leak, bias, drives, state0, microsteps,

@@ -22,13 +22,9 @@ __all__ = ["dropout", "dropout_backward", "int4_quantize", "int4_matvec", "contr
            "pick_tokens"]
 
 
-def _on(device):
-    """The device's context when it is not the current one already."""
-    return torch.cuda.device(device)
-
-
-def _here(t):
-    return t.device.index == torch.cuda.current_device()
+def _here(device: int):
+    """Whether a tensor's device (get_device()) is the current one."""
+    return device == torch.cuda.current_device()
 
 
 # -- dropout ---------------------------------------------------------------------------------
@@ -37,8 +33,6 @@ def _here(t):
 def _as3(x, locked):
     """x as [n0][n1][n2] (with its first axis alone when locked): (x, sizes,
     strides); a copy where its axes do not join into that many."""
-    if x.dim() == 0:
-        x = x.view(1)
     if x.is_contiguous():
         n = x.numel()
         if not locked:
@@ -64,17 +58,18 @@ def _as3(x, locked):
 
 
 def _dropout(x, p, seed, step, locked):
-    if not x.is_cuda:
+    device = x.get_device()
+    if device < 0:
         raise ValueError("dropout takes CUDA tensors")
     if locked and x.dim() < 2:
         raise ValueError("a locked mask is shared along the first of at least two dimensions")
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    x, (n0, n1, n2), strides = _as3(x, locked)
-    args = (x, y, (n0, n1, n2), strides, (n1 * n2, n2, 1), p, seed, step, locked)
-    if _here(x):
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    x, shape, strides = _as3(x, locked)
+    args = (x, y, shape, strides, (shape[1] * shape[2], shape[2], 1), p, seed, step, locked)
+    if _here(device):
         _ck.ck_dropout(*args)
     else:
-        with _on(x.device):
+        with torch.cuda.device(device):
             _ck.ck_dropout(*args)
     return y
 
@@ -100,7 +95,7 @@ def dropout(x, p: float, seed: int, step=0, locked: bool = False):
     int64[1] that ck_step_advance counts up (also inside a captured step).
     With locked=True one mask serves every entry of the first dimension, as for
     the T input steps of out[T, B, N].  float32, bfloat16 or float16, any strides."""
-    if torch.is_grad_enabled() and x.requires_grad:
+    if x.requires_grad and torch.is_grad_enabled():
         return _Dropout.apply(x, p, seed, step, locked)
     return _dropout(x, p, seed, step, locked)
 
@@ -130,7 +125,7 @@ def int4_quantize(w, group_size: int = 128, symmetric: bool = True, scale_dtype=
     q = torch.zeros((V, -(-n // 16) * 16), dtype=torch.uint8, device=w.device)[:, :n]
     scales = torch.empty((V, G), dtype=scale_dtype or w.dtype, device=w.device)
     zeros = None if symmetric else torch.empty((V, G), dtype=torch.uint8, device=w.device)
-    with _on(w.device):
+    with torch.cuda.device(w.device):
         _ck.ck_int4_quantize(w, group_size, q, scales, zeros)
     return q, scales, zeros
 
@@ -142,6 +137,9 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
     new tensor."""
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError("int4_matvec has no gradient: call it under no_grad or on a detached x")
+    device = x.get_device()
+    if device < 0:
+        raise ValueError("int4_matvec takes CUDA tensors")
     if x.dim() < 1 or qweight.dim() != 2:
         raise ValueError("x is [..., K] and qweight [V, (K + 1) // 2]")
     V = qweight.shape[0]
@@ -149,18 +147,17 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
     if x2.shape[1] > 1 and x2.stride(1) != 1:
         x2 = x2.contiguous()
     if out is None:
-        y = torch.empty((x2.shape[0], V), dtype=x.dtype, device=x.device)
+        y = x.new_empty((x2.shape[0], V))
     else:
         if tuple(out.shape) != (*x.shape[:-1], V):
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(*x.shape[:-1], V)}")
         y = out if out.dim() == 2 else out.view(-1, V)
-    if not x.is_cuda:
-        raise ValueError("int4_matvec takes CUDA tensors")
-    if _here(x):
-        _ck.ck_int4_matvec(x2, qweight, scales, zeros, bias, group_size, y)
+    args = (x2, qweight, scales, zeros, bias, group_size, y)
+    if _here(device):
+        _ck.ck_int4_matvec(*args)
     else:
-        with _on(x.device):
-            _ck.ck_int4_matvec(x2, qweight, scales, zeros, bias, group_size, y)
+        with torch.cuda.device(device):
+            _ck.ck_int4_matvec(*args)
     if out is not None:
         return out
     return y if x.dim() == 2 else y.view(*x.shape[:-1], V)
@@ -169,70 +166,86 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
 # -- controls on logits, and the token -------------------------------------------------------
 
 
-def _per_row(call, name, v, B, device, low):
-    """A control given as one number or as float32 [B]."""
+def _per_row(name, v, default, low, B, device):
+    """(pointer, number) of a control given as one number or as float32 [B]."""
+    if v is None:
+        return None, default
     if isinstance(v, torch.Tensor):
-        if v.dtype != torch.float32 or v.shape != (B,) or v.device != device or not v.is_contiguous():
-            raise ValueError(f"{name} must be a number or a contiguous float32 [{B}] on {device}")
-        setattr(call, name, v.data_ptr())
-        return
+        if v.dtype != torch.float32 or v.shape != (B,) or v.get_device() != device or not v.is_contiguous():
+            raise ValueError(f"{name} must be a number or a contiguous float32 [{B}] on cuda:{device}")
+        return v.data_ptr(), default
     v = float(v)
-    if not (v >= low and v < math.inf):
+    if not low <= v < math.inf:
         raise ValueError(f"{name} = {v} is out of range")
-    setattr(call, name + "_all", v)
+    return None, v
+
+
+def _lengths(name, t, dtype, B, device):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != (B,) or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} [{B}] on cuda:{device}")
+    return t.data_ptr()
+
+
+def _per_token(name, t, dtype, B, n, device):
+    """(pointer, row stride) of a [n] or [B, n] operand."""
+    if t is None:
+        return None, 0
+    shape, strides = t.shape, t.stride()
+    if t.dtype != dtype or t.get_device() != device or shape != (B, n) and shape != (n,):
+        raise ValueError(f"{name} must be {dtype} [{n}] or [{B}, {n}] on cuda:{device}")
+    if n > 1 and strides[-1] != 1:
+        raise ValueError(f"the rows of {name} must be dense")
+    return t.data_ptr(), strides[0] if len(shape) == 2 else 0
 
 
 def _control(logits, history, history_len, prompt_len, repetition, frequency, presence, bias, mask,
              temperature, out, tokens, seed, step):
-    if not logits.is_cuda or logits.dtype not in _ck.DTYPES or logits.dim() != 2:
+    dtype, dev = _ck.DTYPES.get(logits.dtype), logits.get_device()
+    if dtype is None or dev < 0 or logits.dim() != 2:
         raise ValueError("logits must be a CUDA tensor [B, V] of float32, bfloat16 or float16")
     if logits.requires_grad and torch.is_grad_enabled():
         raise ValueError("the logit controls have no gradient: call them under no_grad")
     B, V = logits.shape
-    dev = logits.device
-    c = _ck.LogitCall(logits=logits.data_ptr(), dtype=_ck.DTYPES[logits.dtype], B=B, V=V,
-                      logits_stride=_ck._rows(logits, "logits"))
+    text = text_len = prompt = None
+    bits = L = text_stride = 0
     if history is not None:
         it = history.dtype
-        if it not in (torch.int64, torch.int32) or history.dim() != 2 or history.shape[0] != B or history.device != dev:
-            raise ValueError(f"history must be int64 or int32 [{B}, L] on {dev}")
-        c.history, c.history_bits = history.data_ptr(), 64 if it == torch.int64 else 32
-        c.L, c.history_stride = history.shape[1], _ck._rows(history, "history")
-        for name, t in (("history_len", history_len), ("prompt_len", prompt_len)):
-            if t is None:
-                continue
-            if t.dtype != it or t.shape != (B,) or t.device != dev or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {it} [{B}] on {dev}")
-            setattr(c, name, t.data_ptr())
+        if (it is not torch.int64 and it is not torch.int32 or history.dim() != 2
+                or history.shape[0] != B or history.get_device() != dev):
+            raise ValueError(f"history must be int64 or int32 [{B}, L] on cuda:{dev}")
+        text, bits, L = history.data_ptr(), 64 if it is torch.int64 else 32, history.shape[1]
+        text_stride = _ck._rows(history, "history")
+        text_len = _lengths("history_len", history_len, it, B, dev)
+        prompt = _lengths("prompt_len", prompt_len, it, B, dev)
     elif history_len is not None or prompt_len is not None:
         raise ValueError("history_len and prompt_len need a history")
-    _per_row(c, "repetition", 1.0 if repetition is None else repetition, B, dev, 1e-30)
-    _per_row(c, "frequency", 0.0 if frequency is None else frequency, B, dev, -1e30)
-    _per_row(c, "presence", 0.0 if presence is None else presence, B, dev, -1e30)
-    _per_row(c, "temperature", 1.0 if temperature is None else temperature, B, dev, 0.0)
-    for name, t, n, dt in (("bias", bias, V, torch.float32), ("mask", mask, -(-V // 32), torch.int32)):
-        if t is None:
-            continue
-        if t.dtype != dt or t.device != dev or t.shape not in ((n,), (B, n)):
-            raise ValueError(f"{name} must be {dt} [{n}] or [{B}, {n}] on {dev}")
-        if n > 1 and t.stride(-1) != 1:
-            raise ValueError(f"the rows of {name} must be dense")
-        setattr(c, name, t.data_ptr())
-        setattr(c, name + "_stride", t.stride(0) if t.dim() == 2 else 0)
+    rep, rep_all = _per_row("repetition", repetition, 1.0, 1e-30, B, dev)
+    freq, freq_all = _per_row("frequency", frequency, 0.0, -1e30, B, dev)
+    pres, pres_all = _per_row("presence", presence, 0.0, -1e30, B, dev)
+    temp, temp_all = _per_row("temperature", temperature, 1.0, 0.0, B, dev)
+    bias_at, bias_stride = _per_token("bias", bias, torch.float32, B, V, dev)
+    mask_at, mask_stride = _per_token("mask", mask, torch.int32, B, -(-V // 32), dev)
+    out_at, out_stride = None, 0
     if out is not None:
-        if out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev:
+        if out.dtype != logits.dtype or out.shape != logits.shape or out.get_device() != dev:
             raise ValueError("out must be like logits")
-        c.out, c.out_stride = out.data_ptr(), _ck._rows(out, "out")
-    if tokens is not None:
-        c.tokens = tokens.data_ptr()
-        if seed is not None:
-            c.sample, c.seed = 1, int(seed) & _ck._U64
-            c.step, c.step_dev = _ck._step_args(step, dev)
-    if _here(logits):
-        _ck.ck_control_logits(c)
+        out_at, out_stride = out.data_ptr(), _ck._rows(out, "out")
+    at = step_dev = None
+    if seed is not None:
+        at, step_dev = _ck._step_args(step, dev)
+    call = _ck.LogitCall(
+        logits.data_ptr(), dtype, B, V, _ck._rows(logits, "logits"), text, text_len, prompt, bits, L,
+        text_stride, rep, freq, pres, temp, rep_all, freq_all, pres_all, temp_all, bias_at,
+        bias_stride, mask_at, mask_stride, out_at, out_stride,
+        None if tokens is None else tokens.data_ptr(), 0 if seed is None else 1,
+        0 if seed is None else int(seed) & _ck._U64, at or 0, step_dev)
+    if _here(dev):
+        _ck.ck_control_logits(call)
     else:
-        with _on(dev):
-            _ck.ck_control_logits(c)
+        with torch.cuda.device(dev):
+            _ck.ck_control_logits(call)
 
 
 def control_logits(logits, history=None, history_len=None, prompt_len=None, repetition=None,
@@ -246,7 +259,7 @@ def control_logits(logits, history=None, history_len=None, prompt_len=None, repe
     Penalties and temperature are numbers or float32 [B]; history int64 or int32
     [B, L], ids outside [0, V) ignored; lengths [B] in its type."""
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = torch.empty_like(logits, memory_format=torch.contiguous_format)
     _control(logits, history, history_len, prompt_len, repetition, frequency, presence, bias, mask,
              temperature, out, None, None, 0)
     return out
@@ -262,7 +275,7 @@ def pick_tokens(logits, history=None, history_len=None, prompt_len=None, repetit
     every token drawn.  With return_logits=True, or an `out` to write them to,
     (tokens, controlled logits)."""
     if out is None and return_logits:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = torch.empty_like(logits, memory_format=torch.contiguous_format)
     tokens = torch.empty(logits.shape[:1], dtype=torch.int64, device=logits.device)
     _control(logits, history, history_len, prompt_len, repetition, frequency, presence, bias, mask,
              temperature, out, tokens, seed, step)
