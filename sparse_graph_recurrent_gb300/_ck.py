@@ -100,7 +100,8 @@ def load() -> ctypes.CDLL:
         "ck_set_option": [ctypes.c_int, i64],
         "ck_dropout": [p, p, i64, *[i64] * 9, i64, ctypes.c_double, u64, u64, p, p],
         "ck_int4_matvec": [p, i64, i64, i64, i64, p, i64, i64, p, i64, i64, p, i64, p, i64, p, i64,
-                           p],
+                           p, sz, p],
+        "ck_int4_workspace_size": [i64, i64, i64, i64, psz],
         "ck_int4_quantize": [p, i64, i64, i64, i64, i64, i64, p, i64, p, i64, i64, p, i64, p],
         "ck_control_logits": [ctypes.POINTER(LogitCall), p],
         "ck_forward_static_scratch": [p, p, p, p, p, p, i64, i64, i64, p, p, sz, p],
@@ -363,8 +364,18 @@ def _rows(t, name):
     return pitch if n > 1 else m
 
 
+def ck_int4_workspace_size(dtype, M: int, K: int, V: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().ck_int4_workspace_size(DTYPES[dtype], M, K, V, ctypes.byref(n)))
+    return n.value
+
+
+_int4_ws = {}  # bytes by (device, dtype, M, K, V): sizes only, no memory
+
+
 def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
-    """x [M, K], qweight uint8 [V, (K + 1) / 2], scales and zeros [V, ceil(K / group)], y [M, V]."""
+    """x [M, K], qweight uint8 [V, (K + 1) / 2], scales and zeros [V, ceil(K / group)], y [M, V].
+    The workspace is taken from torch's allocator on the current stream."""
     if x.dtype not in DTYPES or scales.dtype not in DTYPES or not x.is_cuda:
         raise ValueError("x and scales are CUDA tensors of float32, bfloat16 or float16")
     if group not in INT4_GROUPS:
@@ -389,12 +400,21 @@ def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
     pitch = _rows(qweight, "qweight") if V > 1 else -(-qweight.shape[1] // 16) * 16
     if qweight.shape[1] > 1 and qweight.stride(1) != 1:
         raise ValueError("the rows of qweight must be dense")
+    key = (dev, x.dtype, M, K, V)
+    need = _int4_ws.get(key)
+    if need is None:
+        if len(_int4_ws) > 4096:
+            _int4_ws.clear()
+        need = _int4_ws[key] = ck_int4_workspace_size(x.dtype, M, K, V)
+    ws = qweight.new_empty(need) if need else None
+    if ws is not None and stream is not None:
+        ws.record_stream(stream)
     _check((_lib or load()).ck_int4_matvec(
         x.data_ptr(), DTYPES[x.dtype], M, K, _rows(x, "x"), qweight.data_ptr(), V, pitch,
         scales.data_ptr(), DTYPES[scales.dtype], _rows(scales, "scales"),
         None if zeros is None else zeros.data_ptr(), 0 if zeros is None else _rows(zeros, "zeros"),
         None if bias is None else bias.data_ptr(), group, y.data_ptr(), _rows(y, "out"),
-        _raw_stream(stream)))
+        None if ws is None else ws.data_ptr(), need, _raw_stream(stream)))
 
 
 def ck_int4_quantize(w, group: int, qweight, scales, zeros, stream=None):

@@ -25,42 +25,474 @@ struct MatvecArgs {
     int group;
     void *y;
     int64_t y_stride;
+    float *partial;  // slots of sums that cross CTAs or slabs
 };
 
-// One warp per weight row and eight rows of x; a lane takes every 32nd word of
-// eight weights.  A word lies in one group, as groups are multiples of eight.
-constexpr int kRows = 8;
-template <typename T> __global__ void __launch_bounds__(256) k_matvec(MatvecArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t v = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-    if (v >= a.V) return;
+// The product of a few rows.  With w = s (q - z), a group's sum factors into
+// s * sum (q - z) x, and q - z is a whole number of at most 15 in magnitude, so
+// it is exact in 16-bit floats: the tensor cores multiply it with x as it is,
+// sums are held in 32 bits, and the scale is applied once a group.  32-bit x is
+// split into three bf16 parts of eight bits each, cut by truncation, which
+// hold all 24 bits over the whole range; the parts are columns of their own.
+//
+// What bounds it is the stream of weights: 0.5 byte each, while a column costs
+// 2 operations a weight.  So the weights flow through a ring of asynchronous
+// copies that each warp keeps for itself, and no warp waits for another until
+// the end.
+//
+// A unit is 16 weight rows by 256 columns (2 KB).  K is cut into slabs whose x
+// fits in shared memory; the units, in the order (slab, 16-row tile, chunk),
+// are dealt to CTAs, and a CTA's to its warps, in equal runs.  A run's first and
+// last tile may be shared with its neighbours: those sums meet in shared memory
+// and, where a tile crosses CTAs or slabs, in the slots of `partial`, which
+// k_join adds up in a fixed order.
+constexpr int kWarpsMv = 16;                // warps of a CTA, one CTA on an SM
+constexpr int kStages = 4;                  // ring of units per warp
+constexpr int kUnitBytes = 16 * 128;
+constexpr int kChunk = 256;                 // columns of a unit
+constexpr size_t kSmemMost = 232448;
+
+struct MatvecPlan {
+    int rows;          // rows of x in this launch
+    int cols;          // tensor-core columns: rows times parts
+    int64_t tiles;     // 16-row tiles of V
+    int64_t chunks;    // chunks of K
+    int64_t slab;      // chunks of a slab (the last may have fewer)
+    int64_t slabs;
+    int ctas;
+    int aligned;       // CTAs take whole tiles: nothing crosses them
+    size_t x_pitch;    // bytes between columns of x in shared memory
+    size_t smem;
+
+    __host__ __device__ int64_t units() const { return tiles * chunks; }
+    // first unit of CTA b
+    __host__ __device__ int64_t cut(int64_t b) const {
+        return aligned ? tiles * b / ctas * chunks : units() * b / ctas;
+    }
+    __host__ __device__ int64_t slab_chunks(int64_t s) const {
+        return s + 1 < slabs ? slab : chunks - (slabs - 1) * slab;
+    }
+    __host__ __device__ int64_t slab_first(int64_t s) const { return s * slab * tiles; }
+    // the CTA whose run holds unit u
+    __host__ __device__ int64_t cta_of(int64_t u) const {
+        int64_t b = u * ctas / units();
+        while (b + 1 < ctas && cut(b + 1) <= u) ++b;
+        while (b > 0 && cut(b) > u) --b;
+        return b;
+    }
+    // slot of CTA b's part of a tile in a slab: no two parts share one, as from
+    // a part to the next the tile or the CTA moves on and neither goes back
+    __host__ __device__ int64_t slot(int64_t s, int64_t tile, int64_t b) const {
+        return s * tiles + tile + b;
+    }
+};
+
+// Pairs of 16-bit floats: bf16 for 32-bit and bf16 x, fp16 for fp16 x.
+template <typename T> struct Pair {
+    static constexpr uint32_t kBase = 0x43004300u;   // 128: + a nibble is exact in 8 bits
+    static __device__ __forceinline__ uint32_t base_plus(uint32_t z) { return kBase + z * 0x00010001u; }
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+template <> struct Pair<__half> {
+    static constexpr uint32_t kBase = 0x64006400u;   // 1024
+    static __device__ __forceinline__ uint32_t base_plus(uint32_t z) { return kBase + z * 0x00010001u; }
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+template <typename T> constexpr int kParts = 1;
+template <> constexpr int kParts<float> = 3;
+
+// Three parts of a 32-bit float: each takes the top eight bits of what is left.
+// Truncation keeps the first part of a large number finite; what is not finite
+// goes whole into the first part.
+__device__ __forceinline__ void split3(float v, uint16_t (&part)[3]) {
+    const uint32_t b = __float_as_uint(v);
+    const bool odd = (b & 0x7f800000u) == 0x7f800000u;
+    const uint32_t nan = (b & 0x007fffffu) && odd ? 0x00400000u : 0u;  // NaN stays NaN when cut
+    const uint32_t h = (b | nan) & 0xffff0000u;
+    const float r = odd ? 0.f : v - __uint_as_float(h);
+    const uint32_t m = __float_as_uint(r) & 0xffff0000u;
+    const float l = r - __uint_as_float(m);
+    part[0] = (uint16_t)(h >> 16);
+    part[1] = (uint16_t)(m >> 16);
+    part[2] = (uint16_t)(__float_as_uint(l) >> 16);
+}
+
+__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// x of a slab into shared memory, one line a column, eight columns of K at a
+// time in the order 0 4 1 5 2 6 3 7: the order in which nibbles come out of a
+// word two at a time.
+template <typename T>
+__device__ void stage_x(const MatvecArgs &a, const MatvecPlan &p, int64_t k0, int64_t n8, char *xs) {
     const T *x = (const T *)a.x;
-    T *y = (T *)a.y;
-    for (int64_t m0 = (int64_t)blockIdx.y * kRows; m0 < a.M; m0 += (int64_t)gridDim.y * kRows) {
-        float acc[kRows] = {};
-        for (int64_t k = 8 * lane; k < a.K; k += 8 * 32) {
-            const int64_t g = k / a.group;
-            const float s = load_scale(a.scales, a.scale_dtype, v * a.s_stride + g);
-            const float z = a.zeros ? (float)(a.zeros[v * a.z_stride + g] & 15) : 8.f;
-            const int n = a.K - k < 8 ? (int)(a.K - k) : 8;
-            float w[8];
-            for (int j = 0; j < n; ++j) {
-                const uint8_t b = a.q[v * a.q_pitch + (k + j) / 2];
-                w[j] = s * ((float)(j & 1 ? b >> 4 : b & 15) - z);
+    for (int64_t i = threadIdx.x; i < n8 * p.rows; i += blockDim.x) {
+        const int64_t m = i / n8, j = i % n8, k = k0 + 8 * j;
+        alignas(32) T v[8];
+        const T *src = x + m * a.x_stride + k;
+        if (k + 8 <= a.K && ((uintptr_t)src & (sizeof(T) == 4 ? 31 : 15)) == 0) {
+            if constexpr (sizeof(T) == 4) {
+                *(float4 *)v = *(const float4 *)src;
+                *(float4 *)(v + 4) = *(const float4 *)(src + 4);
+            } else {
+                *(uint4 *)v = *(const uint4 *)src;
             }
+        } else {
 #pragma unroll
-            for (int i = 0; i < kRows; ++i)
-                if (m0 + i < a.M)
-                    for (int j = 0; j < n; ++j)
-                        acc[i] = fmaf(w[j], to_float(x[(m0 + i) * a.x_stride + k + j]), acc[i]);
+            for (int e = 0; e < 8; ++e) v[e] = k + e < a.K ? src[e] : from_float<T>(0.f);
         }
+        if constexpr (sizeof(T) == 4) {
+            uint16_t part[8][3];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            float t = acc[i];
-            for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
-            if (lane == 0 && m0 + i < a.M)
-                y[(m0 + i) * a.y_stride + v] = from_float<T>(t + (a.bias ? a.bias[v] : 0.f));
+            for (int e = 0; e < 8; ++e) split3(v[e], part[e]);
+#pragma unroll
+            for (int s = 0; s < 3; ++s) {
+                uint4 w;
+                w.x = part[0][s] | (uint32_t)part[4][s] << 16;
+                w.y = part[1][s] | (uint32_t)part[5][s] << 16;
+                w.z = part[2][s] | (uint32_t)part[6][s] << 16;
+                w.w = part[3][s] | (uint32_t)part[7][s] << 16;
+                *(uint4 *)(xs + (3 * m + s) * p.x_pitch + 16 * j) = w;
+            }
+        } else {
+            const uint16_t *h = (const uint16_t *)v;
+            uint4 w;
+            w.x = h[0] | (uint32_t)h[4] << 16;
+            w.y = h[1] | (uint32_t)h[5] << 16;
+            w.z = h[2] | (uint32_t)h[6] << 16;
+            w.w = h[3] | (uint32_t)h[7] << 16;
+            *(uint4 *)(xs + m * p.x_pitch + 16 * j) = w;
         }
+    }
+}
+
+// A unit into a warp's ring, 16 bytes a lane and copy: lines of 128 bytes, the
+// eight 16-byte pieces of line r exchanged by r, so that eight lines are read
+// without a conflict.  Bytes past a row's end and rows past V become zeros.
+__device__ __forceinline__ void copy_unit(const MatvecArgs &a, int64_t tile, int64_t chunk, uint32_t dst) {
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+    const int64_t at = chunk * 128 + piece * 16, row_bytes = (a.K + 1) / 2;
+    int n = row_bytes - at >= 16 ? 16 : row_bytes > at ? (int)(row_bytes - at) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        const int64_t v = tile * 16 + r;
+        const int m = v < a.V ? n : 0;
+        const uint8_t *src = m ? a.q + v * a.q_pitch + at : a.q;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         dst + r * 128 + ((piece ^ (r & 7)) << 4)),
+                     "l"(src), "r"(m));
+    }
+}
+
+template <int GROUP> struct UnitScales {
+    static constexpr int kGroups = kChunk / GROUP, kPer = kGroups / 2;  // values a lane holds
+    float s[kPer];
+    uint32_t z[kPer];
+};
+
+// Scales and zero points of a unit, dealt over the four lanes of a row: value
+// 2 group + half is that of row (lane / 4) + 8 half.
+template <typename T, int GROUP>
+__device__ __forceinline__ void load_scales(const MatvecArgs &a, int64_t tile, int64_t chunk,
+                                            UnitScales<GROUP> &u) {
+    const int lane = threadIdx.x & 31;
+    const int64_t groups = (a.K + GROUP - 1) / GROUP;
+#pragma unroll
+    for (int i = 0; i < UnitScales<GROUP>::kPer; ++i) {
+        const int idx = 4 * i + (lane & 3);
+        const int64_t g = chunk * (kChunk / GROUP) + idx / 2, v = tile * 16 + (lane >> 2) + 8 * (idx & 1);
+        const bool in = g < groups && v < a.V;
+        u.s[i] = in ? load_scale(a.scales, a.scale_dtype, v * a.s_stride + g) : 0.f;
+        u.z[i] = a.zeros ? Pair<T>::base_plus(in ? a.zeros[v * a.z_stride + g] & 15 : 8) : 0;
+    }
+}
+
+// sum over the columns of a row's parts
+__device__ __forceinline__ float join_parts(const float *c, int parts) {
+    return parts == 1 ? c[0] : (c[2] + c[1]) + c[0];
+}
+
+template <typename T, int GROUP, int NT>
+__global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, MatvecPlan p) {
+    extern __shared__ __align__(128) char smem[];
+    constexpr int kCols = 8 * NT;
+    char *ring = smem;
+    float *slots = (float *)(ring + kWarpsMv * kStages * kUnitBytes);  // [warps][2][16][kCols]
+    int64_t *slot_tile = (int64_t *)(slots + kWarpsMv * 2 * 16 * kCols);
+    char *xs = (char *)(slot_tile + kWarpsMv * 2);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = lane >> 2, quad = lane & 3;
+    const uint32_t my_ring = smem_at(ring) + warp * kStages * kUnitBytes;
+    T *y = (T *)a.y;
+    const int64_t cta0 = p.cut(blockIdx.x), cta1 = p.cut(blockIdx.x + 1);
+    asm volatile("griddepcontrol.launch_dependents;");
+    for (int64_t s = 0; s < p.slabs; ++s) {
+        const int64_t sc = p.slab_chunks(s), base = p.slab_first(s);
+        const int64_t u0 = cta0 > base ? cta0 : base;
+        const int64_t u1 = cta1 < base + sc * p.tiles ? cta1 : base + sc * p.tiles;
+        if (u0 >= u1) continue;
+        const int64_t w0 = u0 + (u1 - u0) * warp / kWarpsMv, w1 = u0 + (u1 - u0) * (warp + 1) / kWarpsMv;
+        const int64_t first = s * p.slab;  // the slab's first chunk
+        int64_t n = w1 - w0;
+        int64_t pt = (w0 - base) / sc, pc = (w0 - base) % sc, left = n;  // next to copy
+        int64_t t = pt, c = pc;                                         // next to multiply
+        int put = 0;
+        auto copy_next = [&] {
+            if (left > 0) {
+                copy_unit(a, pt, first + pc, my_ring + put * kUnitBytes);
+                --left;
+                if (++pc == sc) pc = 0, ++pt;
+            }
+            put = put + 1 == kStages ? 0 : put + 1;
+            asm volatile("cp.async.commit_group;");
+        };
+        for (int i = 0; i < kStages - 1; ++i) copy_next();
+        UnitScales<GROUP> next;
+        if (n > 0) load_scales<T, GROUP>(a, t, first + c, next);
+        __syncthreads();  // the last slab's x and slots are done with
+        if (lane < 2) slot_tile[2 * warp + lane] = -1;
+        stage_x<T>(a, p, first * kChunk, sc * (kChunk / 8), xs);
+        __syncthreads();
+        float acc[NT][4] = {};
+        int64_t seg0 = c;  // chunk at which this tile's part began
+        int used = 0, get = 0;
+        for (; n > 0; --n) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2));
+            __syncwarp();
+            copy_next();
+            const UnitScales<GROUP> cur = next;
+            if (n > 1) {
+                const bool wrap = c + 1 == sc;
+                load_scales<T, GROUP>(a, wrap ? t + 1 : t, first + (wrap ? 0 : c + 1), next);
+            }
+            const uint32_t unit = my_ring + get * kUnitBytes;
+            get = get + 1 == kStages ? 0 : get + 1;
+            float part[NT][4];
+            uint32_t zero[2] = {Pair<T>::base_plus(8), Pair<T>::base_plus(8)};
+            float scale[2];
+#pragma unroll
+            for (int blk = 0; blk < kChunk / 32; ++blk) {  // 32 columns: one piece of each line
+                constexpr int kBlocks = GROUP / 32;
+                if (blk % kBlocks == 0) {
+                    const int g = blk / kBlocks;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int idx = 2 * g + h;
+                        scale[h] = __shfl_sync(~0u, cur.s[idx / 4], (lane & ~3) | (idx & 3));
+                        if (a.zeros) zero[h] = __shfl_sync(~0u, cur.z[idx / 4], (lane & ~3) | (idx & 3));
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.f;
+                }
+                uint32_t w[2];
+                {
+                    const int r = lane & 15;
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
+                                 : "=r"(w[0]), "=r"(w[1])
+                                 : "r"(unit + r * 128 + ((blk ^ (r & 7)) << 4)));
+                }
+                uint32_t v[4][2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        v[j][h] = Pair<T>::sub((w[h] >> (4 * j) & 0x000f000fu) | Pair<T>::kBase, zero[h]);
+                const uint32_t a0[4] = {v[0][0], v[0][1], v[1][0], v[1][1]};
+                const uint32_t a1[4] = {v[2][0], v[2][1], v[3][0], v[3][1]};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    uint4 b = make_uint4(0, 0, 0, 0);
+                    if (8 * j + row < p.cols)
+                        b = *(const uint4 *)(xs + (8 * j + row) * p.x_pitch + c * (2 * kChunk) + blk * 64 +
+                                             quad * 16);
+                    Pair<T>::mma(part[j], a0, b.x, b.y);
+                    Pair<T>::mma(part[j], a1, b.z, b.w);
+                }
+                if (blk % kBlocks == kBlocks - 1) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(scale[e >> 1], part[j][e], acc[j][e]);
+                }
+            }
+            const bool whole = c + 1 == sc;
+            if (whole || n == 1) {  // this tile's part ends here
+                const int slot = 2 * warp + used;
+                float *mine = slots + slot * 16 * kCols;
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    *(float2 *)(mine + row * kCols + 8 * j + 2 * quad) = make_float2(acc[j][0], acc[j][1]);
+                    *(float2 *)(mine + (row + 8) * kCols + 8 * j + 2 * quad) =
+                        make_float2(acc[j][2], acc[j][3]);
+                    acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+                }
+                __syncwarp();
+                if (whole && seg0 == 0) {  // all of the slab's K: no other warp has a part
+                    for (int i = lane; i < 16 * p.rows; i += 32) {
+                        const int r = i & 15, m = i >> 4;
+                        const int64_t v = t * 16 + r;
+                        if (v >= a.V) continue;
+                        const float sum = join_parts(mine + r * kCols + m * kParts<T>, kParts<T>);
+                        if (p.slabs == 1)
+                            y[m * a.y_stride + v] = from_float<T>(sum + (a.bias ? a.bias[v] : 0.f));
+                        else
+                            a.partial[(p.slot(s, t, blockIdx.x) * p.rows + m) * 16 + r] = sum;
+                    }
+                } else {
+                    if (lane == 0) slot_tile[slot] = t;
+                    ++used;
+                }
+                seg0 = 0;
+            }
+            if (whole) c = 0, ++t; else ++c;
+        }
+        __syncthreads();
+        // parts of one tile lie in a row of slots: the warp that holds the first adds them up
+        for (int k = 0; k < 2; ++k) {
+            const int at = 2 * warp + k;
+            const int64_t tile = slot_tile[at];
+            if (tile < 0) continue;
+            bool head = true;
+            for (int i = at - 1; i >= 0 && head; --i)
+                if (slot_tile[i] >= 0) {
+                    head = slot_tile[i] != tile;
+                    break;
+                }
+            if (!head) continue;
+            const int64_t tu = base + tile * sc;
+            const bool alone = p.slabs == 1 && tu >= u0 && tu + sc <= u1;
+            for (int i = lane; i < 16 * p.rows; i += 32) {
+                const int r = i & 15, m = i >> 4;
+                const int64_t v = tile * 16 + r;
+                float sum = 0.f;
+                for (int e = at; e < 2 * kWarpsMv; ++e) {
+                    if (slot_tile[e] < 0) continue;
+                    if (slot_tile[e] != tile) break;
+                    sum += join_parts(slots + e * 16 * kCols + r * kCols + m * kParts<T>, kParts<T>);
+                }
+                if (v >= a.V) continue;
+                if (alone)
+                    y[m * a.y_stride + v] = from_float<T>(sum + (a.bias ? a.bias[v] : 0.f));
+                else
+                    a.partial[(p.slot(s, tile, blockIdx.x) * p.rows + m) * 16 + r] = sum;
+            }
+        }
+    }
+}
+
+// Sums that cross CTAs or slabs, in the order of K.
+template <typename T> __global__ void __launch_bounds__(128) k_join(MatvecArgs a, MatvecPlan p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    T *y = (T *)a.y;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.tiles * 16 * p.rows;
+         i += (int64_t)gridDim.x * blockDim.x) {
+        const int r = (int)(i & 15);
+        const int64_t tile = i / 16 % p.tiles, m = i / 16 / p.tiles, v = tile * 16 + r;
+        if (v >= a.V) continue;
+        float sum = 0.f;
+        bool crossed = p.slabs > 1;
+        for (int64_t s = 0; s < p.slabs; ++s) {
+            const int64_t u = p.slab_first(s) + tile * p.slab_chunks(s), e = u + p.slab_chunks(s);
+            const int64_t b0 = p.cta_of(u), b1 = p.cta_of(e - 1);
+            crossed |= b0 != b1;
+            if (!crossed) break;
+            for (int64_t b = b0; b <= b1; ++b) sum += a.partial[(p.slot(s, tile, b) * p.rows + m) * 16 + r];
+        }
+        if (crossed) y[m * a.y_stride + v] = from_float<T>(sum + (a.bias ? a.bias[v] : 0.f));
+    }
+}
+
+size_t matvec_fixed_smem(int nt) {
+    return (size_t)kWarpsMv * kStages * kUnitBytes + (size_t)kWarpsMv * 2 * (16 * 8 * nt * 4 + 8);
+}
+
+int parts_of(int64_t dtype) { return dtype == CK_F32 ? 3 : 1; }
+// Rows of x that one launch takes: two tensor-core tiles of eight columns.
+int rows_at_once(int64_t dtype) { return 16 / parts_of(dtype); }
+
+MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms) {
+    MatvecPlan p{};
+    p.rows = (int)rows;
+    p.cols = (int)rows * parts_of(dtype);
+    p.tiles = (V + 15) / 16;
+    p.chunks = (K + kChunk - 1) / kChunk;
+    const int nt = (p.cols + 7) / 8;
+    const int64_t room = (int64_t)(kSmemMost - matvec_fixed_smem(nt)) / p.cols - 64;
+    const int64_t most = room / (2 * kChunk);
+    p.slabs = (p.chunks + most - 1) / most;
+    p.slab = (p.chunks + p.slabs - 1) / p.slabs;
+    p.slabs = (p.chunks + p.slab - 1) / p.slab;
+    // Whole tiles to each CTA, and no second kernel, or equal runs with one: a
+    // unit takes an SM about 0.05 us, the second kernel about 2 us.
+    const double unit = 0.05;
+    const int64_t even = p.units() / kWarpsMv, by_tile = p.tiles < sms ? p.tiles : sms;
+    const double whole = (double)((p.tiles + by_tile - 1) / by_tile) * p.chunks * unit;
+    const double equal = (double)p.units() / sms * unit + 2.0;
+    p.aligned = p.slabs == 1 && whole <= equal;
+    p.ctas = (int)(p.aligned ? by_tile : even < 1 ? 1 : even < sms ? even : sms);
+    p.x_pitch = (size_t)p.slab * 2 * kChunk + 64;
+    p.smem = matvec_fixed_smem(nt) + p.cols * p.x_pitch;
+    return p;
+}
+
+size_t partial_bytes(const MatvecPlan &p) {
+    return p.aligned ? 0 : (size_t)(p.slabs * p.tiles + p.ctas) * 16 * p.rows * sizeof(float);
+}
+
+template <typename T, int GROUP, int NT>
+cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(k_matvec<T, GROUP, NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
+    if (e != cudaSuccess) return e;
+    k_matvec<T, GROUP, NT><<<p.ctas, kWarpsMv * 32, p.smem, stream>>>(a, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.aligned) return e;
+    cudaLaunchConfig_t cfg{};
+    const int64_t want = (p.tiles * 16 * p.rows + 127) / 128;
+    cfg.gridDim = dim3((unsigned)(want < 1024 ? want : 1024));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_join<T>, a, p);
+}
+
+template <typename T>
+cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
+    const bool two = p.cols > 8;
+    switch (a.group) {
+        case 32: return two ? launch_matvec<T, 32, 2>(a, p, stream) : launch_matvec<T, 32, 1>(a, p, stream);
+        case 64: return two ? launch_matvec<T, 64, 2>(a, p, stream) : launch_matvec<T, 64, 1>(a, p, stream);
+        default: return two ? launch_matvec<T, 128, 2>(a, p, stream) : launch_matvec<T, 128, 1>(a, p, stream);
     }
 }
 
@@ -138,7 +570,7 @@ extern "C" ck_status ck_int4_matvec(const void *x, int64_t dtype, int64_t M, int
                                     int64_t q_pitch, const void *scales, int64_t scale_dtype,
                                     int64_t s_stride, const uint8_t *zeros, int64_t z_stride,
                                     const float *bias, int64_t group, void *y, int64_t y_stride,
-                                    void *stream) {
+                                    void *workspace, size_t workspace_bytes, void *stream) {
     if (!known_dtype(dtype) || !known_dtype(scale_dtype))
         return fail(CK_ERR_INVALID_ARG, "int4_matvec: unknown dtype");
     if (!known_group(group))
@@ -154,16 +586,45 @@ extern "C" ck_status ck_int4_matvec(const void *x, int64_t dtype, int64_t M, int
     if (s_stride < (K + group - 1) / group || (zeros && z_stride < (K + group - 1) / group) ||
         x_stride < 0 || y_stride < V)
         return fail(CK_ERR_INVALID_ARG, "int4_matvec: a row stride is shorter than its row");
-    MatvecArgs a{x, M, K, x_stride, qweight, V, q_pitch, scales, (int)scale_dtype, s_stride, zeros,
-                 z_stride, bias, (int)group, y, y_stride};
-    const int64_t my = (M + kRows - 1) / kRows;
-    const dim3 grid((unsigned)((V + 7) / 8), (unsigned)(my < 1024 ? my : 1024));
-    with_dtype(dtype, [&](auto *tag) {
-        using T = std::remove_pointer_t<decltype(tag)>;
-        k_matvec<T><<<grid, 256, 0, (cudaStream_t)stream>>>(a);
-    });
-    const cudaError_t e = cudaGetLastError();
+    size_t need = 0;
+    const ck_status st = ck_int4_workspace_size(dtype, M, K, V, &need);
+    if (st != CK_OK) return st;
+    if (need > 0 && !workspace) return fail(CK_ERR_INVALID_ARG, "int4_matvec: workspace is NULL");
+    if (workspace_bytes < need || ((uintptr_t)workspace & 15u) != 0)
+        return fail(CK_ERR_WORKSPACE, "int4_matvec: workspace of %zu bytes (%zu needed, 16-byte aligned)",
+                    workspace_bytes, need);
+    const int sms = device_sms();
+    cudaError_t e = cudaSuccess;
+    for (int64_t m = 0; m < M && e == cudaSuccess; m += rows_at_once(dtype)) {
+        const int64_t rows = M - m < rows_at_once(dtype) ? M - m : rows_at_once(dtype);
+        const size_t el = dtype_size(dtype);
+        MatvecArgs a{(const char *)x + m * x_stride * el, rows, K, x_stride, qweight, V, q_pitch, scales,
+                     (int)scale_dtype, s_stride, zeros, z_stride, bias, (int)group,
+                     (char *)y + m * y_stride * el, y_stride, (float *)workspace};
+        const MatvecPlan p = matvec_plan(dtype, rows, K, V, sms);
+        with_dtype(dtype, [&](auto *tag) {
+            using T = std::remove_pointer_t<decltype(tag)>;
+            e = launch_matvec<T>(a, p, (cudaStream_t)stream);
+        });
+    }
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "k_matvec launch");
+}
+
+extern "C" ck_status ck_int4_workspace_size(int64_t dtype, int64_t M, int64_t K, int64_t V,
+                                            size_t *bytes) {
+    if (!known_dtype(dtype) || M < 0 || K < 1 || V < 0 || K >= ((int64_t)1 << 30) || V >= ((int64_t)1 << 30) ||
+        !bytes)
+        return fail(CK_ERR_INVALID_ARG, "int4_workspace_size: bad dtype, size or NULL bytes");
+    *bytes = 0;
+    if (M == 0 || V == 0) return CK_OK;
+    const int sms = device_sms();
+    const int64_t most = rows_at_once(dtype), tail = M % most;
+    if (M >= most) *bytes = partial_bytes(matvec_plan(dtype, most, K, V, sms));
+    if (tail) {
+        const size_t b = partial_bytes(matvec_plan(dtype, tail, K, V, sms));
+        if (b > *bytes) *bytes = b;
+    }
+    return CK_OK;
 }
 
 extern "C" ck_status ck_int4_quantize(const void *w, int64_t dtype, int64_t V, int64_t K,

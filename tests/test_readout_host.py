@@ -86,7 +86,7 @@ def test_int4_refuses_on_the_host():
     def call(x=base, dtype=0, M=1, K=64, xs=64, q=base, V=2, pitch=32, s=base, sdt=0, ss=2, z=None,
              zs=0, group=32, y=base, ys=2):
         return lib.ck_int4_matvec(x, dtype, M, K, xs, q, V, pitch, s, sdt, ss, z, zs, None, group, y,
-                                  ys, None)
+                                  ys, None, 0, None)
 
     assert call(dtype=5) == 1 and call(sdt=9) == 1
     for g in (0, 16, 33, 256, -32):
