@@ -361,7 +361,7 @@ ck_status ck_dropout(const void *x, void *y, int64_t dtype, int64_t n0, int64_t 
  *   group    32, 64 or 128
  *   y        (device) `dtype` [M][V], rows y_stride elements apart, overwritten
  *   workspace (device) at least what ck_int4_workspace_size says for the same
- *            dtype, M, K and V on this device, 16-byte aligned; its contents need
+ *            dtype, M, K, V and group on this device, 16-byte aligned; its contents need
  *            no setting and mean nothing afterwards; NULL when that is 0 bytes
  * An x row that holds an infinity or NaN gives outputs that are not finite.
  * Sums are added up in an order that depends on the sizes and the device alone.
@@ -374,7 +374,8 @@ ck_status ck_int4_matvec(const void *x, int64_t dtype, int64_t M, int64_t K, int
                          int64_t scale_dtype, int64_t s_stride, const uint8_t *zeros,
                          int64_t z_stride, const float *bias, int64_t group, void *y,
                          int64_t y_stride, void *workspace, size_t workspace_bytes, void *stream);
-ck_status ck_int4_workspace_size(int64_t dtype, int64_t M, int64_t K, int64_t V, size_t *bytes);
+ck_status ck_int4_workspace_size(int64_t dtype, int64_t M, int64_t K, int64_t V,
+                                 int64_t group, size_t *bytes);
 
 /*
  * ck_int4_quantize -- weights for ck_int4_matvec from (device) `dtype` w[V][K],

@@ -101,7 +101,7 @@ def load() -> ctypes.CDLL:
         "ck_dropout": [p, p, i64, *[i64] * 9, i64, ctypes.c_double, u64, u64, p, p],
         "ck_int4_matvec": [p, i64, i64, i64, i64, p, i64, i64, p, i64, i64, p, i64, p, i64, p, i64,
                            p, sz, p],
-        "ck_int4_workspace_size": [i64, i64, i64, i64, psz],
+        "ck_int4_workspace_size": [i64, i64, i64, i64, i64, psz],
         "ck_int4_quantize": [p, i64, i64, i64, i64, i64, i64, p, i64, p, i64, i64, p, i64, p],
         "ck_control_logits": [ctypes.POINTER(LogitCall), p],
         "ck_forward_static_scratch": [p, p, p, p, p, p, i64, i64, i64, p, p, sz, p],
@@ -364,13 +364,13 @@ def _rows(t, name):
     return pitch if n > 1 else m
 
 
-def ck_int4_workspace_size(dtype, M: int, K: int, V: int) -> int:
+def ck_int4_workspace_size(dtype, M: int, K: int, V: int, group: int) -> int:
     n = ctypes.c_size_t()
-    _check(load().ck_int4_workspace_size(DTYPES[dtype], M, K, V, ctypes.byref(n)))
+    _check(load().ck_int4_workspace_size(DTYPES[dtype], M, K, V, group, ctypes.byref(n)))
     return n.value
 
 
-_int4_ws = {}  # bytes by (device, dtype, M, K, V): sizes only, no memory
+_int4_ws = {}  # bytes by (device, dtype, M, K, V, group): sizes only, no memory
 
 
 def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
@@ -400,12 +400,12 @@ def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
     pitch = _rows(qweight, "qweight") if V > 1 else -(-qweight.shape[1] // 16) * 16
     if qweight.shape[1] > 1 and qweight.stride(1) != 1:
         raise ValueError("the rows of qweight must be dense")
-    key = (dev, x.dtype, M, K, V)
+    key = (dev, x.dtype, M, K, V, group)
     need = _int4_ws.get(key)
     if need is None:
         if len(_int4_ws) > 4096:
             _int4_ws.clear()
-        need = _int4_ws[key] = ck_int4_workspace_size(x.dtype, M, K, V)
+        need = _int4_ws[key] = ck_int4_workspace_size(x.dtype, M, K, V, group)
     ws = qweight.new_empty(need) if need else None
     if ws is not None and stream is not None:
         ws.record_stream(stream)

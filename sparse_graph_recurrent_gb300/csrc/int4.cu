@@ -13,7 +13,7 @@ __device__ __forceinline__ float load_scale(const void *p, int dtype, int64_t i)
 
 struct MatvecArgs {
     const void *x;
-    int64_t M, K, x_stride;
+    int64_t dtype, M, K, x_stride;
     const uint8_t *q;
     int64_t V, q_pitch;
     const void *scales;
@@ -22,18 +22,19 @@ struct MatvecArgs {
     const uint8_t *zeros;
     int64_t z_stride;
     const float *bias;
-    int group;
     void *y;
     int64_t y_stride;
     float *partial;  // slots of sums that cross CTAs or slabs
 };
 
-// The product of a few rows.  With w = s (q - z), a group's sum factors into
-// s * sum (q - z) x, and q - z is a whole number of at most 15 in magnitude, so
-// it is exact in 16-bit floats: the tensor cores multiply it with x as it is,
-// sums are held in 32 bits, and the scale is applied once a group.  32-bit x is
-// split into three bf16 parts of eight bits each, cut by truncation, which
-// hold all 24 bits over the whole range; the parts are columns of their own.
+// The product of a few rows, on tensor cores.  With w = s (q - z) a group's sum is
+// s * sum (q - z) x, and q - z, a whole number of at most 15 in magnitude, is exact
+// in a 16-bit float; so x meets the weights as they are, sums are held in 32 bits
+// and the scale is applied once a group.  A 32-bit x is cut into three bf16 parts
+// of eight bits, 24 together over the whole range of the type; the parts are
+// columns of their own.  (Two fp16 parts under a scale of the row, and the zero
+// points taken off the sums, cost a third fewer instructions and two thirds of the
+// columns, but an outlier that meets q = z then drowns the rest of its row.)
 //
 // What bounds it is the stream of weights: 0.5 byte each, while a column costs
 // 2 operations a weight.  So the weights flow through a ring of asynchronous
@@ -51,17 +52,19 @@ constexpr int kStages = 4;                  // ring of units per warp
 constexpr int kUnitBytes = 16 * 128;
 constexpr int kChunk = 256;                 // columns of a unit
 constexpr size_t kSmemMost = 232448;
+constexpr int kMostCols = 32;               // tensor-core columns of one launch
 
 struct MatvecPlan {
     int rows;          // rows of x in this launch
-    int cols;          // tensor-core columns: rows times parts
+    int parts;         // 16-bit parts of an x: columns m * parts + part
+    int cols;
     int64_t tiles;     // 16-row tiles of V
     int64_t chunks;    // chunks of K
     int64_t slab;      // chunks of a slab (the last may have fewer)
     int64_t slabs;
     int ctas;
     int aligned;       // CTAs take whole tiles: nothing crosses them
-    size_t x_pitch;    // bytes between columns of x in shared memory
+    int x_pitch;       // bytes between columns of x in shared memory
     size_t smem;
 
     __host__ __device__ int64_t units() const { return tiles * chunks; }
@@ -87,46 +90,65 @@ struct MatvecPlan {
     }
 };
 
-// Pairs of 16-bit floats: bf16 for 32-bit and bf16 x, fp16 for fp16 x.
-template <typename T> struct Pair {
-    static constexpr uint32_t kBase = 0x43004300u;   // 128: + a nibble is exact in 8 bits
-    static __device__ __forceinline__ uint32_t base_plus(uint32_t z) { return kBase + z * 0x00010001u; }
-    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-        uint32_t r;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
-template <> struct Pair<__half> {
-    static constexpr uint32_t kBase = 0x64006400u;   // 1024
-    static __device__ __forceinline__ uint32_t base_plus(uint32_t z) { return kBase + z * 0x00010001u; }
-    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-        uint32_t r;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
-template <typename T> constexpr int kParts = 1;
-template <> constexpr int kParts<float> = 3;
+__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// Three parts of a 32-bit float: each takes the top eight bits of what is left.
-// Truncation keeps the first part of a large number finite; what is not finite
+// Weights and x in bf16 (for 32-bit and bf16 x) or fp16.
+template <bool HALF, bool FIRST>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+    const float z = 0.f;  // FIRST: a new sum
+    const float c0 = FIRST ? z : c[0], c1 = FIRST ? z : c[1], c2 = FIRST ? z : c[2], c3 = FIRST ? z : c[3];
+    if constexpr (HALF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%11,%12,%13};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%11,%12,%13};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+// q - z of a word's eight nibbles, as pairs (0, 4), (1, 5), (2, 6), (3, 7).  Put
+// below the exponent of 2^7 (bf16) or 2^10 (fp16), a nibble q is the number 128 + q
+// or 1024 + q, and subtracting 128 + z or 1024 + z is exact.  In fp16 the next
+// nibble is read where it is, as 1024 + 16 q: a product with 1/16 saves its shift.
+template <bool HALF> struct Zero;
+template <> struct Zero<false> {
+    uint32_t even;
+    // of byte i of four packed zero points
+    __device__ __forceinline__ void set(uint32_t packed, int i) {
+        even = __byte_perm(packed, 0x43u, 0x4040u | i | i << 8);
+    }
+};
+template <> struct Zero<true> {
+    uint32_t even, odd;  // 1024 + z and -(64 + z), twice
+    __device__ __forceinline__ void set(uint32_t packed, int i) {
+        even = __byte_perm(packed, 0x64u, 0x4040u | i | i << 8);
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(odd) : "r"(even), "r"(0xbc00bc00u), "r"(0x63806380u));
+    }
+};
+template <bool HALF>
+__device__ __forceinline__ void nibbles(uint32_t w, const Zero<HALF> &z, uint32_t (&v)[4]) {
+    if constexpr (HALF) {
+        const uint32_t w8 = w >> 8;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[0]) : "r"((w & 0x000f000fu) | 0x64006400u), "r"(z.even));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;"
+            : "=r"(v[1]) : "r"((w & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(z.odd));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[2]) : "r"((w8 & 0x000f000fu) | 0x64006400u), "r"(z.even));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;"
+            : "=r"(v[3]) : "r"((w8 & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(z.odd));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            asm("sub.rn.bf16x2 %0, %1, %2;"
+                : "=r"(v[j]) : "r"((w >> (4 * j) & 0x000f000fu) | 0x43004300u), "r"(z.even));
+    }
+}
+
+// Three bf16 parts of a 32-bit float: each takes the top eight bits of what is
+// left.  Cutting keeps the first part of a large number finite; what is not finite
 // goes whole into the first part.
 __device__ __forceinline__ void split3(float v, uint16_t (&part)[3]) {
     const uint32_t b = __float_as_uint(v);
@@ -141,105 +163,177 @@ __device__ __forceinline__ void split3(float v, uint16_t (&part)[3]) {
     part[2] = (uint16_t)(__float_as_uint(l) >> 16);
 }
 
-__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Eight numbers of a row of x from column k on, zeros past K.
+template <typename T>
+__device__ __forceinline__ void load8(const MatvecArgs &a, int64_t m, int64_t k, T (&v)[8]) {
+    const T *src = (const T *)a.x + m * a.x_stride + k;
+    if (k + 8 <= a.K && ((uintptr_t)src & 15) == 0) {
+        constexpr int kVec = (int)sizeof(T) / 2;
+        uint4 t[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) t[i] = ((const uint4 *)src)[i];
+        memcpy(v, t, sizeof(t));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = k + e < a.K ? src[e] : from_float<T>(0.f);
+    }
+}
 
 // x of a slab into shared memory, one line a column, eight columns of K at a
-// time in the order 0 4 1 5 2 6 3 7: the order in which nibbles come out of a
-// word two at a time.
+// time in the order 0 4 1 5 2 6 3 7, in which nibbles come out of a word two at a
+// time.
 template <typename T>
-__device__ void stage_x(const MatvecArgs &a, const MatvecPlan &p, int64_t k0, int64_t n8, char *xs) {
-    const T *x = (const T *)a.x;
-    for (int64_t i = threadIdx.x; i < n8 * p.rows; i += blockDim.x) {
-        const int64_t m = i / n8, j = i % n8, k = k0 + 8 * j;
-        alignas(32) T v[8];
-        const T *src = x + m * a.x_stride + k;
-        if (k + 8 <= a.K && ((uintptr_t)src & (sizeof(T) == 4 ? 31 : 15)) == 0) {
-            if constexpr (sizeof(T) == 4) {
-                *(float4 *)v = *(const float4 *)src;
-                *(float4 *)(v + 4) = *(const float4 *)(src + 4);
-            } else {
-                *(uint4 *)v = *(const uint4 *)src;
-            }
-        } else {
+__device__ void stage_x(const MatvecArgs &a, const MatvecPlan &p, int64_t k0, int lines, char *xs) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // a warp takes a line of 256 columns: 32 times eight
+    for (int i = warp; i < lines * p.rows; i += kWarpsMv) {
+        const int m = i / lines, j = i % lines * 32 + lane;
+        T v[8];
+        load8<T>(a, m, k0 + 8 * j, v);
+        constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+        uint16_t part[8][3];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = k + e < a.K ? src[e] : from_float<T>(0.f);
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (sizeof(T) == 4)
+                split3(v[e], part[e]);
+            else
+                memcpy(&part[e][0], &v[e], 2);
         }
-        if constexpr (sizeof(T) == 4) {
-            uint16_t part[8][3];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) split3(v[e], part[e]);
-#pragma unroll
-            for (int s = 0; s < 3; ++s) {
-                uint4 w;
-                w.x = part[0][s] | (uint32_t)part[4][s] << 16;
-                w.y = part[1][s] | (uint32_t)part[5][s] << 16;
-                w.z = part[2][s] | (uint32_t)part[6][s] << 16;
-                w.w = part[3][s] | (uint32_t)part[7][s] << 16;
-                *(uint4 *)(xs + (3 * m + s) * p.x_pitch + 16 * j) = w;
-            }
-        } else {
-            const uint16_t *h = (const uint16_t *)v;
+        for (int s = 0; s < kParts; ++s) {
             uint4 w;
-            w.x = h[0] | (uint32_t)h[4] << 16;
-            w.y = h[1] | (uint32_t)h[5] << 16;
-            w.z = h[2] | (uint32_t)h[6] << 16;
-            w.w = h[3] | (uint32_t)h[7] << 16;
-            *(uint4 *)(xs + m * p.x_pitch + 16 * j) = w;
+            w.x = part[0][s] | (uint32_t)part[4][s] << 16;
+            w.y = part[1][s] | (uint32_t)part[5][s] << 16;
+            w.z = part[2][s] | (uint32_t)part[6][s] << 16;
+            w.w = part[3][s] | (uint32_t)part[7][s] << 16;
+            *(uint4 *)(xs + (kParts * m + s) * p.x_pitch + 16 * j) = w;
         }
     }
 }
 
-// A unit into a warp's ring, 16 bytes a lane and copy: lines of 128 bytes, the
-// eight 16-byte pieces of line r exchanged by r, so that eight lines are read
-// without a conflict.  Bytes past a row's end and rows past V become zeros.
-__device__ __forceinline__ void copy_unit(const MatvecArgs &a, int64_t tile, int64_t chunk, uint32_t dst) {
-    const int lane = threadIdx.x & 31, piece = lane & 7;
-    const int64_t at = chunk * 128 + piece * 16, row_bytes = (a.K + 1) / 2;
-    int n = row_bytes - at >= 16 ? 16 : row_bytes > at ? (int)(row_bytes - at) : 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        const int64_t v = tile * 16 + r;
-        const int m = v < a.V ? n : 0;
-        const uint8_t *src = m ? a.q + v * a.q_pitch + at : a.q;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         dst + r * 128 + ((piece ^ (r & 7)) << 4)),
-                     "l"(src), "r"(m));
+// What a warp copies next: its lanes' place in the weights, moved on by a chunk
+// at a time.  A unit is eight 16-byte pieces of 16 lines of 128 bytes; the
+// pieces of line r lie exchanged by r, so that eight lines are read without a
+// conflict.
+struct Copier {
+    const uint8_t *src;  // the lane's piece in line lane / 8
+    int64_t tile, chunk, end;  // the slab's chunks: [first, end)
+    __device__ __forceinline__ void seek(const MatvecArgs &a, int64_t tile_, int64_t chunk_) {
+        const int lane = threadIdx.x & 31;
+        tile = tile_;
+        chunk = chunk_;
+        src = a.q + (tile * 16 + (lane >> 3)) * a.q_pitch + chunk * 128 + (lane & 7) * 16;
     }
-}
-
-template <int GROUP> struct UnitScales {
-    static constexpr int kGroups = kChunk / GROUP, kPer = kGroups / 2;  // values a lane holds
-    float s[kPer];
-    uint32_t z[kPer];
+    __device__ __forceinline__ void copy(const MatvecArgs &a, uint32_t dst) const {
+        const int lane = threadIdx.x & 31;
+        // lines 4 i + lane / 8: their low three bits are those of lane / 8, and 4 for odd i
+        const uint32_t at = dst + (lane >> 3) * 128, p0 = ((lane & 7) ^ (lane >> 3)) << 4, p1 = p0 ^ 64;
+        if (tile * 16 + 16 <= a.V && (chunk + 1) * 256 <= a.K) {
+            const uint8_t *s = src;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + i * 512 + (i & 1 ? p1 : p0)),
+                             "l"(s));
+                s += 4 * a.q_pitch;
+            }
+            return;
+        }
+        // bytes past a row's end and rows past V become zeros
+        const int64_t from = chunk * 128 + (lane & 7) * 16, row_bytes = (a.K + 1) / 2;
+        const int n = row_bytes - from >= 16 ? 16 : row_bytes > from ? (int)(row_bytes - from) : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = tile * 16 + 4 * i + (lane >> 3) < a.V ? n : 0;
+            const uint8_t *s = m ? src + 4 * i * a.q_pitch : a.q;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             at + i * 512 + (i & 1 ? p1 : p0)),
+                         "l"(s), "r"(m));
+        }
+    }
+    __device__ __forceinline__ void next(const MatvecArgs &a, int64_t first) {
+        if (++chunk == end)
+            seek(a, tile + 1, first);
+        else
+            src += 128;
+    }
 };
 
-// Scales and zero points of a unit, dealt over the four lanes of a row: value
-// 2 group + half is that of row (lane / 4) + 8 half.
-template <typename T, int GROUP>
-__device__ __forceinline__ void load_scales(const MatvecArgs &a, int64_t tile, int64_t chunk,
-                                            UnitScales<GROUP> &u) {
-    const int lane = threadIdx.x & 31;
-    const int64_t groups = (a.K + GROUP - 1) / GROUP;
-#pragma unroll
-    for (int i = 0; i < UnitScales<GROUP>::kPer; ++i) {
-        const int idx = 4 * i + (lane & 3);
-        const int64_t g = chunk * (kChunk / GROUP) + idx / 2, v = tile * 16 + (lane >> 2) + 8 * (idx & 1);
-        const bool in = g < groups && v < a.V;
-        u.s[i] = in ? load_scale(a.scales, a.scale_dtype, v * a.s_stride + g) : 0.f;
-        u.z[i] = a.zeros ? Pair<T>::base_plus(in ? a.zeros[v * a.z_stride + g] & 15 : 8) : 0;
+// Scales and zero points of a unit, dealt over the four lanes of a row: lane
+// quad holds groups (quad / 2) kPer .. + kPer - 1 of row (lane / 4) + 8 (quad % 2).
+// Kept as they come from memory until the unit is multiplied: a conversion here
+// would wait for the loads.
+template <int GROUP> struct UnitScales {
+    static constexpr int kGroups = kChunk / GROUP, kPer = kGroups / 2;
+    uint32_t s[kPer], z[kPer];
+};
+
+template <int GROUP> struct ScaleReader {
+    using Unit = UnitScales<GROUP>;
+    const char *s;
+    const uint8_t *z;
+    int64_t left;  // groups of the row from this lane's on; none for rows past V
+    __device__ __forceinline__ void seek(const MatvecArgs &a, int64_t tile, int64_t chunk, int64_t groups) {
+        const int lane = threadIdx.x & 31;
+        const int64_t v = tile * 16 + (lane >> 2) + 8 * (lane & 1);
+        const int64_t g = chunk * Unit::kGroups + (lane >> 1 & 1) * Unit::kPer;
+        left = v < a.V ? groups - g : 0;
+        s = (const char *)a.scales + ((v * a.s_stride + g) << (a.scale_dtype == CK_F32 ? 2 : 1));
+        z = a.zeros ? a.zeros + v * a.z_stride + g : nullptr;
     }
+    __device__ __forceinline__ void load(const MatvecArgs &a, Unit &u) const {
+#pragma unroll
+        for (int i = 0; i < Unit::kPer; ++i) {
+            u.s[i] = 0;
+            u.z[i] = 8;
+        }
+        if (a.scale_dtype == CK_F32) {
+#pragma unroll
+            for (int i = 0; i < Unit::kPer; ++i)
+                if (i < left) u.s[i] = ((const uint32_t *)s)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < Unit::kPer; ++i)
+                if (i < left) u.s[i] = ((const uint16_t *)s)[i];
+        }
+        if (z) {
+#pragma unroll
+            for (int i = 0; i < Unit::kPer; ++i)
+                if (i < left) u.z[i] = z[i];
+        }
+    }
+    __device__ __forceinline__ void next(const MatvecArgs &a) {
+        s += Unit::kGroups << (a.scale_dtype == CK_F32 ? 2 : 1);
+        if (z) z += Unit::kGroups;
+        left -= Unit::kGroups;
+    }
+};
+
+__device__ __forceinline__ float scale_value(uint32_t raw, int dtype) {
+    if (dtype == CK_F32) return __uint_as_float(raw);
+    if (dtype == CK_BF16) return __uint_as_float(raw << 16);
+    return __half2float(__ushort_as_half((unsigned short)raw));
 }
 
-// sum over the columns of a row's parts
+// The sum of a row's parts.
 __device__ __forceinline__ float join_parts(const float *c, int parts) {
     return parts == 1 ? c[0] : (c[2] + c[1]) + c[0];
 }
 
-template <typename T, int GROUP, int NT>
+__device__ __forceinline__ void store_y(const MatvecArgs &a, int64_t m, int64_t v, float sum) {
+    sum += a.bias ? a.bias[v] : 0.f;
+    const int64_t at = m * a.y_stride + v;
+    if (a.dtype == CK_F32)
+        ((float *)a.y)[at] = sum;
+    else if (a.dtype == CK_BF16)
+        ((__nv_bfloat16 *)a.y)[at] = __float2bfloat16_rn(sum);
+    else
+        ((__half *)a.y)[at] = __float2half_rn(sum);
+}
+
+template <bool HALF, int GROUP, int NT>
 __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, MatvecPlan p) {
-    extern __shared__ __align__(128) char smem[];
-    constexpr int kCols = 8 * NT;
+    extern __shared__ __align__(1024) char smem[];
+    constexpr int kCols = 8 * NT, kPer = kChunk / GROUP / 2;
     char *ring = smem;
     float *slots = (float *)(ring + kWarpsMv * kStages * kUnitBytes);  // [warps][2][16][kCols]
     int64_t *slot_tile = (int64_t *)(slots + kWarpsMv * 2 * 16 * kCols);
@@ -247,7 +341,12 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = lane >> 2, quad = lane & 3;
     const uint32_t my_ring = smem_at(ring) + warp * kStages * kUnitBytes;
-    T *y = (T *)a.y;
+    const uint32_t my_line = (lane & 15) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
+    // A lane's columns of x.  Those past the last read it again: their sums are not used.
+    int x_at[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) x_at[j] = min(8 * j + row, p.cols - 1) * p.x_pitch + quad * 16;
+    const int64_t groups = (a.K + GROUP - 1) / GROUP;
     const int64_t cta0 = p.cut(blockIdx.x), cta1 = p.cut(blockIdx.x + 1);
     asm volatile("griddepcontrol.launch_dependents;");
     for (int64_t s = 0; s < p.slabs; ++s) {
@@ -257,90 +356,100 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
         if (u0 >= u1) continue;
         const int64_t w0 = u0 + (u1 - u0) * warp / kWarpsMv, w1 = u0 + (u1 - u0) * (warp + 1) / kWarpsMv;
         const int64_t first = s * p.slab;  // the slab's first chunk
-        int64_t n = w1 - w0;
-        int64_t pt = (w0 - base) / sc, pc = (w0 - base) % sc, left = n;  // next to copy
-        int64_t t = pt, c = pc;                                         // next to multiply
-        int put = 0;
+        int n = (int)(w1 - w0), left = n;
+        int64_t t = (w0 - base) / sc;
+        int c = (int)((w0 - base) % sc);
+        Copier from;
+        from.end = first + sc;
+        from.seek(a, t, first + c);
+        uint32_t put = my_ring, get = my_ring;
         auto copy_next = [&] {
             if (left > 0) {
-                copy_unit(a, pt, first + pc, my_ring + put * kUnitBytes);
+                from.copy(a, put);
+                from.next(a, first);
                 --left;
-                if (++pc == sc) pc = 0, ++pt;
             }
-            put = put + 1 == kStages ? 0 : put + 1;
+            put = put + kUnitBytes == my_ring + kStages * kUnitBytes ? my_ring : put + kUnitBytes;
             asm volatile("cp.async.commit_group;");
         };
         for (int i = 0; i < kStages - 1; ++i) copy_next();
+        ScaleReader<GROUP> scales;
+        scales.seek(a, t, first + c, groups);
         UnitScales<GROUP> next;
-        if (n > 0) load_scales<T, GROUP>(a, t, first + c, next);
+        if (n > 0) scales.load(a, next);
         __syncthreads();  // the last slab's x and slots are done with
         if (lane < 2) slot_tile[2 * warp + lane] = -1;
-        stage_x<T>(a, p, first * kChunk, sc * (kChunk / 8), xs);
+        if constexpr (HALF)
+            stage_x<__half>(a, p, first * kChunk, (int)sc, xs);
+        else if (a.dtype == CK_F32)
+            stage_x<float>(a, p, first * kChunk, (int)sc, xs);
+        else
+            stage_x<__nv_bfloat16>(a, p, first * kChunk, (int)sc, xs);
         __syncthreads();
         float acc[NT][4] = {};
-        int64_t seg0 = c;  // chunk at which this tile's part began
-        int used = 0, get = 0;
+        bool from_start = c == 0;  // this tile's part began with the slab
+        int used = 0;
         for (; n > 0; --n) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2));
             __syncwarp();
             copy_next();
-            const UnitScales<GROUP> cur = next;
-            if (n > 1) {
-                const bool wrap = c + 1 == sc;
-                load_scales<T, GROUP>(a, wrap ? t + 1 : t, first + (wrap ? 0 : c + 1), next);
+            float cur[kPer];
+            uint32_t cur_z = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                cur[i] = scale_value(next.s[i], a.scale_dtype);
+                cur_z |= next.z[i] << (8 * i);
             }
-            const uint32_t unit = my_ring + get * kUnitBytes;
-            get = get + 1 == kStages ? 0 : get + 1;
-            float part[NT][4];
-            uint32_t zero[2] = {Pair<T>::base_plus(8), Pair<T>::base_plus(8)};
-            float scale[2];
+            cur_z &= 0x0f0f0f0fu;
+            const bool whole = c + 1 == (int)sc;
+            if (whole)
+                scales.seek(a, t + 1, first, groups);
+            else
+                scales.next(a);
+            if (n > 1) scales.load(a, next);
+            const uint32_t lines = get + my_line;
+            get = get + kUnitBytes == my_ring + kStages * kUnitBytes ? my_ring : get + kUnitBytes;
+            float part[NT][4], scale[2];
+            Zero<HALF> zero[2];
 #pragma unroll
-            for (int blk = 0; blk < kChunk / 32; ++blk) {  // 32 columns: one piece of each line
-                constexpr int kBlocks = GROUP / 32;
-                if (blk % kBlocks == 0) {
-                    const int g = blk / kBlocks;
+            for (int pair = 0; pair < kChunk / 64; ++pair) {
+                uint32_t w[2][2];  // [block of 32 columns][line, line + 8]
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(w[0][0]), "=r"(w[0][1]), "=r"(w[1][0]), "=r"(w[1][1])
+                             : "r"(lines ^ (pair << 5)));
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int idx = 2 * g + h;
-                        scale[h] = __shfl_sync(~0u, cur.s[idx / 4], (lane & ~3) | (idx & 3));
-                        if (a.zeros) zero[h] = __shfl_sync(~0u, cur.z[idx / 4], (lane & ~3) | (idx & 3));
+                for (int half = 0; half < 2; ++half) {
+                    constexpr int kBlocks = GROUP / 32;
+                    const int blk = 2 * pair + half, g = blk / kBlocks;
+                    if (blk % kBlocks == 0) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int from_lane = (lane & ~3) | (g / kPer * 2 + h);
+                            scale[h] = __shfl_sync(~0u, cur[g % kPer], from_lane);
+                            zero[h].set(__shfl_sync(~0u, cur_z, from_lane), g % kPer);
+                        }
                     }
+                    uint32_t lo[4], hi[4];
+                    nibbles<HALF>(w[half][0], zero[0], lo);
+                    nibbles<HALF>(w[half][1], zero[1], hi);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.f;
-                }
-                uint32_t w[2];
-                {
-                    const int r = lane & 15;
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
-                                 : "=r"(w[0]), "=r"(w[1])
-                                 : "r"(unit + r * 128 + ((blk ^ (r & 7)) << 4)));
-                }
-                uint32_t v[4][2];
+                    for (int j = 0; j < NT; ++j) {
+                        const uint4 b = *(const uint4 *)(xs + x_at[j] + c * (2 * kChunk) + blk * 64);
+                        if (blk % kBlocks == 0)
+                            mma<HALF, true>(part[j], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+                        else
+                            mma<HALF, false>(part[j], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+                        mma<HALF, false>(part[j], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+                    }
+                    if (blk % kBlocks == kBlocks - 1) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                        for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        v[j][h] = Pair<T>::sub((w[h] >> (4 * j) & 0x000f000fu) | Pair<T>::kBase, zero[h]);
-                const uint32_t a0[4] = {v[0][0], v[0][1], v[1][0], v[1][1]};
-                const uint32_t a1[4] = {v[2][0], v[2][1], v[3][0], v[3][1]};
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    uint4 b = make_uint4(0, 0, 0, 0);
-                    if (8 * j + row < p.cols)
-                        b = *(const uint4 *)(xs + (8 * j + row) * p.x_pitch + c * (2 * kChunk) + blk * 64 +
-                                             quad * 16);
-                    Pair<T>::mma(part[j], a0, b.x, b.y);
-                    Pair<T>::mma(part[j], a1, b.z, b.w);
-                }
-                if (blk % kBlocks == kBlocks - 1) {
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(scale[e >> 1], part[j][e], acc[j][e]);
+                            for (int e = 0; e < 4; ++e)
+                                acc[j][e] = fmaf(scale[e >> 1], part[j][e], acc[j][e]);
+                    }
                 }
             }
-            const bool whole = c + 1 == sc;
             if (whole || n == 1) {  // this tile's part ends here
                 const int slot = 2 * warp + used;
                 float *mine = slots + slot * 16 * kCols;
@@ -353,14 +462,14 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
                     acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
                 }
                 __syncwarp();
-                if (whole && seg0 == 0) {  // all of the slab's K: no other warp has a part
+                if (whole && from_start) {  // all of the slab's K: no other warp has a part
                     for (int i = lane; i < 16 * p.rows; i += 32) {
                         const int r = i & 15, m = i >> 4;
                         const int64_t v = t * 16 + r;
                         if (v >= a.V) continue;
-                        const float sum = join_parts(mine + r * kCols + m * kParts<T>, kParts<T>);
+                        const float sum = join_parts(mine + r * kCols + m * p.parts, p.parts);
                         if (p.slabs == 1)
-                            y[m * a.y_stride + v] = from_float<T>(sum + (a.bias ? a.bias[v] : 0.f));
+                            store_y(a, m, v, sum);
                         else
                             a.partial[(p.slot(s, t, blockIdx.x) * p.rows + m) * 16 + r] = sum;
                     }
@@ -368,9 +477,10 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
                     if (lane == 0) slot_tile[slot] = t;
                     ++used;
                 }
-                seg0 = 0;
+                from_start = true;
             }
-            if (whole) c = 0, ++t; else ++c;
+            c = whole ? 0 : c + 1;
+            t += whole;
         }
         __syncthreads();
         // parts of one tile lie in a row of slots: the warp that holds the first adds them up
@@ -394,11 +504,11 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
                 for (int e = at; e < 2 * kWarpsMv; ++e) {
                     if (slot_tile[e] < 0) continue;
                     if (slot_tile[e] != tile) break;
-                    sum += join_parts(slots + e * 16 * kCols + r * kCols + m * kParts<T>, kParts<T>);
+                    sum += join_parts(slots + e * 16 * kCols + r * kCols + m * p.parts, p.parts);
                 }
                 if (v >= a.V) continue;
                 if (alone)
-                    y[m * a.y_stride + v] = from_float<T>(sum + (a.bias ? a.bias[v] : 0.f));
+                    store_y(a, m, v, sum);
                 else
                     a.partial[(p.slot(s, tile, blockIdx.x) * p.rows + m) * 16 + r] = sum;
             }
@@ -407,9 +517,8 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
 }
 
 // Sums that cross CTAs or slabs, in the order of K.
-template <typename T> __global__ void __launch_bounds__(128) k_join(MatvecArgs a, MatvecPlan p) {
+__global__ void __launch_bounds__(128) k_join(MatvecArgs a, MatvecPlan p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    T *y = (T *)a.y;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.tiles * 16 * p.rows;
          i += (int64_t)gridDim.x * blockDim.x) {
         const int r = (int)(i & 15);
@@ -424,7 +533,7 @@ template <typename T> __global__ void __launch_bounds__(128) k_join(MatvecArgs a
             if (!crossed) break;
             for (int64_t b = b0; b <= b1; ++b) sum += a.partial[(p.slot(s, tile, b) * p.rows + m) * 16 + r];
         }
-        if (crossed) y[m * a.y_stride + v] = from_float<T>(sum + (a.bias ? a.bias[v] : 0.f));
+        if (crossed) store_y(a, m, v, sum);
     }
 }
 
@@ -433,18 +542,18 @@ size_t matvec_fixed_smem(int nt) {
 }
 
 int parts_of(int64_t dtype) { return dtype == CK_F32 ? 3 : 1; }
-// Rows of x that one launch takes: two tensor-core tiles of eight columns.
-int rows_at_once(int64_t dtype) { return 16 / parts_of(dtype); }
+int rows_at_once(int64_t dtype) { return kMostCols / parts_of(dtype); }
+int column_tiles(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
 
 MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms) {
     MatvecPlan p{};
     p.rows = (int)rows;
-    p.cols = (int)rows * parts_of(dtype);
+    p.parts = parts_of(dtype);
+    p.cols = (int)rows * p.parts;
     p.tiles = (V + 15) / 16;
     p.chunks = (K + kChunk - 1) / kChunk;
-    const int nt = (p.cols + 7) / 8;
-    const int64_t room = (int64_t)(kSmemMost - matvec_fixed_smem(nt)) / p.cols - 64;
-    const int64_t most = room / (2 * kChunk);
+    const size_t fixed = matvec_fixed_smem(column_tiles(p.cols));
+    const int64_t most = ((int64_t)(kSmemMost - fixed) / p.cols - 64) / (2 * kChunk);
     p.slabs = (p.chunks + most - 1) / most;
     p.slab = (p.chunks + p.slabs - 1) / p.slabs;
     p.slabs = (p.chunks + p.slab - 1) / p.slab;
@@ -456,8 +565,9 @@ MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sm
     const double equal = (double)p.units() / sms * unit + 2.0;
     p.aligned = p.slabs == 1 && whole <= equal;
     p.ctas = (int)(p.aligned ? by_tile : even < 1 ? 1 : even < sms ? even : sms);
-    p.x_pitch = (size_t)p.slab * 2 * kChunk + 64;
-    p.smem = matvec_fixed_smem(nt) + p.cols * p.x_pitch;
+    // 64 bytes past a multiple of 128: two columns side by side fill all banks
+    p.x_pitch = (int)p.slab * 2 * kChunk + 64;
+    p.smem = fixed + (size_t)p.cols * p.x_pitch;
     return p;
 }
 
@@ -465,12 +575,12 @@ size_t partial_bytes(const MatvecPlan &p) {
     return p.aligned ? 0 : (size_t)(p.slabs * p.tiles + p.ctas) * 16 * p.rows * sizeof(float);
 }
 
-template <typename T, int GROUP, int NT>
+template <bool HALF, int GROUP, int NT>
 cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(k_matvec<T, GROUP, NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
+    cudaError_t e = cudaFuncSetAttribute(k_matvec<HALF, GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmemMost);
     if (e != cudaSuccess) return e;
-    k_matvec<T, GROUP, NT><<<p.ctas, kWarpsMv * 32, p.smem, stream>>>(a, p);
+    k_matvec<HALF, GROUP, NT><<<p.ctas, kWarpsMv * 32, p.smem, stream>>>(a, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.aligned) return e;
     cudaLaunchConfig_t cfg{};
@@ -483,17 +593,21 @@ cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_join<T>, a, p);
+    return cudaLaunchKernelEx(&cfg, k_join, a, p);
 }
 
-template <typename T>
-cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
-    const bool two = p.cols > 8;
-    switch (a.group) {
-        case 32: return two ? launch_matvec<T, 32, 2>(a, p, stream) : launch_matvec<T, 32, 1>(a, p, stream);
-        case 64: return two ? launch_matvec<T, 64, 2>(a, p, stream) : launch_matvec<T, 64, 1>(a, p, stream);
-        default: return two ? launch_matvec<T, 128, 2>(a, p, stream) : launch_matvec<T, 128, 1>(a, p, stream);
+template <bool HALF, int GROUP>
+cudaError_t launch_columns(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
+    switch (column_tiles(p.cols)) {
+        case 1: return launch_matvec<HALF, GROUP, 1>(a, p, stream);
+        case 2: return launch_matvec<HALF, GROUP, 2>(a, p, stream);
+        default: return launch_matvec<HALF, GROUP, 4>(a, p, stream);
     }
+}
+
+template <int GROUP> cudaError_t launch_group(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
+    return a.dtype == CK_F16 ? launch_columns<true, GROUP>(a, p, stream)
+                             : launch_columns<false, GROUP>(a, p, stream);
 }
 
 struct QuantArgs {
@@ -587,7 +701,7 @@ extern "C" ck_status ck_int4_matvec(const void *x, int64_t dtype, int64_t M, int
         x_stride < 0 || y_stride < V)
         return fail(CK_ERR_INVALID_ARG, "int4_matvec: a row stride is shorter than its row");
     size_t need = 0;
-    const ck_status st = ck_int4_workspace_size(dtype, M, K, V, &need);
+    const ck_status st = ck_int4_workspace_size(dtype, M, K, V, group, &need);
     if (st != CK_OK) return st;
     if (need > 0 && !workspace) return fail(CK_ERR_INVALID_ARG, "int4_matvec: workspace is NULL");
     if (workspace_bytes < need || ((uintptr_t)workspace & 15u) != 0)
@@ -598,23 +712,22 @@ extern "C" ck_status ck_int4_matvec(const void *x, int64_t dtype, int64_t M, int
     for (int64_t m = 0; m < M && e == cudaSuccess; m += rows_at_once(dtype)) {
         const int64_t rows = M - m < rows_at_once(dtype) ? M - m : rows_at_once(dtype);
         const size_t el = dtype_size(dtype);
-        MatvecArgs a{(const char *)x + m * x_stride * el, rows, K, x_stride, qweight, V, q_pitch, scales,
-                     (int)scale_dtype, s_stride, zeros, z_stride, bias, (int)group,
+        MatvecArgs a{(const char *)x + m * x_stride * el, dtype, rows, K, x_stride, qweight, V, q_pitch,
+                     scales, (int)scale_dtype, s_stride, zeros, z_stride, bias,
                      (char *)y + m * y_stride * el, y_stride, (float *)workspace};
         const MatvecPlan p = matvec_plan(dtype, rows, K, V, sms);
-        with_dtype(dtype, [&](auto *tag) {
-            using T = std::remove_pointer_t<decltype(tag)>;
-            e = launch_matvec<T>(a, p, (cudaStream_t)stream);
-        });
+        cudaStream_t st = (cudaStream_t)stream;
+        e = group == 32 ? launch_group<32>(a, p, st) : group == 64 ? launch_group<64>(a, p, st)
+                                                                  : launch_group<128>(a, p, st);
     }
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "k_matvec launch");
 }
 
 extern "C" ck_status ck_int4_workspace_size(int64_t dtype, int64_t M, int64_t K, int64_t V,
-                                            size_t *bytes) {
+                                            int64_t group, size_t *bytes) {
     if (!known_dtype(dtype) || M < 0 || K < 1 || V < 0 || K >= ((int64_t)1 << 30) || V >= ((int64_t)1 << 30) ||
-        !bytes)
-        return fail(CK_ERR_INVALID_ARG, "int4_workspace_size: bad dtype, size or NULL bytes");
+        !known_group(group) || !bytes)
+        return fail(CK_ERR_INVALID_ARG, "int4_workspace_size: bad dtype, size, group or NULL bytes");
     *bytes = 0;
     if (M == 0 || V == 0) return CK_OK;
     const int sms = device_sms();
