@@ -5,12 +5,6 @@
 namespace ck {
 namespace {
 
-__device__ __forceinline__ float load_scale(const void *p, int dtype, int64_t i) {
-    if (dtype == CK_F32) return ((const float *)p)[i];
-    if (dtype == CK_BF16) return __bfloat162float(((const __nv_bfloat16 *)p)[i]);
-    return __half2float(((const __half *)p)[i]);
-}
-
 struct MatvecArgs {
     const void *x;
     int64_t dtype, M, K, x_stride;
@@ -41,30 +35,29 @@ struct MatvecArgs {
 // copies that each warp keeps for itself, and no warp waits for another until
 // the end.
 //
-// A unit is 16 weight rows by 256 columns (2 KB).  K is cut into slabs whose x
-// fits in shared memory; the units, in the order (slab, 16-row tile, chunk),
+// A unit is 32 weight rows by 128 columns (2 KB).  K is cut into slabs whose x
+// fits in shared memory; the units, in the order (slab, 32-row tile, chunk),
 // are dealt to CTAs, and a CTA's to its warps, in equal runs.  A run's first and
 // last tile may be shared with its neighbours: those sums meet in shared memory
 // and, where a tile crosses CTAs or slabs, in the slots of `partial`, which
 // k_join adds up in a fixed order.
 constexpr int kWarpsMv = 16;                // warps of a CTA, one CTA on an SM
 constexpr int kStages = 4;                  // ring of units per warp
-constexpr int kUnitBytes = 16 * 128;
-constexpr int kChunk = 256;                 // columns of a unit
+constexpr int kTileRows = 32;
+constexpr int kChunk = 128;                 // columns of a unit
+constexpr int kUnitBytes = kTileRows * kChunk / 2;
 constexpr size_t kSmemMost = 232448;
-constexpr int kMostCols = 32;               // tensor-core columns of one launch
 
 struct MatvecPlan {
     int rows;          // rows of x in this launch
-    int parts;         // 16-bit parts of an x: columns m * parts + part
-    int cols;
-    int64_t tiles;     // 16-row tiles of V
+    int64_t tiles;     // 32-row tiles of V
     int64_t chunks;    // chunks of K
     int64_t slab;      // chunks of a slab (the last may have fewer)
     int64_t slabs;
     int ctas;
     int aligned;       // CTAs take whole tiles: nothing crosses them
     int x_pitch;       // bytes between columns of x in shared memory
+    int x_cols;        // tensor-core columns that x takes
     size_t smem;
 
     __host__ __device__ int64_t units() const { return tiles * chunks; }
@@ -129,21 +122,25 @@ template <> struct Zero<true> {
         asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(odd) : "r"(even), "r"(0xbc00bc00u), "r"(0x63806380u));
     }
 };
+// (w & mask) | base in one instruction
+__device__ __forceinline__ uint32_t put_under(uint32_t w, uint32_t mask, uint32_t base) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(base));
+    return r;
+}
 template <bool HALF>
 __device__ __forceinline__ void nibbles(uint32_t w, const Zero<HALF> &z, uint32_t (&v)[4]) {
     if constexpr (HALF) {
-        const uint32_t w8 = w >> 8;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[0]) : "r"((w & 0x000f000fu) | 0x64006400u), "r"(z.even));
-        asm("fma.rn.f16x2 %0, %1, %2, %3;"
-            : "=r"(v[1]) : "r"((w & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(z.odd));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[2]) : "r"((w8 & 0x000f000fu) | 0x64006400u), "r"(z.even));
-        asm("fma.rn.f16x2 %0, %1, %2, %3;"
-            : "=r"(v[3]) : "r"((w8 & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(z.odd));
+        const uint32_t w8 = w >> 8, lo = 0x000f000fu, hi = 0x00f000f0u, base = 0x64006400u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[0]) : "r"(put_under(w, lo, base)), "r"(z.even));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[1]) : "r"(put_under(w, hi, base)), "r"(0x2c002c00u), "r"(z.odd));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[2]) : "r"(put_under(w8, lo, base)), "r"(z.even));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[3]) : "r"(put_under(w8, hi, base)), "r"(0x2c002c00u), "r"(z.odd));
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             asm("sub.rn.bf16x2 %0, %1, %2;"
-                : "=r"(v[j]) : "r"((w >> (4 * j) & 0x000f000fu) | 0x43004300u), "r"(z.even));
+                : "=r"(v[j]) : "r"(put_under(w >> (4 * j), 0x000f000fu, 0x43004300u)), "r"(z.even));
     }
 }
 
@@ -179,132 +176,99 @@ __device__ __forceinline__ void load8(const MatvecArgs &a, int64_t m, int64_t k,
     }
 }
 
+// The tensor-core column of part `part` of row m: the parts of two rows of 32-bit
+// x lie in one tile of eight columns such that a lane's two sums are those of the
+// two rows, and its neighbours' those of the other parts.
+template <typename T> __device__ __forceinline__ int column(int m, int part) {
+    return sizeof(T) == 4 ? 8 * (m >> 1) + 2 * part + (m & 1) : m;
+}
+
 // x of a slab into shared memory, one line a column, eight columns of K at a
 // time in the order 0 4 1 5 2 6 3 7, in which nibbles come out of a word two at a
 // time.
 template <typename T>
-__device__ void stage_x(const MatvecArgs &a, const MatvecPlan &p, int64_t k0, int lines, char *xs) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // a warp takes a line of 256 columns: 32 times eight
-    for (int i = warp; i < lines * p.rows; i += kWarpsMv) {
-        const int m = i / lines, j = i % lines * 32 + lane;
-        T v[8];
-        load8<T>(a, m, k0 + 8 * j, v);
-        constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
-        uint16_t part[8][3];
+__device__ __forceinline__ void stage_x(const MatvecArgs &a, const MatvecPlan &p, int k0, int blocks, char *xs) {
+    constexpr int kParts = sizeof(T) == 4 ? 3 : 1, kBatch = sizeof(T) == 4 ? 2 : 4;
+    int m = 0, j = threadIdx.x;
+    auto settle = [&] {
+        while (j >= blocks && m < p.rows) j -= blocks, ++m;
+    };
+    settle();
+    while (m < p.rows) {
+        T v[kBatch][8];
+        int at_m[kBatch], at_j[kBatch];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (sizeof(T) == 4)
-                split3(v[e], part[e]);
-            else
-                memcpy(&part[e][0], &v[e], 2);
+        for (int i = 0; i < kBatch; ++i) {  // all loads of a batch are on their way before the first is used
+            at_m[i] = m;
+            at_j[i] = j;
+            if (m < p.rows) load8<T>(a, m, k0 + 8 * j, v[i]);
+            j += kWarpsMv * 32;
+            settle();
         }
 #pragma unroll
-        for (int s = 0; s < kParts; ++s) {
-            uint4 w;
-            w.x = part[0][s] | (uint32_t)part[4][s] << 16;
-            w.y = part[1][s] | (uint32_t)part[5][s] << 16;
-            w.z = part[2][s] | (uint32_t)part[6][s] << 16;
-            w.w = part[3][s] | (uint32_t)part[7][s] << 16;
-            *(uint4 *)(xs + (kParts * m + s) * p.x_pitch + 16 * j) = w;
+        for (int i = 0; i < kBatch; ++i) {
+            if (at_m[i] >= p.rows) break;
+            uint16_t part[8][3];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if constexpr (sizeof(T) == 4)
+                    split3(v[i][e], part[e]);
+                else
+                    memcpy(&part[e][0], &v[i][e], 2);
+            }
+#pragma unroll
+            for (int s = 0; s < kParts; ++s) {
+                uint4 w;
+                w.x = part[0][s] | (uint32_t)part[4][s] << 16;
+                w.y = part[1][s] | (uint32_t)part[5][s] << 16;
+                w.z = part[2][s] | (uint32_t)part[6][s] << 16;
+                w.w = part[3][s] | (uint32_t)part[7][s] << 16;
+                *(uint4 *)(xs + column<T>(at_m[i], s) * p.x_pitch + 16 * at_j[i]) = w;
+            }
         }
     }
 }
 
 // What a warp copies next: its lanes' place in the weights, moved on by a chunk
-// at a time.  A unit is eight 16-byte pieces of 16 lines of 128 bytes; the
-// pieces of line r lie exchanged by r, so that eight lines are read without a
-// conflict.
+// at a time.  A unit is four 16-byte pieces of 32 lines of 64 bytes; the pieces
+// of line r lie exchanged by r / 2, so that a piece of eight lines is read without
+// a conflict.
 struct Copier {
-    const uint8_t *src;  // the lane's piece in line lane / 8
-    int64_t tile, chunk, end;  // the slab's chunks: [first, end)
-    __device__ __forceinline__ void seek(const MatvecArgs &a, int64_t tile_, int64_t chunk_) {
+    const uint8_t *src;     // the lane's piece in line lane / 4
+    int tile, chunk;
+    __device__ __forceinline__ void seek(const MatvecArgs &a, int tile_, int chunk_) {
         const int lane = threadIdx.x & 31;
         tile = tile_;
         chunk = chunk_;
-        src = a.q + (tile * 16 + (lane >> 3)) * a.q_pitch + chunk * 128 + (lane & 7) * 16;
+        src = a.q + (int64_t)(tile * kTileRows + (lane >> 2)) * a.q_pitch + chunk * (kChunk / 2) + (lane & 3) * 16;
     }
     __device__ __forceinline__ void copy(const MatvecArgs &a, uint32_t dst) const {
         const int lane = threadIdx.x & 31;
-        // lines 4 i + lane / 8: their low three bits are those of lane / 8, and 4 for odd i
-        const uint32_t at = dst + (lane >> 3) * 128, p0 = ((lane & 7) ^ (lane >> 3)) << 4, p1 = p0 ^ 64;
-        if (tile * 16 + 16 <= a.V && (chunk + 1) * 256 <= a.K) {
+        const uint32_t at = dst + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3)) << 4);
+        if ((tile + 1) * kTileRows <= (int)a.V && (chunk + 1) * kChunk <= (int)a.K) {
             const uint8_t *s = src;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + i * 512 + (i & 1 ? p1 : p0)),
-                             "l"(s));
-                s += 4 * a.q_pitch;
+                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(at + i * 512), "l"(s));
+                s += 8 * a.q_pitch;
             }
             return;
         }
         // bytes past a row's end and rows past V become zeros
-        const int64_t from = chunk * 128 + (lane & 7) * 16, row_bytes = (a.K + 1) / 2;
-        const int n = row_bytes - from >= 16 ? 16 : row_bytes > from ? (int)(row_bytes - from) : 0;
+        const int from = chunk * (kChunk / 2) + (lane & 3) * 16, row_bytes = (int)((a.K + 1) / 2);
+        const int n = row_bytes - from >= 16 ? 16 : row_bytes > from ? row_bytes - from : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int m = tile * 16 + 4 * i + (lane >> 3) < a.V ? n : 0;
-            const uint8_t *s = m ? src + 4 * i * a.q_pitch : a.q;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             at + i * 512 + (i & 1 ? p1 : p0)),
-                         "l"(s), "r"(m));
+            const int m = tile * kTileRows + 8 * i + (lane >> 2) < (int)a.V ? n : 0;
+            const uint8_t *s = m ? src + 8 * i * a.q_pitch : a.q;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + i * 512), "l"(s), "r"(m));
         }
     }
-    __device__ __forceinline__ void next(const MatvecArgs &a, int64_t first) {
+    __device__ __forceinline__ void next(const MatvecArgs &a, int first, int end) {
         if (++chunk == end)
             seek(a, tile + 1, first);
         else
-            src += 128;
-    }
-};
-
-// Scales and zero points of a unit, dealt over the four lanes of a row: lane
-// quad holds groups (quad / 2) kPer .. + kPer - 1 of row (lane / 4) + 8 (quad % 2).
-// Kept as they come from memory until the unit is multiplied: a conversion here
-// would wait for the loads.
-template <int GROUP> struct UnitScales {
-    static constexpr int kGroups = kChunk / GROUP, kPer = kGroups / 2;
-    uint32_t s[kPer], z[kPer];
-};
-
-template <int GROUP> struct ScaleReader {
-    using Unit = UnitScales<GROUP>;
-    const char *s;
-    const uint8_t *z;
-    int64_t left;  // groups of the row from this lane's on; none for rows past V
-    __device__ __forceinline__ void seek(const MatvecArgs &a, int64_t tile, int64_t chunk, int64_t groups) {
-        const int lane = threadIdx.x & 31;
-        const int64_t v = tile * 16 + (lane >> 2) + 8 * (lane & 1);
-        const int64_t g = chunk * Unit::kGroups + (lane >> 1 & 1) * Unit::kPer;
-        left = v < a.V ? groups - g : 0;
-        s = (const char *)a.scales + ((v * a.s_stride + g) << (a.scale_dtype == CK_F32 ? 2 : 1));
-        z = a.zeros ? a.zeros + v * a.z_stride + g : nullptr;
-    }
-    __device__ __forceinline__ void load(const MatvecArgs &a, Unit &u) const {
-#pragma unroll
-        for (int i = 0; i < Unit::kPer; ++i) {
-            u.s[i] = 0;
-            u.z[i] = 8;
-        }
-        if (a.scale_dtype == CK_F32) {
-#pragma unroll
-            for (int i = 0; i < Unit::kPer; ++i)
-                if (i < left) u.s[i] = ((const uint32_t *)s)[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < Unit::kPer; ++i)
-                if (i < left) u.s[i] = ((const uint16_t *)s)[i];
-        }
-        if (z) {
-#pragma unroll
-            for (int i = 0; i < Unit::kPer; ++i)
-                if (i < left) u.z[i] = z[i];
-        }
-    }
-    __device__ __forceinline__ void next(const MatvecArgs &a) {
-        s += Unit::kGroups << (a.scale_dtype == CK_F32 ? 2 : 1);
-        if (z) z += Unit::kGroups;
-        left -= Unit::kGroups;
+            src += kChunk / 2;
     }
 };
 
@@ -314,10 +278,44 @@ __device__ __forceinline__ float scale_value(uint32_t raw, int dtype) {
     return __half2float(__ushort_as_half((unsigned short)raw));
 }
 
-// The sum of a row's parts.
-__device__ __forceinline__ float join_parts(const float *c, int parts) {
-    return parts == 1 ? c[0] : (c[2] + c[1]) + c[0];
-}
+// Scales and zero points, read eight groups of a tile's 32 rows at a time: lane l
+// of load i takes group l % 8 of row 4 i + l / 8, so that a load touches four rows'
+// sectors and not 32.  Kept as they come from memory until the groups are begun (a
+// conversion would wait for the loads), then left in shared memory as [row][8].
+template <int GROUP> struct ScaleReader {
+    static constexpr int kUnits = 8 * GROUP / kChunk;  // units of eight groups
+    uint32_t s[8], z[8];
+    int tile, eight;  // what s and z hold
+    __device__ __forceinline__ void load(const MatvecArgs &a, int tile_, int eight_, int groups) {
+        tile = tile_;
+        eight = eight_;
+        const int lane = threadIdx.x & 31, g = 8 * eight + (lane & 7), v = tile * kTileRows + (lane >> 3);
+        const int rows = g < groups ? (int)a.V - v : 0;  // row 4 i is there if 4 i < rows
+        if (a.scale_dtype == CK_F32) {
+            const uint32_t *p = (const uint32_t *)a.scales + v * a.s_stride + g;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = 4 * i < rows ? p[4 * i * a.s_stride] : 0u;
+        } else {
+            const uint16_t *p = (const uint16_t *)a.scales + v * a.s_stride + g;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = 4 * i < rows ? p[4 * i * a.s_stride] : 0u;
+        }
+        if (a.zeros) {
+            const uint8_t *p = a.zeros + v * a.z_stride + g;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = 4 * i < rows ? p[4 * i * a.z_stride] : 8u;
+        }
+    }
+    __device__ __forceinline__ void leave(const MatvecArgs &a, float *scales, uint8_t *zeros) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            scales[32 * i + lane] = scale_value(s[i], a.scale_dtype);
+            zeros[32 * i + lane] = a.zeros ? (uint8_t)(z[i] & 15) : (uint8_t)8;
+        }
+    }
+};
+
 
 __device__ __forceinline__ void store_y(const MatvecArgs &a, int64_t m, int64_t v, float sum) {
     sum += a.bias ? a.bias[v] : 0.f;
@@ -333,184 +331,220 @@ __device__ __forceinline__ void store_y(const MatvecArgs &a, int64_t m, int64_t 
 template <bool HALF, int GROUP, int NT>
 __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, MatvecPlan p) {
     extern __shared__ __align__(1024) char smem[];
-    constexpr int kCols = 8 * NT, kPer = kChunk / GROUP / 2;
-    char *ring = smem;
-    float *slots = (float *)(ring + kWarpsMv * kStages * kUnitBytes);  // [warps][2][16][kCols]
-    int64_t *slot_tile = (int64_t *)(slots + kWarpsMv * 2 * 16 * kCols);
-    char *xs = (char *)(slot_tile + kWarpsMv * 2);
+    constexpr int kGroups = kChunk / GROUP;
+    // per warp: its ring, in which its last part of a sum is left when it is done; its
+    // first part; scales and zero points of the eight groups at hand
+    const int part_floats = kTileRows * p.rows;
+    float *heads = (float *)(smem + kWarpsMv * kStages * kUnitBytes);
+    float *all_scales = heads + kWarpsMv * part_floats;
+    uint8_t *all_zeros = (uint8_t *)(all_scales + kWarpsMv * kTileRows * 8);
+    int *part_tile = (int *)(all_zeros + kWarpsMv * kTileRows * 8);  // [warps][first, last]
+    char *xs = (char *)(part_tile + kWarpsMv * 2);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = lane >> 2, quad = lane & 3;
-    const uint32_t my_ring = smem_at(ring) + warp * kStages * kUnitBytes;
-    const uint32_t my_line = (lane & 15) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
+    const uint32_t my_ring = smem_at(smem) + warp * kStages * kUnitBytes;
+    const uint32_t my_line = lane * 64, my_swap = (lane >> 1 & 3) << 4;
+    float *my_scales = all_scales + warp * kTileRows * 8;
+    uint8_t *my_zeros = all_zeros + warp * kTileRows * 8;
+    auto part_at = [&](int w, int k) {
+        return k ? (float *)(smem + w * kStages * kUnitBytes) : heads + w * part_floats;
+    };
     // A lane's columns of x.  Those past the last read it again: their sums are not used.
     int x_at[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) x_at[j] = min(8 * j + row, p.cols - 1) * p.x_pitch + quad * 16;
-    const int64_t groups = (a.K + GROUP - 1) / GROUP;
+    for (int j = 0; j < NT; ++j) {
+        int col = 8 * j + row;
+        if (!HALF && a.dtype == CK_F32 && (col & 7) >= 6) col = 8 * j;
+        while (!HALF && a.dtype == CK_F32 && 2 * (col >> 3) + (col & 1) >= p.rows) --col;
+        x_at[j] = min(col, p.x_cols - 1) * p.x_pitch + quad * 16;
+    }
+    const int groups = (int)((a.K + GROUP - 1) / GROUP);
     const int64_t cta0 = p.cut(blockIdx.x), cta1 = p.cut(blockIdx.x + 1);
     asm volatile("griddepcontrol.launch_dependents;");
     for (int64_t s = 0; s < p.slabs; ++s) {
-        const int64_t sc = p.slab_chunks(s), base = p.slab_first(s);
+        const int sc = (int)p.slab_chunks(s);
+        const int64_t base = p.slab_first(s);
         const int64_t u0 = cta0 > base ? cta0 : base;
         const int64_t u1 = cta1 < base + sc * p.tiles ? cta1 : base + sc * p.tiles;
         if (u0 >= u1) continue;
         const int64_t w0 = u0 + (u1 - u0) * warp / kWarpsMv, w1 = u0 + (u1 - u0) * (warp + 1) / kWarpsMv;
-        const int64_t first = s * p.slab;  // the slab's first chunk
+        const int first = (int)(s * p.slab);  // the slab's first chunk
         int n = (int)(w1 - w0), left = n;
-        int64_t t = (w0 - base) / sc;
-        int c = (int)((w0 - base) % sc);
+        int t = (int)((w0 - base) / sc), c = (int)((w0 - base) % sc);
+        __syncthreads();  // the last slab's x and parts of sums are done with
         Copier from;
-        from.end = first + sc;
         from.seek(a, t, first + c);
         uint32_t put = my_ring, get = my_ring;
         auto copy_next = [&] {
             if (left > 0) {
                 from.copy(a, put);
-                from.next(a, first);
+                from.next(a, first, first + sc);
                 --left;
             }
             put = put + kUnitBytes == my_ring + kStages * kUnitBytes ? my_ring : put + kUnitBytes;
             asm volatile("cp.async.commit_group;");
         };
         for (int i = 0; i < kStages - 1; ++i) copy_next();
-        ScaleReader<GROUP> scales;
-        scales.seek(a, t, first + c, groups);
-        UnitScales<GROUP> next;
-        if (n > 0) scales.load(a, next);
-        __syncthreads();  // the last slab's x and slots are done with
-        if (lane < 2) slot_tile[2 * warp + lane] = -1;
+        ScaleReader<GROUP> next;
+        constexpr int kUnits = ScaleReader<GROUP>::kUnits;
+        if (n > 0) next.load(a, t, (first + c) / kUnits, groups);
+        bool begin = true;  // the next unit is the first of its eight groups here
+        if (lane < 2) part_tile[2 * warp + lane] = -1;
         if constexpr (HALF)
-            stage_x<__half>(a, p, first * kChunk, (int)sc, xs);
+            stage_x<__half>(a, p, first * kChunk, sc * (kChunk / 8), xs);
         else if (a.dtype == CK_F32)
-            stage_x<float>(a, p, first * kChunk, (int)sc, xs);
+            stage_x<float>(a, p, first * kChunk, sc * (kChunk / 8), xs);
         else
-            stage_x<__nv_bfloat16>(a, p, first * kChunk, (int)sc, xs);
+            stage_x<__nv_bfloat16>(a, p, first * kChunk, sc * (kChunk / 8), xs);
         __syncthreads();
-        float acc[NT][4] = {};
+        float acc[NT][2][4] = {};  // [.][rows 0-15, 16-31][.]
         bool from_start = c == 0;  // this tile's part began with the slab
-        int used = 0;
         for (; n > 0; --n) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2));
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
             __syncwarp();
             copy_next();
-            float cur[kPer];
-            uint32_t cur_z = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                cur[i] = scale_value(next.s[i], a.scale_dtype);
-                cur_z |= next.z[i] << (8 * i);
+            const bool whole = c + 1 == sc;
+            if (begin) {
+                next.leave(a, my_scales, my_zeros);
+                int t1 = t, e1 = next.eight + 1;
+                if (e1 * kUnits >= first + sc) ++t1, e1 = first / kUnits;
+                next.load(a, t1, e1, groups);  // past the last tile: nothing
+                __syncwarp();
             }
-            cur_z &= 0x0f0f0f0fu;
-            const bool whole = c + 1 == (int)sc;
-            if (whole)
-                scales.seek(a, t + 1, first, groups);
-            else
-                scales.next(a);
-            if (n > 1) scales.load(a, next);
+            const int in_eight = (first + c) % kUnits;
+            begin = whole || in_eight == kUnits - 1;
+            float scale[4][kGroups];  // of rows row + 8 h
+            uint32_t zeros[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int at = (row + 8 * h) * 8 + in_eight * kGroups;
+                if constexpr (kGroups == 4) {
+                    *(float4 *)scale[h] = *(const float4 *)(my_scales + at);
+                    zeros[h] = *(const uint32_t *)(my_zeros + at);
+                } else if constexpr (kGroups == 2) {
+                    *(float2 *)scale[h] = *(const float2 *)(my_scales + at);
+                    zeros[h] = *(const uint16_t *)(my_zeros + at);
+                } else {
+                    scale[h][0] = my_scales[at];
+                    zeros[h] = my_zeros[at];
+                }
+            }
             const uint32_t lines = get + my_line;
             get = get + kUnitBytes == my_ring + kStages * kUnitBytes ? my_ring : get + kUnitBytes;
-            float part[NT][4], scale[2];
-            Zero<HALF> zero[2];
+            const char *xc = xs + c * (2 * kChunk);
+            float part[NT][2][4];
+            Zero<HALF> zero[4];
 #pragma unroll
-            for (int pair = 0; pair < kChunk / 64; ++pair) {
-                uint32_t w[2][2];  // [block of 32 columns][line, line + 8]
+            for (int blk = 0; blk < kChunk / 32; ++blk) {  // 32 columns: a piece of each line
+                constexpr int kBlocks = GROUP / 32;
+                const int g = blk / kBlocks;
+                uint32_t w[4];  // rows row + 8 h
                 asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(w[0][0]), "=r"(w[0][1]), "=r"(w[1][0]), "=r"(w[1][1])
-                             : "r"(lines ^ (pair << 5)));
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(lines + (my_swap ^ (blk << 4))));
+                uint32_t v[4][4];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    constexpr int kBlocks = GROUP / 32;
-                    const int blk = 2 * pair + half, g = blk / kBlocks;
-                    if (blk % kBlocks == 0) {
+                for (int h = 0; h < 4; ++h) {
+                    if (blk % kBlocks == 0) zero[h].set(zeros[h], g);
+                    nibbles<HALF>(w[h], zero[h], v[h]);
+                }
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int from_lane = (lane & ~3) | (g / kPer * 2 + h);
-                            scale[h] = __shfl_sync(~0u, cur[g % kPer], from_lane);
-                            zero[h].set(__shfl_sync(~0u, cur_z, from_lane), g % kPer);
-                        }
-                    }
-                    uint32_t lo[4], hi[4];
-                    nibbles<HALF>(w[half][0], zero[0], lo);
-                    nibbles<HALF>(w[half][1], zero[1], hi);
+                for (int j = 0; j < NT; ++j) {
+                    const uint4 b = *(const uint4 *)(xc + x_at[j] + blk * 64);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const uint4 b = *(const uint4 *)(xs + x_at[j] + c * (2 * kChunk) + blk * 64);
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t(&lo)[4] = v[2 * i], (&hi)[4] = v[2 * i + 1];
                         if (blk % kBlocks == 0)
-                            mma<HALF, true>(part[j], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+                            mma<HALF, true>(part[j][i], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
                         else
-                            mma<HALF, false>(part[j], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-                        mma<HALF, false>(part[j], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+                            mma<HALF, false>(part[j][i], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
                     }
-                    if (blk % kBlocks == kBlocks - 1) {
 #pragma unroll
-                        for (int j = 0; j < NT; ++j)
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t(&lo)[4] = v[2 * i], (&hi)[4] = v[2 * i + 1];
+                        mma<HALF, false>(part[j][i], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+                    }
+                }
+                if (blk % kBlocks == kBlocks - 1) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                acc[j][e] = fmaf(scale[e >> 1], part[j][e], acc[j][e]);
-                    }
+                                acc[j][i][e] = fmaf(scale[2 * i + (e >> 1)][g], part[j][i][e], acc[j][i][e]);
                 }
             }
             if (whole || n == 1) {  // this tile's part ends here
-                const int slot = 2 * warp + used;
-                float *mine = slots + slot * 16 * kCols;
+                if (!HALF && a.dtype == CK_F32) {
+                    // the three parts of x lie in lanes quad 0, 1 and 2: smallest first
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float p1 = __shfl_down_sync(~0u, acc[j][i][e], 1),
+                                            p2 = __shfl_down_sync(~0u, acc[j][i][e], 2);
+                                acc[j][i][e] = (p2 + p1) + acc[j][i][e];
+                            }
+                }
+                const bool done = whole && from_start;  // all of the slab's K: no other warp has a part
+                const int last = from_start ? 1 : 0;    // a part that runs on from another warp's is a first one
+                float *mine = part_at(warp, last);
+                if (!done && lane == 0) part_tile[2 * warp + last] = t;
                 __syncwarp();
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    *(float2 *)(mine + row * kCols + 8 * j + 2 * quad) = make_float2(acc[j][0], acc[j][1]);
-                    *(float2 *)(mine + (row + 8) * kCols + 8 * j + 2 * quad) =
-                        make_float2(acc[j][2], acc[j][3]);
-                    acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-                }
-                __syncwarp();
-                if (whole && from_start) {  // all of the slab's K: no other warp has a part
-                    for (int i = lane; i < 16 * p.rows; i += 32) {
-                        const int r = i & 15, m = i >> 4;
-                        const int64_t v = t * 16 + r;
-                        if (v >= a.V) continue;
-                        const float sum = join_parts(mine + r * kCols + m * p.parts, p.parts);
-                        if (p.slabs == 1)
-                            store_y(a, m, v, sum);
-                        else
-                            a.partial[(p.slot(s, t, blockIdx.x) * p.rows + m) * 16 + r] = sum;
-                    }
-                } else {
-                    if (lane == 0) slot_tile[slot] = t;
-                    ++used;
-                }
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 16 * i + row + 8 * (e >> 1);
+                            const int m = !HALF && a.dtype == CK_F32 ? (quad ? p.rows : 2 * j + (e & 1))
+                                                                     : 8 * j + 2 * quad + (e & 1);
+                            const float sum = acc[j][i][e];
+                            acc[j][i][e] = 0.f;
+                            if (m >= p.rows) continue;
+                            const int64_t v = (int64_t)t * kTileRows + r;
+                            if (!done)
+                                mine[m * kTileRows + r] = sum;
+                            else if (p.slabs > 1)
+                                a.partial[(p.slot(s, t, blockIdx.x) * p.rows + m) * kTileRows + r] = sum;
+                            else if (v < a.V)
+                                store_y(a, m, v, sum);
+                        }
                 from_start = true;
             }
             c = whole ? 0 : c + 1;
             t += whole;
         }
         __syncthreads();
-        // parts of one tile lie in a row of slots: the warp that holds the first adds them up
+        // parts of one tile follow one another: the warp that holds the first adds them up
         for (int k = 0; k < 2; ++k) {
-            const int at = 2 * warp + k;
-            const int64_t tile = slot_tile[at];
+            const int at = 2 * warp + k, tile = part_tile[at];
             if (tile < 0) continue;
             bool head = true;
-            for (int i = at - 1; i >= 0 && head; --i)
-                if (slot_tile[i] >= 0) {
-                    head = slot_tile[i] != tile;
+            for (int i = at - 1; i >= 0; --i)
+                if (part_tile[i] >= 0) {
+                    head = part_tile[i] != tile;
                     break;
                 }
             if (!head) continue;
-            const int64_t tu = base + tile * sc;
+            const int64_t tu = base + (int64_t)tile * sc;
             const bool alone = p.slabs == 1 && tu >= u0 && tu + sc <= u1;
-            for (int i = lane; i < 16 * p.rows; i += 32) {
-                const int r = i & 15, m = i >> 4;
-                const int64_t v = tile * 16 + r;
+            for (int m = 0; m < p.rows; ++m) {
                 float sum = 0.f;
                 for (int e = at; e < 2 * kWarpsMv; ++e) {
-                    if (slot_tile[e] < 0) continue;
-                    if (slot_tile[e] != tile) break;
-                    sum += join_parts(slots + e * 16 * kCols + r * kCols + m * p.parts, p.parts);
+                    if (part_tile[e] < 0) continue;
+                    if (part_tile[e] != tile) break;
+                    sum += part_at(e >> 1, e & 1)[m * kTileRows + lane];
                 }
-                if (v >= a.V) continue;
-                if (alone)
+                const int64_t v = (int64_t)tile * kTileRows + lane;
+                if (!alone)
+                    a.partial[(p.slot(s, tile, blockIdx.x) * p.rows + m) * kTileRows + lane] = sum;
+                else if (v < a.V)
                     store_y(a, m, v, sum);
-                else
-                    a.partial[(p.slot(s, tile, blockIdx.x) * p.rows + m) * 16 + r] = sum;
             }
         }
     }
@@ -519,10 +553,10 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
 // Sums that cross CTAs or slabs, in the order of K.
 __global__ void __launch_bounds__(128) k_join(MatvecArgs a, MatvecPlan p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.tiles * 16 * p.rows;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.tiles * kTileRows * p.rows;
          i += (int64_t)gridDim.x * blockDim.x) {
-        const int r = (int)(i & 15);
-        const int64_t tile = i / 16 % p.tiles, m = i / 16 / p.tiles, v = tile * 16 + r;
+        const int r = (int)(i % kTileRows);
+        const int64_t tile = i / kTileRows % p.tiles, m = i / kTileRows / p.tiles, v = tile * kTileRows + r;
         if (v >= a.V) continue;
         float sum = 0.f;
         bool crossed = p.slabs > 1;
@@ -531,29 +565,25 @@ __global__ void __launch_bounds__(128) k_join(MatvecArgs a, MatvecPlan p) {
             const int64_t b0 = p.cta_of(u), b1 = p.cta_of(e - 1);
             crossed |= b0 != b1;
             if (!crossed) break;
-            for (int64_t b = b0; b <= b1; ++b) sum += a.partial[(p.slot(s, tile, b) * p.rows + m) * 16 + r];
+            for (int64_t b = b0; b <= b1; ++b)
+                sum += a.partial[(p.slot(s, tile, b) * p.rows + m) * kTileRows + r];
         }
         if (crossed) store_y(a, m, v, sum);
     }
 }
 
-size_t matvec_fixed_smem(int nt) {
-    return (size_t)kWarpsMv * kStages * kUnitBytes + (size_t)kWarpsMv * 2 * (16 * 8 * nt * 4 + 8);
-}
-
-int parts_of(int64_t dtype) { return dtype == CK_F32 ? 3 : 1; }
-int rows_at_once(int64_t dtype) { return kMostCols / parts_of(dtype); }
-int column_tiles(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
+// Rows of x in one launch: what two tensor-core tiles of eight columns hold.
+int rows_at_once(int64_t dtype) { return dtype == CK_F32 ? 4 : 16; }
 
 MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms) {
     MatvecPlan p{};
     p.rows = (int)rows;
-    p.parts = parts_of(dtype);
-    p.cols = (int)rows * p.parts;
-    p.tiles = (V + 15) / 16;
+    p.tiles = (V + kTileRows - 1) / kTileRows;
     p.chunks = (K + kChunk - 1) / kChunk;
-    const size_t fixed = matvec_fixed_smem(column_tiles(p.cols));
-    const int64_t most = ((int64_t)(kSmemMost - fixed) / p.cols - 64) / (2 * kChunk);
+    // the columns in use lie below x_cols; the two spare ones of a tile take no memory
+    p.x_cols = dtype == CK_F32 ? (int)(8 * ((rows - 1) / 2) + 6) : (int)rows;
+    const size_t fixed = (size_t)kWarpsMv * (kStages * kUnitBytes + kTileRows * (4 * rows + 40) + 8);
+    const int64_t most = ((int64_t)(kSmemMost - fixed) / p.x_cols - 64) / (2 * kChunk);
     p.slabs = (p.chunks + most - 1) / most;
     p.slab = (p.chunks + p.slabs - 1) / p.slabs;
     p.slabs = (p.chunks + p.slab - 1) / p.slab;
@@ -567,12 +597,12 @@ MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sm
     p.ctas = (int)(p.aligned ? by_tile : even < 1 ? 1 : even < sms ? even : sms);
     // 64 bytes past a multiple of 128: two columns side by side fill all banks
     p.x_pitch = (int)p.slab * 2 * kChunk + 64;
-    p.smem = fixed + (size_t)p.cols * p.x_pitch;
+    p.smem = fixed + (size_t)p.x_cols * p.x_pitch;
     return p;
 }
 
 size_t partial_bytes(const MatvecPlan &p) {
-    return p.aligned ? 0 : (size_t)(p.slabs * p.tiles + p.ctas) * 16 * p.rows * sizeof(float);
+    return p.aligned ? 0 : (size_t)(p.slabs * p.tiles + p.ctas) * kTileRows * p.rows * sizeof(float);
 }
 
 template <bool HALF, int GROUP, int NT>
@@ -584,7 +614,7 @@ cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t
     e = cudaGetLastError();
     if (e != cudaSuccess || p.aligned) return e;
     cudaLaunchConfig_t cfg{};
-    const int64_t want = (p.tiles * 16 * p.rows + 127) / 128;
+    const int64_t want = (p.tiles * kTileRows * p.rows + 127) / 128;
     cfg.gridDim = dim3((unsigned)(want < 1024 ? want : 1024));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
@@ -598,11 +628,7 @@ cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t
 
 template <bool HALF, int GROUP>
 cudaError_t launch_columns(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
-    switch (column_tiles(p.cols)) {
-        case 1: return launch_matvec<HALF, GROUP, 1>(a, p, stream);
-        case 2: return launch_matvec<HALF, GROUP, 2>(a, p, stream);
-        default: return launch_matvec<HALF, GROUP, 4>(a, p, stream);
-    }
+    return p.x_cols <= 8 ? launch_matvec<HALF, GROUP, 1>(a, p, stream) : launch_matvec<HALF, GROUP, 2>(a, p, stream);
 }
 
 template <int GROUP> cudaError_t launch_group(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
