@@ -35,16 +35,17 @@ struct MatvecArgs {
 // copies that each warp keeps for itself, and no warp waits for another until
 // the end.
 //
-// A unit is 32 weight rows by 128 columns (2 KB).  K is cut into slabs whose x
+// A unit is 32 weight rows by 256 columns (4 KB).  K is cut into slabs whose x
 // fits in shared memory; the units, in the order (slab, 32-row tile, chunk),
 // are dealt to CTAs, and a CTA's to its warps, in equal runs.  A run's first and
 // last tile may be shared with its neighbours: those sums meet in shared memory
 // and, where a tile crosses CTAs or slabs, in the slots of `partial`, which
 // k_join adds up in a fixed order.
-constexpr int kWarpsMv = 16;                // warps of a CTA, one CTA on an SM
-constexpr int kStages = 4;                  // ring of units per warp
+constexpr int kWarpsMv = 12;                // warps of a CTA, one CTA on an SM
+constexpr int kStages = 3;                  // ring of units per warp
 constexpr int kTileRows = 32;
-constexpr int kChunk = 128;                 // columns of a unit
+constexpr int kChunk = 256;                 // columns of a unit
+constexpr int kHalf = 128;                  // scales are taken up for half a unit
 constexpr int kUnitBytes = kTileRows * kChunk / 2;
 constexpr size_t kSmemMost = 232448;
 
@@ -56,25 +57,23 @@ struct MatvecPlan {
     int64_t slabs;
     int ctas;
     int aligned;       // CTAs take whole tiles: nothing crosses them
+    int64_t run, more; // CTAs take `run` grains, the first `more` of them one more
+    int64_t grain;     // units of a grain: a tile's where aligned, else one
     int x_pitch;       // bytes between columns of x in shared memory
     int x_cols;        // tensor-core columns that x takes
     size_t smem;
 
     __host__ __device__ int64_t units() const { return tiles * chunks; }
     // first unit of CTA b
-    __host__ __device__ int64_t cut(int64_t b) const {
-        return aligned ? tiles * b / ctas * chunks : units() * b / ctas;
-    }
+    __host__ __device__ int64_t cut(int64_t b) const { return grain * (b * run + (b < more ? b : more)); }
     __host__ __device__ int64_t slab_chunks(int64_t s) const {
         return s + 1 < slabs ? slab : chunks - (slabs - 1) * slab;
     }
     __host__ __device__ int64_t slab_first(int64_t s) const { return s * slab * tiles; }
     // the CTA whose run holds unit u
     __host__ __device__ int64_t cta_of(int64_t u) const {
-        int64_t b = u * ctas / units();
-        while (b + 1 < ctas && cut(b + 1) <= u) ++b;
-        while (b > 0 && cut(b) > u) --b;
-        return b;
+        const int64_t g = u / grain, big = more * (run + 1);
+        return g < big ? g / (run + 1) : more + (g - big) / run;
     }
     // slot of CTA b's part of a tile in a slab: no two parts share one, as from
     // a part to the next the tile or the CTA moves on and neither goes back
@@ -103,46 +102,35 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// q - z of a word's eight nibbles, as pairs (0, 4), (1, 5), (2, 6), (3, 7).  Put
-// below the exponent of 2^7 (bf16) or 2^10 (fp16), a nibble q is the number 128 + q
-// or 1024 + q, and subtracting 128 + z or 1024 + z is exact.  In fp16 the next
-// nibble is read where it is, as 1024 + 16 q: a product with 1/16 saves its shift.
-template <bool HALF> struct Zero;
-template <> struct Zero<false> {
-    uint32_t even;
-    // of byte i of four packed zero points
-    __device__ __forceinline__ void set(uint32_t packed, int i) {
-        even = __byte_perm(packed, 0x43u, 0x4040u | i | i << 8);
+// q - z of a word's eight nibbles, as pairs (0, 4), (1, 5), (2, 6), (3, 7), times
+// 2^-6 (bf16) or 2^-9 (fp16).  Alone in the low bits of a bf16 a nibble is the
+// number q 2^-133, in the next place 16 q 2^-133 (fp16: 2^-24), exactly: so an AND
+// and a multiply-add, whose factor evens out the places, give the exact difference,
+// and of the four pairs two cost a shift.
+template <bool HALF> struct Nibble {
+    static constexpr uint32_t kLow = HALF ? 0x78007800u : 0x7f007f00u;   // 2^15, 2^127
+    static constexpr uint32_t kHigh = HALF ? 0x68006800u : 0x7d007d00u;  // 2^11, 2^123
+    static constexpr float kBack = HALF ? 512.f : 64.f;
+    static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        if constexpr (HALF)
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        else
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+    // -z, likewise, of byte i of four packed zero points
+    static __device__ __forceinline__ uint32_t minus(uint32_t packed, int i) {
+        return fma(__byte_perm(packed, 0u, 0x4040u | i | i << 8), kLow ^ 0x80008000u, 0u);
+    }
+    static __device__ __forceinline__ void pairs(uint32_t w, uint32_t z, uint32_t (&v)[4]) {
+        const uint32_t w8 = w >> 8;
+        v[0] = fma(w & 0x000f000fu, kLow, z);
+        v[1] = fma(w & 0x00f000f0u, kHigh, z);
+        v[2] = fma(w8 & 0x000f000fu, kLow, z);
+        v[3] = fma(w8 & 0x00f000f0u, kHigh, z);
     }
 };
-template <> struct Zero<true> {
-    uint32_t even, odd;  // 1024 + z and -(64 + z), twice
-    __device__ __forceinline__ void set(uint32_t packed, int i) {
-        even = __byte_perm(packed, 0x64u, 0x4040u | i | i << 8);
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(odd) : "r"(even), "r"(0xbc00bc00u), "r"(0x63806380u));
-    }
-};
-// (w & mask) | base in one instruction
-__device__ __forceinline__ uint32_t put_under(uint32_t w, uint32_t mask, uint32_t base) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(base));
-    return r;
-}
-template <bool HALF>
-__device__ __forceinline__ void nibbles(uint32_t w, const Zero<HALF> &z, uint32_t (&v)[4]) {
-    if constexpr (HALF) {
-        const uint32_t w8 = w >> 8, lo = 0x000f000fu, hi = 0x00f000f0u, base = 0x64006400u;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[0]) : "r"(put_under(w, lo, base)), "r"(z.even));
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[1]) : "r"(put_under(w, hi, base)), "r"(0x2c002c00u), "r"(z.odd));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[2]) : "r"(put_under(w8, lo, base)), "r"(z.even));
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[3]) : "r"(put_under(w8, hi, base)), "r"(0x2c002c00u), "r"(z.odd));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            asm("sub.rn.bf16x2 %0, %1, %2;"
-                : "=r"(v[j]) : "r"(put_under(w >> (4 * j), 0x000f000fu, 0x43004300u)), "r"(z.even));
-    }
-}
 
 // Three bf16 parts of a 32-bit float: each takes the top eight bits of what is
 // left.  Cutting keeps the first part of a large number finite; what is not finite
@@ -230,38 +218,40 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, const MatvecPlan &p
 }
 
 // What a warp copies next: its lanes' place in the weights, moved on by a chunk
-// at a time.  A unit is four 16-byte pieces of 32 lines of 64 bytes; the pieces
-// of line r lie exchanged by r / 2, so that a piece of eight lines is read without
-// a conflict.
+// at a time.  A unit is eight 16-byte pieces of 32 lines of 128 bytes; the pieces
+// of line r lie exchanged by r, so that a piece of eight lines is read without a
+// conflict.
 struct Copier {
-    const uint8_t *src;     // the lane's piece in line lane / 4
+    const uint8_t *src;     // the lane's piece in line lane / 8
     int tile, chunk;
     __device__ __forceinline__ void seek(const MatvecArgs &a, int tile_, int chunk_) {
         const int lane = threadIdx.x & 31;
         tile = tile_;
         chunk = chunk_;
-        src = a.q + (int64_t)(tile * kTileRows + (lane >> 2)) * a.q_pitch + chunk * (kChunk / 2) + (lane & 3) * 16;
+        src = a.q + (int64_t)(tile * kTileRows + (lane >> 3)) * a.q_pitch + chunk * (kChunk / 2) + (lane & 7) * 16;
     }
     __device__ __forceinline__ void copy(const MatvecArgs &a, uint32_t dst) const {
         const int lane = threadIdx.x & 31;
-        const uint32_t at = dst + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3)) << 4);
+        // lines 4 i + lane / 8: their low three bits are lane / 8, and 4 for odd i
+        const uint32_t at = dst + (lane >> 3) * 128, p0 = ((lane & 7) ^ (lane >> 3)) << 4, p1 = p0 ^ 64;
         if ((tile + 1) * kTileRows <= (int)a.V && (chunk + 1) * kChunk <= (int)a.K) {
             const uint8_t *s = src;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(at + i * 512), "l"(s));
-                s += 8 * a.q_pitch;
+            for (int i = 0; i < 8; ++i) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + (i & 1 ? p1 : p0) + i * 512),
+                             "l"(s));
+                s += 4 * a.q_pitch;
             }
             return;
         }
         // bytes past a row's end and rows past V become zeros
-        const int from = chunk * (kChunk / 2) + (lane & 3) * 16, row_bytes = (int)((a.K + 1) / 2);
+        const int from = chunk * (kChunk / 2) + (lane & 7) * 16, row_bytes = (int)((a.K + 1) / 2);
         const int n = row_bytes - from >= 16 ? 16 : row_bytes > from ? row_bytes - from : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = tile * kTileRows + 8 * i + (lane >> 2) < (int)a.V ? n : 0;
-            const uint8_t *s = m ? src + 8 * i * a.q_pitch : a.q;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + i * 512), "l"(s), "r"(m));
+        for (int i = 0; i < 8; ++i) {
+            const int m = tile * kTileRows + 4 * i + (lane >> 3) < (int)a.V ? n : 0;
+            const uint8_t *s = m ? src + 4 * i * a.q_pitch : a.q;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + (i & 1 ? p1 : p0) + i * 512),
+                         "l"(s), "r"(m));
         }
     }
     __device__ __forceinline__ void next(const MatvecArgs &a, int first, int end) {
@@ -331,7 +321,7 @@ __device__ __forceinline__ void store_y(const MatvecArgs &a, int64_t m, int64_t 
 template <bool HALF, int GROUP, int NT>
 __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, MatvecPlan p) {
     extern __shared__ __align__(1024) char smem[];
-    constexpr int kGroups = kChunk / GROUP;
+    constexpr int kGroups = kHalf / GROUP;  // of half a unit
     // per warp: its ring, in which its last part of a sum is left when it is done; its
     // first part; scales and zero points of the eight groups at hand
     const int part_floats = kTileRows * p.rows;
@@ -343,7 +333,7 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = lane >> 2, quad = lane & 3;
     const uint32_t my_ring = smem_at(smem) + warp * kStages * kUnitBytes;
-    const uint32_t my_line = lane * 64, my_swap = (lane >> 1 & 3) << 4;
+    const uint32_t my_line = lane * 128, my_swap = (lane & 7) << 4;
     float *my_scales = all_scales + warp * kTileRows * 8;
     uint8_t *my_zeros = all_zeros + warp * kTileRows * 8;
     auto part_at = [&](int w, int k) {
@@ -367,10 +357,11 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
         const int64_t u0 = cta0 > base ? cta0 : base;
         const int64_t u1 = cta1 < base + sc * p.tiles ? cta1 : base + sc * p.tiles;
         if (u0 >= u1) continue;
-        const int64_t w0 = u0 + (u1 - u0) * warp / kWarpsMv, w1 = u0 + (u1 - u0) * (warp + 1) / kWarpsMv;
         const int first = (int)(s * p.slab);  // the slab's first chunk
-        int n = (int)(w1 - w0), left = n;
-        int t = (int)((w0 - base) / sc), c = (int)((w0 - base) % sc);
+        const int span = (int)(u1 - u0), skip = (int)((u0 - base) % sc);
+        const int w0 = (int)((int64_t)span * warp / kWarpsMv), w1 = (int)((int64_t)span * (warp + 1) / kWarpsMv);
+        int n = w1 - w0, left = n;
+        int t = (int)((u0 - base) / sc) + (skip + w0) / sc, c = (skip + w0) % sc;
         __syncthreads();  // the last slab's x and parts of sums are done with
         Copier from;
         from.seek(a, t, first + c);
@@ -411,68 +402,71 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
                 next.load(a, t1, e1, groups);  // past the last tile: nothing
                 __syncwarp();
             }
-            const int in_eight = (first + c) % kUnits;
+            const int in_eight = (first + c) & (kUnits - 1);
             begin = whole || in_eight == kUnits - 1;
-            float scale[4][kGroups];  // of rows row + 8 h
-            uint32_t zeros[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const int at = (row + 8 * h) * 8 + in_eight * kGroups;
-                if constexpr (kGroups == 4) {
-                    *(float4 *)scale[h] = *(const float4 *)(my_scales + at);
-                    zeros[h] = *(const uint32_t *)(my_zeros + at);
-                } else if constexpr (kGroups == 2) {
-                    *(float2 *)scale[h] = *(const float2 *)(my_scales + at);
-                    zeros[h] = *(const uint16_t *)(my_zeros + at);
-                } else {
-                    scale[h][0] = my_scales[at];
-                    zeros[h] = my_zeros[at];
-                }
-            }
             const uint32_t lines = get + my_line;
             get = get + kUnitBytes == my_ring + kStages * kUnitBytes ? my_ring : get + kUnitBytes;
             const char *xc = xs + c * (2 * kChunk);
-            float part[NT][2][4];
-            Zero<HALF> zero[4];
 #pragma unroll
-            for (int blk = 0; blk < kChunk / 32; ++blk) {  // 32 columns: a piece of each line
-                constexpr int kBlocks = GROUP / 32;
-                const int g = blk / kBlocks;
-                uint32_t w[4];  // rows row + 8 h
-                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                             : "r"(lines + (my_swap ^ (blk << 4))));
-                uint32_t v[4][4];
+            for (int half = 0; half < kChunk / kHalf; ++half) {
+                float scale[4][kGroups];  // of rows row + 8 h
+                uint32_t zeros[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    if (blk % kBlocks == 0) zero[h].set(zeros[h], g);
-                    nibbles<HALF>(w[h], zero[h], v[h]);
-                }
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const uint4 b = *(const uint4 *)(xc + x_at[j] + blk * 64);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t(&lo)[4] = v[2 * i], (&hi)[4] = v[2 * i + 1];
-                        if (blk % kBlocks == 0)
-                            mma<HALF, true>(part[j][i], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-                        else
-                            mma<HALF, false>(part[j][i], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t(&lo)[4] = v[2 * i], (&hi)[4] = v[2 * i + 1];
-                        mma<HALF, false>(part[j][i], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+                    const int at = (row + 8 * h) * 8 + (2 * in_eight + half) * kGroups;
+                    if constexpr (kGroups == 4) {
+                        *(float4 *)scale[h] = *(const float4 *)(my_scales + at);
+                        zeros[h] = *(const uint32_t *)(my_zeros + at);
+                    } else if constexpr (kGroups == 2) {
+                        *(float2 *)scale[h] = *(const float2 *)(my_scales + at);
+                        zeros[h] = *(const uint16_t *)(my_zeros + at);
+                    } else {
+                        scale[h][0] = my_scales[at];
+                        zeros[h] = my_zeros[at];
                     }
                 }
-                if (blk % kBlocks == kBlocks - 1) {
+                float part[NT][2][4];
+                uint32_t zero[4];
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                for (int blk = 0; blk < kHalf / 32; ++blk) {  // 32 columns: a piece of each line
+                    constexpr int kBlocks = GROUP / 32;
+                    const int g = blk / kBlocks, piece = 4 * half + blk;
+                    uint32_t w[4];  // rows row + 8 h
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(lines + (my_swap ^ (piece << 4))));
+                    uint32_t v[4][4];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
+                    for (int h = 0; h < 4; ++h) {
+                        if (blk % kBlocks == 0) zero[h] = Nibble<HALF>::minus(zeros[h], g);
+                        Nibble<HALF>::pairs(w[h], zero[h], v[h]);
+                    }
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[j][i][e] = fmaf(scale[2 * i + (e >> 1)][g], part[j][i][e], acc[j][i][e]);
+                    for (int j = 0; j < NT; ++j) {
+                        const uint4 b = *(const uint4 *)(xc + x_at[j] + piece * 64);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t(&lo)[4] = v[2 * i], (&hi)[4] = v[2 * i + 1];
+                            if (blk % kBlocks == 0)
+                                mma<HALF, true>(part[j][i], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+                            else
+                                mma<HALF, false>(part[j][i], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t(&lo)[4] = v[2 * i], (&hi)[4] = v[2 * i + 1];
+                            mma<HALF, false>(part[j][i], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+                        }
+                    }
+                    if (blk % kBlocks == kBlocks - 1) {
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    acc[j][i][e] = fmaf(scale[2 * i + (e >> 1)][g], part[j][i][e], acc[j][i][e]);
+                    }
                 }
             }
             if (whole || n == 1) {  // this tile's part ends here
@@ -503,7 +497,7 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
                             const int r = 16 * i + row + 8 * (e >> 1);
                             const int m = !HALF && a.dtype == CK_F32 ? (quad ? p.rows : 2 * j + (e & 1))
                                                                      : 8 * j + 2 * quad + (e & 1);
-                            const float sum = acc[j][i][e];
+                            const float sum = acc[j][i][e] * Nibble<HALF>::kBack;
                             acc[j][i][e] = 0.f;
                             if (m >= p.rows) continue;
                             const int64_t v = (int64_t)t * kTileRows + r;
@@ -521,23 +515,17 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
         }
         __syncthreads();
         // parts of one tile follow one another: the warp that holds the first adds them up
+        const int theirs = lane < 2 * kWarpsMv ? part_tile[lane] : -1;
         for (int k = 0; k < 2; ++k) {
-            const int at = 2 * warp + k, tile = part_tile[at];
-            if (tile < 0) continue;
-            bool head = true;
-            for (int i = at - 1; i >= 0; --i)
-                if (part_tile[i] >= 0) {
-                    head = part_tile[i] != tile;
-                    break;
-                }
-            if (!head) continue;
+            const int at = 2 * warp + k, tile = __shfl_sync(~0u, theirs, at);
+            const uint32_t same = __ballot_sync(~0u, theirs == tile);
+            if (tile < 0 || __ffs(same) - 1 != at) continue;
             const int64_t tu = base + (int64_t)tile * sc;
             const bool alone = p.slabs == 1 && tu >= u0 && tu + sc <= u1;
             for (int m = 0; m < p.rows; ++m) {
                 float sum = 0.f;
-                for (int e = at; e < 2 * kWarpsMv; ++e) {
-                    if (part_tile[e] < 0) continue;
-                    if (part_tile[e] != tile) break;
+                for (uint32_t rest = same; rest; rest &= rest - 1) {
+                    const int e = __ffs(rest) - 1;
                     sum += part_at(e >> 1, e & 1)[m * kTileRows + lane];
                 }
                 const int64_t v = (int64_t)tile * kTileRows + lane;
@@ -588,13 +576,16 @@ MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sm
     p.slab = (p.chunks + p.slabs - 1) / p.slabs;
     p.slabs = (p.chunks + p.slab - 1) / p.slab;
     // Whole tiles to each CTA, and no second kernel, or equal runs with one: a
-    // unit takes an SM about 0.05 us, the second kernel about 2 us.
-    const double unit = 0.05;
+    // unit takes an SM about 0.1 us, the second kernel about 2 us.
+    const double unit = 0.1;
     const int64_t even = p.units() / kWarpsMv, by_tile = p.tiles < sms ? p.tiles : sms;
     const double whole = (double)((p.tiles + by_tile - 1) / by_tile) * p.chunks * unit;
     const double equal = (double)p.units() / sms * unit + 2.0;
     p.aligned = p.slabs == 1 && whole <= equal;
     p.ctas = (int)(p.aligned ? by_tile : even < 1 ? 1 : even < sms ? even : sms);
+    p.grain = p.aligned ? p.chunks : 1;
+    p.run = p.units() / p.grain / p.ctas;
+    p.more = p.units() / p.grain % p.ctas;
     // 64 bytes past a multiple of 128: two columns side by side fill all banks
     p.x_pitch = (int)p.slab * 2 * kChunk + 64;
     p.smem = fixed + (size_t)p.x_cols * p.x_pitch;
