@@ -296,6 +296,19 @@ template <int GROUP> struct ScaleReader {
             for (int i = 0; i < 8; ++i) z[i] = 4 * i < rows ? p[4 * i * a.z_stride] : 8u;
         }
     }
+    // A line of each row towards L2, a row to a lane, once for each 128 bytes: a load a
+    // unit ahead alone waits for memory.
+    static __device__ __forceinline__ void ahead(const MatvecArgs &a, int tile, int eight, int groups, bool start) {
+        const int v = tile * kTileRows + (threadIdx.x & 31), g = 8 * eight;
+        if (v >= (int)a.V || g >= groups) return;
+        const int size = a.scale_dtype == CK_F32 ? 4 : 2;
+        const char *p = (const char *)a.scales + (v * a.s_stride + g) * size;
+        if (start || ((uintptr_t)p & 127) < 8 * size) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+        if (a.zeros) {
+            const uint8_t *q = a.zeros + v * a.z_stride + g;
+            if (start || ((uintptr_t)q & 127) < 8) asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+        }
+    }
     __device__ __forceinline__ void leave(const MatvecArgs &a, float *scales, uint8_t *zeros) const {
         const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -377,7 +390,7 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
         };
         for (int i = 0; i < kStages - 1; ++i) copy_next();
         ScaleReader<GROUP> next;
-        constexpr int kUnits = ScaleReader<GROUP>::kUnits;
+        constexpr int kUnits = ScaleReader<GROUP>::kUnits, kAhead = 4;
         if (n > 0) next.load(a, t, (first + c) / kUnits, groups);
         bool begin = true;  // the next unit is the first of its eight groups here
         if (lane < 2) part_tile[2 * warp + lane] = -1;
@@ -400,6 +413,9 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
                 int t1 = t, e1 = next.eight + 1;
                 if (e1 * kUnits >= first + sc) ++t1, e1 = first / kUnits;
                 next.load(a, t1, e1, groups);  // past the last tile: nothing
+                int t2 = t1, e2 = e1 + kAhead;
+                if (e2 * kUnits >= first + sc) ++t2, e2 += first / kUnits - (first + sc + kUnits - 1) / kUnits;
+                ScaleReader<GROUP>::ahead(a, t2, e2, groups, e2 == first / kUnits);
                 __syncwarp();
             }
             const int in_eight = (first + c) & (kUnits - 1);
