@@ -49,36 +49,47 @@ constexpr int kHalf = 128;                  // scales are taken up for half a un
 constexpr int kUnitBytes = kTileRows * kChunk / 2;
 constexpr size_t kSmemMost = 232448;
 
+// a / b, in 32 bits where that does: a 64-bit division costs ten times as much
+__host__ __device__ inline int64_t quotient(int64_t a, int64_t b) {
+    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// n things dealt to `to` owners in runs that differ by one at most
+struct Deal {
+    int64_t each, more;
+    static __host__ __device__ Deal of(int64_t n, int64_t to) {
+        const int64_t q = quotient(n, to);
+        return Deal{q, n - q * to};
+    }
+    __host__ __device__ int64_t first(int64_t owner) const { return owner * each + (owner < more ? owner : more); }
+    __host__ __device__ int64_t owner(int64_t i) const {
+        const int64_t big = more * (each + 1);
+        return i < big ? quotient(i, each + 1) : more + quotient(i - big, each);
+    }
+};
+
 struct MatvecPlan {
     int rows;          // rows of x in this launch
     int64_t tiles;     // 32-row tiles of V
     int64_t chunks;    // chunks of K
-    int64_t slab;      // chunks of a slab (the last may have fewer)
-    int64_t slabs;
-    int ctas;
-    int aligned;       // CTAs take whole tiles: nothing crosses them
-    int64_t run, more; // CTAs take `run` grains, the first `more` of them one more
-    int64_t grain;     // units of a grain: a tile's where aligned, else one
+    int64_t slabs;     // parts of K
+    int64_t ctas;
+    int aligned;       // one slab, and CTAs take whole tiles: nothing crosses them
+    Deal chunk;        // chunks to slabs
+    // Where there are no more slabs than CTAs, a CTA keeps to one slab, whose units
+    // are dealt to its CTAs in equal runs; else CTAs take whole slabs.
+    Deal cta;          // CTAs to slabs
+    Deal slab;         // slabs to CTAs
+    Deal tile;         // aligned: tiles to CTAs
     int x_pitch;       // bytes between columns of x in shared memory
     int x_cols;        // tensor-core columns that x takes
     size_t smem;
 
-    __host__ __device__ int64_t units() const { return tiles * chunks; }
-    // first unit of CTA b
-    __host__ __device__ int64_t cut(int64_t b) const { return grain * (b * run + (b < more ? b : more)); }
-    __host__ __device__ int64_t slab_chunks(int64_t s) const {
-        return s + 1 < slabs ? slab : chunks - (slabs - 1) * slab;
-    }
-    __host__ __device__ int64_t slab_first(int64_t s) const { return s * slab * tiles; }
-    // the CTA whose run holds unit u
-    __host__ __device__ int64_t cta_of(int64_t u) const {
-        const int64_t g = u / grain, big = more * (run + 1);
-        return g < big ? g / (run + 1) : more + (g - big) / run;
-    }
+    __host__ __device__ bool shared_slabs() const { return slabs <= ctas; }
     // slot of CTA b's part of a tile in a slab: no two parts share one, as from
     // a part to the next the tile or the CTA moves on and neither goes back
-    __host__ __device__ int64_t slot(int64_t s, int64_t tile, int64_t b) const {
-        return s * tiles + tile + b;
+    __host__ __device__ int64_t slot(int64_t s, int64_t t, int64_t b) const {
+        return s * tiles + t + (shared_slabs() ? b : 0);
     }
 };
 
@@ -362,19 +373,25 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
         x_at[j] = min(col, p.x_cols - 1) * p.x_pitch + quad * 16;
     }
     const int groups = (int)((a.K + GROUP - 1) / GROUP);
-    const int64_t cta0 = p.cut(blockIdx.x), cta1 = p.cut(blockIdx.x + 1);
     asm volatile("griddepcontrol.launch_dependents;");
-    for (int64_t s = 0; s < p.slabs; ++s) {
-        const int sc = (int)p.slab_chunks(s);
-        const int64_t base = p.slab_first(s);
-        const int64_t u0 = cta0 > base ? cta0 : base;
-        const int64_t u1 = cta1 < base + sc * p.tiles ? cta1 : base + sc * p.tiles;
-        if (u0 >= u1) continue;
-        const int first = (int)(s * p.slab);  // the slab's first chunk
-        const int span = (int)(u1 - u0), skip = (int)((u0 - base) % sc);
+    const bool one = p.shared_slabs();
+    const int64_t s0 = one ? p.cta.owner(blockIdx.x) : p.slab.first(blockIdx.x);
+    const int64_t s1 = one ? s0 + 1 : p.slab.first(blockIdx.x + 1);
+    for (int64_t s = s0; s < s1; ++s) {
+        const int first = (int)p.chunk.first(s), sc = (int)p.chunk.first(s + 1) - first;  // the slab's chunks
+        int64_t u0 = 0, u1 = sc * p.tiles;  // units of the slab
+        if (p.aligned) {
+            u0 = p.tile.first(blockIdx.x) * sc, u1 = p.tile.first(blockIdx.x + 1) * sc;
+        } else if (one) {
+            const int64_t b0 = p.cta.first(s);
+            const Deal unit = Deal::of(u1, p.cta.first(s + 1) - b0);
+            u0 = unit.first(blockIdx.x - b0), u1 = unit.first(blockIdx.x - b0 + 1);
+        }
+        const int tile0 = (int)quotient(u0, sc), skip = (int)(u0 - (int64_t)tile0 * sc);
+        const int span = (int)(u1 - u0);
         const int w0 = (int)((int64_t)span * warp / kWarpsMv), w1 = (int)((int64_t)span * (warp + 1) / kWarpsMv);
         int n = w1 - w0, left = n;
-        int t = (int)((u0 - base) / sc) + (skip + w0) / sc, c = (skip + w0) % sc;
+        int t = tile0 + (skip + w0) / sc, c = (skip + w0) % sc;
         __syncthreads();  // the last slab's x and parts of sums are done with
         Copier from;
         from.seek(a, t, first + c);
@@ -536,7 +553,7 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
             const int at = 2 * warp + k, tile = __shfl_sync(~0u, theirs, at);
             const uint32_t same = __ballot_sync(~0u, theirs == tile);
             if (tile < 0 || __ffs(same) - 1 != at) continue;
-            const int64_t tu = base + (int64_t)tile * sc;
+            const int64_t tu = (int64_t)tile * sc;
             const bool alone = p.slabs == 1 && tu >= u0 && tu + sc <= u1;
             for (int m = 0; m < p.rows; ++m) {
                 float sum = 0.f;
@@ -554,26 +571,61 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
     }
 }
 
-// Sums that cross CTAs or slabs, in the order of K.
+// Sums that cross CTAs or slabs, in the order of K: a warp for a tile and a row of
+// x, a lane for a row of V.  Its lanes first find the CTAs of a slab each.  Every
+// thread waits for the product before it ends: what follows in the stream waits for
+// this kernel alone.
 __global__ void __launch_bounds__(128) k_join(MatvecArgs a, MatvecPlan p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.tiles * kTileRows * p.rows;
-         i += (int64_t)gridDim.x * blockDim.x) {
-        const int r = (int)(i % kTileRows);
-        const int64_t tile = i / kTileRows % p.tiles, m = i / kTileRows / p.tiles, v = tile * kTileRows + r;
-        if (v >= a.V) continue;
-        float sum = 0.f;
-        bool crossed = p.slabs > 1;
-        for (int64_t s = 0; s < p.slabs; ++s) {
-            const int64_t u = p.slab_first(s) + tile * p.slab_chunks(s), e = u + p.slab_chunks(s);
-            const int64_t b0 = p.cta_of(u), b1 = p.cta_of(e - 1);
-            crossed |= b0 != b1;
-            if (!crossed) break;
-            for (int64_t b = b0; b <= b1; ++b)
-                sum += a.partial[(p.slot(s, tile, b) * p.rows + m) * kTileRows + r];
-        }
-        if (crossed) store_y(a, m, v, sum);
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+    if (item >= p.tiles * p.rows) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
     }
+    const int64_t m = quotient(item, p.tiles), tile = item - m * p.tiles, v = tile * kTileRows + lane;
+    float sum = 0.f;
+    bool crossed = p.slabs > 1;
+    for (int64_t s0 = 0; s0 < p.slabs; s0 += 32) {
+        int64_t at = 0;
+        int parts = 1;
+        const int64_t s = s0 + lane;
+        if (s < p.slabs) {
+            int64_t b0 = 0;
+            if (p.shared_slabs()) {
+                const int64_t sc = p.chunk.first(s + 1) - p.chunk.first(s), c0 = p.cta.first(s);
+                const Deal unit = Deal::of(sc * p.tiles, p.cta.first(s + 1) - c0);
+                const int64_t i0 = unit.owner(tile * sc), i1 = unit.owner(tile * sc + sc - 1);
+                b0 = c0 + i0;
+                parts = (int)(i1 - i0) + 1;
+            }
+            at = (p.slot(s, tile, b0) * p.rows + m) * kTileRows;
+        }
+        crossed |= __any_sync(~0u, parts > 1);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (!crossed) return;
+        const int n = p.slabs - s0 < 32 ? (int)(p.slabs - s0) : 32;
+        for (int i = 0; i < n; i += 4) {
+            // the first two parts of four slabs at once: waits for memory add up
+            float got[4][2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t from = __shfl_sync(~0u, at, (i + k) & 31);
+                const int np = __shfl_sync(~0u, parts, (i + k) & 31);
+                got[k][0] = i + k < n ? a.partial[from + lane] : 0.f;
+                got[k][1] = i + k < n && np > 1 ? a.partial[from + p.rows * kTileRows + lane] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                sum += got[k][0];
+                sum += got[k][1];
+                const int64_t from = __shfl_sync(~0u, at, (i + k) & 31);
+                const int np = __shfl_sync(~0u, parts, (i + k) & 31);
+                if (i + k < n)
+                    for (int q = 2; q < np; ++q) sum += a.partial[from + (int64_t)q * p.rows * kTileRows + lane];
+            }
+        }
+    }
+    if (v < a.V) store_y(a, m, v, sum);
 }
 
 // Rows of x in one launch: what two tensor-core tiles of eight columns hold.
@@ -589,21 +641,27 @@ MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sm
     const size_t fixed = (size_t)kWarpsMv * (kStages * kUnitBytes + kTileRows * (4 * rows + 40) + 8);
     const int64_t most = ((int64_t)(kSmemMost - fixed) / p.x_cols - 64) / (2 * kChunk);
     p.slabs = (p.chunks + most - 1) / most;
-    p.slab = (p.chunks + p.slabs - 1) / p.slabs;
-    p.slabs = (p.chunks + p.slab - 1) / p.slab;
+    const int64_t units = p.tiles * p.chunks, by_tile = p.tiles < sms ? p.tiles : sms;
     // Whole tiles to each CTA, and no second kernel, or equal runs with one: a
     // unit takes an SM about 0.1 us, the second kernel about 2 us.
     const double unit = 0.1;
-    const int64_t even = p.units() / kWarpsMv, by_tile = p.tiles < sms ? p.tiles : sms;
     const double whole = (double)((p.tiles + by_tile - 1) / by_tile) * p.chunks * unit;
-    const double equal = (double)p.units() / sms * unit + 2.0;
+    const double equal = (double)units / sms * unit + 2.0;
     p.aligned = p.slabs == 1 && whole <= equal;
-    p.ctas = (int)(p.aligned ? by_tile : even < 1 ? 1 : even < sms ? even : sms);
-    p.grain = p.aligned ? p.chunks : 1;
-    p.run = p.units() / p.grain / p.ctas;
-    p.more = p.units() / p.grain % p.ctas;
+    const int64_t even = units / kWarpsMv;  // a unit for each warp at least
+    p.ctas = p.aligned ? by_tile : even < 1 ? 1 : even < sms ? even : sms;
+    // as many CTAs to every slab, or slabs to every CTA, by taking more of them
+    if (p.slabs > 1) {
+        const int64_t want = p.slabs <= p.ctas ? p.ctas / (p.ctas / p.slabs) : (p.slabs + p.ctas - 1) / p.ctas * p.ctas;
+        p.slabs = want < p.chunks ? want : p.chunks;
+    }
+    p.chunk = Deal::of(p.chunks, p.slabs);
+    p.cta = Deal::of(p.ctas, p.slabs);
+    p.slab = Deal::of(p.slabs, p.ctas);
+    p.tile = Deal::of(p.tiles, p.ctas);
+    const int64_t slab = (p.chunks + p.slabs - 1) / p.slabs;
     // 64 bytes past a multiple of 128: two columns side by side fill all banks
-    p.x_pitch = (int)p.slab * 2 * kChunk + 64;
+    p.x_pitch = (int)slab * 2 * kChunk + 64;
     p.smem = fixed + (size_t)p.x_cols * p.x_pitch;
     return p;
 }
@@ -617,12 +675,11 @@ cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t
     cudaError_t e = cudaFuncSetAttribute(k_matvec<HALF, GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemMost);
     if (e != cudaSuccess) return e;
-    k_matvec<HALF, GROUP, NT><<<p.ctas, kWarpsMv * 32, p.smem, stream>>>(a, p);
+    k_matvec<HALF, GROUP, NT><<<(unsigned)p.ctas, kWarpsMv * 32, p.smem, stream>>>(a, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.aligned) return e;
     cudaLaunchConfig_t cfg{};
-    const int64_t want = (p.tiles * kTileRows * p.rows + 127) / 128;
-    cfg.gridDim = dim3((unsigned)(want < 1024 ? want : 1024));
+    cfg.gridDim = dim3((unsigned)((p.tiles * p.rows + 3) / 4));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
