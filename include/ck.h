@@ -341,7 +341,7 @@ typedef enum { CK_F32 = 0, CK_BF16 = 1, CK_F16 = 2 } ck_dtype;
  * gradient is the same call on the output's gradient with the same p, seed,
  * step and shape.  y may be x where their strides agree.
  * Asynchronous.  Errors: CK_ERR_INVALID_ARG (dtype, p outside [0, 1], negative
- * size, NULL pointer), CK_ERR_UNSUPPORTED (2^59 elements), CK_ERR_CUDA.
+ * size, NULL pointer), CK_ERR_UNSUPPORTED (more than 2^40 elements), CK_ERR_CUDA.
  */
 ck_status ck_dropout(const void *x, void *y, int64_t dtype, int64_t n0, int64_t n1, int64_t n2,
                      int64_t x0, int64_t x1, int64_t x2, int64_t y0, int64_t y1, int64_t y2,

@@ -2,6 +2,7 @@
 // never stored.  The backward is the same call on the gradient: the element's
 // index gives its word again.
 #include <cmath>
+#include <cstring>
 
 #include "ck_philox.h"
 #include "ck_types.h"
@@ -48,6 +49,231 @@ __global__ void __launch_bounds__(256) k_dropout(DropArgs a) {
     }
 }
 
+
+// Where x's innermost axis is dense and y is dense and aligned, a thread takes 16
+// bytes of y: E elements whose words are those of E / 4 of the generator's blocks,
+// as y is dense in the order of the mask.  What bounds it is memory, 2 bytes
+// read and written twice over for each 16-bit element, with the generator close behind:
+// a block is twenty 32 x 32 -> 64 bit products for four elements.
+constexpr int kDropThreads = 256;
+
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
+
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", PLDI 1994).
+struct Divider {
+    uint32_t d, mul, shift;
+    static Divider of(uint32_t d) {
+        uint32_t s = 0;
+        while (((uint64_t)1 << s) < d) ++s;
+        return Divider{d, (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1), s};
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
+        return (__umulhi(n, mul) + n) >> shift;
+    }
+};
+
+struct DropFlat {
+    DropArgs a;
+    int64_t n;             // elements of y
+    int64_t period;        // locked: elements of the mask, else n
+    Divider row, plane;    // n3 and n2 (for n < 2^31)
+    int small;             // n < 2^31
+    int rows_joined;       // rows n3 apart: x is one dense line
+};
+
+// Elements e .. e + E - 1 of a dense line at p + e (element e itself there), of which
+// `room` are there, whatever p's alignment: from the two aligned 16-byte pieces that
+// hold them, where both lie inside the line, else one by one.
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const T *line, int64_t e, int64_t length) {
+    constexpr int E = kVec<T>;
+    const T *p = line + e;
+    const uint32_t off = (uint32_t)(uintptr_t)p & 15u;
+    if (off == 0) return __ldcs((const uint4 *)p);
+    const uint4 *lo = (const uint4 *)((uintptr_t)p - off);
+    if ((const char *)lo >= (const char *)line && (const char *)(lo + 2) <= (const char *)(line + length)) {
+        const uint4 u = __ldg(lo), v = __ldg(lo + 1);
+        uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        if (off & 8) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = w[7];
+        if (off & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t bits = (off & 2) * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    alignas(16) T t[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) t[i] = p[i];
+    return *(const uint4 *)t;
+}
+
+template <typename T> __device__ __forceinline__ uint4 select_scale(uint4 v, uint32_t keep, float scale) {
+    constexpr int E = kVec<T>;
+    alignas(16) T t[E];
+    memcpy(t, &v, 16);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const float f = to_float(t[i]) * scale;
+        t[i] = from_float<T>(keep >> i & 1 ? f : 0.f);
+    }
+    memcpy(&v, t, 16);
+    return v;
+}
+
+// Keep bits of elements m .. m + E - 1 of the mask.
+template <typename T, bool SHIFTED>
+__device__ __forceinline__ uint32_t keep_bits(const DropArgs &a, const PhiloxKey &key, int64_t m) {
+    constexpr int E = kVec<T>, kBlocks = E / 4 + (SHIFTED ? 1 : 0);
+    uint32_t bits = 0;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+        const uint4 r = philox((uint64_t)(m >> 2) + b, key);
+        bits |= ((r.x >= a.threshold) | (r.y >= a.threshold) << 1 | (r.z >= a.threshold) << 2 |
+                 (r.w >= a.threshold) << 3) << (4 * b);
+    }
+    if (SHIFTED) bits >>= m & 3;
+    return a.drop_all ? 0u : bits;
+}
+
+// SHIFTED: a locked mask whose length is no multiple of four, so that a piece of y
+// begins anywhere in a block.
+template <typename T, bool SHIFTED>
+__global__ void __launch_bounds__(kDropThreads) k_dropout_flat(DropFlat f) {
+    constexpr int E = kVec<T>, kUnroll = 2;
+    const DropArgs &a = f.a;
+    const PhiloxKey key = philox_key(a.seed, a.step, a.step_dev);
+    const T *x = (const T *)a.x;
+    T *y = (T *)a.y;
+    const int64_t q0 = ((int64_t)blockIdx.x * kUnroll) * kDropThreads + threadIdx.x;
+    uint4 v[kUnroll];
+    bool whole[kUnroll];
+    int64_t at[kUnroll];  // the element of x that a piece begins with
+    int64_t left[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        const int64_t e = (q0 + i * kDropThreads) * E;
+        whole[i] = false;
+        if (e >= f.n) continue;
+        int64_t row, c, plane, r2;
+        if (f.rows_joined) {
+            whole[i] = e + E <= f.n;
+            if (whole[i]) v[i] = load_vec<T>(x, e, f.n);
+            continue;
+        }
+        if (f.small) {
+            row = f.row.quotient((uint32_t)e);
+            plane = f.plane.quotient((uint32_t)row);
+        } else {
+            row = e / a.n3;
+            plane = row / a.n2;
+        }
+        c = e - row * a.n3;
+        r2 = row - plane * a.n2;
+        // plane counts [repeat][n1], which have one stride where both are there (a.rep > 1: n1 = 1)
+        at[i] = plane * a.x1 + r2 * a.x2;
+        left[i] = a.n3 - c;
+        whole[i] = left[i] >= E;
+        if (whole[i]) v[i] = load_vec<T>(x + at[i], c, a.n3);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        const int64_t e = (q0 + i * kDropThreads) * E;
+        if (e >= f.n) continue;
+        int64_t m = e;
+        if (SHIFTED || a.rep > 1) m = e % f.period;
+        if (whole[i] && (!(SHIFTED || a.rep > 1) || m + E <= f.period)) {
+            const uint32_t keep = keep_bits<T, SHIFTED>(a, key, m);
+            __stcs((uint4 *)(y + e), select_scale<T>(v[i], keep, a.scale));
+            continue;
+        }
+        // a piece that crosses rows, repeats or the end
+        for (int64_t k = e; k < e + E && k < f.n; ++k) {
+            const int64_t mk = k % f.period, row = k / a.n3, c = k - row * a.n3, plane = row / a.n2;
+            const uint4 r = philox((uint64_t)(mk >> 2), key);
+            const uint32_t w = (mk & 2) ? (mk & 1 ? r.w : r.z) : (mk & 1 ? r.y : r.x);
+            const float t = to_float(x[plane * a.x1 + (row - plane * a.n2) * a.x2 + c]) * a.scale;
+            y[k] = from_float<T>(!a.drop_all && w >= a.threshold ? t : 0.f);
+        }
+    }
+}
+
+// One mask for `rep` dense lines of n elements, n a multiple of E: its bits are
+// made once and used for the lines of blockIdx.y's share.
+template <typename T> __global__ void __launch_bounds__(kDropThreads) k_dropout_lines(DropFlat f, int lines) {
+    constexpr int E = kVec<T>, kUnroll = 4;
+    const DropArgs &a = f.a;
+    const int64_t m = ((int64_t)blockIdx.x * kDropThreads + threadIdx.x) * E;
+    if (m >= f.period) return;
+    const uint32_t keep = keep_bits<T, false>(a, philox_key(a.seed, a.step, a.step_dev), m);
+    const int64_t k0 = (int64_t)blockIdx.y * lines, k1 = k0 + lines < a.rep ? k0 + lines : a.rep;
+    const T *x = (const T *)a.x + k0 * a.xr;
+    T *y = (T *)a.y + k0 * f.period + m;
+    for (int64_t k = k0; k < k1; k += kUnroll) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+            if (k + i < k1) v[i] = load_vec<T>(x + i * a.xr, m, f.period);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+            if (k + i < k1) __stcs((uint4 *)(y + i * f.period), select_scale<T>(v[i], keep, a.scale));
+        x += kUnroll * a.xr;
+        y += kUnroll * f.period;
+    }
+}
+
+template <typename T> void launch_dropout(const DropArgs &a, cudaStream_t stream) {
+    constexpr int E = kVec<T>;
+    const int sms = device_sms();
+    DropFlat f{};
+    f.a = a;
+    f.period = a.n1 * a.n2 * a.n3;
+    f.n = f.period * a.rep;
+    // y dense in the order of the mask and its repeats, and aligned; x's innermost axis dense
+    const bool y_dense = (a.n3 == 1 || a.y3 == 1) && (a.n2 == 1 || a.y2 == a.n3) &&
+                         (a.n1 == 1 || a.y1 == a.n2 * a.n3) && (a.rep == 1 || a.yr == f.period) &&
+                         ((uintptr_t)a.y & 15) == 0;
+    const bool x_line = a.n3 == 1 ? a.n2 * a.n1 * a.rep == 1 : a.x3 == 1;
+    if (!y_dense || !x_line) {
+        const int64_t want = (f.period / 4 + 255) / 256, most = 8 * (int64_t)sms;
+        k_dropout<T><<<(int)(want < 1 ? 1 : want < most ? want : most), 256, 0, stream>>>(a);
+        return;
+    }
+    const bool joined = (a.n2 == 1 || a.x2 == a.n3) && (a.n1 == 1 || a.x1 == a.n2 * a.n3);
+    if (a.rep > 1 && joined && f.period % E == 0) {
+        // a share of lines for each y of the grid: enough threads to fill the device twice
+        const int64_t across = (f.period / E + kDropThreads - 1) / kDropThreads;
+        int64_t shares = (16 * (int64_t)sms + across - 1) / across;
+        if (shares > (a.rep + 3) / 4) shares = (a.rep + 3) / 4;
+        if (shares > 65535) shares = 65535;
+        const int64_t lines = (a.rep + shares - 1) / shares;
+        const dim3 grid((unsigned)across, (unsigned)((a.rep + lines - 1) / lines));
+        if (across < ((int64_t)1 << 31) && lines < ((int64_t)1 << 31)) {
+            k_dropout_lines<T><<<grid, kDropThreads, 0, stream>>>(f, (int)lines);
+            return;
+        }
+    }
+    if (a.rep > 1) {
+        // the repeats as the outermost axis
+        f.a.n1 = a.rep;
+        f.a.x1 = a.xr;
+    }
+    f.small = f.n < ((int64_t)1 << 31);
+    f.rows_joined = joined && (a.rep == 1 || a.xr == f.period);
+    if (f.small) {
+        f.row = Divider::of((uint32_t)a.n3);
+        f.plane = Divider::of((uint32_t)a.n2);
+    }
+    const int64_t pieces = (f.n + E - 1) / E;
+    const unsigned grid = (unsigned)((pieces + 2 * kDropThreads - 1) / (2 * kDropThreads));
+    if (a.rep > 1 && f.period % 4 != 0)
+        k_dropout_flat<T, true><<<grid, kDropThreads, 0, stream>>>(f);
+    else
+        k_dropout_flat<T, false><<<grid, kDropThreads, 0, stream>>>(f);
+}
+
 }  // namespace
 }  // namespace ck
 
@@ -61,8 +287,9 @@ extern "C" ck_status ck_dropout(const void *x, void *y, int64_t dtype, int64_t n
     if (!(p >= 0.0 && p <= 1.0)) return fail(CK_ERR_INVALID_ARG, "dropout: p must be in [0, 1]");
     if (n0 < 0 || n1 < 0 || n2 < 0) return fail(CK_ERR_INVALID_ARG, "dropout: negative size");
     if (n0 == 0 || n1 == 0 || n2 == 0) return CK_OK;
-    if (n0 > INT64_MAX / n1 || n0 * n1 > INT64_MAX / 16 / n2)
-        return fail(CK_ERR_UNSUPPORTED, "dropout: more than 2^59 elements");
+    constexpr int64_t kMost = (int64_t)1 << 40;
+    if (n0 > kMost / n1 || n0 * n1 > kMost / n2)
+        return fail(CK_ERR_UNSUPPORTED, "dropout: more than 2^40 elements");
     if (!x || !y) return fail(CK_ERR_INVALID_ARG, "a required pointer is NULL");
     DropArgs a{};
     a.x = x;
@@ -81,11 +308,8 @@ extern "C" ck_status ck_dropout(const void *x, void *y, int64_t dtype, int64_t n
     a.seed = seed;
     a.step = step;
     a.step_dev = step_dev;
-    const int64_t want = (a.n1 * a.n2 * a.n3 / 4 + 255) / 256, most = 8 * (int64_t)device_sms();
-    const int grid = (int)(want < 1 ? 1 : want < most ? want : most);
     with_dtype(dtype, [&](auto *tag) {
-        using T = std::remove_pointer_t<decltype(tag)>;
-        k_dropout<T><<<grid, 256, 0, (cudaStream_t)stream>>>(a);
+        launch_dropout<std::remove_pointer_t<decltype(tag)>>(a, (cudaStream_t)stream);
     });
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "k_dropout launch");
