@@ -12,35 +12,35 @@
 
 namespace ck {
 
-struct PhiloxKey {
-    uint32_t k0, k1;    // seed, low and high word
-    uint32_t c2, c3;    // step, low and high word
+struct PhiloxKeys {
+    uint32_t k[10][2];  // the keys of the ten rounds: the seed, moved on by two constants
+    uint64_t step;
+    const int64_t *step_dev;  // when given, a device word that holds the step
+    static PhiloxKeys of(uint64_t seed, uint64_t step, const int64_t *step_dev) {
+        PhiloxKeys p{};
+        for (int i = 0; i < 10; ++i) {
+            p.k[i][0] = (uint32_t)seed + (uint32_t)i * 0x9E3779B9u;
+            p.k[i][1] = (uint32_t)(seed >> 32) + (uint32_t)i * 0xBB67AE85u;
+        }
+        p.step = step;
+        p.step_dev = step_dev;
+        return p;
+    }
+    __device__ __forceinline__ uint64_t at() const { return step_dev ? (uint64_t)*step_dev : step; }
 };
 
-__device__ __forceinline__ uint4 philox(uint64_t block, const PhiloxKey &key) {
-    uint32_t a = (uint32_t)block, b = (uint32_t)(block >> 32), c = key.c2, d = key.c3;
-    uint32_t k0 = key.k0, k1 = key.k1;
+// `keys` is a kernel's argument: its words then are operands from constant memory.
+__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t step, const PhiloxKeys &keys) {
+    uint32_t a = (uint32_t)block, b = (uint32_t)(block >> 32), c = (uint32_t)step, d = (uint32_t)(step >> 32);
 #pragma unroll
     for (int round = 0; round < 10; ++round) {
         const uint64_t x = (uint64_t)a * 0xD2511F53u, y = (uint64_t)c * 0xCD9E8D57u;
-        const uint32_t na = (uint32_t)(y >> 32) ^ b ^ k0, nc = (uint32_t)(x >> 32) ^ d ^ k1;
+        a = (uint32_t)(y >> 32) ^ b ^ keys.k[round][0];
+        c = (uint32_t)(x >> 32) ^ d ^ keys.k[round][1];
         b = (uint32_t)y;
         d = (uint32_t)x;
-        a = na;
-        c = nc;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
     return make_uint4(a, b, c, d);
-}
-
-// The key of (seed, step); step_dev, when given, is a device word that holds
-// the step in place of `step`.
-__device__ __forceinline__ PhiloxKey philox_key(uint64_t seed, uint64_t step,
-                                                const int64_t *step_dev) {
-    if (step_dev) step = (uint64_t)*step_dev;
-    return PhiloxKey{(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)step,
-                     (uint32_t)(step >> 32)};
 }
 
 }  // namespace ck

@@ -19,20 +19,19 @@ struct DropArgs {
     uint32_t threshold;                   // keep an element whose word is >= threshold
     int drop_all;
     float scale;
-    uint64_t seed, step;
-    const int64_t *step_dev;
+    PhiloxKeys keys;
 };
 
 // A select and not a product: a dropped element is 0 whatever it held.
 template <typename T>
-__global__ void __launch_bounds__(256) k_dropout(DropArgs a) {
-    const PhiloxKey key = philox_key(a.seed, a.step, a.step_dev);
+__global__ void __launch_bounds__(256) k_dropout(const __grid_constant__ DropArgs a) {
+    const uint64_t step = a.keys.at();
     const T *x = (const T *)a.x;
     T *y = (T *)a.y;
     const int64_t n = a.n1 * a.n2 * a.n3, blocks = (n + 3) / 4;
     for (int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; q < blocks;
          q += (int64_t)gridDim.x * blockDim.x) {
-        const uint4 r = philox((uint64_t)q, key);
+        const uint4 r = philox((uint64_t)q, step, a.keys);
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -110,59 +109,67 @@ __device__ __forceinline__ uint4 load_vec(const T *line, int64_t e, int64_t leng
     return *(const uint4 *)t;
 }
 
-template <typename T> __device__ __forceinline__ uint4 select_scale(uint4 v, uint32_t keep, float scale) {
-    constexpr int E = kVec<T>;
-    alignas(16) T t[E];
-    memcpy(t, &v, 16);
+// Which of a piece's E elements are kept.
+template <typename T> struct Keep {
+    bool k[kVec<T>];
+    // elements m .. m + E - 1 of the mask; SHIFTED: m is not a multiple of four
+    template <bool SHIFTED>
+    __device__ __forceinline__ void make(const DropArgs &a, uint64_t step, int64_t m) {
+        constexpr int E = kVec<T>, kBlocks = E / 4 + (SHIFTED ? 1 : 0);
+        bool b[4 * kBlocks];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const float f = to_float(t[i]) * scale;
-        t[i] = from_float<T>(keep >> i & 1 ? f : 0.f);
-    }
-    memcpy(&v, t, 16);
-    return v;
-}
-
-// Keep bits of elements m .. m + E - 1 of the mask.
-template <typename T, bool SHIFTED>
-__device__ __forceinline__ uint32_t keep_bits(const DropArgs &a, const PhiloxKey &key, int64_t m) {
-    constexpr int E = kVec<T>, kBlocks = E / 4 + (SHIFTED ? 1 : 0);
-    uint32_t bits = 0;
+        for (int i = 0; i < kBlocks; ++i) {
+            const uint4 r = philox((uint64_t)(m >> 2) + i, step, a.keys);
+            b[4 * i] = r.x >= a.threshold;
+            b[4 * i + 1] = r.y >= a.threshold;
+            b[4 * i + 2] = r.z >= a.threshold;
+            b[4 * i + 3] = r.w >= a.threshold;
+        }
+        if constexpr (SHIFTED) {
+            uint32_t bits = 0;
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-        const uint4 r = philox((uint64_t)(m >> 2) + b, key);
-        bits |= ((r.x >= a.threshold) | (r.y >= a.threshold) << 1 | (r.z >= a.threshold) << 2 |
-                 (r.w >= a.threshold) << 3) << (4 * b);
+            for (int i = 0; i < 4 * kBlocks; ++i) bits |= (uint32_t)b[i] << i;
+            bits >>= m & 3;
+#pragma unroll
+            for (int i = 0; i < E; ++i) k[i] = bits >> i & 1;
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) k[i] = b[i];
+        }
     }
-    if (SHIFTED) bits >>= m & 3;
-    return a.drop_all ? 0u : bits;
-}
+    __device__ __forceinline__ uint4 apply(uint4 v, float scale) const {
+        alignas(16) T t[kVec<T>];
+        memcpy(t, &v, 16);
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) {
+            const float f = to_float(t[i]) * scale;
+            t[i] = from_float<T>(k[i] ? f : 0.f);
+        }
+        memcpy(&v, t, 16);
+        return v;
+    }
+};
 
-// SHIFTED: a locked mask whose length is no multiple of four, so that a piece of y
-// begins anywhere in a block.
-template <typename T, bool SHIFTED>
-__global__ void __launch_bounds__(kDropThreads) k_dropout_flat(DropFlat f) {
+// LOCKED: the mask has `period` elements and y several times as many.  SHIFTED: and
+// the period is no multiple of four, so that a piece of y begins anywhere in a block.
+template <typename T, bool LOCKED, bool SHIFTED>
+__global__ void __launch_bounds__(kDropThreads) k_dropout_flat(const __grid_constant__ DropFlat f) {
     constexpr int E = kVec<T>, kUnroll = 2;
     const DropArgs &a = f.a;
-    const PhiloxKey key = philox_key(a.seed, a.step, a.step_dev);
+    const uint64_t step = a.keys.at();
     const T *x = (const T *)a.x;
     T *y = (T *)a.y;
     const int64_t q0 = ((int64_t)blockIdx.x * kUnroll) * kDropThreads + threadIdx.x;
     uint4 v[kUnroll];
-    bool whole[kUnroll];
-    int64_t at[kUnroll];  // the element of x that a piece begins with
-    int64_t left[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
         const int64_t e = (q0 + i * kDropThreads) * E;
-        whole[i] = false;
         if (e >= f.n) continue;
-        int64_t row, c, plane, r2;
-        if (f.rows_joined) {
-            whole[i] = e + E <= f.n;
-            if (whole[i]) v[i] = load_vec<T>(x, e, f.n);
+        if (f.rows_joined && e + E <= f.n) {
+            v[i] = load_vec<T>(x, e, f.n);
             continue;
         }
+        int64_t row, plane;
         if (f.small) {
             row = f.row.quotient((uint32_t)e);
             plane = f.plane.quotient((uint32_t)row);
@@ -170,44 +177,71 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout_flat(DropFlat f) {
             row = e / a.n3;
             plane = row / a.n2;
         }
-        c = e - row * a.n3;
-        r2 = row - plane * a.n2;
-        // plane counts [repeat][n1], which have one stride where both are there (a.rep > 1: n1 = 1)
-        at[i] = plane * a.x1 + r2 * a.x2;
-        left[i] = a.n3 - c;
-        whole[i] = left[i] >= E;
-        if (whole[i]) v[i] = load_vec<T>(x + at[i], c, a.n3);
+        int64_t c = e - row * a.n3, r2 = row - plane * a.n2;
+        // plane counts n1 or, locked, the repeats
+        if (c + E <= a.n3) {
+            v[i] = load_vec<T>(x + plane * a.x1 + r2 * a.x2, c, a.n3);
+            continue;
+        }
+        alignas(16) T t[E];  // across a row's end, or the last
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            t[k] = e + k < f.n ? x[plane * a.x1 + r2 * a.x2 + c] : from_float<T>(0.f);
+            if (++c == a.n3) {
+                c = 0;
+                if (++r2 == a.n2) r2 = 0, ++plane;
+            }
+        }
+        memcpy(&v[i], t, 16);
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
         const int64_t e = (q0 + i * kDropThreads) * E;
         if (e >= f.n) continue;
-        int64_t m = e;
-        if (SHIFTED || a.rep > 1) m = e % f.period;
-        if (whole[i] && (!(SHIFTED || a.rep > 1) || m + E <= f.period)) {
-            const uint32_t keep = keep_bits<T, SHIFTED>(a, key, m);
-            __stcs((uint4 *)(y + e), select_scale<T>(v[i], keep, a.scale));
-            continue;
+        const int64_t m = LOCKED ? (f.small ? (uint32_t)e % (uint32_t)f.period : e % f.period) : e;
+        Keep<T> keep;
+        keep.template make<SHIFTED>(a, step, m);
+        if (LOCKED && m + E > f.period) {  // the mask begins again, perhaps more than once
+            for (int k = 0; k < E; ++k) {
+                const int64_t mk = (m + k) % f.period;
+                const uint4 r = philox((uint64_t)(mk >> 2), step, a.keys);
+                const uint32_t w = (mk & 2) ? (mk & 1 ? r.w : r.z) : (mk & 1 ? r.y : r.x);
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    if (j == k) keep.k[j] = w >= a.threshold;
+            }
         }
-        // a piece that crosses rows, repeats or the end
-        for (int64_t k = e; k < e + E && k < f.n; ++k) {
-            const int64_t mk = k % f.period, row = k / a.n3, c = k - row * a.n3, plane = row / a.n2;
-            const uint4 r = philox((uint64_t)(mk >> 2), key);
-            const uint32_t w = (mk & 2) ? (mk & 1 ? r.w : r.z) : (mk & 1 ? r.y : r.x);
-            const float t = to_float(x[plane * a.x1 + (row - plane * a.n2) * a.x2 + c]) * a.scale;
-            y[k] = from_float<T>(!a.drop_all && w >= a.threshold ? t : 0.f);
+        if (a.drop_all) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) keep.k[j] = false;
+        }
+        const uint4 out = keep.apply(v[i], a.scale);
+        if (e + E <= f.n) {
+            __stcs((uint4 *)(y + e), out);
+        } else {
+            alignas(16) T t[E];
+            memcpy(t, &out, 16);
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                if (e + k < f.n) y[e + k] = t[k];
         }
     }
 }
 
-// One mask for `rep` dense lines of n elements, n a multiple of E: its bits are
-// made once and used for the lines of blockIdx.y's share.
-template <typename T> __global__ void __launch_bounds__(kDropThreads) k_dropout_lines(DropFlat f, int lines) {
+// One mask for `rep` dense lines of n elements, n a multiple of E: it is made once
+// and used for the lines of blockIdx.y's share.
+template <typename T>
+__global__ void __launch_bounds__(kDropThreads) k_dropout_lines(const __grid_constant__ DropFlat f, int lines) {
     constexpr int E = kVec<T>, kUnroll = 4;
     const DropArgs &a = f.a;
     const int64_t m = ((int64_t)blockIdx.x * kDropThreads + threadIdx.x) * E;
     if (m >= f.period) return;
-    const uint32_t keep = keep_bits<T, false>(a, philox_key(a.seed, a.step, a.step_dev), m);
+    Keep<T> keep;
+    keep.template make<false>(a, a.keys.at(), m);
+    if (a.drop_all) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) keep.k[j] = false;
+    }
     const int64_t k0 = (int64_t)blockIdx.y * lines, k1 = k0 + lines < a.rep ? k0 + lines : a.rep;
     const T *x = (const T *)a.x + k0 * a.xr;
     T *y = (T *)a.y + k0 * f.period + m;
@@ -218,7 +252,7 @@ template <typename T> __global__ void __launch_bounds__(kDropThreads) k_dropout_
             if (k + i < k1) v[i] = load_vec<T>(x + i * a.xr, m, f.period);
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
-            if (k + i < k1) __stcs((uint4 *)(y + i * f.period), select_scale<T>(v[i], keep, a.scale));
+            if (k + i < k1) __stcs((uint4 *)(y + i * f.period), keep.apply(v[i], a.scale));
         x += kUnroll * a.xr;
         y += kUnroll * f.period;
     }
@@ -268,10 +302,12 @@ template <typename T> void launch_dropout(const DropArgs &a, cudaStream_t stream
     }
     const int64_t pieces = (f.n + E - 1) / E;
     const unsigned grid = (unsigned)((pieces + 2 * kDropThreads - 1) / (2 * kDropThreads));
-    if (a.rep > 1 && f.period % 4 != 0)
-        k_dropout_flat<T, true><<<grid, kDropThreads, 0, stream>>>(f);
+    if (a.rep == 1)
+        k_dropout_flat<T, false, false><<<grid, kDropThreads, 0, stream>>>(f);
+    else if (f.period % 4 == 0)
+        k_dropout_flat<T, true, false><<<grid, kDropThreads, 0, stream>>>(f);
     else
-        k_dropout_flat<T, false><<<grid, kDropThreads, 0, stream>>>(f);
+        k_dropout_flat<T, true, true><<<grid, kDropThreads, 0, stream>>>(f);
 }
 
 }  // namespace
@@ -305,9 +341,7 @@ extern "C" ck_status ck_dropout(const void *x, void *y, int64_t dtype, int64_t n
     a.drop_all = t >= 4294967296.0;
     a.threshold = a.drop_all ? 0u : (uint32_t)t;
     a.scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.f;
-    a.seed = seed;
-    a.step = step;
-    a.step_dev = step_dev;
+    a.keys = PhiloxKeys::of(seed, step, step_dev);
     with_dtype(dtype, [&](auto *tag) {
         launch_dropout<std::remove_pointer_t<decltype(tag)>>(a, (cudaStream_t)stream);
     });

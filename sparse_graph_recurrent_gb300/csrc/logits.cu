@@ -38,7 +38,8 @@ template <typename I> __device__ __forceinline__ int64_t row_len(const void *p, 
 // tiles.  Counts of a tile's tokens are taken from the row's history with
 // integer additions in shared memory, so their order does not matter.
 template <typename T, typename I>
-__global__ void __launch_bounds__(kLogitThreads) k_logits(ck_logit_call a) {
+__global__ void __launch_bounds__(kLogitThreads) k_logits(const __grid_constant__ ck_logit_call a,
+                                                         const __grid_constant__ PhiloxKeys keys) {
     __shared__ uint32_t count[kTile];
     __shared__ uint64_t best_of[32];
     __shared__ uint64_t best_cta;
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(kLogitThreads) k_logits(ck_logit_call a) {
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     const int64_t per = ((a.V + ranks - 1) / ranks + 127) / 128 * 128;
     const int64_t s0 = rank * per, s1 = s0 + per < a.V ? s0 + per : a.V;
-    const PhiloxKey key = philox_key(a.seed, a.step, a.step_dev);
+    const uint64_t step = keys.at();
     const float rep = a.repetition ? a.repetition[b] : a.repetition_all;
     const float freq = a.frequency ? a.frequency[b] : a.frequency_all;
     const float pres = a.presence ? a.presence[b] : a.presence_all;
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kLogitThreads) k_logits(ck_logit_call a) {
         const int64_t e0 = b * a.V;
         for (int64_t q = (e0 + t0) / 4 + threadIdx.x; 4 * q < e0 + t1; q += kLogitThreads) {
             uint4 r = make_uint4(0, 0, 0, 0);
-            if (noisy) r = philox((uint64_t)q, key);
+            if (noisy) r = philox((uint64_t)q, step, keys);
             const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -154,11 +155,12 @@ extern "C" ck_status ck_control_logits(const ck_logit_call *call, void *stream) 
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
+    const PhiloxKeys keys = PhiloxKeys::of(a.seed, a.step, a.step_dev);
     cudaError_t e = cudaSuccess;
     with_dtype(a.dtype, [&](auto *tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
-        e = a.history && a.history_bits == 32 ? cudaLaunchKernelEx(&cfg, k_logits<T, int32_t>, a)
-                                              : cudaLaunchKernelEx(&cfg, k_logits<T, int64_t>, a);
+        e = a.history && a.history_bits == 32 ? cudaLaunchKernelEx(&cfg, k_logits<T, int32_t>, a, keys)
+                                              : cudaLaunchKernelEx(&cfg, k_logits<T, int64_t>, a, keys);
     });
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "k_logits launch");
 }
