@@ -29,11 +29,13 @@ struct PhiloxKeys {
     __device__ __forceinline__ uint64_t at() const { return step_dev ? (uint64_t)*step_dev : step; }
 };
 
-// `keys` is a kernel's argument: its words then are operands from constant memory.
-__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t step, const PhiloxKeys &keys) {
-    uint32_t a = (uint32_t)block, b = (uint32_t)(block >> 32), c = (uint32_t)step, d = (uint32_t)(step >> 32);
+// Rounds `from` to 9.  `keys` is a kernel's argument: its words then are operands
+// from constant memory.
+template <int from>
+__device__ __forceinline__ uint4 philox_rounds(uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                               const PhiloxKeys &keys) {
 #pragma unroll
-    for (int round = 0; round < 10; ++round) {
+    for (int round = from; round < 10; ++round) {
         const uint64_t x = (uint64_t)a * 0xD2511F53u, y = (uint64_t)c * 0xCD9E8D57u;
         a = (uint32_t)(y >> 32) ^ b ^ keys.k[round][0];
         c = (uint32_t)(x >> 32) ^ d ^ keys.k[round][1];
@@ -41,6 +43,28 @@ __device__ __forceinline__ uint4 philox(uint64_t block, uint64_t step, const Phi
         d = (uint32_t)x;
     }
     return make_uint4(a, b, c, d);
+}
+
+__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t step, const PhiloxKeys &keys) {
+    return philox_rounds<0>((uint32_t)block, (uint32_t)(block >> 32), (uint32_t)step, (uint32_t)(step >> 32),
+                            keys);
+}
+
+// Blocks `block` and block + 1, `block` even, with 37 wide products for 40: they have
+// the product of the step in the first round and that which follows from it in the
+// second in common, and the two other products of the first round differ by the factor.
+__device__ __forceinline__ void philox_two(uint64_t block, uint64_t step, const PhiloxKeys &keys, uint4 &r0,
+                                           uint4 &r1) {
+    const uint64_t x0 = (uint64_t)(uint32_t)block * 0xD2511F53u, x1 = x0 + 0xD2511F53u;
+    const uint64_t y = (uint64_t)(uint32_t)step * 0xCD9E8D57u;
+    const uint32_t a = (uint32_t)(y >> 32) ^ (uint32_t)(block >> 32) ^ keys.k[0][0], b = (uint32_t)y;
+    const uint32_t dk = (uint32_t)(step >> 32) ^ keys.k[0][1];
+    const uint64_t z = (uint64_t)a * 0xD2511F53u;
+    const uint32_t bk = b ^ keys.k[1][0], zk = (uint32_t)(z >> 32) ^ keys.k[1][1];
+    const uint64_t y0 = (uint64_t)((uint32_t)(x0 >> 32) ^ dk) * 0xCD9E8D57u,
+                   y1 = (uint64_t)((uint32_t)(x1 >> 32) ^ dk) * 0xCD9E8D57u;
+    r0 = philox_rounds<2>((uint32_t)(y0 >> 32) ^ bk, (uint32_t)y0, zk ^ (uint32_t)x0, (uint32_t)z, keys);
+    r1 = philox_rounds<2>((uint32_t)(y1 >> 32) ^ bk, (uint32_t)y1, zk ^ (uint32_t)x1, (uint32_t)z, keys);
 }
 
 }  // namespace ck

@@ -17,7 +17,7 @@ struct DropArgs {
     int64_t xr, x1, x2, x3;               // element strides of x: repeat, then the mask's axes
     int64_t yr, y1, y2, y3;
     uint32_t threshold;                   // keep an element whose word is >= threshold
-    int drop_all;
+    int drop_all;                         // p = 1: read as zeros (scale is 0 too)
     float scale;
     PhiloxKeys keys;
 };
@@ -116,14 +116,20 @@ template <typename T> struct Keep {
     template <bool SHIFTED>
     __device__ __forceinline__ void make(const DropArgs &a, uint64_t step, int64_t m) {
         constexpr int E = kVec<T>, kBlocks = E / 4 + (SHIFTED ? 1 : 0);
+        uint4 r[kBlocks];
+        if constexpr (!SHIFTED && kBlocks == 2) {
+            philox_two((uint64_t)(m >> 2), step, a.keys, r[0], r[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) r[i] = philox((uint64_t)(m >> 2) + i, step, a.keys);
+        }
         bool b[4 * kBlocks];
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
-            const uint4 r = philox((uint64_t)(m >> 2) + i, step, a.keys);
-            b[4 * i] = r.x >= a.threshold;
-            b[4 * i + 1] = r.y >= a.threshold;
-            b[4 * i + 2] = r.z >= a.threshold;
-            b[4 * i + 3] = r.w >= a.threshold;
+            b[4 * i] = r[i].x >= a.threshold;
+            b[4 * i + 1] = r[i].y >= a.threshold;
+            b[4 * i + 2] = r[i].z >= a.threshold;
+            b[4 * i + 3] = r[i].w >= a.threshold;
         }
         if constexpr (SHIFTED) {
             uint32_t bits = 0;
@@ -149,6 +155,30 @@ template <typename T> struct Keep {
         return v;
     }
 };
+
+// x one dense, aligned line and the mask as long: the whole pieces of it, `n` of them.
+// Generator and memory take about the same time and have to overlap: many warps, with
+// little between a load and the next.
+template <typename T>
+__global__ void __launch_bounds__(kDropThreads, 7) k_dropout_dense(const __grid_constant__ DropArgs a, int64_t n) {
+    constexpr int kUnroll = 2;
+    const uint64_t step = a.keys.at();
+    const int64_t q0 = (int64_t)blockIdx.x * (kUnroll * kDropThreads) + threadIdx.x;
+    const uint4 *x = (const uint4 *)a.x + q0;
+    uint4 *y = (uint4 *)a.y + q0;
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i)
+        if (q0 + i * kDropThreads < n) v[i] = __ldcs(x + i * kDropThreads);
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        if (q0 + i * kDropThreads >= n) return;
+        Keep<T> keep;
+        keep.template make<false>(a, step, (q0 + i * kDropThreads) * kVec<T>);
+        if (a.drop_all) v[i] = make_uint4(0, 0, 0, 0);
+        __stcs(y + i * kDropThreads, keep.apply(v[i], a.scale));
+    }
+}
 
 // LOCKED: the mask has `period` elements and y several times as many.  SHIFTED: and
 // the period is no multiple of four, so that a piece of y begins anywhere in a block.
@@ -211,10 +241,7 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout_flat(const __grid_cons
                     if (j == k) keep.k[j] = w >= a.threshold;
             }
         }
-        if (a.drop_all) {
-#pragma unroll
-            for (int j = 0; j < E; ++j) keep.k[j] = false;
-        }
+        if (a.drop_all) v[i] = make_uint4(0, 0, 0, 0);
         const uint4 out = keep.apply(v[i], a.scale);
         if (e + E <= f.n) {
             __stcs((uint4 *)(y + e), out);
@@ -238,10 +265,6 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout_lines(const __grid_con
     if (m >= f.period) return;
     Keep<T> keep;
     keep.template make<false>(a, a.keys.at(), m);
-    if (a.drop_all) {
-#pragma unroll
-        for (int j = 0; j < E; ++j) keep.k[j] = false;
-    }
     const int64_t k0 = (int64_t)blockIdx.y * lines, k1 = k0 + lines < a.rep ? k0 + lines : a.rep;
     const T *x = (const T *)a.x + k0 * a.xr;
     T *y = (T *)a.y + k0 * f.period + m;
@@ -252,7 +275,10 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout_lines(const __grid_con
             if (k + i < k1) v[i] = load_vec<T>(x + i * a.xr, m, f.period);
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
-            if (k + i < k1) __stcs((uint4 *)(y + i * f.period), keep.apply(v[i], a.scale));
+            if (k + i < k1) {
+                if (a.drop_all) v[i] = make_uint4(0, 0, 0, 0);
+                __stcs((uint4 *)(y + i * f.period), keep.apply(v[i], a.scale));
+            }
         x += kUnroll * a.xr;
         y += kUnroll * f.period;
     }
@@ -301,6 +327,11 @@ template <typename T> void launch_dropout(const DropArgs &a, cudaStream_t stream
         f.plane = Divider::of((uint32_t)a.n2);
     }
     const int64_t pieces = (f.n + E - 1) / E;
+    if (a.rep == 1 && f.rows_joined && ((uintptr_t)a.x & 15) == 0 && f.n % E == 0) {
+        k_dropout_dense<T><<<(unsigned)((pieces + 2 * kDropThreads - 1) / (2 * kDropThreads)), kDropThreads, 0,
+                             stream>>>(a, pieces);
+        return;
+    }
     const unsigned grid = (unsigned)((pieces + 2 * kDropThreads - 1) / (2 * kDropThreads));
     if (a.rep == 1)
         k_dropout_flat<T, false, false><<<grid, kDropThreads, 0, stream>>>(f);
