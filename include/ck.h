@@ -401,7 +401,8 @@ ck_status ck_int4_quantize(const void *w, int64_t dtype, int64_t V, int64_t K, i
  *      history[b][prompt_b : len_b]
  *   3. z + bias[v]
  *   4. -inf where bit v % 32 of mask word v / 32 is 0
- *   5. z / temperature where temperature > 0
+ *   5. z / temperature where temperature > 0 (in `out` the product with 1 /
+ *      temperature, one rounding more)
  * Ids outside [0, V) in the history are ignored (padding).  len_b and prompt_b
  * are clamped to [0, L].  out[b][v] = z, rounded to the logits' type.
  * tokens[b] = the v of the largest z (of equal ones the lowest v), before
@@ -414,8 +415,11 @@ ck_status ck_int4_quantize(const void *w, int64_t dtype, int64_t V, int64_t K, i
  * 0 (prompt_len), or leaves its control out (history, bias, mask, out, tokens).
  * out may be logits.  Strides are in elements (mask: words); a bias_stride or
  * mask_stride of 0 shares one row.  Asynchronous.
+ * `workspace` (device, 8-byte aligned) holds workspace_bytes, at least what
+ * ck_logits_workspace_size says for the same B, V and L (0 without a history) on this
+ * device; needed where tokens are, if that is not 0 bytes.
  * Errors: CK_ERR_INVALID_ARG (types, sizes, NULL logits, neither out nor
- * tokens), CK_ERR_UNSUPPORTED (V >= 2^31, B > 65535), CK_ERR_CUDA.
+ * tokens), CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED (V >= 2^31, B > 65535), CK_ERR_CUDA.
  */
 typedef struct {
     const void *logits;
@@ -434,7 +438,10 @@ typedef struct {
     int64_t sample;
     uint64_t seed, step;
     const int64_t *step_dev;
+    void *workspace;
+    int64_t workspace_bytes;
 } ck_logit_call;
+ck_status ck_logits_workspace_size(int64_t B, int64_t V, int64_t L, size_t *bytes);
 ck_status ck_control_logits(const ck_logit_call *call, void *stream);
 
 /*

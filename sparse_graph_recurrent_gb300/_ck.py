@@ -43,7 +43,8 @@ class LogitCall(ctypes.Structure):
                 ("temperature_all", _f),
                 ("bias", _p), ("bias_stride", _i), ("mask", _p), ("mask_stride", _i),
                 ("out", _p), ("out_stride", _i), ("tokens", _p), ("sample", _i),
-                ("seed", _u), ("step", _u), ("step_dev", _p)]
+                ("seed", _u), ("step", _u), ("step_dev", _p), ("workspace", _p),
+                ("workspace_bytes", _i)]
 
 
 class CKError(RuntimeError):
@@ -104,6 +105,7 @@ def load() -> ctypes.CDLL:
         "ck_int4_workspace_size": [i64, i64, i64, i64, i64, psz],
         "ck_int4_quantize": [p, i64, i64, i64, i64, i64, i64, p, i64, p, i64, i64, p, i64, p],
         "ck_control_logits": [ctypes.POINTER(LogitCall), p],
+        "ck_logits_workspace_size": [i64, i64, i64, psz],
         "ck_forward_static_scratch": [p, p, p, p, p, p, i64, i64, i64, p, p, sz, p],
         "ck_probe_read": [p, sz, i64, p, p],
         "ck_probe_gather": [p, i64, i64, p, i64, p, p],
@@ -434,6 +436,12 @@ def ck_int4_quantize(w, group: int, qweight, scales, zeros, stream=None):
         qweight.data_ptr(), _rows(qweight, "qweight"), scales.data_ptr(), DTYPES[scales.dtype],
         _rows(scales, "scales"), None if zeros is None else zeros.data_ptr(),
         0 if zeros is None else _rows(zeros, "zeros"), _raw_stream(stream)))
+
+
+def ck_logits_workspace_size(B: int, V: int, L: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().ck_logits_workspace_size(B, V, L, ctypes.byref(n)))
+    return n.value
 
 
 def ck_control_logits(call: LogitCall, stream=None):

@@ -1,17 +1,16 @@
 // ck_control_logits: penalties for repeated tokens, biases, grammar masks and
 // temperature on a batch of logits, and in the same pass the next token.
-#include <cooperative_groups.h>
+#include <cstring>
+#include <type_traits>
 
 #include "ck_philox.h"
 #include "ck_types.h"
 
-namespace cg = cooperative_groups;
-
 namespace ck {
 namespace {
 
-constexpr int kLogitThreads = 512;
-constexpr int kTile = 16384;  // most tokens whose counts one CTA holds at once
+constexpr int kLogitThreads = 256, kLogitCtas = 4;  // threads of a CTA, CTAs of an SM
+constexpr int kTile = 8192;   // most tokens of a CTA, whose counts it holds in shared memory
 constexpr int kOct = 8;       // tokens a thread takes at a time
 
 enum Pick { kNone, kGreedy, kSample };
@@ -43,27 +42,21 @@ __device__ __forceinline__ int64_t row_len(const void *p, int64_t bits, int64_t 
     return n < 0 ? 0 : n < L ? n : L;
 }
 
-// Controls of a row.
-template <typename T> struct Row {
-    const T *in;
-    T *out;
-    const float *bias;
-    const uint32_t *mask;
+struct Row {
     float rep, freq, pres, temp;
-
+    // A logit after the penalties, c what the table holds for its token.
     __device__ __forceinline__ float penalised(float z, uint32_t c) const {
         z = z > 0.f ? z / rep : z * rep;
         return __fsub_rn(z, __fadd_rn(__fmul_rn((float)(c >> 1), freq), c > 1 ? pres : 0.f));
     }
-    // Logit v after all controls, c what the table holds for it.
-    __device__ __forceinline__ float at(int64_t v, uint32_t c) const {
-        float z = to_float(in[v]);
-        if (c) z = penalised(z, c);
-        if (bias) z = __fadd_rn(z, bias[v]);
-        if (mask && !(mask[v >> 5] >> (v & 31) & 1u)) z = minus_inf();
-        return temp > 0.f ? z / temp : z;
-    }
 };
+
+// For bounds; of numbers that are 0 or normal.
+__device__ __forceinline__ float log2_fast(float v) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 
 // count[v - t0] for the tokens t0 <= v < t1 of history[0 .. len): twice the number
 // of occurrences from `prompt` on, odd or not zero where the token was seen at all.
@@ -71,262 +64,330 @@ template <typename T> struct Row {
 template <typename I>
 __device__ __forceinline__ void count_history(const I *h, int64_t len, int64_t prompt, int64_t t0, int64_t t1,
                                               uint32_t *count) {
-    constexpr int kBatch = 8;
-    for (int64_t i0 = threadIdx.x; i0 < len; i0 += kBatch * kLogitThreads) {
-        I v[kBatch];
+    using U = std::make_unsigned_t<I>;
+    constexpr int kPer = 16 / (int)sizeof(I), kBatch = 8;  // ids of a load, loads on their way at once
+    const U first = (U)t0, span = (U)(t1 - t0);  // t1 < 2^31
+    auto take = [&](I id, int64_t i) {
+        const U at = (U)id - first;
+        if (at >= span) return;
+        if (i >= prompt)
+            atomicAdd(&count[at], 2u);  // seen, and made here
+        else
+            atomicOr(&count[at], 1u);
+    };
+    // single ids up to a 16-byte boundary and after the last
+    int64_t head = (int64_t)((16 - ((uintptr_t)h & 15)) & 15) / (int64_t)sizeof(I);
+    if (head > len) head = len;
+    const int64_t pieces = (len - head) / kPer, tail = head + pieces * kPer;
+    if (threadIdx.x < head) take(h[threadIdx.x], threadIdx.x);
+    if (threadIdx.x < len - tail) take(h[tail + threadIdx.x], tail + threadIdx.x);
+    const uint4 *body = (const uint4 *)(h + head);
+    for (int64_t i0 = threadIdx.x; i0 < pieces; i0 += kBatch * kLogitThreads) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (i0 + k * kLogitThreads < pieces) v[k] = __ldg(body + i0 + k * kLogitThreads);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int64_t i = i0 + k * kLogitThreads;
-            v[k] = i < len ? h[i] : (I)-1;
-        }
+            if (i >= pieces) break;
+            I id[kPer];
+            memcpy(id, &v[k], 16);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int64_t i = i0 + k * kLogitThreads;
-            if ((int64_t)v[k] < t0 || (int64_t)v[k] >= t1) continue;
-            if (i >= prompt)
-                atomicAdd(&count[v[k] - t0], 2u);  // seen, and made here
-            else
-                atomicOr(&count[v[k] - t0], 1u);
+            for (int j = 0; j < kPer; ++j) take(id[j], head + i * kPer + j);
         }
     }
 }
 
-// A cluster of CTAs takes one row, each a slice of the vocabulary; the row's best
-// token meets in the first CTA's shared memory.  A thread takes eight tokens at a
-// time, cut so that they are two blocks of the generator (sampling) or 16-byte pieces
-// of the logits (else).
+struct LogitPlan {
+    int64_t slice;  // tokens of a CTA
+    int slices;     // CTAs of a row
+};
+
+// A CTA takes a slice of a row's vocabulary, a thread eight tokens at a time, cut so
+// that they are two blocks of the generator (sampling) or 16-byte pieces of the logits
+// (else).  Where a row has several slices their best tokens go to `keys_out`, which
+// k_pick looks through.
 //
 // What bounds it at large sizes is arithmetic: a token drawn costs a word of the
 // generator and two logarithms.  The logarithms are spared: as -log1p(-u) >= u, the
 // noise is at most -log u, which one approximate logarithm of a number no larger
-// than u bounds from above; only tokens whose bound reaches the best score that
-// their warp has seen are scored as defined, from the start.
+// than u bounds from above; a bound from below for a lane's likeliest token gives a
+// score that the CTA's best has at least.  Only tokens that may reach it are scored as
+// defined, and a lane puts its one off to the end, when few are left.
 template <typename T, int PICK>
-__global__ void __launch_bounds__(kLogitThreads, 2) k_logits(const __grid_constant__ ck_logit_call a,
-                                                         const __grid_constant__ PhiloxKeys keys) {
+__global__ void __launch_bounds__(kLogitThreads, kLogitCtas)
+    k_logits(const __grid_constant__ ck_logit_call a, const __grid_constant__ PhiloxKeys keys, LogitPlan plan,
+             unsigned long long *keys_out) {
     extern __shared__ __align__(16) uint32_t count[];
-    __shared__ unsigned long long best_cta, best_of[8];  // best_of: of the cluster's CTAs, in the first
-    cg::cluster_group cluster = cg::this_cluster();
-    const int64_t b = blockIdx.y;
-    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-    if (PICK != kNone) {
-        if (threadIdx.x == 0) best_cta = 0;
+    __shared__ uint32_t floor_key;  // a score that some token of the CTA has at least
+    __shared__ unsigned long long best_cta;
+    const int64_t b = blockIdx.x / plan.slices;
+    const int slice = (int)(blockIdx.x - b * plan.slices);
+    const int64_t t0 = slice * plan.slice, t1 = t0 + plan.slice < a.V ? t0 + plan.slice : a.V;
+    if (PICK != kNone && threadIdx.x == 0) best_cta = 0, floor_key = 0;
+    const int64_t e0 = b * a.V;
+    const T *row_in = (const T *)a.logits + b * a.logits_stride;
+    // octs begin at tokens v with (v + cut) % 8 == 0; the oct at offset o holds tokens
+    // v0 + o to v0 + o + 7, those with offsets in [from, to) there
+    const int cut = PICK == kSample ? (int)(e0 & 7) : (int)(((uintptr_t)row_in / sizeof(T)) & 7);
+    const int64_t v0 = t0 - cut;
+    const int from = cut, to = cut + (int)(t1 - t0), octs = (to + kOct - 1) / kOct;
+    const int64_t len = a.history ? row_len(a.history_len, a.history_bits, b, a.L) : 0;
+    if (len > 0) {
+        const int64_t prompt = a.prompt_len ? row_len(a.prompt_len, a.history_bits, b, a.L) : 0;
+        for (int i = threadIdx.x; i < octs * 2; i += kLogitThreads) ((uint4 *)count)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        if (a.history_bits == 32)
+            count_history((const int32_t *)a.history + b * a.history_stride, len, prompt, t0, t1, count + cut);
+        else
+            count_history((const int64_t *)a.history + b * a.history_stride, len, prompt, t0, t1, count + cut);
     }
-    const int64_t per = ((a.V + ranks - 1) / ranks + 127) / 128 * 128;
-    const int64_t s0 = rank * per, s1 = s0 + per < a.V ? s0 + per : a.V;
-    Row<T> row;
-    row.in = (const T *)a.logits + b * a.logits_stride;
-    row.out = a.out ? (T *)a.out + b * a.out_stride : nullptr;
-    row.bias = a.bias ? a.bias + b * a.bias_stride : nullptr;
-    row.mask = a.mask ? (const uint32_t *)a.mask + b * a.mask_stride : nullptr;
+    __syncthreads();
+    Row row;
     row.rep = a.repetition ? a.repetition[b] : a.repetition_all;
     row.freq = a.frequency ? a.frequency[b] : a.frequency_all;
     row.pres = a.presence ? a.presence[b] : a.presence_all;
     row.temp = a.temperature ? a.temperature[b] : a.temperature_all;
     const bool heat = row.temp > 0.f, noisy = PICK == kSample && heat;
     const float cool = heat ? 1.f / row.temp : 1.f;
-    const int64_t len = a.history ? row_len(a.history_len, a.history_bits, b, a.L) : 0;
-    const int64_t prompt = a.history && a.prompt_len ? row_len(a.prompt_len, a.history_bits, b, a.L) : 0;
-    const int64_t e0 = b * a.V;
     const uint64_t step = PICK == kSample ? keys.at() : 0;
-    // octs begin at tokens v with (v + cut) % 8 == 0
-    const int cut = PICK == kSample ? (int)(e0 & 7) : (int)(((uintptr_t)row.in / sizeof(T)) & 7);
-    const bool in_vec = (((uintptr_t)row.in - cut * sizeof(T)) & 15) == 0;
-    const bool out_vec = (((uintptr_t)row.out - cut * sizeof(T)) & 15) == 0;
-    const bool bias_vec = (((uintptr_t)row.bias - cut * sizeof(float)) & 15) == 0;
+    const T *in = row_in + v0;
+    T *out = a.out ? (T *)a.out + b * a.out_stride + v0 : nullptr;
+    const float *bias = a.bias ? a.bias + b * a.bias_stride + v0 : nullptr;
+    const uint32_t *mask = a.mask ? (const uint32_t *)a.mask + b * a.mask_stride : nullptr;
+    const bool in_vec = ((uintptr_t)in & 15) == 0, out_vec = ((uintptr_t)out & 15) == 0,
+               bias_vec = ((uintptr_t)bias & 15) == 0;
     unsigned long long best = 0;
-    float floor = minus_inf();  // sampling: the best score that the warp has seen
-    for (int64_t t0 = s0; t0 < s1; t0 += kTile) {
-        const int64_t t1 = t0 + kTile < s1 ? t0 + kTile : s1;
-        const int64_t q0 = (t0 + cut) / kOct, q1 = (t1 + cut + kOct - 1) / kOct;
-        if (len > 0) {
-            if (t0 > s0) __syncthreads();
-            for (int i = threadIdx.x; i < (int)(q1 - q0) * 2; i += kLogitThreads)
-                ((uint4 *)count)[i] = make_uint4(0, 0, 0, 0);
-            __syncthreads();
-            uint32_t *mine = count + cut;
-            if (a.history_bits == 32)
-                count_history((const int32_t *)a.history + b * a.history_stride, len, prompt, t0, t1, mine);
-            else
-                count_history((const int64_t *)a.history + b * a.history_stride, len, prompt, t0, t1, mine);
-            __syncthreads();
+    // sampling: a token that may be the one, to be scored when more is known; its logit
+    // before the temperature
+    float later_high = minus_inf(), later_z = 0.f;
+    uint32_t later_word = 0;
+    int later_o = 0;
+    auto score_later = [&] {
+        const unsigned long long k =
+            pick_key(__fadd_rn(later_z / row.temp, gumbel(later_word)), (uint32_t)(v0 + later_o));
+        best = k > best ? k : best;
+    };
+    for (int ow = threadIdx.x & ~31; ow < octs; ow += kLogitThreads) {
+        const int o = (ow + (int)(threadIdx.x & 31)) * kOct;
+        const bool full = o >= from && o + kOct <= to;
+        float z[kOct];
+        uint32_t there = 0xff;  // tokens of the oct that exist
+        if (full && in_vec) {
+            alignas(16) T t[kOct];
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) ((uint4 *)t)[i] = __ldcs((const uint4 *)(in + o) + i);
+#pragma unroll
+            for (int j = 0; j < kOct; ++j) z[j] = to_float(t[j]);
+        } else {
+            there = 0;
+#pragma unroll
+            for (int j = 0; j < kOct; ++j) {
+                const bool is = o + j >= from && o + j < to;
+                z[j] = is ? to_float(in[o + j]) : minus_inf();  // never picked
+                there |= (uint32_t)is << j;
+            }
         }
-        for (int64_t qw = q0 + (threadIdx.x & ~31); qw < q1; qw += kLogitThreads) {
-            const int64_t q = qw + (threadIdx.x & 31), v0 = q * kOct - cut;
-            float z[kOct];
-            uint32_t ok = 0;  // tokens that are there and allowed
-            if (v0 >= t0 && v0 + kOct <= t1 && in_vec) {
-                alignas(16) T t[kOct];
+        if (len > 0 && there) {
+            const uint4 c0 = ((const uint4 *)count)[o / 4], c1 = ((const uint4 *)count)[o / 4 + 1];
+            const uint32_t c[kOct] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+            uint32_t hit = 0;
 #pragma unroll
-                for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-                    ((uint4 *)t)[i] = __ldcs((const uint4 *)(row.in + v0) + i);
-#pragma unroll
-                for (int j = 0; j < kOct; ++j) z[j] = to_float(t[j]);
-                ok = 0xff;
-            } else {
-#pragma unroll
-                for (int j = 0; j < kOct; ++j) {
-                    const bool in = v0 + j >= t0 && v0 + j < t1;
-                    z[j] = in ? to_float(row.in[v0 + j]) : 0.f;
-                    ok |= (uint32_t)in << j;
-                }
-            }
-            const uint32_t there = ok;
-            if (len > 0 && there) {
-                const uint4 c0 = ((const uint4 *)count)[2 * (q - q0)], c1 = ((const uint4 *)count)[2 * (q - q0) + 1];
-                if (c0.x | c0.y | c0.z | c0.w | c1.x | c1.y | c1.z | c1.w) {
-                    const uint32_t c[kOct] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-                    for (int j = 0; j < kOct; ++j)
-                        if (c[j]) z[j] = row.penalised(z[j], c[j]);
-                }
-            }
-            if (row.bias) {
-                if (there == 0xff && bias_vec) {
-                    const float4 b0 = *(const float4 *)(row.bias + v0), b1 = *(const float4 *)(row.bias + v0 + 4);
-                    const float bb[kOct] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-#pragma unroll
-                    for (int j = 0; j < kOct; ++j) z[j] = __fadd_rn(z[j], bb[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kOct; ++j)
-                        if (there >> j & 1) z[j] = __fadd_rn(z[j], row.bias[v0 + j]);
-                }
-            }
-            if (row.mask) {
-                if (there == 0xff) {
-                    const uint32_t *w = row.mask + (v0 >> 5);
-                    const int from = (int)(v0 & 31);
-                    ok = __funnelshift_r(w[0], from > 32 - kOct ? w[1] : 0u, from) & 0xff;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kOct; ++j)
-                        if ((there >> j & 1) && !(row.mask[(v0 + j) >> 5] >> ((v0 + j) & 31) & 1u)) ok &= ~(1u << j);
-                }
+            for (int j = 0; j < kOct; ++j) hit |= (uint32_t)(c[j] != 0) << j;
+            while (hit) {  // few: one by one
+                const int at = __ffs(hit) - 1;
+                hit &= hit - 1;
+                float zv = 0.f;
+                uint32_t cv = 0;
 #pragma unroll
                 for (int j = 0; j < kOct; ++j)
-                    if (!(ok >> j & 1)) z[j] = minus_inf();
+                    if (j == at) zv = z[j], cv = c[j];
+                zv = row.penalised(zv, cv);
+#pragma unroll
+                for (int j = 0; j < kOct; ++j)
+                    if (j == at) z[j] = zv;
             }
-            if (heat) {
-                // a product would do to find candidates, but is not what is returned
-                if (PICK == kSample && !row.out) {
+        }
+        if (bias) {
+            if (full && bias_vec) {
+                const float4 b0 = *(const float4 *)(bias + o), b1 = *(const float4 *)(bias + o + 4);
+                const float bb[kOct] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
-                    for (int j = 0; j < kOct; ++j) z[j] *= cool;
-                } else if (row.temp != 1.f) {
+                for (int j = 0; j < kOct; ++j) z[j] = __fadd_rn(z[j], bb[j]);
+            } else {
 #pragma unroll
-                    for (int j = 0; j < kOct; ++j) z[j] = z[j] / row.temp;
-                }
+                for (int j = 0; j < kOct; ++j)
+                    if (there >> j & 1) z[j] = __fadd_rn(z[j], bias[o + j]);
             }
-            if (row.out) {
-                if (there == 0xff && out_vec) {
-                    alignas(16) T t[kOct];
+        }
+        if (mask) {
+            uint32_t ok = 0;
+            if (full) {
+                const int64_t v = v0 + o;
+                const uint32_t *w = mask + (v >> 5);
+                const int low = (int)(v & 31);
+                ok = __funnelshift_r(w[0], low > 32 - kOct ? w[1] : 0u, low);
+            } else {
 #pragma unroll
-                    for (int j = 0; j < kOct; ++j) t[j] = from_float<T>(z[j]);
-#pragma unroll
-                    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-                        __stcs((uint4 *)(row.out + v0) + i, ((const uint4 *)t)[i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kOct; ++j)
-                        if (there >> j & 1) row.out[v0 + j] = from_float<T>(z[j]);
-                }
+                for (int j = 0; j < kOct; ++j)
+                    if (there >> j & 1) ok |= (mask[(v0 + o + j) >> 5] >> ((v0 + o + j) & 31) & 1u) << j;
             }
-            if constexpr (PICK != kNone) {
-                if (!noisy) {
-                    float top = minus_inf();
-                    int at = 0;
 #pragma unroll
-                    for (int j = 0; j < kOct; ++j)
-                        if (z[j] > top && (there >> j & 1)) top = z[j], at = j;  // of equal ones the first; no NaN
-                    const unsigned long long k = pick_key(top, (uint32_t)(v0 + at));
-                    best = k > best ? k : best;
-                    continue;
-                }
+            for (int j = 0; j < kOct; ++j)
+                if (!(ok >> j & 1)) z[j] = minus_inf();
+        }
+        if (out) {
+            // z / temperature, but for one more rounding: a division costs as much as the rest
+            if (full && out_vec) {
+                alignas(16) T t[kOct];
+#pragma unroll
+                for (int j = 0; j < kOct; ++j) t[j] = from_float<T>(z[j] * cool);
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(T) / 2; ++i) __stcs((uint4 *)(out + o) + i, ((const uint4 *)t)[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kOct; ++j)
+                    if (there >> j & 1) out[o + j] = from_float<T>(z[j] * cool);
             }
-            if constexpr (PICK == kSample) {
-                uint4 r0, r1;
-                philox_two((uint64_t)(e0 + v0) >> 2, step, keys, r0, r1);
-                const uint32_t w[kOct] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-                // z + noise is at most this
-                float high[kOct];
+        }
+        if constexpr (PICK != kNone) {
+            if (!noisy) {
+                // dividing by a temperature keeps the order, but may make equal what was not
+                float top = minus_inf();
+                int at = 0;
 #pragma unroll
                 for (int j = 0; j < kOct; ++j) {
-                    const float u = __uint_as_float(0x3f800000u | w[j] >> 9) - 1.f;  // u or less
-                    const float s = fmaf(__log2f(u), -0.6931472f, z[j]);
-                    high[j] = there >> j & 1 ? fmaf(fabsf(s), 1e-6f, s) + 1e-4f : minus_inf();
+                    const float s = heat && row.temp != 1.f ? z[j] / row.temp : z[j];
+                    if (s > top) top = s, at = j;  // of equal ones the first; no NaN
                 }
-                for (;;) {
-                    float top = minus_inf();
-                    int at = -1;
+                const unsigned long long k = pick_key(top, (uint32_t)(v0 + o + at));
+                best = k > best ? k : best;
+                continue;
+            }
+        }
+        if constexpr (PICK == kSample) {
+            uint4 r0, r1;
+            philox_two((uint64_t)(e0 + v0 + o) >> 2, step, keys, r0, r1);
+            const uint32_t w[kOct] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+            // a score is at most this (z / temperature as a product: its error is in the margin)
+            float high[kOct], top = minus_inf();
 #pragma unroll
-                    for (int j = 0; j < kOct; ++j)
-                        if (high[j] > top) top = high[j], at = j;
-                    const bool may = at >= 0 && top >= floor;
-                    if (!__any_sync(~0u, may)) break;
-                    unsigned long long k = 0;
-                    if (may) {
-                        const int64_t v = v0 + at;
-                        const uint32_t c = len > 0 ? count[cut + (v - t0)] : 0u;
-                        const uint32_t word = at < 4 ? (at < 2 ? (at ? r0.y : r0.x) : (at < 3 ? r0.z : r0.w))
-                                                     : (at < 6 ? (at < 5 ? r1.x : r1.y) : (at < 7 ? r1.z : r1.w));
-                        // in place, the logit may be overwritten: z is then what is returned, in full
-                        float zv = 0.f;
-                        if (row.out) {
+            for (int j = 0; j < kOct; ++j) {
+                const float u = __uint_as_float(0x3f800000u | w[j] >> 9) - 1.f;  // u or less
+                const float s = fmaf(z[j], cool, log2_fast(u) * -0.6931472f);
+                high[j] = fmaf(fabsf(s), 1e-6f, s + 1e-4f);
+                top = fmaxf(top, high[j]);
+            }
+            const uint32_t seen = *(volatile uint32_t *)&floor_key;
+            float floor = key_score((unsigned long long)seen << 32);
+            if (!__any_sync(~0u, top >= floor && top > minus_inf())) continue;
+            // A score that a lane's likeliest token has at least: with t >= u,
+            // -log1p(-u) <= t / (1 - t).
+            int at = -1;
+            float low = minus_inf(), z_at = 0.f;
+            uint32_t word = 0;
 #pragma unroll
-                            for (int j = 0; j < kOct; ++j)
-                                if (j == at) zv = z[j];
-                        } else {
-                            zv = row.at(v, c);
-                        }
-                        k = pick_key(__fadd_rn(zv, gumbel(word)), (uint32_t)v);
-                        best = k > best ? k : best;
+            for (int j = 0; j < kOct; ++j)
+                if (high[j] == top) at = j, z_at = z[j], word = w[j];
+            if (top > minus_inf()) {
+                const float t = __uint_as_float(0x3f800000u | word >> 9) - (1.f - 2.384185791015625e-07f);
+                const float s = fmaf(z_at, cool, -0.6931472f * (log2_fast(t) - log2_fast(1.f - t)));
+                if (t < 0.5f) low = s - fmaf(fabsf(s), 1e-6f, 1e-4f);
+            }
+            // (an unsigned word in the order of floats, as pick_key's upper one)
+            const uint32_t warp_key = __reduce_max_sync(~0u, (uint32_t)(pick_key(low, 0) >> 32));
+            if (warp_key > seen) {
+                if ((threadIdx.x & 31) == 0) atomicMax(&floor_key, warp_key);
+                floor = key_score((unsigned long long)warp_key << 32);
+            }
+            while (top >= floor && top > minus_inf()) {
+                // a token put off earlier, should it still be one to score, makes room
+                if (later_high >= floor && later_high > minus_inf()) score_later();
+                later_high = top;
+                later_o = o + at;
+                later_z = z_at;
+                later_word = word;
+                top = minus_inf();
+                const int old = at;
 #pragma unroll
-                        for (int j = 0; j < kOct; ++j)
-                            if (j == at) high[j] = minus_inf();
-                    }
-                    const uint32_t seen = __reduce_max_sync(~0u, (uint32_t)(k >> 32));
-                    floor = fmaxf(floor, key_score((unsigned long long)seen << 32));
+                for (int j = 0; j < kOct; ++j) {
+                    if (j == old) high[j] = minus_inf();
+                    if (high[j] > top) top = high[j], at = j, z_at = z[j], word = w[j];
                 }
             }
         }
     }
     if constexpr (PICK != kNone) {
+        __syncthreads();  // the floor is known
+        if (PICK == kSample && later_high > minus_inf() &&
+            later_high >= key_score((unsigned long long)floor_key << 32))
+            score_later();
         for (int o = 16; o; o >>= 1) {
             const unsigned long long k = __shfl_xor_sync(~0u, best, o);
             best = k > best ? k : best;
         }
         if ((threadIdx.x & 31) == 0 && best) atomicMax(&best_cta, best);
         __syncthreads();
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the first CTA has begun
-        if (threadIdx.x == 0) *cluster.map_shared_rank(&best_of[rank], 0) = best_cta;
-        cluster.sync();
-        if (rank == 0 && threadIdx.x == 0) {
-            for (int i = 0; i < ranks; ++i) best = best_of[i] > best ? best_of[i] : best;
-            a.tokens[b] = best ? (int64_t)(0xFFFFFFFFu - (uint32_t)best) : -1;
+        if (threadIdx.x == 0) {
+            if (plan.slices > 1)
+                keys_out[blockIdx.x] = best_cta;
+            else
+                a.tokens[b] = best_cta ? (int64_t)(0xFFFFFFFFu - (uint32_t)best_cta) : -1;
         }
     }
 }
 
+// The best of a row's slices, a warp for a row.
+__global__ void __launch_bounds__(128) k_pick(const unsigned long long *keys, int slices, int64_t B, int64_t *tokens) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t b = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+    if (b >= B) return;
+    unsigned long long best = 0;
+    for (int i = threadIdx.x & 31; i < slices; i += 32) best = keys[b * slices + i] > best ? keys[b * slices + i] : best;
+    for (int o = 16; o; o >>= 1) {
+        const unsigned long long k = __shfl_xor_sync(~0u, best, o);
+        best = k > best ? k : best;
+    }
+    if ((threadIdx.x & 31) == 0) tokens[b] = best ? (int64_t)(0xFFFFFFFFu - (uint32_t)best) : -1;
+}
+
+// Slices of a row: as many CTAs as the device holds at once, or a whole number of
+// times that, of kTile tokens at most.  A CTA reads all of its row's history, so
+// a slice is no smaller than a quarter of that; nor than 1,024 tokens.  Up to 8,192
+// tokens a row stays whole where one is picked: a second kernel costs more.
+LogitPlan logit_plan(int64_t B, int64_t V, int64_t L, bool pick, int sms) {
+    const int64_t slots = (int64_t)sms * kLogitCtas;
+    const int64_t waves = (B * V + kTile * slots - 1) / (kTile * slots);
+    int64_t slices = waves * slots / (B > 0 ? B : 1);
+    int64_t least = L / 4 > 1024 ? L / 4 : 1024;
+    if (least > kTile) least = kTile;
+    if (slices > (V + least - 1) / least) slices = (V + least - 1) / least;
+    if (slices < (V + kTile - 1) / kTile) slices = (V + kTile - 1) / kTile;
+    if (pick && V <= kTile) slices = 1;
+    const int64_t slice = ((V + slices - 1) / slices + 127) / 128 * 128;
+    return LogitPlan{slice, (int)((V + slice - 1) / slice)};
+}
+
 template <typename T, int PICK>
-cudaError_t launch_logits(const ck_logit_call &a, const PhiloxKeys &keys, int ranks, size_t smem,
+cudaError_t launch_logits(const ck_logit_call &a, const PhiloxKeys &keys, const LogitPlan &plan,
                           cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(k_logits<T, PICK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (kTile + 2 * kOct) * (int)sizeof(uint32_t));
-    if (e != cudaSuccess) return e;
+    const size_t smem =
+        a.history ? (size_t)((plan.slice < kTile ? plan.slice : kTile) + 2 * kOct) * sizeof(uint32_t) : 0;
+    k_logits<T, PICK><<<(unsigned)(a.B * plan.slices), kLogitThreads, smem, stream>>>(
+        a, keys, plan, (unsigned long long *)a.workspace);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || PICK == kNone || plan.slices == 1) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ranks, (unsigned)a.B);
-    cfg.blockDim = dim3(kLogitThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)((a.B + 3) / 4));
+    cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)ranks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_logits<T, PICK>, a, keys);
+    return cudaLaunchKernelEx(&cfg, k_pick, (const unsigned long long *)a.workspace, plan.slices, a.B, a.tokens);
 }
 
 }  // namespace
@@ -345,21 +406,29 @@ extern "C" ck_status ck_control_logits(const ck_logit_call *call, void *stream) 
     if (!a.logits || (!a.out && !a.tokens)) return fail(CK_ERR_INVALID_ARG, "a required pointer is NULL");
     if (a.history && ((a.history_bits != 32 && a.history_bits != 64) || a.L < 0 || a.L >= ((int64_t)1 << 30)))
         return fail(CK_ERR_INVALID_ARG, "control_logits: history of 32 or 64 bits, 0 <= L < 2^30");
-    // A CTA for 4,096 tokens of a row, for 1,024 where rows are few; eight at most
-    // make a cluster everywhere.
-    const int64_t few = a.B * 8 < 4 * (int64_t)device_sms() ? 1024 : 4096;
-    int ranks = 1;
-    while (ranks < 8 && ranks * few < a.V) ranks *= 2;
-    const int64_t per = ((a.V + ranks - 1) / ranks + 127) / 128 * 128;
-    const size_t smem = a.history ? (size_t)((per < kTile ? per : kTile) + 2 * kOct) * sizeof(uint32_t) : 0;
+    const LogitPlan plan = logit_plan(a.B, a.V, a.history ? a.L : 0, a.tokens != nullptr, device_sms());
+    if (a.B * (int64_t)plan.slices >= ((int64_t)1 << 31))
+        return fail(CK_ERR_UNSUPPORTED, "control_logits: B V is too large");
+    if (a.tokens && plan.slices > 1 &&
+        (!a.workspace || ((uintptr_t)a.workspace & 7) != 0 || a.workspace_bytes < a.B * plan.slices * 8))
+        return fail(CK_ERR_WORKSPACE, "control_logits: workspace of %lld bytes (%lld needed, 8-byte aligned)",
+                    (long long)(a.workspace ? a.workspace_bytes : 0), (long long)(a.B * plan.slices * 8));
     const PhiloxKeys keys = PhiloxKeys::of(a.seed, a.step, a.step_dev);
     cudaError_t e = cudaSuccess;
     with_dtype(a.dtype, [&](auto *tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
         cudaStream_t s = (cudaStream_t)stream;
-        e = !a.tokens  ? launch_logits<T, kNone>(a, keys, ranks, smem, s)
-            : a.sample ? launch_logits<T, kSample>(a, keys, ranks, smem, s)
-                       : launch_logits<T, kGreedy>(a, keys, ranks, smem, s);
+        e = !a.tokens  ? launch_logits<T, kNone>(a, keys, plan, s)
+            : a.sample ? launch_logits<T, kSample>(a, keys, plan, s)
+                       : launch_logits<T, kGreedy>(a, keys, plan, s);
     });
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "k_logits launch");
+}
+
+extern "C" ck_status ck_logits_workspace_size(int64_t B, int64_t V, int64_t L, size_t *bytes) {
+    if (B < 0 || V < 1 || L < 0 || !bytes)
+        return fail(CK_ERR_INVALID_ARG, "logits_workspace_size: B, L >= 0, V >= 1, bytes not NULL");
+    const LogitPlan plan = logit_plan(B, V, L, true, device_sms());
+    *bytes = plan.slices > 1 ? (size_t)B * plan.slices * 8 : 0;
+    return CK_OK;
 }

@@ -200,6 +200,9 @@ def _per_token(name, t, dtype, B, n, device):
     return t.data_ptr(), strides[0] if len(shape) == 2 else 0
 
 
+_logits_ws = {}  # workspace bytes by (device, B, V, L): sizes only, no memory
+
+
 def _control(logits, history, history_len, prompt_len, repetition, frequency, presence, bias, mask,
              temperature, out, tokens, seed, step):
     dtype, dev = _ck.DTYPES.get(logits.dtype), logits.get_device()
@@ -235,12 +238,24 @@ def _control(logits, history, history_len, prompt_len, repetition, frequency, pr
     at = step_dev = None
     if seed is not None:
         at, step_dev = _ck._step_args(step, dev)
+    ws = need = None
+    if tokens is not None and V > 1024:
+        key = (dev, B, V, L)
+        need = _logits_ws.get(key)
+        if need is None:
+            if len(_logits_ws) > 4096:
+                _logits_ws.clear()
+            with torch.cuda.device(dev):
+                need = _logits_ws[key] = _ck.ck_logits_workspace_size(B, V, L)
+        if need:
+            ws = tokens.new_empty(need // 8)
     call = _ck.LogitCall(
         logits.data_ptr(), dtype, B, V, _ck._rows(logits, "logits"), text, text_len, prompt, bits, L,
         text_stride, rep, freq, pres, temp, rep_all, freq_all, pres_all, temp_all, bias_at,
         bias_stride, mask_at, mask_stride, out_at, out_stride,
         None if tokens is None else tokens.data_ptr(), 0 if seed is None else 1,
-        0 if seed is None else int(seed) & _ck._U64, at or 0, step_dev)
+        0 if seed is None else int(seed) & _ck._U64, at or 0, step_dev,
+        None if ws is None else ws.data_ptr(), need or 0)
     if _here(dev):
         _ck.ck_control_logits(call)
     else:
