@@ -1,25 +1,9 @@
 // ck_int4_matvec and ck_int4_quantize: products of a few state rows with 4-bit
 // weights, and the rounding that makes such weights.
-#include "ck_types.h"
+#include "int4.h"
 
 namespace ck {
 namespace {
-
-struct MatvecArgs {
-    const void *x;
-    int64_t dtype, M, K, x_stride;
-    const uint8_t *q;
-    int64_t V, q_pitch;
-    const void *scales;
-    int scale_dtype;
-    int64_t s_stride;
-    const uint8_t *zeros;
-    int64_t z_stride;
-    const float *bias;
-    void *y;
-    int64_t y_stride;
-    float *partial;  // slots of sums that cross CTAs or slabs
-};
 
 // The product of a few rows, on tensor cores.  With w = s (q - z) a group's sum is
 // s * sum (q - z) x, and q - z, a whole number of at most 15 in magnitude, is exact
@@ -43,30 +27,7 @@ struct MatvecArgs {
 // k_join adds up in a fixed order.
 constexpr int kWarpsMv = 12;                // warps of a CTA, one CTA on an SM
 constexpr int kStages = 3;                  // ring of units per warp
-constexpr int kTileRows = 32;
-constexpr int kChunk = 256;                 // columns of a unit
 constexpr int kHalf = 128;                  // scales are taken up for half a unit
-constexpr int kUnitBytes = kTileRows * kChunk / 2;
-constexpr size_t kSmemMost = 232448;
-
-// a / b, in 32 bits where that does: a 64-bit division costs ten times as much
-__host__ __device__ inline int64_t quotient(int64_t a, int64_t b) {
-    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
-// n things dealt to `to` owners in runs that differ by one at most
-struct Deal {
-    int64_t each, more;
-    static __host__ __device__ Deal of(int64_t n, int64_t to) {
-        const int64_t q = quotient(n, to);
-        return Deal{q, n - q * to};
-    }
-    __host__ __device__ int64_t first(int64_t owner) const { return owner * each + (owner < more ? owner : more); }
-    __host__ __device__ int64_t owner(int64_t i) const {
-        const int64_t big = more * (each + 1);
-        return i < big ? quotient(i, each + 1) : more + quotient(i - big, each);
-    }
-};
 
 struct MatvecPlan {
     int rows;          // rows of x in this launch
@@ -93,8 +54,6 @@ struct MatvecPlan {
     }
 };
 
-__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
 // Weights and x in bf16 (for 32-bit and bf16 x) or fp16.
 template <bool HALF, bool FIRST>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -111,68 +70,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
             "{%10,%11,%12,%13};"
             : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-
-// q - z of a word's eight nibbles, as pairs (0, 4), (1, 5), (2, 6), (3, 7), times
-// 2^-6 (bf16) or 2^-9 (fp16).  Alone in the low bits of a bf16 a nibble is the
-// number q 2^-133, in the next place 16 q 2^-133 (fp16: 2^-24), exactly: so an AND
-// and a multiply-add, whose factor evens out the places, give the exact difference,
-// and of the four pairs two cost a shift.
-template <bool HALF> struct Nibble {
-    static constexpr uint32_t kLow = HALF ? 0x78007800u : 0x7f007f00u;   // 2^15, 2^127
-    static constexpr uint32_t kHigh = HALF ? 0x68006800u : 0x7d007d00u;  // 2^11, 2^123
-    static constexpr float kBack = HALF ? 512.f : 64.f;
-    static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
-        uint32_t r;
-        if constexpr (HALF)
-            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-        else
-            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-        return r;
-    }
-    // -z, likewise, of byte i of four packed zero points
-    static __device__ __forceinline__ uint32_t minus(uint32_t packed, int i) {
-        return fma(__byte_perm(packed, 0u, 0x4040u | i | i << 8), kLow ^ 0x80008000u, 0u);
-    }
-    static __device__ __forceinline__ void pairs(uint32_t w, uint32_t z, uint32_t (&v)[4]) {
-        const uint32_t w8 = w >> 8;
-        v[0] = fma(w & 0x000f000fu, kLow, z);
-        v[1] = fma(w & 0x00f000f0u, kHigh, z);
-        v[2] = fma(w8 & 0x000f000fu, kLow, z);
-        v[3] = fma(w8 & 0x00f000f0u, kHigh, z);
-    }
-};
-
-// Three bf16 parts of a 32-bit float: each takes the top eight bits of what is
-// left.  Cutting keeps the first part of a large number finite; what is not finite
-// goes whole into the first part.
-__device__ __forceinline__ void split3(float v, uint16_t (&part)[3]) {
-    const uint32_t b = __float_as_uint(v);
-    const bool odd = (b & 0x7f800000u) == 0x7f800000u;
-    const uint32_t nan = (b & 0x007fffffu) && odd ? 0x00400000u : 0u;  // NaN stays NaN when cut
-    const uint32_t h = (b | nan) & 0xffff0000u;
-    const float r = odd ? 0.f : v - __uint_as_float(h);
-    const uint32_t m = __float_as_uint(r) & 0xffff0000u;
-    const float l = r - __uint_as_float(m);
-    part[0] = (uint16_t)(h >> 16);
-    part[1] = (uint16_t)(m >> 16);
-    part[2] = (uint16_t)(__float_as_uint(l) >> 16);
-}
-
-// Eight numbers of a row of x from column k on, zeros past K.
-template <typename T>
-__device__ __forceinline__ void load8(const MatvecArgs &a, int64_t m, int64_t k, T (&v)[8]) {
-    const T *src = (const T *)a.x + m * a.x_stride + k;
-    if (k + 8 <= a.K && ((uintptr_t)src & 15) == 0) {
-        constexpr int kVec = (int)sizeof(T) / 2;
-        uint4 t[kVec];
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) t[i] = ((const uint4 *)src)[i];
-        memcpy(v, t, sizeof(t));
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = k + e < a.K ? src[e] : from_float<T>(0.f);
-    }
 }
 
 // The tensor-core column of part `part` of row m: the parts of two rows of 32-bit
@@ -226,120 +123,6 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, const MatvecPlan &p
             }
         }
     }
-}
-
-// What a warp copies next: its lanes' place in the weights, moved on by a chunk
-// at a time.  A unit is eight 16-byte pieces of 32 lines of 128 bytes; the pieces
-// of line r lie exchanged by r, so that a piece of eight lines is read without a
-// conflict.
-struct Copier {
-    const uint8_t *src;     // the lane's piece in line lane / 8
-    int tile, chunk;
-    __device__ __forceinline__ void seek(const MatvecArgs &a, int tile_, int chunk_) {
-        const int lane = threadIdx.x & 31;
-        tile = tile_;
-        chunk = chunk_;
-        src = a.q + (int64_t)(tile * kTileRows + (lane >> 3)) * a.q_pitch + chunk * (kChunk / 2) + (lane & 7) * 16;
-    }
-    __device__ __forceinline__ void copy(const MatvecArgs &a, uint32_t dst) const {
-        const int lane = threadIdx.x & 31;
-        // lines 4 i + lane / 8: their low three bits are lane / 8, and 4 for odd i
-        const uint32_t at = dst + (lane >> 3) * 128, p0 = ((lane & 7) ^ (lane >> 3)) << 4, p1 = p0 ^ 64;
-        if ((tile + 1) * kTileRows <= (int)a.V && (chunk + 1) * kChunk <= (int)a.K) {
-            const uint8_t *s = src;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + (i & 1 ? p1 : p0) + i * 512),
-                             "l"(s));
-                s += 4 * a.q_pitch;
-            }
-            return;
-        }
-        // bytes past a row's end and rows past V become zeros
-        const int from = chunk * (kChunk / 2) + (lane & 7) * 16, row_bytes = (int)((a.K + 1) / 2);
-        const int n = row_bytes - from >= 16 ? 16 : row_bytes > from ? row_bytes - from : 0;
-        for (int i = 0; i < 8; ++i) {
-            const int m = tile * kTileRows + 4 * i + (lane >> 3) < (int)a.V ? n : 0;
-            const uint8_t *s = m ? src + 4 * i * a.q_pitch : a.q;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + (i & 1 ? p1 : p0) + i * 512),
-                         "l"(s), "r"(m));
-        }
-    }
-    __device__ __forceinline__ void next(const MatvecArgs &a, int first, int end) {
-        if (++chunk == end)
-            seek(a, tile + 1, first);
-        else
-            src += kChunk / 2;
-    }
-};
-
-__device__ __forceinline__ float scale_value(uint32_t raw, int dtype) {
-    if (dtype == CK_F32) return __uint_as_float(raw);
-    if (dtype == CK_BF16) return __uint_as_float(raw << 16);
-    return __half2float(__ushort_as_half((unsigned short)raw));
-}
-
-// Scales and zero points, read eight groups of a tile's 32 rows at a time: lane l
-// of load i takes group l % 8 of row 4 i + l / 8, so that a load touches four rows'
-// sectors and not 32.  Kept as they come from memory until the groups are begun (a
-// conversion would wait for the loads), then left in shared memory as [row][8].
-template <int GROUP> struct ScaleReader {
-    static constexpr int kUnits = 8 * GROUP / kChunk;  // units of eight groups
-    uint32_t s[8], z[8];
-    int tile, eight;  // what s and z hold
-    __device__ __forceinline__ void load(const MatvecArgs &a, int tile_, int eight_, int groups) {
-        tile = tile_;
-        eight = eight_;
-        const int lane = threadIdx.x & 31, g = 8 * eight + (lane & 7), v = tile * kTileRows + (lane >> 3);
-        const int rows = g < groups ? (int)a.V - v : 0;  // row 4 i is there if 4 i < rows
-        if (a.scale_dtype == CK_F32) {
-            const uint32_t *p = (const uint32_t *)a.scales + v * a.s_stride + g;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = 4 * i < rows ? p[4 * i * a.s_stride] : 0u;
-        } else {
-            const uint16_t *p = (const uint16_t *)a.scales + v * a.s_stride + g;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = 4 * i < rows ? p[4 * i * a.s_stride] : 0u;
-        }
-        if (a.zeros) {
-            const uint8_t *p = a.zeros + v * a.z_stride + g;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = 4 * i < rows ? p[4 * i * a.z_stride] : 8u;
-        }
-    }
-    // A line of each row towards L2, a row to a lane, once for each 128 bytes: a load a
-    // unit ahead alone waits for memory.
-    static __device__ __forceinline__ void ahead(const MatvecArgs &a, int tile, int eight, int groups, bool start) {
-        const int v = tile * kTileRows + (threadIdx.x & 31), g = 8 * eight;
-        if (v >= (int)a.V || g >= groups) return;
-        const int size = a.scale_dtype == CK_F32 ? 4 : 2;
-        const char *p = (const char *)a.scales + (v * a.s_stride + g) * size;
-        if (start || ((uintptr_t)p & 127) < 8 * size) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-        if (a.zeros) {
-            const uint8_t *q = a.zeros + v * a.z_stride + g;
-            if (start || ((uintptr_t)q & 127) < 8) asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
-        }
-    }
-    __device__ __forceinline__ void leave(const MatvecArgs &a, float *scales, uint8_t *zeros) const {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            scales[32 * i + lane] = scale_value(s[i], a.scale_dtype);
-            zeros[32 * i + lane] = a.zeros ? (uint8_t)(z[i] & 15) : (uint8_t)8;
-        }
-    }
-};
-
-
-__device__ __forceinline__ void store_y(const MatvecArgs &a, int64_t m, int64_t v, float sum) {
-    sum += a.bias ? a.bias[v] : 0.f;
-    const int64_t at = m * a.y_stride + v;
-    if (a.dtype == CK_F32)
-        ((float *)a.y)[at] = sum;
-    else if (a.dtype == CK_BF16)
-        ((__nv_bfloat16 *)a.y)[at] = __float2bfloat16_rn(sum);
-    else
-        ((__half *)a.y)[at] = __float2half_rn(sum);
 }
 
 template <bool HALF, int GROUP, int NT>
@@ -406,8 +189,8 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
             asm volatile("cp.async.commit_group;");
         };
         for (int i = 0; i < kStages - 1; ++i) copy_next();
-        ScaleReader<GROUP> next;
-        constexpr int kUnits = ScaleReader<GROUP>::kUnits, kAhead = 4;
+        ScaleReader<8> next;
+        constexpr int kUnits = 8 * GROUP / kChunk, kAhead = 4;  // units of eight groups
         if (n > 0) next.load(a, t, (first + c) / kUnits, groups);
         bool begin = true;  // the next unit is the first of its eight groups here
         if (lane < 2) part_tile[2 * warp + lane] = -1;
@@ -432,7 +215,7 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
                 next.load(a, t1, e1, groups);  // past the last tile: nothing
                 int t2 = t1, e2 = e1 + kAhead;
                 if (e2 * kUnits >= first + sc) ++t2, e2 += first / kUnits - (first + sc + kUnits - 1) / kUnits;
-                ScaleReader<GROUP>::ahead(a, t2, e2, groups, e2 == first / kUnits);
+                ScaleReader<8>::ahead(a, t2, e2, groups, e2 == first / kUnits);
                 __syncwarp();
             }
             const int in_eight = (first + c) & (kUnits - 1);
@@ -631,6 +414,11 @@ __global__ void __launch_bounds__(128) k_join(MatvecArgs a, MatvecPlan p) {
 // Rows of x in one launch: what two tensor-core tiles of eight columns hold.
 int rows_at_once(int64_t dtype) { return dtype == CK_F32 ? 4 : 16; }
 
+// Rows of the next pass of `left`: k_wide's most, or what is left of them.
+int64_t rows_of_pass(int64_t dtype, int64_t left) {
+    return left < wide_rows(dtype) ? left : wide_rows(dtype);
+}
+
 MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms) {
     MatvecPlan p{};
     p.rows = (int)rows;
@@ -799,14 +587,19 @@ extern "C" ck_status ck_int4_matvec(const void *x, int64_t dtype, int64_t M, int
                     workspace_bytes, need);
     const int sms = device_sms();
     cudaError_t e = cudaSuccess;
-    for (int64_t m = 0; m < M && e == cudaSuccess; m += rows_at_once(dtype)) {
-        const int64_t rows = M - m < rows_at_once(dtype) ? M - m : rows_at_once(dtype);
+    for (int64_t m = 0; m < M && e == cudaSuccess;) {
+        const int64_t rows = rows_of_pass(dtype, M - m);
         const size_t el = dtype_size(dtype);
         MatvecArgs a{(const char *)x + m * x_stride * el, dtype, rows, K, x_stride, qweight, V, q_pitch,
                      scales, (int)scale_dtype, s_stride, zeros, z_stride, bias,
                      (char *)y + m * y_stride * el, y_stride, (float *)workspace};
-        const MatvecPlan p = matvec_plan(dtype, rows, K, V, sms);
         cudaStream_t st = (cudaStream_t)stream;
+        m += rows;
+        if (rows > rows_at_once(dtype)) {
+            e = launch_wide(a, group, workspace, sms, st);
+            continue;
+        }
+        const MatvecPlan p = matvec_plan(dtype, rows, K, V, sms);
         e = group == 32 ? launch_group<32>(a, p, st) : group == 64 ? launch_group<64>(a, p, st)
                                                                   : launch_group<128>(a, p, st);
     }
@@ -821,11 +614,13 @@ extern "C" ck_status ck_int4_workspace_size(int64_t dtype, int64_t M, int64_t K,
     *bytes = 0;
     if (M == 0 || V == 0) return CK_OK;
     const int sms = device_sms();
-    const int64_t most = rows_at_once(dtype), tail = M % most;
-    if (M >= most) *bytes = partial_bytes(matvec_plan(dtype, most, K, V, sms));
-    if (tail) {
-        const size_t b = partial_bytes(matvec_plan(dtype, tail, K, V, sms));
+    // passes of the most rows, then smaller ones
+    for (int64_t m = 0; m < M;) {
+        const int64_t rows = rows_of_pass(dtype, M - m);
+        const size_t b = rows > rows_at_once(dtype) ? wide_workspace(dtype, rows, K, V, sms)
+                                                    : partial_bytes(matvec_plan(dtype, rows, K, V, sms));
         if (b > *bytes) *bytes = b;
+        m += rows == wide_rows(dtype) ? (M - m) / rows * rows : rows;
     }
     return CK_OK;
 }

@@ -1,0 +1,501 @@
+// The product with 4-bit weights for more columns of x than k_matvec takes at a
+// time: 32-bit states in batches of tens are three columns each.
+//
+// The mathematics is k_matvec's: exact weights q - z in 16-bit floats, x in bf16 parts,
+// 32-bit sums, the scale once a group.  But with n columns a weight costs n multiply-
+// adds, which the warps' own matrix instructions do at a quarter of the tensor cores'
+// rate (96 columns: 51 us of them for 32,000 x 5,000 weights that memory delivers in
+// 13), so here the products are tcgen05.mma's: 128 rows of weights by n columns, 16
+// of K at a time, A in tensor memory, where the warps that unpack it put it by row, B
+// from shared memory, sums in tensor memory.  A CTA takes 256 rows, two such products
+// that share B, and a run of K:
+//
+//   warps 0-7   a weight row a lane.  Each warp's weights come through a ring of
+//               asynchronous copies of its own; 64 columns of K are unpacked into one of
+//               two buffers of tensor memory, then the sums of the groups that were
+//               finished meanwhile are fetched, scaled and added up in registers
+//   warp 8      one thread waits for A and B, issues the products, and keeps x
+//               coming, tiles of 64 of K that k_images has laid out as the products read
+//               them, so that each is one bulk copy
+//
+// Tensor memory: sums of two groups for each half (4 x n columns), A twice for each
+// (4 x 32).  Every wait is bounded: one that gives up makes all others give up, and the
+// CTA's outputs NaN.
+#include "int4.h"
+
+namespace ck {
+namespace {
+
+constexpr int kWideRows = 256;
+constexpr int kWorkers = 8, kWideThreads = (kWorkers + 1) * 32;
+constexpr int kRing = 3;          // units of a warp's ring
+constexpr int kImages = 4;        // tiles of x in shared memory
+constexpr int kStep = 64;         // columns of K of a tile of x, and of a buffer of A
+constexpr int kMostColumns = 96;  // of tensor memory's 512, 4 x 96 and 4 x 32
+constexpr int kPitch = 9;         // of scales in shared memory: a bank a row
+
+struct WidePlan {
+    int rows, parts, cols, n;  // rows of x, parts of each, columns, columns padded to 32, 64 or 96
+    int64_t blocks;            // of 256 rows of V
+    int64_t chunks, steps;     // of 256 and of 64 columns of K
+    int64_t splits;            // runs of K
+    Deal chunk;                // chunks to runs
+    size_t images;             // bytes of x's tiles
+    size_t smem;
+    long long timeout_ns;
+    int extra;                 // test hook: arrivals that never come
+};
+
+// Bounded wait on a shared-memory barrier's phase.
+struct Waiter {
+    volatile int *dead;
+    long long limit;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t phase) const {
+        unsigned long long began = 0;
+        for (int i = 0;; ++i) {
+            uint32_t done;
+            asm volatile(
+                "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                : "=r"(done) : "r"(bar), "r"(phase) : "memory");
+            if (done) return true;
+            if ((i & 15) == 15) {
+                if (*dead) return false;
+                unsigned long long now;
+                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+                if (began == 0) began = now;
+                if ((long long)(now - began) > limit) {
+                    *dead = 1;
+                    return false;
+                }
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// the barrier is arrived at when all products issued so far are done
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// x as tiles of n columns by 64 of K: 128 bytes a column, whose eight 16-byte pieces
+// are exchanged by the column (the 128-byte swizzle that the products read), eight
+// columns of K to a piece in the order 0 4 1 5 2 6 3 7 in which nibbles come out of a
+// word.
+template <typename T> __global__ void __launch_bounds__(256) k_images(MatvecArgs a, WidePlan p, char *images) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, pieces = p.steps * 8;
+    const int64_t m = quotient(i, pieces), j = i - m * pieces;
+    if (m >= p.rows + (p.n - p.cols)) return;
+    char *tile = images + (j >> 3) * (p.n * 128);
+    auto place = [&](int col) { return (uint4 *)(tile + col * 128 + (((int)(j & 7) ^ (col & 7)) << 4)); };
+    if (m >= p.rows) {  // a spare column
+        *place(p.cols + (int)(m - p.rows)) = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    T v[8];
+    load8<T>(a, m, 8 * j, v);
+    constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+    uint16_t part[8][3];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (sizeof(T) == 4)
+            split3(v[e], part[e]);
+        else
+            memcpy(&part[e][0], &v[e], 2);
+    }
+#pragma unroll
+    for (int s = 0; s < kParts; ++s) {
+        uint4 w;
+        w.x = part[0][s] | (uint32_t)part[4][s] << 16;
+        w.y = part[1][s] | (uint32_t)part[5][s] << 16;
+        w.z = part[2][s] | (uint32_t)part[6][s] << 16;
+        w.w = part[3][s] | (uint32_t)part[7][s] << 16;
+        *place(kParts * (int)m + s) = w;
+    }
+}
+
+template <bool HALF, int GROUP, int N>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    k_wide(const __grid_constant__ MatvecArgs a, const __grid_constant__ WidePlan p, const char *images, float *partial) {
+    extern __shared__ __align__(1024) char smem[];
+    __shared__ __align__(8) uint64_t bars[2 * kImages + 9];
+    __shared__ uint32_t tmem_base;
+    __shared__ int dead;
+    char *ring = smem + kImages * N * 128;
+    float *all_scales = (float *)(ring + kWorkers * kRing * kUnitBytes);
+    uint8_t *all_zeros = (uint8_t *)(all_scales + kWorkers * kTileRows * kPitch);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t bar0 = smem_at(bars);
+    auto b_full = [&](int i) { return bar0 + 8 * i; };
+    auto b_empty = [&](int i) { return bar0 + 8 * (kImages + i); };
+    auto a_full = [&](int i) { return bar0 + 8 * (2 * kImages + i); };
+    auto a_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 2 + i); };
+    auto d_full = [&](int i) { return bar0 + 8 * (2 * kImages + 4 + i); };
+    auto d_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 6 + i); };
+    const uint32_t idle = bar0 + 8 * (2 * kImages + 8);
+    const Waiter wait{&dead, p.timeout_ns};
+
+    const int64_t split = quotient(blockIdx.x, p.blocks), block = blockIdx.x - split * p.blocks;
+    const int c0 = (int)p.chunk.first(split), c1 = (int)p.chunk.first(split + 1);
+    const int step0 = c0 * (kChunk / kStep), steps = min(c1 * (kChunk / kStep), (int)p.steps) - step0;
+    const bool second = block * kWideRows + 128 < a.V;  // rows in the second half
+
+    if (threadIdx.x == 0) {
+        dead = 0;
+        for (int i = 0; i < kImages; ++i) {
+            barrier_init(b_full(i), 1);
+            barrier_init(b_empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            barrier_init(a_full(i), kWorkers + p.extra);
+            barrier_init(a_empty(i), 1);
+            barrier_init(d_full(i), 1);
+            barrier_init(d_empty(i), kWorkers);
+        }
+        barrier_init(idle, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kWorkers) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_at(&tmem_base))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *(volatile uint32_t *)&tmem_base;
+    auto d_at = [&](int half, int buf) { return tmem + (2 * half + buf) * N; };
+    auto a_at = [&](int half, int buf) { return tmem + 4 * kMostColumns + (2 * half + buf) * (kStep / 2); };
+
+    if (warp == kWorkers) {
+        if (lane == 0) {
+            asm volatile("griddepcontrol.launch_dependents;");
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // k_images is done
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            constexpr uint32_t kTile = N * 128;
+            auto fetch = [&](int i) {
+                const uint32_t bar = b_full(i % kImages);
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kTile) : "memory");
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                        smem_at(smem) + (i % kImages) * kTile),
+                    "l"(images + (int64_t)(step0 + i) * kTile), "r"(kTile), "r"(bar)
+                    : "memory");
+            };
+            // D in 32-bit floats; A and B in fp16 (0) or bf16 (1), both along K; N / 8; 128 / 16 rows
+            constexpr uint32_t kType = HALF ? 0u : 1u;
+            constexpr uint32_t kInstr = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N / 8) << 17 | 8u << 24;
+            // of a tile in shared memory: 128-byte swizzle, 1,024 bytes from eight columns to the next
+            const uint64_t desc0 = (uint64_t)2 << 61 | (uint64_t)1 << 46 | (uint64_t)64 << 32 | (uint64_t)1 << 16;
+            int fetched = 0;
+            for (; fetched < kImages - 1 && fetched < steps; ++fetched) fetch(fetched);
+            bool ok = true;
+            int group = 0;
+            constexpr int kPerGroup = GROUP / 16;
+            for (int i = 0; i < steps && ok; ++i) {
+                const int slot = i % kImages;
+                ok = wait(b_full(slot), (uint32_t)(i / kImages) & 1) && wait(a_full(i & 1), (uint32_t)(i >> 1) & 1);
+                if (!ok) break;
+                fence_after();
+                const uint64_t desc = desc0 | (smem_at(smem) + slot * kTile) >> 4;
+#pragma unroll
+                for (int k = 0; k < kStep / 16; ++k) {
+                    const int at = (i * (kStep / 16) + k) % kPerGroup;  // of the group
+                    const int buf = group & 1;
+                    if (at == 0 && group >= 2 && ok) {
+                        ok = wait(d_empty(buf), (uint32_t)((group >> 1) - 1) & 1);
+                        fence_after();
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (half && !second) break;
+                        asm volatile(
+                            "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_at(half, buf)),
+                            "r"(a_at(half, i & 1) + k * 8), "l"(desc + 2 * k), "r"(kInstr), "r"((uint32_t)(at != 0))
+                            : "memory");
+                    }
+                    if (at == kPerGroup - 1 || (i == steps - 1 && k == kStep / 16 - 1)) {
+                        commit(d_full(buf));
+                        ++group;
+                    }
+                }
+                if (!ok) break;
+                commit(a_empty(i & 1));
+                commit(b_empty(slot));
+                if (fetched < steps) {
+                    // its slot was that of step fetched - kImages, whose products may still run
+                    if (fetched >= kImages) ok = wait(b_empty(fetched % kImages), (uint32_t)(fetched / kImages - 1) & 1);
+                    if (ok) fetch(fetched++);
+                }
+            }
+            // nothing is left on its way into shared memory, nor a product under way
+            volatile int none = 0;
+            const Waiter last_wait{&none, p.timeout_ns};
+            commit(idle);
+            last_wait(idle, 0);
+            for (int i = 0; i < kImages && !ok; ++i) {
+                const int last = fetched - 1 - (fetched - 1 - i + kImages) % kImages;  // last tile of slot i
+                if (last >= 0) last_wait(b_full(i), (uint32_t)(last / kImages) & 1);
+            }
+        }
+        __syncwarp();
+    } else {
+        constexpr int kUnits = 8 * GROUP / kChunk;      // units of eight groups
+        constexpr int kEnds = GROUP == 32 ? 2 : 1;      // groups that a step may end
+        const int t = (int)block * (kWideRows / kTileRows) + warp, groups = (int)((a.K + GROUP - 1) / GROUP);
+        const int half = warp >> 2;
+        const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // lanes 32 (warp % 4) on of tensor memory
+        const bool there = (int64_t)t * kTileRows < a.V;
+        const uint32_t my_ring = smem_at(ring) + warp * kRing * kUnitBytes;
+        const uint32_t my_line = lane * 128, my_swap = (lane & 7) << 4;
+        float *my_scales = all_scales + warp * kTileRows * kPitch;
+        uint8_t *my_zeros = all_zeros + warp * kTileRows * 8;
+        int left = there ? c1 - c0 : 0;
+        Copier from;
+        from.seek(a, t, c0);
+        uint32_t put = my_ring, get = my_ring;
+        auto copy_next = [&] {
+            if (left > 0) {
+                from.copy(a, put);
+                from.next(a, c0, 0x7fffffff);
+                --left;
+            }
+            put = put + kUnitBytes == my_ring + kRing * kUnitBytes ? my_ring : put + kUnitBytes;
+            asm volatile("cp.async.commit_group;");
+        };
+        for (int i = 0; i < kRing - 1; ++i) copy_next();
+        ScaleReader<kPitch> next;
+        next.load(a, t, c0 / kUnits, groups);
+        float acc[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.f;
+        bool ok = true;
+        int fetched = 0;  // groups whose sums have been fetched
+        // The sums of the next group, this lane's row, times its scale.
+        auto take = [&](float scale) {
+            const int buf = fetched & 1;
+            ok = __all_sync(~0u, ok && wait(d_full(buf), (uint32_t)(fetched >> 1) & 1));
+            if (!ok) return;
+            fence_after();
+            if (half == 0 || second) {
+#pragma unroll
+                for (int b = 0; b < N / 16; ++b) {
+                    uint32_t v[16];
+                    asm volatile(
+                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+                          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+                          "=r"(v[14]), "=r"(v[15])
+                        : "r"(d_at(half, buf) + quarter + 16 * b));
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[16 * b + i] = fmaf(scale, __uint_as_float(v[i]), acc[16 * b + i]);
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) barrier_arrive(d_empty(buf));
+            ++fetched;
+        };
+        float now[kEnds], before[kEnds];  // scales of the groups that this step and the last one end
+        int n_before = 0;
+        for (int c = c0; c < c1 && ok; ++c) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+            __syncwarp();
+            copy_next();
+            const int in_eight = c & (kUnits - 1);
+            if (c == c0 || in_eight == 0) {
+                next.leave(a, my_scales, my_zeros);
+                next.load(a, t, c / kUnits + 1, groups);
+                ScaleReader<kPitch>::ahead(a, t, c / kUnits + 5, groups, false);
+                __syncwarp();
+            }
+            const uint32_t line = get + my_line;
+            get = get + kUnitBytes == my_ring + kRing * kUnitBytes ? my_ring : get + kUnitBytes;
+#pragma unroll
+            for (int q = 0; q < kChunk / kStep; ++q) {
+                const int i = (c - c0) * (kChunk / kStep) + q;
+                if (i >= steps) break;
+                const int buf = i & 1;
+                if (i >= 2) {
+                    ok = __all_sync(~0u, ok && wait(a_empty(buf), (uint32_t)((i >> 1) - 1) & 1));
+                    if (!ok) break;
+                    fence_after();
+                }
+                uint32_t v[32];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // pieces of 32 columns
+                    const int piece = 2 * q + e, g = lane * 8 + in_eight * (kChunk / GROUP) + piece * 32 / GROUP;
+                    const uint32_t zero = Nibble<HALF>::minus(my_zeros[g], 0);
+                    uint4 w;
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                 : "r"(line + (my_swap ^ (piece << 4))));
+                    Nibble<HALF>::pairs(w.x, zero, *(uint32_t(*)[4])(v + 16 * e));
+                    Nibble<HALF>::pairs(w.y, zero, *(uint32_t(*)[4])(v + 16 * e + 4));
+                    Nibble<HALF>::pairs(w.z, zero, *(uint32_t(*)[4])(v + 16 * e + 8));
+                    Nibble<HALF>::pairs(w.w, zero, *(uint32_t(*)[4])(v + 16 * e + 12));
+                    if (GROUP == 32 || e == 1)
+                        now[GROUP == 32 ? e : 0] =
+                            my_scales[lane * kPitch + in_eight * (kChunk / GROUP) + piece * 32 / GROUP];
+                }
+                asm volatile(
+                    "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                    "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                    "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a_at(half, buf) + quarter),
+                    "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                    "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+                    "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+                    "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+                    : "memory");
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                fence_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(a_full(buf));
+#pragma unroll
+                for (int e = 0; e < kEnds; ++e)
+                    if (e < n_before && ok) take(before[e]);
+                if (!ok) break;
+                n_before = GROUP < 128 ? kEnds : ((i & 1) || i == steps - 1);
+#pragma unroll
+                for (int e = 0; e < kEnds; ++e) before[e] = now[e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kEnds; ++e)
+            if (e < n_before && ok) take(before[e]);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        const int64_t v = block * kWideRows + 32 * warp + lane;
+        const float back = ok ? Nibble<HALF>::kBack : __int_as_float(0x7fc00000);
+        if (v < a.V) {
+            auto put_y = [&](int m, float sum) {
+                if (p.splits > 1)
+                    partial[(split * p.rows + m) * a.V + v] = sum;
+                else
+                    store_y(a, m, v, sum);
+            };
+            if (p.parts == 3) {
+#pragma unroll
+                for (int m = 0; m < N / 3; ++m)
+                    if (m < p.rows) put_y(m, ((acc[3 * m + 2] + acc[3 * m + 1]) + acc[3 * m]) * back);
+            } else {
+#pragma unroll
+                for (int m = 0; m < N; ++m)
+                    if (m < p.rows) put_y(m, acc[m] * back);
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == kWorkers) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+// Sums over the runs of K, in their order.
+__global__ void __launch_bounds__(256) k_wide_join(MatvecArgs a, WidePlan p, const float *partial) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, n = p.rows * a.V;
+    if (i >= n) return;
+    float sum = 0.f;
+    for (int64_t s = 0; s < p.splits; ++s) sum += partial[s * n + i];
+    const int64_t m = quotient(i, a.V);
+    store_y(a, m, i - m * a.V, sum);
+}
+
+WidePlan wide_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms) {
+    WidePlan p{};
+    p.rows = (int)rows;
+    p.parts = dtype == CK_F32 ? 3 : 1;
+    p.cols = p.rows * p.parts;
+    p.n = (p.cols + 31) / 32 * 32;
+    p.blocks = (V + kWideRows - 1) / kWideRows;
+    p.chunks = (K + kChunk - 1) / kChunk;
+    p.steps = (K + kStep - 1) / kStep;
+    // Runs of K so that the CTAs fill the device evenly: a chunk takes a CTA about 1 us,
+    // its start and end 5 us, the sums of several runs 2 us and their memory traffic.
+    double best = 1e30;
+    for (int64_t s = 1; s <= p.chunks && s <= 64; ++s) {
+        const double waves = (double)((p.blocks * s + sms - 1) / sms), run = (double)((p.chunks + s - 1) / s);
+        const double cost = waves * (run + 5.0) + (s > 1 ? 2.0 + 2e-6 * (double)(s * rows * V) : 0.0);
+        if (cost < best) best = cost, p.splits = s;
+    }
+    p.chunk = Deal::of(p.chunks, p.splits);
+    p.images = (size_t)p.steps * p.n * 128;
+    p.smem = (size_t)kImages * p.n * 128 + kWorkers * (kRing * kUnitBytes + kTileRows * (4 * kPitch + 8));
+    return p;
+}
+
+template <bool HALF, int GROUP, int N>
+cudaError_t run(const MatvecArgs &a, const WidePlan &p, char *images, float *partial, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(k_wide<HALF, GROUP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)p.smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.blocks * p.splits));
+    cfg.blockDim = dim3(kWideThreads);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_wide<HALF, GROUP, N>, a, p, (const char *)images, partial);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    cfg.gridDim = dim3((unsigned)((p.rows * a.V + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, k_wide_join, a, p, (const float *)partial);
+}
+
+template <bool HALF, int GROUP>
+cudaError_t run_columns(const MatvecArgs &a, const WidePlan &p, char *images, float *partial, cudaStream_t stream) {
+    return p.n == 32   ? run<HALF, GROUP, 32>(a, p, images, partial, stream)
+           : p.n == 64 ? run<HALF, GROUP, 64>(a, p, images, partial, stream)
+                       : run<HALF, GROUP, 96>(a, p, images, partial, stream);
+}
+
+}  // namespace
+
+int64_t wide_rows(int64_t dtype) { return dtype == CK_F32 ? kMostColumns / 3 : kMostColumns; }
+
+size_t wide_workspace(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms) {
+    const WidePlan p = wide_plan(dtype, rows, K, V, sms);
+    return p.images + (p.splits > 1 ? (size_t)p.splits * p.rows * V * sizeof(float) : 0);
+}
+
+cudaError_t launch_wide(const MatvecArgs &a, int64_t group, void *workspace, int sms, cudaStream_t stream) {
+    WidePlan p = wide_plan(a.dtype, a.M, a.K, a.V, sms);
+    p.timeout_ns = options().timeout_ns;
+    p.extra = options().barrier_extra;
+    char *images = (char *)workspace;
+    float *partial = (float *)(images + p.images);
+    const int64_t items = (p.rows + (p.n - p.cols)) * p.steps * 8;
+    with_dtype(a.dtype, [&](auto *tag) {
+        using T = std::remove_pointer_t<decltype(tag)>;
+        k_images<T><<<(unsigned)((items + 255) / 256), 256, 0, stream>>>(a, p, images);
+    });
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (a.dtype == CK_F16)
+        return group == 32   ? run_columns<true, 32>(a, p, images, partial, stream)
+               : group == 64 ? run_columns<true, 64>(a, p, images, partial, stream)
+                             : run_columns<true, 128>(a, p, images, partial, stream);
+    return group == 32   ? run_columns<false, 32>(a, p, images, partial, stream)
+           : group == 64 ? run_columns<false, 64>(a, p, images, partial, stream)
+                         : run_columns<false, 128>(a, p, images, partial, stream);
+}
+
+}  // namespace ck
