@@ -10,24 +10,26 @@
 // from shared memory, sums in tensor memory.  A CTA takes 256 rows, two such products
 // that share B, and a run of K:
 //
-//   warps 0-7   a weight row a lane.  Each warp's weights come through a ring of
-//               asynchronous copies of its own; 64 columns of K are unpacked into one of
-//               two buffers of tensor memory, then the sums of the groups that were
-//               finished meanwhile are fetched, scaled and added up in registers
-//   warp 8      one thread waits for A and B, issues the products, and keeps x
-//               coming, tiles of 64 of K that k_images has laid out as the products read
-//               them, so that each is one bulk copy
+//   warps 0-7    a weight row a lane: the sums of a group, once finished, are
+//                fetched, scaled and added up in registers
+//   warps 8-15   a weight row a lane: weights come through a ring of asynchronous
+//                copies that each warp keeps for itself; 64 columns of K at a time
+//                are unpacked into one of two buffers of tensor memory
+//   warp 16      one thread waits for A and B, issues the products, and keeps x
+//                coming, tiles of 64 of K that k_images has laid out as the products
+//                read them, so that each is one bulk copy
 //
 // Tensor memory: sums of two groups for each half (4 x n columns), A twice for each
-// (4 x 32).  Every wait is bounded: one that gives up makes all others give up, and the
-// CTA's outputs NaN.
+// (4 x 32).  Registers move from warps 8-19 to warps 0-7, whose sums take 96.  Every
+// wait is bounded: one that gives up makes all others give up, and the CTA's outputs
+// NaN.
 #include "int4.h"
 
 namespace ck {
 namespace {
 
 constexpr int kWideRows = 256;
-constexpr int kWorkers = 8, kWideThreads = (kWorkers + 1) * 32;
+constexpr int kWorkers = 8, kWideThreads = (2 * kWorkers + 4) * 32;  // warps of a kind; three kinds, whole warpgroups
 constexpr int kRing = 3;          // units of a warp's ring
 constexpr int kImages = 4;        // tiles of x in shared memory
 constexpr int kStep = 64;         // columns of K of a tile of x, and of a buffer of A
@@ -125,12 +127,13 @@ template <bool HALF, int GROUP, int N>
 __global__ void __launch_bounds__(kWideThreads, 1)
     k_wide(const __grid_constant__ MatvecArgs a, const __grid_constant__ WidePlan p, const char *images, float *partial) {
     extern __shared__ __align__(1024) char smem[];
-    __shared__ __align__(8) uint64_t bars[2 * kImages + 9];
+    __shared__ __align__(8) uint64_t bars[2 * kImages + 11];
     __shared__ uint32_t tmem_base;
     __shared__ int dead;
     char *ring = smem + kImages * N * 128;
     float *all_scales = (float *)(ring + kWorkers * kRing * kUnitBytes);
-    uint8_t *all_zeros = (uint8_t *)(all_scales + kWorkers * kTileRows * kPitch);
+    uint8_t *all_zeros = (uint8_t *)(all_scales + 2 * kWorkers * kTileRows * kPitch);
+    constexpr int kUnits = 8 * GROUP / kChunk;  // units of eight groups
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t bar0 = smem_at(bars);
     auto b_full = [&](int i) { return bar0 + 8 * i; };
@@ -139,7 +142,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     auto a_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 2 + i); };
     auto d_full = [&](int i) { return bar0 + 8 * (2 * kImages + 4 + i); };
     auto d_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 6 + i); };
-    const uint32_t idle = bar0 + 8 * (2 * kImages + 8);
+    auto t_full = [&](int i) { return bar0 + 8 * (2 * kImages + 8 + i); };
+    const uint32_t idle = bar0 + 8 * (2 * kImages + 10);
     const Waiter wait{&dead, p.timeout_ns};
 
     const int64_t split = quotient(blockIdx.x, p.blocks), block = blockIdx.x - split * p.blocks;
@@ -158,11 +162,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             barrier_init(a_empty(i), 1);
             barrier_init(d_full(i), 1);
             barrier_init(d_empty(i), kWorkers);
+            barrier_init(t_full(i), kWorkers);
         }
         barrier_init(idle, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kWorkers) {
+    if (warp == 2 * kWorkers) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_at(&tmem_base))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -174,8 +179,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     auto d_at = [&](int half, int buf) { return tmem + (2 * half + buf) * N; };
     auto a_at = [&](int half, int buf) { return tmem + 4 * kMostColumns + (2 * half + buf) * (kStep / 2); };
 
-    if (warp == kWorkers) {
-        if (lane == 0) {
+    if (warp >= 2 * kWorkers) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+        if (warp == 2 * kWorkers && lane == 0) {
             asm volatile("griddepcontrol.launch_dependents;");
             asm volatile("griddepcontrol.wait;" ::: "memory");  // k_images is done
             asm volatile("fence.proxy.async.global;" ::: "memory");
@@ -248,18 +254,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
         }
         __syncwarp();
-    } else {
-        constexpr int kUnits = 8 * GROUP / kChunk;      // units of eight groups
-        constexpr int kEnds = GROUP == 32 ? 2 : 1;      // groups that a step may end
-        const int t = (int)block * (kWideRows / kTileRows) + warp, groups = (int)((a.K + GROUP - 1) / GROUP);
-        const int half = warp >> 2;
-        const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // lanes 32 (warp % 4) on of tensor memory
-        const bool there = (int64_t)t * kTileRows < a.V;
-        const uint32_t my_ring = smem_at(ring) + warp * kRing * kUnitBytes;
+    } else if (warp >= kWorkers) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        const int w = warp - kWorkers, half = w >> 2;
+        const int t = (int)block * (kWideRows / kTileRows) + w, groups = (int)((a.K + GROUP - 1) / GROUP);
+        const uint32_t quarter = (uint32_t)(w & 3) << 21;  // lanes 32 (w % 4) on of tensor memory
+        const uint32_t my_ring = smem_at(ring) + w * kRing * kUnitBytes;
         const uint32_t my_line = lane * 128, my_swap = (lane & 7) << 4;
-        float *my_scales = all_scales + warp * kTileRows * kPitch;
-        uint8_t *my_zeros = all_zeros + warp * kTileRows * 8;
-        int left = there ? c1 - c0 : 0;
+        uint8_t *my_zeros = all_zeros + w * kTileRows * 8;
+        int left = (int64_t)t * kTileRows < a.V ? c1 - c0 : 0;
         Copier from;
         from.seek(a, t, c0);
         uint32_t put = my_ring, get = my_ring;
@@ -275,16 +278,82 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         for (int i = 0; i < kRing - 1; ++i) copy_next();
         ScaleReader<kPitch> next;
         next.load(a, t, c0 / kUnits, groups);
+        bool ok = true;
+        for (int c = c0; c < c1 && ok; ++c) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+            __syncwarp();
+            copy_next();
+            const int in_eight = c & (kUnits - 1);
+            if (c == c0 || in_eight == 0) {
+                // Scales lie in two tables in turn.  The one that is written held groups
+                // whose sums have been fetched: A's last buffer was free, so the products
+                // of three steps ago were done, and they waited for sums of groups before.
+                const int table = (c / kUnits) & 1;
+                next.leave(a, all_scales + (table * kWorkers + w) * kTileRows * kPitch, my_zeros);
+                next.load(a, t, c / kUnits + 1, groups);
+                ScaleReader<kPitch>::ahead(a, t, c / kUnits + 5, groups, false);
+                __syncwarp();
+                if (lane == 0) barrier_arrive(t_full(table));
+            }
+            const uint32_t line = get + my_line;
+            get = get + kUnitBytes == my_ring + kRing * kUnitBytes ? my_ring : get + kUnitBytes;
+#pragma unroll
+            for (int q = 0; q < kChunk / kStep; ++q) {
+                const int i = (c - c0) * (kChunk / kStep) + q;
+                if (i >= steps) break;
+                const int buf = i & 1;
+                uint32_t v[32];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // pieces of 32 columns
+                    const int piece = 2 * q + e;
+                    const uint32_t zero = Nibble<HALF>::minus(
+                        my_zeros[lane * 8 + in_eight * (kChunk / GROUP) + piece * 32 / GROUP], 0);
+                    uint4 n;
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(n.x), "=r"(n.y), "=r"(n.z), "=r"(n.w)
+                                 : "r"(line + (my_swap ^ (piece << 4))));
+                    Nibble<HALF>::pairs(n.x, zero, *(uint32_t(*)[4])(v + 16 * e));
+                    Nibble<HALF>::pairs(n.y, zero, *(uint32_t(*)[4])(v + 16 * e + 4));
+                    Nibble<HALF>::pairs(n.z, zero, *(uint32_t(*)[4])(v + 16 * e + 8));
+                    Nibble<HALF>::pairs(n.w, zero, *(uint32_t(*)[4])(v + 16 * e + 12));
+                }
+                if (i >= 2) {
+                    ok = __all_sync(~0u, wait(a_empty(buf), (uint32_t)((i >> 1) - 1) & 1));
+                    if (!ok) break;
+                    fence_after();
+                }
+                asm volatile(
+                    "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                    "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                    "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a_at(half, buf) + quarter),
+                    "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                    "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+                    "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+                    "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+                    : "memory");
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                fence_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(a_full(buf));
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+        const int half = warp >> 2;
+        const uint32_t quarter = (uint32_t)(warp & 3) << 21;
         float acc[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = 0.f;
         bool ok = true;
-        int fetched = 0;  // groups whose sums have been fetched
-        // The sums of the next group, this lane's row, times its scale.
-        auto take = [&](float scale) {
-            const int buf = fetched & 1;
-            ok = __all_sync(~0u, ok && wait(d_full(buf), (uint32_t)(fetched >> 1) & 1));
-            if (!ok) return;
+        // groups of this run, from its first on: runs begin with a chunk, so with a group
+        const int first = c0 * (kChunk / GROUP), count = (steps * kStep + GROUP - 1) / GROUP;
+        for (int f = 0; f < count && ok; ++f) {
+            const int buf = f & 1, g = first + f, table = (g >> 3) & 1;
+            if (f == 0 || (g & 7) == 0) ok = wait(t_full(table), (uint32_t)(((g >> 3) - (first >> 3)) >> 1) & 1);
+            const float scale = all_scales[((table * kWorkers + warp) * kTileRows + lane) * kPitch + (g & 7)];
+            ok = __all_sync(~0u, ok && wait(d_full(buf), (uint32_t)(f >> 1) & 1));
+            if (!ok) break;
             fence_after();
             if (half == 0 || second) {
 #pragma unroll
@@ -305,76 +374,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             fence_before();
             __syncwarp();
             if (lane == 0) barrier_arrive(d_empty(buf));
-            ++fetched;
-        };
-        float now[kEnds], before[kEnds];  // scales of the groups that this step and the last one end
-        int n_before = 0;
-        for (int c = c0; c < c1 && ok; ++c) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
-            __syncwarp();
-            copy_next();
-            const int in_eight = c & (kUnits - 1);
-            if (c == c0 || in_eight == 0) {
-                next.leave(a, my_scales, my_zeros);
-                next.load(a, t, c / kUnits + 1, groups);
-                ScaleReader<kPitch>::ahead(a, t, c / kUnits + 5, groups, false);
-                __syncwarp();
-            }
-            const uint32_t line = get + my_line;
-            get = get + kUnitBytes == my_ring + kRing * kUnitBytes ? my_ring : get + kUnitBytes;
-#pragma unroll
-            for (int q = 0; q < kChunk / kStep; ++q) {
-                const int i = (c - c0) * (kChunk / kStep) + q;
-                if (i >= steps) break;
-                const int buf = i & 1;
-                if (i >= 2) {
-                    ok = __all_sync(~0u, ok && wait(a_empty(buf), (uint32_t)((i >> 1) - 1) & 1));
-                    if (!ok) break;
-                    fence_after();
-                }
-                uint32_t v[32];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {  // pieces of 32 columns
-                    const int piece = 2 * q + e, g = lane * 8 + in_eight * (kChunk / GROUP) + piece * 32 / GROUP;
-                    const uint32_t zero = Nibble<HALF>::minus(my_zeros[g], 0);
-                    uint4 w;
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                 : "r"(line + (my_swap ^ (piece << 4))));
-                    Nibble<HALF>::pairs(w.x, zero, *(uint32_t(*)[4])(v + 16 * e));
-                    Nibble<HALF>::pairs(w.y, zero, *(uint32_t(*)[4])(v + 16 * e + 4));
-                    Nibble<HALF>::pairs(w.z, zero, *(uint32_t(*)[4])(v + 16 * e + 8));
-                    Nibble<HALF>::pairs(w.w, zero, *(uint32_t(*)[4])(v + 16 * e + 12));
-                    if (GROUP == 32 || e == 1)
-                        now[GROUP == 32 ? e : 0] =
-                            my_scales[lane * kPitch + in_eight * (kChunk / GROUP) + piece * 32 / GROUP];
-                }
-                asm volatile(
-                    "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-                    "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-                    "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a_at(half, buf) + quarter),
-                    "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-                    "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
-                    "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
-                    "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-                    : "memory");
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                fence_before();
-                __syncwarp();
-                if (lane == 0) barrier_arrive(a_full(buf));
-#pragma unroll
-                for (int e = 0; e < kEnds; ++e)
-                    if (e < n_before && ok) take(before[e]);
-                if (!ok) break;
-                n_before = GROUP < 128 ? kEnds : ((i & 1) || i == steps - 1);
-#pragma unroll
-                for (int e = 0; e < kEnds; ++e) before[e] = now[e];
-            }
         }
-#pragma unroll
-        for (int e = 0; e < kEnds; ++e)
-            if (e < n_before && ok) take(before[e]);
-        asm volatile("cp.async.wait_all;" ::: "memory");
         const int64_t v = block * kWideRows + 32 * warp + lane;
         const float back = ok ? Nibble<HALF>::kBack : __int_as_float(0x7fc00000);
         if (v < a.V) {
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     fence_before();
     __syncthreads();
-    if (warp == kWorkers) {
+    if (warp == 2 * kWorkers) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
@@ -433,7 +433,7 @@ WidePlan wide_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms) {
     }
     p.chunk = Deal::of(p.chunks, p.splits);
     p.images = (size_t)p.steps * p.n * 128;
-    p.smem = (size_t)kImages * p.n * 128 + kWorkers * (kRing * kUnitBytes + kTileRows * (4 * kPitch + 8));
+    p.smem = (size_t)kImages * p.n * 128 + kWorkers * (kRing * kUnitBytes + kTileRows * (2 * 4 * kPitch + 8));
     return p;
 }
 
