@@ -15,8 +15,7 @@
 //   warps 8-15   a weight row a lane: weights come through a ring of asynchronous
 //                copies that each warp keeps for itself; 64 columns of K at a time
 //                are unpacked into one of two buffers of tensor memory
-//   warp 16      one thread waits for A and B, issues the products, and keeps x
-//                coming, tiles of 64 of K that k_images has laid out as the products
+//   warp 16      waits for A and B, issues the products, and keeps x coming, tiles of 64 of K that k_images has laid out as the products
 //                read them, so that each is one bulk copy
 //
 // Tensor memory: sums of two groups for each half (4 x n columns), A twice for each
@@ -44,28 +43,28 @@ struct WidePlan {
     Deal chunk;                // chunks to runs
     size_t images;             // bytes of x's tiles
     size_t smem;
-    long long timeout_ns;
+    long long timeout;         // cycles that a wait may last
     int extra;                 // test hook: arrivals that never come
 };
 
-// Bounded wait on a shared-memory barrier's phase.
+// Bounded wait on a shared-memory barrier's phase.  Time is the SM's clock: the
+// global one takes longer to read than most waits last.
 struct Waiter {
     volatile int *dead;
-    long long limit;
+    long long limit;  // cycles
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t phase) const {
-        unsigned long long began = 0;
-        for (int i = 0;; ++i) {
+        long long began = 0;
+        for (int i = 1;; ++i) {
             uint32_t done;
             asm volatile(
                 "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
                 : "=r"(done) : "r"(bar), "r"(phase) : "memory");
             if (done) return true;
-            if ((i & 15) == 15) {
+            if ((i & 63) == 0) {
                 if (*dead) return false;
-                unsigned long long now;
-                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+                const long long now = clock64();
                 if (began == 0) began = now;
-                if ((long long)(now - began) > limit) {
+                if (now - began > limit) {
                     *dead = 1;
                     return false;
                 }
@@ -80,9 +79,14 @@ __device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
 __device__ __forceinline__ void barrier_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// the barrier is arrived at when all products issued so far are done
+// The barrier is arrived at when all products issued so far are done.  This and the
+// products are issued by one thread of a warp that runs as one: in a branch of a
+// single thread their operands would go from its registers to the warp's one by one,
+// 100 cycles a product.
 __device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     float *all_scales = (float *)(ring + kWorkers * kRing * kUnitBytes);
     uint8_t *all_zeros = (uint8_t *)(all_scales + 2 * kWorkers * kTileRows * kPitch);
     constexpr int kUnits = 8 * GROUP / kChunk;  // units of eight groups
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0);  // known to be the warp's
     const uint32_t bar0 = smem_at(bars);
     auto b_full = [&](int i) { return bar0 + 8 * i; };
     auto b_empty = [&](int i) { return bar0 + 8 * (kImages + i); };
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     auto d_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 6 + i); };
     auto t_full = [&](int i) { return bar0 + 8 * (2 * kImages + 8 + i); };
     const uint32_t idle = bar0 + 8 * (2 * kImages + 10);
-    const Waiter wait{&dead, p.timeout_ns};
+    const Waiter wait{&dead, p.timeout};
 
     const int64_t split = quotient(blockIdx.x, p.blocks), block = blockIdx.x - split * p.blocks;
     const int c0 = (int)p.chunk.first(split), c1 = (int)p.chunk.first(split + 1);
@@ -175,22 +179,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = *(volatile uint32_t *)&tmem_base;
+    const uint32_t tmem = __shfl_sync(~0u, *(volatile uint32_t *)&tmem_base, 0);
     auto d_at = [&](int half, int buf) { return tmem + (2 * half + buf) * N; };
     auto a_at = [&](int half, int buf) { return tmem + 4 * kMostColumns + (2 * half + buf) * (kStep / 2); };
 
     if (warp >= 2 * kWorkers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
-        if (warp == 2 * kWorkers && lane == 0) {
+        if (warp == 2 * kWorkers) {
             asm volatile("griddepcontrol.launch_dependents;");
             asm volatile("griddepcontrol.wait;" ::: "memory");  // k_images is done
             asm volatile("fence.proxy.async.global;" ::: "memory");
             constexpr uint32_t kTile = N * 128;
             auto fetch = [&](int i) {
                 const uint32_t bar = b_full(i % kImages);
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kTile) : "memory");
                 asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                    "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+                    "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%3], %2;\n"
+                    "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}" ::"r"(
                         smem_at(smem) + (i % kImages) * kTile),
                     "l"(images + (int64_t)(step0 + i) * kTile), "r"(kTile), "r"(bar)
                     : "memory");
@@ -207,7 +212,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             constexpr int kPerGroup = GROUP / 16;
             for (int i = 0; i < steps && ok; ++i) {
                 const int slot = i % kImages;
-                ok = wait(b_full(slot), (uint32_t)(i / kImages) & 1) && wait(a_full(i & 1), (uint32_t)(i >> 1) & 1);
+                ok = __all_sync(~0u, wait(b_full(slot), (uint32_t)(i / kImages) & 1) && wait(a_full(i & 1), (uint32_t)(i >> 1) & 1));
                 if (!ok) break;
                 fence_after();
                 const uint64_t desc = desc0 | (smem_at(smem) + slot * kTile) >> 4;
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     const int at = (i * (kStep / 16) + k) % kPerGroup;  // of the group
                     const int buf = group & 1;
                     if (at == 0 && group >= 2 && ok) {
-                        ok = wait(d_empty(buf), (uint32_t)((group >> 1) - 1) & 1);
+                        ok = __all_sync(~0u, wait(d_empty(buf), (uint32_t)((group >> 1) - 1) & 1));
                         fence_after();
                     }
                     if (!ok) break;
@@ -224,8 +229,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     for (int half = 0; half < 2; ++half) {
                         if (half && !second) break;
                         asm volatile(
-                            "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_at(half, buf)),
+                            "{\n.reg .pred e, p;\nelect.sync _|e, 0xffffffff;\nsetp.ne.b32 p, %4, 0;\n"
+                            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_at(half, buf)),
                             "r"(a_at(half, i & 1) + k * 8), "l"(desc + 2 * k), "r"(kInstr), "r"((uint32_t)(at != 0))
                             : "memory");
                     }
@@ -239,13 +244,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 commit(b_empty(slot));
                 if (fetched < steps) {
                     // its slot was that of step fetched - kImages, whose products may still run
-                    if (fetched >= kImages) ok = wait(b_empty(fetched % kImages), (uint32_t)(fetched / kImages - 1) & 1);
+                    if (fetched >= kImages)
+                        ok = __all_sync(~0u, wait(b_empty(fetched % kImages), (uint32_t)(fetched / kImages - 1) & 1));
                     if (ok) fetch(fetched++);
                 }
             }
             // nothing is left on its way into shared memory, nor a product under way
             volatile int none = 0;
-            const Waiter last_wait{&none, p.timeout_ns};
+            const Waiter last_wait{&none, p.timeout};
             commit(idle);
             last_wait(idle, 0);
             for (int i = 0; i < kImages && !ok; ++i) {
@@ -478,7 +484,7 @@ size_t wide_workspace(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms
 
 cudaError_t launch_wide(const MatvecArgs &a, int64_t group, void *workspace, int sms, cudaStream_t stream) {
     WidePlan p = wide_plan(a.dtype, a.M, a.K, a.V, sms);
-    p.timeout_ns = options().timeout_ns;
+    p.timeout = 2 * options().timeout_ns;  // at 2 GHz
     p.extra = options().barrier_extra;
     char *images = (char *)workspace;
     float *partial = (float *)(images + p.images);
