@@ -12,16 +12,19 @@
 //
 //   warps 0-7    a weight row a lane: the sums of a group, once finished, are
 //                fetched, scaled and added up in registers
-//   warps 8-15   a weight row a lane: weights come through a ring of asynchronous
-//                copies that each warp keeps for itself; 64 columns of K at a time
-//                are unpacked into one of two buffers of tensor memory
-//   warp 16      waits for A and B, issues the products, and keeps x coming, tiles of 64 of K that k_images has laid out as the products
-//                read them, so that each is one bulk copy
+//   warps 8-15   a weight row a lane: 64 columns of K at a time are unpacked into one
+//                of two buffers of tensor memory
+//   warp 16      waits for A and B and issues the products
+//   warp 17      keeps weights coming: tensor copies of 256 rows by 128 bytes
+//   warp 18      keeps x coming: tiles of 64 of K that k_images has laid out as the
+//                products read them, so that each is one bulk copy
 //
 // Tensor memory: sums of two groups for each half (4 x n columns), A twice for each
 // (4 x 32).  Registers move from warps 8-19 to warps 0-7, whose sums take 96.  Every
 // wait is bounded: one that gives up makes all others give up, and the CTA's outputs
 // NaN.
+#include <cuda.h>
+
 #include "int4.h"
 
 namespace ck {
@@ -29,7 +32,7 @@ namespace {
 
 constexpr int kWideRows = 256;
 constexpr int kWorkers = 8, kWideThreads = (2 * kWorkers + 4) * 32;  // warps of a kind; three kinds, whole warpgroups
-constexpr int kRing = 3;          // units of a warp's ring
+constexpr int kRing = 3;          // units of weights in shared memory
 constexpr int kImages = 4;        // tiles of x in shared memory
 constexpr int kStep = 64;         // columns of K of a tile of x, and of a buffer of A
 constexpr int kMostColumns = 96;  // of tensor memory's 512, 4 x 96 and 4 x 32
@@ -129,9 +132,10 @@ template <typename T> __global__ void __launch_bounds__(256) k_images(MatvecArgs
 
 template <bool HALF, int GROUP, int N>
 __global__ void __launch_bounds__(kWideThreads, 1)
-    k_wide(const __grid_constant__ MatvecArgs a, const __grid_constant__ WidePlan p, const char *images, float *partial) {
+    k_wide(const __grid_constant__ MatvecArgs a, const __grid_constant__ WidePlan p,
+           const __grid_constant__ CUtensorMap weights, const char *images, float *partial) {
     extern __shared__ __align__(1024) char smem[];
-    __shared__ __align__(8) uint64_t bars[2 * kImages + 11];
+    __shared__ __align__(8) uint64_t bars[2 * kImages + 2 * kRing + 11];
     __shared__ uint32_t tmem_base;
     __shared__ int dead;
     char *ring = smem + kImages * N * 128;
@@ -148,6 +152,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     auto d_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 6 + i); };
     auto t_full = [&](int i) { return bar0 + 8 * (2 * kImages + 8 + i); };
     const uint32_t idle = bar0 + 8 * (2 * kImages + 10);
+    auto w_full = [&](int i) { return bar0 + 8 * (2 * kImages + 11 + i); };
+    auto w_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 11 + kRing + i); };
     const Waiter wait{&dead, p.timeout};
 
     const int64_t split = quotient(blockIdx.x, p.blocks), block = blockIdx.x - split * p.blocks;
@@ -169,6 +175,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             barrier_init(t_full(i), kWorkers);
         }
         barrier_init(idle, 1);
+        for (int i = 0; i < kRing; ++i) {
+            barrier_init(w_full(i), 1);
+            barrier_init(w_empty(i), kWorkers);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2 * kWorkers) {
@@ -185,34 +195,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
     if (warp >= 2 * kWorkers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+        constexpr uint32_t kTile = N * 128, kWeights = kWorkers * kUnitBytes;
+        bool ok = true;
+        volatile int none = 0;
+        const Waiter last_wait{&none, p.timeout};
         if (warp == 2 * kWorkers) {
             asm volatile("griddepcontrol.launch_dependents;");
-            asm volatile("griddepcontrol.wait;" ::: "memory");  // k_images is done
-            asm volatile("fence.proxy.async.global;" ::: "memory");
-            constexpr uint32_t kTile = N * 128;
-            auto fetch = [&](int i) {
-                const uint32_t bar = b_full(i % kImages);
-                asm volatile(
-                    "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
-                    "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%3], %2;\n"
-                    "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}" ::"r"(
-                        smem_at(smem) + (i % kImages) * kTile),
-                    "l"(images + (int64_t)(step0 + i) * kTile), "r"(kTile), "r"(bar)
-                    : "memory");
-            };
             // D in 32-bit floats; A and B in fp16 (0) or bf16 (1), both along K; N / 8; 128 / 16 rows
             constexpr uint32_t kType = HALF ? 0u : 1u;
             constexpr uint32_t kInstr = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N / 8) << 17 | 8u << 24;
             // of a tile in shared memory: 128-byte swizzle, 1,024 bytes from eight columns to the next
             const uint64_t desc0 = (uint64_t)2 << 61 | (uint64_t)1 << 46 | (uint64_t)64 << 32 | (uint64_t)1 << 16;
-            int fetched = 0;
-            for (; fetched < kImages - 1 && fetched < steps; ++fetched) fetch(fetched);
-            bool ok = true;
             int group = 0;
             constexpr int kPerGroup = GROUP / 16;
             for (int i = 0; i < steps && ok; ++i) {
                 const int slot = i % kImages;
-                ok = __all_sync(~0u, wait(b_full(slot), (uint32_t)(i / kImages) & 1) && wait(a_full(i & 1), (uint32_t)(i >> 1) & 1));
+                ok = __all_sync(~0u, wait(b_full(slot), (uint32_t)(i / kImages) & 1) &&
+                                         wait(a_full(i & 1), (uint32_t)(i >> 1) & 1));
                 if (!ok) break;
                 fence_after();
                 const uint64_t desc = desc0 | (smem_at(smem) + slot * kTile) >> 4;
@@ -242,53 +241,57 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 if (!ok) break;
                 commit(a_empty(i & 1));
                 commit(b_empty(slot));
-                if (fetched < steps) {
-                    // its slot was that of step fetched - kImages, whose products may still run
-                    if (fetched >= kImages)
-                        ok = __all_sync(~0u, wait(b_empty(fetched % kImages), (uint32_t)(fetched / kImages - 1) & 1));
-                    if (ok) fetch(fetched++);
-                }
             }
-            // nothing is left on its way into shared memory, nor a product under way
-            volatile int none = 0;
-            const Waiter last_wait{&none, p.timeout};
-            commit(idle);
+            commit(idle);  // no product is left under way
             last_wait(idle, 0);
-            for (int i = 0; i < kImages && !ok; ++i) {
-                const int last = fetched - 1 - (fetched - 1 - i + kImages) % kImages;  // last tile of slot i
-                if (last >= 0) last_wait(b_full(i), (uint32_t)(last / kImages) & 1);
+        } else if (warp == 2 * kWorkers + 1) {
+            const int units = c1 - c0;
+            int i = 0;
+            for (; i < units; ++i) {
+                const int slot = i % kRing;
+                if (i >= kRing) ok = __all_sync(~0u, wait(w_empty(slot), (uint32_t)(i / kRing - 1) & 1));
+                if (!ok) break;
+                asm volatile(
+                    "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+                    "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%4], %5;\n"
+                    "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                    "[%0], [%1, {%2, %3}], [%4];\n}" ::"r"(smem_at(ring) + slot * kWeights),
+                    "l"(&weights), "r"((c0 + i) * (kChunk / 2)), "r"((int)block * kWideRows), "r"(w_full(slot)),
+                    "r"(kWeights)
+                    : "memory");
             }
+            for (int k = i > kRing ? i - kRing : 0; !ok && k < i; ++k) last_wait(w_full(k % kRing), (uint32_t)(k / kRing) & 1);
+        } else if (warp == 2 * kWorkers + 2) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // k_images is done
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            int i = 0;
+            for (; i < steps; ++i) {
+                const int slot = i % kImages;
+                if (i >= kImages) ok = __all_sync(~0u, wait(b_empty(slot), (uint32_t)(i / kImages - 1) & 1));
+                if (!ok) break;
+                asm volatile(
+                    "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+                    "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%3], %2;\n"
+                    "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}" ::"r"(
+                        smem_at(smem) + slot * kTile),
+                    "l"(images + (int64_t)(step0 + i) * kTile), "r"(kTile), "r"(b_full(slot))
+                    : "memory");
+            }
+            for (int k = i > kImages ? i - kImages : 0; !ok && k < i; ++k)
+                last_wait(b_full(k % kImages), (uint32_t)(k / kImages) & 1);
         }
-        __syncwarp();
     } else if (warp >= kWorkers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         const int w = warp - kWorkers, half = w >> 2;
         const int t = (int)block * (kWideRows / kTileRows) + w, groups = (int)((a.K + GROUP - 1) / GROUP);
         const uint32_t quarter = (uint32_t)(w & 3) << 21;  // lanes 32 (w % 4) on of tensor memory
-        const uint32_t my_ring = smem_at(ring) + w * kRing * kUnitBytes;
-        const uint32_t my_line = lane * 128, my_swap = (lane & 7) << 4;
+        const uint32_t my_lines = smem_at(ring) + w * kUnitBytes + lane * 128, my_swap = (lane & 7) << 4;
         uint8_t *my_zeros = all_zeros + w * kTileRows * 8;
-        int left = (int64_t)t * kTileRows < a.V ? c1 - c0 : 0;
-        Copier from;
-        from.seek(a, t, c0);
-        uint32_t put = my_ring, get = my_ring;
-        auto copy_next = [&] {
-            if (left > 0) {
-                from.copy(a, put);
-                from.next(a, c0, 0x7fffffff);
-                --left;
-            }
-            put = put + kUnitBytes == my_ring + kRing * kUnitBytes ? my_ring : put + kUnitBytes;
-            asm volatile("cp.async.commit_group;");
-        };
-        for (int i = 0; i < kRing - 1; ++i) copy_next();
         ScaleReader<kPitch> next;
         next.load(a, t, c0 / kUnits, groups);
         bool ok = true;
         for (int c = c0; c < c1 && ok; ++c) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
-            __syncwarp();
-            copy_next();
+            const int slot = (c - c0) % kRing;
             const int in_eight = c & (kUnits - 1);
             if (c == c0 || in_eight == 0) {
                 // Scales lie in two tables in turn.  The one that is written held groups
@@ -301,8 +304,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 __syncwarp();
                 if (lane == 0) barrier_arrive(t_full(table));
             }
-            const uint32_t line = get + my_line;
-            get = get + kUnitBytes == my_ring + kRing * kUnitBytes ? my_ring : get + kUnitBytes;
+            ok = __all_sync(~0u, wait(w_full(slot), (uint32_t)((c - c0) / kRing) & 1));
+            if (!ok) break;
+            const uint32_t line = my_lines + slot * (kWorkers * kUnitBytes);
 #pragma unroll
             for (int q = 0; q < kChunk / kStep; ++q) {
                 const int i = (c - c0) * (kChunk / kStep) + q;
@@ -322,6 +326,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     Nibble<HALF>::pairs(n.y, zero, *(uint32_t(*)[4])(v + 16 * e + 4));
                     Nibble<HALF>::pairs(n.z, zero, *(uint32_t(*)[4])(v + 16 * e + 8));
                     Nibble<HALF>::pairs(n.w, zero, *(uint32_t(*)[4])(v + 16 * e + 12));
+                }
+                if (q == kChunk / kStep - 1 || i == steps - 1) {  // the unit is read
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(w_empty(slot));
                 }
                 if (i >= 2) {
                     ok = __all_sync(~0u, wait(a_empty(buf), (uint32_t)((i >> 1) - 1) & 1));
@@ -343,7 +351,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 if (lane == 0) barrier_arrive(a_full(buf));
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
         const int half = warp >> 2;
@@ -443,10 +450,38 @@ WidePlan wide_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms) {
     return p;
 }
 
+// Weights as a two-dimensional array of bytes, copied 256 rows by 128 bytes at a time
+// with 16-byte pieces exchanged by the row (the 128-byte swizzle); zeros past its ends.
+cudaError_t weight_map(const MatvecArgs &a, CUtensorMap *map) {
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<Encode> known{nullptr};
+    Encode encode = known.load();
+    if (!encode) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+        known = encode = (Encode)f;
+    }
+    const cuuint64_t size[2] = {(cuuint64_t)((a.K + 1) / 2), (cuuint64_t)a.V}, pitch[1] = {(cuuint64_t)a.q_pitch};
+    const cuuint32_t box[2] = {kChunk / 2, kWideRows}, one[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)a.q, size, pitch, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 template <bool HALF, int GROUP, int N>
 cudaError_t run(const MatvecArgs &a, const WidePlan &p, char *images, float *partial, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(k_wide<HALF, GROUP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)p.smem);
+    CUtensorMap weights;
+    if (e == cudaSuccess) e = weight_map(a, &weights);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.blocks * p.splits));
@@ -458,7 +493,7 @@ cudaError_t run(const MatvecArgs &a, const WidePlan &p, char *images, float *par
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_wide<HALF, GROUP, N>, a, p, (const char *)images, partial);
+    e = cudaLaunchKernelEx(&cfg, k_wide<HALF, GROUP, N>, a, p, weights, (const char *)images, partial);
     if (e != cudaSuccess || p.splits == 1) return e;
     cfg.gridDim = dim3((unsigned)((p.rows * a.V + 255) / 256));
     cfg.blockDim = dim3(256);
