@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kDropThreads, 7) k_dropout_dense(const __grid_
 // the period is no multiple of four, so that a piece of y begins anywhere in a block.
 template <typename T, bool LOCKED, bool SHIFTED>
 __global__ void __launch_bounds__(kDropThreads) k_dropout_flat(const __grid_constant__ DropFlat f) {
-    constexpr int E = kVec<T>, kUnroll = 2;
+    constexpr int E = kVec<T>, kUnroll = 1;
     const DropArgs &a = f.a;
     const uint64_t step = a.keys.at();
     const T *x = (const T *)a.x;
@@ -332,7 +332,7 @@ template <typename T> void launch_dropout(const DropArgs &a, cudaStream_t stream
                              stream>>>(a, pieces);
         return;
     }
-    const unsigned grid = (unsigned)((pieces + 2 * kDropThreads - 1) / (2 * kDropThreads));
+    const unsigned grid = (unsigned)((pieces + kDropThreads - 1) / kDropThreads);
     if (a.rep == 1)
         k_dropout_flat<T, false, false><<<grid, kDropThreads, 0, stream>>>(f);
     else if (f.period % 4 == 0)

@@ -9,7 +9,8 @@
 namespace ck {
 namespace {
 
-constexpr int kLogitThreads = 256, kLogitCtas = 4;  // threads of a CTA, CTAs of an SM
+// Threads of a CTA: four CTAs of the first kind fill an SM's registers, one of the second.
+constexpr int kThreads1 = 256, kThreads4 = 1024, kLogitCtas = 4;
 constexpr int kTile = 8192;   // most tokens of a CTA, whose counts it holds in shared memory
 constexpr int kOct = 8;       // tokens a thread takes at a time
 
@@ -61,7 +62,7 @@ __device__ __forceinline__ float log2_fast(float v) {
 // count[v - t0] for the tokens t0 <= v < t1 of history[0 .. len): twice the number
 // of occurrences from `prompt` on, odd or not zero where the token was seen at all.
 // Additions of integers: their order does not matter.
-template <typename I>
+template <int THREADS, typename I>
 __device__ __forceinline__ void count_history(const I *h, int64_t len, int64_t prompt, int64_t t0, int64_t t1,
                                               uint32_t *count) {
     using U = std::make_unsigned_t<I>;
@@ -82,14 +83,14 @@ __device__ __forceinline__ void count_history(const I *h, int64_t len, int64_t p
     if (threadIdx.x < head) take(h[threadIdx.x], threadIdx.x);
     if (threadIdx.x < len - tail) take(h[tail + threadIdx.x], tail + threadIdx.x);
     const uint4 *body = (const uint4 *)(h + head);
-    for (int64_t i0 = threadIdx.x; i0 < pieces; i0 += kBatch * kLogitThreads) {
+    for (int64_t i0 = threadIdx.x; i0 < pieces; i0 += kBatch * THREADS) {
         uint4 v[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            if (i0 + k * kLogitThreads < pieces) v[k] = __ldg(body + i0 + k * kLogitThreads);
+            if (i0 + k * THREADS < pieces) v[k] = __ldg(body + i0 + k * THREADS);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int64_t i = i0 + k * kLogitThreads;
+            const int64_t i = i0 + k * THREADS;
             if (i >= pieces) break;
             I id[kPer];
             memcpy(id, &v[k], 16);
@@ -115,8 +116,8 @@ struct LogitPlan {
 // than u bounds from above; a bound from below for a lane's likeliest token gives a
 // score that the CTA's best has at least.  Only tokens that may reach it are scored as
 // defined, and a lane puts its one off to the end, when few are left.
-template <typename T, int PICK>
-__global__ void __launch_bounds__(kLogitThreads, kLogitCtas)
+template <typename T, int PICK, int THREADS>
+__global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
     k_logits(const __grid_constant__ ck_logit_call a, const __grid_constant__ PhiloxKeys keys, LogitPlan plan,
              unsigned long long *keys_out) {
     extern __shared__ __align__(16) uint32_t count[];
@@ -136,12 +137,12 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas)
     const int64_t len = a.history ? row_len(a.history_len, a.history_bits, b, a.L) : 0;
     if (len > 0) {
         const int64_t prompt = a.prompt_len ? row_len(a.prompt_len, a.history_bits, b, a.L) : 0;
-        for (int i = threadIdx.x; i < octs * 2; i += kLogitThreads) ((uint4 *)count)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < octs * 2; i += THREADS) ((uint4 *)count)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         if (a.history_bits == 32)
-            count_history((const int32_t *)a.history + b * a.history_stride, len, prompt, t0, t1, count + cut);
+            count_history<THREADS>((const int32_t *)a.history + b * a.history_stride, len, prompt, t0, t1, count + cut);
         else
-            count_history((const int64_t *)a.history + b * a.history_stride, len, prompt, t0, t1, count + cut);
+            count_history<THREADS>((const int64_t *)a.history + b * a.history_stride, len, prompt, t0, t1, count + cut);
     }
     __syncthreads();
     Row row;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitCtas)
             pick_key(__fadd_rn(later_z / row.temp, gumbel(later_word)), (uint32_t)(v0 + later_o));
         best = k > best ? k : best;
     };
-    for (int ow = threadIdx.x & ~31; ow < octs; ow += kLogitThreads) {
+    for (int ow = threadIdx.x & ~31; ow < octs; ow += THREADS) {
         const int o = (ow + (int)(threadIdx.x & 31)) * kOct;
         const bool full = o >= from && o + kOct <= to;
         float z[kOct];
@@ -374,8 +375,14 @@ cudaError_t launch_logits(const ck_logit_call &a, const PhiloxKeys &keys, const 
                           cudaStream_t stream) {
     const size_t smem =
         a.history ? (size_t)((plan.slice < kTile ? plan.slice : kTile) + 2 * kOct) * sizeof(uint32_t) : 0;
-    k_logits<T, PICK><<<(unsigned)(a.B * plan.slices), kLogitThreads, smem, stream>>>(
-        a, keys, plan, (unsigned long long *)a.workspace);
+    // Where CTAs are no more than SMs and have much to read, one takes a whole SM: 20
+    // rows of 50,021 tokens with 32,768 of history take 19 us by 256 threads each.
+    const unsigned ctas = (unsigned)(a.B * plan.slices);
+    unsigned long long *best = (unsigned long long *)a.workspace;
+    if (ctas <= (unsigned)device_sms() && (plan.slice >= 4096 || (a.history && a.L >= 4096)))
+        k_logits<T, PICK, kThreads4><<<ctas, kThreads4, smem, stream>>>(a, keys, plan, best);
+    else
+        k_logits<T, PICK, kThreads1><<<ctas, kThreads1, smem, stream>>>(a, keys, plan, best);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || PICK == kNone || plan.slices == 1) return e;
     cudaLaunchConfig_t cfg{};
