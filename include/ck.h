@@ -364,6 +364,9 @@ ck_status ck_dropout(const void *x, void *y, int64_t dtype, int64_t n0, int64_t 
  *            dtype, M, K, V and group on this device, 16-byte aligned; its contents need
  *            no setting and mean nothing afterwards; NULL when that is 0 bytes
  * An x row that holds an infinity or NaN gives outputs that are not finite.
+ * Batches of more rows than 4 (32-bit x) or 16 run on kernels with device-side waits,
+ * bounded by CK_OPT_BARRIER_TIMEOUT_NS; one that gives up (it never should) leaves NaN
+ * in y.
  * Sums are added up in an order that depends on the sizes and the device alone.
  * Asynchronous.  Errors: CK_ERR_INVALID_ARG (types, group, sizes, alignment,
  * short strides, NULL pointers), CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED (a size of 2^30 or more),

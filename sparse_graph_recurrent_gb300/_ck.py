@@ -147,19 +147,16 @@ def _stream(stream):
 _U64 = (1 << 64) - 1
 
 
-# The current device's current stream as a plain integer.  The call torch's own
-# code generators use costs 0.1 us, building a Stream object 3 us, on a path of
-# about 8; the public way stays for a torch that lacks it.
-_get_device = torch.cuda.current_device
-_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device and its current stream as plain integers.  The calls torch's own
+# code generators use cost 0.1 us each, the public ones 0.3 and 3, on a path of about
+# 7; the public ways stay for a torch that lacks the others.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _raw_stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    if _get_raw_stream is not None:
-        return _get_raw_stream(_get_device())
-    return torch.cuda.current_stream().cuda_stream
+    return _get_raw_stream(_get_device()) if stream is None else stream.cuda_stream
 
 
 def _need(t, dtype, name):
@@ -340,16 +337,21 @@ def _step_args(step, device: int):
     return int(step) & _U64, None
 
 
-def ck_dropout(x, y, shape, x_strides, y_strides, p: float, seed: int, step=0, locked=False,
+def ck_dropout(x, y, n0, n1, n2, x0, x1, x2, p: float, seed: int, step=0, locked=False,
                stream=None):
-    """x and y as [n0][n1][n2] with the given sizes and strides in elements."""
+    """x as [n0][n1][n2] with strides x0, x1, x2 in elements; y contiguous in that order."""
     dtype, device = DTYPES.get(x.dtype), x.get_device()
     if dtype is None or device < 0 or y.dtype != x.dtype or y.get_device() != device:
         raise ValueError("dropout takes CUDA tensors of float32, bfloat16 or float16, out like x")
-    at, dev = _step_args(step, device)
-    _check((_lib or load()).ck_dropout(
-        x.data_ptr(), y.data_ptr(), dtype, *shape, *x_strides, *y_strides, 1 if locked else 0, p,
-        int(seed) & _U64, at, dev, _raw_stream(stream)))
+    dev = None
+    if type(step) is not int:
+        step, dev = _step_args(step, device)
+    status = (_lib or load()).ck_dropout(
+        x.data_ptr(), y.data_ptr(), dtype, n0, n1, n2, x0, x1, x2, n1 * n2, n2, 1, locked, p,
+        seed & _U64, step & _U64, dev,
+        _get_raw_stream(_get_device()) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
 
 
 def _like(t, device: int, dtype, shape, name):
@@ -408,15 +410,18 @@ def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
         if len(_int4_ws) > 4096:
             _int4_ws.clear()
         need = _int4_ws[key] = ck_int4_workspace_size(x.dtype, M, K, V, group)
-    ws = qweight.new_empty(need) if need else None
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
     if ws is not None and stream is not None:
         ws.record_stream(stream)
-    _check((_lib or load()).ck_int4_matvec(
+    status = (_lib or load()).ck_int4_matvec(
         x.data_ptr(), DTYPES[x.dtype], M, K, _rows(x, "x"), qweight.data_ptr(), V, pitch,
         scales.data_ptr(), DTYPES[scales.dtype], _rows(scales, "scales"),
         None if zeros is None else zeros.data_ptr(), 0 if zeros is None else _rows(zeros, "zeros"),
         None if bias is None else bias.data_ptr(), group, y.data_ptr(), _rows(y, "out"),
-        None if ws is None else ws.data_ptr(), need, _raw_stream(stream)))
+        None if ws is None else ws.data_ptr(), need,
+        _get_raw_stream(_get_device()) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
 
 
 def ck_int4_quantize(w, group: int, qweight, scales, zeros, stream=None):
@@ -445,7 +450,11 @@ def ck_logits_workspace_size(B: int, V: int, L: int) -> int:
 
 
 def ck_control_logits(call: LogitCall, stream=None):
-    _check((_lib or load()).ck_control_logits(ctypes.byref(call), _raw_stream(stream)))
+    status = (_lib or load()).ck_control_logits(
+        ctypes.byref(call),
+        _get_raw_stream(_get_device()) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
 
 
 def ck_forward_static_scratch(handle, edge_values, leak, bias, drives, state0, microsteps,

@@ -33,13 +33,30 @@ template <typename F> auto with_dtype(int64_t d, F &&f) {
     }
 }
 
-// SMs of the current device (1 when it cannot be asked: the launch then reports why).
+// SMs of the current device, asked once for each (1 when it cannot be asked: the
+// launch then reports why).
 inline int device_sms() {
+    constexpr int kMost = 64;
+    static std::atomic<int> known[kMost];
     int dev = 0, sms = 1;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (dev < kMost && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    if (dev < kMost) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
+}
+
+// Allows a kernel `bytes` of dynamic shared memory, once for each device (`done`: a bit
+// for each that has been told) and not on every launch.
+inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 }  // namespace ck

@@ -460,11 +460,17 @@ size_t partial_bytes(const MatvecPlan &p) {
 
 template <bool HALF, int GROUP, int NT>
 cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(k_matvec<HALF, GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemMost);
+    static std::atomic<uint64_t> told{0};
+    cudaError_t e = allow_smem((const void *)k_matvec<HALF, GROUP, NT>, (int)kSmemMost, told);
     if (e != cudaSuccess) return e;
-    k_matvec<HALF, GROUP, NT><<<(unsigned)p.ctas, kWarpsMv * 32, p.smem, stream>>>(a, p);
-    e = cudaGetLastError();
+    for (int again = 0; again < 2; ++again) {
+        k_matvec<HALF, GROUP, NT><<<(unsigned)p.ctas, kWarpsMv * 32, p.smem, stream>>>(a, p);
+        e = cudaGetLastError();
+        if (e != cudaErrorInvalidValue || again) break;
+        told = 0;  // the device's context was reset since
+        e = allow_smem((const void *)k_matvec<HALF, GROUP, NT>, (int)kSmemMost, told);
+        if (e != cudaSuccess) return e;
+    }
     if (e != cudaSuccess || p.aligned) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((p.tiles * p.rows + 3) / 4));

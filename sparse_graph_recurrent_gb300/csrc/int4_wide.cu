@@ -478,8 +478,8 @@ cudaError_t weight_map(const MatvecArgs &a, CUtensorMap *map) {
 
 template <bool HALF, int GROUP, int N>
 cudaError_t run(const MatvecArgs &a, const WidePlan &p, char *images, float *partial, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(k_wide<HALF, GROUP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)p.smem);
+    static std::atomic<uint64_t> told{0};
+    cudaError_t e = allow_smem((const void *)k_wide<HALF, GROUP, N>, (int)p.smem, told);  // N says how much
     CUtensorMap weights;
     if (e == cudaSuccess) e = weight_map(a, &weights);
     if (e != cudaSuccess) return e;
@@ -494,6 +494,13 @@ cudaError_t run(const MatvecArgs &a, const WidePlan &p, char *images, float *par
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, k_wide<HALF, GROUP, N>, a, p, weights, (const char *)images, partial);
+    if (e == cudaErrorInvalidValue) {  // the device's context was reset since
+        cudaGetLastError();
+        told = 0;
+        e = allow_smem((const void *)k_wide<HALF, GROUP, N>, (int)p.smem, told);
+        if (e == cudaSuccess)
+            e = cudaLaunchKernelEx(&cfg, k_wide<HALF, GROUP, N>, a, p, weights, (const char *)images, partial);
+    }
     if (e != cudaSuccess || p.splits == 1) return e;
     cfg.gridDim = dim3((unsigned)((p.rows * a.V + 255) / 256));
     cfg.blockDim = dim3(256);

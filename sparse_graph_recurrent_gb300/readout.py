@@ -22,11 +22,6 @@ __all__ = ["dropout", "dropout_backward", "int4_quantize", "int4_matvec", "contr
            "pick_tokens"]
 
 
-def _here(device: int):
-    """Whether a tensor's device (get_device()) is the current one."""
-    return device == torch.cuda.current_device()
-
-
 # -- dropout ---------------------------------------------------------------------------------
 
 
@@ -63,14 +58,16 @@ def _dropout(x, p, seed, step, locked):
         raise ValueError("dropout takes CUDA tensors")
     if locked and x.dim() < 2:
         raise ValueError("a locked mask is shared along the first of at least two dimensions")
-    y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if x.is_contiguous():
+        y = torch.empty_like(x)
+    else:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
     x, shape, strides = _as3(x, locked)
-    args = (x, y, shape, strides, (shape[1] * shape[2], shape[2], 1), p, seed, step, locked)
-    if _here(device):
-        _ck.ck_dropout(*args)
+    if device == _ck._get_device():
+        _ck.ck_dropout(x, y, *shape, *strides, p, seed, step, locked)
     else:
         with torch.cuda.device(device):
-            _ck.ck_dropout(*args)
+            _ck.ck_dropout(x, y, *shape, *strides, p, seed, step, locked)
     return y
 
 
@@ -147,13 +144,13 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
     if x2.shape[1] > 1 and x2.stride(1) != 1:
         x2 = x2.contiguous()
     if out is None:
-        y = x.new_empty((x2.shape[0], V))
+        y = torch.empty((x2.shape[0], V), dtype=x.dtype, device=x.device)
     else:
         if tuple(out.shape) != (*x.shape[:-1], V):
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(*x.shape[:-1], V)}")
         y = out if out.dim() == 2 else out.view(-1, V)
     args = (x2, qweight, scales, zeros, bias, group_size, y)
-    if _here(device):
+    if device == _ck._get_device():
         _ck.ck_int4_matvec(*args)
     else:
         with torch.cuda.device(device):
@@ -248,7 +245,7 @@ def _control(logits, history, history_len, prompt_len, repetition, frequency, pr
             with torch.cuda.device(dev):
                 need = _logits_ws[key] = _ck.ck_logits_workspace_size(B, V, L)
         if need:
-            ws = tokens.new_empty(need // 8)
+            ws = torch.empty(need // 8, dtype=torch.int64, device=logits.device)
     call = _ck.LogitCall(
         logits.data_ptr(), dtype, B, V, _ck._rows(logits, "logits"), text, text_len, prompt, bits, L,
         text_stride, rep, freq, pres, temp, rep_all, freq_all, pres_all, temp_all, bias_at,
@@ -256,7 +253,7 @@ def _control(logits, history, history_len, prompt_len, repetition, frequency, pr
         None if tokens is None else tokens.data_ptr(), 0 if seed is None else 1,
         0 if seed is None else int(seed) & _ck._U64, at or 0, step_dev,
         None if ws is None else ws.data_ptr(), need or 0)
-    if _here(dev):
+    if dev == _ck._get_device():
         _ck.ck_control_logits(call)
     else:
         with torch.cuda.device(dev):

@@ -77,6 +77,20 @@ def test_strides(view, locked, dtype):
     same(y, expected(x, 0.4, 7, 1, locked))
 
 
+@pytest.mark.parametrize("cut", [0, 5])
+def test_more_than_two_to_the_31_elements(cut):
+    """Element indexes past 32 bits, dense and in rows cut out of wider ones: windows at
+    both ends and around 2^31 and 2^32 are compared."""
+    import sparse_graph_recurrent_gb300 as ck
+    rows, n = 5, 900_000_000
+    base = torch.ones(rows, n + cut, dtype=torch.bfloat16, device="cuda")
+    y = ck.dropout(base[:, :n], 0.3, 17, 3).view(-1)
+    for at in (0, n - 500, 2 ** 31 - 500, 2 ** 32 - 500, rows * n - 1000):
+        w = ro.philox_words(np.arange(at, at + 1000), 17, 3)
+        want = torch.from_numpy((w.astype(np.int64) >= int(np.rint(0.3 * 2 ** 32))))
+        assert torch.equal(y[at:at + 1000].cpu() > 0, want), at
+
+
 def test_dropped_values_are_zero_whatever_they_hold():
     import sparse_graph_recurrent_gb300 as ck
     x = data((4, 4099), torch.float32)

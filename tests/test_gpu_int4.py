@@ -60,6 +60,83 @@ def test_rows_of_x(M, dtype):
     check(ck.int4_matvec(**c, group_size=64), c, 64)
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype,M", [(torch.float32, 5), (torch.float32, 11), (torch.float32, 21), (torch.float32, 32),
+                                     (torch.bfloat16, 17), (torch.bfloat16, 33), (torch.bfloat16, 96),
+                                     (torch.float16, 32), (torch.float16, 64), (torch.float16, 70)])
+def test_batches_at_every_width(dtype, M, group, zeros):
+    """Every width and group of the product for batches; a block of rows that is not
+    full, a half of it that is empty, K that ends inside every tile."""
+    import sparse_graph_recurrent_gb300 as ck
+    for K, V in ((1, 3), (65, 127), (700, 300), (1217, 129)):
+        c = case(M, K, V, group, dtype, zeros=zeros, seed=M + K, pad_rows=V % 2)
+        check(ck.int4_matvec(**c, group_size=group), c, group)
+
+
+@pytest.mark.parametrize("dtype,M", [(torch.float32, 20), (torch.float16, 40)])
+@pytest.mark.parametrize("K,V", [(40000, 100), (9000, 2000), (300, 45000)])
+def test_batches_in_one_run_of_k_and_in_many(K, V, dtype, M):
+    import sparse_graph_recurrent_gb300 as ck
+    c = case(M, K, V, 128, dtype, seed=K)
+    bias = torch.randn(V, device="cuda")
+    a = ck.int4_matvec(**c, bias=bias)
+    check(a, c, 128, bias)
+    assert torch.equal(ck.int4_matvec(**c, bias=bias), a)
+
+
+def test_batch_side_stream_and_capture():
+    import sparse_graph_recurrent_gb300 as ck
+    c = case(20, 3000, 500, 64, torch.float32, seed=4)
+    a = ck.int4_matvec(**c, group_size=64)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        b = ck.int4_matvec(**c, group_size=64)
+    s.synchronize()
+    assert torch.equal(a, b)
+    out = torch.empty_like(a)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ck.int4_matvec(**c, group_size=64, out=out)
+    c["x"].mul_(0.5)
+    g.replay()
+    assert torch.equal(out, a * 0.5)
+
+
+def test_a_wait_that_runs_out_leaves_nan_and_a_usable_device():
+    """The batch product's waits are bounded: with an arrival asked for that never comes
+    all of them give up, y is NaN, and the next call is right."""
+    import sparse_graph_recurrent_gb300 as ck
+    from sparse_graph_recurrent_gb300 import _ck
+    c = case(8, 2000, 600, 128, torch.float32, seed=6)
+    _ck.ck_set_option(_ck.OPT_TEST_BARRIER_EXTRA, 1)
+    _ck.ck_set_option(_ck.OPT_BARRIER_TIMEOUT_NS, 2_000_000)
+    try:
+        y = ck.int4_matvec(**c)
+        torch.cuda.synchronize()
+        assert torch.isnan(y).all()
+    finally:
+        _ck.ck_set_option(_ck.OPT_TEST_BARRIER_EXTRA, 0)
+        _ck.ck_set_option(_ck.OPT_BARRIER_TIMEOUT_NS, 4_000_000_000)
+    check(ck.int4_matvec(**c), c, 128)
+
+
+@pytest.mark.parametrize("M", [2, 8])
+def test_weights_past_two_gigabytes(M):
+    """Rows whose bytes lie past 2^31; the last ones are compared."""
+    import sparse_graph_recurrent_gb300 as ck
+    K, V, n = 65536, 70000, 64
+    small = case(M, K, n, 128, torch.bfloat16, seed=7)
+    q = torch.zeros(V, K // 2, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(V, K // 128, dtype=torch.bfloat16, device="cuda")
+    z = torch.zeros(V, K // 128, dtype=torch.uint8, device="cuda")
+    q[-n:], s[-n:], z[-n:] = small["qweight"], small["scales"], small["zeros"]
+    y = ck.int4_matvec(small["x"], q, s, z)
+    check(y[:, -n:].contiguous(), small, 128)
+    assert not y[:, :-n].any()
+
+
 @pytest.mark.parametrize("M,V", [(1, 40000), (4, 9001), (32, 5000), (20, 2500)])
 def test_many_outputs(M, V):
     import sparse_graph_recurrent_gb300 as ck

@@ -240,6 +240,31 @@ def test_draws_follow_the_softmax():
     assert (np.abs(count - n * p) <= 6 * np.sqrt(n * p * (1 - p)) + 1e-9).all()
 
 
+def test_element_indexes_past_32_bits():
+    """40,000 rows of 131,072 tokens, one row of logits shared by all: the noise of the
+    last rows is that of elements past 2^32."""
+    import sparse_graph_recurrent_gb300 as ck
+    B, V = 40_000, 131_072
+    z = torch.randn(V, device="cuda")
+    got = ck.pick_tokens(z.expand(B, V), seed=3, step=2)
+    for b in (0, 16384, 32768, B - 1):
+        w = ro.philox_words(np.arange(b * V, (b + 1) * V), 3, 2).astype(np.float64)
+        u = np.minimum(w * 2.0 ** -32 + 2.0 ** -33, 1 - 2.0 ** -24)
+        score = z.double().cpu().numpy() - np.log(-np.log1p(-u))
+        assert score[int(got[b])] >= score.max() - 1e-5
+
+
+def test_in_place_and_many_rows():
+    import sparse_graph_recurrent_gb300 as ck
+    x = torch.randn(70, 9000, device="cuda") * 2
+    t = torch.rand(70, device="cuda") + 0.5
+    want, z = ck.pick_tokens(x, temperature=t, seed=8, step=4, return_logits=True)
+    y = x.clone()
+    got, same = ck.pick_tokens(y, temperature=t, seed=8, step=4, out=y)
+    assert torch.equal(got, want) and torch.equal(y, z) and same is y
+    assert torch.equal(ck.pick_tokens(x, temperature=t, seed=8, step=4), want)
+
+
 def test_step_on_the_device_capture_and_streams():
     import sparse_graph_recurrent_gb300 as ck
     from sparse_graph_recurrent_gb300 import _ck
