@@ -126,7 +126,33 @@ def load() -> ctypes.CDLL:
     lib.ck_last_error_message.argtypes = []
     lib.ck_last_error_message.restype = ctypes.c_char_p
     _lib = lib
+    _load_native(lib)
     return lib
+
+
+_native = None
+
+
+def _load_native(lib):
+    """Load the module ck_binding (the readout operators' short way from Python),
+    building it first if it is missing or stale, and give it this library's entries."""
+    global _native
+    import importlib.machinery
+    import importlib.util
+    loader = importlib.machinery.ExtensionFileLoader("ck_binding", _build.build_binding())
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("ck_binding", loader))
+    loader.exec_module(module)
+    entry = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value  # noqa: E731
+    module.bind(entry("ck_dropout"), entry("ck_int4_matvec"), entry("ck_int4_workspace_size"),
+                entry("ck_control_logits"), entry("ck_logits_workspace_size"), _check)
+    _native = module
+
+
+def native():
+    """The module ck_binding."""
+    if _native is None:
+        load()
+    return _native
 
 
 def _check(status: int):

@@ -12,6 +12,9 @@ being accessed.  The binding loads it when CK_LIBRARY_VARIANT=bounds.
 Variant "prof" (-DCK_PHASE_PROFILE, _build/libck_prof.so) adds %globaltimer
 stamps around each phase of a microstep, read with ck_phase_profile_read; the
 binding loads it when CK_LIBRARY_VARIANT=prof.
+
+csrc/binding.cpp, the short way from Python to the readout operators, is compiled
+by the host compiler against torch's headers into _build/ck_binding-<torch>.so.
 """
 from __future__ import annotations
 
@@ -87,10 +90,40 @@ def build(force: bool = False, verbose: bool = False, variant=None) -> str:
     return lib
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the Python module ck_binding if its source or ck.h is newer than it;
+    return its path."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    src = os.path.join(CSRC, "binding.cpp")
+    out = os.path.join(OUT, f"ck_binding-{torch.__version__}.so")
+    deps = [src, os.path.join(ROOT, "include", "ck.h")]
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(map(os.path.getmtime, deps)):
+        return out
+    os.makedirs(OUT, exist_ok=True)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [os.path.join(ROOT, "include"), *cpp_extension.include_paths(),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = out + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(a for i in includes for a in ("-isystem" if i != includes[0] else "-I", i)), src, "-o", tmp,
+           "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def build_all(force: bool = False) -> list:
-    """Every variant, compiled side by side."""
-    with ThreadPoolExecutor(max_workers=len(VARIANTS)) as ex:
-        return list(ex.map(lambda v: build(force=force, variant=v), list(VARIANTS)))
+    """Every variant and the Python module, compiled side by side."""
+    with ThreadPoolExecutor(max_workers=len(VARIANTS) + 1) as ex:
+        module = ex.submit(build_binding, force)
+        return [*ex.map(lambda v: build(force=force, variant=v), list(VARIANTS)), module.result()]
 
 
 if __name__ == "__main__":

@@ -8,7 +8,9 @@ answers (connectome-kernels page, intro: a connectome trained on text).
     tokens = pick_tokens(logits, history, history_len=n, repetition=1.1,
                          mask=allowed, temperature=0.8, seed=seed, step=step)
 
-Every call runs one kernel on the current stream and returns without waiting.
+Every call enqueues its kernels on the current stream and returns without waiting.
+A call whose arguments are all in order goes through the compiled module
+ck_binding; what that leaves is done, or refused, here.
 """
 from __future__ import annotations
 
@@ -77,11 +79,11 @@ class _Dropout(torch.autograd.Function):
         if isinstance(step, torch.Tensor):
             step = step.clone()  # the backward's mask is this forward's, wherever the counter is by then
         ctx.args = (p, seed, step, locked)
-        return _dropout(x.detach(), p, seed, step, locked)
+        return dropout_backward(x.detach(), *ctx.args)
 
     @staticmethod
     def backward(ctx, d_out):
-        return _dropout(d_out, *ctx.args), None, None, None, None
+        return dropout_backward(d_out, *ctx.args), None, None, None, None
 
 
 def dropout(x, p: float, seed: int, step=0, locked: bool = False):
@@ -92,14 +94,18 @@ def dropout(x, p: float, seed: int, step=0, locked: bool = False):
     int64[1] that ck_step_advance counts up (also inside a captured step).
     With locked=True one mask serves every entry of the first dimension, as for
     the T input steps of out[T, B, N].  float32, bfloat16 or float16, any strides."""
+    y = (_ck._native or _ck.native()).dropout(x, p, seed, step, locked)
+    if y is not None:
+        return y
     if x.requires_grad and torch.is_grad_enabled():
         return _Dropout.apply(x, p, seed, step, locked)
     return _dropout(x, p, seed, step, locked)
 
 
 def dropout_backward(d_out, p: float, seed: int, step=0, locked: bool = False):
-    """The gradient of dropout's x from its output's: the same mask again."""
-    return _dropout(d_out, p, seed, step, locked)
+    """The gradient of dropout's x from its output's: the same mask and factor again."""
+    y = (_ck._native or _ck.native()).dropout(d_out, p, seed, step, locked)
+    return _dropout(d_out, p, seed, step, locked) if y is None else y
 
 
 # -- the 4-bit readout -----------------------------------------------------------------------
@@ -132,6 +138,9 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
     bias (float32 [V]): [..., V] in x's type.  For a few rows of x at a time, as
     when answering; it has no gradient.  `out`, if given, is written instead of a
     new tensor."""
+    y = (_ck._native or _ck.native()).int4_matvec(x, qweight, scales, zeros, bias, group_size, out)
+    if y is not None:
+        return y
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError("int4_matvec has no gradient: call it under no_grad or on a detached x")
     device = x.get_device()
@@ -270,6 +279,11 @@ def control_logits(logits, history=None, history_len=None, prompt_len=None, repe
     allows token v, else -inf), then division by temperature (not where it is 0).
     Penalties and temperature are numbers or float32 [B]; history int64 or int32
     [B, L], ids outside [0, V) ignored; lengths [B] in its type."""
+    got = (_ck._native or _ck.native()).control(
+        logits, history, history_len, prompt_len, repetition, frequency, presence, bias, mask,
+        temperature, True if out is None else out, 0, None, 0)
+    if got is not None:
+        return got
     if out is None:
         out = torch.empty_like(logits, memory_format=torch.contiguous_format)
     _control(logits, history, history_len, prompt_len, repetition, frequency, presence, bias, mask,
@@ -286,6 +300,12 @@ def pick_tokens(logits, history=None, history_len=None, prompt_len=None, repetit
     row with no token left gives -1.  `step` as in dropout: another one for
     every token drawn.  With return_logits=True, or an `out` to write them to,
     (tokens, controlled logits)."""
+    logits_too = return_logits or out is not None
+    got = (_ck._native or _ck.native()).control(
+        logits, history, history_len, prompt_len, repetition, frequency, presence, bias, mask,
+        temperature, True if out is None and return_logits else out, 2 if logits_too else 1, seed, step)
+    if got is not None:
+        return got
     if out is None and return_logits:
         out = torch.empty_like(logits, memory_format=torch.contiguous_format)
     tokens = torch.empty(logits.shape[:1], dtype=torch.int64, device=logits.device)

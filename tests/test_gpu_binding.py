@@ -1,0 +1,97 @@
+"""The compiled module ck_binding and the Python form of the same calls agree, and
+what the module does not take the Python form does or refuses."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+class Nothing:
+    """A module that leaves every call to Python."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+@pytest.fixture
+def both(monkeypatch):
+    from sparse_graph_recurrent_gb300 import _ck
+    native = _ck.native()
+
+    def run(call):
+        monkeypatch.setattr(_ck, "_native", native)
+        a = call()
+        monkeypatch.setattr(_ck, "_native", Nothing())
+        b = call()
+        monkeypatch.setattr(_ck, "_native", native)
+        return a, b
+    return run
+
+
+def same(a, b):
+    if isinstance(a, tuple):
+        assert len(a) == len(b)
+        return all(same(x, y) for x, y in zip(a, b))
+    return a.dtype == b.dtype and a.shape == b.shape and a.stride() == b.stride() and torch.equal(a, b)
+
+
+def test_dropout_both_ways(both):
+    import sparse_graph_recurrent_gb300 as ck
+    x = torch.randn(4, 6, 130, device="cuda")
+    step = torch.tensor([3], device="cuda")
+    for v in (x, x[..., :121], x.transpose(0, 1), x.permute(2, 0, 1)[::2], x[:1].expand(4, 6, 130), x.half(), x[0, 0]):
+        for locked in (False, True) if v.dim() > 1 else (False,):
+            for s in (0, -1, 2 ** 64 - 1, step):
+                assert same(*both(lambda: ck.dropout(v, 0.4, 2 ** 63 + 1, s, locked=locked)))
+    assert same(*both(lambda: ck.dropout(x, 1, 5)))
+    assert same(*both(lambda: ck.dropout_backward(x, 0.5, 5, 6)))
+
+
+def test_int4_both_ways(both):
+    import sparse_graph_recurrent_gb300 as ck
+    w = torch.randn(70, 333, device="cuda")
+    for symmetric in (True, False):
+        q, s, z = ck.int4_quantize(w, 32, symmetric, scale_dtype=torch.bfloat16)
+        for M in (1, 5):
+            x = torch.randn(M, 333, device="cuda")
+            for bias in (None, torch.randn(70, device="cuda")):
+                assert same(*both(lambda: ck.int4_matvec(x, q, s, z, bias, 32)))
+            out = torch.empty(M, 80, device="cuda")[:, :70]
+            assert same(*both(lambda: ck.int4_matvec(x, q, s, z, group_size=32, out=out).clone()))
+    assert same(*both(lambda: ck.int4_matvec(w[0], q, s, z, group_size=32)))
+    assert same(*both(lambda: ck.int4_matvec(w[:1], q[:1], s[:1], z[:1], group_size=32)))
+
+
+def test_controls_both_ways(both):
+    import sparse_graph_recurrent_gb300 as ck
+    B, V = 3, 9001
+    x = torch.randn(B, V, device="cuda")
+    h = torch.randint(0, V, (B, 50), device="cuda")
+    n = torch.tensor([50, 3, 0], device="cuda")
+    rows = torch.rand(B, device="cuda") + 0.5
+    step = torch.tensor([9], device="cuda")
+    for kw in ({}, dict(history=h), dict(history=h.int(), history_len=n.int()), dict(temperature=0.7), dict(temperature=0),
+               dict(history=h, history_len=n, prompt_len=n // 2, repetition=1.2, frequency=rows, presence=rows,
+                    temperature=rows, bias=torch.randn(V, device="cuda"),
+                    mask=torch.full((B, -(-V // 32)), -2, dtype=torch.int32, device="cuda"))):
+        assert same(*both(lambda: ck.control_logits(x, **kw)))
+        for seed in (None, 5):
+            for s in (2, step):
+                assert same(*both(lambda: ck.pick_tokens(x, **kw, seed=seed, step=s)))
+                assert same(*both(lambda: ck.pick_tokens(x, **kw, seed=seed, step=s, return_logits=True)))
+
+
+def test_what_the_module_leaves():
+    from sparse_graph_recurrent_gb300 import _ck
+    n = _ck.native()
+    x = torch.randn(2, 64, device="cuda", requires_grad=True)
+    assert n.dropout(x, 0.5, 1, 0, False) is None
+    assert n.dropout(x.detach().double(), 0.5, 1, 0, False) is None
+    assert n.dropout(x.detach().cpu(), 0.5, 1, 0, False) is None
+    assert n.dropout(x.detach(), 0.5, "1", 0, False) is None
+    assert n.dropout(None, 0.5, 1, 0, False) is None
+    with torch.no_grad():
+        assert n.dropout(x, 0.5, 1, 0, False) is not None
+    with pytest.raises(_ck.CKError) as e:
+        n.dropout(x.detach(), 1.5, 1, 0, False)
+    assert e.value.name == "CK_ERR_INVALID_ARG"

@@ -158,3 +158,11 @@ def test_cpu_tensors_are_refused():
         ck.control_logits(x)
     with pytest.raises(ValueError):
         ck.pick_tokens(x)
+
+
+def test_the_compiled_module_leaves_cpu_tensors():
+    from sparse_graph_recurrent_gb300 import _ck
+    x = torch.zeros(2, 64)
+    assert _ck.native().dropout(x, 0.5, 1, 0, False) is None
+    assert _ck.native().int4_matvec(x, x, x, None, None, 32, None) is None
+    assert _ck.native().control(x, *[None] * 9, True, 0, None, 0) is None
