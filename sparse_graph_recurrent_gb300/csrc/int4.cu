@@ -15,9 +15,8 @@ namespace {
 // columns, but an outlier that meets q = z then drowns the rest of its row.)
 //
 // What bounds it is the stream of weights: 0.5 byte each, while a column costs
-// 2 operations a weight.  So the weights flow through a ring of asynchronous
-// copies that each warp keeps for itself, and no warp waits for another until
-// the end.
+// 2 operations a weight.  So the weights flow through a ring of tensor copies that
+// each warp keeps for itself, and no warp waits for another until the end.
 //
 // A unit is 32 weight rows by 256 columns (4 KB).  K is cut into slabs whose x
 // fits in shared memory; the units, in the order (slab, 32-row tile, chunk),
@@ -42,6 +41,7 @@ struct MatvecPlan {
     Deal cta;          // CTAs to slabs
     Deal slab;         // slabs to CTAs
     Deal tile;         // aligned: tiles to CTAs
+    long long timeout; // cycles that a wait for a copy may last
     int x_pitch;       // bytes between columns of x in shared memory
     int x_cols;        // tensor-core columns that x takes
     size_t smem;
@@ -126,8 +126,12 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, const MatvecPlan &p
 }
 
 template <bool HALF, int GROUP, int NT>
-__global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, MatvecPlan p) {
+__global__ void __launch_bounds__(kWarpsMv * 32, 1)
+    k_matvec(const __grid_constant__ MatvecArgs a, const __grid_constant__ MatvecPlan p,
+             const __grid_constant__ CUtensorMap weights) {
     extern __shared__ __align__(1024) char smem[];
+    __shared__ __align__(8) uint64_t bars[kWarpsMv * kStages];
+    __shared__ int dead;
     constexpr int kGroups = kHalf / GROUP;  // of half a unit
     // per warp: its ring, in which its last part of a sum is left when it is done; its
     // first part; scales and zero points of the eight groups at hand
@@ -137,9 +141,18 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
     uint8_t *all_zeros = (uint8_t *)(all_scales + kWarpsMv * kTileRows * 8);
     int *part_tile = (int *)(all_zeros + kWarpsMv * kTileRows * 8);  // [warps][first, last]
     char *xs = (char *)(part_tile + kWarpsMv * 2);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0);  // known to be the warp's
     const int row = lane >> 2, quad = lane & 3;
-    const uint32_t my_ring = smem_at(smem) + warp * kStages * kUnitBytes;
+    const uint32_t my_ring = smem_at(smem) + warp * kStages * kUnitBytes, my_bars = smem_at(bars) + warp * kStages * 8;
+    const Waiter wait{&dead, p.timeout};
+    if (threadIdx.x == 0) dead = 0;
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i) barrier_init(my_bars + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // A place in the ring, and how often the ring has gone round: the copy that is waited
+    // for next and the one that is asked for next.
+    int get = 0, get_round = 0, put = 0, under_way = 0;
+    bool ok = true;
     const uint32_t my_line = lane * 128, my_swap = (lane & 7) << 4;
     float *my_scales = all_scales + warp * kTileRows * 8;
     uint8_t *my_zeros = all_zeros + warp * kTileRows * 8;
@@ -176,19 +189,18 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
         int n = w1 - w0, left = n;
         int t = tile0 + (skip + w0) / sc, c = (skip + w0) % sc;
         __syncthreads();  // the last slab's x and parts of sums are done with
-        Copier from;
-        from.seek(a, t, first + c);
-        uint32_t put = my_ring, get = my_ring;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        int put_t = t, put_c = c;
         auto copy_next = [&] {
-            if (left > 0) {
-                from.copy(a, put);
-                from.next(a, first, first + sc);
-                --left;
-            }
-            put = put + kUnitBytes == my_ring + kStages * kUnitBytes ? my_ring : put + kUnitBytes;
-            asm volatile("cp.async.commit_group;");
+            if (left == 0 || !ok) return;
+            ++under_way;
+            copy_box(weights, (first + put_c) * (kChunk / 2), put_t * kTileRows, my_ring + put * kUnitBytes,
+                     my_bars + 8 * put, kUnitBytes);
+            put = put + 1 == kStages ? 0 : put + 1;
+            if (++put_c == sc) put_c = 0, ++put_t;
+            --left;
         };
-        for (int i = 0; i < kStages - 1; ++i) copy_next();
+        for (int i = 0; i < kStages; ++i) copy_next();
         ScaleReader<8> next;
         constexpr int kUnits = 8 * GROUP / kChunk, kAhead = 4;  // units of eight groups
         if (n > 0) next.load(a, t, (first + c) / kUnits, groups);
@@ -204,9 +216,7 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
         float acc[NT][2][4] = {};  // [.][rows 0-15, 16-31][.]
         bool from_start = c == 0;  // this tile's part began with the slab
         for (; n > 0; --n) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-            __syncwarp();
-            copy_next();
+            ok = __all_sync(~0u, ok && wait(my_bars + 8 * get, get_round & 1));
             const bool whole = c + 1 == sc;
             if (begin) {
                 next.leave(a, my_scales, my_zeros);
@@ -220,8 +230,11 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
             }
             const int in_eight = (first + c) & (kUnits - 1);
             begin = whole || in_eight == kUnits - 1;
-            const uint32_t lines = get + my_line;
-            get = get + kUnitBytes == my_ring + kStages * kUnitBytes ? my_ring : get + kUnitBytes;
+            const uint32_t lines = my_ring + get * kUnitBytes + my_line;
+            if (ok) {
+                --under_way;
+                if (++get == kStages) get = 0, ++get_round;
+            }
             const char *xc = xs + c * (2 * kChunk);
 #pragma unroll
             for (int half = 0; half < kChunk / kHalf; ++half) {
@@ -285,6 +298,8 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
                     }
                 }
             }
+            __syncwarp();  // the unit is read
+            copy_next();
             if (whole || n == 1) {  // this tile's part ends here
                 if (!HALF && a.dtype == CK_F32) {
                     // the three parts of x lie in lanes quad 0, 1 and 2: smallest first
@@ -313,7 +328,7 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
                             const int r = 16 * i + row + 8 * (e >> 1);
                             const int m = !HALF && a.dtype == CK_F32 ? (quad ? p.rows : 2 * j + (e & 1))
                                                                      : 8 * j + 2 * quad + (e & 1);
-                            const float sum = acc[j][i][e] * Nibble<HALF>::kBack;
+                            const float sum = acc[j][i][e] * (ok ? Nibble<HALF>::kBack : __int_as_float(0x7fc00000));
                             acc[j][i][e] = 0.f;
                             if (m >= p.rows) continue;
                             const int64_t v = (int64_t)t * kTileRows + r;
@@ -350,6 +365,14 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1) k_matvec(MatvecArgs a, Matve
                 else if (v < a.V)
                     store_y(a, m, v, sum);
             }
+        }
+    }
+    if (!ok) {  // a wait gave up: no copy is left on its way into this CTA's memory
+        volatile int none = 0;
+        const Waiter last_wait{&none, p.timeout};
+        for (; under_way > 0; --under_way) {
+            last_wait(my_bars + 8 * get, get_round & 1);
+            if (++get == kStages) get = 0, ++get_round;
         }
     }
 }
@@ -450,6 +473,7 @@ MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sm
     const int64_t slab = (p.chunks + p.slabs - 1) / p.slabs;
     // 64 bytes past a multiple of 128: two columns side by side fill all banks
     p.x_pitch = (int)slab * 2 * kChunk + 64;
+    p.timeout = 2 * options().timeout_ns;  // at 2 GHz
     p.smem = fixed + (size_t)p.x_cols * p.x_pitch;
     return p;
 }
@@ -460,11 +484,14 @@ size_t partial_bytes(const MatvecPlan &p) {
 
 template <bool HALF, int GROUP, int NT>
 cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
+    CUtensorMap weights;
+    cudaError_t mapped = weight_map(a, kTileRows, &weights);
+    if (mapped != cudaSuccess) return mapped;
     static std::atomic<uint64_t> told{0};
     cudaError_t e = allow_smem((const void *)k_matvec<HALF, GROUP, NT>, (int)kSmemMost, told);
     if (e != cudaSuccess) return e;
     for (int again = 0; again < 2; ++again) {
-        k_matvec<HALF, GROUP, NT><<<(unsigned)p.ctas, kWarpsMv * 32, p.smem, stream>>>(a, p);
+        k_matvec<HALF, GROUP, NT><<<(unsigned)p.ctas, kWarpsMv * 32, p.smem, stream>>>(a, p, weights);
         e = cudaGetLastError();
         if (e != cudaErrorInvalidValue || again) break;
         told = 0;  // the device's context was reset since

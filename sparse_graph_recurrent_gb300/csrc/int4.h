@@ -2,6 +2,8 @@
 // of weights and scales into a warp's hands, and weights as 16-bit floats.
 #pragma once
 
+#include <cuda.h>
+
 #include <cstring>
 
 #include "ck_types.h"
@@ -27,7 +29,7 @@ struct MatvecArgs {
 constexpr int kTileRows = 32;               // weight rows of a unit
 constexpr int kChunk = 256;                 // columns of a unit
 constexpr int kUnitBytes = kTileRows * kChunk / 2;
-constexpr size_t kSmemMost = 232448;
+constexpr size_t kSmemMost = 232448 - 1024;  // of a CTA, less what is not dynamic
 
 // a / b, in 32 bits where that does: a 64-bit division costs ten times as much
 __host__ __device__ inline int64_t quotient(int64_t a, int64_t b) {
@@ -112,50 +114,47 @@ __device__ __forceinline__ void load8(const MatvecArgs &a, int64_t m, int64_t k,
     }
 }
 
-// What a warp copies next: its lanes' place in the weights, moved on by a chunk
-// at a time.  A unit is eight 16-byte pieces of 32 lines of 128 bytes; the pieces
-// of line r lie exchanged by r, so that a piece of eight lines is read without a
-// conflict.
-struct Copier {
-    const uint8_t *src;     // the lane's piece in line lane / 8
-    int tile, chunk;
-    __device__ __forceinline__ void seek(const MatvecArgs &a, int tile_, int chunk_) {
-        const int lane = threadIdx.x & 31;
-        tile = tile_;
-        chunk = chunk_;
-        src = a.q + (int64_t)(tile * kTileRows + (lane >> 3)) * a.q_pitch + chunk * (kChunk / 2) + (lane & 7) * 16;
-    }
-    __device__ __forceinline__ void copy(const MatvecArgs &a, uint32_t dst) const {
-        const int lane = threadIdx.x & 31;
-        // lines 4 i + lane / 8: their low three bits are lane / 8, and 4 for odd i
-        const uint32_t at = dst + (lane >> 3) * 128, p0 = ((lane & 7) ^ (lane >> 3)) << 4, p1 = p0 ^ 64;
-        if ((tile + 1) * kTileRows <= (int)a.V && (chunk + 1) * kChunk <= (int)a.K) {
-            const uint8_t *s = src;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + (i & 1 ? p1 : p0) + i * 512),
-                             "l"(s));
-                s += 4 * a.q_pitch;
+// Bounded wait on a shared-memory barrier's phase.  Time is the SM's clock: the
+// global one takes longer to read than most waits last.
+struct Waiter {
+    volatile int *dead;
+    long long limit;  // cycles
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t phase) const {
+        long long began = 0;
+        for (int i = 1;; ++i) {
+            uint32_t done;
+            asm volatile(
+                "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                : "=r"(done) : "r"(bar), "r"(phase) : "memory");
+            if (done) return true;
+            if ((i & 63) == 0) {
+                if (*dead) return false;
+                const long long now = clock64();
+                if (began == 0) began = now;
+                if (now - began > limit) {
+                    *dead = 1;
+                    return false;
+                }
             }
-            return;
         }
-        // bytes past a row's end and rows past V become zeros
-        const int from = chunk * (kChunk / 2) + (lane & 7) * 16, row_bytes = (int)((a.K + 1) / 2);
-        const int n = row_bytes - from >= 16 ? 16 : row_bytes > from ? row_bytes - from : 0;
-        for (int i = 0; i < 8; ++i) {
-            const int m = tile * kTileRows + 4 * i + (lane >> 3) < (int)a.V ? n : 0;
-            const uint8_t *s = m ? src + 4 * i * a.q_pitch : a.q;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + (i & 1 ? p1 : p0) + i * 512),
-                         "l"(s), "r"(m));
-        }
-    }
-    __device__ __forceinline__ void next(const MatvecArgs &a, int first, int end) {
-        if (++chunk == end)
-            seek(a, tile + 1, first);
-        else
-            src += kChunk / 2;
     }
 };
+
+__device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+// One thread of the warp, which runs as one, has a box of the weights copied to shared
+// memory at dst; `bar` is told of its bytes.
+__device__ __forceinline__ void copy_box(const CUtensorMap &map, int byte, int row, uint32_t dst, uint32_t bar,
+                                         uint32_t bytes) {
+    asm volatile(
+        "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%4], %5;\n"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+        "l"(&map), "r"(byte), "r"(row), "r"(bar), "r"(bytes)
+        : "memory");
+}
 
 __device__ __forceinline__ float scale_value(uint32_t raw, int dtype) {
     if (dtype == CK_F32) return __uint_as_float(raw);
@@ -224,6 +223,32 @@ __device__ __forceinline__ void store_y(const MatvecArgs &a, int64_t m, int64_t 
         ((__nv_bfloat16 *)a.y)[at] = __float2bfloat16_rn(sum);
     else
         ((__half *)a.y)[at] = __float2half_rn(sum);
+}
+
+// Weights as a two-dimensional array of bytes, copied `rows` rows by 128 bytes at a
+// time with 16-byte pieces exchanged by the row (the 128-byte swizzle); zeros past its ends.
+inline cudaError_t weight_map(const MatvecArgs &a, int rows, CUtensorMap *map) {
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<Encode> known{nullptr};
+    Encode encode = known.load();
+    if (!encode) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+        known = encode = (Encode)f;
+    }
+    const cuuint64_t size[2] = {(cuuint64_t)((a.K + 1) / 2), (cuuint64_t)a.V}, pitch[1] = {(cuuint64_t)a.q_pitch};
+    const cuuint32_t box[2] = {kChunk / 2, (cuuint32_t)rows}, one[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)a.q, size, pitch, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
 }
 
 // The product for more columns than k_matvec takes (int4_wide.cu): rows of x in one

@@ -23,8 +23,6 @@
 // (4 x 32).  Registers move from warps 8-19 to warps 0-7, whose sums take 96.  Every
 // wait is bounded: one that gives up makes all others give up, and the CTA's outputs
 // NaN.
-#include <cuda.h>
-
 #include "int4.h"
 
 namespace ck {
@@ -50,35 +48,6 @@ struct WidePlan {
     int extra;                 // test hook: arrivals that never come
 };
 
-// Bounded wait on a shared-memory barrier's phase.  Time is the SM's clock: the
-// global one takes longer to read than most waits last.
-struct Waiter {
-    volatile int *dead;
-    long long limit;  // cycles
-    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t phase) const {
-        long long began = 0;
-        for (int i = 1;; ++i) {
-            uint32_t done;
-            asm volatile(
-                "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-                : "=r"(done) : "r"(bar), "r"(phase) : "memory");
-            if (done) return true;
-            if ((i & 63) == 0) {
-                if (*dead) return false;
-                const long long now = clock64();
-                if (began == 0) began = now;
-                if (now - began > limit) {
-                    *dead = 1;
-                    return false;
-                }
-            }
-        }
-    }
-};
-
-__device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
 __device__ __forceinline__ void barrier_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -251,14 +220,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 const int slot = i % kRing;
                 if (i >= kRing) ok = __all_sync(~0u, wait(w_empty(slot), (uint32_t)(i / kRing - 1) & 1));
                 if (!ok) break;
-                asm volatile(
-                    "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
-                    "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%4], %5;\n"
-                    "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-                    "[%0], [%1, {%2, %3}], [%4];\n}" ::"r"(smem_at(ring) + slot * kWeights),
-                    "l"(&weights), "r"((c0 + i) * (kChunk / 2)), "r"((int)block * kWideRows), "r"(w_full(slot)),
-                    "r"(kWeights)
-                    : "memory");
+                copy_box(weights, (c0 + i) * (kChunk / 2), (int)block * kWideRows, smem_at(ring) + slot * kWeights,
+                         w_full(slot), kWeights);
             }
             for (int k = i > kRing ? i - kRing : 0; !ok && k < i; ++k) last_wait(w_full(k % kRing), (uint32_t)(k / kRing) & 1);
         } else if (warp == 2 * kWorkers + 2) {
@@ -450,38 +413,12 @@ WidePlan wide_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms) {
     return p;
 }
 
-// Weights as a two-dimensional array of bytes, copied 256 rows by 128 bytes at a time
-// with 16-byte pieces exchanged by the row (the 128-byte swizzle); zeros past its ends.
-cudaError_t weight_map(const MatvecArgs &a, CUtensorMap *map) {
-    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static std::atomic<Encode> known{nullptr};
-    Encode encode = known.load();
-    if (!encode) {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        const cudaError_t e =
-            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
-        if (e != cudaSuccess) return e;
-        if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
-        known = encode = (Encode)f;
-    }
-    const cuuint64_t size[2] = {(cuuint64_t)((a.K + 1) / 2), (cuuint64_t)a.V}, pitch[1] = {(cuuint64_t)a.q_pitch};
-    const cuuint32_t box[2] = {kChunk / 2, kWideRows}, one[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)a.q, size, pitch, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
-}
-
 template <bool HALF, int GROUP, int N>
 cudaError_t run(const MatvecArgs &a, const WidePlan &p, char *images, float *partial, cudaStream_t stream) {
     static std::atomic<uint64_t> told{0};
     cudaError_t e = allow_smem((const void *)k_wide<HALF, GROUP, N>, (int)p.smem, told);  // N says how much
     CUtensorMap weights;
-    if (e == cudaSuccess) e = weight_map(a, &weights);
+    if (e == cudaSuccess) e = weight_map(a, kWideRows, &weights);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.blocks * p.splits));
