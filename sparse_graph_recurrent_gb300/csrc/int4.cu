@@ -24,8 +24,13 @@ namespace {
 // last tile may be shared with its neighbours: those sums meet in shared memory
 // and, where a tile crosses CTAs or slabs, in the slots of `partial`, which
 // k_join adds up in a fixed order.
-constexpr int kWarpsMv = 12;                // warps of a CTA, one CTA on an SM
-constexpr int kStages = 3;                  // ring of units per warp
+// Warps of a CTA, one CTA on an SM, and units of a warp's ring.  Twelve warps have 168
+// registers a thread and need no more; sixteen, with 128 and some spilled, keep more on
+// its way once a warp's run is long.  1 x 211,577 x 4,096 takes 104 us by twelve and
+// 95 by sixteen, 4 x 20,000 x 16,384 (a third of that run) 70 and 73, 1 x 5,000 x 256
+// 8.2 and 9.7.
+constexpr int kFewWarps = 12, kManyWarps = 16, kLongRun = 40;
+__host__ __device__ constexpr int ring_units(int warps) { return warps == kFewWarps ? 3 : 2; }
 constexpr int kHalf = 128;                  // scales are taken up for half a unit
 
 struct MatvecPlan {
@@ -34,6 +39,7 @@ struct MatvecPlan {
     int64_t chunks;    // chunks of K
     int64_t slabs;     // parts of K
     int64_t ctas;
+    int warps;         // of a CTA
     int aligned;       // one slab, and CTAs take whole tiles: nothing crosses them
     Deal chunk;        // chunks to slabs
     // Where there are no more slabs than CTAs, a CTA keeps to one slab, whose units
@@ -98,7 +104,7 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, const MatvecPlan &p
             at_m[i] = m;
             at_j[i] = j;
             if (m < p.rows) load8<T>(a, m, k0 + 8 * j, v[i]);
-            j += kWarpsMv * 32;
+            j += blockDim.x;
             settle();
         }
 #pragma unroll
@@ -125,22 +131,23 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, const MatvecPlan &p
     }
 }
 
-template <bool HALF, int GROUP, int NT>
-__global__ void __launch_bounds__(kWarpsMv * 32, 1)
+template <bool HALF, int GROUP, int NT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 1)
     k_matvec(const __grid_constant__ MatvecArgs a, const __grid_constant__ MatvecPlan p,
              const __grid_constant__ CUtensorMap weights) {
     extern __shared__ __align__(1024) char smem[];
-    __shared__ __align__(8) uint64_t bars[kWarpsMv * kStages];
+    constexpr int kStages = ring_units(WARPS);
+    __shared__ __align__(8) uint64_t bars[WARPS * kStages];
     __shared__ int dead;
     constexpr int kGroups = kHalf / GROUP;  // of half a unit
     // per warp: its ring, in which its last part of a sum is left when it is done; its
     // first part; scales and zero points of the eight groups at hand
     const int part_floats = kTileRows * p.rows;
-    float *heads = (float *)(smem + kWarpsMv * kStages * kUnitBytes);
-    float *all_scales = heads + kWarpsMv * part_floats;
-    uint8_t *all_zeros = (uint8_t *)(all_scales + kWarpsMv * kTileRows * 8);
-    int *part_tile = (int *)(all_zeros + kWarpsMv * kTileRows * 8);  // [warps][first, last]
-    char *xs = (char *)(part_tile + kWarpsMv * 2);
+    float *heads = (float *)(smem + WARPS * kStages * kUnitBytes);
+    float *all_scales = heads + WARPS * part_floats;
+    uint8_t *all_zeros = (uint8_t *)(all_scales + WARPS * kTileRows * 8);
+    int *part_tile = (int *)(all_zeros + WARPS * kTileRows * 8);  // [warps][first, last]
+    char *xs = (char *)(part_tile + WARPS * 2);
     const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0);  // known to be the warp's
     const int row = lane >> 2, quad = lane & 3;
     const uint32_t my_ring = smem_at(smem) + warp * kStages * kUnitBytes, my_bars = smem_at(bars) + warp * kStages * 8;
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1)
         }
         const int tile0 = (int)quotient(u0, sc), skip = (int)(u0 - (int64_t)tile0 * sc);
         const int span = (int)(u1 - u0);
-        const int w0 = (int)((int64_t)span * warp / kWarpsMv), w1 = (int)((int64_t)span * (warp + 1) / kWarpsMv);
+        const int w0 = (int)((int64_t)span * warp / WARPS), w1 = (int)((int64_t)span * (warp + 1) / WARPS);
         int n = w1 - w0, left = n;
         int t = tile0 + (skip + w0) / sc, c = (skip + w0) % sc;
         __syncthreads();  // the last slab's x and parts of sums are done with
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(kWarpsMv * 32, 1)
         }
         __syncthreads();
         // parts of one tile follow one another: the warp that holds the first adds them up
-        const int theirs = lane < 2 * kWarpsMv ? part_tile[lane] : -1;
+        const int theirs = lane < 2 * WARPS ? part_tile[lane] : -1;
         for (int k = 0; k < 2; ++k) {
             const int at = 2 * warp + k, tile = __shfl_sync(~0u, theirs, at);
             const uint32_t same = __ballot_sync(~0u, theirs == tile);
@@ -449,17 +456,19 @@ MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sm
     p.chunks = (K + kChunk - 1) / kChunk;
     // the columns in use lie below x_cols; the two spare ones of a tile take no memory
     p.x_cols = dtype == CK_F32 ? (int)(8 * ((rows - 1) / 2) + 6) : (int)rows;
-    const size_t fixed = (size_t)kWarpsMv * (kStages * kUnitBytes + kTileRows * (4 * rows + 40) + 8);
+    const int64_t units = p.tiles * p.chunks, by_tile = p.tiles < sms ? p.tiles : sms;
+    p.warps = p.x_cols <= 8 && units >= (int64_t)kLongRun * kFewWarps * sms ? kManyWarps : kFewWarps;
+    const size_t fixed =
+        (size_t)p.warps * (ring_units(p.warps) * kUnitBytes + kTileRows * (4 * rows + 40) + 8);
     const int64_t most = ((int64_t)(kSmemMost - fixed) / p.x_cols - 64) / (2 * kChunk);
     p.slabs = (p.chunks + most - 1) / most;
-    const int64_t units = p.tiles * p.chunks, by_tile = p.tiles < sms ? p.tiles : sms;
     // Whole tiles to each CTA, and no second kernel, or equal runs with one: a
     // unit takes an SM about 0.1 us, the second kernel about 2 us.
     const double unit = 0.1;
     const double whole = (double)((p.tiles + by_tile - 1) / by_tile) * p.chunks * unit;
     const double equal = (double)units / sms * unit + 2.0;
     p.aligned = p.slabs == 1 && whole <= equal;
-    const int64_t even = units / kWarpsMv;  // a unit for each warp at least
+    const int64_t even = units / p.warps;  // a unit for each warp at least
     p.ctas = p.aligned ? by_tile : even < 1 ? 1 : even < sms ? even : sms;
     // as many CTAs to every slab, or slabs to every CTA, by taking more of them
     if (p.slabs > 1) {
@@ -482,20 +491,20 @@ size_t partial_bytes(const MatvecPlan &p) {
     return p.aligned ? 0 : (size_t)(p.slabs * p.tiles + p.ctas) * kTileRows * p.rows * sizeof(float);
 }
 
-template <bool HALF, int GROUP, int NT>
+template <bool HALF, int GROUP, int NT, int WARPS>
 cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
     CUtensorMap weights;
     cudaError_t mapped = weight_map(a, kTileRows, &weights);
     if (mapped != cudaSuccess) return mapped;
     static std::atomic<uint64_t> told{0};
-    cudaError_t e = allow_smem((const void *)k_matvec<HALF, GROUP, NT>, (int)kSmemMost, told);
+    cudaError_t e = allow_smem((const void *)k_matvec<HALF, GROUP, NT, WARPS>, (int)kSmemMost, told);
     if (e != cudaSuccess) return e;
     for (int again = 0; again < 2; ++again) {
-        k_matvec<HALF, GROUP, NT><<<(unsigned)p.ctas, kWarpsMv * 32, p.smem, stream>>>(a, p, weights);
+        k_matvec<HALF, GROUP, NT, WARPS><<<(unsigned)p.ctas, WARPS * 32, p.smem, stream>>>(a, p, weights);
         e = cudaGetLastError();
         if (e != cudaErrorInvalidValue || again) break;
         told = 0;  // the device's context was reset since
-        e = allow_smem((const void *)k_matvec<HALF, GROUP, NT>, (int)kSmemMost, told);
+        e = allow_smem((const void *)k_matvec<HALF, GROUP, NT, WARPS>, (int)kSmemMost, told);
         if (e != cudaSuccess) return e;
     }
     if (e != cudaSuccess || p.aligned) return e;
@@ -513,7 +522,9 @@ cudaError_t launch_matvec(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t
 
 template <bool HALF, int GROUP>
 cudaError_t launch_columns(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
-    return p.x_cols <= 8 ? launch_matvec<HALF, GROUP, 1>(a, p, stream) : launch_matvec<HALF, GROUP, 2>(a, p, stream);
+    return p.x_cols > 8            ? launch_matvec<HALF, GROUP, 2, kFewWarps>(a, p, stream)
+           : p.warps == kFewWarps ? launch_matvec<HALF, GROUP, 1, kFewWarps>(a, p, stream)
+                                  : launch_matvec<HALF, GROUP, 1, kManyWarps>(a, p, stream);
 }
 
 template <int GROUP> cudaError_t launch_group(const MatvecArgs &a, const MatvecPlan &p, cudaStream_t stream) {
