@@ -24,6 +24,8 @@ namespace {
 // last tile may be shared with its neighbours: those sums meet in shared memory
 // and, where a tile crosses CTAs or slabs, in the slots of `partial`, which
 // k_join adds up in a fixed order.
+constexpr int kHalf = 128;  // columns: scales are taken up for half a unit
+
 // Warps of a CTA, one CTA on an SM, and units of a warp's ring.  Twelve warps have 168
 // registers a thread and need no more; sixteen, with 128 and some spilled, keep more on
 // its way once a warp's run is long.  1 x 211,577 x 4,096 takes 104 us by twelve and
@@ -31,7 +33,14 @@ namespace {
 // 8.2 and 9.7.
 constexpr int kFewWarps = 12, kManyWarps = 16, kLongRun = 40;
 __host__ __device__ constexpr int ring_units(int warps) { return warps == kFewWarps ? 3 : 2; }
-constexpr int kHalf = 128;                  // scales are taken up for half a unit
+
+// Tables of scales and zero points: a second one, filled in the middle of a unit while
+// the first is in use, where groups are short (a table a unit) or runs long, and x
+// leaves room.  1 x 200,000 x 4,096 in groups of 32 takes 221 us with one and 170 with
+// two, 1 x 211,577 x 4,096 in groups of 128 96 and 94; but 1 x 5,000 x 256 8.2 and 9.4.
+__host__ __device__ constexpr int tables(int column_tiles, int group, int warps) {
+    return column_tiles == 1 && (group == 32 || warps == kManyWarps) ? 2 : 1;
+}
 
 struct MatvecPlan {
     int rows;          // rows of x in this launch
@@ -141,12 +150,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     __shared__ int dead;
     constexpr int kGroups = kHalf / GROUP;  // of half a unit
     // per warp: its ring, in which its last part of a sum is left when it is done; its
-    // first part; scales and zero points of the eight groups at hand
+    // first part; scales and zero points of eight groups
     const int part_floats = kTileRows * p.rows;
     float *heads = (float *)(smem + WARPS * kStages * kUnitBytes);
-    float *all_scales = heads + WARPS * part_floats;
-    uint8_t *all_zeros = (uint8_t *)(all_scales + WARPS * kTileRows * 8);
-    int *part_tile = (int *)(all_zeros + WARPS * kTileRows * 8);  // [warps][first, last]
+    constexpr int kTables = tables(NT, GROUP, WARPS);
+    float *all_scales = heads + WARPS * part_floats;  // [warps][tables][rows][8]
+    uint8_t *all_zeros = (uint8_t *)(all_scales + WARPS * kTables * kTileRows * 8);
+    int *part_tile = (int *)(all_zeros + WARPS * kTables * kTileRows * 8);  // [warps][first, last]
     char *xs = (char *)(part_tile + WARPS * 2);
     const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0);  // known to be the warp's
     const int row = lane >> 2, quad = lane & 3;
@@ -161,8 +171,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     int get = 0, get_round = 0, put = 0, under_way = 0;
     bool ok = true;
     const uint32_t my_line = lane * 128, my_swap = (lane & 7) << 4;
-    float *my_scales = all_scales + warp * kTileRows * 8;
-    uint8_t *my_zeros = all_zeros + warp * kTileRows * 8;
+    float *my_scales = all_scales + warp * kTables * kTileRows * 8;
+    uint8_t *my_zeros = all_zeros + warp * kTables * kTileRows * 8;
     auto part_at = [&](int w, int k) {
         return k ? (float *)(smem + w * kStages * kUnitBytes) : heads + w * part_floats;
     };
@@ -208,10 +218,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             --left;
         };
         for (int i = 0; i < kStages; ++i) copy_next();
-        ScaleReader<8> next;
+        ScaleReader<8> next{};
         constexpr int kUnits = 8 * GROUP / kChunk, kAhead = 4;  // units of eight groups
+        // the eight groups after those that `next` holds, and a line of some further on
+        auto load_next = [&] {
+            int t1 = next.tile, e1 = next.eight + 1;
+            if (e1 * kUnits >= first + sc) ++t1, e1 = first / kUnits;
+            next.load(a, t1, e1, groups);  // past the last tile: nothing
+            int t2 = t1, e2 = e1 + kAhead;
+            if (e2 * kUnits >= first + sc) ++t2, e2 += first / kUnits - (first + sc + kUnits - 1) / kUnits;
+            ScaleReader<8>::ahead(a, t2, e2, groups, e2 == first / kUnits);
+        };
+        int table = 0;  // of the eight groups at hand
         if (n > 0) next.load(a, t, (first + c) / kUnits, groups);
-        bool begin = true;  // the next unit is the first of its eight groups here
         if (lane < 2) part_tile[2 * warp + lane] = -1;
         if constexpr (HALF)
             stage_x<__half>(a, p, first * kChunk, sc * (kChunk / 8), xs);
@@ -220,23 +239,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         else
             stage_x<__nv_bfloat16>(a, p, first * kChunk, sc * (kChunk / 8), xs);
         __syncthreads();
+        if (n > 0) {
+            next.leave(a, my_scales, my_zeros);
+            load_next();
+            __syncwarp();
+        }
         float acc[NT][2][4] = {};  // [.][rows 0-15, 16-31][.]
         bool from_start = c == 0;  // this tile's part began with the slab
         for (; n > 0; --n) {
             ok = __all_sync(~0u, ok && wait(my_bars + 8 * get, get_round & 1));
             const bool whole = c + 1 == sc;
-            if (begin) {
-                next.leave(a, my_scales, my_zeros);
-                int t1 = t, e1 = next.eight + 1;
-                if (e1 * kUnits >= first + sc) ++t1, e1 = first / kUnits;
-                next.load(a, t1, e1, groups);  // past the last tile: nothing
-                int t2 = t1, e2 = e1 + kAhead;
-                if (e2 * kUnits >= first + sc) ++t2, e2 += first / kUnits - (first + sc + kUnits - 1) / kUnits;
-                ScaleReader<8>::ahead(a, t2, e2, groups, e2 == first / kUnits);
-                __syncwarp();
-            }
             const int in_eight = (first + c) & (kUnits - 1);
-            begin = whole || in_eight == kUnits - 1;
+            const bool turn = whole || in_eight == kUnits - 1;  // the next unit has other eight groups
+            const float *scales = my_scales + table * kTileRows * 8;
+            const uint8_t *zero_points = my_zeros + table * kTileRows * 8;
             const uint32_t lines = my_ring + get * kUnitBytes + my_line;
             if (ok) {
                 --under_way;
@@ -245,20 +261,26 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             const char *xc = xs + c * (2 * kChunk);
 #pragma unroll
             for (int half = 0; half < kChunk / kHalf; ++half) {
+                if (kTables == 2 && half == 1 && turn && n > 1) {
+                    // in the middle of a unit, whose products go on meanwhile
+                    table ^= 1;
+                    next.leave(a, my_scales + table * kTileRows * 8, my_zeros + table * kTileRows * 8);
+                    load_next();
+                }
                 float scale[4][kGroups];  // of rows row + 8 h
                 uint32_t zeros[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     const int at = (row + 8 * h) * 8 + (2 * in_eight + half) * kGroups;
                     if constexpr (kGroups == 4) {
-                        *(float4 *)scale[h] = *(const float4 *)(my_scales + at);
-                        zeros[h] = *(const uint32_t *)(my_zeros + at);
+                        *(float4 *)scale[h] = *(const float4 *)(scales + at);
+                        zeros[h] = *(const uint32_t *)(zero_points + at);
                     } else if constexpr (kGroups == 2) {
-                        *(float2 *)scale[h] = *(const float2 *)(my_scales + at);
-                        zeros[h] = *(const uint16_t *)(my_zeros + at);
+                        *(float2 *)scale[h] = *(const float2 *)(scales + at);
+                        zeros[h] = *(const uint16_t *)(zero_points + at);
                     } else {
-                        scale[h][0] = my_scales[at];
-                        zeros[h] = my_zeros[at];
+                        scale[h][0] = scales[at];
+                        zeros[h] = zero_points[at];
                     }
                 }
                 float part[NT][2][4];
@@ -307,6 +329,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             }
             __syncwarp();  // the unit is read
             copy_next();
+            if (kTables == 1 && turn && n > 1) {
+                next.leave(a, my_scales, my_zeros);
+                load_next();
+                __syncwarp();
+            }
             if (whole || n == 1) {  // this tile's part ends here
                 if (!HALF && a.dtype == CK_F32) {
                     // the three parts of x lie in lanes quad 0, 1 and 2: smallest first
@@ -449,7 +476,7 @@ int64_t rows_of_pass(int64_t dtype, int64_t left) {
     return left < wide_rows(dtype) ? left : wide_rows(dtype);
 }
 
-MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sms) {
+MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int64_t group, int sms) {
     MatvecPlan p{};
     p.rows = (int)rows;
     p.tiles = (V + kTileRows - 1) / kTileRows;
@@ -458,8 +485,9 @@ MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int sm
     p.x_cols = dtype == CK_F32 ? (int)(8 * ((rows - 1) / 2) + 6) : (int)rows;
     const int64_t units = p.tiles * p.chunks, by_tile = p.tiles < sms ? p.tiles : sms;
     p.warps = p.x_cols <= 8 && units >= (int64_t)kLongRun * kFewWarps * sms ? kManyWarps : kFewWarps;
+    const int scale_tables = tables(p.x_cols > 8 ? 2 : 1, (int)group, p.warps);
     const size_t fixed =
-        (size_t)p.warps * (ring_units(p.warps) * kUnitBytes + kTileRows * (4 * rows + 40) + 8);
+        (size_t)p.warps * (ring_units(p.warps) * kUnitBytes + kTileRows * (4 * rows + 40 * scale_tables) + 8);
     const int64_t most = ((int64_t)(kSmemMost - fixed) / p.x_cols - 64) / (2 * kChunk);
     p.slabs = (p.chunks + most - 1) / most;
     // Whole tiles to each CTA, and no second kernel, or equal runs with one: a
@@ -643,7 +671,7 @@ extern "C" ck_status ck_int4_matvec(const void *x, int64_t dtype, int64_t M, int
             e = launch_wide(a, group, workspace, sms, st);
             continue;
         }
-        const MatvecPlan p = matvec_plan(dtype, rows, K, V, sms);
+        const MatvecPlan p = matvec_plan(dtype, rows, K, V, group, sms);
         e = group == 32 ? launch_group<32>(a, p, st) : group == 64 ? launch_group<64>(a, p, st)
                                                                   : launch_group<128>(a, p, st);
     }
@@ -662,7 +690,7 @@ extern "C" ck_status ck_int4_workspace_size(int64_t dtype, int64_t M, int64_t K,
     for (int64_t m = 0; m < M;) {
         const int64_t rows = rows_of_pass(dtype, M - m);
         const size_t b = rows > rows_at_once(dtype) ? wide_workspace(dtype, rows, K, V, sms)
-                                                    : partial_bytes(matvec_plan(dtype, rows, K, V, sms));
+                                                    : partial_bytes(matvec_plan(dtype, rows, K, V, group, sms));
         if (b > *bytes) *bytes = b;
         m += rows == wide_rows(dtype) ? (M - m) / rows * rows : rows;
     }
