@@ -11,7 +11,9 @@ namespace {
 
 // Threads of a CTA: four CTAs of the first kind fill an SM's registers, one of the second.
 constexpr int kThreads1 = 256, kThreads4 = 1024, kLogitCtas = 4;
-constexpr int kTile = 8192;   // most tokens of a CTA, whose counts it holds in shared memory
+// Most tokens of a CTA, whose counts it holds in shared memory: in 16 bits each where the
+// history is too short to count further, else in 32.
+constexpr int kTile = 16256, kTileWide = 8064, kNarrow = 32767;
 constexpr int kOct = 8;       // tokens a thread takes at a time
 
 enum Pick { kNone, kGreedy, kSample };
@@ -59,39 +61,75 @@ __device__ __forceinline__ float log2_fast(float v) {
     return r;
 }
 
-// count[v - t0] for the tokens t0 <= v < t1 of history[0 .. len): twice the number
-// of occurrences from `prompt` on, odd or not zero where the token was seen at all.
-// Additions of integers: their order does not matter.
-template <int THREADS, typename I>
-__device__ __forceinline__ void count_history(const I *h, int64_t len, int64_t prompt, int64_t t0, int64_t t1,
-                                              uint32_t *count) {
-    using U = std::make_unsigned_t<I>;
-    constexpr int kPer = 16 / (int)sizeof(I), kBatch = 8;  // ids of a load, loads on their way at once
-    const U first = (U)t0, span = (U)(t1 - t0);  // t1 < 2^31
-    auto take = [&](I id, int64_t i) {
-        const U at = (U)id - first;
-        if (at >= span) return;
-        if (i >= prompt)
-            atomicAdd(&count[at], 2u);  // seen, and made here
+// Counts of the tokens that a CTA looks after: twice the number of occurrences in the
+// history from `prompt` on, odd or not zero where the token was seen at all.  Additions
+// of integers: their order does not matter.
+struct Counts {
+    uint32_t *slots;
+    bool narrow;
+    template <bool NARROW> __device__ __forceinline__ void put(uint32_t at, bool made) const {
+        uint32_t *word = slots + (NARROW ? at >> 1 : at);
+        const int up = NARROW ? (at & 1) * 16 : 0;
+        if (made)
+            atomicAdd(word, 2u << up);  // seen, and made here
         else
-            atomicOr(&count[at], 1u);
+            atomicOr(word, 1u << up);
+    }
+    __device__ __forceinline__ uint32_t at(int o) const {
+        return narrow ? ((const uint16_t *)slots)[o] : slots[o];
+    }
+    // a bit for each token of an oct that was seen
+    __device__ __forceinline__ uint32_t seen(int o) const {
+        uint32_t hit = 0;
+        if (narrow) {
+            const uint4 c = ((const uint4 *)slots)[o / 8];
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                hit |= (uint32_t)((w[j] & 0xffff) != 0) << 2 * j | (uint32_t)(w[j] > 0xffff) << (2 * j + 1);
+        } else {
+            const uint4 c0 = ((const uint4 *)slots)[o / 4], c1 = ((const uint4 *)slots)[o / 4 + 1];
+            const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) hit |= (uint32_t)(w[j] != 0) << j;
+        }
+        return hit;
+    }
+};
+
+// Counts the tokens first <= v < first + span of history[0 .. len), len <= most, in slots
+// from `slot` on.  The first ids are asked for before len is known; begin() empties the
+// slots and says what len and prompt are.
+template <int THREADS, bool NARROW, typename I, typename Begin>
+__device__ __forceinline__ void count_history(const I *h, int most, uint32_t first, uint32_t span,
+                                              const Counts &counts, int slot, Begin begin) {
+    constexpr int kPer = 16 / (int)sizeof(I), kBatch = 4;  // ids of a load, loads on their way at once
+    int len = 0, prompt = 0;
+    auto take = [&](I id, int i) {
+        const uint32_t at = (uint32_t)id - first;
+        if ((sizeof(I) == 4 || (uint64_t)id >> 32 == 0) && at < span && i < len)
+            counts.put<NARROW>(slot + at, i >= prompt);
     };
     // single ids up to a 16-byte boundary and after the last
-    int64_t head = (int64_t)((16 - ((uintptr_t)h & 15)) & 15) / (int64_t)sizeof(I);
-    if (head > len) head = len;
-    const int64_t pieces = (len - head) / kPer, tail = head + pieces * kPer;
-    if (threadIdx.x < head) take(h[threadIdx.x], threadIdx.x);
-    if (threadIdx.x < len - tail) take(h[tail + threadIdx.x], tail + threadIdx.x);
+    int head = (int)((16 - ((uintptr_t)h & 15)) & 15) / (int)sizeof(I);
+    if (head > most) head = most;
+    const int pieces = (most - head) / kPer, tail = head + pieces * kPer;
     const uint4 *body = (const uint4 *)(h + head);
-    for (int64_t i0 = threadIdx.x; i0 < pieces; i0 += kBatch * THREADS) {
+    for (int base = 0; base == 0 || (base < pieces && head + base * kPer < len); base += kBatch * THREADS) {
+        const int i0 = base + threadIdx.x;
         uint4 v[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
             if (i0 + k * THREADS < pieces) v[k] = __ldg(body + i0 + k * THREADS);
+        if (base == 0) {
+            begin(len, prompt);
+            if (threadIdx.x < head) take(__ldg(h + threadIdx.x), threadIdx.x);
+            if (threadIdx.x < most - tail) take(__ldg(h + tail + threadIdx.x), tail + threadIdx.x);
+        }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int64_t i = i0 + k * THREADS;
-            if (i >= pieces) break;
+            const int i = i0 + k * THREADS;
+            if (i >= pieces || head + i * kPer >= len) break;
             I id[kPer];
             memcpy(id, &v[k], 16);
 #pragma unroll
@@ -111,11 +149,13 @@ struct LogitPlan {
 // k_pick looks through.
 //
 // What bounds it at large sizes is arithmetic: a token drawn costs a word of the
-// generator and two logarithms.  The logarithms are spared: as -log1p(-u) >= u, the
-// noise is at most -log u, which one approximate logarithm of a number no larger
-// than u bounds from above; a bound from below for a lane's likeliest token gives a
-// score that the CTA's best has at least.  Only tokens that may reach it are scored as
-// defined, and a lane puts its one off to the end, when few are left.
+// generator, two logarithms and a division by the temperature.  All but the first are
+// spared: as -log1p(-u) >= u, the noise is at most -log u, so a product and one
+// approximate logarithm bound a score from above; a bound from below for a lane's
+// likeliest token gives a score that the CTA's best has at least.  Only tokens that may
+// reach it are scored as defined, and a lane puts its one off to the end, when few are
+// left.  Bounds are a quarter of scores, which cannot overflow before the scores do,
+// and leave out the scale of a word: log u = log word - 32 log 2.
 template <typename T, int PICK, int THREADS>
 __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
     k_logits(const __grid_constant__ ck_logit_call a, const __grid_constant__ PhiloxKeys keys, LogitPlan plan,
@@ -123,10 +163,10 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
     extern __shared__ __align__(16) uint32_t count[];
     __shared__ uint32_t floor_key;  // a score that some token of the CTA has at least
     __shared__ unsigned long long best_cta;
-    const int64_t b = blockIdx.x / plan.slices;
-    const int slice = (int)(blockIdx.x - b * plan.slices);
+    const int64_t b = blockIdx.x / (unsigned)plan.slices;
+    const int slice = (int)(blockIdx.x - (unsigned)b * plan.slices);
     const int64_t t0 = slice * plan.slice, t1 = t0 + plan.slice < a.V ? t0 + plan.slice : a.V;
-    if (PICK != kNone && threadIdx.x == 0) best_cta = 0, floor_key = 0;
+    if (threadIdx.x == 0) best_cta = 0, floor_key = 0;
     const int64_t e0 = b * a.V;
     const T *row_in = (const T *)a.logits + b * a.logits_stride;
     // octs begin at tokens v with (v + cut) % 8 == 0; the oct at offset o holds tokens
@@ -134,42 +174,73 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
     const int cut = PICK == kSample ? (int)(e0 & 7) : (int)(((uintptr_t)row_in / sizeof(T)) & 7);
     const int64_t v0 = t0 - cut;
     const int from = cut, to = cut + (int)(t1 - t0), octs = (to + kOct - 1) / kOct;
-    const int64_t len = a.history ? row_len(a.history_len, a.history_bits, b, a.L) : 0;
-    if (len > 0) {
-        const int64_t prompt = a.prompt_len ? row_len(a.prompt_len, a.history_bits, b, a.L) : 0;
-        for (int i = threadIdx.x; i < octs * 2; i += THREADS) ((uint4 *)count)[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-        if (a.history_bits == 32)
-            count_history<THREADS>((const int32_t *)a.history + b * a.history_stride, len, prompt, t0, t1, count + cut);
-        else
-            count_history<THREADS>((const int64_t *)a.history + b * a.history_stride, len, prompt, t0, t1, count + cut);
-    }
-    __syncthreads();
-    Row row;
-    row.rep = a.repetition ? a.repetition[b] : a.repetition_all;
-    row.freq = a.frequency ? a.frequency[b] : a.frequency_all;
-    row.pres = a.presence ? a.presence[b] : a.presence_all;
-    row.temp = a.temperature ? a.temperature[b] : a.temperature_all;
-    const bool heat = row.temp > 0.f, noisy = PICK == kSample && heat;
-    const float cool = heat ? 1.f / row.temp : 1.f;
-    const uint64_t step = PICK == kSample ? keys.at() : 0;
     const T *in = row_in + v0;
     T *out = a.out ? (T *)a.out + b * a.out_stride + v0 : nullptr;
     const float *bias = a.bias ? a.bias + b * a.bias_stride + v0 : nullptr;
     const uint32_t *mask = a.mask ? (const uint32_t *)a.mask + b * a.mask_stride : nullptr;
     const bool in_vec = ((uintptr_t)in & 15) == 0, out_vec = ((uintptr_t)out & 15) == 0,
                bias_vec = ((uintptr_t)bias & 15) == 0;
+    // a thread's next oct, if it is all there: asked for while the one before is at work
+    constexpr int kRaw = (int)sizeof(T) / 2;
+    uint4 raw[kRaw];
+    auto ask = [&](int ow) {
+        const int o = (ow + (int)(threadIdx.x & 31)) * kOct;
+        if (!in_vec || o < from || o + kOct > to) return;
+#pragma unroll
+        for (int i = 0; i < kRaw; ++i) raw[i] = __ldcs((const uint4 *)(in + o) + i);
+    };
+    const Counts counts{count, a.L <= kNarrow};
+    const bool history = a.history && a.L > 0;
+    if (history) {
+        auto begin = [&](int &len, int &prompt) {
+            len = (int)row_len(a.history_len, a.history_bits, b, a.L);
+            prompt = a.prompt_len ? (int)row_len(a.prompt_len, a.history_bits, b, a.L) : 0;
+            const int quads = counts.narrow ? octs : 2 * octs;
+            for (int i = threadIdx.x; i < quads; i += THREADS) ((uint4 *)count)[i] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
+        };
+        auto count_all = [&](auto *tag) {
+            const auto *h = (decltype(tag))a.history + b * a.history_stride;
+            if (counts.narrow)
+                count_history<THREADS, true>(h, (int)a.L, (uint32_t)t0, (uint32_t)(t1 - t0), counts, cut, begin);
+            else
+                count_history<THREADS, false>(h, (int)a.L, (uint32_t)t0, (uint32_t)(t1 - t0), counts, cut, begin);
+        };
+        if (a.history_bits == 32)
+            count_all((const int32_t *)nullptr);
+        else
+            count_all((const int64_t *)nullptr);
+    }
+    ask(threadIdx.x & ~31);
+    Row row;
+    row.rep = a.repetition ? a.repetition[b] : a.repetition_all;
+    row.freq = a.frequency ? a.frequency[b] : a.frequency_all;
+    row.pres = a.presence ? a.presence[b] : a.presence_all;
+    row.temp = a.temperature ? a.temperature[b] : a.temperature_all;
+    const uint64_t step = PICK == kSample ? keys.at() : 0;
+    __syncthreads();
+    const bool heat = row.temp > 0.f;
+    float cool = heat ? 1.f / row.temp : 1.f;
+    // where the reciprocal is not precise the division comes first of all
+    const float divide = !heat || (cool > 1e-37f && cool < 1e37f) ? 1.f : row.temp;
+    if (divide != 1.f) row.temp = cool = 1.f;
+    const float cool4 = cool * 0.25f;
+    const bool bounded = heat && (PICK == kSample || row.temp != 1.f);
     unsigned long long best = 0;
-    // sampling: a token that may be the one, to be scored when more is known; its logit
-    // before the temperature
+    // a token that may be the one, to be scored when more is known; its logit before
+    // the temperature
     float later_high = minus_inf(), later_z = 0.f;
     uint32_t later_word = 0;
     int later_o = 0;
     auto score_later = [&] {
-        const unsigned long long k =
-            pick_key(__fadd_rn(later_z / row.temp, gumbel(later_word)), (uint32_t)(v0 + later_o));
+        const float noise = PICK == kSample ? gumbel(later_word) : 0.f;
+        const unsigned long long k = pick_key(__fadd_rn(later_z / row.temp, noise), (uint32_t)(v0 + later_o));
         best = k > best ? k : best;
     };
+    // margins of bounds; NaN for what is -inf or NaN, and for +inf from below
+    constexpr float kLog = 0.25f * 0.69314718f;  // a quarter of log 2
+    auto above = [](float s) { return fmaf(fabsf(s), 1e-6f, s) + 1e-4f; };
+    auto below = [](float s) { return fmaf(fabsf(s), -1e-6f, s) - 1e-4f; };
     for (int ow = threadIdx.x & ~31; ow < octs; ow += THREADS) {
         const int o = (ow + (int)(threadIdx.x & 31)) * kOct;
         const bool full = o >= from && o + kOct <= to;
@@ -178,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
         if (full && in_vec) {
             alignas(16) T t[kOct];
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) ((uint4 *)t)[i] = __ldcs((const uint4 *)(in + o) + i);
+            for (int i = 0; i < kRaw; ++i) ((uint4 *)t)[i] = raw[i];
 #pragma unroll
             for (int j = 0; j < kOct; ++j) z[j] = to_float(t[j]);
         } else {
@@ -190,21 +261,27 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
                 there |= (uint32_t)is << j;
             }
         }
-        if (len > 0 && there) {
-            const uint4 c0 = ((const uint4 *)count)[o / 4], c1 = ((const uint4 *)count)[o / 4 + 1];
-            const uint32_t c[kOct] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-            uint32_t hit = 0;
-#pragma unroll
-            for (int j = 0; j < kOct; ++j) hit |= (uint32_t)(c[j] != 0) << j;
+        ask(ow + THREADS);
+        // asked for here and used below
+        float4 b0, b1;
+        if (bias && full && bias_vec) b0 = *(const float4 *)(bias + o), b1 = *(const float4 *)(bias + o + 4);
+        uint32_t allowed = ~0u;
+        if (mask && full) {
+            const int64_t v = v0 + o;
+            const uint32_t *w = mask + (v >> 5);
+            const int low = (int)(v & 31);
+            allowed = __funnelshift_r(w[0], low > 32 - kOct ? w[1] : 0u, low);
+        }
+        if (history && there) {
+            uint32_t hit = counts.seen(o);
             while (hit) {  // few: one by one
                 const int at = __ffs(hit) - 1;
                 hit &= hit - 1;
                 float zv = 0.f;
-                uint32_t cv = 0;
 #pragma unroll
                 for (int j = 0; j < kOct; ++j)
-                    if (j == at) zv = z[j], cv = c[j];
-                zv = row.penalised(zv, cv);
+                    if (j == at) zv = z[j];
+                zv = row.penalised(zv, counts.at(o + at));
 #pragma unroll
                 for (int j = 0; j < kOct; ++j)
                     if (j == at) z[j] = zv;
@@ -212,7 +289,6 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
         }
         if (bias) {
             if (full && bias_vec) {
-                const float4 b0 = *(const float4 *)(bias + o), b1 = *(const float4 *)(bias + o + 4);
                 const float bb[kOct] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
                 for (int j = 0; j < kOct; ++j) z[j] = __fadd_rn(z[j], bb[j]);
@@ -223,20 +299,19 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
             }
         }
         if (mask) {
-            uint32_t ok = 0;
-            if (full) {
-                const int64_t v = v0 + o;
-                const uint32_t *w = mask + (v >> 5);
-                const int low = (int)(v & 31);
-                ok = __funnelshift_r(w[0], low > 32 - kOct ? w[1] : 0u, low);
-            } else {
+            if (!full) {
+                allowed = 0;
 #pragma unroll
                 for (int j = 0; j < kOct; ++j)
-                    if (there >> j & 1) ok |= (mask[(v0 + o + j) >> 5] >> ((v0 + o + j) & 31) & 1u) << j;
+                    if (there >> j & 1) allowed |= (mask[(v0 + o + j) >> 5] >> ((v0 + o + j) & 31) & 1u) << j;
             }
 #pragma unroll
             for (int j = 0; j < kOct; ++j)
-                if (!(ok >> j & 1)) z[j] = minus_inf();
+                if (!(allowed >> j & 1)) z[j] = minus_inf();
+        }
+        if (divide != 1.f) {
+#pragma unroll
+            for (int j = 0; j < kOct; ++j) z[j] = z[j] / divide;
         }
         if (out) {
             // z / temperature, but for one more rounding: a division costs as much as the rest
@@ -253,36 +328,34 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
             }
         }
         if constexpr (PICK != kNone) {
-            if (!noisy) {
-                // dividing by a temperature keeps the order, but may make equal what was not
+            if (!bounded) {
                 float top = minus_inf();
                 int at = 0;
 #pragma unroll
-                for (int j = 0; j < kOct; ++j) {
-                    const float s = heat && row.temp != 1.f ? z[j] / row.temp : z[j];
-                    if (s > top) top = s, at = j;  // of equal ones the first; no NaN
-                }
+                for (int j = 0; j < kOct; ++j)
+                    if (z[j] > top) top = z[j], at = j;  // of equal ones the first; no NaN
                 const unsigned long long k = pick_key(top, (uint32_t)(v0 + o + at));
                 best = k > best ? k : best;
                 continue;
             }
-        }
-        if constexpr (PICK == kSample) {
-            uint4 r0, r1;
-            philox_two((uint64_t)(e0 + v0 + o) >> 2, step, keys, r0, r1);
-            const uint32_t w[kOct] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-            // a score is at most this (z / temperature as a product: its error is in the margin)
-            float high[kOct], top = minus_inf();
+            uint32_t w[kOct] = {};
+            if constexpr (PICK == kSample) {
+                uint4 r0, r1;
+                philox_two((uint64_t)(e0 + v0 + o) >> 2, step, keys, r0, r1);
+                w[0] = r0.x, w[1] = r0.y, w[2] = r0.z, w[3] = r0.w;
+                w[4] = r1.x, w[5] = r1.y, w[6] = r1.z, w[7] = r1.w;
+            }
+            // a score is at most above(s) (errors of products and logarithms, the word as
+            // a float and z / temperature as a product are in the margin)
+            float s[kOct], top = minus_inf();
 #pragma unroll
             for (int j = 0; j < kOct; ++j) {
-                const float u = __uint_as_float(0x3f800000u | w[j] >> 9) - 1.f;  // u or less
-                const float s = fmaf(z[j], cool, log2_fast(u) * -0.6931472f);
-                high[j] = fmaf(fabsf(s), 1e-6f, s + 1e-4f);
-                top = fmaxf(top, high[j]);
+                s[j] = PICK == kSample ? fmaf(log2_fast((float)w[j]), -kLog, z[j] * cool4) : z[j] * cool4;
+                top = fmaxf(top, s[j]);
             }
             const uint32_t seen = *(volatile uint32_t *)&floor_key;
             float floor = key_score((unsigned long long)seen << 32);
-            if (!__any_sync(~0u, top >= floor && top > minus_inf())) continue;
+            if (!__any_sync(~0u, above(top) >= floor)) continue;
             // A score that a lane's likeliest token has at least: with t >= u,
             // -log1p(-u) <= t / (1 - t).
             int at = -1;
@@ -290,22 +363,23 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
             uint32_t word = 0;
 #pragma unroll
             for (int j = 0; j < kOct; ++j)
-                if (high[j] == top) at = j, z_at = z[j], word = w[j];
-            if (top > minus_inf()) {
-                const float t = __uint_as_float(0x3f800000u | word >> 9) - (1.f - 2.384185791015625e-07f);
-                const float s = fmaf(z_at, cool, -0.6931472f * (log2_fast(t) - log2_fast(1.f - t)));
-                if (t < 0.5f) low = s - fmaf(fabsf(s), 1e-6f, 1e-4f);
+                if (s[j] == top) at = j, z_at = z[j], word = w[j];
+            if constexpr (PICK == kSample) {
+                const float t = fmaf((float)word, 1.0000003f, 1.f), rest = fmaf(t, -2.3283064365386963e-10f, 1.f);
+                if (rest > 0.5f) low = below(fmaf(log2_fast(rest) - log2_fast(t), kLog, z_at * cool4));
+            } else {
+                low = below(top);
             }
             // (an unsigned word in the order of floats, as pick_key's upper one)
-            const uint32_t warp_key = __reduce_max_sync(~0u, (uint32_t)(pick_key(low, 0) >> 32));
+            const uint32_t warp_key = __reduce_max_sync(~0u, at < 0 ? 0 : (uint32_t)(pick_key(low, 0) >> 32));
             if (warp_key > seen) {
                 if ((threadIdx.x & 31) == 0) atomicMax(&floor_key, warp_key);
                 floor = key_score((unsigned long long)warp_key << 32);
             }
-            while (top >= floor && top > minus_inf()) {
+            while (above(top) >= floor) {
                 // a token put off earlier, should it still be one to score, makes room
                 if (later_high >= floor && later_high > minus_inf()) score_later();
-                later_high = top;
+                later_high = above(top);
                 later_o = o + at;
                 later_z = z_at;
                 later_word = word;
@@ -313,15 +387,15 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
                 const int old = at;
 #pragma unroll
                 for (int j = 0; j < kOct; ++j) {
-                    if (j == old) high[j] = minus_inf();
-                    if (high[j] > top) top = high[j], at = j, z_at = z[j], word = w[j];
+                    if (j == old) s[j] = minus_inf();
+                    if (s[j] > top) top = s[j], at = j, z_at = z[j], word = w[j];
                 }
             }
         }
     }
     if constexpr (PICK != kNone) {
         __syncthreads();  // the floor is known
-        if (PICK == kSample && later_high > minus_inf() &&
+        if (later_high > minus_inf() &&
             later_high >= key_score((unsigned long long)floor_key << 32))
             score_later();
         for (int o = 16; o; o >>= 1) {
@@ -354,18 +428,19 @@ __global__ void __launch_bounds__(128) k_pick(const unsigned long long *keys, in
 }
 
 // Slices of a row: as many CTAs as the device holds at once, or a whole number of
-// times that, of kTile tokens at most.  A CTA reads all of its row's history, so
-// a slice is no smaller than a quarter of that; nor than 1,024 tokens.  Up to 8,192
-// tokens a row stays whole where one is picked: a second kernel costs more.
+// times that, of as many tokens at most as the table has room for.  A CTA reads all of
+// its row's history, so a slice is no smaller than a quarter of that; nor than 1,024
+// tokens.  Up to kTileWide tokens a row stays whole where one is picked: a second kernel
+// costs more.
 LogitPlan logit_plan(int64_t B, int64_t V, int64_t L, bool pick, int sms) {
-    const int64_t slots = (int64_t)sms * kLogitCtas;
-    const int64_t waves = (B * V + kTile * slots - 1) / (kTile * slots);
+    const int64_t slots = (int64_t)sms * kLogitCtas, tile = L <= kNarrow ? kTile : kTileWide;
+    const int64_t waves = (B * V + tile * slots - 1) / (tile * slots);
     int64_t slices = waves * slots / (B > 0 ? B : 1);
     int64_t least = L / 4 > 1024 ? L / 4 : 1024;
-    if (least > kTile) least = kTile;
+    if (least > tile) least = tile;
     if (slices > (V + least - 1) / least) slices = (V + least - 1) / least;
-    if (slices < (V + kTile - 1) / kTile) slices = (V + kTile - 1) / kTile;
-    if (pick && V <= kTile) slices = 1;
+    if (slices < (V + tile - 1) / tile) slices = (V + tile - 1) / tile;
+    if (pick && V <= kTileWide) slices = 1;
     const int64_t slice = ((V + slices - 1) / slices + 127) / 128 * 128;
     return LogitPlan{slice, (int)((V + slice - 1) / slice)};
 }
@@ -373,8 +448,7 @@ LogitPlan logit_plan(int64_t B, int64_t V, int64_t L, bool pick, int sms) {
 template <typename T, int PICK>
 cudaError_t launch_logits(const ck_logit_call &a, const PhiloxKeys &keys, const LogitPlan &plan,
                           cudaStream_t stream) {
-    const size_t smem =
-        a.history ? (size_t)((plan.slice < kTile ? plan.slice : kTile) + 2 * kOct) * sizeof(uint32_t) : 0;
+    const size_t smem = a.history ? (size_t)(plan.slice + 2 * kOct) * (a.L <= kNarrow ? 2 : 4) : 0;
     // Where CTAs are no more than SMs and have much to read, one takes a whole SM: 20
     // rows of 50,021 tokens with 32,768 of history take 19 us by 256 threads each.
     const unsigned ctas = (unsigned)(a.B * plan.slices);

@@ -310,3 +310,60 @@ def test_refusals():
     with pytest.raises(ValueError):
         ck.pick_tokens(x, seed=1, step=torch.tensor([1]))
     assert ck.pick_tokens(x[:0]).shape == (0,)
+
+
+def test_temperatures_at_the_ends_of_their_type():
+    """Where 1 / T is no normal number: z / T within an ulp of it, tokens as z / T + noise orders them."""
+    import sparse_graph_recurrent_gb300 as ck
+    temps = np.array([1e-39, 1e-44, 2.5e38, 3.4e38, np.inf, 1e37, 1e-37], np.float32)
+    B, V = len(temps), 300
+    rng = np.random.default_rng(8)
+    z = rng.standard_normal((B, V)).astype(np.float32)
+    z[:, ::7] = 0.0
+    z[0, :] = np.minimum(z[0], 0.0)  # the best is 0 / T
+    z[2] *= np.float32(1e38)
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = z / temps[:, None]
+    x, t = torch.from_numpy(z).cuda(), torch.from_numpy(temps).cuda()
+    got = ck.control_logits(x, temperature=t).cpu().numpy()
+    fin = np.isfinite(want)
+    assert np.array_equal(got[~fin], want[~fin])
+    assert (np.abs(got - want)[fin] <= 2.0 ** -22 * np.abs(want)[fin] + 2.0 ** -148).all()
+    assert ck.pick_tokens(x, temperature=t).cpu().tolist() == want.argmax(1).tolist()
+    score = want.astype(np.float64) + ro.gumbel(B, V, 9, 2)
+    tokens = ck.pick_tokens(x, temperature=t, seed=9, step=2).cpu().numpy()
+    for b in range(B):
+        best = score[b].max()
+        assert score[b, tokens[b]] == best or best - score[b, tokens[b]] < 1e-5, b
+
+
+@pytest.mark.parametrize("L", [32767, 32768, 40000])
+@pytest.mark.parametrize("ints", [np.int32, np.int64])
+def test_one_token_all_along_a_long_history(L, ints):
+    """Counts up to the history's length, on both sides of where they are kept in more bits."""
+    import sparse_graph_recurrent_gb300 as ck
+    V, token = 9001, 8070
+    x = torch.zeros(2, V)
+    x[:, token] = 3.0
+    history = torch.full((2, L), token, dtype=torch.from_numpy(np.zeros(1, ints)).dtype)
+    prompt = torch.tensor([0, L - 1], dtype=history.dtype)
+    out = ck.control_logits(x.cuda(), history=history.cuda(), prompt_len=prompt.cuda(), repetition=2.0,
+                            frequency=0.5, presence=0.25).cpu()
+    assert out[0, token] == 1.5 - (L * 0.5 + 0.25) and out[1, token] == 1.5 - 0.75
+    out[:, token] = 0.0
+    assert not out.any()
+
+
+@pytest.mark.parametrize("V", [8064, 8065, 16256, 16257, 33000])
+@pytest.mark.parametrize("dtype", list(ULP))
+def test_many_rows_and_equal_scores(V, dtype):
+    """Whole waves of rows; half of a row shares its highest logit: the lowest index, at any temperature."""
+    import sparse_graph_recurrent_gb300 as ck
+    B = 700
+    x = torch.zeros(B, V, dtype=dtype)
+    first = torch.arange(B) * 11 % (V // 2)
+    top = torch.arange(V)[None, :] >= first[:, None]
+    x[top] = 5.0
+    for temperature in (1.0, 0.7, 0.0):
+        tokens = ck.pick_tokens(x.cuda(), temperature=temperature)
+        assert torch.equal(tokens.cpu(), first)
