@@ -364,9 +364,8 @@ ck_status ck_dropout(const void *x, void *y, int64_t dtype, int64_t n0, int64_t 
  *            dtype, M, K, V and group on this device, 16-byte aligned; its contents need
  *            no setting and mean nothing afterwards; NULL when that is 0 bytes
  * An x row that holds an infinity or NaN gives outputs that are not finite.
- * Batches of more rows than 4 (32-bit x) or 16 run on kernels with device-side waits,
- * bounded by CK_OPT_BARRIER_TIMEOUT_NS; one that gives up (it never should) leaves NaN
- * in y.
+ * The kernels wait on the device for their own copies, at most CK_OPT_BARRIER_TIMEOUT_NS
+ * at a time; a wait that gives up (it never should) leaves NaN in y.
  * Sums are added up in an order that depends on the sizes and the device alone.
  * Asynchronous.  Errors: CK_ERR_INVALID_ARG (types, group, sizes, alignment,
  * short strides, NULL pointers), CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED (a size of 2^30 or more),
@@ -405,7 +404,7 @@ ck_status ck_int4_quantize(const void *w, int64_t dtype, int64_t V, int64_t K, i
  *   3. z + bias[v]
  *   4. -inf where bit v % 32 of mask word v / 32 is 0
  *   5. z / temperature where temperature > 0 (in `out` the product with 1 /
- *      temperature, one rounding more)
+ *      temperature, one rounding more, where that is a normal number)
  * Ids outside [0, V) in the history are ignored (padding).  len_b and prompt_b
  * are clamped to [0, L].  out[b][v] = z, rounded to the logits' type.
  * tokens[b] = the v of the largest z (of equal ones the lowest v), before

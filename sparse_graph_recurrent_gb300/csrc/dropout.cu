@@ -51,9 +51,14 @@ __global__ void __launch_bounds__(256) k_dropout(const __grid_constant__ DropArg
 
 // Where x's innermost axis is dense and y is dense and aligned, a thread takes 16
 // bytes of y: E elements whose words are those of E / 4 of the generator's blocks,
-// as y is dense in the order of the mask.  What bounds it is memory, 2 bytes
-// read and written twice over for each 16-bit element, with the generator close behind:
-// a block is twenty 32 x 32 -> 64 bit products for four elements.
+// as y is dense in the order of the mask.  What bounds it is memory, every element read
+// and written once, with the generator close behind: a block is twenty 32 x 32 -> 64
+// bit products for four elements, of which an SM does 0.1 a nanosecond for each of 32 lanes.
+//
+// Measured: k_dropout_dense on 32 x 256 x 20,000 bf16 131 us (5.0 TB/s; the blocks alone
+// 86), k_dropout_lines on 64 x 32 x 5,000 fp32 with one mask 14 us (5.8 TB/s),
+// k_dropout_flat on 32 x 20 x 4,999 fp16 cut out of wider rows 6.5 us (1.95 TB/s: a
+// start, one way to memory and back, and an end), 8 x 8 x 256 fp32 1.5 us.
 constexpr int kDropThreads = 256;
 
 template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
