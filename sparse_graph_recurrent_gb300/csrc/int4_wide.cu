@@ -14,7 +14,8 @@
 //                fetched, scaled and added up in registers
 //   warps 8-15   a weight row a lane: 64 columns of K at a time are unpacked into one
 //                of two buffers of tensor memory
-//   warp 16      waits for A and B and issues the products
+//   warps 16, 19 wait for A and B and issue the products, of 128 rows each: one warp's
+//                waits, operands and commits for all of them took longer than they do
 //   warp 17      keeps weights coming: tensor copies of 256 rows by 128 bytes
 //   warp 18      keeps x coming: tiles of 64 of K that k_images has laid out as the
 //                products read them, so that each is one bulk copy
@@ -24,11 +25,11 @@
 // wait is bounded: one that gives up makes all others give up, and the CTA's outputs
 // NaN.
 //
-// Measured: 32 x 5,000 fp32 states by 32,000 x 5,000 weights, groups of 128, take 44 us
-// (2.0 TB/s of weights and scales; 96 columns at 700 TFLOP/s), where k_matvec in eight
-// passes takes 288.  What bounds it is the unpacking: a word of eight weights is four
-// pairs of instructions a lane and a store of 16 bytes to tensor memory, shared by warps
-// 8-15 whose stores and the products' reads take turns there.
+// Measured: 32 x 5,000 fp32 states by 32,000 x 5,000 weights, groups of 128, take 41 us
+// (2.2 TB/s of weights and scales; 96 columns at 750 TFLOP/s), in groups of 32 with zero
+// points 73; 8 states take 35. k_matvec in eight passes takes 288.  What bounds it is the
+// way of a step from warp to warp (unpacked, stored, multiplied, its buffer free again):
+// without products, weights or x coming in it is a tenth faster.  A chunk takes 1.6 us.
 #include "int4.h"
 
 namespace ck {
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     k_wide(const __grid_constant__ MatvecArgs a, const __grid_constant__ WidePlan p,
            const __grid_constant__ CUtensorMap weights, const char *images, float *partial) {
     extern __shared__ __align__(1024) char smem[];
-    __shared__ __align__(8) uint64_t bars[2 * kImages + 2 * kRing + 11];
+    __shared__ __align__(8) uint64_t bars[2 * kImages + 2 * kRing + 15];
     __shared__ uint32_t tmem_base;
     __shared__ int dead;
     char *ring = smem + kImages * N * 128;
@@ -123,12 +124,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     auto b_empty = [&](int i) { return bar0 + 8 * (kImages + i); };
     auto a_full = [&](int i) { return bar0 + 8 * (2 * kImages + i); };
     auto a_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 2 + i); };
-    auto d_full = [&](int i) { return bar0 + 8 * (2 * kImages + 4 + i); };
-    auto d_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 6 + i); };
-    auto t_full = [&](int i) { return bar0 + 8 * (2 * kImages + 8 + i); };
-    const uint32_t idle = bar0 + 8 * (2 * kImages + 10);
-    auto w_full = [&](int i) { return bar0 + 8 * (2 * kImages + 11 + i); };
-    auto w_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 11 + kRing + i); };
+    auto d_full = [&](int half, int i) { return bar0 + 8 * (2 * kImages + 4 + 2 * half + i); };
+    auto d_empty = [&](int half, int i) { return bar0 + 8 * (2 * kImages + 8 + 2 * half + i); };
+    auto t_full = [&](int i) { return bar0 + 8 * (2 * kImages + 12 + i); };
+    const uint32_t idle = bar0 + 8 * (2 * kImages + 14);
+    auto w_full = [&](int i) { return bar0 + 8 * (2 * kImages + 15 + i); };
+    auto w_empty = [&](int i) { return bar0 + 8 * (2 * kImages + 15 + kRing + i); };
     const Waiter wait{&dead, p.timeout};
 
     const int64_t split = quotient(blockIdx.x, p.blocks), block = blockIdx.x - split * p.blocks;
@@ -140,16 +141,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         dead = 0;
         for (int i = 0; i < kImages; ++i) {
             barrier_init(b_full(i), 1);
-            barrier_init(b_empty(i), 1);
+            barrier_init(b_empty(i), 2);
         }
         for (int i = 0; i < 2; ++i) {
             barrier_init(a_full(i), kWorkers + p.extra);
-            barrier_init(a_empty(i), 1);
-            barrier_init(d_full(i), 1);
-            barrier_init(d_empty(i), kWorkers);
+            barrier_init(a_empty(i), 2);
+            for (int half = 0; half < 2; ++half) {
+                barrier_init(d_full(half, i), 1);
+                barrier_init(d_empty(half, i), kWorkers / 2);
+            }
             barrier_init(t_full(i), kWorkers);
         }
-        barrier_init(idle, 1);
+        barrier_init(idle, 2);
         for (int i = 0; i < kRing; ++i) {
             barrier_init(w_full(i), 1);
             barrier_init(w_empty(i), kWorkers);
@@ -174,48 +177,53 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         bool ok = true;
         volatile int none = 0;
         const Waiter last_wait{&none, p.timeout};
-        if (warp == 2 * kWorkers) {
+        if (warp == 2 * kWorkers || warp == 2 * kWorkers + 3) {
             asm volatile("griddepcontrol.launch_dependents;");
+            const int half = warp == 2 * kWorkers ? 0 : 1;
+            const bool there = half == 0 || second;
             // D in 32-bit floats; A and B in fp16 (0) or bf16 (1), both along K; N / 8; 128 / 16 rows
             constexpr uint32_t kType = HALF ? 0u : 1u;
             constexpr uint32_t kInstr = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N / 8) << 17 | 8u << 24;
             // of a tile in shared memory: 128-byte swizzle, 1,024 bytes from eight columns to the next
-            const uint64_t desc0 = (uint64_t)2 << 61 | (uint64_t)1 << 46 | (uint64_t)64 << 32 | (uint64_t)1 << 16;
-            int group = 0;
-            constexpr int kPerGroup = GROUP / 16;
-            for (int i = 0; i < steps && ok; ++i) {
-                const int slot = i % kImages;
-                ok = __all_sync(~0u, wait(b_full(slot), (uint32_t)(i / kImages) & 1) &&
-                                         wait(a_full(i & 1), (uint32_t)(i >> 1) & 1));
-                if (!ok) break;
-                fence_after();
-                const uint64_t desc = desc0 | (smem_at(smem) + slot * kTile) >> 4;
+            const uint64_t desc0 =
+                (uint64_t)2 << 61 | (uint64_t)1 << 46 | (uint64_t)64 << 32 | (uint64_t)1 << 16 | smem_at(smem) >> 4;
+            // A turn is four steps: all that depends on a step is then known beforehand, but
+            // for the parities of some barriers.
+            static_assert(kImages == 4, "tiles of x: one for each step of a turn");
+            constexpr int kPerGroup = GROUP / 16, kGroups = 16 / kPerGroup;  // products of a group, groups of a turn
+            for (int i0 = 0, turn = 0; i0 < steps && ok; i0 += 4, ++turn) {
 #pragma unroll
-                for (int k = 0; k < kStep / 16; ++k) {
-                    const int at = (i * (kStep / 16) + k) % kPerGroup;  // of the group
-                    const int buf = group & 1;
-                    if (at == 0 && group >= 2 && ok) {
-                        ok = __all_sync(~0u, wait(d_empty(buf), (uint32_t)((group >> 1) - 1) & 1));
-                        fence_after();
+                for (int q = 0; q < 4; ++q) {
+                    if (i0 + q >= steps || !ok) break;
+                    const bool last = i0 + q == steps - 1;
+                    ok = __all_sync(~0u, wait(b_full(q), (uint32_t)turn & 1) && wait(a_full(q & 1), (uint32_t)(q >> 1)));
+                    if (!ok) break;
+                    fence_after();
+#pragma unroll
+                    for (int k = 0; k < kStep / 16; ++k) {
+                        constexpr int kSteps = kStep / 16;
+                        const int at = (q * kSteps + k) % kPerGroup, group = (q * kSteps + k) / kPerGroup;
+                        const int buf = group & 1;
+                        if (at == 0 && (turn > 0 || group >= 2) && ok) {
+                            // the sums of two groups ago
+                            const int before = turn * (kGroups / 2) + (group >> 1) - 1;
+                            ok = __all_sync(~0u, wait(d_empty(half, buf), (uint32_t)before & 1));
+                            fence_after();
+                        }
+                        if (!ok) break;
+                        if (there)
+                            asm volatile(
+                                "{\n.reg .pred e, p;\nelect.sync _|e, 0xffffffff;\nsetp.ne.b32 p, %4, 0;\n"
+                                "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_at(half, buf)),
+                                "r"(a_at(half, q & 1) + k * 8), "l"(desc0 + q * (kTile >> 4) + 2 * k), "r"(kInstr),
+                                "r"((uint32_t)(at != 0))
+                                : "memory");
+                        if (at == kPerGroup - 1 || (last && k == kSteps - 1)) commit(d_full(half, buf));
                     }
                     if (!ok) break;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (half && !second) break;
-                        asm volatile(
-                            "{\n.reg .pred e, p;\nelect.sync _|e, 0xffffffff;\nsetp.ne.b32 p, %4, 0;\n"
-                            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_at(half, buf)),
-                            "r"(a_at(half, i & 1) + k * 8), "l"(desc + 2 * k), "r"(kInstr), "r"((uint32_t)(at != 0))
-                            : "memory");
-                    }
-                    if (at == kPerGroup - 1 || (i == steps - 1 && k == kStep / 16 - 1)) {
-                        commit(d_full(buf));
-                        ++group;
-                    }
+                    commit(a_empty(q & 1));
+                    commit(b_empty(q));
                 }
-                if (!ok) break;
-                commit(a_empty(i & 1));
-                commit(b_empty(slot));
             }
             commit(idle);  // no product is left under way
             last_wait(idle, 0);
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const int buf = f & 1, g = first + f, table = (g >> 3) & 1;
             if (f == 0 || (g & 7) == 0) ok = wait(t_full(table), (uint32_t)(((g >> 3) - (first >> 3)) >> 1) & 1);
             const float scale = all_scales[((table * kWorkers + warp) * kTileRows + lane) * kPitch + (g & 7)];
-            ok = __all_sync(~0u, ok && wait(d_full(buf), (uint32_t)(f >> 1) & 1));
+            ok = __all_sync(~0u, ok && wait(d_full(half, buf), (uint32_t)(f >> 1) & 1));
             if (!ok) break;
             fence_after();
             if (half == 0 || second) {
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) barrier_arrive(d_empty(buf));
+            if (lane == 0) barrier_arrive(d_empty(half, buf));
         }
         const int64_t v = block * kWideRows + 32 * warp + lane;
         const float back = ok ? Nibble<HALF>::kBack : __int_as_float(0x7fc00000);
