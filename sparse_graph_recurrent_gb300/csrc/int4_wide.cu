@@ -25,11 +25,11 @@
 // wait is bounded: one that gives up makes all others give up, and the CTA's outputs
 // NaN.
 //
-// Measured: 32 x 5,000 fp32 states by 32,000 x 5,000 weights, groups of 128, take 41 us
-// (2.2 TB/s of weights and scales; 96 columns at 750 TFLOP/s), in groups of 32 with zero
-// points 73; 8 states take 35. k_matvec in eight passes takes 288.  What bounds it is the
+// Measured: 32 x 5,000 fp32 states by 32,000 x 5,000 weights, groups of 128, take 38 us
+// (2.3 TB/s of weights and scales; 96 columns at 800 TFLOP/s), in groups of 32 with zero
+// points 74; 8 states take 34. k_matvec in eight passes takes 288.  What bounds it is the
 // way of a step from warp to warp (unpacked, stored, multiplied, its buffer free again):
-// without products, weights or x coming in it is a tenth faster.  A chunk takes 1.6 us.
+// without products, weights or x coming in it is a tenth faster.  A chunk takes 1.5 us.
 #include "int4.h"
 
 namespace ck {
@@ -284,6 +284,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             ok = __all_sync(~0u, wait(w_full(slot), (uint32_t)((c - c0) / kRing) & 1));
             if (!ok) break;
             const uint32_t line = my_lines + slot * (kWorkers * kUnitBytes);
+            uint4 words[2];  // of a step, asked for before the one before is stored
+            auto fetch = [&](int q) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(words[e].x), "=r"(words[e].y), "=r"(words[e].z), "=r"(words[e].w)
+                                 : "r"(line + (my_swap ^ ((2 * q + e) << 4))));
+            };
+            fetch(0);
 #pragma unroll
             for (int q = 0; q < kChunk / kStep; ++q) {
                 const int i = (c - c0) * (kChunk / kStep) + q;
@@ -295,15 +304,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     const int piece = 2 * q + e;
                     const uint32_t zero = Nibble<HALF>::minus(
                         my_zeros[lane * 8 + in_eight * (kChunk / GROUP) + piece * 32 / GROUP], 0);
-                    uint4 n;
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(n.x), "=r"(n.y), "=r"(n.z), "=r"(n.w)
-                                 : "r"(line + (my_swap ^ (piece << 4))));
+                    const uint4 n = words[e];
                     Nibble<HALF>::pairs(n.x, zero, *(uint32_t(*)[4])(v + 16 * e));
                     Nibble<HALF>::pairs(n.y, zero, *(uint32_t(*)[4])(v + 16 * e + 4));
                     Nibble<HALF>::pairs(n.z, zero, *(uint32_t(*)[4])(v + 16 * e + 8));
                     Nibble<HALF>::pairs(n.w, zero, *(uint32_t(*)[4])(v + 16 * e + 12));
                 }
+                if (q + 1 < kChunk / kStep) fetch(q + 1);
                 if (q == kChunk / kStep - 1 || i == steps - 1) {  // the unit is read
                     __syncwarp();
                     if (lane == 0) barrier_arrive(w_empty(slot));
