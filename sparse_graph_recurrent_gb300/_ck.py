@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 
 import torch
 
@@ -405,7 +406,7 @@ _int4_ws = {}  # bytes by (device, dtype, M, K, V, group): sizes only, no memory
 
 def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
     """x [M, K], qweight uint8 [V, (K + 1) / 2], scales and zeros [V, ceil(K / group)], y [M, V].
-    The workspace is taken from torch's allocator on the current stream."""
+    The workspace is taken from torch's allocator on the stream that the product runs on."""
     if x.dtype not in DTYPES or scales.dtype not in DTYPES or not x.is_cuda:
         raise ValueError("x and scales are CUDA tensors of float32, bfloat16 or float16")
     if group not in INT4_GROUPS:
@@ -436,9 +437,11 @@ def ck_int4_matvec(x, qweight, scales, zeros, bias, group: int, y, stream=None):
         if len(_int4_ws) > 4096:
             _int4_ws.clear()
         need = _int4_ws[key] = ck_int4_workspace_size(x.dtype, M, K, V, group)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    if ws is not None and stream is not None:
-        ws.record_stream(stream)
+    ws = None
+    if need:
+        # of the stream that uses it: another's block may still have work of its own pending
+        with nullcontext() if stream is None else torch.cuda.stream(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
     status = (_lib or load()).ck_int4_matvec(
         x.data_ptr(), DTYPES[x.dtype], M, K, _rows(x, "x"), qweight.data_ptr(), V, pitch,
         scales.data_ptr(), DTYPES[scales.dtype], _rows(scales, "scales"),

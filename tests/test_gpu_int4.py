@@ -319,3 +319,24 @@ def test_refusals():
         ck.int4_quantize(torch.zeros(4, 64, device="cuda"), 48)
     with pytest.raises(ValueError):
         ck.int4_quantize(torch.zeros(4, device="cuda"))
+
+
+@pytest.mark.parametrize("M", [4, 20])
+def test_a_named_stream_while_the_current_one_is_busy(M):
+    """Blocks that the current stream has given back, but still writes, are not the
+    workspace of a product on another stream."""
+    import sparse_graph_recurrent_gb300 as ck
+    from sparse_graph_recurrent_gb300 import _ck
+    c = case(M, 3000, 2000, 128, torch.float32, seed=4)
+    want = ck.int4_matvec(**c)
+    need = _ck.ck_int4_workspace_size(torch.float32, M, 3000, 2000, 128)
+    assert need > 0
+    s = torch.cuda.Stream()
+    ys = [torch.empty_like(want) for _ in range(20)]
+    torch.cuda.synchronize()
+    for _ in range(400):
+        torch.empty(need, dtype=torch.uint8, device="cuda").fill_(0x7f)
+    for y in ys:
+        _ck.ck_int4_matvec(c["x"], c["qweight"], c["scales"], c["zeros"], None, 128, y, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in ys)

@@ -166,3 +166,57 @@ def test_the_compiled_module_leaves_cpu_tensors():
     assert _ck.native().dropout(x, 0.5, 1, 0, False) is None
     assert _ck.native().int4_matvec(x, x, x, None, None, 32, None) is None
     assert _ck.native().control(x, *[None] * 9, True, 0, None, 0) is None
+
+
+def test_workspace_comes_from_the_stream_that_uses_it(monkeypatch):
+    """A product on a named stream allocates on that stream: a block of the current one may
+    still be written by kernels that are pending there."""
+    from contextlib import contextmanager
+
+    from sparse_graph_recurrent_gb300 import _ck
+
+    class Cuda:
+        """As much of a CUDA tensor as the call looks at."""
+        is_cuda, device = True, torch.device("cuda", 0)
+
+        def __init__(self, dtype, *shape):
+            self.dtype, self.shape = dtype, torch.Size(shape)
+
+        dim = lambda self: len(self.shape)  # noqa: E731
+        stride = lambda self, i=None: (self.shape[1], 1) if i is None else (self.shape[1], 1)[i]  # noqa: E731
+        get_device = lambda self: 0  # noqa: E731
+        data_ptr = lambda self: 4096  # noqa: E731
+        record_stream = lambda self, stream: None  # noqa: E731
+
+    class Stream:
+        cuda_stream = 77
+
+    at, took, ran = [0], [], []
+
+    @contextmanager
+    def stream(s):
+        at.append(s.cuda_stream)
+        yield
+        at.pop()
+
+    def empty(*size, **kw):
+        took.append(at[-1])
+        return Cuda(torch.uint8, *size)
+
+    class Lib:
+        @staticmethod
+        def ck_int4_matvec(*a):
+            ran.append(a[-1])
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(_ck, "_lib", Lib)
+    monkeypatch.setattr(_ck, "_get_device", lambda: 0)
+    monkeypatch.setattr(_ck, "_get_raw_stream", lambda device: 0)
+    monkeypatch.setattr(_ck, "_int4_ws", {(0, torch.float32, 2, 64, 8, 32): 4096})
+    args = (Cuda(torch.float32, 2, 64), Cuda(torch.uint8, 8, 32), Cuda(torch.float32, 8, 2), None, None, 32,
+            Cuda(torch.float32, 2, 8))
+    _ck.ck_int4_matvec(*args)
+    _ck.ck_int4_matvec(*args, stream=Stream())
+    assert ran == [0, 77] and took == [0, 77]
