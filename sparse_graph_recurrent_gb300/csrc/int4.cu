@@ -63,6 +63,7 @@ struct MatvecPlan {
     Deal slab;         // slabs to CTAs
     Deal tile;         // aligned: tiles to CTAs
     long long timeout; // cycles that a wait for a copy may last
+    int extra;         // test hook: arrivals that never come
     int x_pitch;       // bytes between columns of x in shared memory
     int x_cols;        // tensor-core columns that x takes
     size_t smem;
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     const Waiter wait{&dead, p.timeout};
     if (threadIdx.x == 0) dead = 0;
     if (lane == 0)
-        for (int i = 0; i < kStages; ++i) barrier_init(my_bars + 8 * i, 1);
+        for (int i = 0; i < kStages; ++i) barrier_init(my_bars + 8 * i, 1 + p.extra);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     // A place in the ring, and how often the ring has gone round: the copy that is waited
     // for next and the one that is asked for next.
@@ -385,6 +386,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             t += whole;
         }
         __syncthreads();
+        // Where a wait gave up a late copy may have come over a part in its ring: then what is
+        // added up here is NaN whatever the parts hold.
+        const bool lost = *(volatile int *)&dead != 0;
         // parts of one tile follow one another: the warp that holds the first adds them up
         const int theirs = lane < 2 * WARPS ? part_tile[lane] : -1;
         for (int k = 0; k < 2; ++k) {
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             const int64_t tu = (int64_t)tile * sc;
             const bool alone = p.slabs == 1 && tu >= u0 && tu + sc <= u1;
             for (int m = 0; m < p.rows; ++m) {
-                float sum = 0.f;
+                float sum = lost ? __int_as_float(0x7fc00000) : 0.f;
                 for (uint32_t rest = same; rest; rest &= rest - 1) {
                     const int e = __ffs(rest) - 1;
                     sum += part_at(e >> 1, e & 1)[m * kTileRows + lane];
@@ -517,6 +521,7 @@ MatvecPlan matvec_plan(int64_t dtype, int64_t rows, int64_t K, int64_t V, int64_
     // 64 bytes past a multiple of 128: two columns side by side fill all banks
     p.x_pitch = (int)slab * 2 * kChunk + 64;
     p.timeout = 2 * options().timeout_ns;  // at 2 GHz
+    p.extra = options().barrier_extra;
     p.smem = fixed + (size_t)p.x_cols * p.x_pitch;
     return p;
 }

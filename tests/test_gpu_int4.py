@@ -340,3 +340,26 @@ def test_a_named_stream_while_the_current_one_is_busy(M):
         _ck.ck_int4_matvec(c["x"], c["qweight"], c["scales"], c["zeros"], None, 128, y, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in ys)
+
+
+# (M, K, V, dtype): 12 warps with whole tiles, 12 with the joining kernel, two column tiles,
+# slabs of a long K, 16 warps with a long run
+@pytest.mark.parametrize("M,K,V,dtype", [(1, 5000, 256, torch.float32), (4, 3000, 500, torch.float32),
+                                         (16, 2000, 3000, torch.bfloat16), (4, 211577, 40, torch.float32),
+                                         (1, 40000, 16384, torch.float16)])
+def test_a_wait_that_runs_out_with_few_rows(M, K, V, dtype):
+    """As for batches: every wait for weights gives up, y is NaN wherever sums meet, and the
+    next call is right."""
+    import sparse_graph_recurrent_gb300 as ck
+    from sparse_graph_recurrent_gb300 import _ck
+    c = case(M, K, V, 128, dtype, seed=6)
+    _ck.ck_set_option(_ck.OPT_TEST_BARRIER_EXTRA, 1)
+    _ck.ck_set_option(_ck.OPT_BARRIER_TIMEOUT_NS, 2_000_000)
+    try:
+        ys = [ck.int4_matvec(**c) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.isnan(y).all() for y in ys)
+    finally:
+        _ck.ck_set_option(_ck.OPT_TEST_BARRIER_EXTRA, 0)
+        _ck.ck_set_option(_ck.OPT_BARRIER_TIMEOUT_NS, 4_000_000_000)
+    check(ck.int4_matvec(**c), c, 128)
