@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 copy_box(weights, (c0 + i) * (kChunk / 2), (int)block * kWideRows, smem_at(ring) + slot * kWeights,
                          w_full(slot), kWeights);
             }
-            for (int k = i > kRing ? i - kRing : 0; !ok && k < i; ++k) last_wait(w_full(k % kRing), (uint32_t)(k / kRing) & 1);
+            // the last copies have landed before the CTA ends, also where nobody takes them up any more
+            for (int k = i > kRing ? i - kRing : 0; k < i; ++k) last_wait(w_full(k % kRing), (uint32_t)(k / kRing) & 1);
         } else if (warp == 2 * kWorkers + 2) {
             asm volatile("griddepcontrol.wait;" ::: "memory");  // k_images is done
             asm volatile("fence.proxy.async.global;" ::: "memory");
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     "l"(images + (int64_t)(step0 + i) * kTile), "r"(kTile), "r"(b_full(slot))
                     : "memory");
             }
-            for (int k = i > kImages ? i - kImages : 0; !ok && k < i; ++k)
+            for (int k = i > kImages ? i - kImages : 0; k < i; ++k)
                 last_wait(b_full(k % kImages), (uint32_t)(k / kImages) & 1);
         }
     } else if (warp >= kWorkers) {

@@ -363,3 +363,28 @@ def test_a_wait_that_runs_out_with_few_rows(M, K, V, dtype):
         _ck.ck_set_option(_ck.OPT_TEST_BARRIER_EXTRA, 0)
         _ck.ck_set_option(_ck.OPT_BARRIER_TIMEOUT_NS, 4_000_000_000)
     check(ck.int4_matvec(**c), c, 128)
+
+
+@pytest.mark.parametrize("K", [64, 600, 1217, 20000])
+def test_a_wait_that_runs_out_with_copies_on_their_way(K):
+    """Short runs of K, whose copies have all been asked for when the warps that would take
+    them up give up: the block waits for them before it ends, and other calls follow at once."""
+    import sparse_graph_recurrent_gb300 as ck
+    from sparse_graph_recurrent_gb300 import _ck
+    c, d = case(20, K, 300, 64, torch.float32, seed=6), case(3, 5000, 3000, 64, torch.float32, seed=7)
+    want = ck.int4_matvec(**d, group_size=64)
+    torch.cuda.synchronize()
+    _ck.ck_set_option(_ck.OPT_BARRIER_TIMEOUT_NS, 100_000)
+    try:
+        for _ in range(5):
+            _ck.ck_set_option(_ck.OPT_TEST_BARRIER_EXTRA, 1)
+            y = ck.int4_matvec(**c, group_size=64)
+            _ck.ck_set_option(_ck.OPT_TEST_BARRIER_EXTRA, 0)
+            _ck.ck_set_option(_ck.OPT_BARRIER_TIMEOUT_NS, 4_000_000_000)
+            assert torch.equal(ck.int4_matvec(**d, group_size=64), want)
+            assert torch.isnan(y).all()
+            _ck.ck_set_option(_ck.OPT_BARRIER_TIMEOUT_NS, 100_000)
+    finally:
+        _ck.ck_set_option(_ck.OPT_TEST_BARRIER_EXTRA, 0)
+        _ck.ck_set_option(_ck.OPT_BARRIER_TIMEOUT_NS, 4_000_000_000)
+    check(ck.int4_matvec(**c, group_size=64), c, 64)
