@@ -74,16 +74,21 @@ def _dropout(x, p, seed, step, locked):
 
 
 class _Dropout(torch.autograd.Function):
+    """A linear map and its own transpose: the gradient is dropout again, differentiable in
+    its turn."""
+
     @staticmethod
     def forward(ctx, x, p, seed, step, locked):
         if isinstance(step, torch.Tensor):
             step = step.clone()  # the backward's mask is this forward's, wherever the counter is by then
         ctx.args = (p, seed, step, locked)
-        return dropout_backward(x.detach(), *ctx.args)
+        x = x.detach()
+        y = (_ck._native or _ck.native()).dropout(x, *ctx.args)
+        return _dropout(x, *ctx.args) if y is None else y
 
     @staticmethod
     def backward(ctx, d_out):
-        return dropout_backward(d_out, *ctx.args), None, None, None, None
+        return dropout(d_out, *ctx.args), None, None, None, None
 
 
 def dropout(x, p: float, seed: int, step=0, locked: bool = False):
@@ -103,9 +108,9 @@ def dropout(x, p: float, seed: int, step=0, locked: bool = False):
 
 
 def dropout_backward(d_out, p: float, seed: int, step=0, locked: bool = False):
-    """The gradient of dropout's x from its output's: the same mask and factor again."""
-    y = (_ck._native or _ck.native()).dropout(d_out, p, seed, step, locked)
-    return _dropout(d_out, p, seed, step, locked) if y is None else y
+    """The gradient of dropout's x from its output's: the same mask and factor again, so
+    differentiable in d_out as dropout is in x."""
+    return dropout(d_out, p, seed, step, locked)
 
 
 # -- the 4-bit readout -----------------------------------------------------------------------

@@ -198,3 +198,47 @@ def test_refusals():
         ck.dropout(x, 0.5, 1, torch.tensor([1]))
     with pytest.raises(ValueError):
         ck.dropout(x, 0.5, 1, torch.tensor([1], dtype=torch.int32, device="cuda"))
+
+
+def test_second_derivatives():
+    """A penalty on the gradient through dropout: with y = m x^2 (m the factor or 0) and
+    f = sum y^2, f' = 4 m^2 x^3 and sum f'^2 has the gradient 96 m^4 x^5."""
+    import sparse_graph_recurrent_gb300 as ck
+    for locked in (False, True):
+        x = (data((3, 4, 65), torch.float32, 6) / 4).double().float().requires_grad_()
+        y = ck.dropout(x * x, 0.25, 13, 21, locked=locked)
+        (g,) = torch.autograd.grad((y * y).sum(), x, create_graph=True)
+        assert g.requires_grad
+        (h,) = torch.autograd.grad((g * g).sum(), x)
+        m = torch.from_numpy(ro.keep_mask((3, 4, 65), 0.25, 13, 21, locked).copy()).double() / 0.75
+        xd = x.detach().double().cpu()
+        # a dozen roundings of 2^-24 each at most on either
+        assert ((g.detach().double().cpu() - 4 * m ** 2 * xd ** 3).abs() <= 2.0 ** -20 * (4 * m ** 2 * xd ** 3).abs() + 1e-35).all()
+        want = 96 * m ** 4 * xd ** 5
+        assert ((h.double().cpu() - want).abs() <= 2.0 ** -18 * want.abs() + 1e-35).all()
+
+
+def test_second_derivatives_keep_the_forwards_step():
+    """The counter moves on between the forward, the gradient and the gradient's gradient."""
+    import sparse_graph_recurrent_gb300 as ck
+    from sparse_graph_recurrent_gb300 import _ck
+    step = torch.tensor([7], dtype=torch.int64, device="cuda")
+    x = data((5, 130), torch.float32, 1).requires_grad_()
+    d = data((5, 130), torch.float32, 2).requires_grad_()
+    y = ck.dropout(x, 0.5, 3, step)
+    _ck.ck_step_advance(step)
+    (g,) = torch.autograd.grad(y, x, d, create_graph=True)
+    _ck.ck_step_advance(step)
+    (h,) = torch.autograd.grad(g, d, torch.ones_like(g))
+    same(g.detach(), expected(d.detach(), 0.5, 3, 7, False))
+    same(h, expected(torch.ones(5, 130), 0.5, 3, 7, False))
+
+
+def test_the_gradient_call_is_differentiable():
+    import sparse_graph_recurrent_gb300 as ck
+    d = data((4, 99), torch.float32, 2).requires_grad_()
+    g = ck.dropout_backward(d, 0.3, 5, 6)
+    (h,) = torch.autograd.grad(g, d, torch.ones_like(g))
+    same(h, expected(torch.ones(4, 99), 0.3, 5, 6, False))
+    with torch.no_grad():
+        assert not ck.dropout_backward(d, 0.3, 5, 6).requires_grad
