@@ -90,7 +90,10 @@ bool step_of(PyObject *o, int dev, uint64_t &step, const int64_t *&at_dev) {
     return true;
 }
 
-bool wants_gradient(const at::Tensor &t) { return t.requires_grad() && c10::GradMode::is_enabled(); }
+// Whether autograd follows t: it is to get a gradient, or carries a tangent.
+bool followed(const at::Tensor &t) {
+    return (t.requires_grad() && c10::GradMode::is_enabled()) || t.unsafeGetTensorImpl()->_fw_grad(0, t).defined();
+}
 
 void *stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 
@@ -102,7 +105,7 @@ PyObject *dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Operand x(a[0], dev);
         uint64_t seed, step;
         const int64_t *step_dev;
-        if (!x.good || wants_gradient(*x.t) || !whole_number(a[2], seed) || !step_of(a[3], dev, step, step_dev)) {
+        if (!x.good || followed(*x.t) || !whole_number(a[2], seed) || !step_of(a[3], dev, step, step_dev)) {
             PyErr_Clear();
             return leave_it();
         }
@@ -156,7 +159,7 @@ PyObject *int4_matvec(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Operand x(a[0], dev), q(a[1], dev), s(a[2], dev), z(a[3], dev), b(a[4], dev), o(a[6], dev);
         uint64_t group;
         if (!x.good || q.none || !q.good || s.none || !s.good || !z.good || !b.good || !o.good ||
-            wants_gradient(*x.t) || !whole_number(a[5], group) || (group != 32 && group != 64 && group != 128)) {
+            followed(*x.t) || !whole_number(a[5], group) || (group != 32 && group != 64 && group != 128)) {
             PyErr_Clear();
             return leave_it();
         }
@@ -197,7 +200,7 @@ PyObject *control(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (n != 14 || !cuda_tensor(a[0])) return leave_it();
         const int dev = c10::cuda::current_device();
         const Operand x(a[0], dev), text(a[1], dev), bias(a[7], dev), mask(a[8], dev);
-        if (!x.good || !text.good || !bias.good || !mask.good || x.t->dim() != 2 || wants_gradient(*x.t)) return leave_it();
+        if (!x.good || !text.good || !bias.good || !mask.good || x.t->dim() != 2 || followed(*x.t)) return leave_it();
         ck_logit_call c{};
         const int64_t B = x.t->size(0), V = x.t->size(1);
         c.logits = x.t->const_data_ptr();

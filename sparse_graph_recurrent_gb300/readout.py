@@ -17,11 +17,18 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _ck
 
 __all__ = ["dropout", "dropout_backward", "int4_quantize", "int4_matvec", "control_logits",
            "pick_tokens"]
+
+
+def _followed(t) -> bool:
+    """Whether autograd follows t: it is to get a gradient, or carries a tangent."""
+    return (t.requires_grad and torch.is_grad_enabled()
+            or forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None)
 
 
 # -- dropout ---------------------------------------------------------------------------------
@@ -74,8 +81,8 @@ def _dropout(x, p, seed, step, locked):
 
 
 class _Dropout(torch.autograd.Function):
-    """A linear map and its own transpose: the gradient is dropout again, differentiable in
-    its turn."""
+    """A linear map and its own transpose: the gradient and the tangent are dropout again,
+    differentiable in their turn."""
 
     @staticmethod
     def forward(ctx, x, p, seed, step, locked):
@@ -90,6 +97,10 @@ class _Dropout(torch.autograd.Function):
     def backward(ctx, d_out):
         return dropout(d_out, *ctx.args), None, None, None, None
 
+    @staticmethod
+    def jvp(ctx, x_tangent, *_):
+        return dropout(x_tangent, *ctx.args)
+
 
 def dropout(x, p: float, seed: int, step=0, locked: bool = False):
     """x with each element kept and scaled by 1 / (1 - p), or set to 0 with
@@ -102,7 +113,7 @@ def dropout(x, p: float, seed: int, step=0, locked: bool = False):
     y = (_ck._native or _ck.native()).dropout(x, p, seed, step, locked)
     if y is not None:
         return y
-    if x.requires_grad and torch.is_grad_enabled():
+    if _followed(x):
         return _Dropout.apply(x, p, seed, step, locked)
     return _dropout(x, p, seed, step, locked)
 

@@ -242,3 +242,28 @@ def test_the_gradient_call_is_differentiable():
     same(h, expected(torch.ones(4, 99), 0.3, 5, 6, False))
     with torch.no_grad():
         assert not ck.dropout_backward(d, 0.3, 5, 6).requires_grad
+
+
+def test_forward_mode():
+    """The tangent of dropout is dropout of the tangent, with the same mask; of a tangent
+    that requires a gradient it stays differentiable."""
+    import torch.autograd.forward_ad as fwd
+
+    import sparse_graph_recurrent_gb300 as ck
+    x, t = data((6, 3, 77), torch.float32, 4), data((6, 3, 77), torch.float32, 5)
+    for locked in (False, True):
+        for v in (x, x.transpose(1, 2)):
+            with fwd.dual_level():
+                for call in (ck.dropout, ck.dropout_backward):
+                    y = fwd.unpack_dual(call(fwd.make_dual(v, t.view(v.shape)), 0.25, 13, 21, locked=locked))
+                    same(y.primal, expected(v, 0.25, 13, 21, locked))
+                    same(y.tangent, expected(t.view(v.shape), 0.25, 13, 21, locked))
+    with fwd.dual_level(), torch.no_grad():
+        assert fwd.unpack_dual(ck.dropout(fwd.make_dual(x, t), 0.25, 13)).tangent is not None
+    leaf = t.clone().requires_grad_()
+    with fwd.dual_level():
+        y = fwd.unpack_dual(ck.dropout(fwd.make_dual(x, leaf), 0.25, 13, 21)).tangent
+        (g,) = torch.autograd.grad(y, leaf, torch.ones_like(y))
+    same(g, expected(torch.ones_like(x), 0.25, 13, 21, False))
+    with fwd.dual_level():  # a level alone changes nothing
+        same(ck.dropout(x, 0.25, 13, 21), expected(x, 0.25, 13, 21, False))
