@@ -157,8 +157,8 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
     y = (_ck._native or _ck.native()).int4_matvec(x, qweight, scales, zeros, bias, group_size, out)
     if y is not None:
         return y
-    if x.requires_grad and torch.is_grad_enabled():
-        raise ValueError("int4_matvec has no gradient: call it under no_grad or on a detached x")
+    if _followed(x):
+        raise ValueError("int4_matvec has no derivative: call it under no_grad or on a detached x")
     device = x.get_device()
     if device < 0:
         raise ValueError("int4_matvec takes CUDA tensors")
@@ -230,8 +230,8 @@ def _control(logits, history, history_len, prompt_len, repetition, frequency, pr
     dtype, dev = _ck.DTYPES.get(logits.dtype), logits.get_device()
     if dtype is None or dev < 0 or logits.dim() != 2:
         raise ValueError("logits must be a CUDA tensor [B, V] of float32, bfloat16 or float16")
-    if logits.requires_grad and torch.is_grad_enabled():
-        raise ValueError("the logit controls have no gradient: call them under no_grad")
+    if _followed(logits):
+        raise ValueError("the logit controls have no derivative: call them under no_grad or on detached logits")
     B, V = logits.shape
     text = text_len = prompt = None
     bits = L = text_stride = 0
