@@ -49,7 +49,12 @@ int dtype_of(const at::Tensor &t) {
 // (asked before the device, which a process without one does not have)
 bool cuda_tensor(PyObject *o) { return THPVariable_Check(o) && THPVariable_Unpack(o).is_cuda(); }
 
-// A tensor of a call, on the device `dev`.
+// Whether autograd follows t: it is to get a gradient, or carries a tangent.
+bool followed(const at::Tensor &t) {
+    return (t.requires_grad() && c10::GradMode::is_enabled()) || t.unsafeGetTensorImpl()->_fw_grad(0, t).defined();
+}
+
+// A tensor of a call, on the device `dev` and not followed by autograd.
 struct Operand {
     const at::Tensor *t = nullptr;
     bool none = true, good = true;
@@ -59,7 +64,7 @@ struct Operand {
         good = THPVariable_Check(o);
         if (!good) return;
         t = &THPVariable_Unpack(o);
-        good = t->is_cuda() && t->device().index() == dev && t->layout() == at::kStrided;
+        good = t->is_cuda() && t->device().index() == dev && t->layout() == at::kStrided && !followed(*t);
     }
     bool is(at::ScalarType type) const { return t->scalar_type() == type; }
     bool sizes(int64_t a) const { return t->dim() == 1 && t->size(0) == a; }
@@ -90,11 +95,6 @@ bool step_of(PyObject *o, int dev, uint64_t &step, const int64_t *&at_dev) {
     return true;
 }
 
-// Whether autograd follows t: it is to get a gradient, or carries a tangent.
-bool followed(const at::Tensor &t) {
-    return (t.requires_grad() && c10::GradMode::is_enabled()) || t.unsafeGetTensorImpl()->_fw_grad(0, t).defined();
-}
-
 void *stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 
 // dropout(x, p, seed, step, locked)
@@ -105,7 +105,7 @@ PyObject *dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Operand x(a[0], dev);
         uint64_t seed, step;
         const int64_t *step_dev;
-        if (!x.good || followed(*x.t) || !whole_number(a[2], seed) || !step_of(a[3], dev, step, step_dev)) {
+        if (!x.good || !whole_number(a[2], seed) || !step_of(a[3], dev, step, step_dev)) {
             PyErr_Clear();
             return leave_it();
         }
@@ -159,7 +159,7 @@ PyObject *int4_matvec(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Operand x(a[0], dev), q(a[1], dev), s(a[2], dev), z(a[3], dev), b(a[4], dev), o(a[6], dev);
         uint64_t group;
         if (!x.good || q.none || !q.good || s.none || !s.good || !z.good || !b.good || !o.good ||
-            followed(*x.t) || !whole_number(a[5], group) || (group != 32 && group != 64 && group != 128)) {
+            !whole_number(a[5], group) || (group != 32 && group != 64 && group != 128)) {
             PyErr_Clear();
             return leave_it();
         }
@@ -200,7 +200,7 @@ PyObject *control(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (n != 14 || !cuda_tensor(a[0])) return leave_it();
         const int dev = c10::cuda::current_device();
         const Operand x(a[0], dev), text(a[1], dev), bias(a[7], dev), mask(a[8], dev);
-        if (!x.good || !text.good || !bias.good || !mask.good || x.t->dim() != 2 || followed(*x.t)) return leave_it();
+        if (!x.good || !text.good || !bias.good || !mask.good || x.t->dim() != 2) return leave_it();
         ck_logit_call c{};
         const int64_t B = x.t->size(0), V = x.t->size(1);
         c.logits = x.t->const_data_ptr();

@@ -31,6 +31,12 @@ def _followed(t) -> bool:
             or forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None)
 
 
+def _refuse_derivatives(what, **operands):
+    for name, t in operands.items():
+        if isinstance(t, torch.Tensor) and _followed(t):
+            raise ValueError(f"{what} has no derivative: call it under no_grad or on a detached {name}")
+
+
 # -- dropout ---------------------------------------------------------------------------------
 
 
@@ -157,8 +163,7 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
     y = (_ck._native or _ck.native()).int4_matvec(x, qweight, scales, zeros, bias, group_size, out)
     if y is not None:
         return y
-    if _followed(x):
-        raise ValueError("int4_matvec has no derivative: call it under no_grad or on a detached x")
+    _refuse_derivatives("int4_matvec", x=x, scales=scales, bias=bias, out=out)
     device = x.get_device()
     if device < 0:
         raise ValueError("int4_matvec takes CUDA tensors")
@@ -230,8 +235,8 @@ def _control(logits, history, history_len, prompt_len, repetition, frequency, pr
     dtype, dev = _ck.DTYPES.get(logits.dtype), logits.get_device()
     if dtype is None or dev < 0 or logits.dim() != 2:
         raise ValueError("logits must be a CUDA tensor [B, V] of float32, bfloat16 or float16")
-    if _followed(logits):
-        raise ValueError("the logit controls have no derivative: call them under no_grad or on detached logits")
+    _refuse_derivatives("a logit control", logits=logits, repetition=repetition, frequency=frequency,
+                        presence=presence, bias=bias, temperature=temperature, out=out)
     B, V = logits.shape
     text = text_len = prompt = None
     bits = L = text_stride = 0
