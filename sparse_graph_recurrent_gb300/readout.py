@@ -18,6 +18,7 @@ import math
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import _ck
 
@@ -179,6 +180,7 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
         if tuple(out.shape) != (*x.shape[:-1], V):
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(*x.shape[:-1], V)}")
         y = out if out.dim() == 2 else out.view(-1, V)
+        increment_version(out)
     args = (x2, qweight, scales, zeros, bias, group_size, y)
     if device == _ck._get_device():
         _ck.ck_int4_matvec(*args)
@@ -262,6 +264,7 @@ def _control(logits, history, history_len, prompt_len, repetition, frequency, pr
         if out.dtype != logits.dtype or out.shape != logits.shape or out.get_device() != dev:
             raise ValueError("out must be like logits")
         out_at, out_stride = out.data_ptr(), _ck._rows(out, "out")
+        increment_version(out)
     at = step_dev = None
     if seed is not None:
         at, step_dev = _ck._step_args(step, dev)

@@ -95,3 +95,22 @@ def test_what_the_module_leaves():
     with pytest.raises(_ck.CKError) as e:
         n.dropout(x.detach(), 1.5, 1, 0, False)
     assert e.value.name == "CK_ERR_INVALID_ARG"
+
+
+def test_writing_into_a_tensor_raises_its_version(both):
+    """autograd finds a saved tensor that `out` has changed since."""
+    import sparse_graph_recurrent_gb300 as ck
+    q, s, _ = ck.int4_quantize(torch.randn(64, 64, device="cuda"), 32)
+    x = torch.randn(2, 64, device="cuda")
+    for call in (lambda o: ck.int4_matvec(x, q, s, group_size=32, out=o), lambda o: ck.control_logits(x, out=o),
+                 lambda o: ck.pick_tokens(x, out=o), lambda o: ck.control_logits(o, out=o)):
+        def run():
+            a = torch.randn(2, 64, device="cuda", requires_grad=True)
+            saved = torch.randn(2, 64, device="cuda")
+            y = (a * saved).sum()
+            at = saved._version
+            call(saved)
+            assert saved._version == at + 1
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.backward()
+        both(run)
