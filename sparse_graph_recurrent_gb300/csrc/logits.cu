@@ -154,7 +154,8 @@ struct LogitPlan {
 // approximate logarithm bound a score from above; a bound from below for a lane's
 // likeliest token gives a score that the CTA's best has at least.  Only tokens that may
 // reach it are scored as defined, and a lane puts its one off to the end, when few are
-// left.  Bounds are a quarter of scores, which cannot overflow before the scores do,
+// left.  Bounds are a quarter of scores, which cannot overflow before the scores do
+// (where those may, the bound is infinite, as infinite scores are equal),
 // and leave out the scale of a word: log u = log word - 32 log 2.
 //
 // Measured: 64 x 131,072 bf16 with 4,096 of history, a bias, a mask and the logits wanted
@@ -248,6 +249,9 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
     };
     // margins of bounds; NaN for what is -inf or NaN, and for +inf from below
     constexpr float kLog = 0.25f * 0.69314718f;  // a quarter of log 2
+    // a quarter of the largest float, less more than a bound may be off: scores past it may
+    // be infinite
+    constexpr float kPast = 8.507e37f;
     auto above = [](float s) { return fmaf(fabsf(s), 1e-6f, s) + 1e-4f; };
     auto below = [](float s) { return fmaf(fabsf(s), -1e-6f, s) - 1e-4f; };
     for (int ow = threadIdx.x & ~31; ow < octs; ow += THREADS) {
@@ -361,6 +365,12 @@ __global__ void __launch_bounds__(THREADS, kLogitCtas * kThreads1 / THREADS)
             for (int j = 0; j < kOct; ++j) {
                 s[j] = PICK == kSample ? fmaf(log2_fast((float)w[j]), -kLog, z[j] * cool4) : z[j] * cool4;
                 top = fmaxf(top, s[j]);
+            }
+            if (top > kPast) {  // infinite scores are equal: all that may be are scored
+#pragma unroll
+                for (int j = 0; j < kOct; ++j)
+                    if (s[j] > kPast) s[j] = -minus_inf();
+                top = -minus_inf();
             }
             const uint32_t seen = *(volatile uint32_t *)&floor_key;
             float floor = key_score((unsigned long long)seen << 32);

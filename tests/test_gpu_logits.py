@@ -367,3 +367,32 @@ def test_many_rows_and_equal_scores(V, dtype):
     for temperature in (1.0, 0.7, 0.0):
         tokens = ck.pick_tokens(x.cuda(), temperature=temperature)
         assert torch.equal(tokens.cpu(), first)
+
+
+def test_ties_of_scores_that_overflow():
+    """Logits whose quotients by the temperature are infinite are equal: the lowest token, at
+    temperatures whose reciprocal is a normal number too, in one slice or several."""
+    import sparse_graph_recurrent_gb300 as ck
+    x = torch.tensor([[70.0, 100.0]], device="cuda")
+    for seed in (None, 5):
+        assert ck.pick_tokens(x, temperature=2e-37, seed=seed).tolist() == [0]
+    for V in (300, 20000, 140000):
+        x = torch.randn(6, V, device="cuda")
+        x[:, V // 2] = 80.0                                     # the first that overflows
+        x[:, V // 2 + 5 :: 7] = 90.0
+        x[:, V - 1] = 3e38
+        x[5] = torch.linspace(69.0, 400.0, V, device="cuda")    # near the end of the type, then past it
+        for t in (1.5e-37, 2e-37, 2.0349e-37):
+            with np.errstate(over="ignore"):
+                z = x.cpu().numpy() / np.float32(t)
+            want = z.argmax(1).tolist()
+            assert want[:5] == [V // 2] * 5 and np.isinf(z[5].max())
+            for seed in (None, 5):
+                for kw in (dict(temperature=t), dict(temperature=torch.full((6,), t, device="cuda"))):
+                    assert ck.pick_tokens(x, **kw, seed=seed, step=2).tolist() == want
+                    tok, out = ck.pick_tokens(x, **kw, seed=seed, step=2, return_logits=True)
+                    assert tok.tolist() == want and torch.isinf(out.max(1).values).all()
+    x = torch.zeros(2, 9000, device="cuda")
+    x[0, 4000:], x[1, 7::9] = 3e38, 2e38                        # at an ordinary temperature
+    assert ck.pick_tokens(x, temperature=0.5).tolist() == [4000, 7]
+    assert ck.pick_tokens(x, temperature=0.5, seed=1).tolist() == [4000, 7]
