@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from contextlib import nullcontext
 
 import torch
@@ -68,7 +69,7 @@ def library_path() -> str:
 
 def load() -> ctypes.CDLL:
     """Load the library, building it with nvcc first if it is missing or stale."""
-    global _lib
+    global _lib, _native
     if _lib is not None:
         return _lib
     path = _build.build(variant=library_variant())
@@ -126,31 +127,45 @@ def load() -> ctypes.CDLL:
     lib.ck_status_string.restype = ctypes.c_char_p
     lib.ck_last_error_message.argtypes = []
     lib.ck_last_error_message.restype = ctypes.c_char_p
-    _lib = lib
-    _load_native(lib)
+    native = _load_native(lib)
+    _lib, _native = lib, native
     return lib
 
 
 _native = None
 
 
+class _PythonForms:
+    """In the place of ck_binding where that cannot be had: leaves every call to its Python form."""
+
+    @staticmethod
+    def dropout(*args):
+        return None
+
+    int4_matvec = control = dropout
+
+
 def _load_native(lib):
-    """Load the module ck_binding (the readout operators' short way from Python),
-    building it first if it is missing or stale, and give it this library's entries."""
-    global _native
+    """The module ck_binding (the readout operators' short way from Python), built first if
+    it is missing or stale, with this library's entries.  All else works without it."""
     import importlib.machinery
     import importlib.util
-    loader = importlib.machinery.ExtensionFileLoader("ck_binding", _build.build_binding())
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("ck_binding", loader))
-    loader.exec_module(module)
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("ck_binding", _build.build_binding())
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("ck_binding", loader))
+        loader.exec_module(module)
+    except (ImportError, OSError, RuntimeError) as e:  # no compiler, no headers, another interpreter's
+        warnings.warn("the readout operators' kernels are called through ctypes, some microseconds "
+                      f"slower, as ck_binding cannot be had: {e}", RuntimeWarning, stacklevel=3)
+        return _PythonForms
     entry = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value  # noqa: E731
     module.bind(entry("ck_dropout"), entry("ck_int4_matvec"), entry("ck_int4_workspace_size"),
                 entry("ck_control_logits"), entry("ck_logits_workspace_size"), _check)
-    _native = module
+    return module
 
 
 def native():
-    """The module ck_binding."""
+    """The module ck_binding, or what stands in its place."""
     if _native is None:
         load()
     return _native

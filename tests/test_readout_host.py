@@ -220,3 +220,43 @@ def test_workspace_comes_from_the_stream_that_uses_it(monkeypatch):
     _ck.ck_int4_matvec(*args)
     _ck.ck_int4_matvec(*args, stream=Stream())
     assert ran == [0, 77] and took == [0, 77]
+
+
+def test_the_library_loads_without_the_compiled_module(monkeypatch):
+    """No host compiler for Python modules: the library loads, says so once, and every call
+    is left to its Python form."""
+    import sparse_graph_recurrent_gb300 as ck
+    from sparse_graph_recurrent_gb300 import _ck
+
+    def fails(force=False):
+        raise RuntimeError("g++ failed")
+
+    _ck.load()
+    monkeypatch.setattr(_ck, "_lib", None)
+    monkeypatch.setattr(_ck, "_native", None)
+    monkeypatch.setattr(_ck._build, "build_binding", fails)
+    with pytest.warns(RuntimeWarning, match="g\\+\\+ failed"):
+        lib = _ck.load()
+    assert lib is _ck.load() and lib.ck_query_status is not None
+    x = torch.zeros(2, 64)
+    assert _ck.native().dropout(x, 0.5, 1, 0, False) is None
+    assert _ck.native().int4_matvec(x, x, x, None, None, 32, None) is None
+    assert _ck.native().control(x, *[None] * 9, True, 0, None, 0) is None
+    for call in (lambda: ck.dropout(x, 0.5, 1), lambda: ck.control_logits(x), lambda: ck.pick_tokens(x)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_a_library_that_does_not_load_is_not_half_loaded(monkeypatch):
+    from sparse_graph_recurrent_gb300 import _ck
+
+    def fails(lib):
+        raise RuntimeError("no")
+
+    _ck.load()
+    monkeypatch.setattr(_ck, "_lib", None)
+    monkeypatch.setattr(_ck, "_native", None)
+    monkeypatch.setattr(_ck, "_load_native", fails)
+    for _ in range(2):
+        with pytest.raises(RuntimeError):
+            _ck.load()
