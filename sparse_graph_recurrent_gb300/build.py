@@ -14,7 +14,7 @@ stamps around each phase of a microstep, read with ck_phase_profile_read; the
 binding loads it when CK_LIBRARY_VARIANT=prof.
 
 csrc/binding.cpp, the short way from Python to the readout operators, is compiled
-by the host compiler against torch's headers into _build/ck_binding-<torch>.so.
+by the host compiler against torch's headers into _build/ck_binding-<torch><ABI>.so.
 """
 from __future__ import annotations
 
@@ -22,6 +22,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -90,18 +91,21 @@ def build(force: bool = False, verbose: bool = False, variant=None) -> str:
     return lib
 
 
+def binding_path() -> str:
+    """Where ck_binding lies for this torch and this interpreter, whose ABIs it has."""
+    import torch
+    return os.path.join(OUT, f"ck_binding-{torch.__version__}" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
 def build_binding(force: bool = False) -> str:
     """Compile the Python module ck_binding if its source or ck.h is newer than it;
     return its path."""
-    import sysconfig
-
-    import torch
-    from torch.utils import cpp_extension
-    src = os.path.join(CSRC, "binding.cpp")
-    out = os.path.join(OUT, f"ck_binding-{torch.__version__}.so")
+    src, out = os.path.join(CSRC, "binding.cpp"), binding_path()
     deps = [src, os.path.join(ROOT, "include", "ck.h")]
     if not force and os.path.exists(out) and os.path.getmtime(out) >= max(map(os.path.getmtime, deps)):
         return out
+    import torch
+    from torch.utils import cpp_extension
     os.makedirs(OUT, exist_ok=True)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     includes = [os.path.join(ROOT, "include"), *cpp_extension.include_paths(),

@@ -260,3 +260,17 @@ def test_a_library_that_does_not_load_is_not_half_loaded(monkeypatch):
     for _ in range(2):
         with pytest.raises(RuntimeError):
             _ck.load()
+
+
+def test_the_compiled_module_is_of_one_interpreter(monkeypatch):
+    """Another interpreter or torch has a file of its own; a current one is taken as it is."""
+    import sysconfig
+
+    from sparse_graph_recurrent_gb300 import build
+    here = build.build_binding()
+    assert sysconfig.get_config_var("EXT_SUFFIX") in here and torch.__version__ in here
+    monkeypatch.setattr(build.subprocess, "run", None)  # nothing is compiled again
+    assert build.build_binding() == here
+    real = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".other.so" if name == "EXT_SUFFIX" else real(name))
+    assert build.binding_path() != here
