@@ -114,15 +114,23 @@ __device__ __forceinline__ uint4 load_vec(const T *line, int64_t e, int64_t leng
     return *(const uint4 *)t;
 }
 
+// Where in the generator's blocks of four a piece of E elements begins.
+enum Start {
+    kPiece,  // at a multiple of E
+    kBlock,  // at a multiple of four
+    kWithin  // anywhere
+};
+
 // Which of a piece's E elements are kept.
 template <typename T> struct Keep {
     bool k[kVec<T>];
-    // elements m .. m + E - 1 of the mask; SHIFTED: m is not a multiple of four
-    template <bool SHIFTED>
+    // elements m .. m + E - 1 of the mask
+    template <int START>
     __device__ __forceinline__ void make(const DropArgs &a, uint64_t step, int64_t m) {
+        constexpr bool SHIFTED = START == kWithin;
         constexpr int E = kVec<T>, kBlocks = E / 4 + (SHIFTED ? 1 : 0);
         uint4 r[kBlocks];
-        if constexpr (!SHIFTED && kBlocks == 2) {
+        if constexpr (START == kPiece && kBlocks == 2) {
             philox_two((uint64_t)(m >> 2), step, a.keys, r[0], r[1]);
         } else {
 #pragma unroll
@@ -179,15 +187,15 @@ __global__ void __launch_bounds__(kDropThreads, 7) k_dropout_dense(const __grid_
     for (int i = 0; i < kUnroll; ++i) {
         if (q0 + i * kDropThreads >= n) return;
         Keep<T> keep;
-        keep.template make<false>(a, step, (q0 + i * kDropThreads) * kVec<T>);
+        keep.template make<kPiece>(a, step, (q0 + i * kDropThreads) * kVec<T>);
         if (a.drop_all) v[i] = make_uint4(0, 0, 0, 0);
         __stcs(y + i * kDropThreads, keep.apply(v[i], a.scale));
     }
 }
 
-// LOCKED: the mask has `period` elements and y several times as many.  SHIFTED: and
-// the period is no multiple of four, so that a piece of y begins anywhere in a block.
-template <typename T, bool LOCKED, bool SHIFTED>
+// LOCKED: the mask has `period` elements and y several times as many.  Where its pieces
+// begin then depends on the factors that the period has.
+template <typename T, bool LOCKED, int START>
 __global__ void __launch_bounds__(kDropThreads) k_dropout_flat(const __grid_constant__ DropFlat f) {
     constexpr int E = kVec<T>, kUnroll = 1;
     const DropArgs &a = f.a;
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout_flat(const __grid_cons
         if (e >= f.n) continue;
         const int64_t m = LOCKED ? (f.small ? (uint32_t)e % (uint32_t)f.period : e % f.period) : e;
         Keep<T> keep;
-        keep.template make<SHIFTED>(a, step, m);
+        keep.template make<START>(a, step, m);
         if (LOCKED && m + E > f.period) {  // the mask begins again, perhaps more than once
             for (int k = 0; k < E; ++k) {
                 const int64_t mk = (m + k) % f.period;
@@ -269,7 +277,7 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout_lines(const __grid_con
     const int64_t m = ((int64_t)blockIdx.x * kDropThreads + threadIdx.x) * E;
     if (m >= f.period) return;
     Keep<T> keep;
-    keep.template make<false>(a, a.keys.at(), m);
+    keep.template make<kPiece>(a, a.keys.at(), m);
     const int64_t k0 = (int64_t)blockIdx.y * lines, k1 = k0 + lines < a.rep ? k0 + lines : a.rep;
     const T *x = (const T *)a.x + k0 * a.xr;
     T *y = (T *)a.y + k0 * f.period + m;
@@ -339,11 +347,13 @@ template <typename T> void launch_dropout(const DropArgs &a, cudaStream_t stream
     }
     const unsigned grid = (unsigned)((pieces + kDropThreads - 1) / kDropThreads);
     if (a.rep == 1)
-        k_dropout_flat<T, false, false><<<grid, kDropThreads, 0, stream>>>(f);
+        k_dropout_flat<T, false, kPiece><<<grid, kDropThreads, 0, stream>>>(f);
+    else if (f.period % E == 0)
+        k_dropout_flat<T, true, kPiece><<<grid, kDropThreads, 0, stream>>>(f);
     else if (f.period % 4 == 0)
-        k_dropout_flat<T, true, false><<<grid, kDropThreads, 0, stream>>>(f);
+        k_dropout_flat<T, true, kBlock><<<grid, kDropThreads, 0, stream>>>(f);
     else
-        k_dropout_flat<T, true, true><<<grid, kDropThreads, 0, stream>>>(f);
+        k_dropout_flat<T, true, kWithin><<<grid, kDropThreads, 0, stream>>>(f);
 }
 
 }  // namespace

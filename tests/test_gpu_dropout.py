@@ -267,3 +267,34 @@ def test_forward_mode():
     same(g, expected(torch.ones_like(x), 0.25, 13, 21, False))
     with fwd.dual_level():  # a level alone changes nothing
         same(ck.dropout(x, 0.25, 13, 21), expected(x, 0.25, 13, 21, False))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_locked_mask_past_two_to_the_34_elements(dtype):
+    """A mask whose length is 4 mod 8, so that its repeats begin in the middle of 16 bytes,
+    and long enough that the generator's block number carries into its high word."""
+    import sparse_graph_recurrent_gb300 as ck
+    n2, n3 = 1048321, 16388
+    period = n2 * n3
+    assert period > 2 ** 34 and period % 8 == 4
+    if torch.cuda.mem_get_info()[0] < 2 * period * 2 + 2 ** 34:
+        pytest.skip("needs 80 GB of device memory")
+    row = torch.ones(n3, dtype=dtype, device="cuda")
+    y = ck.dropout(row.expand(2, n2, n3), 0.5, 13, 3, locked=True).view(2, period)
+    for at in (0, 2 ** 33 - 40, 2 ** 34 - 40, period - 80):
+        w = ro.philox_words(np.arange(at, at + 80), 13, 3).astype(np.int64)
+        want = torch.from_numpy(w >= 2 ** 31)
+        for k in (0, 1):
+            assert torch.equal(y[k, at:at + 80].cpu() > 0, want), (at, k)
+    del y
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [8, 12, 10, 9, 2052])
+def test_locked_masks_whose_repeats_begin_anywhere(n, dtype):
+    """Periods of every remainder, dense and in rows cut out of wider ones."""
+    import sparse_graph_recurrent_gb300 as ck
+    for cut in (0, 3):
+        x = data((5, 3, n + cut), dtype, n)[..., :n]
+        same(ck.dropout(x, 0.4, 7, 2 ** 35 + 1, locked=True), expected(x, 0.4, 7, 2 ** 35 + 1, True))
