@@ -17,10 +17,10 @@ import torch
 from . import _ck
 from ._ck import CKError  # noqa: F401
 from .readout import (control_logits, dropout, dropout_backward, int4_matvec, int4_quantize,
-                      pick_tokens)
+                      int4_rows, pick_tokens)
 
 __all__ = ["SparseGraph", "sparse_recurrence", "CKError", "forward", "backward", "dropout",
-           "dropout_backward", "int4_quantize", "int4_matvec", "control_logits", "pick_tokens"]
+           "dropout_backward", "int4_quantize", "int4_rows", "int4_matvec", "control_logits", "pick_tokens"]
 
 
 class SparseGraph:

@@ -174,6 +174,7 @@ PyObject *int4_matvec(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t xs = row_stride(*x.t), qs = row_stride(*q.t), ss = row_stride(*s.t),
                       zs = z.none ? 0 : row_stride(*z.t), os = o.none ? V : row_stride(*o.t);
         if (xs < 0 || qs < 0 || ss < 0 || zs < 0 || os < 0) return leave_it();
+        if (V > 1 && qs % 16 && qs == q.t->size(1)) return leave_it();  // rows to be laid out first
         const int64_t pitch = V > 1 ? qs : (q.t->size(1) + 15) / 16 * 16;
         size_t need = 0;
         ck_status st = matvec_size_entry(dtype, M, K, V, (int64_t)group, &need);

@@ -22,7 +22,7 @@ from torch.autograd.graph import increment_version
 
 from . import _ck
 
-__all__ = ["dropout", "dropout_backward", "int4_quantize", "int4_matvec", "control_logits",
+__all__ = ["dropout", "dropout_backward", "int4_quantize", "int4_rows", "int4_matvec", "control_logits",
            "pick_tokens"]
 
 
@@ -137,8 +137,8 @@ def dropout_backward(d_out, p: float, seed: int, step=0, locked: bool = False):
 def int4_quantize(w, group_size: int = 128, symmetric: bool = True, scale_dtype=None):
     """4-bit weights of w [V, K] in groups of 32, 64 or 128 along K: (qweight,
     scales, zeros) for int4_matvec, zeros None when symmetric.  qweight is uint8
-    [V, (K + 1) // 2], low nibble first, its rows at a multiple of 16 bytes;
-    scales [V, ceil(K / group_size)] in scale_dtype (w's by default)."""
+    [V, (K + 1) // 2], low nibble first, its rows at a multiple of 16 bytes (see
+    int4_rows); scales [V, ceil(K / group_size)] in scale_dtype (w's by default)."""
     if w.dim() != 2 or w.shape[1] < 1 or not w.is_cuda:
         raise ValueError("w must be a CUDA tensor [V, K] with K >= 1")
     if group_size not in _ck.INT4_GROUPS:
@@ -156,11 +156,26 @@ def int4_quantize(w, group_size: int = 128, symmetric: bool = True, scale_dtype=
     return q, scales, zeros
 
 
+def int4_rows(qweight):
+    """qweight uint8 [V, (K + 1) // 2] with its rows at a multiple of 16 bytes, as the
+    product reads them: itself, or a copy where clone, to or a concatenation has put
+    the rows one after another."""
+    if qweight.dim() != 2 or qweight.dtype != torch.uint8:
+        raise ValueError("qweight must be uint8 [V, (K + 1) // 2]")
+    V, n = qweight.shape
+    if ((V < 2 or qweight.stride(0) % 16 == 0) and (n < 2 or qweight.stride(1) == 1)
+            and qweight.data_ptr() % 16 == 0):
+        return qweight
+    q = torch.zeros((V, -(-n // 16) * 16), dtype=torch.uint8, device=qweight.device)[:, :n]
+    return q.copy_(qweight)
+
+
 def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128, out=None):
     """x [..., K] times the transpose of the 4-bit weights (int4_quantize), plus
     bias (float32 [V]): [..., V] in x's type.  For a few rows of x at a time, as
     when answering; it has no gradient.  `out`, if given, is written instead of a
-    new tensor."""
+    new tensor.  Weights whose rows follow one another without a gap, and not at
+    multiples of 16 bytes, are laid out by int4_rows in every call."""
     y = (_ck._native or _ck.native()).int4_matvec(x, qweight, scales, zeros, bias, group_size, out)
     if y is not None:
         return y
@@ -171,6 +186,8 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
     if x.dim() < 1 or qweight.dim() != 2:
         raise ValueError("x is [..., K] and qweight [V, (K + 1) // 2]")
     V = qweight.shape[0]
+    if V > 1 and qweight.shape[1] % 16 and qweight.dtype == torch.uint8 and qweight.is_contiguous():
+        qweight = int4_rows(qweight)
     x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
     if x2.shape[1] > 1 and x2.stride(1) != 1:
         x2 = x2.contiguous()

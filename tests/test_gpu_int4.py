@@ -388,3 +388,20 @@ def test_a_wait_that_runs_out_with_copies_on_their_way(K):
         _ck.ck_set_option(_ck.OPT_TEST_BARRIER_EXTRA, 0)
         _ck.ck_set_option(_ck.OPT_BARRIER_TIMEOUT_NS, 4_000_000_000)
     check(ck.int4_matvec(**c, group_size=64), c, 64)
+
+
+@pytest.mark.parametrize("K", [5000, 64, 333, 1])
+@pytest.mark.parametrize("symmetric", [True, False])
+def test_weights_that_were_copied(K, symmetric):
+    """clone, to and a state_dict's copy make the rows of the weights dense; the product is the same."""
+    import sparse_graph_recurrent_gb300 as ck
+    q, s, z = ck.int4_quantize(torch.randn(70, K, device="cuda"), 32, symmetric)
+    for M in (1, 20):
+        x = torch.randn(M, K, device="cuda")
+        want = ck.int4_matvec(x, q, s, z, group_size=32)
+        for c in (q.clone(), q.cpu().cuda(), q.contiguous(), torch.cat([q[:40], q[40:]])):
+            assert torch.equal(ck.int4_matvec(x, c, s, z, group_size=32), want)
+            again = ck.int4_rows(c)
+            assert torch.equal(again, q) and again.stride(0) % 16 == 0 and again.data_ptr() % 16 == 0
+            assert torch.equal(ck.int4_matvec(x, again, s, z, group_size=32), want)
+    assert ck.int4_rows(q) is q

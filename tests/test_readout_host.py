@@ -274,3 +274,16 @@ def test_the_compiled_module_is_of_one_interpreter(monkeypatch):
     real = sysconfig.get_config_var
     monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".other.so" if name == "EXT_SUFFIX" else real(name))
     assert build.binding_path() != here
+
+
+def test_weight_rows_are_laid_out_again():
+    import sparse_graph_recurrent_gb300 as ck
+    q = torch.randint(0, 256, (7, 33), dtype=torch.uint8)
+    a = ck.int4_rows(q)
+    assert torch.equal(a, q) and a.stride() == (48, 1) and a.data_ptr() % 16 == 0
+    assert ck.int4_rows(a) is a and ck.int4_rows(a[2:5]).data_ptr() == a[2:].data_ptr()
+    for v in (q.t().contiguous().t(), a[:, 1:], q[:1], q[:0]):
+        assert torch.equal(ck.int4_rows(v), v)
+    for bad in (q.int(), q[0]):
+        with pytest.raises(ValueError):
+            ck.int4_rows(bad)
