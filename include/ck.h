@@ -403,8 +403,8 @@ ck_status ck_int4_quantize(const void *w, int64_t dtype, int64_t V, int64_t K, i
  *      history[b][prompt_b : len_b]
  *   3. z + bias[v]
  *   4. -inf where bit v % 32 of mask word v / 32 is 0
- *   5. z / temperature where temperature > 0 (in `out` the product with 1 /
- *      temperature, one rounding more, where that is a normal number)
+ *   5. z / temperature where temperature > 0 (in an `out` of 16 bits the product
+ *      with 1 / temperature, one rounding of 32 bits more, where that is a normal number)
  * Ids outside [0, V) in the history are ignored (padding).  len_b and prompt_b
  * are clamped to [0, L].  out[b][v] = z, rounded to the logits' type.
  * tokens[b] = the v of the largest z (of equal ones the lowest v), before

@@ -317,7 +317,8 @@ def control_logits(logits, history=None, history_len=None, prompt_len=None, repe
     z > 0, else z * r), frequency and presence penalties by its count in
     history[b, prompt_len[b]:history_len[b]], bias (float32 [V] or [B, V]), mask
     (int32 words [ceil(V / 32)] or [B, ceil(V / 32)], bit v % 32 of word v // 32
-    allows token v, else -inf), then division by temperature (not where it is 0).
+    allows token v, else -inf), then division by temperature (not where it is 0; of 16-bit
+    logits a product with its reciprocal, one rounding of 32 bits more).
     Penalties and temperature are numbers or float32 [B]; history int64 or int32
     [B, L], ids outside [0, V) ignored; lengths [B] in its type."""
     got = (_ck._native or _ck.native()).control(

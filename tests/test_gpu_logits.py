@@ -396,3 +396,45 @@ def test_ties_of_scores_that_overflow():
     x[0, 4000:], x[1, 7::9] = 3e38, 2e38                        # at an ordinary temperature
     assert ck.pick_tokens(x, temperature=0.5).tolist() == [4000, 7]
     assert ck.pick_tokens(x, temperature=0.5, seed=1).tolist() == [4000, 7]
+
+
+@pytest.mark.parametrize("V", [300, 20001])
+def test_fp32_logits_are_the_quotient(V):
+    """Of 32-bit logits and no other control the result is z / T, rounded once."""
+    import sparse_graph_recurrent_gb300 as ck
+    rng = np.random.default_rng(V)
+    z = (3 * rng.standard_normal((40, V))).astype(np.float32)
+    t = (0.1 + 2 * rng.random(40)).astype(np.float32)
+    x, temps = torch.from_numpy(z).cuda(), torch.from_numpy(t).cuda()
+    want = z / t[:, None]
+    assert np.array_equal(ck.control_logits(x, temperature=temps).cpu().numpy(), want)
+    for seed in (None, 4):
+        tokens, out = ck.pick_tokens(x, temperature=temps, seed=seed, return_logits=True)
+        assert np.array_equal(out.cpu().numpy(), want)
+        if seed is None:
+            assert tokens.cpu().tolist() == want.argmax(1).tolist()
+    assert np.array_equal(ck.control_logits(x, temperature=0.7).cpu().numpy(), z / np.float32(0.7))
+    assert torch.equal(ck.control_logits(x, temperature=1.0), x)
+
+
+def test_fp32_quotients_over_the_whole_type():
+    """Any 32 bits by any temperature: the division's result, bit for bit but for NaN's payload."""
+    import sparse_graph_recurrent_gb300 as ck
+    g = torch.Generator().manual_seed(3)
+    bits = lambda *n: torch.randint(-2 ** 31, 2 ** 31, n, generator=g).int().view(torch.float32)  # noqa: E731
+    B, V = 400, 40000
+    t = bits(B).abs()
+    t[torch.isnan(t)] = 0.7
+    t[::2] = torch.rand(B, generator=g)[::2] * 3 + 0.01            # half of them ordinary
+    t[:8] = torch.tensor([1 - 2.0 ** -24, 1 + 2.0 ** -23, 2 - 2.0 ** -23, 0.75, 1.5, 2.0, 2.0 ** -126, 2.0 ** 127])
+    x = bits(B, V)
+    near = torch.randn(B // 2, V, generator=g) * 5
+    x[::2] = near
+    x[:, :6] = torch.tensor([0.0, -0.0, INF, -INF, 1e-45, 3.4e38])
+    want = torch.where(t[:, None] > 0, x.cuda().cpu().div(t[:, None]), x)
+    want_dev = torch.where(t.cuda()[:, None] > 0, x.cuda() / t.cuda()[:, None], x.cuda())
+    out = ck.control_logits(x.cuda(), temperature=t.cuda())
+    for w in (want.cuda(), want_dev):
+        nan = torch.isnan(w)
+        assert torch.equal(torch.isnan(out), nan)
+        assert torch.equal(out[~nan].view(torch.int32), w[~nan].view(torch.int32))
