@@ -389,8 +389,8 @@ def ck_dropout(x, y, n0, n1, n2, x0, x1, x2, p: float, seed: int, step=0, locked
     if type(step) is not int:
         step, dev = _step_args(step, device)
     status = (_lib or load()).ck_dropout(
-        x.data_ptr(), y.data_ptr(), dtype, n0, n1, n2, x0, x1, x2, n1 * n2, n2, 1, locked, p,
-        seed & _U64, step & _U64, dev,
+        x.data_ptr(), y.data_ptr(), dtype, n0, n1, n2, x0, x1, x2, n1 * n2, n2, 1, bool(locked), float(p),
+        int(seed) & _U64, step & _U64, dev,
         _get_raw_stream(_get_device()) if stream is None else stream.cuda_stream)
     if status:
         _check(status)

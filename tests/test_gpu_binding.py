@@ -114,3 +114,18 @@ def test_writing_into_a_tensor_raises_its_version(both):
             with pytest.raises(RuntimeError, match="modified by an inplace operation"):
                 y.backward()
         both(run)
+
+
+def test_numpy_numbers(both):
+    import numpy as np
+
+    import sparse_graph_recurrent_gb300 as ck
+    x = torch.randn(2, 64, device="cuda")
+    want = ck.dropout(x, 0.5, 5, 6)
+    a, b = both(lambda: ck.dropout(x, np.float32(0.5), np.int64(5), np.int32(6)))
+    assert torch.equal(a, want) and torch.equal(b, want)
+    h = torch.ones(2, 2, 64, device="cuda")
+    a, b = both(lambda: ck.dropout(h, 0.5, np.uint64(5), np.int64(6), locked=np.bool_(True)))
+    assert torch.equal(a, b) and torch.equal(a[0], a[1])
+    a, b = both(lambda: ck.pick_tokens(x, temperature=np.float32(0.5), seed=np.int64(5), step=np.int64(6)))
+    assert torch.equal(a, ck.pick_tokens(x, temperature=0.5, seed=5, step=6)) and torch.equal(a, b)
