@@ -10,6 +10,9 @@
 // that the process has loaded, whichever variant that is.
 #include <Python.h>
 
+#include <cfloat>
+#include <cmath>
+
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/GradMode.h>
@@ -242,7 +245,7 @@ PyObject *control(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (o == Py_None) continue;
             if (PyFloat_Check(o)) {
                 const double v = PyFloat_AS_DOUBLE(o);
-                if (!(v >= r.least && v < 1e300)) return leave_it();
+                if (!(v >= r.least && v <= FLT_MAX) || (v != 0 && fabs(v) < FLT_MIN)) return leave_it();
                 *r.all = (float)v;
                 continue;
             }

@@ -14,8 +14,6 @@ ck_binding; what that leaves is done, or refused, here.
 """
 from __future__ import annotations
 
-import math
-
 import torch
 from torch.autograd import forward_ad
 from torch.autograd.graph import increment_version
@@ -212,6 +210,10 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
 # -- controls on logits, and the token -------------------------------------------------------
 
 
+_MOST = 3.4028234663852886e38   # of 32-bit floats the largest
+_LEAST = 1.401298464324817e-45  # and the smallest above 0
+
+
 def _per_row(name, v, default, low, B, device):
     """(pointer, number) of a control given as one number or as float32 [B]."""
     if v is None:
@@ -221,7 +223,7 @@ def _per_row(name, v, default, low, B, device):
             raise ValueError(f"{name} must be a number or a contiguous float32 [{B}] on cuda:{device}")
         return v.data_ptr(), default
     v = float(v)
-    if not low <= v < math.inf:
+    if not low <= v <= _MOST or (low == 0 and 0 < v < _LEAST):  # (1e-50 is no temperature of 0)
         raise ValueError(f"{name} = {v} is out of range")
     return None, v
 

@@ -129,3 +129,17 @@ def test_numpy_numbers(both):
     assert torch.equal(a, b) and torch.equal(a[0], a[1])
     a, b = both(lambda: ck.pick_tokens(x, temperature=np.float32(0.5), seed=np.int64(5), step=np.int64(6)))
     assert torch.equal(a, ck.pick_tokens(x, temperature=0.5, seed=5, step=6)) and torch.equal(a, b)
+
+
+def test_numbers_that_32_bits_do_not_hold_are_refused(both):
+    import sparse_graph_recurrent_gb300 as ck
+    x = torch.randn(2, 64, device="cuda")
+    for kw in (dict(temperature=1e39), dict(temperature=1e-50), dict(repetition=1e39), dict(frequency=1e200),
+               dict(presence=4e38)):
+        for call in (ck.control_logits, ck.pick_tokens):
+            def refused():
+                with pytest.raises(ValueError):
+                    call(x, **kw)
+            both(refused)
+    for kw in (dict(temperature=0), dict(temperature=3e38), dict(temperature=2e-45), dict(frequency=1e-60)):
+        both(lambda: ck.control_logits(x, **kw))
