@@ -320,7 +320,8 @@ ck_status ck_step_advance(int64_t *step, void *stream);
  * Readout operators: what a program does with the states of a recurrent token
  * model (connectome-kernels page, intro: a connectome trained on text).  They
  * need no graph handle.  Element types are given as a ck_dtype; everything is
- * computed in 32-bit floats and rounded once to the output's type.
+ * computed in 32-bit floats and rounded once to the output's type.  A pointer that
+ * is not aligned to its elements is refused (CK_ERR_INVALID_ARG).
  */
 typedef enum { CK_F32 = 0, CK_BF16 = 1, CK_F16 = 2 } ck_dtype;
 

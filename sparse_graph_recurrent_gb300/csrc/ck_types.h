@@ -23,6 +23,8 @@ template <> __device__ __forceinline__ __half from_float<__half>(float v) { retu
 
 inline bool known_dtype(int64_t d) { return d == CK_F32 || d == CK_BF16 || d == CK_F16; }
 inline size_t dtype_size(int64_t d) { return d == CK_F32 ? 4 : 2; }
+// Whether p lies at a multiple of `bytes`, as a kernel's loads of that size need.
+inline bool aligned(const void *p, size_t bytes) { return (uintptr_t)p % bytes == 0; }
 
 // f((T *)nullptr) with T the element type of a (checked) ck_dtype.
 template <typename F> auto with_dtype(int64_t d, F &&f) {

@@ -655,6 +655,9 @@ extern "C" ck_status ck_int4_matvec(const void *x, int64_t dtype, int64_t M, int
         return fail(CK_ERR_UNSUPPORTED, "int4_matvec: a size of 2^30 or more");
     if (M == 0 || V == 0) return CK_OK;
     if (!x || !qweight || !scales || !y) return fail(CK_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned(x, dtype_size(dtype)) || !aligned(y, dtype_size(dtype)) ||
+        !aligned(scales, dtype_size(scale_dtype)) || !aligned(bias, 4))
+        return fail(CK_ERR_INVALID_ARG, "int4_matvec: a pointer is not aligned to its elements");
     if (q_pitch % 16 != 0 || ((uintptr_t)qweight & 15u) != 0 || q_pitch < (K + 1) / 2)
         return fail(CK_ERR_INVALID_ARG,
                     "int4_matvec: weight rows must start at multiples of 16 bytes and hold (K + 1) / 2 bytes");
@@ -723,6 +726,8 @@ extern "C" ck_status ck_int4_quantize(const void *w, int64_t dtype, int64_t V, i
     if (V == 0) return CK_OK;
     if (!w || !qweight || !scales || (!symmetric && !zeros))
         return fail(CK_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned(w, dtype_size(dtype)) || !aligned(scales, dtype_size(scale_dtype)))
+        return fail(CK_ERR_INVALID_ARG, "int4_quantize: a pointer is not aligned to its elements");
     const int64_t G = (K + group - 1) / group;
     if (q_pitch < (K + 1) / 2 || s_stride < G || (!symmetric && z_stride < G) || w_stride < 0)
         return fail(CK_ERR_INVALID_ARG, "int4_quantize: a row stride is shorter than its row");

@@ -287,3 +287,32 @@ def test_weight_rows_are_laid_out_again():
     for bad in (q.int(), q[0]):
         with pytest.raises(ValueError):
             ck.int4_rows(bad)
+
+
+def test_misaligned_pointers_are_refused_on_the_host():
+    """Each pointer, off by a byte, is an error and not a misaligned access on the device."""
+    _ck, lib = _lib()
+    raw = ctypes.create_string_buffer(8192)
+    base = -(-ctypes.addressof(raw) // 64) * 64
+
+    def refused(status):
+        return status == 1 and b"not aligned" in lib.ck_last_error_message()
+
+    for dtype in (0, 1, 2):
+        for off in ("x", "y", "step"):
+            a = {k: base + (off == k) for k in ("x", "y", "step")}
+            assert refused(lib.ck_dropout(a["x"], a["y"], dtype, 1, 1, 8, 0, 0, 1, 0, 0, 1, 0, 0.5, 1, 1, a["step"], None))
+        for off in ("x", "s", "b", "y"):
+            a = {k: base + (off == k) for k in ("x", "s", "b", "y")}
+            assert refused(lib.ck_int4_matvec(a["x"], dtype, 1, 64, 64, base, 2, 32, a["s"], dtype, 2, None, 0, a["b"], 32,
+                                              a["y"], 2, None, 0, None))
+        for off in ("w", "s"):
+            a = {k: base + (off == k) for k in ("w", "s")}
+            assert refused(lib.ck_int4_quantize(a["w"], dtype, 2, 64, 64, 32, 1, base, 32, a["s"], dtype, 2, None, 0, None))
+        for bits in (32, 64):
+            for off in ("logits", "out", "tokens", "step_dev", "history", "history_len", "prompt_len", "repetition",
+                        "frequency", "presence", "temperature", "bias", "mask"):
+                a = dict(dtype=dtype, B=1, V=8, logits_stride=8, out_stride=8, repetition_all=1.0, temperature_all=1.0,
+                         logits=base, out=base, history=base, history_bits=bits, L=4, history_stride=4)
+                a[off] = base + 1
+                assert refused(lib.ck_control_logits(ctypes.byref(_ck.LogitCall(**a)), None)), off
