@@ -416,8 +416,8 @@ ck_status ck_int4_quantize(const void *w, int64_t dtype, int64_t V, int64_t K, i
  * All pointers are device pointers; a pointer that is NULL takes the *_all value
  * for every row (repetition, frequency, presence, temperature), L (history_len),
  * 0 (prompt_len), or leaves its control out (history, bias, mask, out, tokens).
- * out may be logits.  Strides are in elements (mask: words); a bias_stride or
- * mask_stride of 0 shares one row.  Asynchronous.
+ * out may be logits.  Strides are in elements (mask: words; that of out at least V);
+ * a bias_stride or mask_stride of 0 shares one row.  Asynchronous.
  * `workspace` (device, 8-byte aligned) holds workspace_bytes, at least what
  * ck_logits_workspace_size says for the same B, V and L (0 without a history) on this
  * device; needed where tokens are, if that is not 0 bytes.

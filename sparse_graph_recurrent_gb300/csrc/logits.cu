@@ -536,6 +536,8 @@ extern "C" ck_status ck_control_logits(const ck_logit_call *call, void *stream) 
     if (!a.logits || (!a.out && !a.tokens)) return fail(CK_ERR_INVALID_ARG, "a required pointer is NULL");
     if (a.history && ((a.history_bits != 32 && a.history_bits != 64) || a.L < 0 || a.L >= ((int64_t)1 << 30)))
         return fail(CK_ERR_INVALID_ARG, "control_logits: history of 32 or 64 bits, 0 <= L < 2^30");
+    if (a.out && a.B > 1 && a.out_stride < a.V)
+        return fail(CK_ERR_INVALID_ARG, "control_logits: the rows of out overlap");
     const size_t el = dtype_size(a.dtype), id = a.history && a.history_bits == 32 ? 4 : 8;
     if (!aligned(a.logits, el) || !aligned(a.out, el) || !aligned(a.tokens, 8) || !aligned(a.step_dev, 8) ||
         (a.history && (!aligned(a.history, id) || !aligned(a.history_len, id) || !aligned(a.prompt_len, id))) ||

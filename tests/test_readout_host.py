@@ -316,3 +316,14 @@ def test_misaligned_pointers_are_refused_on_the_host():
                          logits=base, out=base, history=base, history_bits=bits, L=4, history_stride=4)
                 a[off] = base + 1
                 assert refused(lib.ck_control_logits(ctypes.byref(_ck.LogitCall(**a)), None)), off
+
+
+def test_rows_of_out_that_overlap_are_refused():
+    """Several rows written to one place would leave whichever came last."""
+    _ck, lib = _lib()
+    buf = (ctypes.c_float * 64)()
+    for stride in (0, 7, -8):
+        a = dict(logits=ctypes.addressof(buf), dtype=0, B=2, V=8, logits_stride=8, out=ctypes.addressof(buf), out_stride=stride,
+                 repetition_all=1.0, temperature_all=1.0)
+        assert lib.ck_control_logits(ctypes.byref(_ck.LogitCall(**a)), None) == 1
+        assert b"overlap" in lib.ck_last_error_message()
