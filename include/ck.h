@@ -334,7 +334,7 @@ typedef enum { CK_F32 = 0, CK_BF16 = 1, CK_F16 = 2 } ck_dtype;
  * it (ck_step_advance) draws anew on every replay.
  *
  * ck_dropout -- y[i] = keep_i ? x[i] / (1 - p) : 0 over a tensor [n0][n1][n2]
- * of `dtype` with the element strides given for x and y (x strides may be 0);
+ * of `dtype` with the element strides given for x and y (x strides may be 0, y strides not);
  * keep_i = word_i >= round(p 2^32), i the row-major index in [n0][n1][n2], or in
  * [n1][n2] when `locked` (one mask for all n0 entries: the input steps of a
  * recurrence).  The factor is 1 / (1 - p) rounded to 32 bits; p = 1 drops all.

@@ -373,6 +373,8 @@ extern "C" ck_status ck_dropout(const void *x, void *y, int64_t dtype, int64_t n
     if (n0 > kMost / n1 || n0 * n1 > kMost / n2)
         return fail(CK_ERR_UNSUPPORTED, "dropout: more than 2^40 elements");
     if (!x || !y) return fail(CK_ERR_INVALID_ARG, "a required pointer is NULL");
+    if ((n0 > 1 && y0 == 0) || (n1 > 1 && y1 == 0) || (n2 > 1 && y2 == 0))
+        return fail(CK_ERR_INVALID_ARG, "dropout: elements of y share a place (a stride of 0)");
     if (!aligned(x, dtype_size(dtype)) || !aligned(y, dtype_size(dtype)) || !aligned(step_dev, 8))
         return fail(CK_ERR_INVALID_ARG, "dropout: a pointer is not aligned to its elements");
     DropArgs a{};

@@ -327,3 +327,11 @@ def test_rows_of_out_that_overlap_are_refused():
                  repetition_all=1.0, temperature_all=1.0)
         assert lib.ck_control_logits(ctypes.byref(_ck.LogitCall(**a)), None) == 1
         assert b"overlap" in lib.ck_last_error_message()
+
+
+def test_a_dropout_output_that_shares_places_is_refused():
+    _, lib = _lib()
+    buf = (ctypes.c_float * 64)()
+    for y in ((0, 8, 1), (8, 0, 1), (16, 8, 0)):
+        assert lib.ck_dropout(buf, buf, 0, 2, 2, 2, 0, 0, 0, *y, 0, 0.5, 1, 1, None, None) == 1
+        assert b"share a place" in lib.ck_last_error_message()
