@@ -143,3 +143,35 @@ def test_numbers_that_32_bits_do_not_hold_are_refused(both):
             both(refused)
     for kw in (dict(temperature=0), dict(temperature=3e38), dict(temperature=2e-45), dict(frequency=1e-60)):
         both(lambda: ck.control_logits(x, **kw))
+
+
+def test_two_threads_on_two_streams():
+    """Calls of several threads at once, each on a stream of its own, give what one gives."""
+    import threading
+
+    import sparse_graph_recurrent_gb300 as ck
+    q, s, z = ck.int4_quantize(torch.randn(3000, 2000, device="cuda"), 64, symmetric=False)
+    xs = [torch.randn(M, 2000, device="cuda") for M in (1, 20, 4, 33)]
+
+    def work(x):
+        h = ck.dropout(x, 0.3, 5, 6)
+        y = ck.int4_matvec(h, q, s, z, group_size=64)
+        return h, y, *ck.pick_tokens(y, temperature=0.7, seed=3, step=4, return_logits=True)
+
+    want, wrong = [work(x) for x in xs], []
+    torch.cuda.synchronize()
+
+    def run(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(50):
+                got = work(xs[i])
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
