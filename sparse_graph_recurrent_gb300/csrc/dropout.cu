@@ -22,6 +22,11 @@ struct DropArgs {
     PhiloxKeys keys;
 };
 
+// Any strides, element by element: for an innermost axis of x that is not dense.
+// 64 x 32 x 5,000 fp32 take 74 us with the last two axes swapped, 69 as every second
+// element and 60 as one number repeated; the divisions of an element's index and, of
+// the first, sectors read for four bytes of them bound it.
+//
 // A select and not a product: a dropped element is 0 whatever it held.
 template <typename T>
 __global__ void __launch_bounds__(256) k_dropout(const __grid_constant__ DropArgs a) {

@@ -20,9 +20,10 @@ namespace {
 //
 // Measured: 1 x 211,577 bf16 by 4,096 rows, groups of 128, 94 us (4.9 TB/s), 1 x 5,000
 // fp32 by 64,000 rows 40 us (4.3 TB/s), 4 x 20,000 fp16 by 16,384 rows in groups of 32
-// with zero points 69 us (2.8 TB/s: there the instructions bound it, a scale and a zero
-// point for every two products), 1 x 5,000 fp32 by 256 rows 8.2 us (a start, x to shared
-// memory, two units a warp, the sums of twelve warps).
+// with zero points 69 us (2.8 TB/s: with schedulers that issue 44% of their cycles from
+// three warps each it waits for a group's way through ldmatrix, unpacking, two products
+// and a scale), 1 x 5,000 fp32 by 256 rows 8.8 us (a start, x to shared memory, two units
+// a warp, the sums of twelve warps).
 //
 // A unit is 32 weight rows by 256 columns (4 KB).  K is cut into slabs whose x
 // fits in shared memory; the units, in the order (slab, 32-row tile, chunk),
@@ -32,11 +33,13 @@ namespace {
 // k_join adds up in a fixed order.
 constexpr int kHalf = 128;  // columns: scales are taken up for half a unit
 
-// Warps of a CTA, one CTA on an SM, and units of a warp's ring.  Twelve warps have 168
-// registers a thread and need no more; sixteen, with 128 and some spilled, keep more on
-// its way once a warp's run is long.  1 x 211,577 x 4,096 takes 104 us by twelve and
-// 95 by sixteen, 4 x 20,000 x 16,384 (a third of that run) 70 and 73, 1 x 5,000 x 256
-// 8.2 and 9.7.
+// Warps of a CTA, one CTA on an SM, and units of a warp's ring.  Sixteen keep more on its
+// way and pay for it at the start and at the end, so they are taken where a warp's run is
+// long: 1 x 200,000 fp16 by 4,096 in groups of 128 (55 units a warp of twelve) takes 94 us
+// by twelve and 86 by sixteen, 4 x 20,000 by 32,768 (44) 79 and 74, 1 x 5,000 fp32 by 8,192
+// (3) 11.9 and 13.6.  Between 10 and 40 units sixteen are up to 10% faster with 16-bit x
+// and even with 32-bit x, whose three parts leave them no registers: there the two lie
+// within 2% of each other up to 55 units.  4 x 200,000 fp16 loses by sixteen, 100 and 104.
 constexpr int kFewWarps = 12, kManyWarps = 16, kLongRun = 40;
 __host__ __device__ constexpr int ring_units(int warps) { return warps == kFewWarps ? 3 : 2; }
 
@@ -478,7 +481,10 @@ __global__ void __launch_bounds__(128) k_join(MatvecArgs a, MatvecPlan p) {
     if (v < a.V) store_y(a, m, v, sum);
 }
 
-// Rows of x in one launch: what two tensor-core tiles of eight columns hold.
+// Rows of x in one launch: what two tensor-core tiles of eight columns hold.  One row more
+// goes to k_wide, at any size: 5 x 5,000 fp32 by 256, 2,000 and 32,000 rows take 8.8, 10.2
+// and 34 us there and 19, 21 and 59 in two passes of this kernel, 5 x 200,000 by 256 30
+// and 64; 17 rows of bf16 9.2, 10.5, 34 and 31, and 23, 25, 69 and 100.
 int rows_at_once(int64_t dtype) { return dtype == CK_F32 ? 4 : 16; }
 
 // Rows of the next pass of `left`: k_wide's most, or what is left of them.
@@ -585,7 +591,10 @@ struct QuantArgs {
 };
 
 // One warp per group: its range, the scale as it will be stored, then the
-// nibbles rounded against that stored scale.
+// nibbles rounded against that stored scale.  Run once for a readout: 32,000 x 5,000
+// take 472 us in fp32 and 479 in bf16 by groups of 128 (1.5 TB/s and 0.8 of what is read
+// and written), 1,513 in bf16 by groups of 32, which leave half of the lanes idle in the
+// second loop; loads of single elements, each weight twice, bound it.
 template <typename T> __global__ void __launch_bounds__(256) k_quantize(QuantArgs a) {
     const int lane = threadIdx.x & 31;
     const int64_t G = (a.K + a.group - 1) / a.group, items = a.V * G;
