@@ -126,7 +126,8 @@ def dropout(x, p: float, seed: int, step=0, locked: bool = False):
 def dropout_backward(d_out, p: float, seed: int, step=0, locked: bool = False):
     """The gradient of dropout's x from its output's: the same mask and factor again, so
     differentiable in d_out as dropout is in x."""
-    return dropout(d_out, p, seed, step, locked)
+    y = (_ck._native or _ck.native()).dropout(d_out, p, seed, step, locked)
+    return dropout(d_out, p, seed, step, locked) if y is None else y
 
 
 # -- the 4-bit readout -----------------------------------------------------------------------
