@@ -98,6 +98,11 @@ bool step_of(PyObject *o, int dev, uint64_t &step, const int64_t *&at_dev) {
     return true;
 }
 
+// Raises the version of a tensor that a call is about to write, for those who saved it.
+void written(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 void *stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 
 // dropout(x, p, seed, step, locked)
@@ -184,7 +189,7 @@ PyObject *int4_matvec(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (st != CK_OK) return raise_status(st);
         at::Tensor y = o.none ? at::empty({M, V}, x.t->options().requires_grad(false)) : *o.t, ws;
         if (need) ws = at::empty({(int64_t)need}, q.t->options());
-        if (!o.none) y.unsafeGetTensorImpl()->bump_version();  // for those who saved it
+        if (!o.none) written(y);
         st = matvec_entry(x.t->const_data_ptr(), dtype, M, K, xs, (const uint8_t *)q.t->const_data_ptr(), V, pitch,
                           s.t->const_data_ptr(), scale_dtype, ss, z.none ? nullptr : (const uint8_t *)z.t->const_data_ptr(),
                           zs, b.none ? nullptr : (const float *)b.t->const_data_ptr(), (int64_t)group, y.data_ptr(), os,
@@ -304,7 +309,7 @@ PyObject *control(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 c.workspace_bytes = (int64_t)need;
             }
         }
-        if (a[10] != Py_True && out.defined()) out.unsafeGetTensorImpl()->bump_version();  // for those who saved it
+        if (a[10] != Py_True && out.defined()) written(out);
         const ck_status st = logits_entry(&c, stream_of(dev));
         if (st != CK_OK) return raise_status(st);
         if (give == 0) return THPVariable_Wrap(std::move(out));

@@ -36,6 +36,11 @@ def _refuse_derivatives(what, **operands):
             raise ValueError(f"{what} has no derivative: call it under no_grad or on a detached {name}")
 
 
+def _written(out):
+    if not out.is_inference():  # those have no version
+        increment_version(out)
+
+
 # -- dropout ---------------------------------------------------------------------------------
 
 
@@ -196,7 +201,7 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
         if tuple(out.shape) != (*x.shape[:-1], V):
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(*x.shape[:-1], V)}")
         y = out if out.dim() == 2 else out.view(-1, V)
-        increment_version(out)
+        _written(out)
     args = (x2, qweight, scales, zeros, bias, group_size, y)
     if device == _ck._get_device():
         _ck.ck_int4_matvec(*args)
@@ -284,7 +289,7 @@ def _control(logits, history, history_len, prompt_len, repetition, frequency, pr
         if out.dtype != logits.dtype or out.shape != logits.shape or out.get_device() != dev:
             raise ValueError("out must be like logits")
         out_at, out_stride = out.data_ptr(), _ck._rows(out, "out")
-        increment_version(out)
+        _written(out)
     at = step_dev = None
     if seed is not None:
         at, step_dev = _ck._step_args(step, dev)

@@ -175,3 +175,14 @@ def test_two_threads_on_two_streams():
     for t in threads:
         t.join()
     assert not wrong
+
+
+def test_out_made_in_inference_mode(both):
+    """Written outside of it as well as inside: such tensors have no version to raise."""
+    import sparse_graph_recurrent_gb300 as ck
+    q, s, _ = ck.int4_quantize(torch.randn(64, 64, device="cuda"), 32)
+    with torch.inference_mode():
+        out, x = torch.empty(2, 64, device="cuda"), torch.randn(2, 64, device="cuda")
+        inside = both(lambda: (ck.int4_matvec(x, q, s, group_size=32, out=out).clone(), ck.control_logits(x, out=out).clone()))
+    outside = both(lambda: (ck.int4_matvec(x, q, s, group_size=32, out=out).clone(), ck.control_logits(x, out=out).clone()))
+    assert all(torch.equal(u, v) for a, b in zip(inside, outside) for u, v in zip(a, b))
