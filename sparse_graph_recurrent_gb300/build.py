@@ -5,8 +5,8 @@ sparse_graph_recurrent_gb300/_build/libck.so.  Rebuilds only when a source or
 header is newer than the library.
 
 Variant "bounds" builds the same sources with -DCK_DEBUG_BOUNDS into
-_build/libck_bounds.so: every gathered row, table and carry index is checked
-on the device, and a bad one is reported through ck_query_status instead of
+_build/libck_bounds.so: every gathered row, table and carry index of the
+recurrence is checked on the device (the readout operators are as they are), and a bad one is reported through ck_query_status instead of
 being accessed.  The binding loads it when CK_LIBRARY_VARIANT=bounds.
 
 Variant "prof" (-DCK_PHASE_PROFILE, _build/libck_prof.so) adds %globaltimer
