@@ -448,6 +448,54 @@ ck_status ck_logits_workspace_size(int64_t B, int64_t V, int64_t L, size_t *byte
 ck_status ck_control_logits(const ck_logit_call *call, void *stream);
 
 /*
+ * ck_gated_forward, ck_gated_backward -- a linear recurrence over T steps with a gate for
+ * every step, sequence and node, in 32-bit floats:
+ *   CK_GATED_LEAK   l = sigmoid(gate_t), h_t = (1 - l) h_{t-1} + l x_t  (the leak blend of
+ *                   ck_forward with a leak of its own for every step)
+ *   CK_GATED_DECAY  h_t = gate_t h_{t-1} + x_t
+ *   x, gate   (device) `dtype` [T][B][N]: steps x_step (gate_step) and sequences x_row
+ *             (gate_row) elements apart, nodes dense; strides may be 0
+ *   state0    (device) float[B][N] or NULL (zeros)
+ *   lengths   (device) int64[B] or NULL (T for all), clamped to [0, T]: from step
+ *             lengths[b] on the state stays, x and gate are not looked at, out is 0
+ *   out       (device) `dtype` [T][B][N], h_t rounded once
+ *   state     (device) float[B][N], h after the last step
+ *   kept      (device) kept_bytes of ck_gated_sizes, for the backward; NULL: not wanted
+ * The backward takes x, gate, lengths and kept again and, for a loss of which
+ * d_out (device, `dtype` [T][B][N], strides d_out_step and d_out_row; NULL: zeros) and
+ * d_state (float[B][N] or NULL) are the gradients, gives
+ *   dx, dgate (device) `dtype` [T][B][N], d_state0 float[B][N]; a NULL one is not computed
+ * Gradients are 0 from step lengths[b] on.  Long sequences of few nodes are cut along the
+ * steps: products of gates over runs of steps are formed, so in the decay form such a
+ * product must not overflow 32 bits.
+ *   workspace (device) workspace_bytes of ck_gated_sizes on this device, 8-byte aligned;
+ *             its contents need no setting and mean nothing afterwards; NULL when 0 bytes
+ * Results depend on the operands, sizes and the device alone.  Asynchronous.  Errors:
+ * CK_ERR_INVALID_ARG (type, form, negative size, NULL pointer, alignment),
+ * CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED (more than 2^40 elements or 2^30 steps), CK_ERR_CUDA.
+ */
+typedef enum { CK_GATED_LEAK = 0, CK_GATED_DECAY = 1 } ck_gated_form;
+typedef struct {
+    const void *x, *gate;
+    int64_t dtype, form, T, B, N;
+    int64_t x_step, x_row, gate_step, gate_row;
+    const float *state0;
+    const int64_t *lengths;
+    void *out;
+    float *state, *kept;
+    const void *d_out;
+    int64_t d_out_step, d_out_row;
+    const float *d_state;
+    void *dx, *dgate;
+    float *d_state0;
+    void *workspace;
+    int64_t workspace_bytes;
+} ck_gated_call;
+ck_status ck_gated_sizes(int64_t T, int64_t B, int64_t N, size_t *kept_bytes, size_t *workspace_bytes);
+ck_status ck_gated_forward(const ck_gated_call *call, void *stream);
+ck_status ck_gated_backward(const ck_gated_call *call, void *stream);
+
+/*
  * ck_forward_static_scratch -- ck_forward without a scratch buffer: the
  * temporary workspace comes from a 32 MiB array of device memory compiled into
  * the library.  The pages have no counterpart for this call; it exists for

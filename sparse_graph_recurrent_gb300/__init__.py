@@ -16,11 +16,13 @@ import torch
 
 from . import _ck
 from ._ck import CKError  # noqa: F401
+from .gated import gated_recurrence, gated_recurrence_backward, gated_recurrence_forward
 from .readout import (control_logits, dropout, dropout_backward, int4_matvec, int4_quantize,
                       int4_rows, pick_tokens)
 
 __all__ = ["SparseGraph", "sparse_recurrence", "CKError", "forward", "backward", "dropout",
-           "dropout_backward", "int4_quantize", "int4_rows", "int4_matvec", "control_logits", "pick_tokens"]
+           "dropout_backward", "int4_quantize", "int4_rows", "int4_matvec", "control_logits", "pick_tokens",
+           "gated_recurrence", "gated_recurrence_forward", "gated_recurrence_backward"]
 
 
 class SparseGraph:

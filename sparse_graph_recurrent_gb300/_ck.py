@@ -30,6 +30,7 @@ PROBE_BARRIER_WORDS = 16384
 PHASE_PROFILE_CTAS, PHASE_PROFILE_WORDS = 1024, 8  # ck_phase_profile_read
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # ck_dtype
 INT4_GROUPS = (32, 64, 128)
+GATED_FORMS = {"leak": 0, "decay": 1}  # ck_gated_form
 
 _lib = None
 
@@ -47,6 +48,16 @@ class LogitCall(ctypes.Structure):
                 ("out", _p), ("out_stride", _i), ("tokens", _p), ("sample", _i),
                 ("seed", _u), ("step", _u), ("step_dev", _p), ("workspace", _p),
                 ("workspace_bytes", _i)]
+
+
+class GatedCall(ctypes.Structure):
+    """ck_gated_call: the arguments of ck_gated_forward and ck_gated_backward."""
+    _p, _i = ctypes.c_void_p, ctypes.c_int64
+    _fields_ = [("x", _p), ("gate", _p), ("dtype", _i), ("form", _i), ("T", _i), ("B", _i), ("N", _i),
+                ("x_step", _i), ("x_row", _i), ("gate_step", _i), ("gate_row", _i), ("state0", _p),
+                ("lengths", _p), ("out", _p), ("state", _p), ("kept", _p), ("d_out", _p),
+                ("d_out_step", _i), ("d_out_row", _i), ("d_state", _p), ("dx", _p), ("dgate", _p),
+                ("d_state0", _p), ("workspace", _p), ("workspace_bytes", _i)]
 
 
 class CKError(RuntimeError):
@@ -108,6 +119,9 @@ def load() -> ctypes.CDLL:
         "ck_int4_quantize": [p, i64, i64, i64, i64, i64, i64, p, i64, p, i64, i64, p, i64, p],
         "ck_control_logits": [ctypes.POINTER(LogitCall), p],
         "ck_logits_workspace_size": [i64, i64, i64, psz],
+        "ck_gated_sizes": [i64, i64, i64, psz, psz],
+        "ck_gated_forward": [ctypes.POINTER(GatedCall), p],
+        "ck_gated_backward": [ctypes.POINTER(GatedCall), p],
         "ck_forward_static_scratch": [p, p, p, p, p, p, i64, i64, i64, p, p, sz, p],
         "ck_probe_read": [p, sz, i64, p, p],
         "ck_probe_gather": [p, i64, i64, p, i64, p, p],
@@ -499,6 +513,21 @@ def ck_control_logits(call: LogitCall, stream=None):
         _get_raw_stream(_get_device()) if stream is None else stream.cuda_stream)
     if status:
         _check(status)
+
+
+def ck_gated_sizes(T: int, B: int, N: int):
+    """(bytes of kept, bytes of workspace)."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().ck_gated_sizes(T, B, N, ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
+
+
+def ck_gated_forward(call: GatedCall, stream=None):
+    _check((_lib or load()).ck_gated_forward(ctypes.byref(call), _raw_stream(stream)))
+
+
+def ck_gated_backward(call: GatedCall, stream=None):
+    _check((_lib or load()).ck_gated_backward(ctypes.byref(call), _raw_stream(stream)))
 
 
 def ck_forward_static_scratch(handle, edge_values, leak, bias, drives, state0, microsteps,
