@@ -496,6 +496,80 @@ ck_status ck_gated_forward(const ck_gated_call *call, void *stream);
 ck_status ck_gated_backward(const ck_gated_call *call, void *stream);
 
 /*
+ * ck_grad_norm, ck_clip_gradients -- over `count` tensors of a (host) list, read during the
+ * call: norm[0] (device, float) = the root of the sum of all elements' squares, and with
+ * clipping out = grad * min(1, max_norm / (norm + 1e-6)), rounded once.  out may be grad
+ * itself; no tensor's out may overlap another's grad or out, or its own grad in part.  The
+ * norm is right where squares leave 32 bits (down to elements of 2^-126).  A norm that is
+ * infinite makes the factor 0, one that is NaN makes it NaN.
+ *   workspace (device, 8-byte aligned) at least what ck_clip_workspace_size says for the
+ *             same list on this device; needs no setting, means nothing afterwards
+ * Sums are added up in an order that depends on the list and the device alone.
+ * Asynchronous.  Errors: CK_ERR_INVALID_ARG, CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED (more
+ * than 2^40 elements in a tensor), CK_ERR_OUT_OF_MEMORY (host), CK_ERR_CUDA.
+ */
+typedef struct {
+    const void *grad;
+    void *out; /* not looked at by ck_grad_norm */
+    int64_t n, dtype;
+} ck_gradient;
+ck_status ck_clip_workspace_size(const ck_gradient *list, int64_t count, size_t *bytes);
+ck_status ck_grad_norm(const ck_gradient *list, int64_t count, float *norm, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+ck_status ck_clip_gradients(const ck_gradient *list, int64_t count, double max_norm, float *norm,
+                            void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * ck_beam_select -- a step of beam search over logits[B][K][V] (`dtype`, rows of V dense,
+ * logits_row and logits_beam elements apart).  A candidate is a beam k and a token v, its
+ * score scores[b][k] + logits[b][k][v] - log(sum over w of exp(logits[b][k][w])), compared
+ * in 64 bits.  The `beams` best of the K V candidates of a sequence are kept, best first, of
+ * equal ones the lowest k, then the lowest v:
+ *   scores_out (device) float[B][beams], parents int64[B][beams] (k), tokens
+ *   int64[B][beams] (v), ended_out uint8[B][beams] (v == end_token)
+ * A beam with ended[b][k] (device, uint8, 0 or 1; NULL: none) has one candidate alone:
+ * end_token at scores[b][k].  A logit of -inf or NaN is no candidate; neither is any of a
+ * beam whose score is not finite or whose logits hold +inf.  Where candidates run out:
+ * score -inf, parent k of its place (0 past the last beam), token -1, not ended.
+ * end_token -1: none.  scores float[B][K].
+ *   workspace (device, 8-byte aligned) at least what ck_beam_workspace_size says
+ * Asynchronous.  Errors: CK_ERR_INVALID_ARG, CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED (K or
+ * beams above 64, V >= 2^24, B > 65535), CK_ERR_CUDA.
+ */
+typedef struct {
+    const void *logits;
+    int64_t dtype, B, K, V, logits_row, logits_beam;
+    const float *scores;
+    const uint8_t *ended;
+    int64_t end_token, beams;
+    float *scores_out;
+    int64_t *parents, *tokens;
+    uint8_t *ended_out;
+    void *workspace;
+    int64_t workspace_bytes;
+} ck_beam_call;
+ck_status ck_beam_workspace_size(int64_t dtype, int64_t B, int64_t K, int64_t V, int64_t beams, size_t *bytes);
+ck_status ck_beam_select(const ck_beam_call *call, void *stream);
+
+/*
+ * ck_reorder_states -- out[b][j] = in[b][parents[b][j]] for the rows, of `bytes` bytes each,
+ * of `count` (host list, read during the call) arrays in[B][K] and out[B][beams], whose
+ * sequences and beams lie in_row, in_beam (out_row, out_beam) bytes apart.  parents:
+ * (device) int64[B][beams].  A parent outside [0, K) gives a row of zeros.  Either out is
+ * in itself, with the same strides and beams == K, or the two do not overlap; no array's
+ * out may overlap another's in or out.
+ * Asynchronous.  Errors: CK_ERR_INVALID_ARG, CK_ERR_UNSUPPORTED (K or beams above 64,
+ * B > 65535), CK_ERR_CUDA.
+ */
+typedef struct {
+    const void *in;
+    void *out;
+    int64_t bytes, in_row, in_beam, out_row, out_beam;
+} ck_beam_state;
+ck_status ck_reorder_states(const ck_beam_state *list, int64_t count, const int64_t *parents, int64_t B,
+                            int64_t K, int64_t beams, void *stream);
+
+/*
  * ck_forward_static_scratch -- ck_forward without a scratch buffer: the
  * temporary workspace comes from a 32 MiB array of device memory compiled into
  * the library.  The pages have no counterpart for this call; it exists for

@@ -16,13 +16,16 @@ import torch
 
 from . import _ck
 from ._ck import CKError  # noqa: F401
+from .beams import beam_select, reorder_states
 from .gated import gated_recurrence, gated_recurrence_backward, gated_recurrence_forward
+from .gradients import clip_gradients, grad_norm
 from .readout import (control_logits, dropout, dropout_backward, int4_matvec, int4_quantize,
                       int4_rows, pick_tokens)
 
 __all__ = ["SparseGraph", "sparse_recurrence", "CKError", "forward", "backward", "dropout",
            "dropout_backward", "int4_quantize", "int4_rows", "int4_matvec", "control_logits", "pick_tokens",
-           "gated_recurrence", "gated_recurrence_forward", "gated_recurrence_backward"]
+           "gated_recurrence", "gated_recurrence_forward", "gated_recurrence_backward", "grad_norm",
+           "clip_gradients", "beam_select", "reorder_states"]
 
 
 class SparseGraph:
@@ -159,7 +162,9 @@ class TrainStep:
     captured once as a CUDA graph and replayed (TrainKernel page: a captured
     step holds the forward, the gradients and the parameter update, with no
     per-operator host launches).  Adam's moments and step count live on the
-    device, and each replay advances the count.
+    device, and each replay advances the count.  With max_norm the three
+    gradients are clipped to that global norm before the update (clip_gradients);
+    `norm`, one float on the device, is what it was before.
 
     The parameters are updated in place; drives, state0 and d_out are read from
     the tensors given here, so copy new inputs into them before a replay.
@@ -168,7 +173,7 @@ class TrainStep:
 
     def __init__(self, graph: SparseGraph, edge_values, leak, bias, drives, state0, d_out,
                  microsteps: int, lr: float, optimizer: str = "sgd", betas=(0.9, 0.999),
-                 eps: float = 1e-8):
+                 eps: float = 1e-8, max_norm: float | None = None):
         if optimizer not in ("sgd", "adam"):
             raise ValueError("optimizer is 'sgd' or 'adam'")
         self.graph, self.M = graph, microsteps
@@ -187,6 +192,12 @@ class TrainStep:
         self.grads = (torch.empty(E, device=dev), torch.empty(N, device=dev),
                       torch.empty(N, device=dev), torch.empty((T, n_in, B), device=dev),
                       torch.empty((B, N), device=dev))
+        self.max_norm = max_norm
+        if max_norm is not None:
+            self.clip_list = _ck.gradient_list(self.grads[:3])
+            self.clip_space = torch.empty(_ck.ck_clip_workspace_size(self.clip_list) // 8, dtype=torch.int64,
+                                          device=dev)
+            self.norm = torch.zeros(1, device=dev)
         params = (edge_values, leak, bias)
         self.moments = [(torch.zeros_like(p), torch.zeros_like(p)) for p in params]
         self.step_count = torch.zeros(1, dtype=torch.int64, device=dev)
@@ -214,6 +225,8 @@ class TrainStep:
                        self.out, self.saved, self.scratch)
         _ck.ck_backward(g.handle, self.w, self.leak, self.B, self.T, M, self.saved, self.d_out,
                         dw, dl, db, dd, dh, self.scratch)
+        if self.max_norm is not None:
+            _ck.ck_clip_gradients(self.clip_list, self.max_norm, self.norm, self.clip_space)
         if self.optimizer == "sgd":
             _ck.ck_sgd_update(self.w, dw, lr)
             _ck.ck_sgd_update(self.leak, dl, lr)

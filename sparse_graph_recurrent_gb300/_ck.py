@@ -60,6 +60,27 @@ class GatedCall(ctypes.Structure):
                 ("d_state0", _p), ("workspace", _p), ("workspace_bytes", _i)]
 
 
+class Gradient(ctypes.Structure):
+    """ck_gradient: a tensor of ck_grad_norm and ck_clip_gradients."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int64)]
+
+
+class BeamCall(ctypes.Structure):
+    """ck_beam_call: the arguments of ck_beam_select."""
+    _p, _i = ctypes.c_void_p, ctypes.c_int64
+    _fields_ = [("logits", _p), ("dtype", _i), ("B", _i), ("K", _i), ("V", _i), ("logits_row", _i),
+                ("logits_beam", _i), ("scores", _p), ("ended", _p), ("end_token", _i), ("beams", _i),
+                ("scores_out", _p), ("parents", _p), ("tokens", _p), ("ended_out", _p), ("workspace", _p),
+                ("workspace_bytes", _i)]
+
+
+class BeamState(ctypes.Structure):
+    """ck_beam_state: an array of ck_reorder_states."""
+    _p, _i = ctypes.c_void_p, ctypes.c_int64
+    _fields_ = [("in_", _p), ("out", _p), ("bytes", _i), ("in_row", _i), ("in_beam", _i), ("out_row", _i),
+                ("out_beam", _i)]
+
+
 class CKError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -122,6 +143,12 @@ def load() -> ctypes.CDLL:
         "ck_gated_sizes": [i64, i64, i64, psz, psz],
         "ck_gated_forward": [ctypes.POINTER(GatedCall), p],
         "ck_gated_backward": [ctypes.POINTER(GatedCall), p],
+        "ck_clip_workspace_size": [ctypes.POINTER(Gradient), i64, psz],
+        "ck_grad_norm": [ctypes.POINTER(Gradient), i64, p, p, i64, p],
+        "ck_clip_gradients": [ctypes.POINTER(Gradient), i64, ctypes.c_double, p, p, i64, p],
+        "ck_beam_workspace_size": [i64, i64, i64, i64, i64, psz],
+        "ck_beam_select": [ctypes.POINTER(BeamCall), p],
+        "ck_reorder_states": [ctypes.POINTER(BeamState), i64, p, i64, i64, i64, p],
         "ck_forward_static_scratch": [p, p, p, p, p, p, i64, i64, i64, p, p, sz, p],
         "ck_probe_read": [p, sz, i64, p, p],
         "ck_probe_gather": [p, i64, i64, p, i64, p, p],
@@ -528,6 +555,49 @@ def ck_gated_forward(call: GatedCall, stream=None):
 
 def ck_gated_backward(call: GatedCall, stream=None):
     _check((_lib or load()).ck_gated_backward(ctypes.byref(call), _raw_stream(stream)))
+
+
+def gradient_list(grads, outs=None):
+    """A ck_gradient array of dense tensors and of where they are clipped to (themselves)."""
+    array = (Gradient * len(grads))()
+    for g, o, entry in zip(grads, outs or grads, array):
+        if g.dtype not in DTYPES or not g.is_cuda or o.dtype != g.dtype or o.numel() != g.numel():
+            raise ValueError("gradients are CUDA tensors of float32, bfloat16 or float16, out like them")
+        entry.grad, entry.out, entry.n, entry.dtype = g.data_ptr(), o.data_ptr(), g.numel(), DTYPES[g.dtype]
+    return array
+
+
+def ck_clip_workspace_size(array) -> int:
+    n = ctypes.c_size_t()
+    _check(load().ck_clip_workspace_size(array, len(array), ctypes.byref(n)))
+    return n.value
+
+
+def ck_grad_norm(array, norm, workspace, stream=None):
+    _need(norm, torch.float32, "norm")
+    _check((_lib or load()).ck_grad_norm(array, len(array), _ptr(norm), _ptr(workspace), workspace.numel() * 8,
+                                         _raw_stream(stream)))
+
+
+def ck_clip_gradients(array, max_norm: float, norm, workspace, stream=None):
+    _need(norm, torch.float32, "norm")
+    _check((_lib or load()).ck_clip_gradients(array, len(array), float(max_norm), _ptr(norm), _ptr(workspace),
+                                              workspace.numel() * 8, _raw_stream(stream)))
+
+
+def ck_beam_workspace_size(dtype, B: int, K: int, V: int, beams: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().ck_beam_workspace_size(DTYPES[dtype], B, K, V, beams, ctypes.byref(n)))
+    return n.value
+
+
+def ck_beam_select(call: BeamCall, stream=None):
+    _check((_lib or load()).ck_beam_select(ctypes.byref(call), _raw_stream(stream)))
+
+
+def ck_reorder_states(array, parents, B: int, K: int, beams: int, stream=None):
+    _need(parents, torch.int64, "parents")
+    _check((_lib or load()).ck_reorder_states(array, len(array), _ptr(parents), B, K, beams, _raw_stream(stream)))
 
 
 def ck_forward_static_scratch(handle, edge_values, leak, bias, drives, state0, microsteps,

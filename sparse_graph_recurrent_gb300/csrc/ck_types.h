@@ -21,6 +21,37 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(f
 }
 template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 
+// Elements of 16 bytes.
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
+
+// Elements e .. e + E - 1 of a dense line at p + e (element e itself there), of which
+// `room` are there, whatever p's alignment: from the two aligned 16-byte pieces that
+// hold them, where both lie inside the line, else one by one.
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const T *line, int64_t e, int64_t length) {
+    constexpr int E = kVec<T>;
+    const T *p = line + e;
+    const uint32_t off = (uint32_t)(uintptr_t)p & 15u;
+    if (off == 0) return __ldcs((const uint4 *)p);
+    const uint4 *lo = (const uint4 *)((uintptr_t)p - off);
+    if ((const char *)lo >= (const char *)line && (const char *)(lo + 2) <= (const char *)(line + length)) {
+        const uint4 u = __ldg(lo), v = __ldg(lo + 1);
+        uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        if (off & 8) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = w[7];
+        if (off & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t bits = (off & 2) * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    alignas(16) T t[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) t[i] = p[i];
+    return *(const uint4 *)t;
+}
+
 inline bool known_dtype(int64_t d) { return d == CK_F32 || d == CK_BF16 || d == CK_F16; }
 inline size_t dtype_size(int64_t d) { return d == CK_F32 ? 4 : 2; }
 // Whether p lies at a multiple of `bytes`, as a kernel's loads of that size need.

@@ -66,8 +66,6 @@ __global__ void __launch_bounds__(256) k_dropout(const __grid_constant__ DropArg
 // start, one way to memory and back, and an end), 8 x 8 x 256 fp32 1.5 us.
 constexpr int kDropThreads = 256;
 
-template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
-
 // n / d for n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
 // invariant integers using multiplication", PLDI 1994).
 struct Divider {
@@ -90,34 +88,6 @@ struct DropFlat {
     int small;             // n < 2^31
     int rows_joined;       // rows n3 apart: x is one dense line
 };
-
-// Elements e .. e + E - 1 of a dense line at p + e (element e itself there), of which
-// `room` are there, whatever p's alignment: from the two aligned 16-byte pieces that
-// hold them, where both lie inside the line, else one by one.
-template <typename T>
-__device__ __forceinline__ uint4 load_vec(const T *line, int64_t e, int64_t length) {
-    constexpr int E = kVec<T>;
-    const T *p = line + e;
-    const uint32_t off = (uint32_t)(uintptr_t)p & 15u;
-    if (off == 0) return __ldcs((const uint4 *)p);
-    const uint4 *lo = (const uint4 *)((uintptr_t)p - off);
-    if ((const char *)lo >= (const char *)line && (const char *)(lo + 2) <= (const char *)(line + length)) {
-        const uint4 u = __ldg(lo), v = __ldg(lo + 1);
-        uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-        if (off & 8) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = w[7];
-        if (off & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
-        if constexpr (sizeof(T) == 2) {
-            const uint32_t bits = (off & 2) * 8;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    alignas(16) T t[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) t[i] = p[i];
-    return *(const uint4 *)t;
-}
 
 // Where in the generator's blocks of four a piece of E elements begins.
 enum Start {

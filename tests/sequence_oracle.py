@@ -91,3 +91,48 @@ def within(got, want, off, dtype="float32"):
     if bad.any():
         i = np.unravel_index(np.argmax(np.where(bad, np.abs(got - want) / tol, 0)), bad.shape)
         raise AssertionError(f"{bad.sum()} of {bad.size} off; at {i}: {got[i]} for {want[i]}, tolerance {tol[i]}")
+
+
+def clip(grads, max_norm):
+    """(norm, factor) of a list of arrays in 64 bits."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        norm = np.sqrt(sum((np.asarray(g, np.float64) ** 2).sum() for g in grads))
+        f = max_norm / (norm + 1e-6)
+    return norm, (1.0 if f >= 1 else f)
+
+
+def beam(logits, scores, ended, end_token, beams):
+    """(scores, parents, tokens, ended) of a step of beam search."""
+    B, K, V = logits.shape
+    out = np.full((B, beams), -np.inf), np.zeros((B, beams), np.int64), np.full((B, beams), -1), np.zeros((B, beams), bool)
+    for b in range(B):
+        options = []
+        for k in range(K):
+            z, s = logits[b, k].astype(np.float64), float(scores[b, k])
+            if not np.isfinite(s):
+                continue
+            if ended is not None and ended[b, k]:
+                options.append((-s, k, end_token))
+                continue
+            z = np.where(np.isnan(z), -np.inf, z)
+            top = z.max()
+            if not np.isfinite(top):
+                continue
+            lse = top + np.log(np.exp(z - top).sum())
+            best = np.argsort(-z, kind="stable")[:beams]
+            options += [(-(s - lse + z[v]), k, int(v)) for v in best if z[v] > -np.inf]
+        options.sort()
+        for j in range(beams):
+            if j < len(options):
+                out[0][b, j], out[1][b, j], out[2][b, j] = -options[j][0], options[j][1], options[j][2]
+                out[3][b, j] = options[j][2] == end_token
+            else:
+                out[1][b, j] = j if j < K else 0
+    return out
+
+
+def beam_score_off(V):
+    """What a score may be off by, before its rounding: a sum of 32-bit exponentials.  Each
+    is off by 2 + 1.2 |x| units (the intrinsic's documented bound), |x| on average no more
+    than log V + 1 over the sum; a thread adds 32 of them, the rest is in 64 bits."""
+    return (36 + 1.2 * (np.log(V) + 1)) * 2.0 ** -23

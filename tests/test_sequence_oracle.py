@@ -36,3 +36,15 @@ def test_a_constant_decay_is_a_geometric_sum():
     T = 9
     got, _ = so.gated(np.ones((T, 1, 1)), np.full((T, 1, 1), 0.5), None, None, "decay")
     assert np.allclose(got["out"][:, 0, 0], 2 - 0.5 ** np.arange(T))
+
+
+def test_beams_of_a_small_case_by_hand():
+    z = np.log(np.array([[[0.5, 0.25, 0.25], [0.1, 0.2, 0.7]]]))
+    s, p, t, e = so.beam(z, np.log(np.array([[0.5, 0.5]])), None, 2, 3)
+    assert p.tolist() == [[1, 0, 0]] and t.tolist() == [[2, 0, 1]] and e.tolist() == [[True, False, False]]
+    assert np.allclose(np.exp(s), [[0.35, 0.25, 0.125]])
+
+
+def test_clipping_by_hand():
+    norm, factor = so.clip([np.array([3.0]), np.array([4.0])], 2.5)
+    assert norm == 5 and abs(factor - 0.5) < 1e-6 and so.clip([np.array([3.0])], 4)[1] == 1
