@@ -183,11 +183,11 @@ class _PythonForms:
     def dropout(*args):
         return None
 
-    int4_matvec = control = dropout
+    int4_matvec = control = gated = gated_backward = clip = beam = reorder = dropout
 
 
 def _load_native(lib):
-    """The module ck_binding (the readout operators' short way from Python), built first if
+    """The module ck_binding (the token model's operators' short way from Python), built first if
     it is missing or stale, with this library's entries.  All else works without it."""
     import importlib.machinery
     import importlib.util
@@ -196,12 +196,14 @@ def _load_native(lib):
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("ck_binding", loader))
         loader.exec_module(module)
     except (ImportError, OSError, RuntimeError) as e:  # no compiler, no headers, another interpreter's
-        warnings.warn("the readout operators' kernels are called through ctypes, some microseconds "
+        warnings.warn("the token model's operators are called through ctypes, some microseconds "
                       f"slower, as ck_binding cannot be had: {e}", RuntimeWarning, stacklevel=3)
         return _PythonForms
     entry = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value  # noqa: E731
-    module.bind(entry("ck_dropout"), entry("ck_int4_matvec"), entry("ck_int4_workspace_size"),
-                entry("ck_control_logits"), entry("ck_logits_workspace_size"), _check)
+    module.bind(tuple(entry("ck_" + name) for name in (
+        "dropout", "int4_matvec", "int4_workspace_size", "control_logits", "logits_workspace_size", "gated_sizes",
+        "gated_forward", "gated_backward", "clip_workspace_size", "grad_norm", "clip_gradients",
+        "beam_workspace_size", "beam_select", "reorder_states")), _check)
     return module
 
 

@@ -30,6 +30,9 @@ def beam_select(logits, scores, ended=None, end_token=None, beams=None):
     beam whose score is not finite (the beams of a first step but one) or whose logits hold
     +inf.  Where candidates run out: score -inf, token -1, parent the beam of that place
     (0 past the last)."""
+    got = (_ck._native or _ck.native()).beam(logits, scores, ended, end_token, beams)
+    if got is not None:
+        return got
     if not logits.is_cuda or logits.dtype not in _ck.DTYPES or logits.dim() != 3:
         raise ValueError("logits must be a CUDA tensor [B, K, V] of float32, bfloat16 or float16")
     _refuse_derivatives("beam_select", logits=logits, scores=scores)
@@ -84,6 +87,9 @@ def reorder_states(states, parents, out=None):
     parents is int64 [B, beams] as beam_select returns it; one outside [0, K) gives zeros.
     `out`, a tensor or as many as there are states, is written instead; a state may be its
     own `out`, where beams == K."""
+    got = (_ck._native or _ck.native()).reorder(states, parents, out)
+    if got is not None:
+        return got
     single = isinstance(states, torch.Tensor)
     some = [states] if single else list(states)
     if parents.dtype != torch.int64 or parents.dim() != 2 or not parents.is_cuda:

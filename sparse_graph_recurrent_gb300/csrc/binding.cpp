@@ -1,4 +1,4 @@
-// The short way from Python to the readout operators, for the calls of an answering
+// The short way from Python to the operators of a token model, for the calls of an answering
 // loop, whose kernels take less time than marshalling a dozen arguments through
 // ctypes does.  Each function here checks its arguments, allocates what the call
 // returns and calls the library's C entry.  What it does not take (a wrong type or
@@ -12,6 +12,8 @@
 
 #include <cfloat>
 #include <cmath>
+#include <initializer_list>
+#include <vector>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
@@ -29,6 +31,15 @@ decltype(&ck_int4_matvec) matvec_entry;
 decltype(&ck_int4_workspace_size) matvec_size_entry;
 decltype(&ck_control_logits) logits_entry;
 decltype(&ck_logits_workspace_size) logits_size_entry;
+decltype(&ck_gated_sizes) gated_size_entry;
+decltype(&ck_gated_forward) gated_forward_entry;
+decltype(&ck_gated_backward) gated_backward_entry;
+decltype(&ck_clip_workspace_size) clip_size_entry;
+decltype(&ck_grad_norm) norm_entry;
+decltype(&ck_clip_gradients) clip_entry;
+decltype(&ck_beam_workspace_size) beam_size_entry;
+decltype(&ck_beam_select) beam_entry;
+decltype(&ck_reorder_states) reorder_entry;
 PyObject *fail_callable;  // raises CKError for a status
 
 PyObject *leave_it() { Py_RETURN_NONE; }
@@ -325,17 +336,341 @@ PyObject *control(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
 }
 
-// bind(dropout, int4_matvec, int4_workspace_size, control_logits, logits_workspace_size,
-// fail): addresses of the library's entries, and what raises an error for a status
+// A tuple of tensors, None for those that are not defined.
+PyObject *tuple_of(std::initializer_list<at::Tensor> list) {
+    PyObject *r = PyTuple_New((Py_ssize_t)list.size());
+    if (!r) return nullptr;
+    Py_ssize_t i = 0;
+    for (const at::Tensor &t : list) {
+        PyObject *o = t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);
+        if (!o) {
+            Py_DECREF(r);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(r, i++, o);
+    }
+    return r;
+}
+
+at::Tensor empty_like_type(at::IntArrayRef sizes, const at::Tensor &like, at::ScalarType type) {
+    return at::empty(sizes, like.options().dtype(type).requires_grad(false));
+}
+
+// The operands that both directions of a gated recurrence take.
+bool gated_operands(ck_gated_call &c, const Operand &x, const Operand &gate, const Operand &lengths, PyObject *form) {
+    if (x.none || !x.good || gate.none || !gate.good || !lengths.good || x.t->dim() != 3 || !PyUnicode_Check(form)) return false;
+    c.dtype = dtype_of(*x.t);
+    if (c.dtype < 0 || gate.t->scalar_type() != x.t->scalar_type() || gate.t->sizes() != x.t->sizes()) return false;
+    if (PyUnicode_CompareWithASCIIString(form, "leak") == 0)
+        c.form = CK_GATED_LEAK;
+    else if (PyUnicode_CompareWithASCIIString(form, "decay") == 0)
+        c.form = CK_GATED_DECAY;
+    else
+        return false;
+    c.T = x.t->size(0), c.B = x.t->size(1), c.N = x.t->size(2);
+    if (c.N > 1 && (x.t->stride(2) != 1 || gate.t->stride(2) != 1)) return false;
+    c.x = x.t->const_data_ptr(), c.gate = gate.t->const_data_ptr();
+    c.x_step = x.t->stride(0), c.x_row = x.t->stride(1);
+    c.gate_step = gate.t->stride(0), c.gate_row = gate.t->stride(1);
+    if (!lengths.none) {
+        if (!lengths.is(at::kLong) || !lengths.sizes(c.B) || !lengths.t->is_contiguous()) return false;
+        c.lengths = lengths.t->const_data_ptr<int64_t>();
+    }
+    return true;
+}
+
+bool state_operand(const float *&at, const Operand &s, int64_t B, int64_t N) {
+    at = nullptr;
+    if (s.none) return true;
+    if (!s.good || !s.is(at::kFloat) || !s.sizes(B, N) || !s.t->is_contiguous()) return false;
+    at = s.t->const_data_ptr<float>();
+    return true;
+}
+
+// gated(x, gate, state0, lengths, form, keep): (out, state, kept or None)
+PyObject *gated(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    try {
+        if (n != 6 || !cuda_tensor(a[0])) return leave_it();
+        const int dev = c10::cuda::current_device();
+        const Operand x(a[0], dev), gate(a[1], dev), state0(a[2], dev), lengths(a[3], dev);
+        ck_gated_call c{};
+        if (!gated_operands(c, x, gate, lengths, a[4]) || !state_operand(c.state0, state0, c.B, c.N)) return leave_it();
+        size_t kept_bytes = 0, need = 0;
+        ck_status st = gated_size_entry(c.T, c.B, c.N, &kept_bytes, &need);
+        if (st != CK_OK) return raise_status(st);
+        at::Tensor out = empty_like_type({c.T, c.B, c.N}, *x.t, x.t->scalar_type());
+        at::Tensor state = empty_like_type({c.B, c.N}, *x.t, at::kFloat), kept, ws;
+        c.out = out.data_ptr();
+        c.state = state.data_ptr<float>();
+        if (a[5] == Py_True) {
+            kept = empty_like_type({(int64_t)(kept_bytes / 4)}, *x.t, at::kFloat);
+            c.kept = kept.data_ptr<float>();
+        }
+        if (need) {
+            ws = empty_like_type({(int64_t)(need / 8)}, *x.t, at::kLong);
+            c.workspace = ws.data_ptr();
+            c.workspace_bytes = (int64_t)need;
+        }
+        st = gated_forward_entry(&c, stream_of(dev));
+        if (st != CK_OK) return raise_status(st);
+        return tuple_of({out, state, kept});
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// gated_backward(x, gate, kept, d_out, d_state, lengths, form, want_x, want_gate, want_state0)
+PyObject *gated_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    try {
+        if (n != 10 || !cuda_tensor(a[0])) return leave_it();
+        const int dev = c10::cuda::current_device();
+        const Operand x(a[0], dev), gate(a[1], dev), kept(a[2], dev), d(a[3], dev), ds(a[4], dev), lengths(a[5], dev);
+        ck_gated_call c{};
+        if (!gated_operands(c, x, gate, lengths, a[6]) || !state_operand(c.d_state, ds, c.B, c.N)) return leave_it();
+        size_t kept_bytes = 0, need = 0;
+        ck_status st = gated_size_entry(c.T, c.B, c.N, &kept_bytes, &need);
+        if (st != CK_OK) return raise_status(st);
+        if (kept.none || !kept.good || !kept.is(at::kFloat) || kept.t->numel() * 4 != (int64_t)kept_bytes || !kept.t->is_contiguous())
+            return leave_it();
+        c.kept = const_cast<float *>(kept.t->const_data_ptr<float>());  // the backward reads it
+        if (!d.none) {
+            if (!d.good || d.t->scalar_type() != x.t->scalar_type() || d.t->sizes() != x.t->sizes() || (c.N > 1 && d.t->stride(2) != 1))
+                return leave_it();
+            c.d_out = d.t->const_data_ptr();
+            c.d_out_step = d.t->stride(0), c.d_out_row = d.t->stride(1);
+        }
+        at::Tensor dx, dgate, dstate0, ws;
+        if (a[7] == Py_True) {
+            dx = empty_like_type({c.T, c.B, c.N}, *x.t, x.t->scalar_type());
+            c.dx = dx.data_ptr();
+        }
+        if (a[8] == Py_True) {
+            dgate = empty_like_type({c.T, c.B, c.N}, *x.t, x.t->scalar_type());
+            c.dgate = dgate.data_ptr();
+        }
+        if (a[9] == Py_True) {
+            dstate0 = empty_like_type({c.B, c.N}, *x.t, at::kFloat);
+            c.d_state0 = dstate0.data_ptr<float>();
+        }
+        if (need) {
+            ws = empty_like_type({(int64_t)(need / 8)}, *x.t, at::kLong);
+            c.workspace = ws.data_ptr();
+            c.workspace_bytes = (int64_t)need;
+        }
+        st = gated_backward_entry(&c, stream_of(dev));
+        if (st != CK_OK) return raise_status(st);
+        return tuple_of({dx, dgate, dstate0});
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+bool list_of(PyObject *o) { return PyList_CheckExact(o) || PyTuple_CheckExact(o); }
+
+// clip(grads, max_norm, out): the norm of a list of tensors; max_norm None: no clipping;
+// out None: in place
+PyObject *clip(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    try {
+        if (n != 3 || !list_of(a[0]) || (a[2] != Py_None && !list_of(a[2]))) return leave_it();
+        const bool clips = a[1] != Py_None, apart = a[2] != Py_None;
+        if (clips && !PyFloat_Check(a[1])) return leave_it();
+        const Py_ssize_t count = PySequence_Fast_GET_SIZE(a[0]);
+        if (count < 1 || (apart && PySequence_Fast_GET_SIZE(a[2]) != count)) return leave_it();
+        PyObject **in = PySequence_Fast_ITEMS(a[0]), **to = apart ? PySequence_Fast_ITEMS(a[2]) : in;
+        if (!cuda_tensor(in[0])) return leave_it();
+        const int dev = c10::cuda::current_device();
+        std::vector<ck_gradient> list((size_t)count);
+        std::vector<const at::Tensor *> outs((size_t)count);
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            const Operand g(in[i], dev);
+            if (g.none || !g.good || !g.t->is_contiguous()) return leave_it();
+            list[i].grad = g.t->const_data_ptr();
+            list[i].n = g.t->numel();
+            list[i].dtype = dtype_of(*g.t);
+            if (list[i].dtype < 0) return leave_it();
+            outs[i] = g.t;
+            if (apart) {
+                const Operand o(to[i], dev);
+                if (o.none || !o.good || !o.t->is_contiguous() || o.t->scalar_type() != g.t->scalar_type() || o.t->sizes() != g.t->sizes())
+                    return leave_it();
+                outs[i] = o.t;
+            }
+            if (clips) list[i].out = outs[i]->data_ptr();
+        }
+        size_t need = 0;
+        ck_status st = clip_size_entry(list.data(), count, &need);
+        if (st != CK_OK) return raise_status(st);
+        at::Tensor norm = empty_like_type({}, *outs[0], at::kFloat), ws;
+        if (need) ws = empty_like_type({(int64_t)(need / 8)}, norm, at::kLong);
+        void *at = need ? ws.data_ptr() : nullptr;
+        st = clips ? clip_entry(list.data(), count, PyFloat_AS_DOUBLE(a[1]), norm.data_ptr<float>(), at, (int64_t)need, stream_of(dev))
+                   : norm_entry(list.data(), count, norm.data_ptr<float>(), at, (int64_t)need, stream_of(dev));
+        if (st != CK_OK) return raise_status(st);
+        if (clips)
+            for (const at::Tensor *o : outs) written(*o);
+        return THPVariable_Wrap(std::move(norm));
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// beam(logits, scores, ended, end_token, beams): (scores, parents, tokens, ended)
+PyObject *beam(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    try {
+        if (n != 5 || !cuda_tensor(a[0])) return leave_it();
+        const int dev = c10::cuda::current_device();
+        const Operand z(a[0], dev), s(a[1], dev), e(a[2], dev);
+        if (!z.good || s.none || !s.good || !e.good || z.t->dim() != 3) return leave_it();
+        ck_beam_call c{};
+        c.dtype = dtype_of(*z.t);
+        c.B = z.t->size(0), c.K = z.t->size(1), c.V = z.t->size(2);
+        c.beams = c.K;
+        c.end_token = -1;
+        uint64_t v;
+        if (a[3] != Py_None) {
+            if (!whole_number(a[3], v) || v >= (uint64_t)c.V) {
+                PyErr_Clear();
+                return leave_it();
+            }
+            c.end_token = (int64_t)v;
+        }
+        if (a[4] != Py_None) {
+            if (!whole_number(a[4], v) || v < 1 || v > 64) {
+                PyErr_Clear();
+                return leave_it();
+            }
+            c.beams = (int64_t)v;
+        }
+        if (c.dtype < 0 || c.K < 1 || c.V < 1 || (c.V > 1 && z.t->stride(2) != 1) || !s.is(at::kFloat) || !s.sizes(c.B, c.K) ||
+            !s.t->is_contiguous())
+            return leave_it();
+        if (!e.none) {
+            if (!e.is(at::kBool) || !e.sizes(c.B, c.K) || !e.t->is_contiguous() || c.end_token < 0) return leave_it();
+            c.ended = (const uint8_t *)e.t->const_data_ptr();
+        }
+        c.logits = z.t->const_data_ptr();
+        c.logits_row = z.t->stride(0), c.logits_beam = z.t->stride(1);
+        c.scores = s.t->const_data_ptr<float>();
+        size_t need = 0;
+        ck_status st = beam_size_entry(c.dtype, c.B, c.K, c.V, c.beams, &need);
+        if (st != CK_OK) return raise_status(st);
+        at::Tensor scores = empty_like_type({c.B, c.beams}, *z.t, at::kFloat);
+        at::Tensor parents = empty_like_type({c.B, c.beams}, *z.t, at::kLong);
+        at::Tensor tokens = empty_like_type({c.B, c.beams}, *z.t, at::kLong);
+        at::Tensor over = empty_like_type({c.B, c.beams}, *z.t, at::kBool);
+        at::Tensor ws = empty_like_type({(int64_t)((need + 7) / 8)}, *z.t, at::kLong);
+        c.scores_out = scores.data_ptr<float>();
+        c.parents = parents.data_ptr<int64_t>(), c.tokens = tokens.data_ptr<int64_t>();
+        c.ended_out = (uint8_t *)over.data_ptr();
+        c.workspace = ws.data_ptr();
+        c.workspace_bytes = (int64_t)need;
+        st = beam_entry(&c, stream_of(dev));
+        if (st != CK_OK) return raise_status(st);
+        return tuple_of({scores, parents, tokens, over});
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// Whether t[b][k] is a dense row.
+bool rows_inside(const at::Tensor &t) {
+    int64_t at = 1;
+    for (int64_t i = t.dim() - 1; i > 1; --i) {
+        if (t.size(i) != 1 && t.stride(i) != at) return false;
+        at *= t.size(i);
+    }
+    return true;
+}
+
+// reorder(states, parents, out): a list of tensors; out None: new ones
+PyObject *reorder(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    try {
+        if (n != 3 || !list_of(a[0]) || (a[2] != Py_None && !list_of(a[2])) || !cuda_tensor(a[1])) return leave_it();
+        const int dev = c10::cuda::current_device();
+        const Operand p(a[1], dev);
+        const Py_ssize_t count = PySequence_Fast_GET_SIZE(a[0]);
+        const bool apart = a[2] != Py_None;
+        if (!p.good || !p.is(at::kLong) || p.t->dim() != 2 || !p.t->is_contiguous() || count < 1 ||
+            (apart && PySequence_Fast_GET_SIZE(a[2]) != count))
+            return leave_it();
+        PyObject **in = PySequence_Fast_ITEMS(a[0]), **to = apart ? PySequence_Fast_ITEMS(a[2]) : nullptr;
+        const int64_t B = p.t->size(0), beams = p.t->size(1);
+        int64_t K = 0;
+        std::vector<ck_beam_state> list((size_t)count);
+        std::vector<at::Tensor> outs((size_t)count);
+        if (B < 1) return leave_it();
+        // all are looked at before any is made or written
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            const Operand s(in[i], dev);
+            if (s.none || !s.good || s.t->dim() < 2 || s.t->size(0) != B || !rows_inside(*s.t)) return leave_it();
+            if (i == 0) K = s.t->size(1);
+            if (s.t->size(1) != K || K < 1) return leave_it();
+            if (apart) {
+                const Operand o(to[i], dev);
+                if (o.none || !o.good || o.t->scalar_type() != s.t->scalar_type() || o.t->dim() != s.t->dim() || o.t->size(0) != B ||
+                    o.t->size(1) != beams || o.t->sizes().slice(2) != s.t->sizes().slice(2) || !rows_inside(*o.t))
+                    return leave_it();
+                outs[i] = *o.t;
+            }
+        }
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            const at::Tensor &s = THPVariable_Unpack(in[i]);
+            if (!apart) {
+                c10::SmallVector<int64_t, 8> shape(s.sizes().begin(), s.sizes().end());
+                shape[1] = beams;
+                outs[i] = empty_like_type(shape, s, s.scalar_type());
+            }
+            const int64_t size = (int64_t)s.element_size();
+            ck_beam_state &e = list[i];
+            e.in = s.const_data_ptr();
+            e.out = outs[i].data_ptr();
+            e.bytes = s.numel() / (B * K) * size;
+            e.in_row = s.stride(0) * size, e.in_beam = s.stride(1) * size;
+            e.out_row = outs[i].stride(0) * size, e.out_beam = outs[i].stride(1) * size;
+        }
+        const ck_status st = reorder_entry(list.data(), count, p.t->const_data_ptr<int64_t>(), B, K, beams, stream_of(dev));
+        if (st != CK_OK) return raise_status(st);
+        PyObject *r = PyList_New(count);
+        if (!r) return nullptr;
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            if (apart) written(outs[i]);
+            PyObject *o = apart ? Py_NewRef(to[i]) : THPVariable_Wrap(outs[i]);
+            if (!o) {
+                Py_DECREF(r);
+                return nullptr;
+            }
+            PyList_SET_ITEM(r, i, o);
+        }
+        return r;
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// bind(addresses, fail): the library's entries, in the order below, and what raises an
+// error for a status
 PyObject *bind(PyObject *, PyObject *args) {
-    unsigned long long at[5];
-    PyObject *fail;
-    if (!PyArg_ParseTuple(args, "KKKKKO", &at[0], &at[1], &at[2], &at[3], &at[4], &fail)) return nullptr;
-    dropout_entry = (decltype(dropout_entry))at[0];
-    matvec_entry = (decltype(matvec_entry))at[1];
-    matvec_size_entry = (decltype(matvec_size_entry))at[2];
-    logits_entry = (decltype(logits_entry))at[3];
-    logits_size_entry = (decltype(logits_size_entry))at[4];
+    PyObject *list, *fail;
+    if (!PyArg_ParseTuple(args, "O!O", &PyTuple_Type, &list, &fail)) return nullptr;
+    void **entries[] = {(void **)&dropout_entry, (void **)&matvec_entry, (void **)&matvec_size_entry, (void **)&logits_entry,
+                        (void **)&logits_size_entry, (void **)&gated_size_entry, (void **)&gated_forward_entry,
+                        (void **)&gated_backward_entry, (void **)&clip_size_entry, (void **)&norm_entry, (void **)&clip_entry,
+                        (void **)&beam_size_entry, (void **)&beam_entry, (void **)&reorder_entry};
+    constexpr Py_ssize_t kEntries = sizeof(entries) / sizeof(entries[0]);
+    if (PyTuple_GET_SIZE(list) != kEntries) {
+        PyErr_SetString(PyExc_ValueError, "bind takes an address for each entry");
+        return nullptr;
+    }
+    for (Py_ssize_t i = 0; i < kEntries; ++i) {
+        void *at = PyLong_AsVoidPtr(PyTuple_GET_ITEM(list, i));
+        if (!at && PyErr_Occurred()) return nullptr;
+        *entries[i] = at;
+    }
     Py_INCREF(fail);
     Py_XSETREF(fail_callable, fail);
     Py_RETURN_NONE;
@@ -345,6 +680,11 @@ PyMethodDef methods[] = {
     {"dropout", (PyCFunction)(void (*)(void))dropout, METH_FASTCALL, nullptr},
     {"int4_matvec", (PyCFunction)(void (*)(void))int4_matvec, METH_FASTCALL, nullptr},
     {"control", (PyCFunction)(void (*)(void))control, METH_FASTCALL, nullptr},
+    {"gated", (PyCFunction)(void (*)(void))gated, METH_FASTCALL, nullptr},
+    {"gated_backward", (PyCFunction)(void (*)(void))gated_backward, METH_FASTCALL, nullptr},
+    {"clip", (PyCFunction)(void (*)(void))clip, METH_FASTCALL, nullptr},
+    {"beam", (PyCFunction)(void (*)(void))beam, METH_FASTCALL, nullptr},
+    {"reorder", (PyCFunction)(void (*)(void))reorder, METH_FASTCALL, nullptr},
     {"bind", bind, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

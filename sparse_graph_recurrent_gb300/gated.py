@@ -105,11 +105,17 @@ def _forward(x, gate, state0, lengths, form, keep):
 def gated_recurrence_forward(x, gate, state0=None, lengths=None, form: str = "leak"):
     """gated_recurrence without autograd: (out, state, kept), kept for
     gated_recurrence_backward (32-bit states at every 16th step)."""
+    got = (_ck._native or _ck.native()).gated(x, gate, state0, lengths, form, True)
+    if got is not None:
+        return got
     x, gate = x.detach(), gate.detach()
     return _forward(x, gate, None if state0 is None else state0.detach(), lengths, form, True)
 
 
 def _backward(x, gate, kept, d_out, d_state, lengths, form, want=(True, True, True)):
+    got = (_ck._native or _ck.native()).gated_backward(x, gate, kept, d_out, d_state, lengths, form, *want)
+    if got is not None:
+        return got
     call, held, device, (T, B, N) = _call(x, gate, lengths, form)
     kept_bytes, need = _space(device, T, B, N)
     if kept.dtype != torch.float32 or kept.numel() * 4 != kept_bytes or kept.get_device() != device or not kept.is_contiguous():
@@ -133,6 +139,9 @@ def _backward(x, gate, kept, d_out, d_state, lengths, form, want=(True, True, Tr
 def gated_recurrence_backward(x, gate, kept, d_out, d_state=None, lengths=None, form: str = "leak"):
     """(dx, dgate, dstate0) from the gradients of gated_recurrence_forward's out and state
     (either may be None: zeros), for the same x, gate, lengths and form."""
+    got = (_ck._native or _ck.native()).gated_backward(x, gate, kept, d_out, d_state, lengths, form, True, True, True)
+    if got is not None:
+        return got
     return _backward(x.detach(), gate.detach(), kept, None if d_out is None else d_out.detach(),
                      None if d_state is None else d_state.detach(), lengths, form)
 
@@ -164,6 +173,9 @@ def gated_recurrence(x, gate, state0=None, lengths=None, form: str = "leak"):
     it; state0 is float32 [B, N] (zeros by default) and so is state, whatever x's type.
     lengths, int64 [B]: from step lengths[b] on the state stays as it is, out is 0 and x
     and gate are not looked at.  Differentiable (once) in x, gate and state0."""
+    got = (_ck._native or _ck.native()).gated(x, gate, state0, lengths, form, False)
+    if got is not None:
+        return got[:2]
     if gate.shape != x.shape:
         gate = gate.expand(x.shape)
     if _followed(x) or _followed(gate) or state0 is not None and _followed(state0):

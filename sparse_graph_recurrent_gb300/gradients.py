@@ -55,6 +55,9 @@ def grad_norm(grads):
     """The root of the sum of the squares of all elements of a tensor or of several
     (float32, bfloat16 or float16, mixed as they are; None is skipped): a float32 scalar
     on the device.  No tensor at all gives 0 on the current device."""
+    norm = (_ck._native or _ck.native()).clip(grads, None, None)
+    if norm is not None:
+        return norm
     some = [t for t in _tensors(grads, "gradients") if t is not None]
     for t in some:
         _refuse_derivatives("grad_norm", gradient=t)
@@ -73,6 +76,9 @@ def clip_gradients(grads, max_norm: float, out=None):
     tensor or as many as there are gradients, of their types and shapes, receives the
     products instead.  None is skipped.  Tensors that share memory are refused where it
     is written."""
+    norm = (_ck._native or _ck.native()).clip(grads, max_norm, out) if max_norm is not None else None
+    if norm is not None:
+        return norm
     single = isinstance(grads, torch.Tensor)
     some = _tensors(grads, "gradients")
     to = some if out is None else _tensors(out, "out")
