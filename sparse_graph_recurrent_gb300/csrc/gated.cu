@@ -4,15 +4,21 @@
 //   leak form    l = sigmoid(f), h_t = (1 - l) h_{t-1} + l x_t
 //   decay form   h_t = f h_{t-1} + x_t
 //
-// A step is the map h -> a h + u, and a run of steps is one too: (A2, U2) after (A1, U1)
-// is (A2 A1, A2 U1 + U2).  So the steps are cut: a thread takes kSteps steps of V
-// neighbouring nodes into registers and composes them, the warps of a CTA that hold
-// consecutive stretches of the same nodes exchange their maps through shared memory, and
-// each then runs its own steps once more from the state that it now knows.  x and the gate
-// are read once.  Where there are too few nodes to fill the device the steps are cut into
-// chunks for several CTAs, by two kernels: the first composes each chunk, the second
-// begins with the maps of the chunks before its own (it reads x and the gate again, mostly
-// from L2).
+// A thread takes V neighbouring nodes and walks along the steps, kSteps at a time.  Its warp
+// has the next steps copied into shared memory meanwhile, one to three such blocks ahead:
+// registers could not hold as much as has to be under way (with loads into registers, one
+// block ahead, 64 x 32 x 5,000 fp32 took 27 us and its gradient 45; with copies 23 and 41).
+// Where the nodes alone fill the device that is all: x and the gate are read once, nothing
+// is exchanged.
+//
+// Where they do not, the steps are cut into parts, one for each warp.  A step is the map
+// h -> a h + u, and so is a run of steps: (A2, U2) after (A1, U1) is (A2 A1, A2 U1 + U2).
+// Each warp first composes its part; the warps of a CTA exchange their maps through shared
+// memory; each then runs its part from the state that it now knows, reading it again,
+// mostly from L2.  With more parts than a CTA has warps these are two kernels: the first
+// leaves the maps of all CTAs and the second begins with those before its own.  The
+// composing goes through a part in the order opposite to the run that follows, so that what
+// was read last, and is in L2 still, is read first again.
 //
 // The gradient runs the other way: with g_t = d_out_t + r_{t+1}, r_t = a_t g_t is a map of
 // r_{t+1}, and
@@ -20,14 +26,17 @@
 // The states are built again in 32 bits from those that the forward keeps at every
 // kSteps-th step (its outputs may be rounded to 16 bits; this also reads less).
 //
-// What bounds both is memory.
+// What bounds it: memory for 32 bits (64 x 32 x 5,000, forward and gradients: 5.4 and
+// 5.0 TB/s of what each reads and writes), instructions for 16 (4.0 TB/s; a sigmoid alone is
+// 11, and a step of the gradient some 40 for each node).
 #include "ck_types.h"
 
 namespace ck {
 namespace {
 
-constexpr int kSteps = 16;      // steps of a thread
+constexpr int kSteps = 8;       // steps that a thread takes at a time
 constexpr int kGatedWarps = 8;  // warps of a CTA, at most
+constexpr int kMostSmem = 128 * 1024;
 
 struct GatedArgs {
     const void *x, *gate, *dout;  // [T][B][N], nodes dense
@@ -40,33 +49,30 @@ struct GatedArgs {
     float *kept;                   // [ceil(T / kSteps)][B][N]
     void *dx, *dgate;              // [T][B][N] dense, may be null
     float *dstate0;                // may be null
-    float2 *maps;                  // [chunks][B][N]
-    int chunk_tiles;               // tiles of a chunk
-    int64_t tiles;
+    float2 *maps, *inner;          // [chunks][B][N]; [parts][B][N]: of the CTA's parts before
+    int parts;                     // chunks * wt
+    int64_t blocks;                // kSteps steps each
     int wt, wc;                    // warps along the steps, along the nodes
+    int exchange;                  // bytes of shared memory before the rings
+    int copy;                      // bytes that a lane copies at a time
+    int apart;                     // rows of outputs that packs cannot be stored to
 };
+
+__device__ __forceinline__ void gated_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void gated_pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // V elements that lie together, as they are loaded and stored.
 template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
     T v[V];
 };
 
-template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(const T *p) {
-    Pack<T, V> r;
-    if constexpr (sizeof(r) == 8) {
-        const uint2 w = __ldg((const uint2 *)p);
-        memcpy(&r, &w, 8);
-    } else if constexpr (sizeof(r) == 4) {
-        const uint32_t w = __ldg((const uint32_t *)p);
-        memcpy(&r, &w, 4);
-    } else {
-        const uint16_t w = __ldg((const uint16_t *)p);
-        memcpy(&r, &w, 2);
-    }
-    return r;
-}
-template <typename T, int V> __device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &r) {
-    if constexpr (sizeof(r) == 8) {
+// Stores a pack: at once, or its first `count` one by one where it may lie anywhere (SHIFTED).
+template <bool SHIFTED, typename T, int V> __device__ __forceinline__ void store_pack(const GatedArgs &a, T *p, const Pack<T, V> &r, int count) {
+    if (SHIFTED && a.apart) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < count) p[v] = r.v[v];
+    } else if constexpr (sizeof(r) == 8) {
         uint2 w;
         memcpy(&w, &r, 8);
         __stcs((uint2 *)p, w);
@@ -81,45 +87,255 @@ template <typename T, int V> __device__ __forceinline__ void store_pack(T *p, co
     }
 }
 
-// sigmoid(f) and 1 - sigmoid(f), each to a few units of the last place whatever f: from
-// exp(-|f|), which does not overflow, and the reciprocal of a number in [1, 2].
-__device__ __forceinline__ void sigmoids(float f, float &l, float &a) {
-    const float e = expf(-fabsf(f)), r = __fdividef(1.f, 1.f + e), q = e * r;
-    l = f >= 0.f ? r : q;
-    a = f >= 0.f ? q : r;
-    if (f != f) l = a = f;
+// A copy of N bytes into shared memory that is waited for later.  Two bytes are too few for
+// one: they are loaded and stored.
+template <int N> __device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
+    if constexpr (N == 2) {
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(__ldg((const uint16_t *)from)) : "memory");
+    } else if constexpr (N == 16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
+    }
 }
+template <typename P> __device__ __forceinline__ P load_shared(uint32_t from) {
+    P r;
+    if constexpr (sizeof(P) == 8) {
+        uint2 w;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(from));
+        memcpy(&r, &w, 8);
+    } else if constexpr (sizeof(P) == 4) {
+        uint32_t w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(from));
+        memcpy(&r, &w, 4);
+    } else {
+        uint16_t w;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(from));
+        memcpy(&r, &w, 2);
+    }
+    return r;
+}
+template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// A thread's nodes: where they lie and how many steps each has.
+// A thread's nodes, and how many steps each has.
 template <int V> struct Nodes {
-    int64_t c, b, n;
-    int len[V], most;  // steps of each, of the longest
-    __device__ __forceinline__ bool find(const GatedArgs &a) {
+    int64_t c, warp_c;         // of [B][N], the first; the warp's first
+    int count;                 // of V, those that there are
+    int len[V], most, least;   // steps of each, of the longest, of the shortest
+    int warp_most;             // of the warp's longest
+    __device__ __forceinline__ bool has(int v) const { return v < count; }
+    __device__ __forceinline__ explicit Nodes(const GatedArgs &a) {
         const int lane = threadIdx.x & 31, wc = (threadIdx.x >> 5) / a.wt;
-        c = (((int64_t)blockIdx.x * a.wc + wc) * 32 + lane) * V;
+        warp_c = ((int64_t)blockIdx.x * a.wc + wc) * 32 * V;
+        c = warp_c + lane * V;
         const int64_t C = a.B * a.N;
-        const bool valid = c < C;
-        const int64_t at = valid ? c : 0;
-        if (C < ((int64_t)1 << 31)) {
-            b = (uint32_t)at / (uint32_t)a.N;
-        } else {
-            b = at / a.N;
-        }
-        n = at - b * a.N;
+        count = c >= C ? 0 : C - c < V ? (int)(C - c) : V;
         most = 0;
+        least = (int)a.T;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            len[v] = (int)a.T;
-            if (a.lengths && valid) {
-                const int64_t i = n + v >= a.N ? b + (n + v) / a.N : b, l = __ldg(a.lengths + i);
+            len[v] = v < count ? (int)a.T : 0;
+            if (a.lengths && v < count) {
+                const int64_t l = __ldg(a.lengths + (uint32_t)(c + v) / (uint32_t)a.N);
                 len[v] = l < 0 ? 0 : l < a.T ? (int)l : (int)a.T;
             }
-            if (!valid) len[v] = 0;
             most = len[v] > most ? len[v] : most;
+            if (v < count) least = len[v] < least ? len[v] : least;
         }
-        return valid;
+        warp_most = __reduce_max_sync(0xffffffffu, most);
     }
 };
+
+// Where a warp's blocks wait on their way from memory: for each of STAGES blocks kSteps rows
+// of 32 packs of each of NT tensors, and the states kept before it (KEPT).  The lanes copy
+// together, `copy` bytes each at a time, whatever a lane's own pack: with 16 bytes the copies
+// pass L1 by, which beside this much shared memory is too small to hold what is under way.
+//
+// SHIFTED: rows that begin anywhere.  The 16-byte pieces that hold a row are copied as they
+// lie, one more than it fills, and a row is read from where it begins inside the first.  Of
+// a piece that the row ends in, what lies behind the row is not read; what lies before its
+// begin shares an aligned 16 bytes with it.
+template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct Ring {
+    using P = Pack<T, V>;
+    static constexpr int kRow = 32 * (int)sizeof(P), kPitch = kRow + (SHIFTED ? 16 : 0);
+    static constexpr int kTensor = kSteps * kPitch, kStage = NT * kTensor + (KEPT ? 128 * V : 0);
+    static constexpr int kBytes = STAGES * kStage;
+    uint32_t base, put, get;  // stages to be filled and to be read next, times kStage
+    int lane, row, copy;  // of the copies: this lane's row of those that go at once
+    // SHIFTED: the low bits of the addresses of step 0 and of a step (the tensors' agree), and
+    // of the block that is read
+    uint32_t shift0, shift_step, shift;
+    int left, last_left;      // bytes that a row has from this lane's first on, and behind its last whole piece
+    const T *p[NT];
+    int64_t step[NT];
+    const float *kept;    // this thread's
+    int64_t kept_step;
+    int kept_count;
+    // The place that this lane copies from: sequence b, node n.
+    int64_t b, n;
+    __device__ __forceinline__ void begin(uint32_t smem, const GatedArgs &a, int64_t c) {
+        lane = threadIdx.x & 31;
+        base = smem + (threadIdx.x >> 5) * kBytes;
+        put = get = 0;
+        copy = a.copy;
+        const int lanes = kRow / copy;  // of a row
+        row = lane / lanes;
+        const int first = (lane - row * lanes) * (copy / (int)sizeof(T));
+        const int64_t room = (a.B * a.N - c - first) * (int64_t)sizeof(T);
+        left = room < -16 ? -16 : room > kRow ? kRow : (int)room;
+        const int64_t behind = (a.B * a.N - c) * (int64_t)sizeof(T) - kRow;
+        last_left = behind < -16 ? -16 : behind > 0 ? 0 : (int)behind;
+        if (SHIFTED) {
+            b = 0, n = c + first;  // (sequences join)
+        } else {
+            c = room > 0 ? c + first : 0;
+            b = (uint32_t)c / (uint32_t)a.N;
+            n = c - b * a.N;
+        }
+    }
+    __device__ __forceinline__ void tensor(int i, const void *from, int64_t to_step, int64_t to_row) {
+        p[i] = from ? (const T *)from + b * to_row + n + row * to_step : nullptr;
+        step[i] = to_step;
+        if (i == 0) {
+            shift_step = (uint32_t)to_step * (uint32_t)sizeof(T);
+            shift0 = (uint32_t)(uintptr_t)((const T *)from + n);
+        }
+    }
+    // Zeros, which nothing is copied over, in the place of a tensor that is not there.
+    __device__ __forceinline__ void clear(int i) {
+        for (int g = 0; g < kBytes; g += kStage)
+            for (int j = lane * 4; j < kTensor; j += 128)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + g + i * kTensor + j), "r"(0) : "memory");
+    }
+    template <int W> __device__ __forceinline__ void ask_rows(int steps) {
+        if constexpr (W >= (int)sizeof(P)) {
+            constexpr int R = W / (int)sizeof(P);
+            if (left <= 0) return;
+            const uint32_t to = base + put + lane * W;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                if (!p[i]) continue;
+                const T *q = p[i];
+                if (W >= 8 && steps >= kSteps) {
+#pragma unroll
+                    for (int s = 0; s < kSteps; s += R, q += R * step[i]) copy_async<W>(to + i * kTensor + s * kRow, q);
+                } else {
+                    const int most = steps < kSteps ? steps : kSteps;
+#pragma unroll 1
+                    for (int s = 0; s + row < most; s += R, q += R * step[i]) copy_async<W>(to + i * kTensor + s * kRow, q);
+                }
+            }
+        }
+    }
+    // The n bytes (at most 16) of the piece that holds q.
+    __device__ __forceinline__ void piece(uint32_t to, const T *q, int n) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"((uintptr_t)q & ~(uintptr_t)15), "r"(n) : "memory");
+    }
+    __device__ __forceinline__ void ask_shifted(int k, int steps) {
+        constexpr int R = 16 / (int)sizeof(P), kPieces = kRow / 16;
+        const uint32_t to = base + put + row * kPitch + (lane % kPieces) * 16, last = base + put + lane * kPitch + kRow;
+        const uint32_t block = shift0 + (uint32_t)(k * kSteps) * shift_step;
+#pragma unroll
+        for (int s = 0; s < kSteps; s += R) {
+            const int n = left + (int)((block + (s + row) * shift_step) & 15);
+            if (n <= 0 || s + row >= steps) continue;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                if (p[i]) piece(to + i * kTensor + s * kPitch, p[i] + s * step[i], n < 16 ? n : 16);
+        }
+        // the last piece of row `lane`
+        const int n = last_left + (int)((block + lane * shift_step) & 15);
+        if (lane < kSteps && lane < steps && n > 0) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                if (p[i]) piece(last + i * kTensor, p[i] + (lane - row) * step[i] + (kPieces - lane % kPieces) * (16 / (int)sizeof(T)), n);
+        }
+    }
+    // Asks for the first `steps` steps of block k, and leaves a mark to wait for.
+    __device__ __forceinline__ void ask(int k, int steps) {
+        if (SHIFTED)
+            ask_shifted(k, steps);
+        else if (copy == 16)
+            ask_rows<16>(steps);
+        else if (copy == 8)
+            ask_rows<8>(steps);
+        else if (copy == 4)
+            ask_rows<4>(steps);
+        else
+            ask_rows<2>(steps);
+        if constexpr (KEPT) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v < kept_count) copy_async<4>(base + put + kept_place(v), kept + v);
+        }
+    }
+    // Takes the places that are copied from on by n blocks.
+    __device__ __forceinline__ void go(int n) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            if (p[i]) p[i] += (int64_t)n * kSteps * step[i];
+        if (KEPT) kept += n * kept_step;
+    }
+    __device__ __forceinline__ void asked(int way) {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        go(way);
+        put = put == (STAGES - 1) * kStage ? 0 : put + kStage;
+    }
+    __device__ __forceinline__ uint32_t kept_place(int v) const { return NT * kTensor + v * 128 + lane * 4; }
+    // Of the block that is read: where step s of tensor i lies, what it is, the state before.
+    __device__ __forceinline__ uint32_t place(int i, int s) const {
+        const uint32_t at = base + get + lane * (int)sizeof(P) + i * kTensor + s * kPitch;
+        return SHIFTED ? at + ((shift + s * shift_step) & 15u) : at;
+    }
+    __device__ __forceinline__ P step_of(int i, int s) const {
+        if constexpr (!SHIFTED) {
+            return load_shared<P>(place(i, s));
+        } else {
+            P r;
+#pragma unroll
+            for (int v = 0; v < V; ++v) r.v[v] = load_shared<T>(place(i, s) + v * (int)sizeof(T));
+            return r;
+        }
+    }
+    __device__ __forceinline__ float kept_of(int v) const { return load_shared<float>(base + get + kept_place(v)); }
+
+    // `count` blocks from `first` on in the order of `way` (1 or -1): take(k) for each, when
+    // it has come.  most: the steps of the warp's longest sequence.
+    template <typename F> __device__ __forceinline__ void each(int first, int count, int way, int most, F take) {
+        go(first);
+        for (int i = 0; i < count + STAGES - 1; ++i) {  // block i is asked for, then the one STAGES - 1 before it taken
+            const int next = first + way * i, k = next - way * (STAGES - 1);
+            __syncwarp();  // the stage that is asked for has been read by all lanes
+            if (i < count) ask(next, most - next * kSteps);
+            asked(way);
+            if (i < STAGES - 1) continue;
+            wait_copies<STAGES - 1>();
+            __syncwarp();
+            shift = shift0 + (uint32_t)(k * kSteps) * shift_step;
+            take(k);
+            get = get == (STAGES - 1) * kStage ? 0 : get + kStage;
+        }
+        wait_copies<0>();
+        __syncwarp();
+        put = get = 0;
+        go(-(first + way * (count + STAGES - 1)));
+    }
+};
+
+// l = sigmoid(f) and a = 1 - l, each to a few units of its last place: with e = exp(-f),
+// l = 1 / (1 + e) and a = e l.  2^t for t = -f log2(e) is the device's approximation (2^-22.5
+// relative); what the rounding of t lost, -f - t ln 2, is put in again by e (1 + that).  f is
+// kept between the borders of e's range, NaN as it is; below -30 a is 1 to the last place.
+__device__ __forceinline__ void sigmoids(float f, float &l, float &a) {
+    float c, e;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(f), "f"(-87.f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(c), "f"(100.f));
+    const float t = c * -1.4426950408889634f, lost = fmaf(t, -0.6931471805599453f, -c);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = fmaf(e, lost, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(l) : "f"(1.f + e));
+    a = c < -30.f ? 1.f : e * l;
+}
 
 // A product of factors of which none is 0 is not 0 either, or an infinite state would
 // become NaN where its steps leave it infinite: the least number above 0 stands for it.
@@ -132,305 +348,403 @@ __device__ __forceinline__ float2 compose(float2 later, float2 earlier) {
                        fmaf(later.x, earlier.y, later.y));
 }
 
-// The maps of the warps' stretches, [parity][warp][V][lane].
+// The maps of the warps' parts.
 template <int V> struct Exchange {
-    float2 m[2][kGatedWarps][V][32];
+    float2 m[kGatedWarps][V][32];
 };
 
-// The map of chunks [first, last) for this thread's nodes, the warps along the steps
-// taking a part each.  REVERSE: a later chunk's map is applied first.
+// The blocks [lo, hi) of a part.
+struct Part {
+    int lo, hi, i;
+    __device__ __forceinline__ Part(const GatedArgs &a, int wt) {
+        i = blockIdx.y * a.wt + wt;
+        lo = (int)(a.blocks * i / a.parts);
+        hi = (int)(a.blocks * (i + 1) / a.parts);
+    }
+};
+
+// carry through the maps of chunks [first, last), the warps along the steps taking some
+// each.  REVERSE: a later chunk's map is applied first.
 template <int V, bool REVERSE>
-__device__ __forceinline__ void chunk_maps(const GatedArgs &a, const Nodes<V> &at, bool valid, int first, int last,
-                                           Exchange<V> &ex, float (&carry)[V]) {
+__device__ __forceinline__ void through_chunks(const GatedArgs &a, const Nodes<V> &at, int first, int last,
+                                               Exchange<V> &ex, float (&carry)[V]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp % a.wt;
     const int n = last - first, lo = first + n * wt / a.wt, hi = first + n * (wt + 1) / a.wt;
     const int64_t C = a.B * a.N;
     float2 m[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) m[v] = make_float2(1.f, 0.f);
-    if (valid) {
 #pragma unroll 4
-        for (int i = 0; i < hi - lo; ++i) {
-            const float2 *p = a.maps + (int64_t)(REVERSE ? hi - 1 - i : lo + i) * C + at.c;
+    for (int i = 0; i < hi - lo; ++i) {
+        const float2 *p = a.maps + (int64_t)(REVERSE ? hi - 1 - i : lo + i) * C + at.c;
 #pragma unroll
-            for (int v = 0; v < V; ++v) m[v] = compose(__ldcg(p + v), m[v]);
-        }
+        for (int v = 0; v < V; ++v)
+            if (at.has(v)) m[v] = compose(__ldcg(p + v), m[v]);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) ex.m[0][warp][v][lane] = m[v];
+    for (int v = 0; v < V; ++v) ex.m[warp][v][lane] = m[v];
     __syncthreads();
     const int base = warp - wt;
     for (int j = 0; j < a.wt; ++j)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float2 p = ex.m[0][base + (REVERSE ? a.wt - 1 - j : j)][v][lane];
+            const float2 p = ex.m[base + (REVERSE ? a.wt - 1 - j : j)][v][lane];
             carry[v] = fmaf(p.x, carry[v], p.y);
         }
-    __syncthreads();
 }
 
-// MAPS: composes the chunk and writes its map.  Otherwise runs it.
-template <typename T, int V, bool LEAK, bool MAPS>
-__global__ void __launch_bounds__(32 * kGatedWarps, 2) k_gated_forward(const __grid_constant__ GatedArgs a) {
-    __shared__ Exchange<V> ex;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp % a.wt;
-    Nodes<V> at;
-    const bool valid = at.find(a);
+// What is carried into this warp's part.  MAPS: composes the part with part_map(m) and
+// leaves the maps; otherwise carry goes through all that comes before.
+template <int V, bool MAPS, bool REVERSE, typename F>
+__device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at, Exchange<V> &ex,
+                                         float (&carry)[V], F part_map) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp % a.wt, base = warp - wt;
     const int64_t C = a.B * a.N;
-    const T *x = (const T *)a.x + at.b * a.xb + at.n, *gate = (const T *)a.gate + at.b * a.gb + at.n;
-    const int64_t k0 = (int64_t)blockIdx.y * a.chunk_tiles;
-    const int64_t k1 = k0 + a.chunk_tiles < a.tiles ? k0 + a.chunk_tiles : a.tiles;
-    float h[V];      // the state before the tile
-    float2 all[V];   // MAPS: the map of the tiles so far
+    const int64_t part = (int64_t)blockIdx.y * a.wt + wt;
+    if (!MAPS && gridDim.y > 1) {
+        gated_pdl_wait();
+        if (REVERSE ? blockIdx.y + 1 < gridDim.y : blockIdx.y > 0)
+            through_chunks<V, REVERSE>(a, at, REVERSE ? blockIdx.y + 1 : 0, REVERSE ? gridDim.y : blockIdx.y, ex, carry);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (!at.has(v)) continue;
+            const float2 p = __ldcg(a.inner + part * C + at.c + v);
+            carry[v] = fmaf(p.x, carry[v], p.y);
+        }
+        return;
+    }
+    if (!MAPS && a.wt == 1) return;
+    float2 m[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) m[v] = make_float2(1.f, 0.f);
+    if (MAPS || (REVERSE ? wt > 0 : wt + 1 < a.wt)) part_map(m);  // (nothing follows the last)
+#pragma unroll
+    for (int v = 0; v < V; ++v) ex.m[warp][v][lane] = m[v];
+    __syncthreads();
+    if constexpr (MAPS) {
+        float2 p[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) p[v] = make_float2(1.f, 0.f);
+        const int before = REVERSE ? a.wt - 1 - wt : wt;
+        for (int j = 0; j < before; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) p[v] = compose(ex.m[base + (REVERSE ? a.wt - 1 - j : j)][v][lane], p[v]);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (!at.has(v)) continue;
+            a.inner[part * C + at.c + v] = p[v];
+            if (before == a.wt - 1) a.maps[(int64_t)blockIdx.y * C + at.c + v] = compose(m[v], p[v]);
+        }
+    } else {
+        const int before = REVERSE ? a.wt - 1 - wt : wt;
+        for (int j = 0; j < before; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float2 q = ex.m[base + (REVERSE ? a.wt - 1 - j : j)][v][lane];
+                carry[v] = fmaf(q.x, carry[v], q.y);
+            }
+    }
+}
+
+// What step t keeps of the state and puts in, for node v.
+template <bool LEAK> __device__ __forceinline__ void gates(float f, float x, float &keep, float &put) {
+    if constexpr (LEAK) {
+        float l;
+        sigmoids(f, l, keep);
+        put = l * x;
+    } else {
+        keep = f;
+        put = x;
+    }
+}
+
+// Stages of a ring: more of smaller ones, so that 16 warps of an SM have 64 KB or more under
+// way, and as many as 16 warps have room for.
+template <typename T, int V> constexpr int kForwardStages = sizeof(T) * V >= 8 ? 3 : 4;
+template <typename T, int V> constexpr int kBackwardStages = sizeof(T) * V >= 8 ? 2 : 4;
+template <typename T, int V, bool SHIFTED> using ForwardRing = Ring<T, V, 2, false, kForwardStages<T, V>, SHIFTED>;
+template <typename T, int V, bool SHIFTED, bool MAPS>
+using BackwardRing = Ring<T, V, MAPS ? 2 : 3, !MAPS, kBackwardStages<T, V>, SHIFTED>;
+
+// The map of one block of gates and inputs.  WHOLE: all nodes have all its steps.
+template <typename T, int V, bool LEAK, bool WHOLE, typename R>
+__device__ __forceinline__ void forward_map(const R &in, const Nodes<V> &at, int t0, float2 (&all)[V]) {
+    float2 m[V];
+    float least[V];  // of the factors' magnitudes
+#pragma unroll
+    for (int v = 0; v < V; ++v) m[v] = make_float2(least[v] = 1.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const Pack<T, V> g = in.step_of(0, s), x = in.step_of(1, s);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float keep, put;
+            gates<LEAK>(to_float(g.v[v]), to_float(x.v[v]), keep, put);
+            if (!WHOLE && t0 + s >= at.len[v]) keep = 1.f, put = 0.f;
+            m[v] = make_float2(keep * m[v].x, fmaf(keep, m[v].y, put));
+            least[v] = fminf(least[v], fabsf(keep));
+        }
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        h[v] = !MAPS && a.state0 && valid ? __ldg(a.state0 + at.c + v) : 0.f;
-        all[v] = make_float2(1.f, 0.f);
+        m[v].x = not_lost(m[v].x, least[v] > 0.f);
+        all[v] = compose(all[v], m[v]);
     }
-    if (!MAPS && blockIdx.y > 0) chunk_maps<V, false>(a, at, valid, 0, blockIdx.y, ex, h);
-    for (int64_t k = k0; k < k1; ++k) {
-        const int t0 = (int)(k * a.wt + wt) * kSteps;
-        Pack<T, V> px[kSteps], pg[kSteps];
+}
+
+// One block's steps from the state h on.
+template <typename T, int V, bool LEAK, bool SHIFTED, bool WHOLE, typename R>
+__device__ __forceinline__ void forward_run(const GatedArgs &a, const R &in, const Nodes<V> &at, int t0, float (&h)[V]) {
+    const int64_t C = a.B * a.N;
+    T *out = (T *)a.out + (int64_t)t0 * C + at.c;
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
-            if (t0 + s < at.most) {
-                px[s] = load_pack<T, V>(x + (t0 + s) * a.xt);
-                pg[s] = load_pack<T, V>(gate + (t0 + s) * a.gt);
-            }
-        float keep[kSteps][V], put[kSteps][V];
-        float2 m[V];
-        float least[V];  // of the factors' magnitudes
+    for (int s = 0; s < kSteps; ++s, out += C) {
+        const Pack<T, V> g = in.step_of(0, s), x = in.step_of(1, s);
+        Pack<T, V> o;
 #pragma unroll
-        for (int v = 0; v < V; ++v) m[v] = make_float2(least[v] = 1.f, 0.f);
+        for (int v = 0; v < V; ++v) {
+            const bool live = WHOLE || t0 + s < at.len[v];
+            float keep, put;
+            gates<LEAK>(to_float(g.v[v]), to_float(x.v[v]), keep, put);
+            const float r = fmaf(keep, h[v], put);
+            h[v] = live ? r : h[v];
+            o.v[v] = from_float<T>(live ? r : 0.f);
+        }
+        if (WHOLE || t0 + s < a.T) store_pack<SHIFTED>(a, out, o, at.count);
+    }
+}
+
+// A block behind all sequences.
+template <typename T, int V, bool SHIFTED>
+__device__ __forceinline__ void store_zeros(const GatedArgs &a, void *to, const Nodes<V> &at, int t0) {
+    if (!to) return;
+    const int64_t C = a.B * a.N;
+    T *out = (T *)to + (int64_t)t0 * C + at.c;
+    Pack<T, V> zero;
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
+    for (int v = 0; v < V; ++v) zero.v[v] = from_float<T>(0.f);
+    for (int s = 0; s < kSteps && t0 + s < a.T; ++s, out += C) store_pack<SHIFTED>(a, out, zero, at.count);
+}
+
+// MAPS: composes the parts and writes their maps.  Otherwise runs them.
+template <typename T, int V, bool LEAK, bool SHIFTED, bool MAPS>
+__global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArgs a) {
+    extern __shared__ __align__(16) char shared[];
+    const uint32_t smem = (uint32_t)__cvta_generic_to_shared(shared) + a.exchange;
+    Exchange<V> &ex = *(Exchange<V> *)shared;  // where there is one
+    const int wt = (threadIdx.x >> 5) % a.wt;
+    const Nodes<V> at(a);
+    const int64_t C = a.B * a.N;
+    ForwardRing<T, V, SHIFTED> in;
+    in.begin(smem, a, at.warp_c);
+    in.tensor(0, a.gate, a.gt, a.gb);
+    in.tensor(1, a.x, a.xt, a.xb);
+    const Part part(a, wt);
+    if constexpr (MAPS) gated_pdl_launch();
+    float h[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float ka = 1.f, u = 0.f;
-                if (t0 + s < at.len[v]) {
-                    if constexpr (LEAK) {
-                        float l;
-                        sigmoids(to_float(pg[s].v[v]), l, ka);
-                        u = l * to_float(px[s].v[v]);
-                    } else {
-                        ka = to_float(pg[s].v[v]);
-                        u = to_float(px[s].v[v]);
-                    }
-                }
-                keep[s][v] = ka;
-                put[s][v] = u;
-                m[v] = make_float2(ka * m[v].x, fmaf(ka, m[v].y, u));
-                least[v] = fminf(least[v], fabsf(ka));
-            }
-#pragma unroll
-        for (int v = 0; v < V; ++v) m[v].x = not_lost(m[v].x, least[v] > 0.f);
-        float mine[V];
-        const int p = (int)(k & 1);
-#pragma unroll
-        for (int v = 0; v < V; ++v) ex.m[p][warp][v][lane] = m[v];
-        __syncthreads();
-        const int base = warp - wt;
-        for (int j = 0; j < a.wt; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float2 q = ex.m[p][base + j][v][lane];
-                if constexpr (MAPS) {
-                    all[v] = compose(q, all[v]);
-                } else {
-                    if (j == wt) mine[v] = h[v];
-                    h[v] = fmaf(q.x, h[v], q.y);
-                }
-            }
-        if constexpr (!MAPS) {
-            if (!valid || t0 >= a.T) continue;
+    for (int v = 0; v < V; ++v) h[v] = !MAPS && a.state0 && at.has(v) ? __ldg(a.state0 + at.c + v) : 0.f;
+    exchange<V, MAPS, false>(a, at, ex, h, [&](float2 (&m)[V]) {
+        in.each(part.hi - 1, part.hi - part.lo, -1, at.warp_most, [&](int k) {
+            const int t0 = k * kSteps;
+            if (t0 + kSteps <= at.least)
+                forward_map<T, V, LEAK, true>(in, at, t0, m);
+            else if (t0 < at.most)
+                forward_map<T, V, LEAK, false>(in, at, t0, m);
+        });
+    });
+    if constexpr (!MAPS) {
+        in.each(part.lo, part.hi - part.lo, 1, at.warp_most, [&](int k) {
+            const int t0 = k * kSteps;
+            if (!at.count) return;
             if (a.kept) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) a.kept[(int64_t)(t0 / kSteps) * C + at.c + v] = mine[v];
+                for (int v = 0; v < V; ++v)
+                    if (at.has(v)) a.kept[(int64_t)k * C + at.c + v] = h[v];
             }
-            T *out = (T *)a.out + (int64_t)t0 * C + at.c;
+            if (t0 + kSteps <= at.least)
+                forward_run<T, V, LEAK, SHIFTED, true>(a, in, at, t0, h);
+            else if (t0 < at.most)
+                forward_run<T, V, LEAK, SHIFTED, false>(a, in, at, t0, h);
+            else
+                store_zeros<T, V, SHIFTED>(a, a.out, at, t0);
+        });
+        if (part.i + 1 == a.parts) {
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                if (t0 + s >= a.T) break;
-                Pack<T, V> o;
+            for (int v = 0; v < V; ++v)
+                if (at.has(v)) a.state[at.c + v] = h[v];
+        }
+    }
+}
+
+template <typename T, int V, bool LEAK, bool WHOLE, typename R>
+__device__ __forceinline__ void backward_map(const R &in, const Nodes<V> &at, int t0, float2 (&all)[V]) {
+    float2 m[V];
+    float least[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    mine[v] = fmaf(keep[s][v], mine[v], put[s][v]);
-                    o.v[v] = from_float<T>(t0 + s < at.len[v] ? mine[v] : 0.f);
-                }
-                store_pack<T, V>(out + s * C, o);
+    for (int v = 0; v < V; ++v) m[v] = make_float2(least[v] = 1.f, 0.f);
+#pragma unroll
+    for (int s = kSteps - 1; s >= 0; --s) {
+        const Pack<T, V> g = in.step_of(0, s), d = in.step_of(1, s);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float l, keep = to_float(g.v[v]), add = to_float(d.v[v]);
+            if constexpr (LEAK) sigmoids(keep, l, keep);
+            if (!WHOLE && t0 + s >= at.len[v]) keep = 1.f, add = 0.f;
+            m[v] = make_float2(keep * m[v].x, keep * (m[v].y + add));
+            least[v] = fminf(least[v], fabsf(keep));
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        m[v].x = not_lost(m[v].x, least[v] > 0.f);
+        all[v] = compose(all[v], m[v]);
+    }
+}
+
+// One block's gradients, r being that of the state after it.
+template <typename T, int V, bool LEAK, bool SHIFTED, bool WHOLE, typename R>
+__device__ __forceinline__ void backward_run(const GatedArgs &a, const R &in, const Nodes<V> &at, int t0, float (&r)[V]) {
+    const int64_t C = a.B * a.N;
+    // of each step: what it keeps, and what the gradients are multiplied with
+    float keep[kSteps][V], leak[kSteps][V], by[kSteps][V], h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = in.kept_of(v);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const Pack<T, V> pg = in.step_of(0, s), px = in.step_of(2, s);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const bool live = WHOLE || t0 + s < at.len[v];
+            const float x = live ? to_float(px.v[v]) : 0.f, f = live ? to_float(pg.v[v]) : 0.f;
+            if constexpr (LEAK) {
+                sigmoids(f, leak[s][v], keep[s][v]);
+                by[s][v] = keep[s][v] * (x - h[v]);
+                h[v] = fmaf(keep[s][v], h[v], leak[s][v] * x);
+            } else {
+                keep[s][v] = f;
+                by[s][v] = h[v];
+                h[v] = fmaf(f, h[v], x);
             }
         }
     }
-    if (!valid || wt != 0) return;
+    T *dx = (T *)a.dx + (int64_t)(t0 + kSteps - 1) * C + at.c, *dgate = (T *)a.dgate + (int64_t)(t0 + kSteps - 1) * C + at.c;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if constexpr (MAPS) {
-            a.maps[(int64_t)blockIdx.y * C + at.c + v] = all[v];
-        } else {
-            if (blockIdx.y + 1 == gridDim.y) a.state[at.c + v] = h[v];
+    for (int s = kSteps - 1; s >= 0; --s, dx -= C, dgate -= C) {
+        const Pack<T, V> pd = in.step_of(1, s);
+        Pack<T, V> ox, og;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const bool live = WHOLE || t0 + s < at.len[v];
+            const float g = r[v] + to_float(pd.v[v]), vx = LEAK ? g * leak[s][v] : g;
+            ox.v[v] = from_float<T>(live ? vx : 0.f);
+            og.v[v] = from_float<T>(live ? vx * by[s][v] : 0.f);
+            r[v] = live ? keep[s][v] * g : r[v];
+        }
+        if (WHOLE || t0 + s < a.T) {
+            if (a.dx) store_pack<SHIFTED>(a, dx, ox, at.count);
+            if (a.dgate) store_pack<SHIFTED>(a, dgate, og, at.count);
         }
     }
 }
 
 // The same with time reversed, and the gradients.
-template <typename T, int V, bool LEAK, bool MAPS>
-__global__ void __launch_bounds__(32 * kGatedWarps, 2) k_gated_backward(const __grid_constant__ GatedArgs a) {
-    __shared__ Exchange<V> ex;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp % a.wt;
-    Nodes<V> at;
-    const bool valid = at.find(a);
+template <typename T, int V, bool LEAK, bool SHIFTED, bool MAPS>
+__global__ void __maxnreg__(112) k_gated_backward(const __grid_constant__ GatedArgs a) {
+    extern __shared__ __align__(16) char shared[];
+    const uint32_t smem = (uint32_t)__cvta_generic_to_shared(shared) + a.exchange;
+    Exchange<V> &ex = *(Exchange<V> *)shared;  // where there is one
+    const int wt = (threadIdx.x >> 5) % a.wt;
+    const Nodes<V> at(a);
     const int64_t C = a.B * a.N;
-    const T *x = (const T *)a.x + at.b * a.xb + at.n, *gate = (const T *)a.gate + at.b * a.gb + at.n;
-    const T *dout = (const T *)a.dout + at.b * a.db + at.n;
-    const int64_t k0 = (int64_t)blockIdx.y * a.chunk_tiles;
-    const int64_t k1 = k0 + a.chunk_tiles < a.tiles ? k0 + a.chunk_tiles : a.tiles;
+    const Part part(a, wt);
+    if constexpr (MAPS) gated_pdl_launch();
+    const auto begin = [&](auto &in) {
+        in.begin(smem, a, at.warp_c);
+        in.tensor(0, a.gate, a.gt, a.gb);
+        in.tensor(1, a.dout, a.dt, a.db);
+        if (!a.dout) in.clear(1);
+    };
     float r[V];
-    float2 all[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        r[v] = !MAPS && a.dstate && valid ? __ldg(a.dstate + at.c + v) : 0.f;
-        all[v] = make_float2(1.f, 0.f);
-    }
-    if (!MAPS && blockIdx.y + 1 < gridDim.y)
-        chunk_maps<V, true>(a, at, valid, blockIdx.y + 1, gridDim.y, ex, r);
-    for (int64_t k = k1 - 1; k >= k0; --k) {
-        const int t0 = (int)(k * a.wt + wt) * kSteps;
-        Pack<T, V> px[kSteps], pg[kSteps], pd[kSteps];
-        float before[kSteps][V];  // decay: the state before the step; leak: x less that
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s)
-            if (t0 + s < at.most) {
-                pg[s] = load_pack<T, V>(gate + (t0 + s) * a.gt);
-                pd[s] = a.dout ? load_pack<T, V>(dout + (t0 + s) * a.dt) : Pack<T, V>{};
-                if (!MAPS) px[s] = load_pack<T, V>(x + (t0 + s) * a.xt);
+    for (int v = 0; v < V; ++v) r[v] = !MAPS && a.dstate && at.has(v) ? __ldg(a.dstate + at.c + v) : 0.f;
+    exchange<V, MAPS, true>(a, at, ex, r, [&](float2 (&m)[V]) {
+        BackwardRing<T, V, SHIFTED, true> in;
+        begin(in);
+        in.each(part.lo, part.hi - part.lo, 1, at.warp_most, [&](int k) {
+            const int t0 = k * kSteps;
+            if (t0 + kSteps <= at.least)
+                backward_map<T, V, LEAK, true>(in, at, t0, m);
+            else if (t0 < at.most)
+                backward_map<T, V, LEAK, false>(in, at, t0, m);
+        });
+    });
+    if constexpr (!MAPS) {
+        BackwardRing<T, V, SHIFTED, false> in;
+        begin(in);
+        in.tensor(2, a.x, a.xt, a.xb);
+        in.kept = a.kept + at.c, in.kept_count = at.count;
+        in.kept_step = C;
+        in.each(part.hi - 1, part.hi - part.lo, -1, at.warp_most, [&](int k) {
+            const int t0 = k * kSteps;
+            if (!at.count) return;
+            if (t0 + kSteps <= at.least) {
+                backward_run<T, V, LEAK, SHIFTED, true>(a, in, at, t0, r);
+            } else if (t0 < at.most) {
+                backward_run<T, V, LEAK, SHIFTED, false>(a, in, at, t0, r);
+            } else {
+                store_zeros<T, V, SHIFTED>(a, a.dx, at, t0);
+                store_zeros<T, V, SHIFTED>(a, a.dgate, at, t0);
             }
-        if constexpr (!MAPS) {
-            float h[V];
-            if (t0 < at.most) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) h[v] = __ldg(a.kept + (int64_t)(t0 / kSteps) * C + at.c + v);
-            }
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (t0 + s < at.len[v]) {
-                        const float xs = to_float(px[s].v[v]), f = to_float(pg[s].v[v]);
-                        if constexpr (LEAK) {
-                            float l, ka;
-                            sigmoids(f, l, ka);
-                            before[s][v] = xs - h[v];
-                            h[v] = fmaf(ka, h[v], l * xs);
-                        } else {
-                            before[s][v] = h[v];
-                            h[v] = fmaf(f, h[v], xs);
-                        }
-                    }
-        }
-        float2 m[V];
-        float least[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) m[v] = make_float2(least[v] = 1.f, 0.f);
-#pragma unroll
-        for (int s = kSteps - 1; s >= 0; --s)
+        });
+        if (part.i == 0 && a.dstate0) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (t0 + s < at.len[v]) {
-                    float l, ka = to_float(pg[s].v[v]);
-                    if constexpr (LEAK) sigmoids(ka, l, ka);
-                    m[v] = make_float2(ka * m[v].x, ka * (m[v].y + to_float(pd[s].v[v])));
-                    least[v] = fminf(least[v], fabsf(ka));
-                }
-#pragma unroll
-        for (int v = 0; v < V; ++v) m[v].x = not_lost(m[v].x, least[v] > 0.f);
-        float mine[V];
-        const int p = (int)(k & 1);
-#pragma unroll
-        for (int v = 0; v < V; ++v) ex.m[p][warp][v][lane] = m[v];
-        __syncthreads();
-        const int base = warp - wt;
-        for (int j = a.wt - 1; j >= 0; --j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float2 q = ex.m[p][base + j][v][lane];
-                if constexpr (MAPS) {
-                    all[v] = compose(q, all[v]);
-                } else {
-                    if (j == wt) mine[v] = r[v];
-                    r[v] = fmaf(q.x, r[v], q.y);
-                }
-            }
-        if constexpr (!MAPS) {
-            if (!valid || t0 >= a.T) continue;
-            T *dx = (T *)a.dx + (int64_t)t0 * C + at.c, *dgate = (T *)a.dgate + (int64_t)t0 * C + at.c;
-#pragma unroll
-            for (int s = kSteps - 1; s >= 0; --s) {
-                if (t0 + s >= a.T) continue;
-                Pack<T, V> ox, og;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float vx = 0.f, vg = 0.f;
-                    if (t0 + s < at.len[v]) {
-                        const float g = mine[v] + to_float(pd[s].v[v]);
-                        float l, ka = to_float(pg[s].v[v]);
-                        if constexpr (LEAK) {
-                            sigmoids(ka, l, ka);
-                            vx = g * l;
-                            vg = vx * ka * before[s][v];
-                        } else {
-                            vx = g;
-                            vg = g * before[s][v];
-                        }
-                        mine[v] = ka * g;
-                    }
-                    ox.v[v] = from_float<T>(vx);
-                    og.v[v] = from_float<T>(vg);
-                }
-                if (a.dx) store_pack<T, V>(dx + s * C, ox);
-                if (a.dgate) store_pack<T, V>(dgate + s * C, og);
-            }
-        }
-    }
-    if (!valid || wt != 0) return;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if constexpr (MAPS) {
-            a.maps[(int64_t)blockIdx.y * C + at.c + v] = all[v];
-        } else {
-            if (blockIdx.y == 0 && a.dstate0) a.dstate0[at.c + v] = r[v];
+                if (at.has(v)) a.dstate0[at.c + v] = r[v];
         }
     }
 }
 
 // How a call is cut.
 struct GatedPlan {
-    int wt, wc;
-    int64_t blocks, tiles;
-    int chunk_tiles, chunks;
+    int wt, wc, chunks;
+    int64_t blocks, grid;  // of kSteps steps; CTAs along the nodes
 };
 
 GatedPlan gated_plan(int64_t T, int64_t C, int V, int sms) {
     GatedPlan p{};
+    p.blocks = (T + kSteps - 1) / kSteps;
+    const int64_t warps = (C + 32 * V - 1) / (32 * V);
+    // parts: as many as give every SM kFill warps, which is what fits (65,536 x 256 bf16: 119 us
+    // with 16, 143 with 12, 151 with 24, before the copies), of at least four blocks each
+    constexpr int64_t kFill = 16;
+    int64_t parts = warps >= 8 * sms ? 1 : (kFill * sms + warps - 1) / warps;
+    if (parts > p.blocks / 4) parts = p.blocks / 4;
+    if (parts < 1) parts = 1;
     p.wt = 1;
-    while (p.wt < kGatedWarps && (int64_t)p.wt * kSteps < T) p.wt *= 2;
-    p.wc = kGatedWarps / p.wt;
-    while (p.wc > 1 && C < (int64_t)p.wc * 32 * V * sms) p.wc /= 2;
-    p.tiles = (T + (int64_t)p.wt * kSteps - 1) / ((int64_t)p.wt * kSteps);
-    p.blocks = (C + (int64_t)p.wc * 32 * V - 1) / ((int64_t)p.wc * 32 * V);
-    // chunks: so many that every SM has two CTAs, of at least two tiles
-    int64_t chunks = p.blocks >= sms ? 1 : (2 * (int64_t)sms + p.blocks - 1) / p.blocks;
-    if (chunks > p.tiles / 2) chunks = p.tiles / 2;
-    if (chunks < 1) chunks = 1;
-    p.chunk_tiles = (int)((p.tiles + chunks - 1) / chunks);
-    p.chunks = (int)((p.tiles + p.chunk_tiles - 1) / p.chunk_tiles);
+    while (p.wt < kGatedWarps && 2 * p.wt <= parts) p.wt *= 2;
+    p.chunks = parts >= 2 * kGatedWarps ? (int)(parts / kGatedWarps) : 1;
+    p.wc = p.wt == 1 ? 2 : kGatedWarps / p.wt;  // (small CTAs fill an SM to the last warp)
+    while (p.wc > 1 && warps < (int64_t)p.wc * sms) p.wc /= 2;
+    p.grid = (warps + p.wc - 1) / p.wc;
     return p;
 }
 
-// Elements that a thread may take at a time: two where every row of steps and sequences
-// begins at a multiple of two of them and no pair crosses into a row that does not follow.
-bool in_pairs(const void *p, int64_t st, int64_t sb, int64_t B, int64_t N, int64_t T, size_t size) {
+size_t maps_bytes(const GatedPlan &p, int64_t C) { return (size_t)p.chunks * (1 + p.wt) * C * sizeof(float2); }
+
+// Whether a thread may take V elements at a time: every row of steps and sequences begins
+// at a multiple of them, and none crosses into a row that does not follow.
+bool in_packs(const void *p, int V, int64_t st, int64_t sb, int64_t B, int64_t N, int64_t T, size_t size) {
     const bool joined = B == 1 || sb == N;
-    return aligned(p, 2 * size) && (T == 1 || st % 2 == 0) && (joined ? B * N % 2 == 0 : N % 2 == 0 && sb % 2 == 0);
+    return aligned(p, V * size) && (T == 1 || st % V == 0) && (joined ? B * N % V == 0 : N % V == 0 && sb % V == 0);
+}
+
+ck_status check_gated_sizes(int64_t T, int64_t B, int64_t N) {
+    if (T < 0 || B < 0 || N < 0) return fail(CK_ERR_INVALID_ARG, "gated recurrence: negative size");
+    // (a step's nodes are counted, and their bytes, in 32 bits)
+    constexpr int64_t kNodes = (int64_t)1 << 28, kSteps30 = (int64_t)1 << 30;
+    if (T > kSteps30 || (B && N > kNodes / B)) return fail(CK_ERR_UNSUPPORTED, "gated recurrence: more than 2^28 nodes or 2^30 steps");
+    return CK_OK;
 }
 
 ck_status check_gated(const ck_gated_call *c, bool backward) {
@@ -438,11 +752,8 @@ ck_status check_gated(const ck_gated_call *c, bool backward) {
     if (!known_dtype(c->dtype)) return fail(CK_ERR_INVALID_ARG, "gated recurrence: unknown dtype %lld", (long long)c->dtype);
     if (c->form != CK_GATED_LEAK && c->form != CK_GATED_DECAY)
         return fail(CK_ERR_INVALID_ARG, "gated recurrence: unknown form %lld", (long long)c->form);
-    if (c->T < 0 || c->B < 0 || c->N < 0) return fail(CK_ERR_INVALID_ARG, "gated recurrence: negative size");
-    constexpr int64_t kMost = (int64_t)1 << 40;
-    if (c->T > ((int64_t)1 << 30) || (c->B && c->N > kMost / c->B) ||
-        (c->T && c->B && c->N && c->B * c->N > kMost / c->T))
-        return fail(CK_ERR_UNSUPPORTED, "gated recurrence: more than 2^40 elements or 2^30 steps");
+    const ck_status st = check_gated_sizes(c->T, c->B, c->N);
+    if (st != CK_OK) return st;
     if (c->B == 0 || c->N == 0) return CK_OK;
     const size_t e = dtype_size(c->dtype);
     const bool some = c->T > 0;
@@ -458,21 +769,44 @@ ck_status check_gated(const ck_gated_call *c, bool backward) {
     return CK_OK;
 }
 
-template <typename T, int V, bool LEAK>
+template <auto KERNEL>
+cudaError_t launch_one(dim3 grid, dim3 block, int smem, bool early, const GatedArgs &a, cudaStream_t s) {
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = smem > 32 * 1024 ? allow_smem((const void *)KERNEL, kMostSmem, done) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, KERNEL, a);
+}
+
+template <typename T, int V, bool LEAK, bool SHIFTED>
 cudaError_t launch_gated(GatedArgs a, const GatedPlan &p, bool backward, cudaStream_t s) {
     a.wt = p.wt;
     a.wc = p.wc;
-    a.tiles = p.tiles;
-    a.chunk_tiles = p.chunk_tiles;
-    const dim3 grid((unsigned)p.blocks, (unsigned)p.chunks), block(32 * p.wt * p.wc);
+    a.blocks = p.blocks;
+    a.parts = p.wt * p.chunks;
+    const dim3 grid((unsigned)p.grid, (unsigned)p.chunks), block(32 * p.wt * p.wc);
+    a.exchange = p.wt > 1 ? (int)sizeof(Exchange<V>) : 0;
+    const int warps = p.wt * p.wc, two = p.chunks > 1;
+    cudaError_t e = cudaSuccess;
     if (!backward) {
-        if (p.chunks > 1) k_gated_forward<T, V, LEAK, true><<<grid, block, 0, s>>>(a);
-        k_gated_forward<T, V, LEAK, false><<<grid, block, 0, s>>>(a);
+        constexpr int kBytes = ForwardRing<T, V, SHIFTED>::kBytes;
+        if (two) e = launch_one<k_gated_forward<T, V, LEAK, SHIFTED, true>>(grid, block, a.exchange + warps * kBytes, false, a, s);
+        if (e == cudaSuccess) e = launch_one<k_gated_forward<T, V, LEAK, SHIFTED, false>>(grid, block, a.exchange + warps * kBytes, two, a, s);
     } else {
-        if (p.chunks > 1) k_gated_backward<T, V, LEAK, true><<<grid, block, 0, s>>>(a);
-        k_gated_backward<T, V, LEAK, false><<<grid, block, 0, s>>>(a);
+        constexpr int kBytes = BackwardRing<T, V, SHIFTED, false>::kBytes, kMapBytes = BackwardRing<T, V, SHIFTED, true>::kBytes;
+        if (two) e = launch_one<k_gated_backward<T, V, LEAK, SHIFTED, true>>(grid, block, a.exchange + warps * kMapBytes, false, a, s);
+        if (e == cudaSuccess) e = launch_one<k_gated_backward<T, V, LEAK, SHIFTED, false>>(grid, block, a.exchange + warps * kBytes, two, a, s);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 ck_status run_gated(const ck_gated_call *c, bool backward, cudaStream_t s) {
@@ -496,22 +830,47 @@ ck_status run_gated(const ck_gated_call *c, bool backward, cudaStream_t s) {
     a.out = c->out, a.state = c->state, a.kept = c->kept;
     a.dx = c->dx, a.dgate = c->dgate, a.dstate0 = c->d_state0;
     const size_t e = dtype_size(c->dtype);
-    const bool pairs = in_pairs(a.x, a.xt, a.xb, c->B, c->N, c->T, e) && in_pairs(a.gate, a.gt, a.gb, c->B, c->N, c->T, e) &&
-                       (!a.dout || in_pairs(a.dout, a.dt, a.db, c->B, c->N, c->T, e)) && aligned(a.out, 2 * e) &&
-                       aligned(a.dx, 2 * e) && aligned(a.dgate, 2 * e) && C % 2 == 0;
-    const GatedPlan p = gated_plan(c->T, C, pairs ? 2 : 1, device_sms());
-    if (p.blocks > 0x7fffffff || p.chunks > 65535) return fail(CK_ERR_UNSUPPORTED, "gated recurrence: too many nodes");
+    // What a lane copies at once (at most 16 bytes), and the elements of a thread (at most 2)
+    const auto takes = [&](int n) {
+        return in_packs(a.x, n, a.xt, a.xb, c->B, c->N, c->T, e) && in_packs(a.gate, n, a.gt, a.gb, c->B, c->N, c->T, e) &&
+               (!a.dout || in_packs(a.dout, n, a.dt, a.db, c->B, c->N, c->T, e));
+    };
+    a.copy = 16;
+    while (a.copy > (int)e && !takes(a.copy / (int)e)) a.copy /= 2;
+    const bool pairs = C % 2 == 0 && aligned(a.out, 2 * e) && aligned(a.dx, 2 * e) && aligned(a.dgate, 2 * e);
+    // Rows that 8 bytes cannot be copied of, but that hold all sequences one after another and
+    // begin alike in all tensors, are taken as they lie (500 x 3 x 4,999 fp32, both directions:
+    // 83 us).  With 8 bytes the plain copies are faster: 96 x 20 x 4,999 fp16 takes 42 us so and
+    // 55 shifted, the shifts costing instructions.
+    const auto like_x = [&](const void *p, int64_t st, int64_t sb) {
+        return ((uintptr_t)p - (uintptr_t)a.x) % 16 == 0 && (c->T == 1 || (st - a.xt) * (int64_t)e % 16 == 0) && (c->B == 1 || sb == c->N);
+    };
+    const bool shifted = (a.copy < 8 || !pairs) && like_x(a.x, a.xt, a.xb) && like_x(a.gate, a.gt, a.gb) &&
+                         (!a.dout || like_x(a.dout, a.dt, a.db));
+    if (shifted) a.copy = 16;
+    a.apart = !pairs;
+    const int V = shifted || (pairs && a.copy >= 2 * (int)e) ? 2 : 1;
+    const GatedPlan p = gated_plan(c->T, C, V, device_sms());
+    if (p.grid > 0x7fffffff || p.chunks > 65535) return fail(CK_ERR_UNSUPPORTED, "gated recurrence: too many nodes");
     if (p.chunks > 1) {
-        const size_t need = (size_t)p.chunks * C * sizeof(float2);
+        const size_t need = maps_bytes(p, C);
         if (!c->workspace || (size_t)c->workspace_bytes < need)
             return fail(CK_ERR_WORKSPACE, "gated recurrence: a workspace of %zu bytes is needed", need);
         a.maps = (float2 *)c->workspace;
+        a.inner = a.maps + (int64_t)p.chunks * C;
     }
     const cudaError_t err = with_dtype(c->dtype, [&](auto *tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
-        if (c->form == CK_GATED_LEAK)
-            return pairs ? launch_gated<T, 2, true>(a, p, backward, s) : launch_gated<T, 1, true>(a, p, backward, s);
-        return pairs ? launch_gated<T, 2, false>(a, p, backward, s) : launch_gated<T, 1, false>(a, p, backward, s);
+        const auto go = [&](auto width, auto rows) {
+            constexpr int W = decltype(width)::value;
+            constexpr bool S = decltype(rows)::value;
+            return c->form == CK_GATED_LEAK ? launch_gated<T, W, true, S>(a, p, backward, s)
+                                            : launch_gated<T, W, false, S>(a, p, backward, s);
+        };
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        if (shifted) return go(Two(), std::true_type());
+        return V == 2 ? go(Two(), std::false_type()) : go(One(), std::false_type());
     });
     return err == cudaSuccess ? CK_OK : cuda_fail(err, "k_gated launch");
 }
@@ -522,19 +881,17 @@ ck_status run_gated(const ck_gated_call *c, bool backward, cudaStream_t s) {
 using namespace ck;
 
 extern "C" ck_status ck_gated_sizes(int64_t T, int64_t B, int64_t N, size_t *kept_bytes, size_t *workspace_bytes) {
-    if (T < 0 || B < 0 || N < 0) return fail(CK_ERR_INVALID_ARG, "gated recurrence: negative size");
+    const ck_status st = check_gated_sizes(T, B, N);
+    if (st != CK_OK) return st;
     if (!kept_bytes || !workspace_bytes) return fail(CK_ERR_INVALID_ARG, "a required pointer is NULL");
     *kept_bytes = *workspace_bytes = 0;
-    constexpr int64_t kMost = (int64_t)1 << 40;
-    if (T > ((int64_t)1 << 30) || (B && N > kMost / B) || (T && B && N && B * N > kMost / T))
-        return fail(CK_ERR_UNSUPPORTED, "gated recurrence: more than 2^40 elements or 2^30 steps");
     const int64_t C = B * N;
     if (C == 0 || T == 0) return CK_OK;
     *kept_bytes = (size_t)((T + kSteps - 1) / kSteps) * C * 4;
-    // of the widths that the alignment may leave, the one with more chunks
+    // of the widths that the alignment may leave, the one with most chunks
     for (int V = 1; V <= 2; ++V) {
         const GatedPlan p = gated_plan(T, C, V, device_sms());
-        const size_t need = p.chunks > 1 ? (size_t)p.chunks * C * sizeof(float2) : 0;
+        const size_t need = p.chunks > 1 ? maps_bytes(p, C) : 0;
         if (need > *workspace_bytes) *workspace_bytes = need;
     }
     return CK_OK;

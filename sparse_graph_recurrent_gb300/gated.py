@@ -104,7 +104,7 @@ def _forward(x, gate, state0, lengths, form, keep):
 
 def gated_recurrence_forward(x, gate, state0=None, lengths=None, form: str = "leak"):
     """gated_recurrence without autograd: (out, state, kept), kept for
-    gated_recurrence_backward (32-bit states at every 16th step)."""
+    gated_recurrence_backward (32-bit states at every 8th step)."""
     got = (_ck._native or _ck.native()).gated(x, gate, state0, lengths, form, True)
     if got is not None:
         return got
