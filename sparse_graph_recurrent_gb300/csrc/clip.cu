@@ -12,12 +12,15 @@
 // The list of tensors is an argument of the kernels: nothing is copied, and a captured
 // call holds it.
 //
-// Squares leave the range of 32 bits long before numbers do.  So three sums are kept: of
-// g^2, of (g 2^-80)^2 for when that overflows and of (g 2^64)^2 for when it is so small
-// that squares were lost.
+// Squares leave the range of 32 bits long before numbers do.  Where a CTA's sum says that they
+// have, it adds up its run again with numbers scaled by a power of 2; the sums of CTAs are
+// of 64 bits.
 //
 // What bounds both is memory: the gradients are read twice and written once, except what L2
-// holds from the first time.
+// holds from the first time.  207 MB out of place: 36 us for the norm (5.8 TB/s) and 64 for the
+// scaling (6.4 TB/s).  Operations of 64 bits are slow here (a warp's takes an SM some 20
+// cycles); with one for every thread, three sums and their reductions, they took 11 and 18 us
+// of the two kernels, so one warp of a CTA does the few that there are.
 #include <algorithm>
 #include <vector>
 
@@ -30,10 +33,9 @@ constexpr int kClipThreads = 256, kClipVecs = 4;
 constexpr int kChunkBytes = kClipThreads * kClipVecs * 16;
 constexpr int kFew = 32, kMany = 1000;  // tensors of a launch: the arguments then take 1 and 29 KB
 constexpr int kClipCtas = 4;            // CTAs an SM
-
-struct Sums {
-    float mid, big, small;
-};
+// What the second kernel finds in L2 of what the first has read, where that marks the rest as
+// not to be held (79 M numbers, 207 MB: 100.4 us, 105.2 with all marked, 103.2 with none).
+constexpr int kHeldBytes = 80 << 20;
 
 template <int MOST> struct ClipList {
     const void *in[MOST];
@@ -42,11 +44,12 @@ template <int MOST> struct ClipList {
     int32_t start[MOST + 1];  // the tensor's first chunk
     uint8_t dtype[MOST];
     int count;
-    double *sums;    // [CTAs of all launches][3]
+    double *sums;    // [CTAs of all launches]
     int first;       // the CTAs of the launches before
     int all;         // of all launches
     float *norm;
     double max_norm;
+    int held;        // chunks that the second kernel finds in L2
 };
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -55,9 +58,8 @@ __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.laun
 // Where chunk c lies: the tensor, and elements [lo, hi) of it.  Chunks begin at multiples of
 // 16 bytes in memory; what lies before the first such place belongs to the first chunk.
 struct Where {
-    int i;
-    int64_t lo, hi;
-    int head;  // elements before the first multiple of 16 bytes
+    int i, vecs;         // pieces of 16 bytes, from element `body` on
+    int64_t lo, body, hi;
 };
 
 template <typename L> __device__ __forceinline__ Where locate(const L &a, int c, int from) {
@@ -71,155 +73,35 @@ template <typename L> __device__ __forceinline__ Where locate(const L &a, int c,
     }
     Where w;
     w.i = lo;
-    const int e = a.dtype[lo] == CK_F32 ? 4 : 2;
-    const int64_t per = kChunkBytes / e, k = c - a.start[lo], n = a.n[lo];
-    w.head = (int)((16 - ((uintptr_t)a.in[lo] & 15)) & 15) / e;
-    if (w.head > n) w.head = (int)n;
-    w.lo = k ? w.head + k * per : 0;
-    w.hi = w.head + (k + 1) * per;
+    const int shift = a.dtype[lo] == CK_F32 ? 2 : 1;  // bytes of an element, as a power of 2
+    const int64_t k = c - a.start[lo], n = a.n[lo];
+    int head = (int)((16 - ((uintptr_t)a.in[lo] & 15)) & 15) >> shift;
+    if (head > n) head = (int)n;
+    w.body = head + k * (kChunkBytes >> shift);
+    w.lo = k ? w.body : 0;
+    w.hi = head + (k + 1) * (kChunkBytes >> shift);
     if (w.hi > n) w.hi = n;
+    w.vecs = (int)((w.hi - w.body) >> (4 - shift));
     return w;
 }
 
-template <typename T> struct Scaled {
-    // Only where a type's squares may leave 32 bits.
-    static constexpr bool kThree = !std::is_same<T, __half>::value;
-};
-
-template <typename T> __device__ __forceinline__ void add_square(Sums &s, T g) {
-    const float v = to_float(g);
-    s.mid = fmaf(v, v, s.mid);
-    if constexpr (Scaled<T>::kThree) {
-        const float b = v * 8.271806125530277e-25f, t = v * 1.8446744073709552e19f;
-        s.big = fmaf(b, b, s.big);
-        s.small = fmaf(t, t, s.small);
-    }
-}
-
-template <typename T> __device__ __forceinline__ void chunk_sum(const T *in, const Where &w, Sums &total) {
-    constexpr int E = 16 / (int)sizeof(T);
-    const int64_t body = w.lo > w.head ? w.lo : w.head;  // a multiple of 16 bytes in memory
-    const int64_t vecs = (w.hi - body) / E;
-    const uint4 *p = (const uint4 *)(in + body);
-    uint4 v[kClipVecs];
+// This thread's pieces of a chunk, kClipVecs of them or fewer.
+// last: nothing reads them after this, soon enough to find them in L2.
+template <typename L> __device__ __forceinline__ void chunk_load(const L &a, const Where &w, bool last, uint4 (&v)[kClipVecs]) {
+    const uint4 *p = (const uint4 *)((const char *)a.in[w.i] + (w.body << (a.dtype[w.i] == CK_F32 ? 2 : 1))) + threadIdx.x;
+    if (last && w.vecs == kClipThreads * kClipVecs) {
 #pragma unroll
-    for (int j = 0; j < kClipVecs; ++j)
-        if (threadIdx.x + j * kClipThreads < vecs) v[j] = __ldg(p + threadIdx.x + j * kClipThreads);
-    Sums s{0.f, 0.f, 0.f};
+        for (int j = 0; j < kClipVecs; ++j) v[j] = __ldcs(p + j * kClipThreads);
+    } else if (w.vecs == kClipThreads * kClipVecs) {
 #pragma unroll
-    for (int j = 0; j < kClipVecs; ++j) {
-        if (threadIdx.x + j * kClipThreads >= vecs) continue;
-        alignas(16) T t[E];
-        memcpy(t, &v[j], 16);
+        for (int j = 0; j < kClipVecs; ++j) v[j] = __ldg(p + j * kClipThreads);
+    } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) add_square(s, t[e]);
-    }
-    if (w.lo + threadIdx.x < body) add_square(s, in[w.lo + threadIdx.x]);
-    const int64_t tail = body + vecs * E + threadIdx.x;
-    if (tail < w.hi) add_square(s, in[tail]);
-    total.mid += s.mid;
-    total.big += s.big;
-    total.small += s.small;
-    if constexpr (!Scaled<T>::kThree) {
-        if (!(s.mid <= 3.402823466e38f)) total.big += s.mid;  // infinities and NaN
-    }
-}
-
-__device__ __forceinline__ double block_sum(double v, double *shared) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double t = 0;
-#pragma unroll
-    for (int i = 0; i < kClipThreads / 32; ++i) t += shared[i];
-    __syncthreads();
-    return t;
-}
-
-__device__ __forceinline__ void run_of(int chunks, int &lo, int &hi) {
-    lo = (int)((int64_t)chunks * blockIdx.x / gridDim.x);
-    hi = (int)((int64_t)chunks * (blockIdx.x + 1) / gridDim.x);
-}
-
-template <int MOST> __global__ void __launch_bounds__(kClipThreads) k_norm(const __grid_constant__ ClipList<MOST> a) {
-    __shared__ double shared[kClipThreads / 32];
-    pdl_launch();
-    int lo, hi, i = 0;
-    run_of(a.start[a.count], lo, hi);
-    Sums s{0.f, 0.f, 0.f};
-    for (int c = lo; c < hi; ++c) {
-        const Where w = locate(a, c, i);
-        i = w.i;
-        if (a.dtype[i] == CK_F32)
-            chunk_sum((const float *)a.in[i], w, s);
-        else if (a.dtype[i] == CK_BF16)
-            chunk_sum((const __nv_bfloat16 *)a.in[i], w, s);
-        else
-            chunk_sum((const __half *)a.in[i], w, s);
-    }
-    const double mid = block_sum(s.mid, shared), big = block_sum(s.big, shared), small = block_sum(s.small, shared);
-    if (threadIdx.x == 0) {
-        double *to = a.sums + 3 * (a.first + blockIdx.x);
-        to[0] = mid, to[1] = big, to[2] = small;
-    }
-}
-
-// The norm from all CTAs' sums.
-__device__ __forceinline__ float norm_of(const double *sums, int all, double *shared) {
-    double mid = 0, big = 0, small = 0;
-    for (int i = threadIdx.x; i < all; i += kClipThreads) {
-        mid += __ldcg(sums + 3 * i);
-        big += __ldcg(sums + 3 * i + 1);
-        small += __ldcg(sums + 3 * i + 2);
-    }
-    mid = block_sum(mid, shared), big = block_sum(big, shared), small = block_sum(small, shared);
-    if (!(mid <= 1.7976931348623157e308)) return (float)(sqrt(big) * 1.2089258196146292e24);  // 2^80; inf and NaN too
-    if (mid < 8.67e-19) return (float)(sqrt(small) * 5.421010862427522e-20);                   // 2^-60, 2^-64
-    return (float)sqrt(mid);
-}
-
-template <int MOST> __global__ void __launch_bounds__(kClipThreads) k_norm_end(const __grid_constant__ ClipList<MOST> a) {
-    __shared__ double shared[kClipThreads / 32];
-    pdl_wait();
-    const float n = norm_of(a.sums, a.all, shared);
-    if (threadIdx.x == 0) *a.norm = n;
-}
-
-template <typename T>
-__device__ __forceinline__ void chunk_load(const T *in, const Where &w, uint4 (&v)[kClipVecs]) {
-    constexpr int E = 16 / (int)sizeof(T);
-    const int64_t body = w.lo > w.head ? w.lo : w.head, vecs = (w.hi - body) / E;
-    const uint4 *p = (const uint4 *)(in + body);
-#pragma unroll
-    for (int j = 0; j < kClipVecs; ++j)
-        if (threadIdx.x + j * kClipThreads < vecs) v[j] = p[threadIdx.x + j * kClipThreads];
-}
-
-template <typename T>
-__device__ __forceinline__ void chunk_scale(const T *in, T *out, const Where &w, uint4 (&v)[kClipVecs], float factor) {
-    constexpr int E = 16 / (int)sizeof(T);
-    const int64_t body = w.lo > w.head ? w.lo : w.head, vecs = (w.hi - body) / E;
-    const bool wide = ((uintptr_t)(out + body) & 15) == 0;
-#pragma unroll
-    for (int j = 0; j < kClipVecs; ++j) {
-        if (threadIdx.x + j * kClipThreads >= vecs) continue;
-        alignas(16) T t[E];
-        memcpy(t, &v[j], 16);
-#pragma unroll
-        for (int e = 0; e < E; ++e) t[e] = from_float<T>(to_float(t[e]) * factor);
-        T *to = out + body + (threadIdx.x + j * kClipThreads) * E;
-        if (wide) {
-            memcpy(&v[j], t, 16);
-            __stcs((uint4 *)to, v[j]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) to[e] = t[e];
+        for (int j = 0; j < kClipVecs; ++j) {
+            v[j] = make_uint4(0, 0, 0, 0);
+            if ((int)threadIdx.x + j * kClipThreads < w.vecs) v[j] = __ldg(p + j * kClipThreads);
         }
     }
-    const int64_t head = w.lo + threadIdx.x, tail = body + vecs * E + threadIdx.x;
-    if (head < body) out[head] = from_float<T>(to_float(in[head]) * factor);
-    if (tail < w.hi) out[tail] = from_float<T>(to_float(in[tail]) * factor);
 }
 
 // f((T *)nullptr) with T the element type.
@@ -232,32 +114,199 @@ template <typename F> __device__ __forceinline__ void by_dtype(uint8_t d, F &&f)
         f((__half *)nullptr);
 }
 
-template <int MOST> __global__ void __launch_bounds__(kClipThreads) k_clip(const __grid_constant__ ClipList<MOST> a) {
-    __shared__ double shared[kClipThreads / 32];
+// The sum of this thread's squares in a chunk.
+template <typename T> __device__ __forceinline__ float chunk_sum(const T *in, const Where &w, const uint4 (&v)[kClipVecs]) {
+    constexpr int E = 16 / (int)sizeof(T);
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < kClipVecs; ++j) {
+        alignas(16) T t[E];
+        memcpy(t, &v[j], 16);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s = fmaf(to_float(t[e]), to_float(t[e]), s);
+    }
+    const int64_t edge = w.lo + threadIdx.x, tail = w.body + w.vecs * E + threadIdx.x;
+    if (edge < w.body) s = fmaf(to_float(in[edge]), to_float(in[edge]), s);
+    if (tail < w.hi) s = fmaf(to_float(in[tail]), to_float(in[tail]), s);
+    return s;
+}
+
+// The sum of the warps' numbers, in the first warp.  (A warp's operation of 64 bits takes some
+// 20 cycles of its SM, so one warp adds them up: 13 of them, not 100.)
+__device__ __forceinline__ double block_sum(double v, double *shared) {
+    shared[threadIdx.x] = v;
+    __syncthreads();
+    double t = 0;
+    if (threadIdx.x < 32) {
+#pragma unroll
+        for (int i = 0; i < kClipThreads / 32; ++i) t += shared[threadIdx.x + 32 * i];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    return t;
+}
+
+__device__ __forceinline__ void run_of(int chunks, int &lo, int &hi) {
+    lo = (int)((int64_t)chunks * blockIdx.x / gridDim.x);
+    hi = (int)((int64_t)chunks * (blockIdx.x + 1) / gridDim.x);
+}
+
+// The same of a run's numbers each times a power of 2, in the first warp: for the few runs
+// that need it, one by one.
+template <int MOST> __device__ __noinline__ double scaled_sum(const ClipList<MOST> &a, int lo, int hi, float scale, double *shared) {
+    float s = 0.f;
+    for (int c = lo; c < hi; ++c) {
+        const Where w = locate(a, c, 0);
+        by_dtype(a.dtype[w.i], [&](auto *t) {
+            const auto *in = (const std::remove_pointer_t<decltype(t)> *)a.in[w.i];
+            float part = 0.f;
+            for (int64_t e = w.lo + threadIdx.x; e < w.hi; e += kClipThreads) {
+                const float g = to_float(in[e]) * scale;
+                part = fmaf(g, g, part);
+            }
+            s += part;
+        });
+    }
+    __syncthreads();
+    return block_sum(s, shared) / ((double)scale * (double)scale);
+}
+
+template <int MOST>
+__global__ void __launch_bounds__(kClipThreads, kClipCtas) k_norm(const __grid_constant__ ClipList<MOST> a) {
+    __shared__ double shared[kClipThreads];
+    __shared__ double sum;
+    pdl_launch();
     int lo, hi;
     run_of(a.start[a.count], lo, hi);
-    uint4 v[kClipVecs];
-    Where w{};
-    auto load = [&]() {
-        by_dtype(a.dtype[w.i], [&](auto *t) { chunk_load((const std::remove_pointer_t<decltype(t)> *)a.in[w.i], w, v); });
-    };
+    // what this run has in L2 at the end, if all do likewise
+    const int keep = hi - (int)(a.held / gridDim.x);
+    float part = 0.f;
+    // a chunk ahead is under way while one is added up
+    uint4 v[kClipVecs], next[kClipVecs];
+    Where w{}, then{};
+    if (hi > lo) {
+        w = locate(a, lo, 0);
+        chunk_load(a, w, lo < keep, v);
+    }
+    for (int c = lo; c < hi; ++c) {
+        if (c + 1 < hi) {
+            then = locate(a, c + 1, w.i);
+            chunk_load(a, then, c + 1 < keep, next);
+        }
+        by_dtype(a.dtype[w.i], [&](auto *t) { part += chunk_sum((const std::remove_pointer_t<decltype(t)> *)a.in[w.i], w, v); });
+        w = then;
+#pragma unroll
+        for (int j = 0; j < kClipVecs; ++j) v[j] = next[j];
+    }
+    double s = block_sum(part, shared);
+    if (threadIdx.x == 0) sum = s;
+    __syncthreads();
+    // Squares that left 32 bits, or may have been lost below them beside what is left: once more,
+    // of numbers made smaller, or larger.
+    if (!(sum <= 3.402823466e38f))
+        s = scaled_sum(a, lo, hi, 8.271806125530277e-25f, shared);  // 2^-80
+    else if (sum < 8.67e-19)  // 2^-60
+        s = scaled_sum(a, lo, hi, 1.8446744073709552e19f, shared);  // 2^64
+    if (threadIdx.x == 0) a.sums[a.first + blockIdx.x] = s;
+}
+
+// The root of a number that is not negative, rounded to 32 bits: of its first 24 bits, and what
+// the rest adds.  (The root of 64 bits takes some 30 of the slow operations.)
+__device__ __forceinline__ float root(double s) {
+    if (!(s > 0) || !(s <= 1.7976931348623157e308)) return (float)s;  // 0, infinite, NaN
+    const long long bits = __double_as_longlong(s);
+    const int half = ((int)(bits >> 52) - 1023) >> 1;                // (s is no subnormal: it is a square over 2^-298)
+    const double m = __longlong_as_double(bits - ((long long)(2 * half) << 52));  // in [1, 4)
+    const float y = sqrtf((float)m);
+    return ldexpf(y + (float)(m - (double)y * (double)y) / (2.f * y), half);
+}
+
+// The norm from all CTAs' sums and what the gradients are multiplied with, in all threads.
+struct Factor {
+    float norm, by;
+};
+__device__ __forceinline__ Factor factor_of(const double *sums, int all, double max_norm) {
+    __shared__ Factor f;
+    if (threadIdx.x < 32) {
+        double s = 0;
+        for (int i = threadIdx.x; i < all; i += 32) s += __ldcg(sums + i);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) {
+            f.norm = root(s);
+            // max_norm / (norm + 1e-6), rounded once but for what a 32-bit quotient's rest loses
+            const double d = (double)f.norm + 1e-6;
+            if (max_norm >= d) {
+                f.by = 1.f;
+            } else {
+                const float q = (float)max_norm / (float)d;
+                f.by = f.norm <= 3.402823466e38f ? q + (float)(max_norm - (double)q * d) / (float)d : q;  // (NaN stays)
+            }
+        }
+    }
+    __syncthreads();
+    return f;
+}
+
+template <int MOST> __global__ void __launch_bounds__(kClipThreads) k_norm_end(const __grid_constant__ ClipList<MOST> a) {
+    pdl_wait();
+    const Factor f = factor_of(a.sums, a.all, 0);
+    if (threadIdx.x == 0) *a.norm = f.norm;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T *in, T *out, const Where &w, uint4 (&v)[kClipVecs], float factor) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const bool wide = ((uintptr_t)(out + w.body) & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < kClipVecs; ++j) {
+        if ((int)threadIdx.x + j * kClipThreads >= w.vecs) continue;
+        alignas(16) T t[E];
+        memcpy(t, &v[j], 16);
+#pragma unroll
+        for (int e = 0; e < E; ++e) t[e] = from_float<T>(to_float(t[e]) * factor);
+        T *to = out + w.body + (threadIdx.x + j * kClipThreads) * E;
+        if (wide) {
+            memcpy(&v[j], t, 16);
+            __stcs((uint4 *)to, v[j]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) to[e] = t[e];
+        }
+    }
+    const int64_t head = w.lo + threadIdx.x, tail = w.body + w.vecs * E + threadIdx.x;
+    if (head < w.body) out[head] = from_float<T>(to_float(in[head]) * factor);
+    if (tail < w.hi) out[tail] = from_float<T>(to_float(in[tail]) * factor);
+}
+
+template <int MOST>
+__global__ void __launch_bounds__(kClipThreads, kClipCtas) k_clip(const __grid_constant__ ClipList<MOST> a) {
+    int lo, hi;
+    run_of(a.start[a.count], lo, hi);
+    // a chunk ahead is under way while one is scaled
+    uint4 v[kClipVecs], next[kClipVecs];
+    Where w{}, then{};
     if (hi > lo) {
         w = locate(a, hi - 1, 0);
-        load();
+        chunk_load(a, w, true, v);
     }
     pdl_wait();
-    const float norm = norm_of(a.sums, a.all, shared);
-    const float f = (float)(a.max_norm / ((double)norm + 1e-6));
-    const float factor = f >= 1.f ? 1.f : f;  // (NaN stays)
-    if (blockIdx.x == 0 && a.first == 0 && threadIdx.x == 0) *a.norm = norm;
+    const Factor all = factor_of(a.sums, a.all, a.max_norm);
+    const float factor = all.by;
+    if (blockIdx.x == 0 && a.first == 0 && threadIdx.x == 0) *a.norm = all.norm;
     for (int c = hi - 1; c >= lo; --c) {
-        if (c < hi - 1) w = locate(a, c, 0);
-        if (factor == 1.f && a.in[w.i] == a.out[w.i]) continue;
-        if (c < hi - 1) load();
-        by_dtype(a.dtype[w.i], [&](auto *t) {
-            using T = std::remove_pointer_t<decltype(t)>;
-            chunk_scale((const T *)a.in[w.i], (T *)a.out[w.i], w, v, factor);
-        });
+        if (c > lo) {
+            then = locate(a, c - 1, 0);
+            if (factor != 1.f || a.in[then.i] != a.out[then.i]) chunk_load(a, then, true, next);
+        }
+        if (factor != 1.f || a.in[w.i] != a.out[w.i])
+            by_dtype(a.dtype[w.i], [&](auto *t) {
+                using T = std::remove_pointer_t<decltype(t)>;
+                chunk_scale((const T *)a.in[w.i], (T *)a.out[w.i], w, v, factor);
+            });
+        w = then;
+#pragma unroll
+        for (int j = 0; j < kClipVecs; ++j) v[j] = next[j];
     }
 }
 
@@ -281,29 +330,76 @@ ck_status check_list(const ck_gradient *list, int64_t count, bool clip) {
     return CK_OK;
 }
 
+size_t clip_workspace(const ck_gradient *list, int64_t count) {
+    // a sum for each CTA of a launch; a launch ends at kMany tensors or 2^31 chunks
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < count; ++i)
+        if (list[i].n) chunks += chunks_of(list[i]);
+    const int64_t launches = 1 + count / kMany + chunks / ((int64_t)1 << 30);
+    const int64_t most = launches * kClipCtas * device_sms();
+    return (size_t)(chunks < most ? chunks : most) * sizeof(double);
+}
+
 struct Span {
     uintptr_t lo, hi;
     bool written;
 };
 
+bool by_begin(const Span &a, const Span &b) { return a.lo < b.lo; }
+
 // Whether what one tensor writes is read or written for another.  A tensor clipped in its
-// own place is one span.
+// own place is one span.  What is written is looked at by itself first, by type: it often
+// lies in the order of the list, one line of memory for a type, and what is read elsewhere.
 bool tangled(const ck_gradient *list, int64_t count) {
-    std::vector<Span> spans;
-    spans.reserve(2 * (size_t)count);
+    std::vector<Span> written[3], all;
+    uintptr_t lo = UINTPTR_MAX, hi = 0, read_lo = UINTPTR_MAX, read_hi = 0;
     for (int64_t i = 0; i < count; ++i) {
         const ck_gradient &g = list[i];
         if (!g.n) continue;
-        const uintptr_t bytes = (uintptr_t)g.n * dtype_size(g.dtype);
-        spans.push_back({(uintptr_t)g.out, (uintptr_t)g.out + bytes, true});
-        if (g.out != g.grad) spans.push_back({(uintptr_t)g.grad, (uintptr_t)g.grad + bytes, false});
+        const uintptr_t bytes = (uintptr_t)g.n * dtype_size(g.dtype), to = (uintptr_t)g.out, from = (uintptr_t)g.grad;
+        written[g.dtype].push_back({to, to + bytes, true});
+        lo = std::min(lo, to), hi = std::max(hi, to + bytes);
+        if (to != from) read_lo = std::min(read_lo, from), read_hi = std::max(read_hi, from + bytes);
     }
-    const auto before = [](const Span &a, const Span &b) { return a.lo < b.lo; };
-    if (!std::is_sorted(spans.begin(), spans.end(), before)) std::sort(spans.begin(), spans.end(), before);
-    uintptr_t written = 0, read = 0;
-    for (const Span &s : spans) {
-        if (s.lo < written || (s.written && s.lo < read)) return true;
-        uintptr_t &end = s.written ? written : read;
+    for (std::vector<Span> &spans : written) {
+        if (!std::is_sorted(spans.begin(), spans.end(), by_begin)) std::sort(spans.begin(), spans.end(), by_begin);
+        const size_t before = all.size();
+        all.insert(all.end(), spans.begin(), spans.end());
+        if (before && before < all.size() && all[before].lo < all[before - 1].lo)
+            std::inplace_merge(all.begin(), all.begin() + before, all.end(), by_begin);
+    }
+    // What is read: mostly far from the few stretches that are written
+    std::vector<Span> stretches;
+    for (const Span &s : all) {
+        if (!stretches.empty() && s.lo <= stretches.back().hi + 4096)
+            stretches.back().hi = std::max(stretches.back().hi, s.hi);
+        else
+            stretches.push_back(s);
+    }
+    bool near = read_lo < hi && read_hi > lo;  // (nothing read: false)
+    if (near && stretches.size() <= 8) {
+        near = false;
+        for (int64_t i = 0; i < count && !near; ++i) {
+            const ck_gradient &g = list[i];
+            const uintptr_t from = (uintptr_t)g.grad, end = from + (uintptr_t)g.n * dtype_size(g.dtype);
+            if (g.n && g.out != g.grad)
+                for (const Span &s : stretches) near |= from < s.hi && end > s.lo;
+        }
+    }
+    if (near) {
+        const size_t before = all.size();
+        for (int64_t i = 0; i < count; ++i) {
+            const ck_gradient &g = list[i];
+            const uintptr_t from = (uintptr_t)g.grad;
+            if (g.n && g.out != g.grad) all.push_back({from, from + (uintptr_t)g.n * dtype_size(g.dtype), false});
+        }
+        std::sort(all.begin() + before, all.end(), by_begin);
+        std::inplace_merge(all.begin(), all.begin() + before, all.end(), by_begin);
+    }
+    uintptr_t end_written = 0, end_read = 0;
+    for (const Span &s : all) {
+        if (s.lo < end_written || (s.written && s.lo < end_read)) return true;
+        uintptr_t &end = s.written ? end_written : end_read;
         end = std::max(end, s.hi);
     }
     return false;
@@ -355,6 +451,7 @@ ck_status run_clip(const ck_gradient *list, int64_t count, bool clip, double max
     a.norm = norm;
     a.max_norm = max_norm;
     a.all = a.first = 0;
+    a.held = kHeldBytes / kChunkBytes;
     cudaError_t e = cudaSuccess;
     int launches = 0;
     for (int64_t at = 0; at < count && e == cudaSuccess;) {
@@ -396,9 +493,7 @@ ck_status clip_call(const ck_gradient *list, int64_t count, bool clip, double ma
     if (clip && !(max_norm >= 0)) return fail(CK_ERR_INVALID_ARG, "gradients: max_norm must be a number of at least 0");
     if (!aligned(norm, 4) || !aligned(workspace, 8))
         return fail(CK_ERR_INVALID_ARG, "gradients: a pointer is not aligned to its elements");
-    size_t need = 0;
-    st = ck_clip_workspace_size(list, count, &need);
-    if (st != CK_OK) return st;
+    const size_t need = clip_workspace(list, count);
     if (need && (!workspace || (size_t)workspace_bytes < need))
         return fail(CK_ERR_WORKSPACE, "gradients: a workspace of %zu bytes is needed", need);
     if (clip) {
@@ -422,13 +517,7 @@ extern "C" ck_status ck_clip_workspace_size(const ck_gradient *list, int64_t cou
     const ck_status st = check_list(list, count, false);
     if (st != CK_OK) return st;
     if (!bytes) return fail(CK_ERR_INVALID_ARG, "a required pointer is NULL");
-    // three sums for each CTA of a launch; a launch ends at kMany tensors or 2^31 chunks
-    int64_t chunks = 0;
-    for (int64_t i = 0; i < count; ++i)
-        if (list[i].n) chunks += chunks_of(list[i]);
-    const int64_t launches = 1 + count / kMany + chunks / ((int64_t)1 << 30);
-    const int64_t most = launches * kClipCtas * device_sms();
-    *bytes = (size_t)(chunks < most ? chunks : most) * 3 * sizeof(double);
+    *bytes = clip_workspace(list, count);
     return CK_OK;
 }
 
