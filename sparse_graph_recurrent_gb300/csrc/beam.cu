@@ -162,7 +162,7 @@ template <> struct Pieces<__half> : Halves<__half, __half2> {
     static __device__ __forceinline__ uint32_t clean(uint32_t w) { return larger(w, kNothing); }
 };
 
-template <typename T> __global__ void __launch_bounds__(kBeamThreads, 4) k_beam_slices(const __grid_constant__ BeamArgs a) {
+template <typename T> __device__ __forceinline__ void beam_slice(const BeamArgs &a, int slice, int64_t k, int64_t b) {
     using P = Pieces<T>;
     constexpr int E = P::E;
     __shared__ float maxima[kBeamThreads];
@@ -171,14 +171,12 @@ template <typename T> __global__ void __launch_bounds__(kBeamThreads, 4) k_beam_
     __shared__ uint64_t keys[kBeamThreads], bound_key;
     __shared__ int n_found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t b = blockIdx.z, k = blockIdx.y, row = b * a.K + k, slot = row * a.slices + blockIdx.x;
-    beam_pdl_wait();
-    beam_pdl_launch();
+    const int64_t row = b * a.K + k, slot = row * a.slices + slice;
     if (!alive(a, row)) return;  // its slots are not read
     const T *line = (const T *)a.logits + b * a.row + k * a.beam;
     // elements go to threads by their index, wherever the row begins: rows that are equal
     // have equal sums
-    const int e0 = blockIdx.x * kSlice<T>;
+    const int e0 = slice * kSlice<T>;
     const bool whole = ((uintptr_t)line & 15) == 0 && e0 + kSlice<T> <= a.V;
     // piece j of this thread, NaN as -inf, and -inf behind the row
     auto fetch = [&](int j, uint32_t (&w)[4]) {
@@ -361,6 +359,12 @@ template <typename T> __global__ void __launch_bounds__(kBeamThreads, 4) k_beam_
     }
 }
 
+template <typename T> __global__ void __launch_bounds__(kBeamThreads, 4) k_beam_slices(const __grid_constant__ BeamArgs a) {
+    beam_pdl_wait();
+    beam_pdl_launch();
+    beam_slice<T>(a, blockIdx.x, blockIdx.y, blockIdx.z);
+}
+
 // A candidate of a sequence: larger is better.
 struct Head {
     uint64_t score;  // 0: none
@@ -385,7 +389,7 @@ __device__ __forceinline__ Head best_of_warp(Head h) {
     return h;
 }
 
-__global__ void __launch_bounds__(kBeamThreads) k_beam_pick(const __grid_constant__ BeamArgs a) {
+__device__ __forceinline__ void beam_pick(const BeamArgs &a, int64_t b) {
     extern __shared__ uint8_t place[];  // of each list: how many have been taken
     __shared__ double base[kMostBeams];  // what a row's logits are added to
     __shared__ float about[kMostBeams];  // the same in 32 bits
@@ -396,11 +400,8 @@ __global__ void __launch_bounds__(kBeamThreads) k_beam_pick(const __grid_constan
     __shared__ uint32_t maxima[kBeamThreads * kAhead];
     __shared__ int n_found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t b = blockIdx.x;
     const int K = (int)a.K, lists = K * a.slices;
     if (tid == 0) n_found = 0;
-    beam_pdl_wait();
-    beam_pdl_launch();
     // Where there are not many lists, the first places of each are asked for before it is
     // known which rows' are looked at.  (The kernel is a chain of latencies, each of memory
     // some 0.4 us.)  Neighbouring threads take neighbouring lists, not places: the best are in
@@ -576,21 +577,43 @@ __global__ void __launch_bounds__(kBeamThreads) k_beam_pick(const __grid_constan
     }
 }
 
+__global__ void __launch_bounds__(kBeamThreads) k_beam_pick(const __grid_constant__ BeamArgs a) {
+    beam_pdl_wait();
+    beam_pdl_launch();
+    beam_pick(a, blockIdx.x);
+}
+
+// Both in one, where a cluster holds a sequence's slices: its first CTA picks when all have
+// left theirs.
+constexpr int kCluster = 8;
+template <typename T> __global__ void __launch_bounds__(kBeamThreads) k_beam_cluster(const __grid_constant__ BeamArgs a) {
+    beam_pdl_wait();
+    beam_pdl_launch();
+    beam_slice<T>(a, blockIdx.x, blockIdx.y, blockIdx.z);
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    if (blockIdx.x == 0 && blockIdx.y == 0) beam_pick(a, blockIdx.z);
+}
+
 // Launches a kernel whose CTAs may take their places while the one before ends: each waits
 // for that before it reads anything (8 x 8 beams over 32,000 tokens and their states: 17.4 us
 // instead of 21.9).
 template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, size_t smem, cudaStream_t s, const A &...args) {
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 cluster, size_t smem, cudaStream_t s, const A &...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kBeamThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster.x;
+    attr[1].val.clusterDim.y = cluster.y;
+    attr[1].val.clusterDim.z = cluster.z;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster.x * cluster.y * cluster.z > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -795,7 +818,7 @@ ck_status run_reorder(const ck_beam_state *list, int64_t count, const int64_t *p
             if (!a.count) return cudaSuccess;
             const dim3 grid((unsigned)a.start[a.count]);
             a.count = 0;
-            return in_place ? launch_early(k_reorder_in_place, grid, 0, s, a, piece) : launch_early(k_reorder, grid, 0, s, a);
+            return in_place ? launch_early(k_reorder_in_place, grid, 1, 0, s, a, piece) : launch_early(k_reorder, grid, 1, 0, s, a);
         };
         cudaError_t e = cudaSuccess;
         for (int64_t i = 0; i < count && e == cudaSuccess; ++i) {
@@ -854,12 +877,19 @@ extern "C" ck_status ck_beam_select(const ck_beam_call *c, void *stream) {
     a.sum = (double *)(ws + sp.sum), a.top = (float *)(ws + sp.top), a.count = (int *)(ws + sp.count);
     a.value = (float *)(ws + sp.value), a.token = (int *)(ws + sp.token);
     const cudaStream_t s = (cudaStream_t)stream;
+    const dim3 grid((unsigned)sp.slices, (unsigned)c->K, (unsigned)c->B);
+    const size_t places = (size_t)c->K * sp.slices;  // a byte for each list
+    if (places <= kCluster) {
+        const cudaError_t e = with_dtype(c->dtype, [&](auto *tag) {
+            return launch_early(k_beam_cluster<std::remove_pointer_t<decltype(tag)>>, grid, dim3(grid.x, grid.y), places, s, a);
+        });
+        return e == cudaSuccess ? CK_OK : cuda_fail(e, "k_beam_cluster launch");
+    }
     cudaError_t e = with_dtype(c->dtype, [&](auto *tag) {
-        return launch_early(k_beam_slices<std::remove_pointer_t<decltype(tag)>>,
-                            dim3((unsigned)sp.slices, (unsigned)c->K, (unsigned)c->B), 0, s, a);
+        return launch_early(k_beam_slices<std::remove_pointer_t<decltype(tag)>>, grid, 1, 0, s, a);
     });
     if (e != cudaSuccess) return cuda_fail(e, "k_beam_slices launch");
-    e = launch_early(k_beam_pick, dim3((unsigned)c->B), (size_t)c->K * sp.slices, s, a);
+    e = launch_early(k_beam_pick, dim3((unsigned)c->B), 1, places, s, a);
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "k_beam_pick launch");
 }
 

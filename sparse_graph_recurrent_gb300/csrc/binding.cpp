@@ -18,6 +18,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/GradMode.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -352,6 +353,19 @@ PyObject *tuple_of(std::initializer_list<at::Tensor> list) {
     return r;
 }
 
+// A workspace on the current device and stream, without a tensor around it.
+struct Space {
+    void *at = nullptr;
+    explicit Space(size_t bytes) {
+        if (bytes) at = c10::cuda::CUDACachingAllocator::raw_alloc(bytes);
+    }
+    ~Space() {
+        if (at) c10::cuda::CUDACachingAllocator::raw_delete(at);
+    }
+    Space(const Space &) = delete;
+    Space &operator=(const Space &) = delete;
+};
+
 at::Tensor empty_like_type(at::IntArrayRef sizes, const at::Tensor &like, at::ScalarType type) {
     return at::empty(sizes, like.options().dtype(type).requires_grad(false));
 }
@@ -399,18 +413,16 @@ PyObject *gated(PyObject *, PyObject *const *a, Py_ssize_t n) {
         ck_status st = gated_size_entry(c.T, c.B, c.N, &kept_bytes, &need);
         if (st != CK_OK) return raise_status(st);
         at::Tensor out = empty_like_type({c.T, c.B, c.N}, *x.t, x.t->scalar_type());
-        at::Tensor state = empty_like_type({c.B, c.N}, *x.t, at::kFloat), kept, ws;
+        at::Tensor state = empty_like_type({c.B, c.N}, *x.t, at::kFloat), kept;
         c.out = out.data_ptr();
         c.state = state.data_ptr<float>();
         if (a[5] == Py_True) {
             kept = empty_like_type({(int64_t)(kept_bytes / 4)}, *x.t, at::kFloat);
             c.kept = kept.data_ptr<float>();
         }
-        if (need) {
-            ws = empty_like_type({(int64_t)(need / 8)}, *x.t, at::kLong);
-            c.workspace = ws.data_ptr();
-            c.workspace_bytes = (int64_t)need;
-        }
+        const Space ws(need);
+        c.workspace = ws.at;
+        c.workspace_bytes = (int64_t)need;
         st = gated_forward_entry(&c, stream_of(dev));
         if (st != CK_OK) return raise_status(st);
         return tuple_of({out, state, kept});
@@ -440,7 +452,7 @@ PyObject *gated_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
             c.d_out = d.t->const_data_ptr();
             c.d_out_step = d.t->stride(0), c.d_out_row = d.t->stride(1);
         }
-        at::Tensor dx, dgate, dstate0, ws;
+        at::Tensor dx, dgate, dstate0;
         if (a[7] == Py_True) {
             dx = empty_like_type({c.T, c.B, c.N}, *x.t, x.t->scalar_type());
             c.dx = dx.data_ptr();
@@ -453,11 +465,9 @@ PyObject *gated_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
             dstate0 = empty_like_type({c.B, c.N}, *x.t, at::kFloat);
             c.d_state0 = dstate0.data_ptr<float>();
         }
-        if (need) {
-            ws = empty_like_type({(int64_t)(need / 8)}, *x.t, at::kLong);
-            c.workspace = ws.data_ptr();
-            c.workspace_bytes = (int64_t)need;
-        }
+        const Space ws(need);
+        c.workspace = ws.at;
+        c.workspace_bytes = (int64_t)need;
         st = gated_backward_entry(&c, stream_of(dev));
         if (st != CK_OK) return raise_status(st);
         return tuple_of({dx, dgate, dstate0});
@@ -499,14 +509,19 @@ PyObject *clip(PyObject *, PyObject *const *a, Py_ssize_t n) {
             }
             if (clips) list[i].out = outs[i]->data_ptr();
         }
-        size_t need = 0;
-        ck_status st = clip_size_entry(list.data(), count, &need);
-        if (st != CK_OK) return raise_status(st);
-        at::Tensor norm = empty_like_type({}, *outs[0], at::kFloat), ws;
-        if (need) ws = empty_like_type({(int64_t)(need / 8)}, norm, at::kLong);
-        void *at = need ? ws.data_ptr() : nullptr;
-        st = clips ? clip_entry(list.data(), count, PyFloat_AS_DOUBLE(a[1]), norm.data_ptr<float>(), at, (int64_t)need, stream_of(dev))
-                   : norm_entry(list.data(), count, norm.data_ptr<float>(), at, (int64_t)need, stream_of(dev));
+        at::Tensor norm = empty_like_type({}, *outs[0], at::kFloat);
+        const auto call = [&](size_t bytes) {
+            const Space ws(bytes);
+            return clips ? clip_entry(list.data(), count, PyFloat_AS_DOUBLE(a[1]), norm.data_ptr<float>(), ws.at, (int64_t)bytes, stream_of(dev))
+                         : norm_entry(list.data(), count, norm.data_ptr<float>(), ws.at, (int64_t)bytes, stream_of(dev));
+        };
+        // (enough for any list of some thousand tensors; asked for where it is not)
+        ck_status st = call(1 << 16);
+        if (st == CK_ERR_WORKSPACE) {
+            size_t need = 0;
+            st = clip_size_entry(list.data(), count, &need);
+            if (st == CK_OK) st = call(need);
+        }
         if (st != CK_OK) return raise_status(st);
         if (clips)
             for (const at::Tensor *o : outs) written(*o);
@@ -561,11 +576,11 @@ PyObject *beam(PyObject *, PyObject *const *a, Py_ssize_t n) {
         at::Tensor parents = empty_like_type({c.B, c.beams}, *z.t, at::kLong);
         at::Tensor tokens = empty_like_type({c.B, c.beams}, *z.t, at::kLong);
         at::Tensor over = empty_like_type({c.B, c.beams}, *z.t, at::kBool);
-        at::Tensor ws = empty_like_type({(int64_t)((need + 7) / 8)}, *z.t, at::kLong);
+        const Space ws(need);
         c.scores_out = scores.data_ptr<float>();
         c.parents = parents.data_ptr<int64_t>(), c.tokens = tokens.data_ptr<int64_t>();
         c.ended_out = (uint8_t *)over.data_ptr();
-        c.workspace = ws.data_ptr();
+        c.workspace = ws.at;
         c.workspace_bytes = (int64_t)need;
         st = beam_entry(&c, stream_of(dev));
         if (st != CK_OK) return raise_status(st);
