@@ -167,6 +167,7 @@ template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct
     uint32_t shift0, shift_step, shift;
     int left, last_left;      // bytes that a row has from this lane's first on, and behind its last whole piece
     const T *p[NT];
+    bool absent;  // the second tensor: zeros
     int64_t step[NT];
     const float *kept;    // this thread's
     int64_t kept_step;
@@ -194,8 +195,9 @@ template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct
         }
     }
     __device__ __forceinline__ void tensor(int i, const void *from, int64_t to_step, int64_t to_row) {
-        p[i] = from ? (const T *)from + b * to_row + n + row * to_step : nullptr;
+        p[i] = (const T *)from + b * to_row + n + row * to_step;
         step[i] = to_step;
+        if (i == 1) absent = !from;
         if (i == 0) {
             shift_step = (uint32_t)to_step * (uint32_t)sizeof(T);
             shift0 = (uint32_t)(uintptr_t)((const T *)from + n);
@@ -214,7 +216,7 @@ template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct
             const uint32_t to = base + put + lane * W;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                if (!p[i]) continue;
+                if (i == 1 && absent) continue;
                 const T *q = p[i];
                 if (W >= 8 && steps >= kSteps) {
 #pragma unroll
@@ -241,14 +243,14 @@ template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct
             if (n <= 0 || s + row >= steps) continue;
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                if (p[i]) piece(to + i * kTensor + s * kPitch, p[i] + s * step[i], n < 16 ? n : 16);
+                if (i != 1 || !absent) piece(to + i * kTensor + s * kPitch, p[i] + s * step[i], n < 16 ? n : 16);
         }
         // the last piece of row `lane`
         const int n = last_left + (int)((block + lane * shift_step) & 15);
         if (lane < kSteps && lane < steps && n > 0) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                if (p[i]) piece(last + i * kTensor, p[i] + (lane - row) * step[i] + (kPieces - lane % kPieces) * (16 / (int)sizeof(T)), n);
+                if (i != 1 || !absent) piece(last + i * kTensor, p[i] + (lane - row) * step[i] + (kPieces - lane % kPieces) * (16 / (int)sizeof(T)), n);
         }
     }
     // Asks for the first `steps` steps of block k, and leaves a mark to wait for.
@@ -273,7 +275,7 @@ template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct
     __device__ __forceinline__ void go(int n) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-            if (p[i]) p[i] += (int64_t)n * kSteps * step[i];
+            p[i] += (int64_t)n * kSteps * step[i];
         if (KEPT) kept += n * kept_step;
     }
     __device__ __forceinline__ void asked(int way) {
@@ -494,9 +496,7 @@ __device__ __forceinline__ void forward_map(const R &in, const Nodes<V> &at, int
 
 // One block's steps from the state h on.
 template <typename T, int V, bool LEAK, bool SHIFTED, bool WHOLE, typename R>
-__device__ __forceinline__ void forward_run(const GatedArgs &a, const R &in, const Nodes<V> &at, int t0, float (&h)[V]) {
-    const int64_t C = a.B * a.N;
-    T *out = (T *)a.out + (int64_t)t0 * C + at.c;
+__device__ __forceinline__ void forward_run(const GatedArgs &a, const R &in, const Nodes<V> &at, int t0, int64_t C, T *&out, float (&h)[V]) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s, out += C) {
         const Pack<T, V> g = in.step_of(0, s), x = in.step_of(1, s);
@@ -514,16 +514,15 @@ __device__ __forceinline__ void forward_run(const GatedArgs &a, const R &in, con
     }
 }
 
-// A block behind all sequences.
-template <typename T, int V, bool SHIFTED>
-__device__ __forceinline__ void store_zeros(const GatedArgs &a, void *to, const Nodes<V> &at, int t0) {
-    if (!to) return;
-    const int64_t C = a.B * a.N;
-    T *out = (T *)to + (int64_t)t0 * C + at.c;
+// A block behind all sequences, `row` being its first (WAY 1) or last (-1) step's; goes on to the
+// next block's.
+template <typename T, int V, bool SHIFTED, int WAY>
+__device__ __forceinline__ void store_zeros(const GatedArgs &a, T *&row, const Nodes<V> &at, int t0, int64_t C, bool wanted) {
     Pack<T, V> zero;
 #pragma unroll
     for (int v = 0; v < V; ++v) zero.v[v] = from_float<T>(0.f);
-    for (int s = 0; s < kSteps && t0 + s < a.T; ++s, out += C) store_pack<SHIFTED>(a, out, zero, at.count);
+    for (int s = WAY > 0 ? 0 : kSteps - 1; s >= 0 && s < kSteps; s += WAY, row += WAY * C)
+        if (wanted && t0 + s < a.T) store_pack<SHIFTED>(a, row, zero, at.count);
 }
 
 // MAPS: composes the parts and writes their maps.  Otherwise runs them.
@@ -554,20 +553,23 @@ __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArg
         });
     });
     if constexpr (!MAPS) {
+        T *out = (T *)a.out + (int64_t)part.lo * kSteps * C + at.c;
+        float *kept = a.kept + (int64_t)part.lo * C + at.c;
         in.each(part.lo, part.hi - part.lo, 1, at.warp_most, [&](int k) {
             const int t0 = k * kSteps;
             if (!at.count) return;
             if (a.kept) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    if (at.has(v)) a.kept[(int64_t)k * C + at.c + v] = h[v];
+                    if (at.has(v)) kept[v] = h[v];
+                kept += C;
             }
             if (t0 + kSteps <= at.least)
-                forward_run<T, V, LEAK, SHIFTED, true>(a, in, at, t0, h);
+                forward_run<T, V, LEAK, SHIFTED, true>(a, in, at, t0, C, out, h);
             else if (t0 < at.most)
-                forward_run<T, V, LEAK, SHIFTED, false>(a, in, at, t0, h);
+                forward_run<T, V, LEAK, SHIFTED, false>(a, in, at, t0, C, out, h);
             else
-                store_zeros<T, V, SHIFTED>(a, a.out, at, t0);
+                store_zeros<T, V, SHIFTED, 1>(a, out, at, t0, C, true);
         });
         if (part.i + 1 == a.parts) {
 #pragma unroll
@@ -604,8 +606,7 @@ __device__ __forceinline__ void backward_map(const R &in, const Nodes<V> &at, in
 
 // One block's gradients, r being that of the state after it.
 template <typename T, int V, bool LEAK, bool SHIFTED, bool WHOLE, typename R>
-__device__ __forceinline__ void backward_run(const GatedArgs &a, const R &in, const Nodes<V> &at, int t0, float (&r)[V]) {
-    const int64_t C = a.B * a.N;
+__device__ __forceinline__ void backward_run(const GatedArgs &a, const R &in, const Nodes<V> &at, int t0, int64_t C, T *&dx, T *&dgate, float (&r)[V]) {
     // of each step: what it keeps, and what the gradients are multiplied with
     float keep[kSteps][V], leak[kSteps][V], by[kSteps][V], h[V];
 #pragma unroll
@@ -628,7 +629,6 @@ __device__ __forceinline__ void backward_run(const GatedArgs &a, const R &in, co
             }
         }
     }
-    T *dx = (T *)a.dx + (int64_t)(t0 + kSteps - 1) * C + at.c, *dgate = (T *)a.dgate + (int64_t)(t0 + kSteps - 1) * C + at.c;
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s, dx -= C, dgate -= C) {
         const Pack<T, V> pd = in.step_of(1, s);
@@ -685,16 +685,17 @@ __global__ void __maxnreg__(112) k_gated_backward(const __grid_constant__ GatedA
         in.tensor(2, a.x, a.xt, a.xb);
         in.kept = a.kept + at.c, in.kept_count = at.count;
         in.kept_step = C;
+        T *dx = (T *)a.dx + ((int64_t)part.hi * kSteps - 1) * C + at.c, *dgate = (T *)a.dgate + ((int64_t)part.hi * kSteps - 1) * C + at.c;
         in.each(part.hi - 1, part.hi - part.lo, -1, at.warp_most, [&](int k) {
             const int t0 = k * kSteps;
             if (!at.count) return;
             if (t0 + kSteps <= at.least) {
-                backward_run<T, V, LEAK, SHIFTED, true>(a, in, at, t0, r);
+                backward_run<T, V, LEAK, SHIFTED, true>(a, in, at, t0, C, dx, dgate, r);
             } else if (t0 < at.most) {
-                backward_run<T, V, LEAK, SHIFTED, false>(a, in, at, t0, r);
+                backward_run<T, V, LEAK, SHIFTED, false>(a, in, at, t0, C, dx, dgate, r);
             } else {
-                store_zeros<T, V, SHIFTED>(a, a.dx, at, t0);
-                store_zeros<T, V, SHIFTED>(a, a.dgate, at, t0);
+                store_zeros<T, V, SHIFTED, -1>(a, dx, at, t0, C, a.dx);
+                store_zeros<T, V, SHIFTED, -1>(a, dgate, at, t0, C, a.dgate);
             }
         });
         if (part.i == 0 && a.dstate0) {
