@@ -114,20 +114,27 @@ template <typename F> __device__ __forceinline__ void by_dtype(uint8_t d, F &&f)
         f((__half *)nullptr);
 }
 
-// The sum of this thread's squares in a chunk.
-template <typename T> __device__ __forceinline__ float chunk_sum(const T *in, const Where &w, const uint4 (&v)[kClipVecs]) {
+// The sum of this thread's squares in a chunk; bits: those that any of its numbers has.
+template <typename T> __device__ __forceinline__ float chunk_sum(const T *in, const Where &w, const uint4 (&v)[kClipVecs], uint32_t &bits) {
     constexpr int E = 16 / (int)sizeof(T);
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < kClipVecs; ++j) {
         alignas(16) T t[E];
         memcpy(t, &v[j], 16);
+        bits |= v[j].x | v[j].y | v[j].z | v[j].w;
 #pragma unroll
         for (int e = 0; e < E; ++e) s = fmaf(to_float(t[e]), to_float(t[e]), s);
     }
     const int64_t edge = w.lo + threadIdx.x, tail = w.body + w.vecs * E + threadIdx.x;
-    if (edge < w.body) s = fmaf(to_float(in[edge]), to_float(in[edge]), s);
-    if (tail < w.hi) s = fmaf(to_float(in[tail]), to_float(in[tail]), s);
+    if (edge < w.body) {
+        bits |= to_float(in[edge]) != 0.f;
+        s = fmaf(to_float(in[edge]), to_float(in[edge]), s);
+    }
+    if (tail < w.hi) {
+        bits |= to_float(in[tail]) != 0.f;
+        s = fmaf(to_float(in[tail]), to_float(in[tail]), s);
+    }
     return s;
 }
 
@@ -188,24 +195,27 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas) k_norm(const __grid_c
         w = locate(a, lo, 0);
         chunk_load(a, w, lo < keep, v);
     }
+    uint32_t bits = 0;
+    double total = 0;
     for (int c = lo; c < hi; ++c) {
         if (c + 1 < hi) {
             then = locate(a, c + 1, w.i);
             chunk_load(a, then, c + 1 < keep, next);
         }
-        by_dtype(a.dtype[w.i], [&](auto *t) { part += chunk_sum((const std::remove_pointer_t<decltype(t)> *)a.in[w.i], w, v); });
+        by_dtype(a.dtype[w.i], [&](auto *t) { part += chunk_sum((const std::remove_pointer_t<decltype(t)> *)a.in[w.i], w, v, bits); });
+        if ((c - lo) % 32 == 31) total += part, part = 0.f;
         w = then;
 #pragma unroll
         for (int j = 0; j < kClipVecs; ++j) v[j] = next[j];
     }
-    double s = block_sum(part, shared);
+    double s = block_sum(total + (double)part, shared);
     if (threadIdx.x == 0) sum = s;
-    __syncthreads();
+    const bool some = __syncthreads_or(bits);
     // Squares that left 32 bits, or may have been lost below them beside what is left: once more,
     // of numbers made smaller, or larger.
     if (!(sum <= 3.402823466e38f))
         s = scaled_sum(a, lo, hi, 8.271806125530277e-25f, shared);  // 2^-80
-    else if (sum < 8.67e-19)  // 2^-60
+    else if (sum < 8.67e-19 && some)  // 2^-60; not where all are 0
         s = scaled_sum(a, lo, hi, 1.8446744073709552e19f, shared);  // 2^64
     if (threadIdx.x == 0) a.sums[a.first + blockIdx.x] = s;
 }
