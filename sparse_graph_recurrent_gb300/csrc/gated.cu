@@ -15,8 +15,9 @@
 // h -> a h + u, and so is a run of steps: (A2, U2) after (A1, U1) is (A2 A1, A2 U1 + U2).
 // Each warp first composes its part; the warps of a CTA exchange their maps through shared
 // memory; each then runs its part from the state that it now knows, reading it again,
-// mostly from L2.  With more parts than a CTA has warps these are two kernels: the first
-// leaves the maps of all CTAs and the second begins with those before its own.  The
+// mostly from L2.  With more parts than a CTA has warps the CTAs of a cluster leave their maps
+// in memory and begin with those before their own; with more than a cluster's these are two
+// kernels (1,024 x 8 x 1,024 bf16, forward: 22.7 us with a cluster, 24.7 with two kernels).  The
 // composing goes through a part in the order opposite to the run that follows, so that what
 // was read last, and is in L2 still, is read first again.
 //
@@ -36,6 +37,7 @@ namespace {
 
 constexpr int kSteps = 8;       // steps that a thread takes at a time
 constexpr int kGatedWarps = 8;  // warps of a CTA, at most
+constexpr int kCluster = 8;  // CTAs that a cluster may have on any device
 constexpr int kMostSmem = 128 * 1024;
 
 struct GatedArgs {
@@ -54,6 +56,7 @@ struct GatedArgs {
     int64_t blocks;                // kSteps steps each
     int wt, wc;                    // warps along the steps, along the nodes
     int exchange;                  // bytes of shared memory before the rings
+    int cluster;                   // the chunks are the CTAs of a cluster
     int copy;                      // bytes that a lane copies at a time
     int apart;                     // rows of outputs that packs cannot be stored to
 };
@@ -403,7 +406,7 @@ __device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp % a.wt, base = warp - wt;
     const int64_t C = a.B * a.N;
     const int64_t part = (int64_t)blockIdx.y * a.wt + wt;
-    if (!MAPS && gridDim.y > 1) {
+    if (!MAPS && gridDim.y > 1 && !a.cluster) {
         gated_pdl_wait();
         if (REVERSE ? blockIdx.y + 1 < gridDim.y : blockIdx.y > 0)
             through_chunks<V, REVERSE>(a, at, REVERSE ? blockIdx.y + 1 : 0, REVERSE ? gridDim.y : blockIdx.y, ex, carry);
@@ -415,30 +418,39 @@ __device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at,
         }
         return;
     }
-    if (!MAPS && a.wt == 1) return;
+    const bool maps = MAPS || gridDim.y > 1;
+    if (!maps && a.wt == 1) return;
     float2 m[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) m[v] = make_float2(1.f, 0.f);
-    if (MAPS || (REVERSE ? wt > 0 : wt + 1 < a.wt)) part_map(m);  // (nothing follows the last)
+    if (maps || (REVERSE ? wt > 0 : wt + 1 < a.wt)) part_map(m);  // (nothing follows the last)
 #pragma unroll
     for (int v = 0; v < V; ++v) ex.m[warp][v][lane] = m[v];
     __syncthreads();
-    if constexpr (MAPS) {
-        float2 p[V];
+    const int before = REVERSE ? a.wt - 1 - wt : wt;
+    if (maps) {
+        float2 p[V];  // of the CTA's parts before
 #pragma unroll
         for (int v = 0; v < V; ++v) p[v] = make_float2(1.f, 0.f);
-        const int before = REVERSE ? a.wt - 1 - wt : wt;
         for (int j = 0; j < before; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) p[v] = compose(ex.m[base + (REVERSE ? a.wt - 1 - j : j)][v][lane], p[v]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if (!at.has(v)) continue;
-            a.inner[part * C + at.c + v] = p[v];
+            if (MAPS) a.inner[part * C + at.c + v] = p[v];
             if (before == a.wt - 1) a.maps[(int64_t)blockIdx.y * C + at.c + v] = compose(m[v], p[v]);
         }
+        if constexpr (!MAPS) {
+            // all of the cluster's maps are there after this
+            asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+            asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            if (REVERSE ? blockIdx.y + 1 < gridDim.y : blockIdx.y > 0)
+                through_chunks<V, REVERSE>(a, at, REVERSE ? blockIdx.y + 1 : 0, REVERSE ? gridDim.y : blockIdx.y, ex, carry);
+#pragma unroll
+            for (int v = 0; v < V; ++v) carry[v] = fmaf(p[v].x, carry[v], p[v].y);
+        }
     } else {
-        const int before = REVERSE ? a.wt - 1 - wt : wt;
         for (int j = 0; j < before; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -725,6 +737,12 @@ GatedPlan gated_plan(int64_t T, int64_t C, int V, int sms) {
     p.wt = 1;
     while (p.wt < kGatedWarps && 2 * p.wt <= parts) p.wt *= 2;
     p.chunks = parts >= 2 * kGatedWarps ? (int)(parts / kGatedWarps) : 1;
+    // Clusters do not fill the device to the last CTA: with fewer that are all there at once
+    // 2,000 x 5 x 600 fp16, forward, takes 20.6 us instead of 26.8.  (Pairs always fit.)
+    if (p.chunks > 2 && p.chunks <= kCluster) {
+        const int64_t fewer = 14 * (int64_t)sms / warps / kGatedWarps;
+        if (fewer < p.chunks) p.chunks = fewer < 2 ? 2 : (int)fewer;
+    }
     p.wc = p.wt == 1 ? 2 : kGatedWarps / p.wt;  // (small CTAs fill an SM to the last warp)
     while (p.wc > 1 && warps < (int64_t)p.wc * sms) p.wc /= 2;
     p.grid = (warps + p.wc - 1) / p.wc;
@@ -781,10 +799,16 @@ cudaError_t launch_one(dim3 grid, dim3 block, int smem, bool early, const GatedA
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+    if (a.cluster) {
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = attr.val.clusterDim.z = 1;
+        attr.val.clusterDim.y = grid.y;
+    } else {
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = &attr;
-    cfg.numAttrs = early ? 1 : 0;
+    cfg.numAttrs = early || a.cluster ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, KERNEL, a);
 }
 
@@ -796,7 +820,8 @@ cudaError_t launch_gated(GatedArgs a, const GatedPlan &p, bool backward, cudaStr
     a.parts = p.wt * p.chunks;
     const dim3 grid((unsigned)p.grid, (unsigned)p.chunks), block(32 * p.wt * p.wc);
     a.exchange = p.wt > 1 ? (int)sizeof(Exchange<V>) : 0;
-    const int warps = p.wt * p.wc, two = p.chunks > 1;
+    a.cluster = p.chunks > 1 && p.chunks <= kCluster;
+    const int warps = p.wt * p.wc, two = p.chunks > 1 && !a.cluster;
     cudaError_t e = cudaSuccess;
     if (!backward) {
         constexpr int kBytes = ForwardRing<T, V, SHIFTED>::kBytes;
