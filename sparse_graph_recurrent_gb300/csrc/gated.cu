@@ -729,10 +729,11 @@ GatedPlan gated_plan(int64_t T, int64_t C, int V, int sms) {
     p.blocks = (T + kSteps - 1) / kSteps;
     const int64_t warps = (C + 32 * V - 1) / (32 * V);
     // parts: as many as give every SM kFill warps, which is what fits (65,536 x 256 bf16: 119 us
-    // with 16, 143 with 12, 151 with 24, before the copies), of at least four blocks each
+    // with 16, 143 with 12, 151 with 24, before the copies), of at least three blocks each
+    // (1,000 x 2 x 500 bf16, both directions: 23 us, 31 with four; 64 x 8 x 5,000 fp32 25 us, 29 with two)
     constexpr int64_t kFill = 16;
     int64_t parts = warps >= 8 * sms ? 1 : (kFill * sms + warps - 1) / warps;
-    if (parts > p.blocks / 4) parts = p.blocks / 4;
+    if (parts > p.blocks / 3) parts = p.blocks / 3;
     if (parts < 1) parts = 1;
     p.wt = 1;
     while (p.wt < kGatedWarps && 2 * p.wt <= parts) p.wt *= 2;
