@@ -53,8 +53,9 @@ struct GatedArgs {
     float *dstate0;                // may be null
     float2 *maps, *inner;          // [chunks][B][N]; [parts][B][N]: of the CTA's parts before
     int parts;                     // chunks * wt
-    int64_t blocks;                // kSteps steps each
-    int wt, wc;                    // warps along the steps, along the nodes
+    int each, more;                // blocks of kSteps steps of a part; parts with one more
+    int wt, wc;                    // warps along the steps (1 << wt_shift), along the nodes
+    int wt_shift, lane_shift;      // lanes that copy a row, as a power of 2
     int exchange;                  // bytes of shared memory before the rings
     int cluster;                   // the chunks are the CTAs of a cluster
     int copy;                      // bytes that a lane copies at a time
@@ -128,7 +129,7 @@ template <int V> struct Nodes {
     int warp_most;             // of the warp's longest
     __device__ __forceinline__ bool has(int v) const { return v < count; }
     __device__ __forceinline__ explicit Nodes(const GatedArgs &a) {
-        const int lane = threadIdx.x & 31, wc = (threadIdx.x >> 5) / a.wt;
+        const int lane = threadIdx.x & 31, wc = (threadIdx.x >> 5) >> a.wt_shift;
         warp_c = ((int64_t)blockIdx.x * a.wc + wc) * 32 * V;
         c = warp_c + lane * V;
         const int64_t C = a.B * a.N;
@@ -182,9 +183,8 @@ template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct
         base = smem + (threadIdx.x >> 5) * kBytes;
         put = get = 0;
         copy = a.copy;
-        const int lanes = kRow / copy;  // of a row
-        row = lane / lanes;
-        const int first = (lane - row * lanes) * (copy / (int)sizeof(T));
+        row = lane >> a.lane_shift;
+        const int first = (lane - (row << a.lane_shift)) * copy / (int)sizeof(T);
         const int64_t room = (a.B * a.N - c - first) * (int64_t)sizeof(T);
         left = room < -16 ? -16 : room > kRow ? kRow : (int)room;
         const int64_t behind = (a.B * a.N - c) * (int64_t)sizeof(T) - kRow;
@@ -362,9 +362,9 @@ template <int V> struct Exchange {
 struct Part {
     int lo, hi, i;
     __device__ __forceinline__ Part(const GatedArgs &a, int wt) {
-        i = blockIdx.y * a.wt + wt;
-        lo = (int)(a.blocks * i / a.parts);
-        hi = (int)(a.blocks * (i + 1) / a.parts);
+        i = (blockIdx.y << a.wt_shift) + wt;
+        lo = i * a.each + (i < a.more ? i : a.more);
+        hi = lo + a.each + (i < a.more);
     }
 };
 
@@ -373,8 +373,8 @@ struct Part {
 template <int V, bool REVERSE>
 __device__ __forceinline__ void through_chunks(const GatedArgs &a, const Nodes<V> &at, int first, int last,
                                                Exchange<V> &ex, float (&carry)[V]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp % a.wt;
-    const int n = last - first, lo = first + n * wt / a.wt, hi = first + n * (wt + 1) / a.wt;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp & (a.wt - 1);
+    const int n = last - first, lo = first + (n * wt >> a.wt_shift), hi = first + (n * (wt + 1) >> a.wt_shift);
     const int64_t C = a.B * a.N;
     float2 m[V];
 #pragma unroll
@@ -403,7 +403,7 @@ __device__ __forceinline__ void through_chunks(const GatedArgs &a, const Nodes<V
 template <int V, bool MAPS, bool REVERSE, typename F>
 __device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at, Exchange<V> &ex,
                                          float (&carry)[V], F part_map) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp % a.wt, base = warp - wt;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp & (a.wt - 1), base = warp - wt;
     const int64_t C = a.B * a.N;
     const int64_t part = (int64_t)blockIdx.y * a.wt + wt;
     if (!MAPS && gridDim.y > 1 && !a.cluster) {
@@ -543,7 +543,7 @@ __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArg
     extern __shared__ __align__(16) char shared[];
     const uint32_t smem = (uint32_t)__cvta_generic_to_shared(shared) + a.exchange;
     Exchange<V> &ex = *(Exchange<V> *)shared;  // where there is one
-    const int wt = (threadIdx.x >> 5) % a.wt;
+    const int wt = (threadIdx.x >> 5) & (a.wt - 1);
     const Nodes<V> at(a);
     const int64_t C = a.B * a.N;
     ForwardRing<T, V, SHIFTED> in;
@@ -666,7 +666,7 @@ __global__ void __maxnreg__(112) k_gated_backward(const __grid_constant__ GatedA
     extern __shared__ __align__(16) char shared[];
     const uint32_t smem = (uint32_t)__cvta_generic_to_shared(shared) + a.exchange;
     Exchange<V> &ex = *(Exchange<V> *)shared;  // where there is one
-    const int wt = (threadIdx.x >> 5) % a.wt;
+    const int wt = (threadIdx.x >> 5) & (a.wt - 1);
     const Nodes<V> at(a);
     const int64_t C = a.B * a.N;
     const Part part(a, wt);
@@ -734,6 +734,10 @@ GatedPlan gated_plan(int64_t T, int64_t C, int V, int sms) {
     constexpr int64_t kFill = 16;
     int64_t parts = warps >= 8 * sms ? 1 : (kFill * sms + warps - 1) / warps;
     if (parts > p.blocks / 3) parts = p.blocks / 3;
+    // ...or of fewer, where there are so few warps that the steps' own latency is what counts
+    // (64 x 39 x 21 fp32, both directions: 14.4 us, 26.6 with three)
+    const int64_t few = 8 * (int64_t)sms / warps < p.blocks ? 8 * (int64_t)sms / warps : p.blocks;
+    if (p.blocks >= 6 && parts < few) parts = few;
     if (parts < 1) parts = 1;
     p.wt = 1;
     while (p.wt < kGatedWarps && 2 * p.wt <= parts) p.wt *= 2;
@@ -817,8 +821,11 @@ template <typename T, int V, bool LEAK, bool SHIFTED>
 cudaError_t launch_gated(GatedArgs a, const GatedPlan &p, bool backward, cudaStream_t s) {
     a.wt = p.wt;
     a.wc = p.wc;
-    a.blocks = p.blocks;
     a.parts = p.wt * p.chunks;
+    a.each = (int)(p.blocks / a.parts);
+    a.more = (int)(p.blocks % a.parts);
+    while (1 << a.wt_shift < p.wt) ++a.wt_shift;
+    while (a.copy << a.lane_shift < 32 * V * (int)sizeof(T)) ++a.lane_shift;
     const dim3 grid((unsigned)p.grid, (unsigned)p.chunks), block(32 * p.wt * p.wc);
     a.exchange = p.wt > 1 ? (int)sizeof(Exchange<V>) : 0;
     a.cluster = p.chunks > 1 && p.chunks <= kCluster;
@@ -865,14 +872,16 @@ ck_status run_gated(const ck_gated_call *c, bool backward, cudaStream_t s) {
     a.copy = 16;
     while (a.copy > (int)e && !takes(a.copy / (int)e)) a.copy /= 2;
     const bool pairs = C % 2 == 0 && aligned(a.out, 2 * e) && aligned(a.dx, 2 * e) && aligned(a.dgate, 2 * e);
-    // Rows that 8 bytes cannot be copied of, but that hold all sequences one after another and
-    // begin alike in all tensors, are taken as they lie (500 x 3 x 4,999 fp32, both directions:
-    // 83 us).  With 8 bytes the plain copies are faster: 96 x 20 x 4,999 fp16 takes 42 us so and
-    // 55 shifted, the shifts costing instructions.
+    // Rows that 16 bytes cannot be copied of, but that hold all sequences one after another and
+    // begin alike in all tensors, may be taken as they lie.  That is faster than copies of less
+    // than 8 bytes, and than those of 8 where 32-bit rows are many: they go by way of what is
+    // left of L1 (64 x 30 x 4,999 fp32, both directions: 63 us shifted, 76 with 8 bytes; 2,000 x 2
+    // x 301 31 and 27; 96 x 20 x 4,999 fp16 47 and 45, the shifts costing instructions).
     const auto like_x = [&](const void *p, int64_t st, int64_t sb) {
         return ((uintptr_t)p - (uintptr_t)a.x) % 16 == 0 && (c->T == 1 || (st - a.xt) * (int64_t)e % 16 == 0) && (c->B == 1 || sb == c->N);
     };
-    const bool shifted = (a.copy < 8 || !pairs) && like_x(a.x, a.xt, a.xb) && like_x(a.gate, a.gt, a.gb) &&
+    const int least = e == 4 && c->T * C >= (int64_t)1 << 22 ? 16 : 8;
+    const bool shifted = (a.copy < least || !pairs) && like_x(a.x, a.xt, a.xb) && like_x(a.gate, a.gt, a.gb) &&
                          (!a.dout || like_x(a.dout, a.dt, a.db));
     if (shifted) a.copy = 16;
     a.apart = !pairs;
