@@ -6,14 +6,14 @@ header is newer than the library.
 
 Variant "bounds" builds the same sources with -DCK_DEBUG_BOUNDS into
 _build/libck_bounds.so: every gathered row, table and carry index of the
-recurrence is checked on the device (the readout operators are as they are), and a bad one is reported through ck_query_status instead of
+recurrence is checked on the device (the token model's operators are as they are), and a bad one is reported through ck_query_status instead of
 being accessed.  The binding loads it when CK_LIBRARY_VARIANT=bounds.
 
 Variant "prof" (-DCK_PHASE_PROFILE, _build/libck_prof.so) adds %globaltimer
 stamps around each phase of a microstep, read with ck_phase_profile_read; the
 binding loads it when CK_LIBRARY_VARIANT=prof.
 
-csrc/binding.cpp, the short way from Python to the readout operators, is compiled
+csrc/binding.cpp, the short way from Python to the token model's operators, is compiled
 by the host compiler against torch's headers into _build/ck_binding-<torch><ABI>.so.
 """
 from __future__ import annotations

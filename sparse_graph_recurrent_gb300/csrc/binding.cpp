@@ -66,6 +66,7 @@ bool cuda_tensor(PyObject *o) { return THPVariable_Check(o) && THPVariable_Unpac
 
 // Whether autograd follows t: it is to get a gradient, or carries a tangent.
 bool followed(const at::Tensor &t) {
+    if (!t.unsafeGetTensorImpl()->autograd_meta()) return false;  // (most have none)
     return (t.requires_grad() && c10::GradMode::is_enabled()) || t.unsafeGetTensorImpl()->_fw_grad(0, t).defined();
 }
 

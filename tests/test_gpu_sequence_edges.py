@@ -71,6 +71,12 @@ def test_steps_cut_into_parts(T, B, N, dtype):
     check(inputs(T, B, N, dtype, "leak", seed=T), "leak", dtype)
 
 
+@pytest.mark.parametrize("form", ["leak", "decay"])
+def test_many_rows_of_whole_pairs(form):
+    """Enough of them that 32-bit rows at multiples of 8 bytes are taken as they lie."""
+    check(inputs(131, 2, 16_141, "float32", form, seed=1, lengths=True), form, "float32")
+
+
 def test_a_gradient_of_what_was_not_given():
     """d_out or d_state alone, at rows that begin anywhere."""
     import sparse_graph_recurrent_gb300 as ck
