@@ -182,7 +182,8 @@ template <int MOST>
 __global__ void __launch_bounds__(kClipThreads, kClipCtas) k_norm(const __grid_constant__ ClipList<MOST> a) {
     __shared__ double shared[kClipThreads];
     __shared__ double sum;
-    pdl_launch();
+    pdl_wait();
+    pdl_launch();  // only now: what the second kernel reads before it waits is there then
     int lo, hi;
     run_of(a.start[a.count], lo, hi);
     // what this run has in L2 at the end, if all do likewise
@@ -468,8 +469,7 @@ ck_status run_clip(const ck_gradient *list, int64_t count, bool clip, double max
         at = fill(a, list, count, at);
         if (!a.count) break;
         const int grid = clip_grid(a.start[a.count]);
-        k_norm<MOST><<<grid, kClipThreads, 0, s>>>(a);
-        e = cudaGetLastError();
+        e = launch_after(k_norm<MOST>, grid, a, true, s);
         a.first += grid;
         ++launches;
     }

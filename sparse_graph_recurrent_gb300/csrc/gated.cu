@@ -58,6 +58,7 @@ struct GatedArgs {
     int wt_shift, lane_shift;      // lanes that copy a row, as a power of 2
     int exchange;                  // bytes of shared memory before the rings
     int cluster;                   // the chunks are the CTAs of a cluster
+    int early;                     // the next kernel's CTAs may come at once, not when these go
     int copy;                      // bytes that a lane copies at a time
     int apart;                     // rows of outputs that packs cannot be stored to
 };
@@ -407,7 +408,6 @@ __device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at,
     const int64_t C = a.B * a.N;
     const int64_t part = (int64_t)blockIdx.y * a.wt + wt;
     if (!MAPS && gridDim.y > 1 && !a.cluster) {
-        gated_pdl_wait();
         if (REVERSE ? blockIdx.y + 1 < gridDim.y : blockIdx.y > 0)
             through_chunks<V, REVERSE>(a, at, REVERSE ? blockIdx.y + 1 : 0, REVERSE ? gridDim.y : blockIdx.y, ex, carry);
 #pragma unroll
@@ -541,6 +541,8 @@ __device__ __forceinline__ void store_zeros(const GatedArgs &a, T *&row, const N
 template <typename T, int V, bool LEAK, bool SHIFTED, bool MAPS>
 __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArgs a) {
     extern __shared__ __align__(16) char shared[];
+    gated_pdl_wait();
+    if (a.early) gated_pdl_launch();
     const uint32_t smem = (uint32_t)__cvta_generic_to_shared(shared) + a.exchange;
     Exchange<V> &ex = *(Exchange<V> *)shared;  // where there is one
     const int wt = (threadIdx.x >> 5) & (a.wt - 1);
@@ -551,7 +553,6 @@ __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArg
     in.tensor(0, a.gate, a.gt, a.gb);
     in.tensor(1, a.x, a.xt, a.xb);
     const Part part(a, wt);
-    if constexpr (MAPS) gated_pdl_launch();
     float h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = !MAPS && a.state0 && at.has(v) ? __ldg(a.state0 + at.c + v) : 0.f;
@@ -664,13 +665,14 @@ __device__ __forceinline__ void backward_run(const GatedArgs &a, const R &in, co
 template <typename T, int V, bool LEAK, bool SHIFTED, bool MAPS>
 __global__ void __maxnreg__(112) k_gated_backward(const __grid_constant__ GatedArgs a) {
     extern __shared__ __align__(16) char shared[];
+    gated_pdl_wait();
+    if (a.early) gated_pdl_launch();
     const uint32_t smem = (uint32_t)__cvta_generic_to_shared(shared) + a.exchange;
     Exchange<V> &ex = *(Exchange<V> *)shared;  // where there is one
     const int wt = (threadIdx.x >> 5) & (a.wt - 1);
     const Nodes<V> at(a);
     const int64_t C = a.B * a.N;
     const Part part(a, wt);
-    if constexpr (MAPS) gated_pdl_launch();
     const auto begin = [&](auto &in) {
         in.begin(smem, a, at.warp_c);
         in.tensor(0, a.gate, a.gt, a.gb);
@@ -794,7 +796,7 @@ ck_status check_gated(const ck_gated_call *c, bool backward) {
 }
 
 template <auto KERNEL>
-cudaError_t launch_one(dim3 grid, dim3 block, int smem, bool early, const GatedArgs &a, cudaStream_t s) {
+cudaError_t launch_one(dim3 grid, dim3 block, int smem, const GatedArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> done;
     const cudaError_t e = smem > 32 * 1024 ? allow_smem((const void *)KERNEL, kMostSmem, done) : cudaSuccess;
     if (e != cudaSuccess) return e;
@@ -803,17 +805,15 @@ cudaError_t launch_one(dim3 grid, dim3 block, int smem, bool early, const GatedA
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    if (a.cluster) {
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = attr.val.clusterDim.z = 1;
-        attr.val.clusterDim.y = grid.y;
-    } else {
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-    }
-    cfg.attrs = &attr;
-    cfg.numAttrs = early || a.cluster ? 1 : 0;
+    // Its CTAs may take their places while the kernel before ends; each waits for that first.
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.y = grid.y;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, KERNEL, a);
 }
 
@@ -829,16 +829,21 @@ cudaError_t launch_gated(GatedArgs a, const GatedPlan &p, bool backward, cudaStr
     const dim3 grid((unsigned)p.grid, (unsigned)p.chunks), block(32 * p.wt * p.wc);
     a.exchange = p.wt > 1 ? (int)sizeof(Exchange<V>) : 0;
     a.cluster = p.chunks > 1 && p.chunks <= kCluster;
+    // The next kernel, if it is one of these, has its CTAs come while there is room for all of them
+    // beside this one's, or where they fill the device many times.  Else those that came early would
+    // lie unevenly (96 x 20 x 4,999 fp16, both directions: 52 us then, 38 so).
+    const int64_t all = p.grid * p.chunks * p.wt * p.wc;
+    a.early = all <= 8 * (int64_t)device_sms() || (a.parts == 1 && all >= 16 * (int64_t)device_sms());
     const int warps = p.wt * p.wc, two = p.chunks > 1 && !a.cluster;
     cudaError_t e = cudaSuccess;
     if (!backward) {
         constexpr int kBytes = ForwardRing<T, V, SHIFTED>::kBytes;
-        if (two) e = launch_one<k_gated_forward<T, V, LEAK, SHIFTED, true>>(grid, block, a.exchange + warps * kBytes, false, a, s);
-        if (e == cudaSuccess) e = launch_one<k_gated_forward<T, V, LEAK, SHIFTED, false>>(grid, block, a.exchange + warps * kBytes, two, a, s);
+        if (two) e = launch_one<k_gated_forward<T, V, LEAK, SHIFTED, true>>(grid, block, a.exchange + warps * kBytes, a, s);
+        if (e == cudaSuccess) e = launch_one<k_gated_forward<T, V, LEAK, SHIFTED, false>>(grid, block, a.exchange + warps * kBytes, a, s);
     } else {
         constexpr int kBytes = BackwardRing<T, V, SHIFTED, false>::kBytes, kMapBytes = BackwardRing<T, V, SHIFTED, true>::kBytes;
-        if (two) e = launch_one<k_gated_backward<T, V, LEAK, SHIFTED, true>>(grid, block, a.exchange + warps * kMapBytes, false, a, s);
-        if (e == cudaSuccess) e = launch_one<k_gated_backward<T, V, LEAK, SHIFTED, false>>(grid, block, a.exchange + warps * kBytes, two, a, s);
+        if (two) e = launch_one<k_gated_backward<T, V, LEAK, SHIFTED, true>>(grid, block, a.exchange + warps * kMapBytes, a, s);
+        if (e == cudaSuccess) e = launch_one<k_gated_backward<T, V, LEAK, SHIFTED, false>>(grid, block, a.exchange + warps * kBytes, a, s);
     }
     return e;
 }
