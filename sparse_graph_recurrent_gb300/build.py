@@ -115,7 +115,8 @@ def build_binding(force: bool = False) -> str:
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(a for i in includes for a in ("-isystem" if i != includes[0] else "-I", i)), src, "-o", tmp,
-           "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")

@@ -13,9 +13,11 @@
 #include <cfloat>
 #include <cmath>
 #include <initializer_list>
+#include <optional>
 #include <vector>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
@@ -367,8 +369,9 @@ struct Space {
     Space &operator=(const Space &) = delete;
 };
 
+// (without the dispatcher's way to the same function)
 at::Tensor empty_like_type(at::IntArrayRef sizes, const at::Tensor &like, at::ScalarType type) {
-    return at::empty(sizes, like.options().dtype(type).requires_grad(false));
+    return at::Tensor(at::detail::empty_cuda(sizes, type, like.device(), std::nullopt));
 }
 
 // The operands that both directions of a gated recurrence take.
