@@ -7,7 +7,8 @@
 // A thread takes V neighbouring nodes and walks along the steps, kSteps at a time.  Its warp
 // has the next steps copied into shared memory meanwhile, one to three such blocks ahead:
 // registers could not hold as much as has to be under way (with loads into registers, one
-// block ahead, 64 x 32 x 5,000 fp32 took 27 us and its gradient 45; with copies 23 and 41).
+// block ahead, 64 x 32 x 5,000 fp32 took 27 us and its gradient 45; with copies 23 and 41, and
+// 20 and 34 with two nodes' numbers in one operation and kernels that start early).
 // Where the nodes alone fill the device that is all: x and the gate are read once, nothing
 // is exchanged.
 //
@@ -17,7 +18,7 @@
 // memory; each then runs its part from the state that it now knows, reading it again,
 // mostly from L2.  With more parts than a CTA has warps the CTAs of a cluster leave their maps
 // in memory and begin with those before their own; with more than a cluster's these are two
-// kernels (1,024 x 8 x 1,024 bf16, forward: 22.7 us with a cluster, 24.7 with two kernels).  The
+// kernels (1,024 x 8 x 1,024 bf16, forward: 22.7 us with a cluster, 24.7 with two kernels then).  The
 // composing goes through a part in the order opposite to the run that follows, so that what
 // was read last, and is in L2 still, is read first again.
 //
@@ -27,9 +28,9 @@
 // The states are built again in 32 bits from those that the forward keeps at every
 // kSteps-th step (its outputs may be rounded to 16 bits; this also reads less).
 //
-// What bounds it: memory for 32 bits (64 x 32 x 5,000, forward and gradients: 5.4 and
-// 5.0 TB/s of what each reads and writes), instructions for 16 (4.0 TB/s; a sigmoid alone is
-// 11, and a step of the gradient some 40 for each node).
+// What bounds it: memory for 32 bits (64 x 32 x 5,000, forward and gradients: 6.2 and
+// 6.0 TB/s of what each reads and writes), instructions for 16 (96 x 20 x 5,000 fp16: 5.2 and
+// 6.1 TB/s; a step of the gradient is some 30 for each node, 9 of them its sigmoid).
 #include "ck_types.h"
 
 namespace ck {
@@ -37,6 +38,8 @@ namespace {
 
 constexpr int kSteps = 8;       // steps that a thread takes at a time
 constexpr int kGatedWarps = 8;  // warps of a CTA, at most
+// How rows lie: at multiples of what a lane copies; at multiples of a pack; anywhere.
+constexpr int kInPlace = 0, kWholePacks = 1, kAnywhere = 2;
 constexpr int kCluster = 8;  // CTAs that a cluster may have on any device
 constexpr int kMostSmem = 128 * 1024;
 
@@ -71,9 +74,9 @@ template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
     T v[V];
 };
 
-// Stores a pack: at once, or its first `count` one by one where it may lie anywhere (SHIFTED).
-template <bool SHIFTED, typename T, int V> __device__ __forceinline__ void store_pack(const GatedArgs &a, T *p, const Pack<T, V> &r, int count) {
-    if (SHIFTED && a.apart) {
+// Stores a pack: at once, or its first `count` one by one where it may lie anywhere.
+template <int SHIFT, typename T, int V> __device__ __forceinline__ void store_pack(const GatedArgs &a, T *p, const Pack<T, V> &r, int count) {
+    if (SHIFT == kAnywhere && a.apart) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (v < count) p[v] = r.v[v];
@@ -156,18 +159,18 @@ template <int V> struct Nodes {
 // together, `copy` bytes each at a time, whatever a lane's own pack: with 16 bytes the copies
 // pass L1 by, which beside this much shared memory is too small to hold what is under way.
 //
-// SHIFTED: rows that begin anywhere.  The 16-byte pieces that hold a row are copied as they
+// SHIFT: rows that do not begin at multiples of 16 bytes.  The 16-byte pieces that hold a row are copied as they
 // lie, one more than it fills, and a row is read from where it begins inside the first.  Of
 // a piece that the row ends in, what lies behind the row is not read; what lies before its
 // begin shares an aligned 16 bytes with it.
-template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct Ring {
+template <typename T, int V, int NT, bool KEPT, int STAGES, int SHIFT> struct Ring {
     using P = Pack<T, V>;
-    static constexpr int kRow = 32 * (int)sizeof(P), kPitch = kRow + (SHIFTED ? 16 : 0);
+    static constexpr int kRow = 32 * (int)sizeof(P), kPitch = kRow + (SHIFT ? 16 : 0);
     static constexpr int kTensor = kSteps * kPitch, kStage = NT * kTensor + (KEPT ? 128 * V : 0);
     static constexpr int kBytes = STAGES * kStage;
     uint32_t base, put, get;  // stages to be filled and to be read next, times kStage
     int lane, row, copy;  // of the copies: this lane's row of those that go at once
-    // SHIFTED: the low bits of the addresses of step 0 and of a step (the tensors' agree), and
+    // SHIFT: the low bits of the addresses of step 0 and of a step (the tensors' agree), and
     // of the block that is read
     uint32_t shift0, shift_step, shift;
     int left, last_left;      // bytes that a row has from this lane's first on, and behind its last whole piece
@@ -190,7 +193,7 @@ template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct
         left = room < -16 ? -16 : room > kRow ? kRow : (int)room;
         const int64_t behind = (a.B * a.N - c) * (int64_t)sizeof(T) - kRow;
         last_left = behind < -16 ? -16 : behind > 0 ? 0 : (int)behind;
-        if (SHIFTED) {
+        if (SHIFT) {
             b = 0, n = c + first;  // (sequences join)
         } else {
             c = room > 0 ? c + first : 0;
@@ -259,7 +262,7 @@ template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct
     }
     // Asks for the first `steps` steps of block k, and leaves a mark to wait for.
     __device__ __forceinline__ void ask(int k, int steps) {
-        if (SHIFTED)
+        if (SHIFT)
             ask_shifted(k, steps);
         else if (copy == 16)
             ask_rows<16>(steps);
@@ -291,10 +294,10 @@ template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct
     // Of the block that is read: where step s of tensor i lies, what it is, the state before.
     __device__ __forceinline__ uint32_t place(int i, int s) const {
         const uint32_t at = base + get + lane * (int)sizeof(P) + i * kTensor + s * kPitch;
-        return SHIFTED ? at + ((shift + s * shift_step) & 15u) : at;
+        return SHIFT ? at + ((shift + s * shift_step) & 15u) : at;
     }
     __device__ __forceinline__ P step_of(int i, int s) const {
-        if constexpr (!SHIFTED) {
+        if constexpr (SHIFT != kAnywhere) {
             return load_shared<P>(place(i, s));
         } else {
             P r;
@@ -328,19 +331,71 @@ template <typename T, int V, int NT, bool KEPT, int STAGES, bool SHIFTED> struct
     }
 };
 
+// Products and sums of a thread's numbers: of two at once, each rounded as by itself.
+__device__ __forceinline__ unsigned long long both(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+template <int V> __device__ __forceinline__ void multiply(float (&r)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 2) {
+        unsigned long long w;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(both(a[0], a[1])), "l"(both(b[0], b[1])));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r[0]), "=f"(r[1]) : "l"(w));
+    } else {
+        r[0] = a[0] * b[0];
+    }
+}
+template <int V> __device__ __forceinline__ void add(float (&r)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 2) {
+        unsigned long long w;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(both(a[0], a[1])), "l"(both(b[0], b[1])));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r[0]), "=f"(r[1]) : "l"(w));
+    } else {
+        r[0] = a[0] + b[0];
+    }
+}
+// r = a b + c
+template <int V>
+__device__ __forceinline__ void multiply_add(float (&r)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+    if constexpr (V == 2) {
+        unsigned long long w;
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(w) : "l"(both(a[0], a[1])), "l"(both(b[0], b[1])), "l"(both(c[0], c[1])));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r[0]), "=f"(r[1]) : "l"(w));
+    } else {
+        r[0] = fmaf(a[0], b[0], c[0]);
+    }
+}
+template <int V> struct All {
+    float v[V];
+    __device__ __forceinline__ explicit All(float x) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = x;
+    }
+};
+
 // l = sigmoid(f) and a = 1 - l, each to a few units of its last place: with e = exp(-f),
 // l = 1 / (1 + e) and a = e l.  2^t for t = -f log2(e) is the device's approximation (2^-22.5
 // relative); what the rounding of t lost, -f - t ln 2, is put in again by e (1 + that).  f is
 // kept between the borders of e's range, NaN as it is; below -30 a is 1 to the last place.
-__device__ __forceinline__ void sigmoids(float f, float &l, float &a) {
-    float c, e;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(f), "f"(-87.f));
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(c), "f"(100.f));
-    const float t = c * -1.4426950408889634f, lost = fmaf(t, -0.6931471805599453f, -c);
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    e = fmaf(e, lost, e);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(l) : "f"(1.f + e));
-    a = c < -30.f ? 1.f : e * l;
+template <int V> __device__ __forceinline__ void sigmoids(const float (&f)[V], float (&l)[V], float (&a)[V]) {
+    float c[V], t[V], lost[V], e[V], d[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(c[v]) : "f"(-f[v]), "f"(-100.f));
+        asm("min.NaN.f32 %0, %1, %2;" : "=f"(c[v]) : "f"(c[v]), "f"(87.f));
+    }
+    multiply(t, c, All<V>(1.4426950408889634f).v);
+    multiply_add(lost, t, All<V>(-0.6931471805599453f).v, c);
+#pragma unroll
+    for (int v = 0; v < V; ++v) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[v]) : "f"(t[v]));
+    multiply_add(e, e, lost, e);
+    add(d, e, All<V>(1.f).v);
+#pragma unroll
+    for (int v = 0; v < V; ++v) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(l[v]) : "f"(d[v]));
+    multiply(a, e, l);
+#pragma unroll
+    for (int v = 0; v < V; ++v) a[v] = c[v] > 30.f ? 1.f : a[v];
 }
 
 // A product of factors of which none is 0 is not 0 either, or an infinite state would
@@ -460,85 +515,90 @@ __device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at,
     }
 }
 
-// What step t keeps of the state and puts in, for node v.
-template <bool LEAK> __device__ __forceinline__ void gates(float f, float x, float &keep, float &put) {
+// What a step keeps of the states and puts in.
+template <bool LEAK, int V>
+__device__ __forceinline__ void gates(const float (&f)[V], const float (&x)[V], float (&keep)[V], float (&put)[V]) {
     if constexpr (LEAK) {
-        float l;
+        float l[V];
         sigmoids(f, l, keep);
-        put = l * x;
+        multiply(put, l, x);
     } else {
-        keep = f;
-        put = x;
+#pragma unroll
+        for (int v = 0; v < V; ++v) keep[v] = f[v], put[v] = x[v];
     }
+}
+
+template <typename T, int V> __device__ __forceinline__ void floats(const Pack<T, V> &p, float (&r)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) r[v] = to_float(p.v[v]);
 }
 
 // Stages of a ring: more of smaller ones, so that 16 warps of an SM have 64 KB or more under
 // way, and as many as 16 warps have room for.
 template <typename T, int V> constexpr int kForwardStages = sizeof(T) * V >= 8 ? 3 : 4;
 template <typename T, int V> constexpr int kBackwardStages = sizeof(T) * V >= 8 ? 2 : 4;
-template <typename T, int V, bool SHIFTED> using ForwardRing = Ring<T, V, 2, false, kForwardStages<T, V>, SHIFTED>;
-template <typename T, int V, bool SHIFTED, bool MAPS>
-using BackwardRing = Ring<T, V, MAPS ? 2 : 3, !MAPS, kBackwardStages<T, V>, SHIFTED>;
+template <typename T, int V, int SHIFT> using ForwardRing = Ring<T, V, 2, false, kForwardStages<T, V>, SHIFT>;
+template <typename T, int V, int SHIFT, bool MAPS>
+using BackwardRing = Ring<T, V, MAPS ? 2 : 3, !MAPS, kBackwardStages<T, V>, SHIFT>;
 
 // The map of one block of gates and inputs.  WHOLE: all nodes have all its steps.
 template <typename T, int V, bool LEAK, bool WHOLE, typename R>
 __device__ __forceinline__ void forward_map(const R &in, const Nodes<V> &at, int t0, float2 (&all)[V]) {
-    float2 m[V];
-    float least[V];  // of the factors' magnitudes
+    float by[V], plus[V], least[V];  // the map; the least of the factors' magnitudes
 #pragma unroll
-    for (int v = 0; v < V; ++v) m[v] = make_float2(least[v] = 1.f, 0.f);
+    for (int v = 0; v < V; ++v) by[v] = least[v] = 1.f, plus[v] = 0.f;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-        const Pack<T, V> g = in.step_of(0, s), x = in.step_of(1, s);
+        float f[V], x[V], keep[V], put[V];
+        floats(in.step_of(0, s), f);
+        floats(in.step_of(1, s), x);
+        gates<LEAK>(f, x, keep, put);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float keep, put;
-            gates<LEAK>(to_float(g.v[v]), to_float(x.v[v]), keep, put);
-            if (!WHOLE && t0 + s >= at.len[v]) keep = 1.f, put = 0.f;
-            m[v] = make_float2(keep * m[v].x, fmaf(keep, m[v].y, put));
-            least[v] = fminf(least[v], fabsf(keep));
+            if (!WHOLE && t0 + s >= at.len[v]) keep[v] = 1.f, put[v] = 0.f;
+            least[v] = fminf(least[v], fabsf(keep[v]));
         }
+        multiply(by, keep, by);
+        multiply_add(plus, keep, plus, put);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        m[v].x = not_lost(m[v].x, least[v] > 0.f);
-        all[v] = compose(all[v], m[v]);
-    }
+    for (int v = 0; v < V; ++v) all[v] = compose(all[v], make_float2(not_lost(by[v], least[v] > 0.f), plus[v]));
 }
 
 // One block's steps from the state h on.
-template <typename T, int V, bool LEAK, bool SHIFTED, bool WHOLE, typename R>
+template <typename T, int V, bool LEAK, int SHIFT, bool WHOLE, typename R>
 __device__ __forceinline__ void forward_run(const GatedArgs &a, const R &in, const Nodes<V> &at, int t0, int64_t C, T *&out, float (&h)[V]) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s, out += C) {
-        const Pack<T, V> g = in.step_of(0, s), x = in.step_of(1, s);
+        float f[V], x[V], keep[V], put[V], r[V];
+        floats(in.step_of(0, s), f);
+        floats(in.step_of(1, s), x);
+        gates<LEAK>(f, x, keep, put);
+        multiply_add(r, keep, h, put);
         Pack<T, V> o;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const bool live = WHOLE || t0 + s < at.len[v];
-            float keep, put;
-            gates<LEAK>(to_float(g.v[v]), to_float(x.v[v]), keep, put);
-            const float r = fmaf(keep, h[v], put);
-            h[v] = live ? r : h[v];
-            o.v[v] = from_float<T>(live ? r : 0.f);
+            h[v] = live ? r[v] : h[v];
+            o.v[v] = from_float<T>(live ? r[v] : 0.f);
         }
-        if (WHOLE || t0 + s < a.T) store_pack<SHIFTED>(a, out, o, at.count);
+        if (WHOLE || t0 + s < a.T) store_pack<SHIFT>(a, out, o, at.count);
     }
 }
 
 // A block behind all sequences, `row` being its first (WAY 1) or last (-1) step's; goes on to the
 // next block's.
-template <typename T, int V, bool SHIFTED, int WAY>
+template <typename T, int V, int SHIFT, int WAY>
 __device__ __forceinline__ void store_zeros(const GatedArgs &a, T *&row, const Nodes<V> &at, int t0, int64_t C, bool wanted) {
     Pack<T, V> zero;
 #pragma unroll
     for (int v = 0; v < V; ++v) zero.v[v] = from_float<T>(0.f);
     for (int s = WAY > 0 ? 0 : kSteps - 1; s >= 0 && s < kSteps; s += WAY, row += WAY * C)
-        if (wanted && t0 + s < a.T) store_pack<SHIFTED>(a, row, zero, at.count);
+        if (wanted && t0 + s < a.T) store_pack<SHIFT>(a, row, zero, at.count);
 }
 
 // MAPS: composes the parts and writes their maps.  Otherwise runs them.
-template <typename T, int V, bool LEAK, bool SHIFTED, bool MAPS>
+template <typename T, int V, bool LEAK, int SHIFT, bool MAPS>
 __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArgs a) {
     extern __shared__ __align__(16) char shared[];
     gated_pdl_wait();
@@ -548,7 +608,7 @@ __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArg
     const int wt = (threadIdx.x >> 5) & (a.wt - 1);
     const Nodes<V> at(a);
     const int64_t C = a.B * a.N;
-    ForwardRing<T, V, SHIFTED> in;
+    ForwardRing<T, V, SHIFT> in;
     in.begin(smem, a, at.warp_c);
     in.tensor(0, a.gate, a.gt, a.gb);
     in.tensor(1, a.x, a.xt, a.xb);
@@ -578,11 +638,11 @@ __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArg
                 kept += C;
             }
             if (t0 + kSteps <= at.least)
-                forward_run<T, V, LEAK, SHIFTED, true>(a, in, at, t0, C, out, h);
+                forward_run<T, V, LEAK, SHIFT, true>(a, in, at, t0, C, out, h);
             else if (t0 < at.most)
-                forward_run<T, V, LEAK, SHIFTED, false>(a, in, at, t0, C, out, h);
+                forward_run<T, V, LEAK, SHIFT, false>(a, in, at, t0, C, out, h);
             else
-                store_zeros<T, V, SHIFTED, 1>(a, out, at, t0, C, true);
+                store_zeros<T, V, SHIFT, 1>(a, out, at, t0, C, true);
         });
         if (part.i + 1 == a.parts) {
 #pragma unroll
@@ -594,31 +654,30 @@ __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArg
 
 template <typename T, int V, bool LEAK, bool WHOLE, typename R>
 __device__ __forceinline__ void backward_map(const R &in, const Nodes<V> &at, int t0, float2 (&all)[V]) {
-    float2 m[V];
-    float least[V];
+    float by[V], plus[V], least[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) m[v] = make_float2(least[v] = 1.f, 0.f);
+    for (int v = 0; v < V; ++v) by[v] = least[v] = 1.f, plus[v] = 0.f;
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s) {
-        const Pack<T, V> g = in.step_of(0, s), d = in.step_of(1, s);
+        float keep[V], d[V], l[V], sum[V];
+        floats(in.step_of(0, s), keep);
+        floats(in.step_of(1, s), d);
+        if constexpr (LEAK) sigmoids(keep, l, keep);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float l, keep = to_float(g.v[v]), add = to_float(d.v[v]);
-            if constexpr (LEAK) sigmoids(keep, l, keep);
-            if (!WHOLE && t0 + s >= at.len[v]) keep = 1.f, add = 0.f;
-            m[v] = make_float2(keep * m[v].x, keep * (m[v].y + add));
-            least[v] = fminf(least[v], fabsf(keep));
+            if (!WHOLE && t0 + s >= at.len[v]) keep[v] = 1.f, d[v] = 0.f;
+            least[v] = fminf(least[v], fabsf(keep[v]));
         }
+        multiply(by, keep, by);
+        add(sum, plus, d);
+        multiply(plus, keep, sum);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        m[v].x = not_lost(m[v].x, least[v] > 0.f);
-        all[v] = compose(all[v], m[v]);
-    }
+    for (int v = 0; v < V; ++v) all[v] = compose(all[v], make_float2(not_lost(by[v], least[v] > 0.f), plus[v]));
 }
 
 // One block's gradients, r being that of the state after it.
-template <typename T, int V, bool LEAK, bool SHIFTED, bool WHOLE, typename R>
+template <typename T, int V, bool LEAK, int SHIFT, bool WHOLE, typename R>
 __device__ __forceinline__ void backward_run(const GatedArgs &a, const R &in, const Nodes<V> &at, int t0, int64_t C, T *&dx, T *&dgate, float (&r)[V]) {
     // of each step: what it keeps, and what the gradients are multiplied with
     float keep[kSteps][V], leak[kSteps][V], by[kSteps][V], h[V];
@@ -626,44 +685,56 @@ __device__ __forceinline__ void backward_run(const GatedArgs &a, const R &in, co
     for (int v = 0; v < V; ++v) h[v] = in.kept_of(v);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-        const Pack<T, V> pg = in.step_of(0, s), px = in.step_of(2, s);
+        float f[V], x[V];
+        floats(in.step_of(0, s), f);
+        floats(in.step_of(2, s), x);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const bool live = WHOLE || t0 + s < at.len[v];
-            const float x = live ? to_float(px.v[v]) : 0.f, f = live ? to_float(pg.v[v]) : 0.f;
-            if constexpr (LEAK) {
-                sigmoids(f, leak[s][v], keep[s][v]);
-                by[s][v] = keep[s][v] * (x - h[v]);
-                h[v] = fmaf(keep[s][v], h[v], leak[s][v] * x);
-            } else {
-                keep[s][v] = f;
-                by[s][v] = h[v];
-                h[v] = fmaf(f, h[v], x);
-            }
+        for (int v = 0; v < V; ++v)
+            if (!WHOLE && t0 + s >= at.len[v]) f[v] = x[v] = 0.f;
+        if constexpr (LEAK) {
+            float put[V], apart[V];
+            sigmoids(f, leak[s], keep[s]);
+            multiply_add(apart, h, All<V>(-1.f).v, x);
+            multiply(by[s], keep[s], apart);
+            multiply(put, leak[s], x);
+            multiply_add(h, keep[s], h, put);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) keep[s][v] = f[v], by[s][v] = h[v];
+            multiply_add(h, f, h, x);
         }
     }
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s, dx -= C, dgate -= C) {
-        const Pack<T, V> pd = in.step_of(1, s);
+        float d[V], g[V], vx[V], vg[V], before[V];
+        floats(in.step_of(1, s), d);
+        add(g, r, d);
+        if constexpr (LEAK) {
+            multiply(vx, g, leak[s]);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) vx[v] = g[v];
+        }
+        multiply(vg, vx, by[s]);
+        multiply(before, keep[s], g);
         Pack<T, V> ox, og;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const bool live = WHOLE || t0 + s < at.len[v];
-            const float g = r[v] + to_float(pd.v[v]), vx = LEAK ? g * leak[s][v] : g;
-            ox.v[v] = from_float<T>(live ? vx : 0.f);
-            og.v[v] = from_float<T>(live ? vx * by[s][v] : 0.f);
-            r[v] = live ? keep[s][v] * g : r[v];
+            ox.v[v] = from_float<T>(live ? vx[v] : 0.f);
+            og.v[v] = from_float<T>(live ? vg[v] : 0.f);
+            r[v] = live ? before[v] : r[v];
         }
         if (WHOLE || t0 + s < a.T) {
-            if (a.dx) store_pack<SHIFTED>(a, dx, ox, at.count);
-            if (a.dgate) store_pack<SHIFTED>(a, dgate, og, at.count);
+            if (a.dx) store_pack<SHIFT>(a, dx, ox, at.count);
+            if (a.dgate) store_pack<SHIFT>(a, dgate, og, at.count);
         }
     }
 }
 
 // The same with time reversed, and the gradients.
-template <typename T, int V, bool LEAK, bool SHIFTED, bool MAPS>
-__global__ void __maxnreg__(112) k_gated_backward(const __grid_constant__ GatedArgs a) {
+template <typename T, int V, bool LEAK, int SHIFT, bool MAPS>
+__global__ void __maxnreg__(sizeof(T) == 4 ? 112 : 128) k_gated_backward(const __grid_constant__ GatedArgs a) {
     extern __shared__ __align__(16) char shared[];
     gated_pdl_wait();
     if (a.early) gated_pdl_launch();
@@ -683,7 +754,7 @@ __global__ void __maxnreg__(112) k_gated_backward(const __grid_constant__ GatedA
 #pragma unroll
     for (int v = 0; v < V; ++v) r[v] = !MAPS && a.dstate && at.has(v) ? __ldg(a.dstate + at.c + v) : 0.f;
     exchange<V, MAPS, true>(a, at, ex, r, [&](float2 (&m)[V]) {
-        BackwardRing<T, V, SHIFTED, true> in;
+        BackwardRing<T, V, SHIFT, true> in;
         begin(in);
         in.each(part.lo, part.hi - part.lo, 1, at.warp_most, [&](int k) {
             const int t0 = k * kSteps;
@@ -694,7 +765,7 @@ __global__ void __maxnreg__(112) k_gated_backward(const __grid_constant__ GatedA
         });
     });
     if constexpr (!MAPS) {
-        BackwardRing<T, V, SHIFTED, false> in;
+        BackwardRing<T, V, SHIFT, false> in;
         begin(in);
         in.tensor(2, a.x, a.xt, a.xb);
         in.kept = a.kept + at.c, in.kept_count = at.count;
@@ -704,12 +775,12 @@ __global__ void __maxnreg__(112) k_gated_backward(const __grid_constant__ GatedA
             const int t0 = k * kSteps;
             if (!at.count) return;
             if (t0 + kSteps <= at.least) {
-                backward_run<T, V, LEAK, SHIFTED, true>(a, in, at, t0, C, dx, dgate, r);
+                backward_run<T, V, LEAK, SHIFT, true>(a, in, at, t0, C, dx, dgate, r);
             } else if (t0 < at.most) {
-                backward_run<T, V, LEAK, SHIFTED, false>(a, in, at, t0, C, dx, dgate, r);
+                backward_run<T, V, LEAK, SHIFT, false>(a, in, at, t0, C, dx, dgate, r);
             } else {
-                store_zeros<T, V, SHIFTED, -1>(a, dx, at, t0, C, a.dx);
-                store_zeros<T, V, SHIFTED, -1>(a, dgate, at, t0, C, a.dgate);
+                store_zeros<T, V, SHIFT, -1>(a, dx, at, t0, C, a.dx);
+                store_zeros<T, V, SHIFT, -1>(a, dgate, at, t0, C, a.dgate);
             }
         });
         if (part.i == 0 && a.dstate0) {
@@ -750,7 +821,7 @@ GatedPlan gated_plan(int64_t T, int64_t C, int V, int sms) {
         const int64_t fewer = 14 * (int64_t)sms / warps / kGatedWarps;
         if (fewer < p.chunks) p.chunks = fewer < 2 ? 2 : (int)fewer;
     }
-    p.wc = p.wt == 1 ? 2 : kGatedWarps / p.wt;  // (small CTAs fill an SM to the last warp)
+    p.wc = p.wt == 1 ? 1 : kGatedWarps / p.wt;  // (small CTAs fill an SM, and all SMs alike, to the last warp)
     while (p.wc > 1 && warps < (int64_t)p.wc * sms) p.wc /= 2;
     p.grid = (warps + p.wc - 1) / p.wc;
     return p;
@@ -817,7 +888,7 @@ cudaError_t launch_one(dim3 grid, dim3 block, int smem, const GatedArgs &a, cuda
     return cudaLaunchKernelEx(&cfg, KERNEL, a);
 }
 
-template <typename T, int V, bool LEAK, bool SHIFTED>
+template <typename T, int V, bool LEAK, int SHIFT>
 cudaError_t launch_gated(GatedArgs a, const GatedPlan &p, bool backward, cudaStream_t s) {
     a.wt = p.wt;
     a.wc = p.wc;
@@ -837,13 +908,13 @@ cudaError_t launch_gated(GatedArgs a, const GatedPlan &p, bool backward, cudaStr
     const int warps = p.wt * p.wc, two = p.chunks > 1 && !a.cluster;
     cudaError_t e = cudaSuccess;
     if (!backward) {
-        constexpr int kBytes = ForwardRing<T, V, SHIFTED>::kBytes;
-        if (two) e = launch_one<k_gated_forward<T, V, LEAK, SHIFTED, true>>(grid, block, a.exchange + warps * kBytes, a, s);
-        if (e == cudaSuccess) e = launch_one<k_gated_forward<T, V, LEAK, SHIFTED, false>>(grid, block, a.exchange + warps * kBytes, a, s);
+        constexpr int kBytes = ForwardRing<T, V, SHIFT>::kBytes;
+        if (two) e = launch_one<k_gated_forward<T, V, LEAK, SHIFT, true>>(grid, block, a.exchange + warps * kBytes, a, s);
+        if (e == cudaSuccess) e = launch_one<k_gated_forward<T, V, LEAK, SHIFT, false>>(grid, block, a.exchange + warps * kBytes, a, s);
     } else {
-        constexpr int kBytes = BackwardRing<T, V, SHIFTED, false>::kBytes, kMapBytes = BackwardRing<T, V, SHIFTED, true>::kBytes;
-        if (two) e = launch_one<k_gated_backward<T, V, LEAK, SHIFTED, true>>(grid, block, a.exchange + warps * kMapBytes, a, s);
-        if (e == cudaSuccess) e = launch_one<k_gated_backward<T, V, LEAK, SHIFTED, false>>(grid, block, a.exchange + warps * kBytes, a, s);
+        constexpr int kBytes = BackwardRing<T, V, SHIFT, false>::kBytes, kMapBytes = BackwardRing<T, V, SHIFT, true>::kBytes;
+        if (two) e = launch_one<k_gated_backward<T, V, LEAK, SHIFT, true>>(grid, block, a.exchange + warps * kMapBytes, a, s);
+        if (e == cudaSuccess) e = launch_one<k_gated_backward<T, V, LEAK, SHIFT, false>>(grid, block, a.exchange + warps * kBytes, a, s);
     }
     return e;
 }
@@ -878,19 +949,18 @@ ck_status run_gated(const ck_gated_call *c, bool backward, cudaStream_t s) {
     while (a.copy > (int)e && !takes(a.copy / (int)e)) a.copy /= 2;
     const bool pairs = C % 2 == 0 && aligned(a.out, 2 * e) && aligned(a.dx, 2 * e) && aligned(a.dgate, 2 * e);
     // Rows that 16 bytes cannot be copied of, but that hold all sequences one after another and
-    // begin alike in all tensors, may be taken as they lie.  That is faster than copies of less
-    // than 8 bytes, and than those of 8 where 32-bit rows are many: they go by way of what is
-    // left of L1 (64 x 30 x 4,999 fp32, both directions: 63 us shifted, 76 with 8 bytes; 2,000 x 2
-    // x 301 31 and 27; 96 x 20 x 4,999 fp16 47 and 45, the shifts costing instructions).
+    // begin alike in all tensors, are taken as they lie: copies of less go by way of what is left
+    // of L1 (96 x 20 x 4,999 fp16, gradient: 24 us, 29 with copies of 8 bytes; 300 x 2 x 3,001 bf16,
+    // both directions, 21 and 25).
     const auto like_x = [&](const void *p, int64_t st, int64_t sb) {
         return ((uintptr_t)p - (uintptr_t)a.x) % 16 == 0 && (c->T == 1 || (st - a.xt) * (int64_t)e % 16 == 0) && (c->B == 1 || sb == c->N);
     };
-    const int least = e == 4 && c->T * C >= (int64_t)1 << 22 ? 16 : 8;
-    const bool shifted = (a.copy < least || !pairs) && like_x(a.x, a.xt, a.xb) && like_x(a.gate, a.gt, a.gb) &&
+    const bool shifted = (a.copy < 16 || !pairs) && like_x(a.x, a.xt, a.xb) && like_x(a.gate, a.gt, a.gb) &&
                          (!a.dout || like_x(a.dout, a.dt, a.db));
+    const bool whole = pairs && a.copy >= 2 * (int)e;  // packs
     if (shifted) a.copy = 16;
     a.apart = !pairs;
-    const int V = shifted || (pairs && a.copy >= 2 * (int)e) ? 2 : 1;
+    const int V = shifted || whole ? 2 : 1;
     const GatedPlan p = gated_plan(c->T, C, V, device_sms());
     if (p.grid > 0x7fffffff || p.chunks > 65535) return fail(CK_ERR_UNSUPPORTED, "gated recurrence: too many nodes");
     if (p.chunks > 1) {
@@ -904,14 +974,15 @@ ck_status run_gated(const ck_gated_call *c, bool backward, cudaStream_t s) {
         using T = std::remove_pointer_t<decltype(tag)>;
         const auto go = [&](auto width, auto rows) {
             constexpr int W = decltype(width)::value;
-            constexpr bool S = decltype(rows)::value;
+            constexpr int S = decltype(rows)::value;
             return c->form == CK_GATED_LEAK ? launch_gated<T, W, true, S>(a, p, backward, s)
                                             : launch_gated<T, W, false, S>(a, p, backward, s);
         };
         using One = std::integral_constant<int, 1>;
         using Two = std::integral_constant<int, 2>;
-        if (shifted) return go(Two(), std::true_type());
-        return V == 2 ? go(Two(), std::false_type()) : go(One(), std::false_type());
+        if (shifted && whole) return go(Two(), std::integral_constant<int, kWholePacks>());
+        if (shifted) return go(Two(), std::integral_constant<int, kAnywhere>());
+        return V == 2 ? go(Two(), std::integral_constant<int, kInPlace>()) : go(One(), std::integral_constant<int, kInPlace>());
     });
     return err == cudaSuccess ? CK_OK : cuda_fail(err, "k_gated launch");
 }
