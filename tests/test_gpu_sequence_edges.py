@@ -251,3 +251,85 @@ def test_a_layer_trained_in_a_captured_step():
         want = step(eager)
         graph.replay()
         assert torch.equal(eager, captured) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def handed_over(x, gate, read, scores, other, pause=lambda: None):
+    """Each call's operands come from the other stream, which waits for the call before."""
+    import sparse_graph_recurrent_gb300 as ck
+    here = torch.cuda.current_stream()
+
+    def there(make):
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            made = make()
+        here.wait_stream(other)
+        pause()
+        return made
+    B, K = scores.shape
+    state = torch.zeros(B * K, x.shape[2], device="cuda")
+    for _ in range(8):
+        d = there(lambda: x + state.sum() * 1e-3)
+        out, state, kept = ck.gated_recurrence_forward(d, gate, state)
+        pause()
+        g = there(lambda: out * 2 + torch.flip(out, (0,)))
+        dx, dgate, _ = ck.gated_recurrence_backward(d, gate, kept, g, state)
+        pause()
+        both = there(lambda: [dx * 3, dgate - 1])
+        norm = ck.clip_gradients(both, 0.5)
+        pause()
+        logits = there(lambda: ((state + both[0][-1] + both[1][0] * norm) @ read).view(B, K, -1))
+        scores, parents, tokens, _ = ck.beam_select(logits, scores)
+        pause()
+        again = there(lambda: (state + tokens.view(-1, 1) * 1e-4).view(B, K, -1))
+        state = ck.reorder_states(again, parents).view(B * K, -1)
+        pause()
+    return state, scores, norm
+
+
+def test_operands_from_another_stream():
+    """In a row, with pauses, and captured with both streams: the same results."""
+    g = torch.Generator().manual_seed(8)
+    B, K, N, V, T = 2, 3, 500, 9000, 40
+    x, gate = (torch.randn(T, B * K, N, generator=g).cuda() for _ in range(2))
+    read, scores = (torch.randn(N, V, generator=g) * 0.1).cuda(), -torch.rand(B, K, generator=g).cuda()
+    other = torch.cuda.Stream()
+    want = handed_over(x, gate, read, scores, other, torch.cuda.synchronize)
+    for _ in range(5):
+        got = handed_over(x, gate, read, scores, other)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = handed_over(x, gate, read, scores, other)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_from_several_threads():
+    """Calls of several threads, each on a stream of its own."""
+    import threading
+
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    g = torch.Generator().manual_seed(9)
+    sets = []
+    for i in range(4):
+        x, gate = (torch.randn(30 + i, 4, 100 + i, generator=g).cuda() for _ in range(2))
+        sets.append((x, gate, (torch.randn(100 + i, 5000, generator=g) * 0.1).cuda(), -torch.rand(2, 2, generator=g).cuda()))
+    want = [handed_over(*s, streams[0]) for s in sets]
+    torch.cuda.synchronize()
+    got, extra = [None] * 4, [torch.cuda.Stream() for _ in range(4)]
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(5):
+                got[i] = handed_over(*sets[i], extra[i])
+            streams[i].synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for s, w in zip(got, want) for a, b in zip(s, w))
