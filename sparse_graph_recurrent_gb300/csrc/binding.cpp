@@ -23,6 +23,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/forward_grad.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "ck.h"
@@ -67,22 +68,23 @@ int dtype_of(const at::Tensor &t) {
 bool cuda_tensor(PyObject *o) { return THPVariable_Check(o) && THPVariable_Unpack(o).is_cuda(); }
 
 // Whether autograd follows t: it is to get a gradient, or carries a tangent.
-bool followed(const at::Tensor &t) {
+// tangents: whether there can be any.
+bool followed(const at::Tensor &t, bool tangents) {
     if (!t.unsafeGetTensorImpl()->autograd_meta()) return false;  // (most have none)
-    return (t.requires_grad() && c10::GradMode::is_enabled()) || t.unsafeGetTensorImpl()->_fw_grad(0, t).defined();
+    return (t.requires_grad() && c10::GradMode::is_enabled()) || (tangents && t.unsafeGetTensorImpl()->_fw_grad(0, t).defined());
 }
 
 // A tensor of a call, on the device `dev` and not followed by autograd.
 struct Operand {
     const at::Tensor *t = nullptr;
     bool none = true, good = true;
-    Operand(PyObject *o, int dev) {
+    Operand(PyObject *o, int dev, bool tangents = true) {
         if (o == Py_None) return;
         none = false;
         good = THPVariable_Check(o);
         if (!good) return;
         t = &THPVariable_Unpack(o);
-        good = t->is_cuda() && t->device().index() == dev && t->layout() == at::kStrided && !followed(*t);
+        good = t->is_cuda() && t->device().index() == dev && t->layout() == at::kStrided && !followed(*t, tangents);
     }
     bool is(at::ScalarType type) const { return t->scalar_type() == type; }
     bool sizes(int64_t a) const { return t->dim() == 1 && t->size(0) == a; }
@@ -497,8 +499,10 @@ PyObject *clip(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int dev = c10::cuda::current_device();
         std::vector<ck_gradient> list((size_t)count);
         std::vector<const at::Tensor *> outs((size_t)count);
+        // (asked once: a view's tangent is looked for in its base)
+        const bool tangents = torch::autograd::ForwardADLevel::try_get_by_idx(0) != nullptr;
         for (Py_ssize_t i = 0; i < count; ++i) {
-            const Operand g(in[i], dev);
+            const Operand g(in[i], dev, tangents);
             if (g.none || !g.good || !g.t->is_contiguous()) return leave_it();
             list[i].grad = g.t->const_data_ptr();
             list[i].n = g.t->numel();
@@ -506,7 +510,7 @@ PyObject *clip(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (list[i].dtype < 0) return leave_it();
             outs[i] = g.t;
             if (apart) {
-                const Operand o(to[i], dev);
+                const Operand o(to[i], dev, tangents);
                 if (o.none || !o.good || !o.t->is_contiguous() || o.t->scalar_type() != g.t->scalar_type() || o.t->sizes() != g.t->sizes())
                     return leave_it();
                 outs[i] = o.t;
