@@ -470,8 +470,8 @@ ck_status ck_control_logits(const ck_logit_call *call, void *stream);
  * product must not overflow 32 bits.
  *   workspace (device) workspace_bytes of ck_gated_sizes on this device, 8-byte aligned;
  *             its contents need no setting and mean nothing afterwards; NULL when 0 bytes
- * Results depend on the operands, sizes and the device alone.  Asynchronous.  Errors:
- * CK_ERR_INVALID_ARG (type, form, negative size, NULL pointer, alignment),
+ * Results depend on the operands, how they lie, the sizes and the device alone.
+ * Asynchronous.  Errors: CK_ERR_INVALID_ARG (type, form, negative size, NULL pointer, alignment),
  * CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED (B N above 2^28, more than 2^30 steps), CK_ERR_CUDA.
  */
 typedef enum { CK_GATED_LEAK = 0, CK_GATED_DECAY = 1 } ck_gated_form;
