@@ -187,6 +187,70 @@ def test_around_the_kernels_borders(K, V):
         check_beams(logits, scores, ended.cuda(), V - 1, beams=min(16, K * 2))
 
 
+def test_a_vocabulary_of_millions():
+    """More lists than the second kernel looks at side by side."""
+    logits, scores = make_beams(1, 2, 5_000_003, torch.float16, seed=2)
+    check_beams(logits, scores, beams=5)
+    logits, scores = make_beams(1, 1, 4_500_001, torch.float32, seed=2)
+    check_beams(logits, scores, beams=32)
+
+
+# -- offsets that pass 32 bits ---------------------------------------------------------------
+
+
+def test_states_beyond_32_bits():
+    """More than 2^31 elements, whole and by rows far apart; a state that has settled tells
+    whether each step found its own."""
+    import sparse_graph_recurrent_gb300 as ck
+    T, N = 66_000, 32_771
+    x = torch.randn(1, 1, N, device="cuda").bfloat16()
+    gate = torch.full((1, 1, 1), 0.5, device="cuda", dtype=torch.bfloat16)
+    full = lambda t: t.expand(T, 1, N)  # noqa: E731
+    out, state, kept = ck.gated_recurrence_forward(full(x), full(gate), form="decay")
+    assert torch.equal(state, x[0].float() * 2)  # sums of 1, 1/2, ... to the last place
+    settled = (x[0, 0].float() * 2).bfloat16()
+    for i in range(64, T, 6000):
+        assert (out[i:i + 6000] == settled).all()
+    dx, dgate, d0 = ck.gated_recurrence_backward(full(x), full(gate), kept, out, form="decay")
+    # g settles at twice d_out, its product with a settled state at 8 x^2
+    want = (out[100, 0].float() * 2).bfloat16()
+    product = (out[100, 0].float() * 2) * (x[0, 0].float() * 2)
+    for i in range(100, T - 100, 6000):
+        n = min(6000, T - 100 - i)
+        assert (dx[i:i + n] == want).all()
+        assert ((dgate[i:i + n].float() - product).abs() <= product.abs() * 2.0 ** -7).all()
+    last = out[-1].clone()
+    del out, dx, dgate, kept
+    wide = torch.zeros(3, 1, 2 ** 30 + 8, device="cuda", dtype=torch.bfloat16)  # rows far apart
+    far = wide[:, :, 4:4 + N]
+    far.copy_(x.expand(3, 1, N))
+    a, b = (ck.gated_recurrence(v, full(gate)[:3], form="decay") for v in (far, x.expand(3, 1, N).contiguous()))
+    assert all(torch.equal(u, v) for u, v in zip(a, b)) and torch.equal(last[0], settled)
+
+
+def test_gradients_beyond_32_bits():
+    import sparse_graph_recurrent_gb300 as ck
+    n = 2 ** 31 + 12_345
+    g = torch.full((n,), 0.5, device="cuda", dtype=torch.bfloat16)
+    g[-1] = 1024.0
+    want = np.sqrt((n - 1) * 0.25 + 1024.0 ** 2)
+    norm = ck.clip_gradients([g[:3], g[3:]], want / 2)
+    assert abs(float(norm) - want) <= NORM_OFF * want
+    assert float(g[-1]) == 512 and float(g[0]) == 0.25 and (g[-2 ** 20:-1] == 0.25).all() and (g[2 ** 30:2 ** 30 + 9] == 0.25).all()
+
+
+def test_beams_states_beyond_32_bits():
+    import sparse_graph_recurrent_gb300 as ck
+    t = torch.zeros(2, 2, 2 ** 30 + 3, dtype=torch.uint8, device="cuda")
+    t[0, 0], t[0, 1], t[1, 0], t[1, 1] = 1, 2, 3, 4
+    t[1, 1, -1] = 5
+    parents = torch.tensor([[1, 1], [1, 0]], device="cuda")
+    got = ck.reorder_states(t, parents)
+    assert (got[0] == 2).all() and (got[1, 0, :-1] == 4).all() and got[1, 0, -1] == 5 and (got[1, 1] == 3).all()
+    ck.reorder_states([t], parents, out=[t])
+    assert torch.equal(t, got)
+
+
 # -- calls in a row --------------------------------------------------------------------------
 
 
