@@ -937,6 +937,9 @@ ck_status run_gated(const ck_gated_call *c, bool backward, cudaStream_t s) {
     a.x = c->x, a.gate = c->gate, a.dout = backward ? c->d_out : nullptr;
     a.T = c->T, a.B = c->B, a.N = c->N;
     a.xt = c->x_step, a.xb = c->x_row, a.gt = c->gate_step, a.gb = c->gate_row, a.dt = c->d_out_step, a.db = c->d_out_row;
+    // One step has no other to be apart from.  (A block's absent steps are read too, from where
+    // the stride says: a stride that is no multiple of a pack would put them off its alignment.)
+    if (c->T == 1) a.xt = a.gt = a.dt = 0;
     a.state0 = c->state0, a.dstate = c->d_state, a.lengths = c->lengths;
     a.out = c->out, a.state = c->state, a.kept = c->kept;
     a.dx = c->dx, a.dgate = c->dgate, a.dstate0 = c->d_state0;
