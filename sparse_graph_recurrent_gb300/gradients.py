@@ -95,10 +95,12 @@ def clip_gradients(grads, max_norm: float, out=None):
     for g, o in pairs:
         g, own = g.detach(), o is g
         if not _dense(g) or not own and (not _dense(o) or o.stride() != g.stride()):
-            g = g.contiguous()  # by way of a dense one
+            # by way of a dense one: a copy of the gradient, or where the gradient is itself
+            # dense in order, other memory beside it
+            aim, copied, g = o, not g.is_contiguous(), g.contiguous()
             if not o.is_contiguous() or own:
-                back.append((o, g))
-                own = True
+                o, own = g if copied else torch.empty_like(g), False
+                back.append((aim, o))
         ins.append(g)
         outs.append(g if own else o.detach())
     with torch.cuda.device(device):
