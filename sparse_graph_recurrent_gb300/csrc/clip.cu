@@ -429,7 +429,8 @@ template <typename K, typename A> cudaError_t launch_after(K kernel, int grid, c
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Fills a launch's list from entry `at` on; returns the entry after its last.
+// Fills a launch's list from entry `at` on; returns the entry that the next begins with, `count`
+// where nothing but empty tensors is left.
 template <int MOST> int64_t fill(ClipList<MOST> &a, const ck_gradient *list, int64_t count, int64_t at) {
     a.count = 0;
     int64_t chunks = 0;
@@ -445,6 +446,7 @@ template <int MOST> int64_t fill(ClipList<MOST> &a, const ck_gradient *list, int
         a.start[a.count++] = (int32_t)chunks;
         chunks += c;
     }
+    while (at < count && !list[at].n) ++at;
     a.start[a.count] = (int32_t)chunks;
     return at;
 }

@@ -67,3 +67,22 @@ def test_gradients_stay_as_they_are_wherever_out_lies(max_norm, dtype):
     lines = zeros(2, 3000)
     clipped([new(3000)], [lines.t()[:, 1]], max_norm)
     assert not lines[0].any()
+
+
+@pytest.mark.parametrize("count", [1000, 2000, 1001])
+@pytest.mark.parametrize("empty", [1, 3])
+def test_empty_tensors_behind_a_full_list(count, empty):
+    import sparse_graph_recurrent_gb300 as ck
+    g = torch.Generator().manual_seed(count)
+    for apart in (False, True):
+        grads = [torch.randn(1 + i % 50, generator=g).cuda() for i in range(count)]
+        grads[5:5] = [torch.empty(0, device="cuda")] * (count % 1000)  # (more than a launch's, and some in between)
+        grads += [torch.empty(0, device="cuda") for _ in range(empty)]
+        out = [torch.full_like(t, 9) for t in grads] if apart else grads
+        want = [host(t) for t in grads]
+        norm, factor = so.clip(want, 0.5)
+        got = ck.clip_gradients(grads, 0.5, out=out if apart else None)
+        assert abs(float(got) - norm) <= NORM_OFF * norm and factor < 1
+        for t, w in zip(out, want):
+            so.within(host(t), w * factor, np.abs(w * factor) * FACTOR_OFF)
+        assert abs(float(ck.grad_norm(out)) - 0.5) < 1e-5
