@@ -38,10 +38,11 @@ def beam_select(logits, scores, ended=None, end_token=None, beams=None):
     _refuse_derivatives("beam_select", logits=logits, scores=scores)
     device, (B, K, V) = logits.get_device(), logits.shape
     beams = K if beams is None else int(beams)
+    logits = logits.resolve_neg()
     if V > 1 and logits.stride(2) != 1:
         logits = logits.contiguous()
     _ck._like(scores, device, torch.float32, (B, K), "scores")
-    scores = scores.contiguous()
+    scores = scores.resolve_neg().contiguous()
     if ended is not None:
         _ck._like(ended, device, torch.bool, (B, K), "ended")
         if end_token is None:
@@ -79,6 +80,11 @@ def _rows_inside(t):
             return False
         at *= n
     return True
+
+
+def _noted(t):
+    """Whether t's numbers are the conjugated, the negated ones of what its memory holds."""
+    return t.is_conj(), t.is_neg()
 
 
 def reorder_states(states, parents, out=None):
@@ -119,6 +125,10 @@ def reorder_states(states, parents, out=None):
         source = t.detach()
         if not _rows_inside(source):
             source = source.contiguous()
+        if _noted(source) != _noted(o):  # (alike, the bytes move as they are)
+            source = source.resolve_conj().resolve_neg()
+            if any(_noted(o)):
+                raise ValueError("out is conjugated or negated lazily, and the state is not")
         size = t.element_size()
         entry.in_, entry.out, entry.bytes = source.data_ptr(), o.data_ptr(), source[0, 0].numel() * size if B and K else 0
         entry.in_row, entry.in_beam = source.stride(0) * size, source.stride(1) * size

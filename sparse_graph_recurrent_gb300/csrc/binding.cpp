@@ -74,7 +74,8 @@ bool followed(const at::Tensor &t, bool tangents) {
     return (t.requires_grad() && c10::GradMode::is_enabled()) || (tangents && t.unsafeGetTensorImpl()->_fw_grad(0, t).defined());
 }
 
-// A tensor of a call, on the device `dev` and not followed by autograd.
+// A tensor of a call, on the device `dev`, not followed by autograd, and whose memory holds
+// its numbers (a view may be noted as conjugated or negated: those are left).
 struct Operand {
     const at::Tensor *t = nullptr;
     bool none = true, good = true;
@@ -84,7 +85,8 @@ struct Operand {
         good = THPVariable_Check(o);
         if (!good) return;
         t = &THPVariable_Unpack(o);
-        good = t->is_cuda() && t->device().index() == dev && t->layout() == at::kStrided && !followed(*t, tangents);
+        good = t->is_cuda() && t->device().index() == dev && t->layout() == at::kStrided && !t->is_conj() && !t->is_neg() &&
+               !followed(*t, tangents);
     }
     bool is(at::ScalarType type) const { return t->scalar_type() == type; }
     bool sizes(int64_t a) const { return t->dim() == 1 && t->size(0) == a; }

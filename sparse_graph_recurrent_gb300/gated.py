@@ -22,6 +22,7 @@ def _steps(t, name, shape, dtype, device):
     if t.dtype != dtype or t.shape != shape or t.get_device() != device:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on cuda:{device}, not {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
+    t = t.resolve_neg()
     if t.shape[2] > 1 and t.stride(2) != 1:
         t = t.contiguous()
     return t, t.stride(0), t.stride(1)
@@ -33,7 +34,7 @@ def _state(t, name, B, N, device):
     if t.dtype != torch.float32 or t.shape != (B, N) or t.get_device() != device:
         raise ValueError(f"{name} must be float32 [{B}, {N}] on cuda:{device}, not {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}")
-    return t.contiguous()
+    return t.resolve_neg().contiguous()
 
 
 def _call(x, gate, lengths, form):

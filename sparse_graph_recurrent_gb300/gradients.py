@@ -94,11 +94,11 @@ def clip_gradients(grads, max_norm: float, out=None):
     ins, outs, back = [], [], []
     for g, o in pairs:
         g, own = g.detach(), o is g
-        if not _dense(g) or not own and (not _dense(o) or o.stride() != g.stride()):
+        if not _dense(g) or not own and (not _dense(o) or o.stride() != g.stride() or o.is_neg() != g.is_neg()):
             # by way of a dense one: a copy of the gradient, or where the gradient is itself
             # dense in order, other memory beside it
-            aim, copied, g = o, not g.is_contiguous(), g.contiguous()
-            if not o.is_contiguous() or own:
+            aim, copied, g = o, not g.is_contiguous() or g.is_neg(), g.resolve_neg().contiguous()
+            if not o.is_contiguous() or own or o.is_neg():
                 o, own = g if copied else torch.empty_like(g), False
                 back.append((aim, o))
         ins.append(g)

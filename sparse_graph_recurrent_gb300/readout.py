@@ -36,6 +36,11 @@ def _refuse_derivatives(what, **operands):
             raise ValueError(f"{what} has no derivative: call it under no_grad or on a detached {name}")
 
 
+def _plain(t):
+    """t, with its numbers in memory as they are where it is a view that negates them."""
+    return t.resolve_neg() if isinstance(t, torch.Tensor) else t
+
+
 def _written(out):
     if not out.is_inference():  # those have no version
         increment_version(out)
@@ -72,7 +77,7 @@ def _as3(x, locked):
 
 
 def _dropout(x, p, seed, step, locked):
-    device = x.get_device()
+    x, device = _plain(x), x.get_device()
     if device < 0:
         raise ValueError("dropout takes CUDA tensors")
     if locked and x.dim() < 2:
@@ -147,7 +152,7 @@ def int4_quantize(w, group_size: int = 128, symmetric: bool = True, scale_dtype=
         raise ValueError("w must be a CUDA tensor [V, K] with K >= 1")
     if group_size not in _ck.INT4_GROUPS:
         raise ValueError(f"group_size must be one of {_ck.INT4_GROUPS}, not {group_size}")
-    w = w.detach()
+    w = _plain(w.detach())
     if w.shape[1] > 1 and w.stride(1) != 1:
         w = w.contiguous()
     V, K = w.shape
@@ -184,6 +189,7 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
     if y is not None:
         return y
     _refuse_derivatives("int4_matvec", x=x, scales=scales, bias=bias, out=out)
+    x, scales, bias = map(_plain, (x, scales, bias))
     device = x.get_device()
     if device < 0:
         raise ValueError("int4_matvec takes CUDA tensors")
@@ -200,6 +206,8 @@ def int4_matvec(x, qweight, scales, zeros=None, bias=None, group_size: int = 128
     else:
         if tuple(out.shape) != (*x.shape[:-1], V):
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(*x.shape[:-1], V)}")
+        if out.is_neg():
+            raise ValueError("out is negated lazily")
         y = out if out.dim() == 2 else out.view(-1, V)
         _written(out)
     args = (x2, qweight, scales, zeros, bias, group_size, y)
@@ -264,6 +272,8 @@ def _control(logits, history, history_len, prompt_len, repetition, frequency, pr
         raise ValueError("logits must be a CUDA tensor [B, V] of float32, bfloat16 or float16")
     _refuse_derivatives("a logit control", logits=logits, repetition=repetition, frequency=frequency,
                         presence=presence, bias=bias, temperature=temperature, out=out)
+    logits, repetition, frequency, presence, bias, temperature = map(
+        _plain, (logits, repetition, frequency, presence, bias, temperature))
     B, V = logits.shape
     text = text_len = prompt = None
     bits = L = text_stride = 0
@@ -288,6 +298,8 @@ def _control(logits, history, history_len, prompt_len, repetition, frequency, pr
     if out is not None:
         if out.dtype != logits.dtype or out.shape != logits.shape or out.get_device() != dev:
             raise ValueError("out must be like logits")
+        if out.is_neg():
+            raise ValueError("out is negated lazily")
         out_at, out_stride = out.data_ptr(), _ck._rows(out, "out")
         _written(out)
     at = step_dev = None

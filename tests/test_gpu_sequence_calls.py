@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import sequence_oracle as so
+from test_gpu_beams import gathered
 from test_gpu_clip import FACTOR_OFF, NORM_OFF
 from test_gpu_gated import TYPES, check, inputs
 
@@ -86,3 +87,90 @@ def test_empty_tensors_behind_a_full_list(count, empty):
         for t, w in zip(out, want):
             so.within(host(t), w * factor, np.abs(w * factor) * FACTOR_OFF)
         assert abs(float(ck.grad_norm(out)) - 0.5) < 1e-5
+
+
+# -- views that are conjugated or negated when they are read ----------------------------------
+
+
+def negated(t):
+    """t, held as -t with a note to negate it."""
+    n = torch._neg_view(t.neg())
+    assert n.is_neg() and torch.equal(n, t)
+    return n
+
+
+def test_states_that_are_conjugated_or_negated_lazily():
+    import sparse_graph_recurrent_gb300 as ck
+    parents = torch.tensor([[1, 1, 0], [2, 0, 2]], device="cuda")
+    z = torch.randn(2, 3, 40, dtype=torch.complex64, device="cuda")
+    for state in (z.conj(), z.conj().imag, z.transpose(1, 2).contiguous().transpose(1, 2).conj(), negated(z.real.contiguous())):
+        want = gathered(state.resolve_conj().resolve_neg(), parents)
+        assert torch.equal(ck.reorder_states(state, parents).cpu(), want)
+        assert all(torch.equal(t.cpu(), want) for t in ck.reorder_states([state, state], parents))
+        out = torch.zeros(2, 3, 40, dtype=state.dtype, device="cuda")
+        assert ck.reorder_states(state, parents, out=out) is out and torch.equal(out.cpu(), want)
+    own = z.clone().conj()  # in its own place, and into one that is noted alike
+    want = gathered(own.resolve_conj(), parents)
+    like = torch.zeros_like(z).conj()
+    ck.reorder_states(own, parents, out=like)
+    assert like.is_conj() and torch.equal(like.resolve_conj().cpu(), want)
+    ck.reorder_states(own, parents, out=own)
+    assert own.is_conj() and torch.equal(own.resolve_conj().cpu(), want)
+    with pytest.raises(ValueError):
+        ck.reorder_states(z, parents, out=torch.zeros_like(z).conj())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_operands_that_are_negated_lazily(dtype):
+    import sparse_graph_recurrent_gb300 as ck
+    d = inputs(40, 3, 8, dtype, "leak")
+    plain = ck.gated_recurrence_forward(d["x"], d["gate"], d["state0"])
+    want = ck.gated_recurrence_backward(d["x"], d["gate"], plain[2], d["d_out"], d["d_state"])
+    for name in ("x", "gate", "state0", "d_out", "d_state"):
+        n = {**d, name: negated(d[name])}
+        got = ck.gated_recurrence_forward(n["x"], n["gate"], n["state0"])
+        assert all(torch.equal(a, b) for a, b in zip(got, plain))
+        assert all(torch.equal(a, b) for a, b in zip(ck.gated_recurrence(n["x"], n["gate"], n["state0"]), plain))
+        got = ck.gated_recurrence_backward(n["x"], n["gate"], got[2], n["d_out"], n["d_state"])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    z, s = d["x"][:2].transpose(1, 2).contiguous(), -torch.rand(2, 8, device="cuda")
+    want = ck.beam_select(z, s)
+    for args in ((negated(z), s), (z, negated(s))):
+        assert all(torch.equal(a, b) for a, b in zip(ck.beam_select(*args), want))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_clipping_of_what_is_negated_lazily(dtype):
+    import sparse_graph_recurrent_gb300 as ck
+    g = torch.randn(300, device="cuda").to(TYPES[dtype])
+    want = torch.empty_like(g)
+    norm = ck.clip_gradients([g], 0.5, out=[want])
+    for a in (g, negated(g)):
+        for b in (torch.empty_like(g), torch._neg_view(torch.empty_like(g))):
+            assert torch.equal(ck.clip_gradients([a], 0.5, out=[b]), norm)
+            assert torch.equal(b.resolve_neg(), want) and torch.equal(a.resolve_neg(), g)
+    own = negated(g)
+    assert torch.equal(ck.clip_gradients([own], 0.5), norm) and torch.equal(own.resolve_neg(), want)
+
+
+def test_readout_operands_that_are_negated_lazily():
+    """The readout's operators look at their operands the same way."""
+    import sparse_graph_recurrent_gb300 as ck
+    x = torch.randn(3, 64, device="cuda")
+    assert torch.equal(ck.dropout(negated(x), 0.3, 5), ck.dropout(x, 0.3, 5))
+    w = torch.randn(40, 64, device="cuda")
+    q = ck.int4_quantize(w, 32)
+    assert all(torch.equal(a, b) for a, b in zip(ck.int4_quantize(negated(w), 32)[:2], q[:2]))
+    bias = torch.randn(40, device="cuda")
+    want = ck.int4_matvec(x, *q, bias, 32)
+    for args in ((negated(x), *q, bias, 32), (x, q[0], negated(q[1]), q[2], bias, 32), (x, *q, negated(bias), 32)):
+        assert torch.equal(ck.int4_matvec(*args), want)
+    with pytest.raises(ValueError):
+        ck.int4_matvec(x, *q, bias, 32, out=torch._neg_view(want.clone()))
+    heat, extra = torch.rand(3, device="cuda") + 0.5, torch.randn(64, device="cuda")
+    want = ck.control_logits(x, bias=extra, temperature=heat)
+    for z, b, t in ((negated(x), extra, heat), (x, negated(extra), heat), (x, extra, negated(heat))):
+        assert torch.equal(ck.control_logits(z, bias=b, temperature=t), want)
+    assert torch.equal(ck.pick_tokens(negated(x)), ck.pick_tokens(x))
+    with pytest.raises(ValueError):
+        ck.control_logits(x, out=torch._neg_view(want.clone()))
