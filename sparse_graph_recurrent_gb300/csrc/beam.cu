@@ -37,7 +37,6 @@ constexpr int kFound = 4096;  // 64 beams' threads' elements
 constexpr int kAhead = 2;     // candidates that a thread of the second kernel asks for at once
 constexpr int kFew = 512;     // more than this are not ranked without looking for a closer bound
 constexpr int kMostBeams = 64;
-constexpr int kMostLists = 40960;                 // beams times slices
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
@@ -392,7 +391,7 @@ __device__ __forceinline__ Head best_of_warp(Head h) {
 }
 
 __device__ __forceinline__ void beam_pick(const BeamArgs &a, int64_t b) {
-    extern __shared__ uint8_t place[];  // of each list: how many have been taken
+    extern __shared__ uint8_t place[];  // of each list: how many have been taken (64 beams of 2,048 slices at most)
     __shared__ double base[kMostBeams];  // what a row's logits are added to
     __shared__ float about[kMostBeams];  // the same in 32 bits
     __shared__ uint8_t state[kMostBeams];  // 0 nothing, 1 by logits, 2 ended
@@ -642,9 +641,6 @@ ck_status check_beam_sizes(int64_t dtype, int64_t B, int64_t K, int64_t V, int64
     if (B < 0 || K < 1 || V < 1 || beams < 1) return fail(CK_ERR_INVALID_ARG, "beam search: sizes must be positive");
     if (K > kMostBeams || beams > kMostBeams || V >= ((int64_t)1 << 24) || B > 65535)
         return fail(CK_ERR_UNSUPPORTED, "beam search: more than 64 beams, 65535 sequences or 2^24 tokens");
-    // a byte of shared memory for each list
-    if (K * beam_space(dtype, B, K, V, beams).slices > kMostLists)
-        return fail(CK_ERR_UNSUPPORTED, "beam search: too many beams and tokens at once");
     return CK_OK;
 }
 
@@ -891,7 +887,11 @@ extern "C" ck_status ck_beam_select(const ck_beam_call *c, void *stream) {
         return launch_early(k_beam_slices<std::remove_pointer_t<decltype(tag)>>, grid, 1, 0, s, a);
     });
     if (e != cudaSuccess) return cuda_fail(e, "k_beam_slices launch");
-    e = launch_early(k_beam_pick, dim3((unsigned)c->B), 1, places, s, a);
+    // (beside its other 13.5 KB the most that is had without asking is some 34 KB)
+    constexpr int kMostPlaces = kMostBeams * (int)(((1 << 24) + kSlice<float> - 1) / kSlice<float>);
+    static std::atomic<uint64_t> done;
+    if (places > 32 * 1024) e = allow_smem((const void *)k_beam_pick, kMostPlaces, done);
+    if (e == cudaSuccess) e = launch_early(k_beam_pick, dim3((unsigned)c->B), 1, places, s, a);
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "k_beam_pick launch");
 }
 

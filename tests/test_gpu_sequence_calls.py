@@ -174,3 +174,24 @@ def test_readout_operands_that_are_negated_lazily():
     assert torch.equal(ck.pick_tokens(negated(x)), ck.pick_tokens(x))
     with pytest.raises(ValueError):
         ck.control_logits(x, out=torch._neg_view(want.clone()))
+
+
+# -- selection -------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype,K,V", [("float32", 64, 4_600_000), ("float32", 64, 16_777_215), ("bfloat16", 64, 9_400_000)])
+def test_as_many_beams_and_tokens_as_there_may_be(dtype, K, V):
+    import sparse_graph_recurrent_gb300 as ck
+    g = torch.Generator(device="cuda").manual_seed(V)
+    logits = torch.randn(1, K, V, generator=g, device="cuda").to(TYPES[dtype])
+    scores = -torch.rand(1, K, generator=g, device="cuda")
+    got = ck.beam_select(logits, scores)
+    base = torch.stack([torch.logsumexp(z.double(), 0) for z in logits[0]])
+    top = torch.topk(logits[0], 64, dim=1)
+    for r in range(K):
+        k, v = int(got[1][0, r]), int(got[2][0, r])
+        want = float(scores[0, k]) + float(logits[0, k, v]) - float(base[k])
+        assert abs(float(got[0][0, r]) - want) <= so.beam_score_off(V) + abs(want) * so.U32
+    all_of_them = scores[0].double()[:, None] + top.values.double() - base[:, None]
+    best = torch.topk(all_of_them.flatten(), 64).values
+    assert (got[0][0].double() - best).abs().max() <= so.beam_score_off(V) + 2 * so.U32 * float(best.abs().max())
