@@ -79,8 +79,8 @@ __device__ __forceinline__ double unordered(uint64_t u) {
 
 // Whether beam k of sequence b goes on by its logits.
 __device__ __forceinline__ bool alive(const BeamArgs &a, int64_t at) {
-    const float s = __ldg(a.scores + at);
-    return fabsf(s) <= 3.402823466e38f && !(a.ended && __ldg(a.ended + at));
+    const float s = a.scores[at];
+    return fabsf(s) <= 3.402823466e38f && !(a.ended && a.ended[at]);
 }
 
 // 2^x to 2 units; 0 below 2^-126.
@@ -186,7 +186,7 @@ template <typename T> __device__ __forceinline__ void beam_slice(const BeamArgs 
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = P::kNothing;
         } else if (whole || e + E <= a.V) {
-            const uint4 u = whole ? __ldg((const uint4 *)(line + e)) : load_vec<T>(line, e, a.V);
+            const uint4 u = whole ? *(const uint4 *)(line + e) : load_vec<T>(line, e, a.V);
             w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
         } else {
             alignas(16) T t[E];
@@ -421,9 +421,9 @@ __device__ __forceinline__ void beam_pick(const BeamArgs &a, int64_t b) {
         at[r] = i / lists;
         list[r] = i - at[r] * lists;
         const int64_t slot = b * lists + list[r];
-        value[r] = __ldcg(a.value + slot * a.beams + at[r]);
-        token[r] = __ldcg(a.token + slot * a.beams + at[r]);
-        count[r] = __ldcg(a.count + slot);
+        value[r] = load_l2(a.value + slot * a.beams + at[r]);
+        token[r] = load_l2(a.token + slot * a.beams + at[r]);
+        count[r] = load_l2(a.count + slot);
     }
     int width = 1;  // lanes of a row
     while (width < 32 && width < a.slices) width *= 2;
@@ -432,22 +432,22 @@ __device__ __forceinline__ void beam_pick(const BeamArgs &a, int64_t b) {
         const int k = k0 + tid / width;
         const bool there = k < K;
         const int64_t row = b * K + (there ? k : 0), slot = row * a.slices;
-        const float s = __ldg(a.scores + row);
-        const bool over = a.ended && __ldg(a.ended + row);
+        const float s = a.scores[row];
+        const bool over = a.ended && a.ended[row];
         float first_top = neg_inf();
         double first_sum = 0;
-        if (sub < a.slices) first_top = __ldcg(a.top + slot + sub), first_sum = __ldcg(a.sum + slot + sub);
+        if (sub < a.slices) first_top = load_l2(a.top + slot + sub), first_sum = load_l2(a.sum + slot + sub);
         const bool finite = fabsf(s) <= 3.402823466e38f, looks = finite && !over;
         if (!looks) first_top = neg_inf();
         float top = first_top;
         double total = 0;
         if (looks)
-            for (int i = sub + width; i < a.slices; i += width) top = fmaxf(top, __ldcg(a.top + slot + i));
+            for (int i = sub + width; i < a.slices; i += width) top = fmaxf(top, load_l2(a.top + slot + i));
         for (int o = width / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const bool some = fabsf(top) <= 3.402823466e38f;
         if (some) {  // (a factor's error is one of 32 bits, as an exponential's)
             if (first_top > neg_inf()) total = first_sum * (double)expf(first_top - top);
-            for (int i = sub + width; i < a.slices; i += width) total += __ldcg(a.sum + slot + i) * (double)expf(__ldcg(a.top + slot + i) - top);
+            for (int i = sub + width; i < a.slices; i += width) total += load_l2(a.sum + slot + i) * (double)expf(load_l2(a.top + slot + i) - top);
         }
         for (int o = width / 2; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         if (sub == 0 && there) {
@@ -467,9 +467,9 @@ __device__ __forceinline__ void beam_pick(const BeamArgs &a, int64_t b) {
             if (s == 0 && at == 0) h.score = ordered(base[k]), h.token = (uint32_t)a.end_token;
         } else if (state[k] == 1) {
             const int64_t slot = b * lists + l;
-            if (at < __ldcg(a.count + slot)) {
-                h.score = ordered(base[k] + (double)__ldcg(a.value + slot * a.beams + at));
-                h.token = (uint32_t)__ldcg(a.token + slot * a.beams + at);
+            if (at < load_l2(a.count + slot)) {
+                h.score = ordered(base[k] + (double)load_l2(a.value + slot * a.beams + at));
+                h.token = (uint32_t)load_l2(a.token + slot * a.beams + at);
             }
         }
         return h;
@@ -528,8 +528,8 @@ __device__ __forceinline__ void beam_pick(const BeamArgs &a, int64_t b) {
             bool more = hand_in(row_of[r], value[r], token[r]) && at[r] == deep - 1 && state[row_of[r]] == 1;
             for (int next = deep; more && next < count[r]; ++next) {
                 const int64_t slot = (b * lists + list[r]) * a.beams + next;
-                const float v = __ldcg(a.value + slot);
-                more = can_reach(row_of[r], v, bound) && hand_in(row_of[r], v, __ldcg(a.token + slot));
+                const float v = load_l2(a.value + slot);
+                more = can_reach(row_of[r], v, bound) && hand_in(row_of[r], v, load_l2(a.token + slot));
             }
         }
         __syncthreads();
@@ -578,7 +578,7 @@ __device__ __forceinline__ void beam_pick(const BeamArgs &a, int64_t b) {
     }
 }
 
-__global__ void __launch_bounds__(kBeamThreads) k_beam_pick(const __grid_constant__ BeamArgs a) {
+__global__ void __launch_bounds__(kBeamThreads, 4) k_beam_pick(const __grid_constant__ BeamArgs a) {
     beam_pdl_wait();
     beam_pdl_launch();
     beam_pick(a, blockIdx.x);
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kBeamThreads) k_beam_pick(const __grid_constan
 // Both in one, where a cluster holds a sequence's slices: its first CTA picks when all have
 // left theirs.
 constexpr int kCluster = 8;
-template <typename T> __global__ void __launch_bounds__(kBeamThreads) k_beam_cluster(const __grid_constant__ BeamArgs a) {
+template <typename T> __global__ void __launch_bounds__(kBeamThreads, 3) k_beam_cluster(const __grid_constant__ BeamArgs a) {
     beam_pdl_wait();
     beam_pdl_launch();
     beam_slice<T>(a, blockIdx.x, blockIdx.y, blockIdx.z);
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(kBeamThreads) k_reorder(const __grid_constant_
     const ck_beam_state &s = a.s[i];
     const int64_t rows = (c - a.start[i]) / a.chunks[i], piece = (c - a.start[i]) - rows * a.chunks[i];
     const int64_t b = rows / a.beams, j = rows - b * a.beams;
-    const int64_t p = __ldg(a.parents + b * a.beams + j);
+    const int64_t p = a.parents[b * a.beams + j];
     const int64_t at = piece * kRowChunk;
     const int n = (int)(s.bytes - at < kRowChunk ? s.bytes - at : kRowChunk);
     const char *from = p >= 0 && p < a.K ? (const char *)s.in + b * s.in_row + p * s.in_beam + at : nullptr;
@@ -712,13 +712,13 @@ template <typename W> __device__ __forceinline__ void move_rows(const StateList 
     const W zero{};
     for (int i = threadIdx.x; i < a.beams * words; i += kBeamThreads) {
         const int j = i / words, w = i - j * words;
-        const int64_t p = __ldg(a.parents + b * a.beams + j);
+        const int64_t p = a.parents[b * a.beams + j];
         if (p == j) continue;
         ((W *)((char *)s.out + b * s.out_row + j * s.out_beam + at))[w] = p >= 0 && p < a.K ? held[p * words + w] : zero;
     }
 }
 
-__global__ void __launch_bounds__(kBeamThreads) k_reorder_in_place(const __grid_constant__ StateList a, int piece_bytes) {
+__global__ void __launch_bounds__(kBeamThreads, 4) k_reorder_in_place(const __grid_constant__ StateList a, int piece_bytes) {
     __shared__ uint4 held[32768 / 16];
     beam_pdl_wait();
     beam_pdl_launch();

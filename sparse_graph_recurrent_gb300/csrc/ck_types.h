@@ -21,6 +21,32 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(f
 }
 template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 
+// Loads of what a kernel before wrote, where this one starts before that ends: of memory as it
+// is after the wait for it, so none by way of the caches for what nobody writes (those are
+// defined where memory stays as it is for the kernel's life, which began before the wait), and
+// volatile where they are not plain ones, so that none is moved before the wait.
+// From L2.
+template <typename T> __device__ __forceinline__ T load_l2(const T *p) {
+    static_assert(sizeof(T) == 4 || sizeof(T) == 8, "a word or two");
+    T r;
+    if constexpr (sizeof(T) == 4) {
+        uint32_t w;
+        asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(w) : "l"(p));
+        memcpy(&r, &w, 4);
+    } else {
+        uint2 w;
+        asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+        memcpy(&r, &w, 8);
+    }
+    return r;
+}
+// What is not read again.
+__device__ __forceinline__ uint4 load_once(const uint4 *p) {
+    uint4 r;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
 // Elements of 16 bytes.
 template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
 
@@ -32,10 +58,10 @@ __device__ __forceinline__ uint4 load_vec(const T *line, int64_t e, int64_t leng
     constexpr int E = kVec<T>;
     const T *p = line + e;
     const uint32_t off = (uint32_t)(uintptr_t)p & 15u;
-    if (off == 0) return __ldcs((const uint4 *)p);
+    if (off == 0) return load_once((const uint4 *)p);
     const uint4 *lo = (const uint4 *)((uintptr_t)p - off);
     if ((const char *)lo >= (const char *)line && (const char *)(lo + 2) <= (const char *)(line + length)) {
-        const uint4 u = __ldg(lo), v = __ldg(lo + 1);
+        const uint4 u = lo[0], v = lo[1];
         uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
         if (off & 8) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = w[7];
         if (off & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];

@@ -5,9 +5,9 @@
 //
 // The tensors are cut into chunks of kChunkBytes, numbered through, and every CTA takes a
 // run of them.  The first kernel leaves a sum for each CTA; the second, launched so that it
-// starts while the first ends, reads its first chunk, adds up the CTAs' sums (each CTA for
-// itself, in one order, so that results repeat) and scales its run from the end, where
-// memory read last is still in L2.
+// takes its places while the first ends, adds up the CTAs' sums (each CTA for itself, in one
+// order, so that results repeat) and scales its run from the end, where memory read last is
+// still in L2.
 //
 // The list of tensors is an argument of the kernels: nothing is copied, and a captured
 // call holds it.
@@ -91,15 +91,15 @@ template <typename L> __device__ __forceinline__ void chunk_load(const L &a, con
     const uint4 *p = (const uint4 *)((const char *)a.in[w.i] + (w.body << (a.dtype[w.i] == CK_F32 ? 2 : 1))) + threadIdx.x;
     if (last && w.vecs == kClipThreads * kClipVecs) {
 #pragma unroll
-        for (int j = 0; j < kClipVecs; ++j) v[j] = __ldcs(p + j * kClipThreads);
+        for (int j = 0; j < kClipVecs; ++j) v[j] = load_once(p + j * kClipThreads);
     } else if (w.vecs == kClipThreads * kClipVecs) {
 #pragma unroll
-        for (int j = 0; j < kClipVecs; ++j) v[j] = __ldg(p + j * kClipThreads);
+        for (int j = 0; j < kClipVecs; ++j) v[j] = p[j * kClipThreads];
     } else {
 #pragma unroll
         for (int j = 0; j < kClipVecs; ++j) {
             v[j] = make_uint4(0, 0, 0, 0);
-            if ((int)threadIdx.x + j * kClipThreads < w.vecs) v[j] = __ldg(p + j * kClipThreads);
+            if ((int)threadIdx.x + j * kClipThreads < w.vecs) v[j] = p[j * kClipThreads];
         }
     }
 }
@@ -240,7 +240,7 @@ __device__ __forceinline__ Factor factor_of(const double *sums, int all, double 
     __shared__ Factor f;
     if (threadIdx.x < 32) {
         double s = 0;
-        for (int i = threadIdx.x; i < all; i += 32) s += __ldcg(sums + i);
+        for (int i = threadIdx.x; i < all; i += 32) s += load_l2(sums + i);
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (threadIdx.x == 0) {
@@ -297,11 +297,9 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas) k_clip(const __grid_c
     // a chunk ahead is under way while one is scaled
     uint4 v[kClipVecs], next[kClipVecs];
     Where w{}, then{};
-    if (hi > lo) {
-        w = locate(a, hi - 1, 0);
-        chunk_load(a, w, true, v);
-    }
+    if (hi > lo) w = locate(a, hi - 1, 0);
     pdl_wait();
+    if (hi > lo) chunk_load(a, w, true, v);
     const Factor all = factor_of(a.sums, a.all, a.max_norm);
     const float factor = all.by;
     if (blockIdx.x == 0 && a.first == 0 && threadIdx.x == 0) *a.norm = all.norm;
@@ -482,8 +480,8 @@ ck_status run_clip(const ck_gradient *list, int64_t count, bool clip, double max
         e = launch_after(k_norm_end<MOST>, 1, a, launches > 0, s);
         return e == cudaSuccess ? CK_OK : cuda_fail(e, "k_norm_end launch");
     }
-    // The first of the second kernels may start early: all it reads before it waits are
-    // gradients, which no kernel of this call has written yet.
+    // The first of the second kernels may start early: it waits before it reads what another has
+    // written.  (With its first chunk read before that, 98 us of the largest case were 98 too.)
     bool early = true;
     for (int64_t at = 0; at < count && e == cudaSuccess;) {
         if (launches > 1) at = fill(a, list, count, at);

@@ -100,7 +100,7 @@ template <int SHIFT, typename T, int V> __device__ __forceinline__ void store_pa
 // one: they are loaded and stored.
 template <int N> __device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
     if constexpr (N == 2) {
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(__ldg((const uint16_t *)from)) : "memory");
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(*(const uint16_t *)from) : "memory");
     } else if constexpr (N == 16) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
     } else {
@@ -145,7 +145,7 @@ template <int V> struct Nodes {
         for (int v = 0; v < V; ++v) {
             len[v] = v < count ? (int)a.T : 0;
             if (a.lengths && v < count) {
-                const int64_t l = __ldg(a.lengths + (uint32_t)(c + v) / (uint32_t)a.N);
+                const int64_t l = a.lengths[(uint32_t)(c + v) / (uint32_t)a.N];
                 len[v] = l < 0 ? 0 : l < a.T ? (int)l : (int)a.T;
             }
             most = len[v] > most ? len[v] : most;
@@ -441,7 +441,7 @@ __device__ __forceinline__ void through_chunks(const GatedArgs &a, const Nodes<V
         const float2 *p = a.maps + (int64_t)(REVERSE ? hi - 1 - i : lo + i) * C + at.c;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (at.has(v)) m[v] = compose(__ldcg(p + v), m[v]);
+            if (at.has(v)) m[v] = compose(load_l2(p + v), m[v]);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) ex.m[warp][v][lane] = m[v];
@@ -469,7 +469,7 @@ __device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at,
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if (!at.has(v)) continue;
-            const float2 p = __ldcg(a.inner + part * C + at.c + v);
+            const float2 p = load_l2(a.inner + part * C + at.c + v);
             carry[v] = fmaf(p.x, carry[v], p.y);
         }
         return;
@@ -616,7 +616,7 @@ __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArg
     const Part part(a, wt);
     float h[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = !MAPS && a.state0 && at.has(v) ? __ldg(a.state0 + at.c + v) : 0.f;
+    for (int v = 0; v < V; ++v) h[v] = !MAPS && a.state0 && at.has(v) ? a.state0[at.c + v] : 0.f;
     exchange<V, MAPS, false>(a, at, ex, h, [&](float2 (&m)[V]) {
         in.each(part.hi - 1, part.hi - part.lo, -1, at.warp_most, [&](int k) {
             const int t0 = k * kSteps;
@@ -753,7 +753,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 ? 112 : 128) k_gated_backward(const _
     };
     float r[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) r[v] = !MAPS && a.dstate && at.has(v) ? __ldg(a.dstate + at.c + v) : 0.f;
+    for (int v = 0; v < V; ++v) r[v] = !MAPS && a.dstate && at.has(v) ? a.dstate[at.c + v] : 0.f;
     exchange<V, MAPS, true>(a, at, ex, r, [&](float2 (&m)[V]) {
         BackwardRing<T, V, SHIFT, true> in;
         begin(in);

@@ -195,3 +195,56 @@ def test_as_many_beams_and_tokens_as_there_may_be(dtype, K, V):
     all_of_them = scores[0].double()[:, None] + top.values.double() - base[:, None]
     best = torch.topk(all_of_them.flatten(), 64).values
     assert (got[0][0].double() - best).abs().max() <= so.beam_score_off(V) + 2 * so.U32 * float(best.abs().max())
+
+
+# -- calls in a row, each on what the one before has written -----------------------------------
+
+
+@pytest.mark.parametrize("n", [300, 70_000, 3_000_000])
+def test_clipped_again_and_again(n):
+    """The kernels of a call take their places while those before end; what they read was written
+    by the call before, at the same places."""
+    import sparse_graph_recurrent_gb300 as ck
+    g = torch.Generator().manual_seed(n)
+    start = [torch.randn(n, generator=g).cuda(), torch.randn(n // 3, generator=g).bfloat16().cuda()]
+    limits = [300.0, 200.0, 30.0, 10.0, 9.0, 1.0, 0.7, 0.3]
+
+    def run(wait):
+        grads, norms = [t.clone() for t in start], []
+        for limit in limits:
+            norms.append(ck.clip_gradients(grads, limit))
+            if wait:
+                torch.cuda.synchronize()
+        return grads, norms
+    want, norms = run(True)
+    for _ in range(20):
+        got, n2 = run(False)
+        assert all(torch.equal(a, b) for a, b in zip(got + n2, want + norms))
+
+
+def test_searched_again_and_again():
+    """Scores, parents, ends and lengths that the kernels before have just written."""
+    import sparse_graph_recurrent_gb300 as ck
+    g = torch.Generator().manual_seed(3)
+    embed, gates = (torch.randn(50, 64, generator=g).cuda() for _ in range(2))
+    read = torch.randn(64, 50, generator=g).cuda()
+
+    def run(wait):
+        torch.cuda.synchronize()
+        state = torch.zeros(3, 8, 64, device="cuda")
+        scores, ended = torch.zeros(3, 8, device="cuda"), torch.zeros(3, 8, dtype=torch.bool, device="cuda")
+        all_of_it = []
+        for _ in range(12):
+            logits = (state.view(24, 64) @ read).view(3, 8, 50)
+            scores, parents, tokens, ended = ck.beam_select(logits, scores, ended, 7)
+            ck.reorder_states(state, parents, out=state)
+            out, new = ck.gated_recurrence(embed[tokens.view(-1)][None], gates[tokens.view(-1)][None], state.view(24, 64),
+                                           (~ended).long().view(-1))
+            state = new.view(3, 8, 64)
+            all_of_it += [scores, parents, tokens, ended, out, state]
+            if wait:
+                torch.cuda.synchronize()
+        return all_of_it
+    want = run(True)
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))
