@@ -405,9 +405,18 @@ __device__ __forceinline__ float not_lost(float product, bool nonzero) {
     return product == 0.f && nonzero ? copysignf(__int_as_float(1), product) : product;
 }
 
-__device__ __forceinline__ float2 compose(float2 later, float2 earlier) {
-    return make_float2(not_lost(later.x * earlier.x, later.x != 0.f && earlier.x != 0.f),
-                       fmaf(later.x, earlier.y, later.y));
+// A decay's product that has come below the normal numbers and up again may have been anything
+// in between, and what it leaves of a number above 2^23 may be anything up to 2^-126: the map's
+// factor is NaN then.
+constexpr float kLeast = 1.17549435e-38f, kMost = 3.402823466e38f;  // normal numbers
+constexpr float kLarge = 8388608.f;                                 // 2^23
+template <bool LEAK> __device__ __forceinline__ float2 compose(float2 later, float2 earlier) {
+    float by = not_lost(later.x * earlier.x, later.x != 0.f && earlier.x != 0.f);
+    if constexpr (!LEAK) {
+        const bool low = fabsf(later.x) < kLeast, regrown = (low | (fabsf(earlier.x) < kLeast)) & (fabsf(by) >= kLeast);
+        by = regrown | (low & (fabsf(earlier.y) > kLarge)) ? __int_as_float(0x7fffffff) : by;
+    }
+    return make_float2(by, fmaf(later.x, earlier.y, later.y));
 }
 
 // The maps of the warps' parts.
@@ -416,32 +425,107 @@ template <int V> struct Exchange {
 };
 
 // The blocks [lo, hi) of a part.
+__device__ __forceinline__ int first_block(const GatedArgs &a, int part) { return part * a.each + (part < a.more ? part : a.more); }
 struct Part {
     int lo, hi, i;
     __device__ __forceinline__ Part(const GatedArgs &a, int wt) {
         i = (blockIdx.y << a.wt_shift) + wt;
-        lo = i * a.each + (i < a.more ? i : a.more);
+        lo = first_block(a, i);
         hi = lo + a.each + (i < a.more);
     }
 };
 
+// What maps that a state is carried through say of it.  Decays beyond 1 take a map out of 32 bits
+// where the states may stay inside (they are 0, or begin low): what comes out of it is not finite,
+// and stays so.  And what is left of a product below the normal numbers says little of a state
+// above 2^23.
+template <int V> struct Trust {
+    float most[V], least[V];  // of the states', the maps' magnitudes
+    __device__ __forceinline__ Trust() {
+#pragma unroll
+        for (int v = 0; v < V; ++v) most[v] = 0.f, least[v] = 1.f;
+    }
+    __device__ __forceinline__ void through(int v, float2 map, float &carry) {
+        most[v] = fmaxf(most[v], fabsf(carry));
+        least[v] = fminf(least[v], fabsf(map.x));
+        carry = fmaf(map.x, carry, map.y);
+    }
+    __device__ __forceinline__ bool holds(int v, float carry) const {
+        return fabsf(carry) <= kMost && (most[v] <= kLarge || least[v] >= kLeast);
+    }
+};
+
+// Node c's state after the steps of blocks [lo, hi), or in REVERSE its gradient before them, step
+// by step in the decay form.
+template <typename T, bool REVERSE>
+__device__ __forceinline__ float walk(const GatedArgs &a, int64_t c, int len, int lo, int hi, float carry) {
+    const int64_t b = (uint32_t)c / (uint32_t)a.N, n = c - b * a.N;
+    const T *gate = (const T *)a.gate + b * a.gb + n;
+    const int t0 = lo * kSteps, t1 = hi * kSteps < len ? hi * kSteps : len;
+    if constexpr (REVERSE) {
+        const T *d = (const T *)a.dout + b * a.db + n;
+#pragma unroll 8
+        for (int t = t1 - 1; t >= t0; --t)
+            carry = to_float(gate[t * a.gt]) * (carry + (a.dout ? to_float(d[t * a.dt]) : 0.f));
+    } else {
+        const T *x = (const T *)a.x + b * a.xb + n;
+#pragma unroll 8
+        for (int t = t0; t < t1; ++t) carry = fmaf(to_float(gate[t * a.gt]), carry, to_float(x[t * a.xt]));
+    }
+    return carry;
+}
+
+// What is carried into blocks [lo, hi), where the maps do not hold: by those of the chunks that do,
+// and step by step.  (65,536 x 256 fp32, forward: 44 us where they hold; 0.2 ms with a NaN halfway; 9 ms
+// with decays of 2 throughout, whose states only stay inside 32 bits where they are 0.)
+template <typename T, bool REVERSE>
+__device__ __noinline__ float carried_by_steps(const GatedArgs &a, int64_t c, int len, int lo, int hi) {
+    const float *from = REVERSE ? a.dstate : a.state0;
+    float carry = from ? from[c] : 0.f;
+    const int own = blockIdx.y, chunks = gridDim.y;
+#pragma unroll 1
+    for (int i = 0; i < (REVERSE ? chunks - 1 - own : own) + 1; ++i) {
+        const int chunk = REVERSE ? chunks - 1 - i : i;
+        int first = first_block(a, chunk << a.wt_shift), last = first_block(a, (chunk + 1) << a.wt_shift);
+        if (chunk == own) {
+            (REVERSE ? first : last) = REVERSE ? hi : lo;
+        } else {
+            const float2 m = load_l2(a.maps + chunk * (a.B * a.N) + c);
+            const float by = fabsf(m.x), size = fabsf(carry);
+            if (by <= kMost && fabsf(m.y) <= kMost && (by >= kLeast || size <= kLarge || size > kMost)) {
+                carry = fmaf(m.x, carry, m.y);
+                continue;
+            }
+        }
+        if (carry != carry) break;  // and stays so
+        carry = walk<T, REVERSE>(a, c, len, first, last, carry);
+    }
+    return carry;
+}
+
 // carry through the maps of chunks [first, last), the warps along the steps taking some
 // each.  REVERSE: a later chunk's map is applied first.
-template <int V, bool REVERSE>
+template <int V, bool LEAK, bool REVERSE>
 __device__ __forceinline__ void through_chunks(const GatedArgs &a, const Nodes<V> &at, int first, int last,
-                                               Exchange<V> &ex, float (&carry)[V]) {
+                                               Exchange<V> &ex, Trust<V> &trust, float (&carry)[V]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp & (a.wt - 1);
     const int n = last - first, lo = first + (n * wt >> a.wt_shift), hi = first + (n * (wt + 1) >> a.wt_shift);
     const int64_t C = a.B * a.N;
     float2 m[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) m[v] = make_float2(1.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < hi - lo; ++i) {
-        const float2 *p = a.maps + (int64_t)(REVERSE ? hi - 1 - i : lo + i) * C + at.c;
+    for (int i = 0; i < hi - lo; i += 4) {
+        float2 q[4][V];  // four are under way at once
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (at.has(v)) m[v] = compose(load_l2(p + v), m[v]);
+        for (int u = 0; u < 4; ++u) {
+            const float2 *p = a.maps + (int64_t)(REVERSE ? hi - 1 - i - u : lo + i + u) * C + at.c;
+#pragma unroll
+            for (int v = 0; v < V; ++v) q[u][v] = i + u < hi - lo && at.has(v) ? load_l2(p + v) : make_float2(1.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int v = 0; v < V; ++v) m[v] = compose<LEAK>(q[u][v], m[v]);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) ex.m[warp][v][lane] = m[v];
@@ -451,26 +535,25 @@ __device__ __forceinline__ void through_chunks(const GatedArgs &a, const Nodes<V
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const float2 p = ex.m[base + (REVERSE ? a.wt - 1 - j : j)][v][lane];
-            carry[v] = fmaf(p.x, carry[v], p.y);
+            trust.through(v, p, carry[v]);
         }
 }
 
 // What is carried into this warp's part.  MAPS: composes the part with part_map(m) and
 // leaves the maps; otherwise carry goes through all that comes before.
-template <int V, bool MAPS, bool REVERSE, typename F>
-__device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at, Exchange<V> &ex,
+template <int V, bool LEAK, bool MAPS, bool REVERSE, typename F>
+__device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at, Exchange<V> &ex, Trust<V> &trust,
                                          float (&carry)[V], F part_map) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp & (a.wt - 1), base = warp - wt;
     const int64_t C = a.B * a.N;
     const int64_t part = (int64_t)blockIdx.y * a.wt + wt;
     if (!MAPS && gridDim.y > 1 && !a.cluster) {
         if (REVERSE ? blockIdx.y + 1 < gridDim.y : blockIdx.y > 0)
-            through_chunks<V, REVERSE>(a, at, REVERSE ? blockIdx.y + 1 : 0, REVERSE ? gridDim.y : blockIdx.y, ex, carry);
+            through_chunks<V, LEAK, REVERSE>(a, at, REVERSE ? blockIdx.y + 1 : 0, REVERSE ? gridDim.y : blockIdx.y, ex, trust, carry);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if (!at.has(v)) continue;
-            const float2 p = load_l2(a.inner + part * C + at.c + v);
-            carry[v] = fmaf(p.x, carry[v], p.y);
+            trust.through(v, load_l2(a.inner + part * C + at.c + v), carry[v]);
         }
         return;
     }
@@ -490,28 +573,28 @@ __device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at,
         for (int v = 0; v < V; ++v) p[v] = make_float2(1.f, 0.f);
         for (int j = 0; j < before; ++j)
 #pragma unroll
-            for (int v = 0; v < V; ++v) p[v] = compose(ex.m[base + (REVERSE ? a.wt - 1 - j : j)][v][lane], p[v]);
+            for (int v = 0; v < V; ++v) p[v] = compose<LEAK>(ex.m[base + (REVERSE ? a.wt - 1 - j : j)][v][lane], p[v]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if (!at.has(v)) continue;
             if (MAPS) a.inner[part * C + at.c + v] = p[v];
-            if (before == a.wt - 1) a.maps[(int64_t)blockIdx.y * C + at.c + v] = compose(m[v], p[v]);
+            if (before == a.wt - 1) a.maps[(int64_t)blockIdx.y * C + at.c + v] = compose<LEAK>(m[v], p[v]);
         }
         if constexpr (!MAPS) {
             // all of the cluster's maps are there after this
             asm volatile("barrier.cluster.arrive.release;" ::: "memory");
             asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
             if (REVERSE ? blockIdx.y + 1 < gridDim.y : blockIdx.y > 0)
-                through_chunks<V, REVERSE>(a, at, REVERSE ? blockIdx.y + 1 : 0, REVERSE ? gridDim.y : blockIdx.y, ex, carry);
+                through_chunks<V, LEAK, REVERSE>(a, at, REVERSE ? blockIdx.y + 1 : 0, REVERSE ? gridDim.y : blockIdx.y, ex, trust, carry);
 #pragma unroll
-            for (int v = 0; v < V; ++v) carry[v] = fmaf(p[v].x, carry[v], p[v].y);
+            for (int v = 0; v < V; ++v) trust.through(v, p[v], carry[v]);
         }
     } else {
         for (int j = 0; j < before; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float2 q = ex.m[base + (REVERSE ? a.wt - 1 - j : j)][v][lane];
-                carry[v] = fmaf(q.x, carry[v], q.y);
+                trust.through(v, q, carry[v]);
             }
     }
 }
@@ -563,7 +646,7 @@ __device__ __forceinline__ void forward_map(const R &in, const Nodes<V> &at, int
         multiply_add(plus, keep, plus, put);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) all[v] = compose(all[v], make_float2(not_lost(by[v], least[v] > 0.f), plus[v]));
+    for (int v = 0; v < V; ++v) all[v] = compose<LEAK>(all[v], make_float2(not_lost(by[v], least[v] > 0.f), plus[v]));
 }
 
 // One block's steps from the state h on.
@@ -617,7 +700,8 @@ __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArg
     float h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = !MAPS && a.state0 && at.has(v) ? a.state0[at.c + v] : 0.f;
-    exchange<V, MAPS, false>(a, at, ex, h, [&](float2 (&m)[V]) {
+    Trust<V> trust;
+    exchange<V, LEAK, MAPS, false>(a, at, ex, trust, h, [&](float2 (&m)[V]) {
         in.each(part.hi - 1, part.hi - part.lo, -1, at.warp_most, [&](int k) {
             const int t0 = k * kSteps;
             if (t0 + kSteps <= at.least)
@@ -627,6 +711,11 @@ __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArg
         });
     });
     if constexpr (!MAPS) {
+        if constexpr (!LEAK) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (at.has(v) && !trust.holds(v, h[v])) h[v] = carried_by_steps<T, false>(a, at.c + v, at.len[v], part.lo, part.hi);
+        }
         T *out = (T *)a.out + (int64_t)part.lo * kSteps * C + at.c;
         float *kept = a.kept + (int64_t)part.lo * C + at.c;
         in.each(part.lo, part.hi - part.lo, 1, at.warp_most, [&](int k) {
@@ -674,7 +763,7 @@ __device__ __forceinline__ void backward_map(const R &in, const Nodes<V> &at, in
         multiply(plus, keep, sum);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) all[v] = compose(all[v], make_float2(not_lost(by[v], least[v] > 0.f), plus[v]));
+    for (int v = 0; v < V; ++v) all[v] = compose<LEAK>(all[v], make_float2(not_lost(by[v], least[v] > 0.f), plus[v]));
 }
 
 // One block's gradients, r being that of the state after it.
@@ -754,7 +843,8 @@ __global__ void __maxnreg__(sizeof(T) == 4 ? 112 : 128) k_gated_backward(const _
     float r[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) r[v] = !MAPS && a.dstate && at.has(v) ? a.dstate[at.c + v] : 0.f;
-    exchange<V, MAPS, true>(a, at, ex, r, [&](float2 (&m)[V]) {
+    Trust<V> trust;
+    exchange<V, LEAK, MAPS, true>(a, at, ex, trust, r, [&](float2 (&m)[V]) {
         BackwardRing<T, V, SHIFT, true> in;
         begin(in);
         in.each(part.lo, part.hi - part.lo, 1, at.warp_most, [&](int k) {
@@ -766,6 +856,11 @@ __global__ void __maxnreg__(sizeof(T) == 4 ? 112 : 128) k_gated_backward(const _
         });
     });
     if constexpr (!MAPS) {
+        if constexpr (!LEAK) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (at.has(v) && !trust.holds(v, r[v])) r[v] = carried_by_steps<T, true>(a, at.c + v, at.len[v], part.lo, part.hi);
+        }
         BackwardRing<T, V, SHIFT, false> in;
         begin(in);
         in.tensor(2, a.x, a.xt, a.xb);

@@ -173,9 +173,9 @@ def gated_recurrence(x, gate, state0=None, lengths=None, form: str = "leak"):
     x is float32, bfloat16 or float16, gate is of its type and of its shape or expands to
     it; state0 is float32 [B, N] (zeros by default) and so is state, whatever x's type.
     lengths, int64 [B]: from step lengths[b] on the state stays as it is, out is 0 and x
-    and gate do not matter.  Where long sequences are cut along their steps, products of
-    gates over runs of steps are formed: a decay's must stay inside 32 bits.  Differentiable
-    (once) in x, gate and state0."""
+    and gate do not matter.  Decays may lie beyond 1 as long as the states stay inside 32 bits;
+    where long sequences are cut along their steps, runs whose product of decays does not are
+    gone through step by step, which is slow.  Differentiable (once) in x, gate and state0."""
     got = (_ck._native or _ck.native()).gated(x, gate, state0, lengths, form, False)
     if got is not None:
         return got[:2]

@@ -248,3 +248,92 @@ def test_searched_again_and_again():
     want = run(True)
     for _ in range(10):
         assert all(torch.equal(a, b) for a, b in zip(run(False), want))
+
+
+# -- decays beyond 1 -------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T,B,N", [(600, 1, 40), (2000, 3, 4000), (2000, 1, 70), (1100, 2, 601), (9000, 1, 33), (40_000, 1, 6)])
+def test_decays_whose_products_leave_32_bits(T, B, N, dtype):
+    """States that stay inside 32 bits although the products of decays do not: 0 where nothing has
+    come in yet, or begun low.  Steps one after another give them; however they are cut does too."""
+    import sparse_graph_recurrent_gb300 as ck
+    g, dt = torch.Generator().manual_seed(T), TYPES[dtype]
+    gate = torch.full((T, B, N), 2.0, dtype=dt, device="cuda")
+    x, d_out = torch.zeros_like(gate), torch.zeros_like(gate)
+    x[-20:] = torch.randn(20, B, N, generator=g).cuda()
+    d_out[:20] = torch.randn(20, B, N, generator=g).cuda()
+    out, state, kept = ck.gated_recurrence_forward(x, gate, None, None, "decay")
+    assert not out[:-20].any()
+    want, off = so.gated(host(x[-20:]), host(gate[-20:]), None, None, "decay")
+    so.within(host(out[-20:]), want["out"], off["out"], dtype)
+    so.within(host(state), want["state"], off["state"])
+    dx, dgate, dstate0 = ck.gated_recurrence_backward(x, gate, kept, d_out, None, None, "decay")
+    want, off = so.gated(host(x[:20]), host(gate[:20]), None, None, "decay", host(d_out[:20]))
+    so.within(host(dx[:20]), want["dx"], off["dx"], dtype)
+    so.within(host(dstate0), want["dstate0"], off["dstate0"])
+    assert not dx[20:].any() and not dgate.any()
+    # from 2^-100 up by more than 32 bits hold, down again, and so on: powers of 2, and exact
+    t = torch.arange(T) % 400
+    power = torch.where(t < 200, t + 1, 399 - t).double() - 100
+    powers = torch.exp2(power).to(dt).view(T, 1, 1).expand(T, B, N).cuda()
+    gate = torch.where(t < 200, 2.0, 0.5).to(dt).view(T, 1, 1).expand(T, B, N).contiguous().cuda()
+    zero = torch.zeros_like(gate)
+    start = torch.full((B, N), 2.0 ** -100, device="cuda")
+    out, state, kept = ck.gated_recurrence_forward(zero, gate, start, None, "decay")
+    assert torch.equal(out, powers)
+    last = torch.full((B, N), 2.0 ** -float(power[-1]), device="cuda")
+    dx, dgate, dstate0 = ck.gated_recurrence_backward(zero, gate, kept, None, last, None, "decay")
+    assert (dstate0 == 2.0 ** 100).all()
+    assert torch.equal(dx, torch.exp2(-power).to(dt).view(T, 1, 1).expand(T, B, N).cuda())
+    # the same where the last sequence ends before the others
+    lengths = torch.full((B,), T, device="cuda")
+    lengths[-1] = T - 137
+    gate[T - 137:, -1] = float("nan")
+    out, state, kept = ck.gated_recurrence_forward(zero, gate, start, lengths, "decay")
+    assert torch.equal(out[:, :-1], powers[:, :-1]) and torch.equal(out[:T - 137, -1], powers[:T - 137, -1])
+    assert not out[T - 137:, -1].any() and (state[-1] == 2.0 ** float(power[T - 138])).all()
+    last[-1] = 2.0 ** -float(power[T - 138])
+    dx, dgate, dstate0 = ck.gated_recurrence_backward(zero, gate, kept, None, last, lengths, "decay")
+    assert (dstate0 == 2.0 ** 100).all() and not dx[T - 137:, -1].any()
+
+
+@pytest.mark.parametrize("T", [700, 9000])
+def test_an_infinite_input_reaches_what_it_would_step_by_step(T):
+    import sparse_graph_recurrent_gb300 as ck
+    d = inputs(T, 2, 33, "float32", "decay")
+    d["x"][T // 3, 0, 5] = float("inf")
+    d["x"][T // 2, 1, 7] = float("nan")
+    d["gate"][2 * T // 3, 0, 5] = 0.0  # infinity times 0
+    out, state, kept = ck.gated_recurrence_forward(d["x"], d["gate"], d["state0"], None, "decay")
+    h = d["state0"].double()
+    for t in range(T):
+        h = d["gate"][t].double() * h + d["x"][t].double()
+        if t in (0, T // 3, T // 2, 2 * T // 3 - 1, 2 * T // 3, T - 1):
+            assert torch.equal(out[t].isnan(), h.isnan()) and torch.equal(out[t].isinf(), h.isinf())
+    d["d_out"][T // 2, 1, 9] = float("inf")
+    dx = ck.gated_recurrence_backward(d["x"], d["gate"], kept, d["d_out"], d["d_state"], None, "decay")[0]
+    assert dx[:T // 2 + 1, 1, 9].isinf().all() and dx[T // 2 + 1:].isfinite().all()
+
+
+@pytest.mark.parametrize("T,B,N", [(2000, 3, 4000), (2000, 1, 70), (9000, 1, 33)])
+def test_a_large_input_that_fades(T, B, N):
+    """2^100 comes in, and is halved and doubled again and again."""
+    import sparse_graph_recurrent_gb300 as ck
+    t = torch.arange(T) % 500
+    for at in (0, 37, T // 2, T - 300):
+        x = torch.zeros(T, B, N, device="cuda")
+        x[at] = 2.0 ** 100
+        n = (torch.arange(T) - at) % 400
+        gate = torch.where((n > 0) & (n <= 200), 0.5, 2.0)
+        gate[:at + 1] = 1
+        power = 100 - torch.where(n <= 200, n, 400 - n).double()
+        want = torch.where(torch.arange(T) < at, 0.0, torch.exp2(power)).float().view(T, 1, 1).expand(T, B, N).cuda()
+        gate = gate.view(T, 1, 1).expand(T, B, N).contiguous().cuda()
+        assert torch.equal(ck.gated_recurrence(x, gate, None, None, "decay")[0], want)
+        # and the other way round: a gradient
+        x, gate = x.flip(0), torch.cat((gate[1:], gate[:1] * 0 + 1)).flip(0)
+        zero = torch.zeros_like(x)
+        kept = ck.gated_recurrence_forward(zero, gate, None, None, "decay")[2]
+        assert torch.equal(ck.gated_recurrence_backward(zero, gate, kept, x, None, None, "decay")[0], want.flip(0))
