@@ -560,7 +560,7 @@ ck_status ck_beam_select(const ck_beam_call *call, void *stream);
  * sequences and beams lie in_row, in_beam (out_row, out_beam) bytes apart.  parents:
  * (device) int64[B][beams].  A parent outside [0, K) gives a row of zeros.  Either out is
  * in itself, with the same strides and beams == K, or the two do not overlap; no array's
- * out may overlap another's in or out.
+ * out may overlap another's in or out, or the parents.
  * Asynchronous.  Errors: CK_ERR_INVALID_ARG, CK_ERR_UNSUPPORTED (K or beams above 64,
  * B > 65535), CK_ERR_CUDA.
  */

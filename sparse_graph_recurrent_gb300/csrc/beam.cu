@@ -781,7 +781,7 @@ ck_status check_states(const ck_beam_state *list, int64_t count, const int64_t *
     if (!parents) return fail(CK_ERR_INVALID_ARG, "a required pointer is NULL");
     if (!aligned(parents, 8)) return fail(CK_ERR_INVALID_ARG, "states: a pointer is not aligned to its elements");
     std::vector<Extent> all;
-    all.reserve(2 * (size_t)count);
+    all.reserve(2 * (size_t)count + 1);
     for (int64_t i = 0; i < count; ++i) {
         const ck_beam_state &s = list[i];
         if (s.bytes < 0 || s.in_row < 0 || s.in_beam < 0 || s.out_row < 0 || s.out_beam < 0)
@@ -799,7 +799,8 @@ ck_status check_states(const ck_beam_state *list, int64_t count, const int64_t *
         all.push_back(extent_of(s.out, s.out_row, s.out_beam, B, beams, s.bytes, true));
         if (!own) all.push_back(extent_of(s.in, s.in_row, s.in_beam, B, K, s.bytes, false));
     }
-    if (states_tangled(all)) return fail(CK_ERR_INVALID_ARG, "states: an output overlaps another array");
+    all.push_back(extent_of(parents, beams * 8, 8, B, beams, 8, false));
+    if (states_tangled(all)) return fail(CK_ERR_INVALID_ARG, "states: an output overlaps another array or the parents");
     return CK_OK;
 }
 
