@@ -746,21 +746,34 @@ int unit_of(const ck_beam_state &s) {
     return 1;
 }
 
-// The bytes from an array's first to its last, [lo, hi); strides are not negative.
+// The bytes from an array's first to its last, [lo, hi); strides are not negative, and 0 along an
+// axis of one.
 struct Extent {
     uintptr_t lo, hi;
     bool written;
-    int64_t row, beam, bytes;
-    // Whether the two are columns of one array that do not meet.
+    int64_t row, beam, rows, beams, bytes;
+    // The bytes that it takes of every m, from where it begins on, or more than m.
+    int64_t of_every(int64_t m) const {
+        int64_t n = bytes;
+        for (const auto [stride, count] : {std::pair<int64_t, int64_t>{row, rows}, {beam, beams}})
+            if (stride % m) n = stride < m ? n + (count - 1) * stride : m + 1;
+        return n;
+    }
+    // Whether another, that begins no earlier, takes others of every so many bytes: columns of
+    // one array, or halves of its sequences.
     bool beside(const Extent &o) const {
-        if (row != o.row || beam != o.beam || beam <= 0 || row % beam) return false;
-        const int64_t d = (int64_t)((o.lo > lo ? o.lo - lo : lo - o.lo) % (uintptr_t)beam);
-        const int64_t first = o.lo > lo ? bytes : o.bytes, second = o.lo > lo ? o.bytes : bytes;
-        return d >= first && d + second <= beam;
+        for (const int64_t m : {row, beam, o.row, o.beam}) {
+            if (m <= 0) continue;
+            const int64_t apart = (int64_t)((o.lo - lo) % (uintptr_t)m);
+            if (apart >= of_every(m) && o.of_every(m) <= m - apart) return true;
+        }
+        return false;
     }
 };
 Extent extent_of(const void *p, int64_t row, int64_t beam, int64_t B, int64_t n, int64_t bytes, bool written) {
-    return Extent{(uintptr_t)p, (uintptr_t)p + (uintptr_t)((B - 1) * row + (n - 1) * beam + bytes), written, row, beam, bytes};
+    if (B == 1) row = 0;
+    if (n == 1) beam = 0;
+    return Extent{(uintptr_t)p, (uintptr_t)p + (uintptr_t)((B - 1) * row + (n - 1) * beam + bytes), written, row, beam, B, n, bytes};
 }
 
 // Whether what is written for one array is read or written for another.

@@ -337,3 +337,43 @@ def test_a_large_input_that_fades(T, B, N):
         zero = torch.zeros_like(x)
         kept = ck.gated_recurrence_forward(zero, gate, None, None, "decay")[2]
         assert torch.equal(ck.gated_recurrence_backward(zero, gate, kept, x, None, None, "decay")[0], want.flip(0))
+
+
+# -- reordering ------------------------------------------------------------------------------
+
+
+def test_two_halves_of_one_array():
+    """States and where they go side by side in one array, however its axes lie."""
+    import sparse_graph_recurrent_gb300 as ck
+    parents = torch.tensor([[1, 1, 0, 2], [2, 0, 2, 3], [3, 3, 1, 0]], device="cuda")
+    whole = lambda *n: torch.randn(*n, device="cuda")  # noqa: E731
+    for both in (whole(3, 2, 4, 33).unbind(1), whole(2, 3, 4, 33).unbind(0), whole(3, 4, 2, 33).unbind(2),
+                 [t.transpose(0, 1) for t in whole(4, 2, 3, 33).unbind(1)], whole(3, 5, 2, 4, 8).unbind(2)[0].unbind(1)[1:3],
+                 whole(3, 8, 33).split(4, 1), whole(3, 4, 66).split(33, 2)):
+        a, b = both
+        for source, to in ((a, b), (b, a)):
+            if source.shape[1] != 4:
+                continue
+            want, keep = gathered(source, parents), source.clone()
+            assert ck.reorder_states(source, parents, out=to) is to
+            assert torch.equal(to.cpu(), want) and torch.equal(source, keep)
+    # fewer go on than there were
+    line = whole(3, 7, 20)
+    want = gathered(line[:, :4], parents[:, :3])
+    ck.reorder_states(line[:, :4], parents[:, :3], out=line[:, 4:])
+    assert torch.equal(line[:, 4:].cpu(), want)
+    line = whole(3, 7, 20)
+    for source, to in ((line[:, :4], line[:, 3:7]), (line[:, :4, :12], line[:, :4, 8:]), (line[:, :4], line[:, 1:5])):
+        with pytest.raises(RuntimeError):
+            ck.reorder_states(source, parents, out=to)
+
+
+def test_parents_that_are_a_state_too():
+    import sparse_graph_recurrent_gb300 as ck
+    parents = torch.tensor([[1, 1, 0], [2, 0, 2]], device="cuda")
+    assert torch.equal(ck.reorder_states(parents, parents).cpu(), gathered(parents, parents))
+    keep = parents.clone()
+    for states, out in (([parents], [parents]), ([keep], [parents])):
+        with pytest.raises(RuntimeError):
+            ck.reorder_states(states, parents, out=out)
+    assert torch.equal(keep, parents)

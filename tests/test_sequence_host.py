@@ -32,3 +32,41 @@ def test_parents_are_not_written():
     for at in (P + size, P - size):  # beside them
         assert reorder([(A, at, 8, 32, 8, 32, 8)], P, 3, 4, 4) not in (0, INVALID)
     assert reorder([(P, A, 8, 32, 8, 32, 8)], P, 3, 4, 4) not in (0, INVALID)  # read as a state
+
+
+def meet(a, b):
+    """Whether two arrays (lo, row, beam, rows, beams, bytes) share a byte, from all of theirs."""
+    def every(e):
+        lo, row, beam, rows, beams, n = e
+        return {lo + i * row + j * beam + k for i in range(rows) for j in range(beams) for k in range(n)}
+    return bool(every(a) & every(b))
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="calls that are not refused must find no device")
+def test_what_is_taken_for_sharing_memory():
+    """Nothing that shares a byte is let through; halves and columns of one array, in any order of
+    its axes, are."""
+    import random
+    A = 1 << 40
+    rng = random.Random(5)
+    known = 0
+    for i in range(4000):
+        B, K, n = rng.randint(1, 3), rng.randint(1, 4), rng.randint(1, 6)
+        row, beam = rng.choice([(K * n, n), (2 * K * n, n), (K * n * 2, 2 * n), (n, B * n), (n, 2 * B * n), (2 * n, 2 * B * n),
+                                (rng.randint(1, 60), rng.randint(1, 60))])
+        orow, obeam = rng.choice([(row, beam), (row, beam), (2 * row, beam), (rng.randint(1, 60), rng.randint(1, 60))])
+        at = rng.choice([0, n, K * n, B * n, B * K * n, rng.randint(-40, 40), -K * n, -n])
+        if at == 0:
+            continue
+        got = reorder([(A, A + at, n, row, beam, orow, obeam)], 1 << 44, B, K, K)
+        own = len({A + at + i * orow + j * obeam + k for i in range(B) for j in range(K) for k in range(n)}) < B * K * n
+        shared = meet((A, row, beam, B, K, n), (A + at, orow, obeam, B, K, n))
+        if own or shared:
+            assert got == INVALID, (B, K, n, row, beam, orow, obeam, at)
+        known += got != INVALID
+    assert known > 1000
+    N = 33 * 4
+    for row, beam, at in ((8 * N, N, 4 * N), (4 * N, N, 12 * N), (8 * N, 2 * N, N), (N, 6 * N, 3 * N), (8 * N, N, -4 * N),
+                          (N, 6 * N, -3 * N), (8 * N, 2 * N, -N)):
+        assert not meet((0, row, beam, 3, 4, N), (at, row, beam, 3, 4, N))
+        assert reorder([(A, A + at, N, row, beam, row, beam)], 1 << 44, 3, 4, 4) not in (0, INVALID)
