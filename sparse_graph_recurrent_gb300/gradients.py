@@ -40,6 +40,55 @@ def _dense(t):
     return True
 
 
+def _direct(g, o):
+    """Whether the C entry can take g and its output o as they are."""
+    return _dense(g) and (o is g or o.stride() == g.stride() and o.is_neg() == g.is_neg())
+
+
+class _Span:
+    """The bytes from a tensor's first to its last, [lo, hi)."""
+
+    def __init__(self, t, written):
+        self.size, self.written = t.element_size(), written
+        self.axes = [(s * self.size, n) for n, s in zip(t.shape, t.stride()) if n != 1]
+        self.lo = t.data_ptr()
+        self.hi = self.lo + sum(s * (n - 1) for s, n in self.axes) + self.size
+
+    def of_every(self, m):
+        """The bytes that it takes of every m, from where it begins on, or more than m."""
+        return self.size + sum(s * (n - 1) if s < m else m for s, n in self.axes if s % m)
+
+    def beside(self, other):
+        """Whether another, that begins no earlier, takes others of every so many bytes: columns of
+        one array, or its rows by turns."""
+        for m in {s for s, _ in self.axes + other.axes if s}:
+            apart = (other.lo - self.lo) % m
+            if self.of_every(m) <= apart and apart + other.of_every(m) <= m:
+                return True
+        return False
+
+
+def _refuse_shared(pairs):
+    """Refuses tensors that share memory where one of them is written, or may.  (Of dense ones the
+    C entry looks after that; others go there by way of copies.)"""
+    spans = []
+    for g, o in pairs:
+        if not g.numel():
+            continue
+        spans.append(_Span(o, True))
+        if any(not s for s, _ in spans[-1].axes):
+            raise ValueError("elements of a tensor that is written share memory")
+        if (g.data_ptr(), g.stride()) != (o.data_ptr(), o.stride()):
+            spans.append(_Span(g, False))
+    spans.sort(key=lambda s: s.lo)
+    for i, a in enumerate(spans):
+        for b in spans[i + 1:]:
+            if b.lo >= a.hi:
+                break
+            if (a.written or b.written) and not a.beside(b):
+                raise ValueError("two tensors share memory that is written")
+
+
 def _space(array, device):
     return torch.empty(_ck.ck_clip_workspace_size(array) // 8, dtype=torch.int64, device=device)
 
@@ -75,7 +124,7 @@ def clip_gradients(grads, max_norm: float, out=None):
     min(1, max_norm / (norm + 1e-6)): by nothing where the norm is small enough.  `out`, a
     tensor or as many as there are gradients, of their types and shapes, receives the
     products instead.  None is skipped.  Tensors that share memory are refused where it
-    is written."""
+    is written, and so are strided ones of which that cannot be told from their strides."""
     norm = (_ck._native or _ck.native()).clip(grads, max_norm, out) if max_norm is not None else None
     if norm is not None:
         return norm
@@ -92,9 +141,11 @@ def clip_gradients(grads, max_norm: float, out=None):
     device = _one_device([g for g, _ in pairs]) if pairs else torch.device("cuda", torch.cuda.current_device())
     norm = torch.empty((), dtype=torch.float32, device=device)
     ins, outs, back = [], [], []
+    if not all(_direct(g, o) for g, o in pairs):
+        _refuse_shared(pairs)
     for g, o in pairs:
         g, own = g.detach(), o is g
-        if not _dense(g) or not own and (not _dense(o) or o.stride() != g.stride() or o.is_neg() != g.is_neg()):
+        if not _direct(g, o):
             # by way of a dense one: a copy of the gradient, or where the gradient is itself
             # dense in order, other memory beside it
             aim, copied, g = o, not g.is_contiguous() or g.is_neg(), g.resolve_neg().contiguous()

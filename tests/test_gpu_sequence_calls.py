@@ -377,3 +377,41 @@ def test_parents_that_are_a_state_too():
         with pytest.raises(RuntimeError):
             ck.reorder_states(states, parents, out=out)
     assert torch.equal(keep, parents)
+
+
+def test_strided_tensors_that_share_memory():
+    import sparse_graph_recurrent_gb300 as ck
+    w, to = torch.randn(8, 12, device="cuda"), torch.zeros(8, 12, device="cuda")
+    for grads in ([w[:, :3], w[:, 2:5]], [w[:, ::2], w[:, ::3]], [w[::2], w[:3]], [w[:, :5], w], [w.t()[:3], w[:2]],
+                  [w[:, 0], w[0]], [w[:, ::2], w[:, 1:3]]):
+        keep = w.clone()
+        with pytest.raises((ValueError, RuntimeError)):
+            ck.clip_gradients(grads, 0.5)
+        assert torch.equal(w, keep)
+        with pytest.raises((ValueError, RuntimeError)):  # read in one, written in another
+            ck.clip_gradients([grads[0], to[:grads[1].shape[0], :grads[1].shape[1]] if grads[1].dim() == 2 else to[0, :grads[1].shape[0]]],
+                              0.5, out=[torch.empty_like(grads[0]), grads[1]])
+        assert torch.equal(w, keep)
+        ck.grad_norm(grads)  # reading is fine
+    # side by side is fine
+    for cut in (lambda t: [t[:, ::2], t[:, 1::2]], lambda t: [t[:, :3], t[:, 3:7], t[:, 7:]], lambda t: [t[::2, 1::2], t[1::2]],
+                lambda t: [t[:, 0], t[:, 1], t[:4, 2:], t[4:, 2:]], lambda t: [t.t()[:5], t[:, 5:]],
+                lambda t: [t[:, ::2], t[:, 1:2], t[:, 3::2]], lambda t: [t[:, :4].t(), t[:, 4:8], t[:, 11]]):
+        t, o = w.clone(), torch.full_like(w, 7)
+        parts = [host(p) for p in cut(t)]
+        norm, factor = so.clip(parts, 0.5)
+        ck.clip_gradients(cut(t), 0.5, out=cut(o))
+        assert torch.equal(t, w)
+        got = ck.clip_gradients(cut(t), 0.5)
+        assert abs(float(got) - norm) <= NORM_OFF * norm
+        for p, q, v in zip(cut(t), cut(o), parts):
+            assert torch.equal(p, q)
+            so.within(host(p), v * factor, np.abs(v * factor) * FACTOR_OFF)
+    with pytest.raises(ValueError):
+        ck.clip_gradients([w[0]], 0.5, out=[to[:1, :1].expand(1, 12)[0]])
+    # dense, and in another order than its gradient
+    c = torch.zeros(6, 4, device="cuda")
+    for grads, out in (([w[:4, :6].contiguous(), c.view(-1)[3:9]], [c.t(), torch.zeros(6, device="cuda")]),
+                       ([w[:4, :6].contiguous(), w[7]], [c.t(), c.view(-1)[12:]]), ([c.view(4, 6)], [c.t()])):
+        with pytest.raises((ValueError, RuntimeError)):
+            ck.clip_gradients(grads, 0.5, out=out)

@@ -70,3 +70,26 @@ def test_what_is_taken_for_sharing_memory():
                           (N, 6 * N, -3 * N), (8 * N, 2 * N, -N)):
         assert not meet((0, row, beam, 3, 4, N), (at, row, beam, 3, 4, N))
         assert reorder([(A, A + at, N, row, beam, row, beam)], 1 << 44, 3, 4, 4) not in (0, INVALID)
+
+
+def test_strided_tensors_that_may_share_memory():
+    """What is taken to lie side by side does, whatever the strides; plain cases are."""
+    import random
+
+    from sparse_graph_recurrent_gb300.gradients import _Span
+    rng = random.Random(2)
+    line = torch.arange(4000, dtype=torch.float32)
+    known = 0
+    for _ in range(3000):
+        views = []
+        for _ in range(2):
+            shape = [rng.randint(1, 5) for _ in range(rng.randint(1, 3))]
+            stride = [rng.choice([1, 2, 3, 6, 12, 24, rng.randint(0, 40)]) for _ in shape]
+            views.append(torch.as_strided(line, shape, stride, rng.randint(0, 60)))
+        a, b = sorted(views, key=lambda t: t.data_ptr())
+        shared = bool(set(a.flatten().tolist()) & set(b.flatten().tolist()))
+        a, b = _Span(a, True), _Span(b, True)
+        apart = b.lo >= a.hi or a.beside(b)
+        assert not (shared and apart)
+        known += apart and not shared
+    assert known > 500
