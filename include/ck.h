@@ -504,7 +504,8 @@ ck_status ck_gated_backward(const ck_gated_call *call, void *stream);
  * clipping out = grad * min(1, max_norm / (norm + 1e-6)), rounded once.  out may be grad
  * itself; no tensor's out may overlap another's grad or out, or its own grad in part.  The
  * norm is right where squares leave 32 bits (down to elements of 2^-126).  A norm that is
- * infinite makes the factor 0, one that is NaN makes it NaN.
+ * infinite (so is one beyond 32 bits) makes the factor 0, one that is NaN makes it NaN; with a
+ * max_norm that is infinite the factor is 1 for all but NaN.
  *   workspace (device, 8-byte aligned) at least what ck_clip_workspace_size says for the
  *             same list on this device; needs no setting, means nothing afterwards
  * Sums are added up in an order that depends on the list and the device alone.

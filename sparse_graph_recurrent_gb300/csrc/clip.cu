@@ -249,9 +249,11 @@ __device__ __forceinline__ Factor factor_of(const double *sums, int all, double 
             const double d = (double)f.norm + 1e-6;
             if (max_norm >= d) {
                 f.by = 1.f;
-            } else {
+            } else if (f.norm > 3.402823466e38f) {
+                f.by = 0.f;
+            } else {  // (NaN stays; max_norm is below d, and so inside 32 bits)
                 const float q = (float)max_norm / (float)d;
-                f.by = f.norm <= 3.402823466e38f ? q + (float)(max_norm - (double)q * d) / (float)d : q;  // (NaN stays)
+                f.by = q + (float)(max_norm - (double)q * d) / (float)d;
             }
         }
     }

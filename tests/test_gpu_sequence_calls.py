@@ -415,3 +415,22 @@ def test_strided_tensors_that_share_memory():
                        ([w[:4, :6].contiguous(), w[7]], [c.t(), c.view(-1)[12:]]), ([c.view(4, 6)], [c.t()])):
         with pytest.raises((ValueError, RuntimeError)):
             ck.clip_gradients(grads, 0.5, out=out)
+
+
+@pytest.mark.parametrize("max_norm", [1.0, 1e38, 1e39, 1e300])
+def test_an_infinite_norm_gives_a_factor_of_0(max_norm):
+    import sparse_graph_recurrent_gb300 as ck
+    for big in (3e38, float("inf")):  # (the root of two squares of 3e38 is beyond 32 bits too)
+        g = torch.full((5000,), big, device="cuda")
+        rest = torch.randn(77, device="cuda")
+        assert float(ck.clip_gradients([g, rest], max_norm)) == float("inf")
+        assert not rest.any() and (not g.any() if big < float("inf") else g.isnan().all())
+
+
+def test_no_limit_changes_nothing():
+    import sparse_graph_recurrent_gb300 as ck
+    for big in (1.0, 3e38, float("inf")):
+        g = torch.full((5000,), big, device="cuda")
+        out = torch.empty_like(g)
+        ck.clip_gradients([g], float("inf"), out=[out])
+        assert torch.equal(g, out)
