@@ -18,10 +18,10 @@
 // memory; each then runs its part from the state that it now knows, reading it again,
 // mostly from L2.  With more parts than a CTA has warps the CTAs of a cluster leave their maps
 // in memory and begin with those before their own; with more than a cluster's these are two
-// kernels (1,024 x 8 x 1,024 bf16, forward: 22.7 us with a cluster, 24.7 with two kernels then).  The
+// kernels (1,024 x 8 x 1,024 bf16, forward: 20.4 us with a cluster, 21.2 with two kernels).  The
 // composing goes through a part in the order opposite to the run that follows, so that what
-// was read last, and is in L2 still, is read first again (4,000 x 2 x 1,200 fp32, gradient: 40 us,
-// 42 in the same order).
+// was read last, and is in L2 still, is read first again (4,000 x 2 x 1,200 fp32, gradient: 42 us,
+// 44 in the same order).
 //
 // The gradient runs the other way: with g_t = d_out_t + r_{t+1}, r_t = a_t g_t is a map of
 // r_{t+1}, and
@@ -937,14 +937,14 @@ GatedPlan gated_plan(int64_t T, int64_t C, int V, int sms) {
     GatedPlan p{};
     p.blocks = (T + kSteps - 1) / kSteps;
     const int64_t warps = (C + 32 * V - 1) / (32 * V);
-    // parts: as many as give every SM kFill warps, which is what fits (65,536 x 256 bf16: 119 us
-    // with 16, 143 with 12, 151 with 24, before the copies), of at least three blocks each
-    // (1,000 x 2 x 500 bf16, both directions: 23 us, 31 with four; 64 x 8 x 5,000 fp32 25 us, 29 with two)
+    // parts: as many as give every SM kFill warps, which is what fits (65,536 x 256 bf16, both
+    // directions: 60 us with 16, 66 with 12, 74 with 24 and 77 with 32), of at least three blocks each
+    // (64 x 8 x 5,000 fp32, both directions: 21 us, as with four, and 23 with two)
     constexpr int64_t kFill = 16;
     int64_t parts = warps >= 8 * sms ? 1 : (kFill * sms + warps - 1) / warps;
     if (parts > p.blocks / 3) parts = p.blocks / 3;
     // ...or of fewer, where there are so few warps that the steps' own latency is what counts
-    // (64 x 39 x 21 fp32, both directions: 14.4 us, 26.6 with three)
+    // (64 x 39 x 21 fp32, both directions: 10.6 us, 20.2 with three)
     const int64_t few = 8 * (int64_t)sms / warps < p.blocks ? 8 * (int64_t)sms / warps : p.blocks;
     if (p.blocks >= 6 && parts < few) parts = few;
     if (parts < 1) parts = 1;
@@ -952,7 +952,7 @@ GatedPlan gated_plan(int64_t T, int64_t C, int V, int sms) {
     while (p.wt < kGatedWarps && 2 * p.wt <= parts) p.wt *= 2;
     p.chunks = parts >= 2 * kGatedWarps ? (int)(parts / kGatedWarps) : 1;
     // Clusters do not fill the device to the last CTA: with fewer that are all there at once
-    // 2,000 x 5 x 600 fp16, forward, takes 20.6 us instead of 26.8.  (Pairs always fit.)
+    // 2,000 x 5 x 600 fp16, forward, takes 17.9 us instead of 23.7.  (Pairs always fit.)
     if (p.chunks > 2 && p.chunks <= kCluster) {
         const int64_t fewer = 14 * (int64_t)sms / warps / kGatedWarps;
         if (fewer < p.chunks) p.chunks = fewer < 2 ? 2 : (int)fewer;
@@ -1038,7 +1038,7 @@ cudaError_t launch_gated(GatedArgs a, const GatedPlan &p, bool backward, cudaStr
     a.cluster = p.chunks > 1 && p.chunks <= kCluster;
     // The next kernel, if it is one of these, has its CTAs come while there is room for all of them
     // beside this one's, or where they fill the device many times.  Else those that came early would
-    // lie unevenly (96 x 20 x 4,999 fp16, both directions: 52 us then, 38 so).
+    // lie unevenly (96 x 20 x 4,999 fp16, both directions: 45 us then, 35 so).
     const int64_t all = p.grid * p.chunks * p.wt * p.wc;
     a.early = all <= 8 * (int64_t)device_sms() || (a.parts == 1 && all >= 16 * (int64_t)device_sms());
     const int warps = p.wt * p.wc, two = p.chunks > 1 && !a.cluster;
@@ -1089,8 +1089,11 @@ ck_status run_gated(const ck_gated_call *c, bool backward, cudaStream_t s) {
     const bool pairs = C % 2 == 0 && aligned(a.out, 2 * e) && aligned(a.dx, 2 * e) && aligned(a.dgate, 2 * e);
     // Rows that 16 bytes cannot be copied of, but that hold all sequences one after another and
     // begin alike in all tensors, are taken as they lie: copies of less go by way of what is left
-    // of L1 (96 x 20 x 4,999 fp16, gradient: 24 us, 29 with copies of 8 bytes; 300 x 2 x 3,001 bf16,
-    // both directions, 21 and 25).
+    // of L1 (96 x 20 x 4,999 fp16, gradient: 27 us, 31 with copies of 8 bytes; 300 x 2 x 3,001 bf16,
+    // both directions, 25 and 31).  Rows of an odd width that begin unlike are copied by elements: 4
+    // bytes at a time in 32 bits (64 x 32 x 4,999, both directions: 83 us, 55 where they begin
+    // alike), but loaded and stored in 16, with nothing under way ahead (96 x 20 x 4,999 fp16, both
+    // directions: 346 us, 35 where they begin alike).
     const auto like_x = [&](const void *p, int64_t st, int64_t sb) {
         return ((uintptr_t)p - (uintptr_t)a.x) % 16 == 0 && (c->T == 1 || (st - a.xt) * (int64_t)e % 16 == 0) && (c->B == 1 || sb == c->N);
     };
