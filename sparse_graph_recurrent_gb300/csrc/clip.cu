@@ -162,6 +162,7 @@ __device__ __forceinline__ void run_of(int chunks, int &lo, int &hi) {
 // that need it, one by one.
 template <int MOST> __device__ __noinline__ double scaled_sum(const ClipList<MOST> &a, int lo, int hi, float scale, double *shared) {
     float s = 0.f;
+    double total = 0;
     for (int c = lo; c < hi; ++c) {
         const Where w = locate(a, c, 0);
         by_dtype(a.dtype[w.i], [&](auto *t) {
@@ -173,9 +174,10 @@ template <int MOST> __device__ __noinline__ double scaled_sum(const ClipList<MOS
             }
             s += part;
         });
+        if ((c - lo) % 32 == 31) total += s, s = 0.f;
     }
     __syncthreads();
-    return block_sum(s, shared) / ((double)scale * (double)scale);
+    return block_sum(total + (double)s, shared) / ((double)scale * (double)scale);
 }
 
 template <int MOST>

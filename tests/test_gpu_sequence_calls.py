@@ -434,3 +434,22 @@ def test_no_limit_changes_nothing():
         out = torch.empty_like(g)
         ck.clip_gradients([g], float("inf"), out=[out])
         assert torch.equal(g, out)
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -80, 2.0 ** 70])
+def test_the_norm_of_billions(scale):
+    """A number whose squares' sum is rounded the same way again and again, where a thread adds up
+    a thousand chunks of it: a sum of 32 bits that takes in all of them is off by 128 half steps.
+    The bound is of an element's square, 32 additions in a chunk and 32 chunks in a row, in half
+    steps, halved by the root, which is rounded."""
+    import sparse_graph_recurrent_gb300 as ck
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = 4 * sms * 1050 * 4096
+    c = float.fromhex("0x1.ef60e80000000p0") * scale
+    g = torch.full((n,), c, device="cuda")
+    want = c * float(n) ** 0.5
+    assert abs(float(ck.grad_norm(g)) - want) <= ((1 + 32 + 32) / 2 + 1) * so.U32 * want
+    half = 0.5 * want
+    assert abs(float(ck.clip_gradients(g, half)) - want) <= ((1 + 32 + 32) / 2 + 1) * so.U32 * want
+    got = c * half / (want + 1e-6)  # (by the definition: far from half of c where the norm is small)
+    assert abs(float(g[0]) - got) <= 40 * so.U32 * got and (g == g[0]).all()
