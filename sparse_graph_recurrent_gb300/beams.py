@@ -23,8 +23,11 @@ def beam_select(logits, scores, ended=None, end_token=None, beams=None):
     sequence: (scores, parents, tokens, ended), float32, int64, int64 and bool [B, beams],
     best first.  logits [B, K, V] (float32, bfloat16 or float16; after control_logits, where
     there are controls), scores float32 [B, K].  The score of beam k with token v is
-    scores[b, k] + log_softmax(logits[b, k])[v], compared in 64 bits; of equal ones the
-    lowest k, then the lowest v comes first.  A beam with ended[b, k] (bool) goes on as one
+    scores[b, k] + log_softmax(logits[b, k])[v]; of equal ones the lowest k, then the lowest v
+    comes first.  The softmax's sum is one of 32-bit exponentials, whose logarithm is off by
+    6e-6 at most (for 131,072 tokens), the rest is of 64 bits: candidates of one beam are in the
+    order of their logits, those of different beams that lie closer than that may be taken in
+    either order.  A beam with ended[b, k] (bool) goes on as one
     candidate, end_token at the score that it has; the ended that is returned says which
     beams are at end_token now.  A token at -inf or NaN is no candidate, nor is any of a
     beam whose score is not finite (the beams of a first step but one) or whose logits hold
