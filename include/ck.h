@@ -468,9 +468,9 @@ ck_status ck_control_logits(const ck_logit_call *call, void *stream);
  * Gradients are 0 from step lengths[b] on.  Long sequences of few nodes are cut along the
  * steps, and products of gates over runs of steps are formed.  A decay's product that leaves 32
  * bits, where the states do not, is not used: such runs are gone through step by step.  A
- * product below 2^-126 stands for what it is to 2^-149, and is not 0 unless a gate is: what a
- * run leaves of a state is off by 2^-149 of that at most, which in the decay form is used up to
- * states of 2^23.
+ * product below 2^-126 stands for what it is to 2^-149, and is not 0 unless a gate is, so that
+ * what a run leaves of a state is off by 2^-149 of that; in the decay form it is gone through
+ * step by step where that, of a state above 2^23, could be seen beside what the run adds.
  *   workspace (device) workspace_bytes of ck_gated_sizes on this device, 8-byte aligned;
  *             its contents need no setting and mean nothing afterwards; NULL when 0 bytes
  * Results depend on the operands, how they lie, the sizes and the device alone.

@@ -411,23 +411,29 @@ __device__ __forceinline__ float2 compose(float2 later, float2 earlier) {
                        fmaf(later.x, earlier.y, later.y));
 }
 
-// What maps that were composed one after another have gone through.  A decay's product that has
-// come below the normal numbers and up again may have been anything in between, and what it leaves
-// of a number above 2^23 may be anything up to 2^-126: the factor of all is NaN then.  (Looked at
-// once, beside the chain of products: in each of them it was 2% of 65,536 x 256 bf16.)
 constexpr float kLeast = 1.17549435e-38f, kMost = 3.402823466e38f;  // normal numbers
-constexpr float kLarge = 8388608.f;                                 // 2^23
+// What a decay's factor below the normal numbers leaves of a number, `from`, may be off by 2^-126 of
+// it: nothing beside a sum, `to`, of 2^-100 of it, nor where it was 2^23 at most.  Above kFaded it
+// says too little.
+constexpr float kFaded = 6.6174449e-24f;  // 2^-77
+__device__ __forceinline__ float faded(float from, float to) { return fmaf(fabsf(from), 7.8886091e-31f, -fabsf(to)); }
+
+// What maps that were composed one after another have gone through.  A decay's product that has
+// come below the normal numbers and up again may have been anything in between: the factor of all
+// is NaN then, and where too much has faded.  (Looked at once, beside the chain of products: in
+// each of them it was 2 to 8% of 65,536 x 256 bf16 and 40,000 x 6 fp32.)
 template <int V, bool LEAK> struct Composed {
-    float least[V], most[V];  // of the factors' magnitudes; of what comes in
+    float least[V], most_faded[V];  // of the factors' magnitudes; of what came in
     __device__ __forceinline__ Composed() {
 #pragma unroll
-        for (int v = 0; v < V; ++v) least[v] = 1.f, most[v] = 0.f;
+        for (int v = 0; v < V; ++v) least[v] = 1.f, most_faded[v] = 0.f;
     }
-    __device__ __forceinline__ float2 operator()(int v, float2 later, float2 earlier) {
+    // by: the factor of the one that is new
+    __device__ __forceinline__ float2 operator()(int v, float2 later, float2 earlier, float by) {
         const float2 all = compose(later, earlier);
         if constexpr (!LEAK) {
-            least[v] = fminf(least[v], fminf(fabsf(all.x), fminf(fabsf(later.x), fabsf(earlier.x))));
-            most[v] = fmaxf(most[v], fabsf(earlier.y));
+            least[v] = fminf(least[v], fminf(fabsf(all.x), fabsf(by)));
+            most_faded[v] = fmaxf(most_faded[v], faded(earlier.y, all.y));
         }
         return all;
     }
@@ -435,7 +441,7 @@ template <int V, bool LEAK> struct Composed {
         if constexpr (!LEAK) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if ((least[v] < kLeast) & ((fabsf(all[v].x) >= kLeast) | (most[v] > kLarge))) all[v].x = __int_as_float(0x7fffffff);
+                if ((least[v] < kLeast) & ((fabsf(all[v].x) >= kLeast) | (most_faded[v] > kFaded))) all[v].x = __int_as_float(0x7fffffff);
         }
     }
 };
@@ -458,21 +464,21 @@ struct Part {
 
 // What maps that a state is carried through say of it.  Decays beyond 1 take a map out of 32 bits
 // where the states may stay inside (they are 0, or begin low): what comes out of it is not finite,
-// and stays so.  And what is left of a product below the normal numbers says little of a state
-// above 2^23.
-template <int V> struct Trust {
-    float most[V], least[V];  // of the states', the maps' magnitudes
+// and stays so.  And too much of a state may have faded.
+template <int V, bool LEAK> struct Trust {
+    float least[V], most_faded[V];
     __device__ __forceinline__ Trust() {
 #pragma unroll
-        for (int v = 0; v < V; ++v) most[v] = 0.f, least[v] = 1.f;
+        for (int v = 0; v < V; ++v) least[v] = 1.f, most_faded[v] = 0.f;
     }
     __device__ __forceinline__ void through(int v, float2 map, float &carry) {
-        most[v] = fmaxf(most[v], fabsf(carry));
-        least[v] = fminf(least[v], fabsf(map.x));
+        const float from = carry;
         carry = fmaf(map.x, carry, map.y);
+        least[v] = fminf(least[v], fabsf(map.x));
+        most_faded[v] = fmaxf(most_faded[v], faded(from, carry));
     }
     __device__ __forceinline__ bool holds(int v, float carry) const {
-        return fabsf(carry) <= kMost && (most[v] <= kLarge || least[v] >= kLeast);
+        return LEAK || ((fabsf(carry) <= kMost) & ((least[v] >= kLeast) | (most_faded[v] <= kFaded)));
     }
 };
 
@@ -512,9 +518,9 @@ __device__ __noinline__ float carried_by_steps(const GatedArgs &a, int64_t c, in
             (REVERSE ? first : last) = REVERSE ? hi : lo;
         } else {
             const float2 m = load_l2(a.maps + chunk * (a.B * a.N) + c);
-            const float by = fabsf(m.x), size = fabsf(carry);
-            if (by <= kMost && fabsf(m.y) <= kMost && (by >= kLeast || size <= kLarge || size > kMost)) {
-                carry = fmaf(m.x, carry, m.y);
+            const float to = fmaf(m.x, carry, m.y);
+            if (fabsf(m.x) <= kMost && fabsf(m.y) <= kMost && (fabsf(m.x) >= kLeast || !(faded(carry, to) > kFaded))) {
+                carry = to;
                 continue;
             }
         }
@@ -528,7 +534,7 @@ __device__ __noinline__ float carried_by_steps(const GatedArgs &a, int64_t c, in
 // each.  REVERSE: a later chunk's map is applied first.
 template <int V, bool LEAK, bool REVERSE>
 __device__ __forceinline__ void through_chunks(const GatedArgs &a, const Nodes<V> &at, int first, int last,
-                                               Exchange<V> &ex, Trust<V> &trust, float (&carry)[V]) {
+                                               Exchange<V> &ex, Trust<V, LEAK> &trust, float (&carry)[V]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp & (a.wt - 1);
     const int n = last - first, lo = first + (n * wt >> a.wt_shift), hi = first + (n * (wt + 1) >> a.wt_shift);
     const int64_t C = a.B * a.N;
@@ -554,7 +560,7 @@ __device__ __forceinline__ void through_chunks(const GatedArgs &a, const Nodes<V
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int v = 0; v < V; ++v) m[v] = composed(v, q[u][v], m[v]);
+                for (int v = 0; v < V; ++v) m[v] = composed(v, q[u][v], m[v], q[u][v].x);
         }
         composed.settle(m);
     }
@@ -573,7 +579,7 @@ __device__ __forceinline__ void through_chunks(const GatedArgs &a, const Nodes<V
 // What is carried into this warp's part.  MAPS: composes the part with part_map(m) and
 // leaves the maps; otherwise carry goes through all that comes before.
 template <int V, bool LEAK, bool MAPS, bool REVERSE, typename F>
-__device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at, Exchange<V> &ex, Trust<V> &trust,
+__device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at, Exchange<V> &ex, Trust<V, LEAK> &trust,
                                          float (&carry)[V], F part_map) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wt = warp & (a.wt - 1), base = warp - wt;
     const int64_t C = a.B * a.N;
@@ -605,10 +611,13 @@ __device__ __forceinline__ void exchange(const GatedArgs &a, const Nodes<V> &at,
         for (int v = 0; v < V; ++v) p[v] = make_float2(1.f, 0.f);
         for (int j = 0; j < before; ++j)
 #pragma unroll
-            for (int v = 0; v < V; ++v) p[v] = composed(v, ex.m[base + (REVERSE ? a.wt - 1 - j : j)][v][lane], p[v]);
+            for (int v = 0; v < V; ++v) {
+                const float2 q = ex.m[base + (REVERSE ? a.wt - 1 - j : j)][v][lane];
+                p[v] = composed(v, q, p[v], q.x);
+            }
         composed.settle(p);
 #pragma unroll
-        for (int v = 0; v < V; ++v) m[v] = composed(v, m[v], p[v]);
+        for (int v = 0; v < V; ++v) m[v] = composed(v, m[v], p[v], m[v].x);
         composed.settle(m);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -682,7 +691,7 @@ __device__ __forceinline__ void forward_map(const R &in, const Nodes<V> &at, int
         multiply_add(plus, keep, plus, put);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) all[v] = blocks(v, all[v], make_float2(not_lost(by[v], least[v] > 0.f), plus[v]));
+    for (int v = 0; v < V; ++v) all[v] = blocks(v, all[v], make_float2(not_lost(by[v], least[v] > 0.f), plus[v]), by[v]);
 }
 
 // One block's steps from the state h on.
@@ -736,7 +745,7 @@ __global__ void __maxnreg__(96) k_gated_forward(const __grid_constant__ GatedArg
     float h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = !MAPS && a.state0 && at.has(v) ? a.state0[at.c + v] : 0.f;
-    Trust<V> trust;
+    Trust<V, LEAK> trust;
     exchange<V, LEAK, MAPS, false>(a, at, ex, trust, h, [&](float2 (&m)[V]) {
         Composed<V, LEAK> blocks;
         in.each(part.hi - 1, part.hi - part.lo, -1, at.warp_most, [&](int k) {
@@ -801,7 +810,7 @@ __device__ __forceinline__ void backward_map(const R &in, const Nodes<V> &at, in
         multiply(plus, keep, sum);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) all[v] = blocks(v, all[v], make_float2(not_lost(by[v], least[v] > 0.f), plus[v]));
+    for (int v = 0; v < V; ++v) all[v] = blocks(v, all[v], make_float2(not_lost(by[v], least[v] > 0.f), plus[v]), by[v]);
 }
 
 // One block's gradients, r being that of the state after it.
@@ -881,7 +890,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 ? 112 : 128) k_gated_backward(const _
     float r[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) r[v] = !MAPS && a.dstate && at.has(v) ? a.dstate[at.c + v] : 0.f;
-    Trust<V> trust;
+    Trust<V, LEAK> trust;
     exchange<V, LEAK, MAPS, true>(a, at, ex, trust, r, [&](float2 (&m)[V]) {
         BackwardRing<T, V, SHIFT, true> in;
         begin(in);

@@ -299,6 +299,20 @@ def test_decays_whose_products_leave_32_bits(T, B, N, dtype):
     assert (dstate0 == 2.0 ** 100).all() and not dx[T - 137:, -1].any()
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T,B,N", [(300, 2, 30), (2000, 1, 70), (9000, 1, 33)])
+def test_large_states(T, B, N, dtype):
+    """States of 2^30 and more, with nothing coming in at first, for a while, and at last."""
+    d = inputs(T, B, N, dtype, "decay", seed=T)
+    for name in ("x", "d_out"):
+        d[name] *= 2.0 ** 30
+        for lo, hi in ((0, 1), (4, 5), (9, 10)):
+            d[name][T * lo // 10:T * hi // 10] = 0
+    d["state0"] = None
+    d["gate"] = (d["gate"].float() * 0.3 + 0.7).to(TYPES[dtype])
+    check(d, "decay", dtype)
+
+
 @pytest.mark.parametrize("T", [700, 9000])
 def test_an_infinite_input_reaches_what_it_would_step_by_step(T):
     import sparse_graph_recurrent_gb300 as ck
