@@ -569,7 +569,7 @@ ck_status ck_beam_select(const ck_beam_call *call, void *stream);
  * in itself, with the same strides and beams == K, or the two do not overlap; no array's
  * out may overlap another's in or out, or the parents.
  * Asynchronous.  Errors: CK_ERR_INVALID_ARG, CK_ERR_UNSUPPORTED (K or beams above 64,
- * B > 65535), CK_ERR_CUDA.
+ * B > 65535), CK_ERR_OUT_OF_MEMORY (host), CK_ERR_CUDA.
  */
 typedef struct {
     const void *in;

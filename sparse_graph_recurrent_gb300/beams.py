@@ -95,7 +95,7 @@ def reorder_states(states, parents, out=None):
     [B, beams, ...] of a tensor [B, K, ...] or of several, of any types, in one pass.
     parents is int64 [B, beams] as beam_select returns it; one outside [0, K) gives zeros.
     `out`, a tensor or as many as there are states, is written instead; a state may be its
-    own `out`, where beams == K."""
+    own `out`, where beams == K.  An `out` that overlaps another array, or parents, is refused."""
     got = (_ck._native or _ck.native()).reorder(states, parents, out)
     if got is not None:
         return got
