@@ -75,11 +75,12 @@ def _refuse_shared(pairs):
     for g, o in pairs:
         if not g.numel():
             continue
-        spans.append(_Span(o, True))
-        if any(not s for s, _ in spans[-1].axes):
+        read, written = _Span(g, False), _Span(o, True)
+        if any(not s for s, _ in written.axes):
             raise ValueError("elements of a tensor that is written share memory")
-        if (g.data_ptr(), g.stride()) != (o.data_ptr(), o.stride()):
-            spans.append(_Span(g, False))
+        spans.append(written)
+        if (read.lo, read.axes) != (written.lo, written.axes):  # (not in its own place)
+            spans.append(read)
     spans.sort(key=lambda s: s.lo)
     for i, a in enumerate(spans):
         for b in spans[i + 1:]:

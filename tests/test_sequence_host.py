@@ -93,3 +93,17 @@ def test_strided_tensors_that_may_share_memory():
         assert not (shared and apart)
         known += apart and not shared
     assert known > 500
+
+
+def test_what_clipping_takes_and_refuses_of_strided_tensors():
+    """A tensor's own place is its own however it is named: the strides of axes of one do not count."""
+    from sparse_graph_recurrent_gb300.gradients import _refuse_shared
+    w, to = torch.zeros(8, 12), torch.zeros(8, 12)
+    row = w[7:, :5]
+    for pairs in ([(row, row)], [(row, row.as_strided((1, 5), (3, 1), row.storage_offset()))], [(w[:, ::2], w[:, ::2]), (w[:, 1::2], to)],
+                  [(w[:, :0], w[:, :0]), (w, w)], [(w[:, 0], to[:, 3]), (w[:, 1], to[:, 2])]):
+        _refuse_shared(pairs)
+    for pairs in ([(row, row.as_strided((1, 5), (3, 2), row.storage_offset()))], [(w[:, ::2], w[:, 1::2]), (w[:, 1::2], to)],
+                  [(w[:, :3], to[:, :1].expand(8, 3))], [(w[:, 0], to[:, 3]), (to[0], w[1])]):
+        with pytest.raises(ValueError):
+            _refuse_shared(pairs)
